@@ -238,6 +238,104 @@ laga_status laga_mla_absorbed_fwd(const laga_mla_desc* desc, const void* q, cons
                                   const void* W_UK, const void* W_UV, void* out, float* lse, void* workspace,
                                   size_t workspace_bytes, laga_stream_t stream);
 
+/* ---- Masked attention: packed documents, prefixes, windows, capped scores, a bias by
+ * distance. The same rebuild and attention as laga_mla_fwd / laga_mla_bwd, with the
+ * scores (natural-log domain)
+ *   s_ij = softmax_scale * q[i,h,:] . K_h[j]
+ *   s_ij = softcap * tanh(s_ij / softcap)          if softcap > 0
+ *   s_ij = s_ij - slopes[h] * |pos_i - j|          if slopes (pos_i: the row's position)
+ * and key j visible to row i iff key_lo[i] <= j < key_hi[i] (and j <= pos_i when
+ * desc->causal). Bounds outside [0, skv] are clamped; a row with none left sees
+ * nothing: its out is 0, its lse -inf, its dq 0, and it adds to no gradient.
+ * softcap and slopes are constants here (no gradient).
+ * Non-finite values in masked places do no harm: a key that no row sees may hold
+ * infinities or NaN, and so may the q and dout of a row that sees nothing. A row that
+ * sees a key whose latent or RoPE key is not finite gets NaN (out and lse); a key that
+ * is seen by such a row, or by one whose q or dout is not finite, gets NaN gradients. */
+typedef struct {
+  const int32_t* key_lo; /* [B, Sq], device; NULL: 0 */
+  const int32_t* key_hi; /* [B, Sq], device, one past the last visible key; NULL: skv */
+  const float* slopes;   /* [n_h], device; NULL: none */
+  float softcap;         /* 0: none; else finite and > 0 */
+} laga_mla_mods;
+
+/* A tensor saved in 8 bits by laga_mla_pack8 (rows of the tensor's last dimension). */
+typedef struct {
+  const uint8_t* codes;  /* the tensor's shape; 16-byte aligned where laga_mla_masked_bwd reads it */
+  const uint8_t* scales; /* the shape with the last dimension ceil(d / 32) */
+} laga_mla_packed;
+
+/* Workspace of laga_mla_masked_fwd / laga_mla_masked_bwd (0: invalid or unsupported). */
+size_t laga_mla_masked_fwd_workspace_size(const laga_mla_desc* desc);
+size_t laga_mla_masked_bwd_workspace_size(const laga_mla_desc* desc);
+
+/* Forward: out and lse as for laga_mla_fwd. mods may be NULL (no cap, no bias, bounds
+ * from desc->causal alone). Variants AUTO, MATERIALIZE and SIMT; bf16 with the
+ * tensor-core dims, otherwise d_nope + d_rope <= 256 and d_v <= 256 on the CUDA cores.
+ * LAGA_FLAG_KV_PREBUILT is refused. The workspace starts with the rebuilt K and V, as
+ * laga_mla_fwd's does. Errors as for laga_mla_fwd. */
+laga_status laga_mla_masked_fwd(const laga_mla_desc* desc, const laga_mla_mods* mods, const void* q,
+                                const void* c_kv, const void* k_rope, const void* W_UK, const void* W_UV, void* out,
+                                float* lse, void* workspace, size_t workspace_bytes, laga_stream_t stream);
+
+/* Backward: the gradients of <dout, out> as for laga_mla_bwd, with the same mods as the
+ * forward. q and out come either as tensors (q8, out8 NULL) or as 8-bit checkpoints
+ * (q and out NULL): then P = exp(s - lse) with the scores of the restored q, and
+ * D = rowsum(dout o out) of the restored out. LAGA_FLAG_REUSE_KV: the workspace is the
+ * one laga_mla_masked_fwd used for the same inputs, its K and V intact. */
+laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* mods, const void* q,
+                                const void* c_kv, const void* k_rope, const void* W_UK, const void* W_UV,
+                                const void* out, const float* lse, const void* dout, const laga_mla_packed* q8,
+                                const laga_mla_packed* out8, void* dq, void* dc_kv, void* dk_rope, void* dW_UK,
+                                void* dW_UV, void* workspace, size_t workspace_bytes, laga_stream_t stream);
+
+/* key_lo, key_hi [B, Sq] of packed documents. Document k of batch element b holds the keys
+ * [doc_starts[b][k], doc_starts[b][k + 1]) (doc_starts [B, n_docs + 1], ascending; repeated
+ * entries are empty documents). A row at position p of document k sees the keys of k up to p,
+ * at most the last `window` of them (0: all), and, with prefix [B, n_docs], every key of the
+ * document's first prefix[b][k] (pass causal = 0 to the attention then). A row in no document
+ * (before the first, at or past the last end) sees nothing. Positions as in laga_mla_desc
+ * (q_offset, q_split, q_offset2); skv clamps. Device pointers, 4-byte aligned. */
+laga_status laga_mla_key_bounds(int64_t batch, int64_t sq, int64_t skv, int64_t q_offset, int64_t q_split,
+                                int64_t q_offset2, const int32_t* doc_starts, int64_t n_docs, const int32_t* prefix,
+                                int64_t window, int32_t* key_lo, int32_t* key_hi, laga_stream_t stream);
+
+/* ---- Rotary positions with several axes (e.g. time, height, width), on the RoPE part of
+ * q [tokens, n_h, d_nope + d_rope] and on k_rope [tokens, d_rope] (tokens = B * S).
+ * Pair i of the d_rope / 2 pairs (x, y) turns by a = pos[axis(i)][token] * theta^(-2i/d_rope):
+ * (x cos a - y sin a, x sin a + y cos a); the first sections[0] pairs use axis 0, the next
+ * sections[1] axis 1, and so on. interleaved: pair i is (2i, 2i + 1), else (i, i + d_rope/2).
+ * inverse turns by -a, which is also the gradient's way back. Positions may be negative and
+ * as far as their type goes: the angle is exact to 2^-32 turns. */
+#define LAGA_ROPE_MAX_AXES 4
+typedef struct {
+  int64_t tokens, n_h, d_nope, d_rope;
+  int64_t n_axes;
+  int64_t sections[LAGA_ROPE_MAX_AXES]; /* pairs of each axis; they add up to d_rope / 2 */
+  double theta;                         /* >= 1 */
+  int32_t interleaved, inverse;
+  int32_t pos64;                        /* nonzero: pos is int64, else int32 */
+  int32_t dtype;                        /* laga_dtype of q and k_rope */
+} laga_mla_rope_desc;
+
+/* q_out and k_out are the rotated tensors (the no-RoPE part of q is copied); they may be q
+ * and k_rope themselves, and may not overlap them otherwise. q with q_out, or k_rope with
+ * k_out, may be NULL. pos [n_axes, tokens]. d_rope <= 256. Pointers aligned to their type
+ * (16 bytes for the fast path). */
+laga_status laga_mla_rope(const laga_mla_rope_desc* desc, const void* pos, const void* q, const void* k_rope,
+                          void* q_out, void* k_out, laga_stream_t stream);
+
+/* ---- Activation checkpoints in 8 bits. x [rows, cols] becomes e4m3 codes [rows, cols] and,
+ * per block of 32 columns, a biased exponent [rows, ceil(cols / 32)]: value = code *
+ * 2^(scale - 127), the power of two being the smallest that brings the block's largest
+ * finite size to at most 448 (127 for a block of zeros; never below 2^-127). Codes round to
+ * nearest, ties to even; infinities and NaN become the NaN code. unpack8 rounds the value to
+ * dtype. Pointers aligned to their type (x 16, codes 8 bytes for the fast path). */
+laga_status laga_mla_pack8(int32_t dtype, int64_t rows, int64_t cols, const void* x, uint8_t* codes, uint8_t* scales,
+                           laga_stream_t stream);
+laga_status laga_mla_unpack8(int32_t dtype, int64_t rows, int64_t cols, const uint8_t* codes, const uint8_t* scales,
+                             void* x, laga_stream_t stream);
+
 /* Largest workspace, in bytes, that laga_mla_fwd_noalloc can stand in for. */
 #define LAGA_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)
 
@@ -297,7 +395,8 @@ laga_status laga_mla_selftest_timeout(laga_stream_t stream);
 
 /* Library ABI version: major*10000 + minor*100 + patch. 200 (0.2.0): laga_mla_desc
  * gained q_split and q_offset2 (two-segment query shards); zero them for the
- * single-segment behaviour of 100. */
+ * single-segment behaviour of 100. 300 (0.3.0): masked attention, rotary positions,
+ * 8-bit checkpoints; nothing that was there changed. */
 int laga_mla_version(void);
 
 #ifdef __cplusplus

@@ -1,8 +1,7 @@
 // C ABI of the LAGA MLA attention block: argument validation, workspace
 // layout, dispatch between the tensor-core and CUDA-core kernels, status
 // reporting. Nothing here allocates device memory.
-#include "../../include/laga_mla.h"
-#include "internal.h"
+#include "api_util.h"
 #include "ptx.cuh"
 
 #include <algorithm>
@@ -20,7 +19,9 @@ namespace {
 
 thread_local char t_last_error[512] = "";
 
-laga_status fail(laga_status s, const char* fmt, const char* detail = nullptr) {
+}  // namespace
+
+laga_status fail(laga_status s, const char* fmt, const char* detail) {
   std::snprintf(t_last_error, sizeof(t_last_error), fmt, detail ? detail : "");
   return s;
 }
@@ -37,6 +38,8 @@ laga_status from_launch(const LaunchResult& r) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+namespace {
 
 // ---- opt-in kernel timing: one event pair per launch, events pooled per thread.
 // Each record keeps the pool indices of its own two events, so a launch whose
@@ -65,6 +68,8 @@ long prof_event() {
   return static_cast<long>(P.used++);
 }
 
+}  // namespace
+
 // Records the start event of a launch named `name` (no-op when disabled).
 void prof_begin(const char* name, cudaStream_t s) {
   Profiler& P = t_prof;
@@ -87,17 +92,6 @@ void prof_end(cudaStream_t s) {
   }
   P.recs.back().end = static_cast<size_t>(e);
 }
-
-// Run one launcher between two profiling marks.
-template <class F>
-LaunchResult timed(const char* name, cudaStream_t s, F&& f) {
-  prof_begin(name, s);
-  LaunchResult r = f();
-  prof_end(s);
-  return r;
-}
-
-enum class Path { Invalid, Simt, TensorCore, TensorCoreFused };
 
 // Validate the descriptor; fill dims; choose a path. On error, sets *st.
 Path plan(const laga_mla_desc* desc, Dims* d, laga_status* st, bool for_bwd) {
@@ -196,6 +190,8 @@ Path plan(const laga_mla_desc* desc, Dims* d, laga_status* st, bool for_bwd) {
   }
   return Path::Simt;
 }
+
+namespace {
 
 using CuTensorMapEncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
@@ -617,6 +613,6 @@ int laga_mla_profile_read(const char** names, float* ms, int max) {
   return n;
 }
 
-int laga_mla_version(void) { return 200; }
+int laga_mla_version(void) { return 300; }
 
 }  // extern "C"

@@ -47,8 +47,14 @@
 // order dV(i) dK(i) dP(i+1) S(i+2) and dS^T over dP^T, the MMA warp waited
 // ~400 cycles per step at the P^T and dS^T hand-offs, 1820 cycles per step
 // against 1600 of tensor work).
+//
+// Masked instances (MOD >= 0): the query tiles that may see the key tile come from a
+// list; each stage also brings its 64 rows' visible intervals. q and dO may be read
+// from copies whose non-finite rows are zero (a masked query row's P^T and dS^T are 0,
+// but 0 times a NaN of its q or dO row would reach every key of the tile).
 #include "internal.h"
 #include "ptx.cuh"
+#include "score_mod.cuh"
 
 LAGA_TRACE_DEFINE(dkdv)
 
@@ -76,6 +82,12 @@ constexpr int SCR_BYTES = 32 * 64;
 constexpr int OFF_SCR = OFF_ROWV + NSTAGE * 2 * ROWV_BYTES;
 constexpr int OFF_BARS = OFF_SCR + 8 * SCR_BYTES;
 constexpr int SMEM_BYTES = OFF_BARS + 256 + 1024;
+// masked instances: per stage 64 visible intervals (int2) and the query tile's index
+constexpr int BND_BYTES = BQ * 8;
+constexpr int OFF_BND = OFF_BARS + 256;
+constexpr int OFF_QT = OFF_BND + NSTAGE * BND_BYTES;
+constexpr int SMEM_BYTES_MASKED = OFF_QT + 64 + 1024;
+static_assert(OFF_BND % 16 == 0 && SMEM_BYTES_MASKED <= 232448, "shared memory per CTA");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t COL_DV = 0, COL_DK = 128, COL_S = 320, COL_DP = 448;
 constexpr uint32_t IDESC_ST = idesc_bf16(128, 64, false, false);   // S^T, dP^T
@@ -102,14 +114,24 @@ struct Params {
   float scale, scale_log2;
   const float* lse2;
   const float* delta;
+  // masked instances
+  const int2* rows;      // [B][sq_pad] visible interval of each query row
+  const int* kt_count;   // [B][skv_pad / 128] query tiles that may see a key tile
+  const int* kt_list;    // [B][skv_pad / 128][sq_pad / 64] which
+  const int* q_bad;      // nonzero: read q and dO from the clean copies
+  ModParams mod;
 };
 
+template <int MOD>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                          const __grid_constant__ CUtensorMap mR, const __grid_constant__ CUtensorMap mV,
                          const __grid_constant__ CUtensorMap mdO, const __grid_constant__ CUtensorMap mdK,
                          const __grid_constant__ CUtensorMap mdV, const __grid_constant__ CUtensorMap mdKR,
+                         const __grid_constant__ CUtensorMap mQclean, const __grid_constant__ CUtensorMap mdOclean,
                          const Params p) {
+  constexpr bool MASKED = MOD >= 0;
+  constexpr bool CAP = MASKED && (MOD & kModCap) != 0, BIAS = MASKED && (MOD & kModBias) != 0;
   extern __shared__ uint8_t smem_raw[];
   LAGA_TRACE_CTA_BEGIN(dkdv);
   LAGA_TRACE_POINT(dkdv, 30, 0);
@@ -150,8 +172,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int first1 = p.q_split > 0 ? seg_tiles + (p.causal ? min(nq - seg_tiles, max(0, kv0 - p.q_offset2) / BQ) : 0)
                                    : nq;
   const int n0 = seg_tiles - first0;
-  const int n_qt = n0 + (nq - first1);
-  auto qtile = [&](int i) { return i < n0 ? first0 + i : first1 + (i - n0); };
+  const int kt_index = b * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  const int n_qt = MASKED ? p.kt_count[kt_index] : n0 + (nq - first1);
+  const int* kt_list = MASKED ? p.kt_list + static_cast<long long>(kt_index) * (p.sq_pad / BQ) : nullptr;
+  // No query tile sees these keys: their gradients are zeros, and only the key-row warps work
+  // (with nothing to wait for, the roles could run more than one barrier phase apart).
+  const bool unseen = MASKED && n_qt == 0;
+  auto qtile = [&](int i) {
+    if constexpr (MASKED) return kt_list[i];
+    return i < n0 ? first0 + i : first1 + (i - n0);
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -189,8 +219,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // Issue order: what the first MMAs need (the key/value tile, then the first
       // query stages), and only then L2 prefetches. Each TMA instruction takes the
       // issuing thread a while, and S(0) waits on all of the ones ahead of its tiles.
-      tma_prefetch_desc(&mQ);
-      tma_prefetch_desc(&mdO);
+      const bool clean = MASKED && *p.q_bad != 0;
+      const CUtensorMap* mapQ = clean ? &mQclean : &mQ;
+      const CUtensorMap* mapdO = clean ? &mdOclean : &mdO;
+      tma_prefetch_desc(mapQ);
+      tma_prefetch_desc(mapdO);
       const int krow = b * p.skv_pad + kv0;
       // Warm L2 with the first tiles of the CTA that will run next on this SM
       // (about one CTA lifetime from now): its start then waits on L2, not HBM.
@@ -207,6 +240,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tma_prefetch_3d(&mR, 0, nkv0, nbb);
           tma_prefetch_2d(&mV, nh * 128, nrow);
           tma_prefetch_2d(&mV, nh * 128 + 64, nrow);
+          if constexpr (MASKED) return;
           const int nfirst = p.causal ? max(0, nkv0 - p.q_offset) / BQ : 0;
           for (int k = nfirst; k < nfirst + 2 && k < nq; ++k) {
             tma_prefetch_3d(&mQ, nh * 192, k * BQ, nbb);
@@ -220,7 +254,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       bool ok = true;
       int gs = 0;  // global step: head u's step i is u * n_qt + i (stage ring, barrier phases)
       int kv_loads = 0;
-      for (int u = 0; u < G && ok; ++u) {
+      for (int u = 0; u < G && ok && !unseen; ++u) {
         const int h = hg * G + u;
         if (u > 0 && !mbar_wait_or_abort(kv_empty, (u - 1) & 1, abort_flag, 57)) {
           ok = false;
@@ -234,7 +268,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tma_load_2d(smem + OFF_V, &mV, kv_full, h * 128, krow);
         tma_load_2d(smem + OFF_V + KBOX, &mV, kv_full, h * 128 + 64, krow);
         ++kv_loads;
+        int next_qt = MASKED && n_qt > 0 ? kt_list[0] : 0;  // read a step ahead of its use
         for (int i = 0; i < n_qt; ++i, ++gs) {
+          const int this_qt = MASKED ? next_qt : qtile(i);
+          if (MASKED && i + 1 < n_qt) next_qt = kt_list[i + 1];
           if (u + 1 < G && i == max(0, n_qt - 4)) {
             // the next head's key/value tile, into L2 a few steps before the boundary load
             tma_prefetch_2d(&mK, (h + 1) * 128, krow);
@@ -248,15 +285,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             break;
           }
           LAGA_TRACE_POINT(dkdv, 20, gs);
-          const int q0 = qtile(i) * BQ;
+          const int q0 = this_qt * BQ;
           uint8_t* st = smem + OFF_STAGE + s * STAGE_BYTES;
           float* rows = reinterpret_cast<float*>(smem + OFF_ROWV) + s * 2 * BQ;
-          mbar_arrive_expect_tx(&q_full[s], STAGE_BYTES + 2 * ROWV_BYTES);
-          tma_load_3d(st, &mQ, &q_full[s], h * 192, q0, b);
-          tma_load_3d(st + QBOX, &mQ, &q_full[s], h * 192 + 64, q0, b);
-          tma_load_3d(st + 2 * QBOX, &mQ, &q_full[s], h * 192 + 128, q0, b);
-          tma_load_3d(st + Q_BYTES, &mdO, &q_full[s], h * 128, q0, b);
-          tma_load_3d(st + Q_BYTES + QBOX, &mdO, &q_full[s], h * 128 + 64, q0, b);
+          if constexpr (MASKED)  // published by the arrive below
+            reinterpret_cast<volatile int*>(smem + OFF_QT)[s] = this_qt;
+          mbar_arrive_expect_tx(&q_full[s], STAGE_BYTES + 2 * ROWV_BYTES + (MASKED ? BND_BYTES : 0));
+          tma_load_3d(st, mapQ, &q_full[s], h * 192, q0, b);
+          tma_load_3d(st + QBOX, mapQ, &q_full[s], h * 192 + 64, q0, b);
+          tma_load_3d(st + 2 * QBOX, mapQ, &q_full[s], h * 192 + 128, q0, b);
+          tma_load_3d(st + Q_BYTES, mapdO, &q_full[s], h * 128, q0, b);
+          tma_load_3d(st + Q_BYTES + QBOX, mapdO, &q_full[s], h * 128 + 64, q0, b);
+          if constexpr (MASKED)
+            bulk_load(smem + OFF_BND + s * BND_BYTES, p.rows + static_cast<long long>(b) * p.sq_pad + q0, BND_BYTES,
+                      &q_full[s]);
           const long long roff = (static_cast<long long>(b) * p.n_h + h) * p.sq_pad + q0;
           bulk_load(rows, p.lse2 + roff, ROWV_BYTES, &q_full[s]);
           bulk_load(rows + BQ, p.delta + roff, ROWV_BYTES, &q_full[s]);
@@ -283,7 +325,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       return warp_wait_or_abort(bar, parity, abort_flag, where);
     };
     bool all_ok = true;
-    for (int u = 0; u < G && all_ok; ++u) {
+    for (int u = 0; u < G && all_ok && !unseen; ++u) {
       if (!handoff(wait(kv_full, u & 1, 52))) { all_ok = false; break; }
       for (int i = -2; i < n_qt; ++i) {
         const int gs = u * n_qt + i;
@@ -352,7 +394,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #define DKDV_STAT_BEGIN(k)
 #define DKDV_STAT_END(k)
 #endif
-    for (int u = 0; u < G && ok; ++u) {
+    for (int u = 0; u < G && ok && !unseen; ++u) {
       if (!ready()) { ok = false; break; }  // head u's key/value tile
       if (lane == 0) LAGA_TRACE_POINT(dkdv, 4, u);
       for (int i = -2; i < n_qt; ++i) {
@@ -498,12 +540,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    for (int u = 0; u < G && ok; ++u) {
+    if (unseen) {
+      const uint32_t zero[32] = {};
+      for (int u = 0; u < G; ++u) {
+        drain_put(hg * G + u, false, zero, zero);
+        drain_put(hg * G + u, true, zero, zero);
+      }
+      const uint32_t w[16] = {};
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) put_chunk(w, &mdKR, hg * 64 + 32 * half + 16 * hh);
+    }
+    for (int u = 0; u < G && ok && !unseen; ++u) {
       const int h = hg * G + u;
       for (int i = 0; i < n_qt; ++i) {
         const int gs = u * n_qt + i;
         const int s = gs % NSTAGE;
-        const int qt = qtile(i);
+        const int qt = MASKED ? 0 : qtile(i);
         const int qc = qt * BQ + 32 * half;  // this thread's first query column
         const int q_min = qt < seg_tiles ? q_min0 : q_min1;
         if (!warp_wait(&q_full[s], (gs / NSTAGE) & 1, 61)) { ok = false; break; }
@@ -527,11 +579,44 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         const uint32_t s_addr = tmem + COL_S + 64u * (gs & 1) + lane_off;
         float pr[32];
+        uint32_t u[32];
         {
-          uint32_t u[32];
           tmem_ld32(s_addr + 32 * half, u);
           tmem_wait_ld();
-          if (qc >= q_min) {  // every query of the half-tile sees this key
+          if constexpr (MASKED) {
+            const int4* bnd2 = reinterpret_cast<const int4*>(smem + OFF_BND + s * BND_BYTES) + 16 * half;  // two rows each
+            const int2 mine = reinterpret_cast<const int2*>(bnd2)[lane];
+            const int k_first = kv0 + quarter * 32;  // the warp's first key row
+            const bool whole = __all_sync(0xffffffffu, (mine.x & 0x7fffffff) <= k_first && mine.y >= k_first + 32);
+            float slope2 = 0.f, dist = 0.f;
+            if constexpr (BIAS) {
+              const int qi = reinterpret_cast<const volatile int*>(smem + OFF_QT)[s] * BQ + 32 * half;
+              const int qp = (p.q_split > 0 && qi >= p.q_split) ? p.q_offset2 + (qi - p.q_split) : p.q_offset + qi;
+              slope2 = p.mod.slopes[h] * 1.4426950408889634f;
+              dist = static_cast<float>(qp - kv);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float raw = __uint_as_float(u[k]);
+              float t2;
+              if constexpr (CAP) {
+                u[k] = __float_as_uint(tanh_abs(raw * p.mod.u_scale));  // kept for dS's factor
+                t2 = fmaf(p.mod.cap_log2, __uint_as_float(u[k]), -lse[k]);
+              } else {
+                t2 = fmaf(raw, p.scale_log2, -lse[k]);
+              }
+              if constexpr (BIAS) t2 = fmaf(-slope2, fabsf(dist + static_cast<float>(k)), t2);
+              pr[k] = ex2_approx(t2);
+            }
+            if (!whole) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const int4 v = bnd2[k];  // rows 2k, 2k + 1
+                if (kv < (v.x & 0x7fffffff) || kv >= v.y) pr[2 * k] = 0.f;
+                if (kv < (v.z & 0x7fffffff) || kv >= v.w) pr[2 * k + 1] = 0.f;
+              }
+            }
+          } else if (qc >= q_min) {  // every query of the half-tile sees this key
 #pragma unroll
             for (int k = 0; k < 32; ++k) pr[k] = ex2_approx(fmaf(__uint_as_float(u[k]), p.scale_log2, -lse[k]));
           } else {
@@ -547,6 +632,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           // P^T packed in place over this half's own score columns (query pair k -> column
           // 32*half + k), so the other warpgroup's scores are never overwritten unread
           tmem_st16(s_addr + 32 * half, w);
+          if constexpr (CAP) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float th = __uint_as_float(u[k]);
+              pr[k] *= fmaf(-th, th, 1.f);  // d capped / d score
+            }
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -558,7 +650,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tc_fence_after();
         const uint32_t dp_addr = tmem + COL_DP + lane_off;
         {
-          uint32_t u[32];
           tmem_ld32(dp_addr + 32 * half, u);
           tmem_wait_ld();
           tc_fence_before();
@@ -640,7 +731,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 }  // namespace
 
 LaunchResult tc_attn_bwd_dkdv(const Dims& d, const bf16* q, const bf16* k_rope, const bf16* dout,
-                              const BwdWorkspace& w, cudaStream_t st) {
+                              const BwdWorkspace& w, cudaStream_t st, const MaskArgs* mask, const bf16* q_clean,
+                              const bf16* dout_clean) {
   LaunchResult r;
   CUtensorMap mQ, mK, mR, mV, mdO;
   const uint32_t qbox[3] = {64, BQ, 1};
@@ -656,6 +748,18 @@ LaunchResult tc_attn_bwd_dkdv(const Dims& d, const bf16* q, const bf16* k_rope, 
     const uint64_t strides[2] = {inner * 2, inner * 2 * d.Sq};
     r.cu = make_tmap(&mdO, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dout, dims, strides, qbox,
                      CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  CUtensorMap mQc = mQ, mdOc = mdO;
+  if (mask && r.cu == CUDA_SUCCESS) {
+    const uint64_t qi = static_cast<uint64_t>(d.n_h) * 192, oi = static_cast<uint64_t>(d.n_h) * 128;
+    const uint64_t qd[3] = {qi, static_cast<uint64_t>(d.Sq), static_cast<uint64_t>(d.B)};
+    const uint64_t qs[2] = {qi * 2, qi * 2 * d.Sq};
+    const uint64_t od[3] = {oi, static_cast<uint64_t>(d.Sq), static_cast<uint64_t>(d.B)};
+    const uint64_t os[2] = {oi * 2, oi * 2 * d.Sq};
+    r.cu = make_tmap(&mQc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q_clean, qd, qs, qbox, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (r.cu == CUDA_SUCCESS)
+      r.cu = make_tmap(&mdOc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dout_clean, od, os, qbox,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
   }
   const uint64_t kv_inner = static_cast<uint64_t>(d.n_h) * 128;
   const uint64_t kv_rows = static_cast<uint64_t>(d.B) * d.skv_pad;
@@ -721,12 +825,29 @@ LaunchResult tc_attn_bwd_dkdv(const Dims& d, const bf16* q, const bf16* k_rope, 
   p.G = G;
   p.n_hg = d.n_h / G;
   p.successor = sm_count();
-  r.err = cudaFuncSetAttribute(attn_bwd_dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  using M = CUtensorMap;
+  void (*kern)(M, M, M, M, M, M, M, M, M, M, Params) = attn_bwd_dkdv_kernel<-1>;
+  int smem = SMEM_BYTES;
+  if (mask) {
+    p.rows = mask->meta.rows;
+    p.kt_count = mask->meta.kt_count;
+    p.kt_list = mask->meta.kt_list;
+    p.q_bad = mask->meta.q_bad;
+    p.mod = mod_params(d, mask->mods);
+    smem = SMEM_BYTES_MASKED;
+    switch (mod_of(mask->mods)) {
+      case 0: kern = attn_bwd_dkdv_kernel<0>; break;
+      case kModCap: kern = attn_bwd_dkdv_kernel<kModCap>; break;
+      case kModBias: kern = attn_bwd_dkdv_kernel<kModBias>; break;
+      default: kern = attn_bwd_dkdv_kernel<kModCap | kModBias>; break;
+    }
+  }
+  r.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (r.err != cudaSuccess) {
     r.what = "cudaFuncSetAttribute(attn_bwd_dkdv)";
     return r;
   }
-  attn_bwd_dkdv_kernel<<<dim3(d.skv_pad / BKV, p.n_hg, d.B), NTHREADS, SMEM_BYTES, st>>>(mQ, mK, mR, mV, mdO, mdK, mdV, mdKR, p);
+  kern<<<dim3(d.skv_pad / BKV, p.n_hg, d.B), NTHREADS, smem, st>>>(mQ, mK, mR, mV, mdO, mdK, mdV, mdKR, mQc, mdOc, p);
   r.err = cudaGetLastError();
   if (r.err != cudaSuccess) r.what = "attn_bwd_dkdv_kernel launch";
   return r;

@@ -27,8 +27,13 @@
 //   warps 2..9  two warpgroups; each thread owns one query row (TMEM lane) and
 //               half of the tile's 128 key columns: P, dS, and half the epilogue
 //   warp 10     lane 0: TMA for value tiles
+//
+// Masked instances (MOD >= 0): the CTA walks the key tiles between the lowest and the
+// highest key its rows see, as in the forward; with a cap, dS takes the factor
+// 1 - tanh^2 of its score.
 #include "internal.h"
 #include "ptx.cuh"
+#include "score_mod.cuh"
 
 LAGA_TRACE_DEFINE(dq)
 
@@ -68,6 +73,10 @@ struct Params {
   const float* lse2;
   const float* delta;
   const bf16* dout;  // [B][Sq][n_h][128]
+  // masked instances
+  const int2* rows;     // [B][sq_pad] visible interval of each query row
+  const int2* q_tiles;  // [B][n_q_tiles] {first key tile, key tiles}
+  ModParams mod;
 };
 
 // TMEM column of packed bf16 chunk k (16 keys) of dS(j): warpgroup g packs its
@@ -86,6 +95,7 @@ __device__ __forceinline__ int n_kv_tiles(const Params& p, int t) {
   return last / BKV + 1;
 }
 
+template <int MOD>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                        const __grid_constant__ CUtensorMap mR, const __grid_constant__ CUtensorMap mV,
@@ -116,7 +126,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int t = p.n_q_tiles - 1 - static_cast<int>(blockIdx.x);  // heaviest tiles first
   const int h = blockIdx.y;
   const int b = blockIdx.z;
-  const int n_kv = n_kv_tiles(p, t);
+  constexpr bool MASKED = MOD >= 0;
+  constexpr bool CAP = MASKED && (MOD & kModCap) != 0, BIAS = MASKED && (MOD & kModBias) != 0;
+  int n_kv, j0 = 0;  // key tiles walked: [j0, j0 + n_kv)
+  if constexpr (MASKED) {
+    const int2 span = p.q_tiles[b * p.n_q_tiles + t];
+    j0 = span.x;
+    n_kv = span.y;
+  } else {
+    n_kv = n_kv_tiles(p, t);
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -163,10 +182,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!mbar_wait_or_abort(&k_empty[s], ((j / K_STAGES) & 1) ^ 1, abort_flag, 71)) break;
         uint8_t* dst = smem + OFF_K + s * K_BYTES;
         mbar_arrive_expect_tx(&k_full[s], K_BYTES);
-        const int row = b * p.skv_pad + j * BKV;
+        const int row = b * p.skv_pad + (j0 + j) * BKV;
         tma_load_2d(dst, &mK, &k_full[s], h * 128, row);
         tma_load_2d(dst + BOX, &mK, &k_full[s], h * 128 + 64, row);
-        tma_load_3d(dst + 2 * BOX, &mR, &k_full[s], 0, j * BKV, b);
+        tma_load_3d(dst + 2 * BOX, &mR, &k_full[s], 0, (j0 + j) * BKV, b);
       }
       if (j < n_kv) {
         mbar_drain(q_full, 0);
@@ -183,7 +202,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!mbar_wait_or_abort(&v_empty[s], ((j / V_STAGES) & 1) ^ 1, abort_flag, 72)) break;
         uint8_t* dst = smem + OFF_V + s * V_BYTES;
         mbar_arrive_expect_tx(&v_full[s], V_BYTES);
-        const int row = b * p.skv_pad + j * BKV;
+        const int row = b * p.skv_pad + (j0 + j) * BKV;
         tma_load_2d(dst, &mV, &v_full[s], h * 128, row);
         tma_load_2d(dst + BOX, &mV, &v_full[s], h * 128 + 64, row);
       }
@@ -297,6 +316,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const float lse2 = p.lse2[roff];  // +inf on padded rows: P = 0 there
     const float Drow = p.delta[roff];
     const float sl2 = p.scale_log2;
+    int lo = 0, hi = 0;  // masked: this row sees keys [lo, hi)
+    float slope2 = 0.f, pos = 0.f;
+    if constexpr (MASKED) {
+      const int2 v = p.rows[static_cast<long long>(b) * p.sq_pad + q_row];
+      lo = v.x & 0x7fffffff;
+      hi = v.y;
+      if constexpr (BIAS) {
+        slope2 = p.mod.slopes[h] * 1.4426950408889634f;
+        pos = static_cast<float>(q_pos(p, q_row) - j0 * BKV);
+      }
+    }
     bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
       bool w = true;
@@ -339,9 +369,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(s_free);  // dP(j) may now overwrite S(j)
-      const int kv_first = j * BKV + 64 * half;  // this thread's first key column
+      const int kv_first = (j0 + j) * BKV + 64 * half;  // this thread's first key column
       float pr[64];
-      if (kv_first + 63 <= limit) {  // every key of the half-tile visible
+      bool partial = false;  // masked: some row of the warp does not see every key of the half-tile
+      if constexpr (MASKED) {
+        partial = !__all_sync(0xffffffffu, lo <= kv_first && hi >= kv_first + 64);
+        const unsigned first = static_cast<unsigned>(lo - kv_first), width = static_cast<unsigned>(max(hi - lo, 0));
+        const float dist = pos - static_cast<float>(j * BKV + 64 * half);
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          const float raw = __uint_as_float(x[k]);
+          float th = 0.f, t2;
+          if constexpr (CAP) {
+            th = tanh_abs(raw * p.mod.u_scale);
+            t2 = fmaf(p.mod.cap_log2, th, -lse2);
+          } else {
+            t2 = fmaf(raw, sl2, -lse2);
+          }
+          if constexpr (BIAS) t2 = fmaf(-slope2, fabsf(dist - static_cast<float>(k)), t2);
+          float e = ex2_approx(t2);
+          if constexpr (CAP) e *= fmaf(-th, th, 1.f);  // d capped / d score
+          pr[k] = e;
+        }
+        if (partial) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (static_cast<unsigned>(k) - first >= width) pr[k] = 0.f;
+        }
+      } else if (kv_first + 63 <= limit) {  // every key of the half-tile visible
 #pragma unroll
         for (int k = 0; k < 64; ++k) pr[k] = ex2_approx(fmaf(__uint_as_float(x[k]), sl2, -lse2));
       } else {
@@ -355,10 +410,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tmem_ld32(buf + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
       tmem_wait_ld();
       uint32_t w[32];
+      if (MASKED && partial) {  // a masked key's dP may be non-finite (a row of dO is): dS is 0 all the same
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        w[k] = pack_bf16x2(pr[2 * k] * (__uint_as_float(x[2 * k]) - Drow),
-                           pr[2 * k + 1] * (__uint_as_float(x[2 * k + 1]) - Drow));
+        for (int k = 0; k < 32; ++k) {
+          const float d0 = pr[2 * k] == 0.f ? 0.f : pr[2 * k] * (__uint_as_float(x[2 * k]) - Drow);
+          const float d1 = pr[2 * k + 1] == 0.f ? 0.f : pr[2 * k + 1] * (__uint_as_float(x[2 * k + 1]) - Drow);
+          w[k] = pack_bf16x2(d0, d1);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          w[k] = pack_bf16x2(pr[2 * k] * (__uint_as_float(x[2 * k]) - Drow),
+                             pr[2 * k + 1] * (__uint_as_float(x[2 * k + 1]) - Drow));
+      }
       // dS packed into the first 32 of this warpgroup's own 64 dP columns
       tmem_st32(buf, w);
       tmem_wait_st();
@@ -420,7 +484,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 }  // namespace
 
 LaunchResult tc_attn_bwd_dq(const Dims& d, const bf16* q, const bf16* k_rope, const bf16* dout,
-                            const BwdWorkspace& w, bf16* dq, cudaStream_t st) {
+                            const BwdWorkspace& w, bf16* dq, cudaStream_t st, const MaskArgs* mask) {
   LaunchResult r;
   CUtensorMap mQ, mK, mR, mV;
   const uint32_t qbox[3] = {64, BQ, 1};
@@ -478,12 +542,24 @@ LaunchResult tc_attn_bwd_dq(const Dims& d, const bf16* q, const bf16* k_rope, co
   p.lse2 = w.lse2;
   p.delta = w.delta;
   p.dout = dout;
-  r.err = cudaFuncSetAttribute(attn_bwd_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Params) = attn_bwd_dq_kernel<-1>;
+  if (mask) {
+    p.rows = mask->meta.rows;
+    p.q_tiles = mask->meta.q_tiles;
+    p.mod = mod_params(d, mask->mods);
+    switch (mod_of(mask->mods)) {
+      case 0: kern = attn_bwd_dq_kernel<0>; break;
+      case kModCap: kern = attn_bwd_dq_kernel<kModCap>; break;
+      case kModBias: kern = attn_bwd_dq_kernel<kModBias>; break;
+      default: kern = attn_bwd_dq_kernel<kModCap | kModBias>; break;
+    }
+  }
+  r.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (r.err != cudaSuccess) {
     r.what = "cudaFuncSetAttribute(attn_bwd_dq)";
     return r;
   }
-  attn_bwd_dq_kernel<<<dim3(p.n_q_tiles, d.n_h, d.B), NTHREADS, SMEM_BYTES, st>>>(mQ, mK, mR, mV, mdQ, p);
+  kern<<<dim3(p.n_q_tiles, d.n_h, d.B), NTHREADS, SMEM_BYTES, st>>>(mQ, mK, mR, mV, mdQ, p);
   r.err = cudaGetLastError();
   if (r.err != cudaSuccess) r.what = "attn_bwd_dq_kernel launch";
   return r;

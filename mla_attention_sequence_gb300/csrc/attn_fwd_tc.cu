@@ -24,8 +24,14 @@
 // buffer that PV(j) has just read. The softmax warps then run back to back and
 // the step costs the larger of the MMA time and the softmax time rather than a
 // chain of both.
+//
+// Masked instances (MOD >= 0): each query row sees an interval of keys. The CTA walks
+// the 128-key tiles from the lowest key any of its rows sees to the highest; a key tile
+// that every row of a warp sees whole takes no compares. The cap and the distance bias
+// turn the raw scores into exponents before the row maximum is taken.
 #include "internal.h"
 #include "ptx.cuh"
+#include "score_mod.cuh"
 
 LAGA_TRACE_DEFINE(fwd)
 
@@ -64,6 +70,10 @@ struct FwdParams {
   int q_split, q_offset2;  // second query segment (q_split = 0: none)
   float scale_log2;  // softmax scale * log2(e), > 0
   float* lse;
+  // masked instances
+  const int2* rows;     // [B][sq_pad] visible interval of each query row
+  const int2* q_tiles;  // [B][n_q_tiles] {first key tile, key tiles}
+  ModParams mod;
 };
 
 // Absolute position of local query row i (a query tile never straddles the
@@ -77,6 +87,7 @@ __device__ __forceinline__ int n_kv_tiles(const FwdParams& p, int t) {
   return last / BKV + 1;
 }
 
+template <int MOD>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                     const __grid_constant__ CUtensorMap mR, const __grid_constant__ CUtensorMap mV,
@@ -109,7 +120,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int t = p.n_q_tiles - 1 - static_cast<int>(blockIdx.x);
   const int h = blockIdx.y;
   const int b = blockIdx.z;
-  const int n_kv = n_kv_tiles(p, t);
+  constexpr bool MASKED = MOD >= 0;
+  constexpr bool CAP = MASKED && (MOD & kModCap) != 0, BIAS = MASKED && (MOD & kModBias) != 0;
+  int n_kv, j0 = 0;  // key tiles walked: [j0, j0 + n_kv)
+  if constexpr (MASKED) {
+    const int2 span = p.q_tiles[b * p.n_q_tiles + t];
+    j0 = span.x;
+    n_kv = span.y;
+  } else {
+    n_kv = n_kv_tiles(p, t);
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -155,10 +175,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         LAGA_TRACE_POINT(fwd, 20, j);
         uint8_t* dst = sK + s * K_BYTES;
         mbar_arrive_expect_tx(&k_full[s], K_BYTES);
-        const int row = b * p.skv_pad + j * BKV;
+        const int row = b * p.skv_pad + (j0 + j) * BKV;
         tma_load_2d(dst, &mK, &k_full[s], h * 128, row);
         tma_load_2d(dst + BOX, &mK, &k_full[s], h * 128 + 64, row);
-        tma_load_3d(dst + 2 * BOX, &mR, &k_full[s], 0, j * BKV, b);
+        tma_load_3d(dst + 2 * BOX, &mR, &k_full[s], 0, (j0 + j) * BKV, b);
         if (j + PREFETCH < n_kv) {
           tma_prefetch_2d(&mK, h * 128, row + PREFETCH * BKV);
           tma_prefetch_2d(&mK, h * 128 + 64, row + PREFETCH * BKV);
@@ -181,7 +201,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         LAGA_TRACE_POINT(fwd, 21, j);
         uint8_t* dst = sV + s * V_BYTES;
         mbar_arrive_expect_tx(&v_full[s], V_BYTES);
-        const int row = b * p.skv_pad + j * BKV;
+        const int row = b * p.skv_pad + (j0 + j) * BKV;
         tma_load_2d(dst, &mV, &v_full[s], h * 128, row);
         tma_load_2d(dst + BOX, &mV, &v_full[s], h * 128 + 64, row);
         if (j + PREFETCH < n_kv) {
@@ -308,6 +328,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const int limit = p.causal ? q_pos(p, q_row) : p.S - 1;  // last visible key
     const float sl2 = p.scale_log2;
+    int lo = 0, hi = 0;     // masked: this row sees keys [lo, hi)
+    bool poisoned = false;  // masked: one of them is not finite
+    float slope2 = 0.f, pos = 0.f;
+    if constexpr (MASKED) {
+      const int2 v = p.rows[static_cast<long long>(b) * (p.n_q_tiles * BQ) + q_row];
+      poisoned = v.x < 0;
+      lo = v.x & 0x7fffffff;
+      hi = v.y;
+      if constexpr (BIAS) {
+        slope2 = p.mod.slopes[h] * LOG2E;
+        pos = static_cast<float>(q_pos(p, q_row) - j0 * BKV);
+      }
+    }
     float m_run = -INFINITY;  // running max of the scaled (log2-domain) scores
     float l_run = 0.f;
     bool ok = true;
@@ -333,8 +366,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
       tmem_wait_ld();
-      const int kv0 = j * BKV;
-      if (kv0 + BKV - 1 > limit) {
+      const int kv0 = (j0 + j) * BKV;
+      if constexpr (CAP || BIAS) {  // raw scores -> exponents
+        const float dist = pos - static_cast<float>(j * BKV);  // to the tile's first key
+#pragma unroll
+        for (int i = 0; i < 128; ++i) {
+          float t2 = __uint_as_float(x[i]);
+          t2 = CAP ? p.mod.cap_log2 * tanh_abs(t2 * p.mod.u_scale) : t2 * sl2;
+          if constexpr (BIAS) t2 = fmaf(-slope2, fabsf(dist - static_cast<float>(i)), t2);
+          x[i] = __float_as_uint(t2);
+        }
+      }
+      if constexpr (MASKED) {
+        if (!__all_sync(0xffffffffu, lo <= kv0 && hi >= kv0 + BKV)) {
+          const unsigned first = static_cast<unsigned>(lo - kv0), width = static_cast<unsigned>(max(hi - lo, 0));
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (static_cast<unsigned>(i) - first >= width) x[i] = 0xff800000u;  // -inf
+        }
+      } else if (kv0 + BKV - 1 > limit) {
 #pragma unroll
         for (int i = 0; i < 128; ++i)
           if (kv0 + i > limit) x[i] = 0xff800000u;  // -inf
@@ -347,10 +397,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
       for (int i = 4; i < 128; i += 8) {
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int a = 0; a < 4; ++a) {
+          if constexpr (MASKED) {  // exactly the tile's 128 scores: a far biased row's maximum may be any number
+            if (i + 2 * a >= 128) continue;
+          }
           m4[a] = max3f(m4[a], __uint_as_float(x[i + 2 * a]), __uint_as_float(x[i + 2 * a + 1]));
+        }
       }
-      const float mt = max3f(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * sl2;
+      constexpr bool EXPONENTS = CAP || BIAS;  // x holds exponents, not raw scores
+      const float mt = max3f(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * (EXPONENTS ? 1.f : sl2);
       float m_use = m_run;
       float alpha = 1.f;
       bool rescale = false;
@@ -367,8 +422,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       uint32_t pk[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) {
-        const float p0 = ex2_approx(fmaf(__uint_as_float(x[2 * i]), sl2, neg_m));
-        const float p1 = ex2_approx(fmaf(__uint_as_float(x[2 * i + 1]), sl2, neg_m));
+        const float s0 = __uint_as_float(x[2 * i]), s1 = __uint_as_float(x[2 * i + 1]);
+        const float p0 = ex2_approx(EXPONENTS ? s0 + neg_m : fmaf(s0, sl2, neg_m));
+        const float p1 = ex2_approx(EXPONENTS ? s1 + neg_m : fmaf(s1, sl2, neg_m));
         sum2[i & 1] = add_f32x2(sum2[i & 1], make_float2(p0, p1));
         pk[i] = pack_bf16x2(p0, p1);
       }
@@ -412,7 +468,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // 16-byte chunk k of row r at r * 128 + ((k ^ (r & 7)) << 4)); rows past Sq
       // are clipped by the map.
       const uint32_t o_addr = tmem + COL_O + lane_off;
-      const float inv = 1.f / l_run;
+      float inv = 1.f / l_run;
+      if constexpr (MASKED) {
+        if (l_run == 0.f) inv = 0.f;  // the row sees nothing: out = 0, lse = -inf
+        if (poisoned) inv = NAN;
+      }
       uint8_t* stage = sQ + quarter * 8192;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
@@ -440,9 +500,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         bulk_wait_read_all();  // shared memory must not go away under a store
       }
       __syncwarp();
-      if (q_row < p.Sq)
-        p.lse[(static_cast<long long>(b) * p.n_h + h) * p.Sq + q_row] =
-            (m_run + __log2f(l_run)) * 0.6931471805599453f;
+      if (q_row < p.Sq) {
+        float lse = (m_run + __log2f(l_run)) * 0.6931471805599453f;
+        if constexpr (MASKED) {
+          if (l_run == 0.f) lse = -INFINITY;
+          if (poisoned) lse = NAN;
+        }
+        p.lse[(static_cast<long long>(b) * p.n_h + h) * p.Sq + q_row] = lse;
+      }
     }
   }
 
@@ -463,7 +528,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 // The [rows][64] boxes of the operands: 3D q map over [B][Sq][n_h*192], 2D maps
 // over the [B*skv_pad][n_h*128] K/V workspace, 3D k_rope map over [B][S][64].
 LaunchResult tc_attn_fwd(const Dims& d, const bf16* q, const bf16* k_ws, const bf16* v_ws, const bf16* k_rope,
-                         bf16* out, float* lse, cudaStream_t st) {
+                         bf16* out, float* lse, cudaStream_t st, const MaskArgs* mask) {
   LaunchResult r;
   CUtensorMap mQ, mK, mR, mV;
   {
@@ -515,12 +580,24 @@ LaunchResult tc_attn_fwd(const Dims& d, const bf16* q, const bf16* k_ws, const b
   p.scale_log2 = d.scale * LOG2E;
   p.lse = lse;
   p.status = device_status_ptr();
-  r.err = cudaFuncSetAttribute(attn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, FwdParams) = attn_fwd_kernel<-1>;
+  if (mask) {
+    p.rows = mask->meta.rows;
+    p.q_tiles = mask->meta.q_tiles;
+    p.mod = mod_params(d, mask->mods);
+    switch (mod_of(mask->mods)) {
+      case 0: kern = attn_fwd_kernel<0>; break;
+      case kModCap: kern = attn_fwd_kernel<kModCap>; break;
+      case kModBias: kern = attn_fwd_kernel<kModBias>; break;
+      default: kern = attn_fwd_kernel<kModCap | kModBias>; break;
+    }
+  }
+  r.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (r.err != cudaSuccess) {
     r.what = "cudaFuncSetAttribute(attn_fwd)";
     return r;
   }
-  attn_fwd_kernel<<<dim3(p.n_q_tiles, d.n_h, d.B), NTHREADS, SMEM_BYTES, st>>>(mQ, mK, mR, mV, mO, p);
+  kern<<<dim3(p.n_q_tiles, d.n_h, d.B), NTHREADS, SMEM_BYTES, st>>>(mQ, mK, mR, mV, mO, p);
   r.err = cudaGetLastError();
   if (r.err != cudaSuccess) r.what = "attn_fwd_kernel launch";
   return r;

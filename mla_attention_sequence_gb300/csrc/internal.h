@@ -78,8 +78,37 @@ LaunchResult tc_recon_bwd_dc(const Dims& d, const bf16* dk_ws, const bf16* dv_ws
 LaunchResult tc_recon_bwd_dw(const Dims& d, const bf16* c_kv, const bf16* dk_ws, const bf16* dv_ws, bf16* dW_UK,
                              bf16* dW_UV, cudaStream_t st);
 
+// ---- masked attention (key intervals per query row, capped scores, a bias by distance)
+//
+// What the mask's device arrays become before the attention kernels run (mask_prep.cu).
+struct MaskMeta {
+  // [B][sq_pad] {first visible key, one past the last}, clamped to the existing (and, when
+  // causal, the past) keys; {0, 0}: the row sees nothing. Bit 31 of the first: some key that
+  // the row sees holds a non-finite latent value (the row's result is NaN).
+  const int2* rows;
+  const int2* q_tiles;  // [B][sq_pad / 128] {first 128-key tile, tiles >= 1} of a 128-row query tile
+  const int2* q_hull;   // [B][sq_pad / 64] {lowest first key, highest one-past-last} of a 64-row tile
+  const int* kt_count;  // [B][skv_pad / 128] 64-row query tiles that may see a key tile
+  const int* kt_list;   // [B][skv_pad / 128][sq_pad / 64] which, ascending
+  int* q_bad;           // nonzero: some row of q or dout that the backward reads is not finite
+};
+
+struct ScoreMods {
+  float cap;            // > 0: s becomes cap tanh(s / cap)
+  const float* slopes;  // [n_h] or null: s -= slope_h |position - key|
+};
+// The attention kernels' instances: -1 the plain causal ones; >= 0 masked, bits as below.
+constexpr int kModCap = 1, kModBias = 2;
+inline int mod_of(const ScoreMods& m) { return (m.cap > 0.f ? kModCap : 0) | (m.slopes ? kModBias : 0); }
+
+struct MaskArgs {
+  MaskMeta meta;
+  ScoreMods mods;
+};
+
+// mask == nullptr: the plain causal (or full) attention.
 LaunchResult tc_attn_fwd(const Dims& d, const bf16* q, const bf16* k_ws, const bf16* v_ws, const bf16* k_rope,
-                         bf16* out, float* lse, cudaStream_t st);
+                         bf16* out, float* lse, cudaStream_t st, const MaskArgs* mask = nullptr);
 LaunchResult tc_attn_fwd_fused(const Dims& d, const bf16* q, const bf16* c_kv, const bf16* W_UK,
                                const bf16* W_UV, const bf16* k_rope, bf16* out, float* lse, cudaStream_t st);
 
@@ -100,11 +129,13 @@ int dkdv_heads_per_cta(int n_h);
 LaunchResult tc_bwd_pre(const Dims& d, const bf16* out, const bf16* dout, const float* lse, const BwdWorkspace& w,
                         cudaStream_t st);
 // dV, dK_nope (bf16) and per-head RoPE-key gradients (fp32) into the workspace.
+// With a mask: q_clean / dout_clean replace q / dout when *mask->meta.q_bad is set.
 LaunchResult tc_attn_bwd_dkdv(const Dims& d, const bf16* q, const bf16* k_rope, const bf16* dout,
-                              const BwdWorkspace& w, cudaStream_t st);
+                              const BwdWorkspace& w, cudaStream_t st, const MaskArgs* mask = nullptr,
+                              const bf16* q_clean = nullptr, const bf16* dout_clean = nullptr);
 // dq, written once per element from a TMEM accumulator.
 LaunchResult tc_attn_bwd_dq(const Dims& d, const bf16* q, const bf16* k_rope, const bf16* dout,
-                            const BwdWorkspace& w, bf16* dq, cudaStream_t st);
+                            const BwdWorkspace& w, bf16* dq, cudaStream_t st, const MaskArgs* mask = nullptr);
 // dk_rope = sum over heads of the per-head RoPE-key gradients.
 LaunchResult tc_bwd_post(const Dims& d, const BwdWorkspace& w, bf16* dk_rope, cudaStream_t st);
 

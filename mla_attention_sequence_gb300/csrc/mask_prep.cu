@@ -1,0 +1,476 @@
+// What the masked attention runs before its kernels: the visible interval of every
+// query row, the tiles that follow from it, and copies of the inputs in which rows
+// holding a non-finite value are zero.
+//
+// Why the copies: the attention kernels give a masked score the weight 0 and then
+// multiply it by the key's V row (forward), or by the query's q and dO rows (dK, dV).
+// 0 times a NaN is a NaN, so one uninitialised padding row would reach every row of
+// its tile. With such rows zeroed a masked weight contributes exactly nothing; the
+// query rows that do see such a key, and the keys that are seen by such a query, get
+// NaN through the row statistics instead (rows' bit 31 in the forward, lse in the
+// backward). The latent is small (d_c + d_rope values per key, shared by all heads),
+// so its copy is always made: 2 x 19 MB at 16384 keys. q and dout are copied only when
+// a row of theirs is non-finite, which the pass that computes D sees.
+#include "internal.h"
+#include "mask.h"
+
+#include <type_traits>
+
+namespace laga {
+namespace {
+
+using ll = long long;
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(bf16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
+// whether any of eight packed bf16 is infinite or NaN
+__device__ __forceinline__ bool bad_bf16x2(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ bool bad_bf16x8(uint4 v) {
+  return bad_bf16x2(v.x) || bad_bf16x2(v.y) || bad_bf16x2(v.z) || bad_bf16x2(v.w);
+}
+
+// Latent rows -> clean copies; one CTA per 32 keys of a batch element, a warp per row
+// in turn. bad[b][word] bit r: key 32 * word + r holds a non-finite value.
+// 16-byte loads when the rows allow it (VEC), else one value a lane.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) mask_keys_kernel(int S, int d_c, int d_rope, const T* __restrict__ c,
+                                                        const T* __restrict__ r, T* __restrict__ c_out,
+                                                        T* __restrict__ r_out, uint32_t* __restrict__ bad) {
+  __shared__ uint32_t mask;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
+  if (threadIdx.x == 0) mask = 0u;
+  __syncthreads();
+  constexpr int PER = 16 / static_cast<int>(sizeof(T));
+  for (int k = warp; k < 32; k += 8) {
+    const int j = blockIdx.x * 32 + k;
+    if (j >= S) break;
+    const ll row = static_cast<ll>(b) * S + j;
+    const T *cs = c + row * d_c, *rs = r + row * d_rope;
+    T *cd = c_out + row * d_c, *rd = r_out + row * d_rope;
+    bool is_bad = false;
+    if constexpr (VEC) {
+      const int nc = d_c / PER, nr = d_rope / PER;
+      for (int i = lane; i < nc + nr; i += 32) {
+        const uint4 v = i < nc ? reinterpret_cast<const uint4*>(cs)[i] : reinterpret_cast<const uint4*>(rs)[i - nc];
+        if constexpr (sizeof(T) == 2)
+          is_bad |= bad_bf16x8(v);
+        else
+          is_bad |= !finite(__uint_as_float(v.x)) || !finite(__uint_as_float(v.y)) || !finite(__uint_as_float(v.z)) ||
+                    !finite(__uint_as_float(v.w));
+      }
+      is_bad = __any_sync(0xffffffffu, is_bad);
+      for (int i = lane; i < nc + nr; i += 32) {  // the row's second reading is an L1 hit
+        uint4 v = i < nc ? reinterpret_cast<const uint4*>(cs)[i] : reinterpret_cast<const uint4*>(rs)[i - nc];
+        if (is_bad) v = make_uint4(0u, 0u, 0u, 0u);
+        if (i < nc)
+          reinterpret_cast<uint4*>(cd)[i] = v;
+        else
+          reinterpret_cast<uint4*>(rd)[i - nc] = v;
+      }
+    } else {
+      for (int i = lane; i < d_c + d_rope; i += 32) is_bad |= !finite(to_f(i < d_c ? cs[i] : rs[i - d_c]));
+      is_bad = __any_sync(0xffffffffu, is_bad);
+      for (int i = lane; i < d_c + d_rope; i += 32) {
+        T v = i < d_c ? cs[i] : rs[i - d_c];
+        if (is_bad) v = static_cast<T>(0.f);
+        if (i < d_c)
+          cd[i] = v;
+        else
+          rd[i - d_c] = v;
+      }
+    }
+    if (is_bad && lane == 0) atomicOr(&mask, 1u << k);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) bad[static_cast<ll>(b) * gridDim.x + blockIdx.x] = mask;
+}
+
+__device__ __forceinline__ int position(const Dims& d, int i) {
+  return (d.q_split > 0 && i >= d.q_split) ? d.q_offset2 + (i - d.q_split) : d.q_offset + i;
+}
+
+// One CTA of 128 threads per 128-row query tile: thread = row.
+__global__ void __launch_bounds__(128) mask_rows_kernel(Dims d, const int* __restrict__ key_lo,
+                                                        const int* __restrict__ key_hi,
+                                                        const uint32_t* __restrict__ bad, int bad_words,
+                                                        int2* __restrict__ rows, int2* __restrict__ q_tiles,
+                                                        int2* __restrict__ q_hull, int* __restrict__ q_bad) {
+  __shared__ int s_lo[4], s_hi[4];
+  const int t = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = t * 128 + threadIdx.x;
+  if (t == 0 && b == 0 && threadIdx.x == 0) *q_bad = 0;
+  int lo = 0, hi = 0;
+  if (i < d.Sq) {
+    const ll at = static_cast<ll>(b) * d.Sq + i;
+    lo = key_lo ? max(0, key_lo[at]) : 0;
+    hi = key_hi ? min(d.S, key_hi[at]) : d.S;
+    if (d.causal) hi = min(hi, position(d, i) + 1);
+    if (lo >= hi) lo = hi = 0;
+  }
+  // rows that see a bad key: only when there is one in this batch element at all
+  const uint32_t* words = bad + static_cast<ll>(b) * bad_words;
+  bool any = false;
+  for (int w = threadIdx.x; w < bad_words; w += 128) any |= words[w] != 0u;
+  bool poisoned = false;
+  if (__syncthreads_or(any) && lo < hi) {
+    const int w0 = lo >> 5, w1 = (hi - 1) >> 5;
+    for (int w = w0; w <= w1 && !poisoned; ++w) {
+      uint32_t m = words[w];
+      if (w == w0) m &= ~0u << (lo & 31);
+      if (w == w1) m &= ~0u >> (31 - ((hi - 1) & 31));
+      poisoned = m != 0u;
+    }
+  }
+  rows[static_cast<ll>(b) * d.sq_pad + i] = make_int2(poisoned ? lo | static_cast<int>(0x80000000u) : lo, hi);
+  const bool some = lo < hi;
+  const int wlo = __reduce_min_sync(0xffffffffu, some ? lo : 0x7fffffff);
+  const int whi = __reduce_max_sync(0xffffffffu, some ? hi : 0);
+  if (lane == 0) {
+    s_lo[warp] = wlo;
+    s_hi[warp] = whi;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2)
+    q_hull[static_cast<ll>(b) * (d.sq_pad / 64) + t * 2 + threadIdx.x] =
+        make_int2(min(s_lo[2 * threadIdx.x], s_lo[2 * threadIdx.x + 1]),
+                  max(s_hi[2 * threadIdx.x], s_hi[2 * threadIdx.x + 1]));
+  if (threadIdx.x == 0) {
+    const int l = min(min(s_lo[0], s_lo[1]), min(s_lo[2], s_lo[3]));
+    const int h = max(max(s_hi[0], s_hi[1]), max(s_hi[2], s_hi[3]));
+    // a tile whose rows see nothing still walks one (wholly masked) key tile
+    const int first = l < h ? l / 128 : 0, end = l < h ? (h + 127) / 128 : 1;
+    q_tiles[static_cast<ll>(b) * (d.sq_pad / 128) + t] = make_int2(first, end - first);
+  }
+}
+
+// One warp per 128-key tile: the 64-row query tiles whose hull meets it, in order.
+__global__ void __launch_bounds__(128) mask_key_tiles_kernel(int kt, int nq64, const int2* __restrict__ q_hull,
+                                                             int* __restrict__ kt_count, int* __restrict__ kt_list) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
+  if (t >= kt) return;
+  const int2* hull = q_hull + static_cast<ll>(b) * nq64;
+  const ll at = static_cast<ll>(b) * kt + t;
+  int* list = kt_list + at * nq64;
+  int n = 0;
+  for (int q0 = 0; q0 < nq64; q0 += 32) {
+    const int q = q0 + lane;
+    bool meets = false;
+    if (q < nq64) {
+      const int2 v = hull[q];
+      meets = v.x < v.y && v.x < (t + 1) * 128 && v.y > t * 128;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, meets);
+    if (meets) list[n + __popc(m & ((1u << lane) - 1u))] = q;
+    n += __popc(m);
+  }
+  if (lane == 0) kt_count[at] = n;
+}
+
+// key_lo, key_hi of packed documents: one thread per query row.
+__global__ void key_bounds_kernel(Dims d, const int* __restrict__ starts, int n_docs, const int* __restrict__ prefix,
+                                  int window, int* __restrict__ key_lo, int* __restrict__ key_hi) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
+  if (i >= d.Sq) return;
+  const int pos = position(d, i);
+  const int* s = starts + static_cast<ll>(b) * (n_docs + 1);
+  int a = 0, z = n_docs + 1;  // entries <= pos: the last of them starts the row's document
+  while (a < z) {
+    const int m = (a + z) >> 1;
+    if (s[m] <= pos)
+      a = m + 1;
+    else
+      z = m;
+  }
+  const int doc = a - 1;
+  int lo = 0, hi = 0;
+  if (doc >= 0 && doc < n_docs) {
+    const int first = s[doc], last = min(s[doc + 1], d.S);
+    lo = max(first, 0);
+    if (window > 0 && pos - window + 1 > lo) lo = pos - window + 1;
+    hi = pos + 1;
+    if (prefix) {
+      const ll end = static_cast<ll>(first) + prefix[static_cast<ll>(b) * n_docs + doc];
+      if (end > hi) hi = end < last ? static_cast<int>(end) : last;
+    }
+    hi = min(hi, last);
+  }
+  const ll at = static_cast<ll>(b) * d.Sq + i;
+  key_lo[at] = lo;
+  key_hi[at] = hi;
+}
+
+// ---- the backward's row pass, tensor-core dims: 16 lanes per (b, h, i) of the padded rows.
+// lse2 = lse log2(e) (+inf: the row sees nothing or does not exist; NaN: its q, dout or
+// forward result is not finite), delta = rowsum(dout out), *q_bad if q or dout is not finite.
+// PACKED: q and out come from their 8-bit checkpoints; q is written in bf16 to q_clean (zero
+// if the row is bad), out is only summed.
+template <bool PACKED>
+__global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* __restrict__ q, const bf16* __restrict__ out,
+                                                           const Packed q8, const Packed out8,
+                                                           const bf16* __restrict__ dout,
+                                                           const float* __restrict__ lse, float* __restrict__ lse2,
+                                                           float* __restrict__ delta, bf16* __restrict__ q_clean,
+                                                           int* __restrict__ q_bad) {
+  const ll row = (static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
+  const ll rows = static_cast<ll>(d.B) * d.sq_pad * d.n_h;
+  const int l16 = threadIdx.x & 15;
+  // heads fastest: neighbouring rows are neighbours in q, out and dout
+  const int h = static_cast<int>(row % d.n_h);
+  const ll bi = row / d.n_h;
+  const int i = static_cast<int>(bi % d.sq_pad);
+  const int b = static_cast<int>(bi / d.sq_pad);
+  const bool in = row < rows && i < d.Sq;
+  const ll src = (static_cast<ll>(b) * d.Sq + i) * d.n_h + h;
+  float acc = 0.f;
+  bool bad = false;
+  uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
+  if (in) {
+    const uint4 g = reinterpret_cast<const uint4*>(dout + src * 128)[l16];
+    uint4 a;
+    if constexpr (PACKED) {
+      a = unpack8_bf16x8(out8, src, 128, l16);
+      q0 = unpack8_bf16x8(q8, src, 192, l16);
+      if (l16 < 8) q1 = unpack8_bf16x8(q8, src, 192, 16 + l16);
+    } else {
+      a = reinterpret_cast<const uint4*>(out + src * 128)[l16];
+      q0 = reinterpret_cast<const uint4*>(q + src * 192)[l16];
+      if (l16 < 8) q1 = reinterpret_cast<const uint4*>(q + src * 192)[16 + l16];
+    }
+    bad = bad_bf16x8(g) || bad_bf16x8(q0) || bad_bf16x8(q1);
+    const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
+    const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&g);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 af = __bfloat1622float2(a2[k]);
+      const float2 gf = __bfloat1622float2(g2[k]);
+      acc = fmaf(af.x, gf.x, acc);
+      acc = fmaf(af.y, gf.y, acc);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  const unsigned votes = __ballot_sync(0xffffffffu, bad);
+  bad = (votes & (threadIdx.x & 16 ? 0xffff0000u : 0xffffu)) != 0u;
+  if (PACKED && in) {
+    uint4* dst = reinterpret_cast<uint4*>(q_clean + src * 192);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    dst[l16] = bad ? zero : q0;
+    if (l16 < 8) dst[16 + l16] = bad ? zero : q1;
+  }
+  if (row < rows && l16 == 0) {
+    float L = INFINITY, D = 0.f;
+    if (in) {
+      const float v = lse[(static_cast<ll>(b) * d.n_h + h) * d.Sq + i];
+      if (v == -INFINITY) {
+        L = INFINITY;  // the row sees nothing: its weights are 0
+      } else if (bad || !finite(v) || !finite(acc)) {
+        L = NAN;
+      } else {
+        L = v * 1.4426950408889634f;
+        D = acc;
+      }
+      if (bad) *q_bad = 1;
+    }
+    const ll at = (static_cast<ll>(b) * d.n_h + h) * d.sq_pad + i;
+    lse2[at] = L;
+    delta[at] = D;
+  }
+}
+
+// Runs only when *q_bad is set: clean copies of q (unless it was unpacked already) and dout.
+__global__ void __launch_bounds__(256) mask_clean_kernel(ll rows, const bf16* __restrict__ q,
+                                                         const bf16* __restrict__ dout, bf16* __restrict__ q_clean,
+                                                         bf16* __restrict__ dout_clean, const int* __restrict__ q_bad) {
+  if (*q_bad == 0) return;
+  const int l16 = threadIdx.x & 15;
+  const ll step = (static_cast<ll>(gridDim.x) * blockDim.x) >> 4;
+  for (ll row0 = ((static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5) << 1; row0 < rows; row0 += step) {
+    const ll row = row0 + ((threadIdx.x >> 4) & 1);
+    const bool in = row < rows;
+    uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0, g = q0;
+    bool bad = false;
+    if (in) {
+      g = reinterpret_cast<const uint4*>(dout + row * 128)[l16];
+      bad = bad_bf16x8(g);
+      if (q) {
+        q0 = reinterpret_cast<const uint4*>(q + row * 192)[l16];
+        if (l16 < 8) q1 = reinterpret_cast<const uint4*>(q + row * 192)[16 + l16];
+        bad |= bad_bf16x8(q0) || bad_bf16x8(q1);
+      }
+    }
+    const unsigned votes = __ballot_sync(0xffffffffu, bad);
+    bad = (votes & (threadIdx.x & 16 ? 0xffff0000u : 0xffffu)) != 0u;
+    if (in) {
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      reinterpret_cast<uint4*>(dout_clean + row * 128)[l16] = bad ? zero : g;
+      if (q) {
+        reinterpret_cast<uint4*>(q_clean + row * 192)[l16] = bad ? zero : q0;
+        if (l16 < 8) reinterpret_cast<uint4*>(q_clean + row * 192)[16 + l16] = bad ? zero : q1;
+      }
+    }
+  }
+}
+
+// ---- the same for any widths, to fp32 copies: a warp per (b, i, h) row.
+template <typename T>
+__global__ void __launch_bounds__(256) mask_bwd_pre_any_kernel(Dims d, const T* __restrict__ q, const T* __restrict__ out,
+                                                               const Packed q8, const Packed out8, bool packed,
+                                                               const T* __restrict__ dout, const float* __restrict__ lse,
+                                                               float* __restrict__ lse_row, float* __restrict__ delta,
+                                                               float* __restrict__ q_clean, float* __restrict__ dout_clean) {
+  const ll row = (static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const ll rows = static_cast<ll>(d.B) * d.Sq * d.n_h;
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 31, dqk = d.d_qk();
+  const int h = static_cast<int>(row % d.n_h);
+  const ll bi = row / d.n_h;
+  const int i = static_cast<int>(bi % d.Sq);
+  const int b = static_cast<int>(bi / d.Sq);
+  auto q_at = [&](int k) { return packed ? unpack8_value(q8, row, dqk, k) : to_f(q[row * dqk + k]); };
+  float acc = 0.f;
+  bool bad = false;
+  for (int k = lane; k < dqk; k += 32) bad |= !finite(q_at(k));
+  for (int k = lane; k < d.d_v; k += 32) {
+    const float g = to_f(dout[row * d.d_v + k]);
+    bad |= !finite(g);
+    acc = fmaf(packed ? unpack8_value(out8, row, d.d_v, k) : to_f(out[row * d.d_v + k]), g, acc);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  bad = __any_sync(0xffffffffu, bad);
+  for (int k = lane; k < dqk; k += 32) q_clean[row * dqk + k] = bad ? 0.f : q_at(k);
+  for (int k = lane; k < d.d_v; k += 32) dout_clean[row * d.d_v + k] = bad ? 0.f : to_f(dout[row * d.d_v + k]);
+  if (lane == 0) {
+    const ll at = (static_cast<ll>(b) * d.n_h + h) * d.Sq + i;
+    const float v = lse[at];
+    float L = v, D = acc;
+    if (v == -INFINITY) {
+      L = INFINITY;
+      D = 0.f;
+    } else if (bad || !finite(v) || !finite(acc)) {
+      L = NAN;
+      D = 0.f;
+    }
+    lse_row[at] = L;
+    delta[at] = D;
+  }
+}
+
+}  // namespace
+
+size_t mask_bytes(const Dims& d, int elem) {
+  char* const base = reinterpret_cast<char*>(256);  // only measured, never read
+  char* p = base;
+  mask_carve(d, elem, p);
+  return static_cast<size_t>(p - base);
+}
+
+MaskBuffers mask_carve(const Dims& d, int elem, char*& p) {
+  auto take = [&](size_t n) {
+    char* r = p;
+    p += align_up(n, 256);
+    return r;
+  };
+  const size_t B = d.B, kt = d.skv_pad / 128, nq64 = d.sq_pad / 64;
+  MaskBuffers m{};
+  m.rows = reinterpret_cast<int2*>(take(B * d.sq_pad * 8));
+  m.q_tiles = reinterpret_cast<int2*>(take(B * (nq64 / 2) * 8));
+  m.q_hull = reinterpret_cast<int2*>(take(B * nq64 * 8));
+  m.kt_count = reinterpret_cast<int*>(take(B * kt * 4));
+  m.kt_list = reinterpret_cast<int*>(take(B * kt * nq64 * 4));
+  m.q_bad = reinterpret_cast<int*>(take(4));
+  m.bad = reinterpret_cast<uint32_t*>(take(B * ((d.S + 31) / 32) * 4));
+  m.c_kv = take(B * d.S * d.d_c * elem);
+  m.k_rope = take(B * d.S * d.d_rope * elem);
+  return m;
+}
+
+LaunchResult mask_prepare(const Dims& d, bool is_bf16, const int* key_lo, const int* key_hi, const void* c_kv,
+                          const void* k_rope, const MaskBuffers& m, bool key_tiles, cudaStream_t st) {
+  LaunchResult r;
+  const int words = (d.S + 31) / 32;
+  const dim3 grid(words, d.B);
+  const int per = is_bf16 ? 8 : 4;
+  const bool vec = d.d_c % per == 0 && d.d_rope % per == 0;
+  auto keys = [&](auto kern, auto* type) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    kern<<<grid, 256, 0, st>>>(d.S, d.d_c, d.d_rope, static_cast<const T*>(c_kv), static_cast<const T*>(k_rope),
+                               static_cast<T*>(static_cast<void*>(m.c_kv)), static_cast<T*>(static_cast<void*>(m.k_rope)),
+                               m.bad);
+  };
+  if (is_bf16)
+    vec ? keys(mask_keys_kernel<bf16, true>, static_cast<bf16*>(nullptr))
+        : keys(mask_keys_kernel<bf16, false>, static_cast<bf16*>(nullptr));
+  else
+    vec ? keys(mask_keys_kernel<float, true>, static_cast<float*>(nullptr))
+        : keys(mask_keys_kernel<float, false>, static_cast<float*>(nullptr));
+  r.err = cudaGetLastError();
+  if (r.err == cudaSuccess) {
+    mask_rows_kernel<<<dim3(d.sq_pad / 128, d.B), 128, 0, st>>>(d, key_lo, key_hi, m.bad, words, m.rows, m.q_tiles,
+                                                                m.q_hull, m.q_bad);
+    r.err = cudaGetLastError();
+  }
+  if (r.err == cudaSuccess && key_tiles) {
+    const int kt = d.skv_pad / 128;
+    mask_key_tiles_kernel<<<dim3((kt + 3) / 4, d.B), 128, 0, st>>>(kt, d.sq_pad / 64, m.q_hull, m.kt_count, m.kt_list);
+    r.err = cudaGetLastError();
+  }
+  if (r.err != cudaSuccess) r.what = "mask preparation";
+  return r;
+}
+
+LaunchResult mask_key_bounds(const Dims& d, const int* starts, int n_docs, const int* prefix, int window, int* key_lo,
+                             int* key_hi, cudaStream_t st) {
+  LaunchResult r;
+  key_bounds_kernel<<<dim3((d.Sq + 127) / 128, d.B), 128, 0, st>>>(d, starts, n_docs, prefix, window, key_lo, key_hi);
+  r.err = cudaGetLastError();
+  if (r.err != cudaSuccess) r.what = "key bounds";
+  return r;
+}
+
+LaunchResult tc_mask_bwd_pre(const Dims& d, const bf16* q, const bf16* out, const Packed* q8, const Packed* out8,
+                             const bf16* dout, const float* lse, const BwdWorkspace& w, bf16* q_clean,
+                             bf16* dout_clean, int* q_bad, cudaStream_t st) {
+  LaunchResult r;
+  const ll rows = static_cast<ll>(d.B) * d.sq_pad * d.n_h;
+  const unsigned grid = static_cast<unsigned>((rows + 15) / 16);
+  if (q8)
+    mask_bwd_pre_kernel<true><<<grid, 256, 0, st>>>(d, nullptr, nullptr, *q8, *out8, dout, lse, w.lse2, w.delta, q_clean,
+                                                    q_bad);
+  else
+    mask_bwd_pre_kernel<false><<<grid, 256, 0, st>>>(d, q, out, Packed{}, Packed{}, dout, lse, w.lse2, w.delta, q_clean,
+                                                     q_bad);
+  r.err = cudaGetLastError();
+  if (r.err == cudaSuccess) {
+    mask_clean_kernel<<<2 * sm_count(), 256, 0, st>>>(static_cast<ll>(d.B) * d.Sq * d.n_h, q8 ? nullptr : q, dout,
+                                                      q_clean, dout_clean, q_bad);
+    r.err = cudaGetLastError();
+  }
+  if (r.err != cudaSuccess) r.what = "masked backward row pass";
+  return r;
+}
+
+LaunchResult simt_mask_bwd_pre(const Dims& d, bool is_bf16, const void* q, const void* out, const Packed* q8,
+                               const Packed* out8, const void* dout, const float* lse, float* lse_row, float* delta,
+                               float* q_clean, float* dout_clean, cudaStream_t st) {
+  LaunchResult r;
+  const ll rows = static_cast<ll>(d.B) * d.Sq * d.n_h;
+  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+  const Packed a = q8 ? *q8 : Packed{}, o = out8 ? *out8 : Packed{};
+  if (is_bf16)
+    mask_bwd_pre_any_kernel<bf16><<<grid, 256, 0, st>>>(d, static_cast<const bf16*>(q), static_cast<const bf16*>(out), a, o,
+                                                        q8 != nullptr, static_cast<const bf16*>(dout), lse, lse_row,
+                                                        delta, q_clean, dout_clean);
+  else
+    mask_bwd_pre_any_kernel<float><<<grid, 256, 0, st>>>(d, static_cast<const float*>(q), static_cast<const float*>(out), a,
+                                                         o, q8 != nullptr, static_cast<const float*>(dout), lse, lse_row,
+                                                         delta, q_clean, dout_clean);
+  r.err = cudaGetLastError();
+  if (r.err != cudaSuccess) r.what = "masked backward row pass";
+  return r;
+}
+
+}  // namespace laga

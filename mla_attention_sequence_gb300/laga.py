@@ -28,7 +28,9 @@ FLAG_KV_PREBUILT = 2
 EXPORTS = ("laga_mla_fwd_workspace_size", "laga_mla_bwd_workspace_size", "laga_mla_fwd", "laga_mla_bwd",
            "laga_mla_reconstruct", "laga_mla_check", "laga_status_string", "laga_mla_last_error",
            "laga_mla_version", "laga_mla_selftest_timeout", "laga_mla_absorbed_fwd",
-           "laga_mla_absorbed_fwd_workspace_size", "laga_mla_reconstruct_rows")
+           "laga_mla_absorbed_fwd_workspace_size", "laga_mla_reconstruct_rows", "laga_mla_masked_fwd",
+           "laga_mla_masked_bwd", "laga_mla_masked_fwd_workspace_size", "laga_mla_masked_bwd_workspace_size",
+           "laga_mla_key_bounds", "laga_mla_rope", "laga_mla_pack8", "laga_mla_unpack8")
 
 
 class LagaDesc(ctypes.Structure):
@@ -39,6 +41,28 @@ class LagaDesc(ctypes.Structure):
                 ("causal", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("dtype", ctypes.c_int32),
                 ("variant", ctypes.c_int32), ("flags", ctypes.c_int32), ("q_split", ctypes.c_int64),
                 ("q_offset2", ctypes.c_int64)]
+
+
+class LagaMods(ctypes.Structure):
+    """Mirror of laga_mla_mods."""
+    _fields_ = [("key_lo", ctypes.c_void_p), ("key_hi", ctypes.c_void_p), ("slopes", ctypes.c_void_p),
+                ("softcap", ctypes.c_float)]
+
+
+class LagaPacked(ctypes.Structure):
+    """Mirror of laga_mla_packed."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+ROPE_MAX_AXES = 4
+
+
+class LagaRopeDesc(ctypes.Structure):
+    """Mirror of laga_mla_rope_desc."""
+    _fields_ = [("tokens", ctypes.c_int64), ("n_h", ctypes.c_int64), ("d_nope", ctypes.c_int64),
+                ("d_rope", ctypes.c_int64), ("n_axes", ctypes.c_int64), ("sections", ctypes.c_int64 * ROPE_MAX_AXES),
+                ("theta", ctypes.c_double), ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("pos64", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class LagaError(RuntimeError):
@@ -76,6 +100,20 @@ def lib() -> ctypes.CDLL:
     L.laga_mla_reconstruct.restype = st
     L.laga_mla_reconstruct_rows.argtypes = [pd, vp, vp, vp, ctypes.c_int64, ctypes.c_int64, vp, sz, vp]
     L.laga_mla_reconstruct_rows.restype = st
+    pm, pp = ctypes.POINTER(LagaMods), ctypes.POINTER(LagaPacked)
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    for f in (L.laga_mla_masked_fwd_workspace_size, L.laga_mla_masked_bwd_workspace_size):
+        f.argtypes = [pd]
+        f.restype = sz
+    L.laga_mla_masked_fwd.argtypes = [pd, pm] + [vp] * 8 + [sz, vp]
+    L.laga_mla_masked_bwd.argtypes = [pd, pm] + [vp] * 8 + [pp, pp] + [vp] * 6 + [sz, vp]
+    L.laga_mla_key_bounds.argtypes = [i64] * 6 + [vp, i64, vp, i64, vp, vp, vp]
+    L.laga_mla_rope.argtypes = [ctypes.POINTER(LagaRopeDesc)] + [vp] * 6
+    L.laga_mla_pack8.argtypes = [i32, i64, i64, vp, vp, vp, vp]
+    L.laga_mla_unpack8.argtypes = [i32, i64, i64, vp, vp, vp, vp]
+    for f in (L.laga_mla_masked_fwd, L.laga_mla_masked_bwd, L.laga_mla_key_bounds, L.laga_mla_rope, L.laga_mla_pack8,
+              L.laga_mla_unpack8):
+        f.restype = st
     L.laga_mla_check.argtypes = [vp]
     L.laga_mla_check.restype = st
     L.laga_mla_selftest_timeout.argtypes = [vp]
@@ -110,9 +148,10 @@ def _stream(device) -> int:
 
 
 def problem_of(q, c_kv, k_rope, W_UK, W_UV, q_offset: int, causal: bool, q_split: int = 0,
-               q_offset2: int = 0) -> Problem:
+               q_offset2: int = 0, q_stand_in: bool = False) -> Problem:
     """Infer and check the problem sizes from the input tensors. q_split > 0 makes
-    rows [q_split, Sq) a second query segment starting at position q_offset2."""
+    rows [q_split, Sq) a second query segment starting at position q_offset2. q_stand_in:
+    q only has q's shape, type and device, and no memory that is read."""
     if q.dim() != 4 or c_kv.dim() != 3 or k_rope.dim() != 3 or W_UK.dim() != 2 or W_UV.dim() != 2:
         raise ValueError("expected q [B,Sq,n_h,d_qk], c_kv [B,S,d_c], k_rope [B,S,d_rope], W [d_c, n_h*d]")
     B, Sq, n_h, d_qk = q.shape
@@ -133,7 +172,7 @@ def problem_of(q, c_kv, k_rope, W_UK, W_UV, q_offset: int, causal: bool, q_split
             raise TypeError("all inputs must share one dtype")
         if not t.is_cuda:
             raise RuntimeError("LAGA MLA runs on CUDA tensors only")
-        if not t.is_contiguous():
+        if not t.is_contiguous() and not (q_stand_in and t is q):
             raise ValueError("inputs must be contiguous")
     return Problem(B=B, Sq=Sq, S=S, n_h=n_h, d_c=d_c, d_nope=d_nope, d_rope=d_rope, d_v=d_v,
                    q_offset=int(q_offset), causal=bool(causal), dtype=dt, q_split=int(q_split),
@@ -269,6 +308,254 @@ def reconstruct(c_kv, W_UK, W_UV, n_h: int, variant: str = "auto"):
     _raise_if(lib().laga_mla_reconstruct(ctypes.byref(d), _ptr(c_kv), _ptr(W_UK), _ptr(W_UV), _ptr(kn), _ptr(v),
                                          _stream(c_kv.device)))
     return kn, v
+
+
+# ---------------------------------------------------------------- packed documents
+#
+# Every call below runs on the current stream of its tensors' device and makes that device
+# current for its launches; all tensors of a call are on one device.
+
+_TORCH_DTYPES = {torch.float32: "f32", torch.bfloat16: "bf16"}
+
+
+def _dtype_of(t: torch.Tensor) -> str:
+    if t.dtype not in _TORCH_DTYPES:
+        raise TypeError("tensors must be float32 or bfloat16")
+    return _TORCH_DTYPES[t.dtype]
+
+
+def _expect(name: str, t: torch.Tensor, shape, dtypes, device) -> torch.Tensor:
+    """A contiguous CUDA tensor of that shape, type and device, or an error that names it."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise RuntimeError(f"{name}: LAGA MLA runs on CUDA tensors only")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def key_bounds(doc_starts, n_rows: int, q_offset: int = 0, prefix=None, window: int = 0, skv: int | None = None,
+               q_split: int = 0, q_offset2: int = 0):
+    """laga_mla_key_bounds: (key_lo, key_hi), int32 [B, n_rows], for masked_fwd / masked_bwd.
+
+    doc_starts: int32 [B, n_docs + 1], ascending; document k holds the keys [doc_starts[k],
+    doc_starts[k + 1]). A row sees the keys of its own document up to its position, at most
+    the last `window` of them (0: all), and, with prefix (int32 [B, n_docs]), all of the
+    document's first prefix[k] keys (call the attention with causal=False then). Rows in no
+    document see nothing. skv clamps the bounds (None: only the documents do)."""
+    if doc_starts.dim() != 2 or doc_starts.shape[1] < 2:
+        raise ValueError("doc_starts must be [B, n_docs + 1]")
+    B, n_docs = doc_starts.shape[0], doc_starts.shape[1] - 1
+    dev = doc_starts.device
+    _expect("doc_starts", doc_starts, (B, n_docs + 1), (torch.int32,), dev)
+    if prefix is not None:
+        _expect("prefix", prefix, (B, n_docs), (torch.int32,), dev)
+    lo = torch.empty((B, n_rows), dtype=torch.int32, device=dev)
+    hi = torch.empty_like(lo)
+    with torch.cuda.device(dev):
+        _raise_if(lib().laga_mla_key_bounds(B, n_rows, (1 << 30) - 1 if skv is None else int(skv), int(q_offset),
+                                            int(q_split), int(q_offset2), _ptr(doc_starts), n_docs, _ptr(prefix),
+                                            int(window), _ptr(lo), _ptr(hi), _stream(dev)))
+    return lo, hi
+
+
+@dataclass
+class Packed8:
+    """A tensor saved in 8 bits: e4m3 codes (uint8, the tensor's shape), one biased power-of-two
+    exponent per 32 values of the last dimension (uint8), and the type it is restored to."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    dtype: torch.dtype
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _check_packed(name: str, p: Packed8):
+    if p.dtype not in _TORCH_DTYPES:
+        raise TypeError(f"{name}: a checkpoint restores to float32 or bfloat16")
+    _expect(name + ".codes", p.codes, p.codes.shape, (torch.uint8,), p.codes.device)
+    if p.codes.dim() < 1:
+        raise ValueError(f"{name}: a checkpoint has at least one dimension")
+    _expect(name + ".scales", p.scales, (*p.codes.shape[:-1], -(-p.codes.shape[-1] // 32)), (torch.uint8,),
+            p.codes.device)
+
+
+def pack8(x: torch.Tensor) -> Packed8:
+    """laga_mla_pack8: saves a float32 or bfloat16 tensor in 8 bits along its last dimension."""
+    dt = _dtype_of(x)
+    if x.dim() < 1:
+        raise ValueError("pack8 needs at least one dimension")
+    _expect("x", x, x.shape, (x.dtype,), x.device)
+    codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    scales = torch.empty((*x.shape[:-1], -(-x.shape[-1] // 32)), dtype=torch.uint8, device=x.device)
+    if x.numel():
+        with torch.cuda.device(x.device):
+            _raise_if(lib().laga_mla_pack8(DTYPES[dt], x.numel() // x.shape[-1], x.shape[-1], _ptr(x), _ptr(codes),
+                                           _ptr(scales), _stream(x.device)))
+    return Packed8(codes, scales, x.dtype)
+
+
+def unpack8(p: Packed8, out: torch.Tensor | None = None) -> torch.Tensor:
+    """laga_mla_unpack8: the tensor a checkpoint stands for, in its own type."""
+    _check_packed("p", p)
+    if out is None:
+        out = torch.empty(p.shape, dtype=p.dtype, device=p.device)
+    else:
+        _expect("out", out, p.shape, (p.dtype,), p.device)
+    if out.numel():
+        with torch.cuda.device(p.device):
+            _raise_if(lib().laga_mla_unpack8(DTYPES[_TORCH_DTYPES[p.dtype]], out.numel() // p.shape[-1], p.shape[-1],
+                                             _ptr(p.codes), _ptr(p.scales), _ptr(out), _stream(p.device)))
+    return out
+
+
+def rope(q, k_rope, pos, sections=None, theta: float = 10000.0, interleaved: bool = True, inverse: bool = False,
+         q_out=None, k_out=None):
+    """laga_mla_rope: rotates the RoPE part of q [B, S, n_h, d_nope + d_rope] and k_rope
+    [B, S, d_rope] by the positions pos [n_axes, B, S] (int32 or int64); returns (q, k_rope)
+    rotated. sections: pairs per axis (None: one axis with all). The outputs are new tensors,
+    or q_out / k_out, which may be q / k_rope themselves (in place). inverse=True rotates back:
+    pass the gradients of the rotated tensors to get those of q and k_rope."""
+    if k_rope.dim() != 3 or pos.dim() != 3 or q.dim() != 4:
+        raise ValueError("expected q [B,S,n_h,d_nope+d_rope], k_rope [B,S,d_rope], pos [n_axes,B,S]")
+    B, S, n_h, d_qk = q.shape
+    d_rope, dev = k_rope.shape[2], k_rope.device
+    dt = _dtype_of(q)
+    _expect("q", q, q.shape, (q.dtype,), dev)
+    _expect("k_rope", k_rope, (B, S, d_rope), (q.dtype,), dev)
+    _expect("pos", pos, (pos.shape[0], B, S), (torch.int32, torch.int64), dev)
+    if d_rope > d_qk:
+        raise ValueError("q's last dim must be d_nope + d_rope")
+    sections = [d_rope // 2] if sections is None else [int(s) for s in sections]
+    if len(sections) != pos.shape[0] or len(sections) > ROPE_MAX_AXES:
+        raise ValueError(f"one section per axis of pos, at most {ROPE_MAX_AXES}")
+    q_out = torch.empty_like(q) if q_out is None else _expect("q_out", q_out, q.shape, (q.dtype,), dev)
+    k_out = torch.empty_like(k_rope) if k_out is None else _expect("k_out", k_out, k_rope.shape, (q.dtype,), dev)
+    d = LagaRopeDesc(B * S, n_h, d_qk - d_rope, d_rope, len(sections),
+                     (ctypes.c_int64 * ROPE_MAX_AXES)(*sections), float(theta), int(bool(interleaved)),
+                     int(bool(inverse)), int(pos.dtype == torch.int64), DTYPES[dt])
+    with torch.cuda.device(dev):
+        _raise_if(lib().laga_mla_rope(ctypes.byref(d), _ptr(pos), _ptr(q), _ptr(k_rope), _ptr(q_out), _ptr(k_out),
+                                      _stream(dev)))
+    return q_out, k_out
+
+
+def _mods(p: Problem, dev, key_lo, key_hi, softcap, slopes) -> LagaMods:
+    for name, t in (("key_lo", key_lo), ("key_hi", key_hi)):
+        if t is not None:
+            _expect(name, t, (p.B, p.Sq), (torch.int32,), dev)
+    if slopes is not None:
+        _expect("slopes", slopes, (p.n_h,), (torch.float32,), dev)
+    return LagaMods(_ptr(key_lo), _ptr(key_hi), _ptr(slopes), float(softcap or 0.0))
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+
+
+def masked_workspace(q, c_kv, k_rope, W_UK, W_UV, key_lo=None, key_hi=None, softcap: float = 0.0, slopes=None,
+                     q_offset: int = 0, causal: bool = True, softmax_scale: float | None = None, variant: str = "auto",
+                     q_split: int = 0, q_offset2: int = 0) -> torch.Tensor:
+    """A workspace for masked_fwd and masked_bwd of these arguments; the forward's K and V stay in
+    it for a backward with reuse_kv=True."""
+    p = problem_of(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, q_split, q_offset2)
+    d = make_desc(p, softmax_scale, variant)
+    n = int(lib().laga_mla_masked_bwd_workspace_size(ctypes.byref(d)))
+    if n == 0:
+        raise LagaError(2, lib().laga_mla_last_error().decode(errors="replace"))
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def masked_fwd(q, c_kv, k_rope, W_UK, W_UV, key_lo=None, key_hi=None, softcap: float = 0.0, slopes=None,
+               q_offset: int = 0, causal: bool = True, softmax_scale: float | None = None, variant: str = "auto",
+               workspace: torch.Tensor | None = None, out=None, lse=None, q_split: int = 0, q_offset2: int = 0):
+    """laga_mla_masked_fwd: (out [B,Sq,n_h,d_v], lse [B,n_h,Sq] fp32) where row i sees the keys
+    key_lo[i] <= j < key_hi[i] (int32 [B, Sq], as key_bounds makes them; None: no bound) and, when
+    causal, j <= its position. softcap > 0: scores become softcap tanh(s / softcap). slopes
+    (float32 [n_h]): minus slopes[h] times the distance to the key. A row that sees nothing gets
+    out 0 and lse -inf."""
+    p = problem_of(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, q_split, q_offset2)
+    dev = q.device
+    _same_device(dev, c_kv=c_kv, k_rope=k_rope, W_UK=W_UK, W_UV=W_UV, workspace=workspace)
+    m = _mods(p, dev, key_lo, key_hi, softcap, slopes)
+    d = make_desc(p, softmax_scale, variant)
+    L = lib()
+    out = torch.empty((p.B, p.Sq, p.n_h, p.d_v), dtype=q.dtype, device=dev) if out is None else \
+        _expect("out", out, (p.B, p.Sq, p.n_h, p.d_v), (q.dtype,), dev)
+    lse = torch.empty((p.B, p.n_h, p.Sq), dtype=torch.float32, device=dev) if lse is None else \
+        _expect("lse", lse, (p.B, p.n_h, p.Sq), (torch.float32,), dev)
+    nbytes = int(L.laga_mla_masked_fwd_workspace_size(ctypes.byref(d)))
+    ws = _workspace(nbytes, dev, workspace)
+    with torch.cuda.device(dev):
+        _raise_if(L.laga_mla_masked_fwd(ctypes.byref(d), ctypes.byref(m), _ptr(q), _ptr(c_kv), _ptr(k_rope), _ptr(W_UK),
+                                        _ptr(W_UV), _ptr(out), _ptr(lse), _ptr(ws), nbytes, _stream(dev)))
+    return out, lse
+
+
+def masked_bwd(q, c_kv, k_rope, W_UK, W_UV, out, lse, dout, key_lo=None, key_hi=None, softcap: float = 0.0,
+               slopes=None, q_offset: int = 0, causal: bool = True, softmax_scale: float | None = None,
+               variant: str = "auto", workspace: torch.Tensor | None = None, grads: dict | None = None,
+               reuse_kv: bool = False, q_split: int = 0, q_offset2: int = 0):
+    """laga_mla_masked_bwd: dict dq, dc_kv, dk_rope, dW_UK, dW_UV of <dout, out>, with the forward's
+    arguments. q and out may both be Packed8 checkpoints (pack8 of the forward's q and out): the
+    backward reads them in 8 bits. reuse_kv=True: `workspace` is the one the forward ran with, its
+    K and V intact."""
+    packed = isinstance(q, Packed8)
+    if packed != isinstance(out, Packed8):
+        raise ValueError("q and out come either both as tensors or both as 8-bit checkpoints")
+    if packed:
+        _check_packed("q", q)
+        _check_packed("out", out)
+        if q.dtype != c_kv.dtype or out.dtype != c_kv.dtype:
+            raise TypeError("all inputs must share one dtype")
+        p = problem_of(c_kv.new_empty(1).expand(q.shape), c_kv, k_rope, W_UK, W_UV, q_offset, causal, q_split,
+                       q_offset2, q_stand_in=True)
+    else:
+        p = problem_of(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, q_split, q_offset2)
+    dev, dt = c_kv.device, c_kv.dtype
+    _same_device(dev, q=q, k_rope=k_rope, W_UK=W_UK, W_UV=W_UV, workspace=workspace)
+    o_shape = (p.B, p.Sq, p.n_h, p.d_v)
+    if packed:
+        _expect("out.codes", out.codes, o_shape, (torch.uint8,), dev)
+    else:
+        _expect("out", out, o_shape, (dt,), dev)
+    _expect("lse", lse, (p.B, p.n_h, p.Sq), (torch.float32,), dev)
+    _expect("dout", dout, o_shape, (dt,), dev)
+    if reuse_kv and workspace is None:
+        raise ValueError("reuse_kv needs the workspace the forward ran with")
+    m = _mods(p, dev, key_lo, key_hi, softcap, slopes)
+    d = make_desc(p, softmax_scale, variant, FLAG_REUSE_KV if reuse_kv else 0)
+    L = lib()
+    shapes = {"dq": (p.B, p.Sq, p.n_h, p.d_qk), "dc_kv": c_kv.shape, "dk_rope": k_rope.shape, "dW_UK": W_UK.shape,
+              "dW_UV": W_UV.shape}
+    if grads is None:
+        grads = {k: torch.empty(s, dtype=dt, device=dev) for k, s in shapes.items()}
+    else:
+        for k, s in shapes.items():
+            _expect(k, grads[k], s, (dt,), dev)
+    q8, out8 = (ctypes.byref(LagaPacked(_ptr(t.codes), _ptr(t.scales))) if packed else None for t in (q, out))
+    nbytes = int(L.laga_mla_masked_bwd_workspace_size(ctypes.byref(d)))
+    ws = _workspace(nbytes, dev, workspace)
+    with torch.cuda.device(dev):
+        _raise_if(L.laga_mla_masked_bwd(ctypes.byref(d), ctypes.byref(m), None if packed else _ptr(q), _ptr(c_kv),
+                                        _ptr(k_rope), _ptr(W_UK), _ptr(W_UV), None if packed else _ptr(out), _ptr(lse),
+                                        _ptr(dout), q8, out8, _ptr(grads["dq"]), _ptr(grads["dc_kv"]),
+                                        _ptr(grads["dk_rope"]), _ptr(grads["dW_UK"]), _ptr(grads["dW_UV"]), _ptr(ws),
+                                        nbytes, _stream(dev)))
+    return grads
 
 
 def check(device=None) -> None:
