@@ -367,8 +367,8 @@ def _own(case, st):
                 causal=not case["prefix"])
     x = (st["c_kv"], st["k_rope"], st["W_UK"], st["W_UV"])
     if case["op"] == "packed_bwd":
-        q = laga.Packed8(st["q8"].view(torch.uint8), st["q8_scales"], _dtype(case))
-        out = laga.Packed8(st["out8"].view(torch.uint8), st["out8_scales"], _dtype(case))
+        q = laga.Packed8(st["q8"].contiguous().view(torch.uint8), st["q8_scales"], _dtype(case))
+        out = laga.Packed8(st["out8"].contiguous().view(torch.uint8), st["out8_scales"], _dtype(case))
         return laga.masked_bwd(q, *x, out, st["lse"], st["dout"], **mods)
     if case["op"] == "fwd":
         return {"out": laga.masked_fwd(st["q"], *x, **mods)[0]}
