@@ -272,8 +272,7 @@ size_t laga_mla_masked_bwd_workspace_size(const laga_mla_desc* desc);
 /* Forward: out and lse as for laga_mla_fwd. mods may be NULL (no cap, no bias, bounds
  * from desc->causal alone). Variants AUTO, MATERIALIZE and SIMT; bf16 with the
  * tensor-core dims, otherwise d_nope + d_rope <= 256 and d_v <= 256 on the CUDA cores.
- * LAGA_FLAG_KV_PREBUILT is refused. The workspace starts with the rebuilt K and V, as
- * laga_mla_fwd's does. Errors as for laga_mla_fwd. */
+ * LAGA_FLAG_KV_PREBUILT is refused. Errors as for laga_mla_fwd. */
 laga_status laga_mla_masked_fwd(const laga_mla_desc* desc, const laga_mla_mods* mods, const void* q,
                                 const void* c_kv, const void* k_rope, const void* W_UK, const void* W_UV, void* out,
                                 float* lse, void* workspace, size_t workspace_bytes, laga_stream_t stream);
@@ -282,7 +281,9 @@ laga_status laga_mla_masked_fwd(const laga_mla_desc* desc, const laga_mla_mods* 
  * forward. q and out come either as tensors (q8, out8 NULL) or as 8-bit checkpoints
  * (q and out NULL): then P = exp(s - lse) with the scores of the restored q, and
  * D = rowsum(dout o out) of the restored out. LAGA_FLAG_REUSE_KV: the workspace is the
- * one laga_mla_masked_fwd used for the same inputs, its K and V intact. */
+ * one laga_mla_masked_fwd used for the same inputs, descriptor and mods, its first
+ * laga_mla_masked_fwd_workspace_size bytes intact (K, V and what the bounds became: the
+ * bounds are not read again). */
 laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* mods, const void* q,
                                 const void* c_kv, const void* k_rope, const void* W_UK, const void* W_UV,
                                 const void* out, const float* lse, const void* dout, const laga_mla_packed* q8,

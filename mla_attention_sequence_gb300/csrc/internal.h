@@ -91,6 +91,9 @@ struct MaskMeta {
   const int* kt_count;  // [B][skv_pad / 128] 64-row query tiles that may see a key tile
   const int* kt_list;   // [B][skv_pad / 128][sq_pad / 64] which, ascending
   int* q_bad;           // nonzero: some row of q or dout that the backward reads is not finite
+  const int* seen;        // [B][skv_pad / 128] whether some query tile's walk touches a key tile
+  const int* seen_list;   // the touched ones, b * (skv_pad / 128) + tile, ascending
+  const int* seen_count;  // how many
 };
 
 struct ScoreMods {

@@ -50,10 +50,12 @@ __device__ __forceinline__ float unpack8_value(const Packed& p, long long row, i
 struct MaskBuffers {
   int2 *rows, *q_tiles, *q_hull;
   int *kt_count, *kt_list, *q_bad;
+  int *seen, *seen_list;  // [B * kt]: whether a key tile is walked; the walked ones, in order
+  int* counters;          // {tiles in seen_list, CTAs done}
   uint32_t* bad;  // [B][ceil(S / 32)] bit per key: its latent row is not finite
   char* c_kv;     // [B][S][d_c] with such rows zero, in the inputs' type
   char* k_rope;   // [B][S][d_rope]
-  MaskMeta meta() const { return MaskMeta{rows, q_tiles, q_hull, kt_count, kt_list, q_bad}; }
+  MaskMeta meta() const { return MaskMeta{rows, q_tiles, q_hull, kt_count, kt_list, q_bad, seen, seen_list, counters}; }
 };
 size_t mask_bytes(const Dims& d, int elem);
 MaskBuffers mask_carve(const Dims& d, int elem, char*& p);  // advances p
@@ -85,9 +87,5 @@ LaunchResult simt_masked_bwd(const Dims& d, bool is_bf16, const ScoreMods& mods,
                              const void* q, const void* c_kv, const void* k_rope, const void* W_UK, const void* W_UV,
                              const void* out, const Packed* q8, const Packed* out8, const float* lse,
                              const void* dout, const BwdGrads& g, void* ws, bool reuse_kv, cudaStream_t st);
-// dc_kv, dW_UK, dW_UV from fp32 dK_nope [B*S][n_h*d_nope] and dV [B*S][n_h*d_v].
-LaunchResult simt_rebuild_bwd(const Dims& d, bool is_bf16, const void* c_kv, const void* W_UK, const void* W_UV,
-                              const float* dkn, const float* dv, void* dc_kv, void* dW_UK, void* dW_UV,
-                              cudaStream_t st);
 
 }  // namespace laga

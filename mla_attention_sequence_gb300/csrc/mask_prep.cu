@@ -32,60 +32,90 @@ __device__ __forceinline__ bool bad_bf16x8(uint4 v) {
   return bad_bf16x2(v.x) || bad_bf16x2(v.y) || bad_bf16x2(v.z) || bad_bf16x2(v.w);
 }
 
-// Latent rows -> clean copies; one CTA per 32 keys of a batch element, a warp per row
-// in turn. bad[b][word] bit r: key 32 * word + r holds a non-finite value.
-// 16-byte loads when the rows allow it (VEC), else one value a lane.
-template <typename T, bool VEC>
+// Latent rows -> clean copies; one CTA per 32 keys of a batch element, a warp for four of
+// them. bad[b][word] bit r: key 32 * word + r holds a non-finite value.
+// The tensor-core dims: the four rows' 72 16-byte chunks each are loaded before the first is
+// looked at (row by row the kernel took 11 us however few keys there were).
+constexpr int KEY_ROWS = 4;
+
+__global__ void __launch_bounds__(256) mask_keys_tc_kernel(int S, const bf16* __restrict__ c, const bf16* __restrict__ r,
+                                                           bf16* __restrict__ c_out, bf16* __restrict__ r_out,
+                                                           uint32_t* __restrict__ bad) {
+  constexpr int NC = 64, NR = 8;  // chunks of a latent row (512 values), of a RoPE key (64)
+  __shared__ uint32_t warp_bad[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
+  const int j0 = blockIdx.x * 32 + warp * KEY_ROWS;
+  const uint4* cs = reinterpret_cast<const uint4*>(c) + (static_cast<ll>(b) * S + j0) * NC;
+  const uint4* rs = reinterpret_cast<const uint4*>(r) + (static_cast<ll>(b) * S + j0) * NR;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 v[KEY_ROWS][2], w;
+#pragma unroll
+  for (int k = 0; k < KEY_ROWS; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[k][i] = j0 + k < S ? cs[k * NC + 32 * i + lane] : zero;
+  w = j0 + (lane >> 3) < S ? rs[lane] : zero;  // the four RoPE keys, eight lanes each
+  const unsigned rope_bad = __ballot_sync(0xffffffffu, bad_bf16x8(w));
+  uint32_t mask = 0u;
+#pragma unroll
+  for (int k = 0; k < KEY_ROWS; ++k)
+    if (__any_sync(0xffffffffu, bad_bf16x8(v[k][0]) || bad_bf16x8(v[k][1])) || (rope_bad & (0xffu << (8 * k)))) mask |= 1u << k;
+  uint4* cd = reinterpret_cast<uint4*>(c_out) + (static_cast<ll>(b) * S + j0) * NC;
+  uint4* rd = reinterpret_cast<uint4*>(r_out) + (static_cast<ll>(b) * S + j0) * NR;
+#pragma unroll
+  for (int k = 0; k < KEY_ROWS; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (j0 + k < S) cd[k * NC + 32 * i + lane] = (mask >> k) & 1u ? zero : v[k][i];
+  if (j0 + (lane >> 3) < S) rd[lane] = (mask >> (lane >> 3)) & 1u ? zero : w;
+  if (lane == 0) warp_bad[warp] = mask << (KEY_ROWS * warp);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m |= warp_bad[k];
+    bad[static_cast<ll>(b) * gridDim.x + blockIdx.x] = m;
+  }
+}
+
+// Any widths: one value a lane.
+template <typename T>
 __global__ void __launch_bounds__(256) mask_keys_kernel(int S, int d_c, int d_rope, const T* __restrict__ c,
                                                         const T* __restrict__ r, T* __restrict__ c_out,
                                                         T* __restrict__ r_out, uint32_t* __restrict__ bad) {
-  __shared__ uint32_t mask;
+  __shared__ uint32_t warp_bad[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
-  if (threadIdx.x == 0) mask = 0u;
-  __syncthreads();
-  constexpr int PER = 16 / static_cast<int>(sizeof(T));
-  for (int k = warp; k < 32; k += 8) {
-    const int j = blockIdx.x * 32 + k;
-    if (j >= S) break;
-    const ll row = static_cast<ll>(b) * S + j;
-    const T *cs = c + row * d_c, *rs = r + row * d_rope;
-    T *cd = c_out + row * d_c, *rd = r_out + row * d_rope;
-    bool is_bad = false;
-    if constexpr (VEC) {
-      const int nc = d_c / PER, nr = d_rope / PER;
-      for (int i = lane; i < nc + nr; i += 32) {
-        const uint4 v = i < nc ? reinterpret_cast<const uint4*>(cs)[i] : reinterpret_cast<const uint4*>(rs)[i - nc];
-        if constexpr (sizeof(T) == 2)
-          is_bad |= bad_bf16x8(v);
-        else
-          is_bad |= !finite(__uint_as_float(v.x)) || !finite(__uint_as_float(v.y)) || !finite(__uint_as_float(v.z)) ||
-                    !finite(__uint_as_float(v.w));
-      }
-      is_bad = __any_sync(0xffffffffu, is_bad);
-      for (int i = lane; i < nc + nr; i += 32) {  // the row's second reading is an L1 hit
-        uint4 v = i < nc ? reinterpret_cast<const uint4*>(cs)[i] : reinterpret_cast<const uint4*>(rs)[i - nc];
-        if (is_bad) v = make_uint4(0u, 0u, 0u, 0u);
-        if (i < nc)
-          reinterpret_cast<uint4*>(cd)[i] = v;
-        else
-          reinterpret_cast<uint4*>(rd)[i - nc] = v;
-      }
-    } else {
-      for (int i = lane; i < d_c + d_rope; i += 32) is_bad |= !finite(to_f(i < d_c ? cs[i] : rs[i - d_c]));
-      is_bad = __any_sync(0xffffffffu, is_bad);
-      for (int i = lane; i < d_c + d_rope; i += 32) {
-        T v = i < d_c ? cs[i] : rs[i - d_c];
-        if (is_bad) v = static_cast<T>(0.f);
-        if (i < d_c)
-          cd[i] = v;
-        else
-          rd[i - d_c] = v;
+  const int j0 = blockIdx.x * 32 + warp * KEY_ROWS;
+  uint32_t mask = 0u;
+  auto sweep = [&](int width, const T* src, T* dst, bool write) {
+    const T* from = src + (static_cast<ll>(b) * S + j0) * width;
+    T* to = dst + (static_cast<ll>(b) * S + j0) * width;
+    for (int i = lane; i < ((width + 31) & ~31); i += 32) {
+      T v[KEY_ROWS];
+#pragma unroll
+      for (int k = 0; k < KEY_ROWS; ++k)
+        v[k] = i < width && j0 + k < S ? from[static_cast<ll>(k) * width + i] : static_cast<T>(0.f);
+#pragma unroll
+      for (int k = 0; k < KEY_ROWS; ++k) {
+        if (!write) {
+          if (__any_sync(0xffffffffu, !finite(to_f(v[k])))) mask |= 1u << k;
+        } else if (i < width && j0 + k < S) {
+          to[static_cast<ll>(k) * width + i] = (mask >> k) & 1u ? static_cast<T>(0.f) : v[k];
+        }
       }
     }
-    if (is_bad && lane == 0) atomicOr(&mask, 1u << k);
-  }
+  };
+  sweep(d_c, c, c_out, false);
+  sweep(d_rope, r, r_out, false);
+  sweep(d_c, c, c_out, true);  // the second reading hits the caches
+  sweep(d_rope, r, r_out, true);
+  if (lane == 0) warp_bad[warp] = mask << (KEY_ROWS * warp);
   __syncthreads();
-  if (threadIdx.x == 0) bad[static_cast<ll>(b) * gridDim.x + blockIdx.x] = mask;
+  if (threadIdx.x == 0) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m |= warp_bad[k];
+    bad[static_cast<ll>(b) * gridDim.x + blockIdx.x] = m;
+  }
 }
 
 __device__ __forceinline__ int position(const Dims& d, int i) {
@@ -97,11 +127,12 @@ __global__ void __launch_bounds__(128) mask_rows_kernel(Dims d, const int* __res
                                                         const int* __restrict__ key_hi,
                                                         const uint32_t* __restrict__ bad, int bad_words,
                                                         int2* __restrict__ rows, int2* __restrict__ q_tiles,
-                                                        int2* __restrict__ q_hull, int* __restrict__ q_bad) {
+                                                        int2* __restrict__ q_hull, int* __restrict__ q_bad,
+                                                        int* __restrict__ counters) {
   __shared__ int s_lo[4], s_hi[4];
   const int t = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = t * 128 + threadIdx.x;
-  if (t == 0 && b == 0 && threadIdx.x == 0) *q_bad = 0;
+  if (t == 0 && b == 0 && threadIdx.x == 0) *q_bad = counters[0] = counters[1] = 0;
   int lo = 0, hi = 0;
   if (i < d.Sq) {
     const ll at = static_cast<ll>(b) * d.Sq + i;
@@ -146,27 +177,66 @@ __global__ void __launch_bounds__(128) mask_rows_kernel(Dims d, const int* __res
   }
 }
 
-// One warp per 128-key tile: the 64-row query tiles whose hull meets it, in order.
-__global__ void __launch_bounds__(128) mask_key_tiles_kernel(int kt, int nq64, const int2* __restrict__ q_hull,
-                                                             int* __restrict__ kt_count, int* __restrict__ kt_list) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, b = blockIdx.y;
-  if (t >= kt) return;
+// One CTA per batch element, a warp per 128-key tile in turn: the 64-row query tiles whose
+// hull meets it, in order. The CTA that finishes last lists the key tiles (of all batch
+// elements, in order) that some query tile's walk touches: only those are rebuilt, and only
+// their gradients summed.
+__global__ void __launch_bounds__(1024) mask_tiles_kernel(int kt, int nq64, const int2* __restrict__ q_tiles,
+                                                          const int2* __restrict__ q_hull, int* __restrict__ kt_count,
+                                                          int* __restrict__ kt_list, int* __restrict__ seen,
+                                                          int* __restrict__ seen_list, int* __restrict__ counters) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
   const int2* hull = q_hull + static_cast<ll>(b) * nq64;
-  const ll at = static_cast<ll>(b) * kt + t;
-  int* list = kt_list + at * nq64;
-  int n = 0;
-  for (int q0 = 0; q0 < nq64; q0 += 32) {
-    const int q = q0 + lane;
-    bool meets = false;
-    if (q < nq64) {
-      const int2 v = hull[q];
-      meets = v.x < v.y && v.x < (t + 1) * 128 && v.y > t * 128;
+  const int2* walk = q_tiles + static_cast<ll>(b) * (nq64 / 2);
+  for (int t = warp; t < kt; t += 32) {
+    const ll at = static_cast<ll>(b) * kt + t;
+    int* list = kt_list + at * nq64;
+    int n = 0;
+    bool touched = false;
+    for (int q0 = 0; q0 < nq64; q0 += 32) {
+      const int q = q0 + lane;
+      bool meets = false;
+      if (q < nq64) {
+        const int2 v = hull[q], w = walk[q >> 1];
+        meets = v.x < v.y && v.x < (t + 1) * 128 && v.y > t * 128;
+        touched |= w.x <= t && t < w.x + w.y;
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, meets);
+      if (meets) list[n + __popc(m & ((1u << lane) - 1u))] = q;
+      n += __popc(m);
     }
-    const unsigned m = __ballot_sync(0xffffffffu, meets);
-    if (meets) list[n + __popc(m & ((1u << lane) - 1u))] = q;
-    n += __popc(m);
+    touched = __any_sync(0xffffffffu, touched);
+    if (lane == 0) {
+      kt_count[at] = n;
+      seen[at] = touched ? 1 : 0;
+    }
   }
-  if (lane == 0) kt_count[at] = n;
+  __shared__ bool last;
+  __shared__ int warp_n[32];
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(&counters[1], 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  const int total = kt * static_cast<int>(gridDim.x);
+  int base = 0;
+  for (int i0 = 0; i0 < total; i0 += 1024) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    const bool in = i < total && __ldcg(seen + i) != 0;
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) warp_n[warp] = __popc(m);
+    __syncthreads();
+    int before = base, all = 0;
+    for (int k = 0; k < 32; ++k) {
+      if (k < warp) before += warp_n[k];
+      all += warp_n[k];
+    }
+    if (in) seen_list[before + __popc(m & ((1u << lane) - 1u))] = i;
+    base += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) counters[0] = base;
 }
 
 // key_lo, key_hi of packed documents: one thread per query row.
@@ -382,6 +452,9 @@ MaskBuffers mask_carve(const Dims& d, int elem, char*& p) {
   m.kt_count = reinterpret_cast<int*>(take(B * kt * 4));
   m.kt_list = reinterpret_cast<int*>(take(B * kt * nq64 * 4));
   m.q_bad = reinterpret_cast<int*>(take(4));
+  m.counters = reinterpret_cast<int*>(take(8));
+  m.seen = reinterpret_cast<int*>(take(B * kt * 4));
+  m.seen_list = reinterpret_cast<int*>(take(B * kt * 4));
   m.bad = reinterpret_cast<uint32_t*>(take(B * ((d.S + 31) / 32) * 4));
   m.c_kv = take(B * d.S * d.d_c * elem);
   m.k_rope = take(B * d.S * d.d_rope * elem);
@@ -393,29 +466,30 @@ LaunchResult mask_prepare(const Dims& d, bool is_bf16, const int* key_lo, const 
   LaunchResult r;
   const int words = (d.S + 31) / 32;
   const dim3 grid(words, d.B);
-  const int per = is_bf16 ? 8 : 4;
-  const bool vec = d.d_c % per == 0 && d.d_rope % per == 0;
-  auto keys = [&](auto kern, auto* type) {
+  auto keys = [&](auto* type) {
     using T = std::remove_pointer_t<decltype(type)>;
-    kern<<<grid, 256, 0, st>>>(d.S, d.d_c, d.d_rope, static_cast<const T*>(c_kv), static_cast<const T*>(k_rope),
-                               static_cast<T*>(static_cast<void*>(m.c_kv)), static_cast<T*>(static_cast<void*>(m.k_rope)),
-                               m.bad);
+    mask_keys_kernel<T><<<grid, 256, 0, st>>>(d.S, d.d_c, d.d_rope, static_cast<const T*>(c_kv),
+                                              static_cast<const T*>(k_rope), static_cast<T*>(static_cast<void*>(m.c_kv)),
+                                              static_cast<T*>(static_cast<void*>(m.k_rope)), m.bad);
   };
-  if (is_bf16)
-    vec ? keys(mask_keys_kernel<bf16, true>, static_cast<bf16*>(nullptr))
-        : keys(mask_keys_kernel<bf16, false>, static_cast<bf16*>(nullptr));
+  auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  if (is_bf16 && d.d_c == 512 && d.d_rope == 64 && aligned(c_kv) && aligned(k_rope))
+    mask_keys_tc_kernel<<<grid, 256, 0, st>>>(d.S, static_cast<const bf16*>(c_kv), static_cast<const bf16*>(k_rope),
+                                              static_cast<bf16*>(static_cast<void*>(m.c_kv)),
+                                              static_cast<bf16*>(static_cast<void*>(m.k_rope)), m.bad);
+  else if (is_bf16)
+    keys(static_cast<bf16*>(nullptr));
   else
-    vec ? keys(mask_keys_kernel<float, true>, static_cast<float*>(nullptr))
-        : keys(mask_keys_kernel<float, false>, static_cast<float*>(nullptr));
+    keys(static_cast<float*>(nullptr));
   r.err = cudaGetLastError();
   if (r.err == cudaSuccess) {
     mask_rows_kernel<<<dim3(d.sq_pad / 128, d.B), 128, 0, st>>>(d, key_lo, key_hi, m.bad, words, m.rows, m.q_tiles,
-                                                                m.q_hull, m.q_bad);
+                                                                m.q_hull, m.q_bad, m.counters);
     r.err = cudaGetLastError();
   }
   if (r.err == cudaSuccess && key_tiles) {
-    const int kt = d.skv_pad / 128;
-    mask_key_tiles_kernel<<<dim3((kt + 3) / 4, d.B), 128, 0, st>>>(kt, d.sq_pad / 64, m.q_hull, m.kt_count, m.kt_list);
+    mask_tiles_kernel<<<d.B, 1024, 0, st>>>(d.skv_pad / 128, d.sq_pad / 64, m.q_tiles, m.q_hull, m.kt_count, m.kt_list,
+                                            m.seen, m.seen_list, m.counters);
     r.err = cudaGetLastError();
   }
   if (r.err != cudaSuccess) r.what = "mask preparation";

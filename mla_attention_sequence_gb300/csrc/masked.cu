@@ -121,7 +121,7 @@ laga_status laga_mla_masked_fwd(const laga_mla_desc* desc, const laga_mla_mods* 
   const MaskBuffers m = mask_carve(d, elem, at);
   const MaskArgs mask{m.meta(), sm};
   LaunchResult r =
-      timed("mask_prepare", s, [&] { return mask_prepare(d, true, lo, hi, c_kv, k_rope, m, false, s); });
+      timed("mask_prepare", s, [&] { return mask_prepare(d, true, lo, hi, c_kv, k_rope, m, true, s); });
   if (r.ok())
     r = timed("recon_fwd_gemm", s,
               [&] { return tc_recon_fwd(d, cb(m.c_kv), cb(W_UK), cb(W_UV), k_ws, v_ws, d.skv_pad, s); });
@@ -175,17 +175,24 @@ laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* 
                              reuse, s);
     }));
   auto cb = [](const void* p) { return static_cast<const bf16*>(p); };
-  const BwdWorkspace w = tc_bwd_carve(d, workspace);
-  char* at = static_cast<char*>(workspace) + tc_bwd_workspace(d);
+  // K, V and the mask's buffers where the forward has them, then the rest of the plain layout
+  char* at = static_cast<char*>(workspace) + tc_fwd_workspace(d);
   const MaskBuffers m = mask_carve(d, elem, at);
+  BwdWorkspace w = tc_bwd_carve(d, at - tc_fwd_workspace(d));
+  w.k_ws = static_cast<bf16*>(workspace);
+  w.v_ws = w.k_ws + static_cast<size_t>(d.B) * d.skv_pad * d.n_h * 128;
+  at += tc_bwd_workspace(d) - tc_fwd_workspace(d);
   bf16* q_clean = reinterpret_cast<bf16*>(at);
   bf16* dout_clean = reinterpret_cast<bf16*>(at + tc_clean_q_bytes(d));
   const MaskArgs mask{m.meta(), sm};
   const bf16* qr = packed ? q_clean : cb(q);  // what the kernels read as q
   const bf16 *c = cb(m.c_kv), *kr = cb(m.k_rope);
-  LaunchResult r = timed("mask_prepare", s, [&] { return mask_prepare(d, true, lo, hi, c_kv, k_rope, m, true, s); });
-  if (r.ok() && !reuse)
-    r = timed("recon_fwd_gemm", s, [&] { return tc_recon_fwd(d, c, cb(W_UK), cb(W_UV), w.k_ws, w.v_ws, d.skv_pad, s); });
+  LaunchResult r;
+  if (!reuse) {
+    r = timed("mask_prepare", s, [&] { return mask_prepare(d, true, lo, hi, c_kv, k_rope, m, true, s); });
+    if (r.ok())
+      r = timed("recon_fwd_gemm", s, [&] { return tc_recon_fwd(d, c, cb(W_UK), cb(W_UV), w.k_ws, w.v_ws, d.skv_pad, s); });
+  }
   if (r.ok())
     r = timed("masked_bwd_pre", s, [&] {
       return tc_mask_bwd_pre(d, cb(q), cb(out), packed ? &pq : nullptr, packed ? &po : nullptr, cb(dout), lse, w, q_clean,

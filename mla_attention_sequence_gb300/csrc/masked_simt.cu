@@ -1,15 +1,18 @@
 // Masked attention on the CUDA cores in fp32, for any head widths up to 256: the
-// forward, dq and dK/dV. Tiles of 64 rows by 64 (forward) or 32 (backward) columns
-// live in shared memory; one pass over the keys with the running maximum and sum of
-// the softmax; O, dq, dK and dV stay in registers. Rows are stored with a pitch of an
-// odd number of 16-byte units, so the 16 threads that read 16 consecutive rows as
-// float4 touch different banks.
+// forward, dq and dK/dV, and the small products of the K/V rebuild and its backward.
 //
-// Thread (tx, ty) of 16 x 16 owns tile rows 4 ty .. 4 ty + 3 and, of the score tile,
+// Attention: tiles of 16 RI rows by 64 (forward) or 32 (backward) columns live in shared
+// memory; one pass over the keys with the running maximum and sum of the softmax; O, dq,
+// dK and dV stay in registers. Rows are stored with a pitch of an odd number of 16-byte
+// units, so the 16 threads that read 16 consecutive rows as float4 touch different banks.
+// Thread (tx, ty) of 16 x 16 owns tile rows RI ty .. RI ty + RI - 1 and, of the score tile,
 // columns tx, tx + 16, ...; of a head-wide accumulator, columns 64 c + 4 tx .. + 3.
-// Every element of the shared dimension costs a thread 8 (4 + 4) 16-byte loads per 64
-// multiply-adds in the 64 x 64 score product. N = ceil(widest head / 64) picks the
-// accumulator's width.
+// N = ceil(widest head / 64) picks the accumulator's width, RI the rows: 4 gives the most
+// multiply-adds per shared-memory load (64 per 8 16-byte loads in the 64 x 64 product), but a
+// problem of a few hundred rows then fills a tenth of the SMs, each walking its keys alone;
+// RI = 1 gives four times the CTAs (measured at 256 rows, 4 heads: RI_NUMBERS).
+// A tile's global loads are issued eight rows deep per warp, lanes along the width; one
+// value at a time cost 14 us per key step.
 #include "mask.h"
 
 #include <algorithm>
@@ -19,7 +22,6 @@ namespace laga {
 namespace {
 
 using ll = long long;
-constexpr int ROWS = 64;     // tile rows: queries (forward, dq) or keys (dK/dV)
 constexpr int KFWD = 64;     // keys per step, forward
 constexpr int KBWD = 32;     // keys (dq) or queries (dK/dV) per step
 constexpr int THREADS = 256;
@@ -61,15 +63,21 @@ __device__ __forceinline__ void store(void* p, bool is_bf16, ll at, float v) {
     static_cast<float*>(p)[at] = v;
 }
 
-// dst[r][k] = get(r, k) for r < rows, k < width, zero up to the next multiple of four.
-template <class F>
-__device__ __forceinline__ void fill(float4* dst, int pitch, int rows, int width, F&& get) {
-  const int w = (width + 3) & ~3;
+// dst[r][k] = get(r, k) for r < ROWS (a multiple of 8), k < width, zero up to the next multiple of four.
+template <int ROWS, class F>
+__device__ __forceinline__ void fill(float4* dst, int pitch, int width, F&& get) {
+  const int w = (width + 3) & ~3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int DEEP = ROWS / 8 < 8 ? ROWS / 8 : 8;
   float* f = reinterpret_cast<float*>(dst);
-  for (int e = threadIdx.x; e < rows * w; e += THREADS) {
-    const int r = e / w, k = e - r * w;
-    f[r * pitch * 4 + k] = k < width ? get(r, k) : 0.f;
-  }
+  for (int k = lane; k < w; k += 32)
+#pragma unroll
+    for (int r0 = 0; r0 < ROWS; r0 += 8 * DEEP) {
+      float v[DEEP];
+#pragma unroll
+      for (int i = 0; i < DEEP; ++i) v[i] = k < width ? get(r0 + 8 * i + warp, k) : 0.f;
+#pragma unroll
+      for (int i = 0; i < DEEP; ++i) f[(r0 + 8 * i + warp) * pitch * 4 + k] = v[i];
+    }
 }
 
 __device__ __forceinline__ float dot4(float4 a, float4 b, float acc) {
@@ -79,40 +87,65 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float acc) {
   return fmaf(a.w, b.w, acc);
 }
 
-// acc[i][j] += sum_k A[4 ty + i][k] B[tx + 16 j][k]
-template <int NJ>
+// acc[i][j] = sum_k A[RI ty + i][k] B[tx + 16 j][k]
+template <int RI, int NJ>
 __device__ __forceinline__ void score_tile(const float4* A, const float4* B, int pitch, int n4, int tx, int ty,
-                                           float (&acc)[4][NJ]) {
+                                           float (&acc)[RI][NJ]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = 0.f;
+#pragma unroll 2
   for (int k = 0; k < n4; ++k) {
-    float4 a[4], b[NJ];
+    float4 a[RI], b[NJ];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = A[(4 * ty + i) * pitch + k];
+    for (int i = 0; i < RI; ++i) a[i] = A[(RI * ty + i) * pitch + k];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) b[j] = B[(tx + 16 * j) * pitch + k];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = dot4(a[i], b[j], acc[i][j]);
   }
 }
 
-// acc[i][c] += sum_n Wt[n][4 ty + i] B[n][64 c + 4 tx ..]; Wt has a pitch of 17 float4
-template <int N>
-__device__ __forceinline__ void weighted_rows(const float4* Wt, const float4* B, int pitch, int count, int width4, int tx,
-                                              int ty, float4 (&acc)[4][N]) {
+// A column of RI weights per (row of the shared dimension, ty): written by the score tile's
+// owner, read by the accumulators'. Pitch 17 keeps the 16 threads of a write apart.
+template <int RI>
+__device__ __forceinline__ void put_weights(float* w, int n, int ty, const float (&v)[RI]) {
+  float* d = w + (n * 17 + ty) * RI;
+  if constexpr (RI == 4)
+    *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
+  else if constexpr (RI == 2)
+    *reinterpret_cast<float2*>(d) = make_float2(v[0], v[1]);
+  else
+    d[0] = v[0];
+}
+
+// acc[i][c] += sum_n Wt[n][RI ty + i] B[n][64 c + 4 tx ..]
+template <int RI, int N>
+__device__ __forceinline__ void weighted_rows(const float* Wt, const float4* B, int pitch, int count, int width4, int tx,
+                                              int ty, float4 (&acc)[RI][N]) {
+#pragma unroll 4
   for (int n = 0; n < count; ++n) {
-    const float4 w = Wt[n * 17 + ty];
-    const float wi[4] = {w.x, w.y, w.z, w.w};
+    float wi[RI];
+    const float* w = Wt + (n * 17 + ty) * RI;
+    if constexpr (RI == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(w);
+      wi[0] = t.x;
+      wi[1] = t.y;
+      wi[2] = t.z;
+      wi[3] = t.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < RI; ++i) wi[i] = w[i];
+    }
 #pragma unroll
     for (int c = 0; c < N; ++c) {
       if (16 * c + tx >= width4) continue;
       const float4 b = B[n * pitch + 16 * c + tx];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < RI; ++i) {
         acc[i][c].x = fmaf(wi[i], b.x, acc[i][c].x);
         acc[i][c].y = fmaf(wi[i], b.y, acc[i][c].y);
         acc[i][c].z = fmaf(wi[i], b.z, acc[i][c].z);
@@ -133,9 +166,10 @@ __device__ __forceinline__ float score_of(const SimtParams& p, float raw, float 
   return s - slope * fabsf(static_cast<float>(pos - key));
 }
 
-__device__ __forceinline__ void load_k(const SimtParams& p, float4* dst, int pitch, int b, int h, int first, int rows) {
+template <int ROWS>
+__device__ __forceinline__ void load_k(const SimtParams& p, float4* dst, int pitch, int b, int h, int first) {
   const Dims& d = p.d;
-  fill(dst, pitch, rows, d.d_qk(), [&](int r, int k) {
+  fill<ROWS>(dst, pitch, d.d_qk(), [&](int r, int k) {
     const int j = first + r;
     if (j >= d.S) return 0.f;
     const ll row = static_cast<ll>(b) * d.S + j;
@@ -143,23 +177,26 @@ __device__ __forceinline__ void load_k(const SimtParams& p, float4* dst, int pit
                         : load(p.k_rope, p.rope_bf16, row * d.d_rope + (k - d.d_nope));
   });
 }
-__device__ __forceinline__ void load_v(const SimtParams& p, float4* dst, int pitch, int b, int h, int first, int rows) {
+template <int ROWS>
+__device__ __forceinline__ void load_v(const SimtParams& p, float4* dst, int pitch, int b, int h, int first) {
   const Dims& d = p.d;
-  fill(dst, pitch, rows, d.d_v, [&](int r, int k) {
+  fill<ROWS>(dst, pitch, d.d_v, [&](int r, int k) {
     const int j = first + r;
     return j < d.S ? p.v[((static_cast<ll>(b) * d.S + j) * d.n_h + h) * d.d_v + k] : 0.f;
   });
 }
-__device__ __forceinline__ void load_q(const SimtParams& p, float4* dst, int pitch, int b, int h, int first, int rows) {
+template <int ROWS>
+__device__ __forceinline__ void load_q(const SimtParams& p, float4* dst, int pitch, int b, int h, int first) {
   const Dims& d = p.d;
-  fill(dst, pitch, rows, d.d_qk(), [&](int r, int k) {
+  fill<ROWS>(dst, pitch, d.d_qk(), [&](int r, int k) {
     const int i = first + r;
     return i < d.Sq ? load(p.q, p.q_bf16, ((static_cast<ll>(b) * d.Sq + i) * d.n_h + h) * d.d_qk() + k) : 0.f;
   });
 }
-__device__ __forceinline__ void load_do(const SimtParams& p, float4* dst, int pitch, int b, int h, int first, int rows) {
+template <int ROWS>
+__device__ __forceinline__ void load_do(const SimtParams& p, float4* dst, int pitch, int b, int h, int first) {
   const Dims& d = p.d;
-  fill(dst, pitch, rows, d.d_v, [&](int r, int k) {
+  fill<ROWS>(dst, pitch, d.d_v, [&](int r, int k) {
     const int i = first + r;
     return i < d.Sq ? p.dout[((static_cast<ll>(b) * d.Sq + i) * d.n_h + h) * d.d_v + k] : 0.f;
   });
@@ -177,45 +214,47 @@ __device__ __forceinline__ float half_warp_sum(float v) {
 }
 
 // out and lse of 64 query rows of one head.
-template <int N>
+template <int N, int RI>
 __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
+  constexpr int ROWS = 16 * RI;
   extern __shared__ float4 sm[];
   const Dims& d = p.d;
   const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v);
-  float4 *sq = sm, *sk = sq + ROWS * pk, *sv = sk + KFWD * pk, *sp = sv + KFWD * pv;
+  float4 *sq = sm, *sk = sq + ROWS * pk, *sv = sk + KFWD * pk, *weights = sv + KFWD * pv;
+  float* sp = reinterpret_cast<float*>(weights);
   const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int i0 = t * ROWS + 4 * ty;  // this thread's first row
-  load_q(p, sq, pk, b, h, t * ROWS, ROWS);
-  int lo[4], hi[4];
-  bool poisoned[4];
+  const int i0 = t * ROWS + RI * ty;  // this thread's first row
+  load_q<ROWS>(p, sq, pk, b, h, t * ROWS);
+  int lo[RI], hi[RI];
+  bool poisoned[RI];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RI; ++i) {
     const int2 v = p.rows[static_cast<ll>(b) * d.sq_pad + i0 + i];
     poisoned[i] = v.x < 0;
     lo[i] = v.x & 0x7fffffff;
     hi[i] = v.y;
   }
   const float slope = p.slopes ? p.slopes[h] : 0.f;
-  float m[4], l[4];
-  float4 o[4][N];
+  float m[RI], l[RI];
+  float4 o[RI][N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RI; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
     for (int c = 0; c < N; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const int2 hull = p.q_hull[static_cast<ll>(b) * (d.sq_pad / ROWS) + t];
+  const int2 hull = p.q_hull[static_cast<ll>(b) * (d.sq_pad / 64) + t * ROWS / 64];  // of the 64 rows around
   for (int j0 = hull.x < hull.y ? hull.x / KFWD * KFWD : 0; j0 < hull.y; j0 += KFWD) {
     __syncthreads();
-    load_k(p, sk, pk, b, h, j0, KFWD);
-    load_v(p, sv, pv, b, h, j0, KFWD);
+    load_k<KFWD>(p, sk, pk, b, h, j0);
+    load_v<KFWD>(p, sv, pv, b, h, j0);
     __syncthreads();
-    float s[4][4];
-    score_tile(sq, sk, pk, (d.d_qk() + 3) / 4, tx, ty, s);
+    float s[RI][4];
+    score_tile<RI>(sq, sk, pk, (d.d_qk() + 3) / 4, tx, ty, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RI; ++i) {
       const int pos = position(d, i0 + i);
       float unused, mt = -INFINITY;
 #pragma unroll
@@ -244,12 +283,17 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sp[(tx + 16 * j) * 17 + ty] = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+    for (int j = 0; j < 4; ++j) {
+      float w[RI];
+#pragma unroll
+      for (int i = 0; i < RI; ++i) w[i] = s[i][j];
+      put_weights<RI>(sp, tx + 16 * j, ty, w);
+    }
     __syncthreads();
-    weighted_rows<N>(sp, sv, pv, KFWD, (d.d_v + 3) / 4, tx, ty, o);
+    weighted_rows<RI, N>(sp, sv, pv, KFWD, (d.d_v + 3) / 4, tx, ty, o);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RI; ++i) {
     if (i0 + i >= d.Sq) continue;
     float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
     float L = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
@@ -269,21 +313,23 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
 }
 
 // dq of 64 query rows of one head.
-template <int N>
+template <int N, int RI>
 __global__ void __launch_bounds__(THREADS) masked_simt_dq(const SimtParams p) {
+  constexpr int ROWS = 16 * RI;
   extern __shared__ float4 sm[];
   const Dims& d = p.d;
   const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v);
-  float4 *sq = sm, *sdo = sq + ROWS * pk, *sk = sdo + ROWS * pv, *sv = sk + KBWD * pk, *sds = sv + KBWD * pv;
+  float4 *sq = sm, *sdo = sq + ROWS * pk, *sk = sdo + ROWS * pv, *sv = sk + KBWD * pk, *weights = sv + KBWD * pv;
+  float* sds = reinterpret_cast<float*>(weights);
   const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int i0 = t * ROWS + 4 * ty;
-  load_q(p, sq, pk, b, h, t * ROWS, ROWS);
-  load_do(p, sdo, pv, b, h, t * ROWS, ROWS);
-  int lo[4], hi[4];
-  float L[4], D[4];
+  const int i0 = t * ROWS + RI * ty;
+  load_q<ROWS>(p, sq, pk, b, h, t * ROWS);
+  load_do<ROWS>(p, sdo, pv, b, h, t * ROWS);
+  int lo[RI], hi[RI];
+  float L[RI], D[RI];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RI; ++i) {
     const int2 v = p.rows[static_cast<ll>(b) * d.sq_pad + i0 + i];
     lo[i] = v.x & 0x7fffffff;
     hi[i] = v.y;
@@ -293,22 +339,22 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dq(const SimtParams p) {
     D[i] = in ? p.delta[at] : 0.f;
   }
   const float slope = p.slopes ? p.slopes[h] : 0.f;
-  float4 acc[4][N];
+  float4 acc[RI][N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RI; ++i)
 #pragma unroll
     for (int c = 0; c < N; ++c) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int2 hull = p.q_hull[static_cast<ll>(b) * (d.sq_pad / ROWS) + t];
+  const int2 hull = p.q_hull[static_cast<ll>(b) * (d.sq_pad / 64) + t * ROWS / 64];  // of the 64 rows around
   for (int j0 = hull.x < hull.y ? hull.x / KBWD * KBWD : 0; j0 < hull.y; j0 += KBWD) {
     __syncthreads();
-    load_k(p, sk, pk, b, h, j0, KBWD);
-    load_v(p, sv, pv, b, h, j0, KBWD);
+    load_k<KBWD>(p, sk, pk, b, h, j0);
+    load_v<KBWD>(p, sv, pv, b, h, j0);
     __syncthreads();
-    float s[4][2], dp[4][2];
-    score_tile(sq, sk, pk, (d.d_qk() + 3) / 4, tx, ty, s);
-    score_tile(sdo, sv, pv, (d.d_v + 3) / 4, tx, ty, dp);
+    float s[RI][2], dp[RI][2];
+    score_tile<RI>(sq, sk, pk, (d.d_qk() + 3) / 4, tx, ty, s);
+    score_tile<RI>(sdo, sv, pv, (d.d_v + 3) / 4, tx, ty, dp);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RI; ++i) {
       const int pos = position(d, i0 + i);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -319,12 +365,17 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dq(const SimtParams p) {
       }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) sds[(tx + 16 * j) * 17 + ty] = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+    for (int j = 0; j < 2; ++j) {
+      float w[RI];
+#pragma unroll
+      for (int i = 0; i < RI; ++i) w[i] = s[i][j];
+      put_weights<RI>(sds, tx + 16 * j, ty, w);
+    }
     __syncthreads();
-    weighted_rows<N>(sds, sk, pk, KBWD, (d.d_qk() + 3) / 4, tx, ty, acc);
+    weighted_rows<RI, N>(sds, sk, pk, KBWD, (d.d_qk() + 3) / 4, tx, ty, acc);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RI; ++i) {
     if (i0 + i >= d.Sq) continue;
     const ll row = (static_cast<ll>(b) * d.Sq + i0 + i) * d.n_h + h;
 #pragma unroll
@@ -340,22 +391,23 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dq(const SimtParams p) {
 }
 
 // dK (both parts) and dV of 64 keys of one head.
-template <int N>
+template <int N, int RI>
 __global__ void __launch_bounds__(THREADS) masked_simt_dkv(const SimtParams p) {
+  constexpr int ROWS = 16 * RI;
   extern __shared__ float4 sm[];
   const Dims& d = p.d;
   const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v);
-  float4 *sk = sm, *sv = sk + ROWS * pk, *sq = sv + ROWS * pv, *sdo = sq + KBWD * pk, *sp = sdo + KBWD * pv;
-  float4* sds = sp + KBWD * 17;
+  float4 *sk = sm, *sv = sk + ROWS * pk, *sq = sv + ROWS * pv, *sdo = sq + KBWD * pk, *weights = sdo + KBWD * pv;
+  float *sp = reinterpret_cast<float*>(weights), *sds = sp + KBWD * 17 * RI;
   const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int k0 = t * ROWS + 4 * ty;  // this thread's first key
-  load_k(p, sk, pk, b, h, t * ROWS, ROWS);
-  load_v(p, sv, pv, b, h, t * ROWS, ROWS);
+  const int k0 = t * ROWS + RI * ty;  // this thread's first key
+  load_k<ROWS>(p, sk, pk, b, h, t * ROWS);
+  load_v<ROWS>(p, sv, pv, b, h, t * ROWS);
   const float slope = p.slopes ? p.slopes[h] : 0.f;
-  float4 dk[4][N], dv[4][N];
+  float4 dk[RI][N], dv[RI][N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RI; ++i)
 #pragma unroll
     for (int c = 0; c < N; ++c) dk[i][c] = dv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int nq64 = d.sq_pad / 64;
@@ -363,12 +415,12 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dkv(const SimtParams p) {
     const int2 hull = p.q_hull[static_cast<ll>(b) * nq64 + q0 / 64];
     if (hull.x >= hull.y || hull.x >= (t + 1) * ROWS || hull.y <= t * ROWS) continue;  // the same for every thread
     __syncthreads();
-    load_q(p, sq, pk, b, h, q0, KBWD);
-    load_do(p, sdo, pv, b, h, q0, KBWD);
+    load_q<KBWD>(p, sq, pk, b, h, q0);
+    load_do<KBWD>(p, sdo, pv, b, h, q0);
     __syncthreads();
-    float s[4][2], dp[4][2];
-    score_tile(sk, sq, pk, (d.d_qk() + 3) / 4, tx, ty, s);
-    score_tile(sv, sdo, pv, (d.d_v + 3) / 4, tx, ty, dp);
+    float s[RI][2], dp[RI][2];
+    score_tile<RI>(sk, sq, pk, (d.d_qk() + 3) / 4, tx, ty, s);
+    score_tile<RI>(sv, sdo, pv, (d.d_v + 3) / 4, tx, ty, dp);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int i = q0 + tx + 16 * j;
@@ -378,7 +430,7 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dkv(const SimtParams p) {
       const float L = in ? p.lse_row[at] : INFINITY, D = in ? p.delta[at] : 0.f;
       const int pos = position(d, i);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < RI; ++k) {
         const int key = k0 + k;
         float dcap = 1.f;
         const float v = score_of(p, s[k][j], slope, pos, key, &dcap);
@@ -386,15 +438,21 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dkv(const SimtParams p) {
         s[k][j] = e;
         dp[k][j] = e * (dp[k][j] - D) * dcap;
       }
-      sp[(tx + 16 * j) * 17 + ty] = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-      sds[(tx + 16 * j) * 17 + ty] = make_float4(dp[0][j], dp[1][j], dp[2][j], dp[3][j]);
+      float w[RI], g[RI];
+#pragma unroll
+      for (int k = 0; k < RI; ++k) {
+        w[k] = s[k][j];
+        g[k] = dp[k][j];
+      }
+      put_weights<RI>(sp, tx + 16 * j, ty, w);
+      put_weights<RI>(sds, tx + 16 * j, ty, g);
     }
     __syncthreads();
-    weighted_rows<N>(sp, sdo, pv, KBWD, (d.d_v + 3) / 4, tx, ty, dv);
-    weighted_rows<N>(sds, sq, pk, KBWD, (d.d_qk() + 3) / 4, tx, ty, dk);
+    weighted_rows<RI, N>(sp, sdo, pv, KBWD, (d.d_v + 3) / 4, tx, ty, dv);
+    weighted_rows<RI, N>(sds, sq, pk, KBWD, (d.d_qk() + 3) / 4, tx, ty, dk);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RI; ++i) {
     const int j = k0 + i;
     if (j >= d.S) continue;
     const ll row = (static_cast<ll>(b) * d.S + j) * d.n_h + h;
@@ -441,7 +499,7 @@ Ws carve(const Dims& d, int elem, bool bwd, char*& p) {
   };
   const size_t keys = static_cast<size_t>(d.B) * d.S * d.n_h, qs = static_cast<size_t>(d.B) * d.Sq * d.n_h;
   Ws w{};
-  w.kn = take(keys * d.d_nope);  // first: what a backward that reuses the forward's rebuild reads
+  w.kn = take(keys * d.d_nope);  // K, V and the mask's buffers first: what a backward with reuse reads
   w.v = take(keys * d.d_v);
   w.mask = mask_carve(d, elem, p);
   if (bwd) {
@@ -479,15 +537,182 @@ SimtParams params(const Dims& d, bool is_bf16, const ScoreMods& mods, const Ws& 
   return p;
 }
 
-// Launches kern<1>, <2> or <4> by the widest head.
-template <class F1, class F2, class F4>
-cudaError_t launch(const Dims& d, F1 k1, F2 k2, F4 k4, dim3 grid, size_t smem, const SimtParams& p, cudaStream_t st) {
-  const int w = std::max(d.d_qk(), d.d_v);
-  void (*kern)(SimtParams) = w <= 64 ? k1 : w <= 128 ? k2 : k4;
+// Rows per thread: 4 unless that leaves CTAs for fewer than two per SM (1: four times as many).
+int rows_per_thread(const Dims& d, int rows) {
+  const ll ctas = static_cast<ll>((rows + 63) / 64) * d.n_h * d.B;
+  return ctas >= 2 * sm_count() ? 4 : 2 * ctas >= 2 * sm_count() ? 2 : 1;
+}
+
+enum Which { FWD, DQ, DKV };
+template <Which W, int N, int RI>
+constexpr auto kernel_of() {
+  if constexpr (W == FWD)
+    return masked_simt_fwd<N, RI>;
+  else if constexpr (W == DQ)
+    return masked_simt_dq<N, RI>;
+  else
+    return masked_simt_dkv<N, RI>;
+}
+
+template <Which W, int RI>
+cudaError_t launch_rows(const Dims& d, int rows, const SimtParams& p, cudaStream_t st) {
+  const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v), w = std::max(d.d_qk(), d.d_v);
+  constexpr int R = 16 * RI;
+  const size_t smem = W == FWD ? sizeof(float4) * ((R + KFWD) * pk + KFWD * pv) + sizeof(float) * KFWD * 17 * RI
+                               : sizeof(float4) * (R + KBWD) * (pk + pv) +
+                                     sizeof(float) * (W == DKV ? 2 : 1) * KBWD * 17 * RI;
+  void (*kern)(SimtParams) = w <= 64 ? kernel_of<W, 1, RI>() : w <= 128 ? kernel_of<W, 2, RI>() : kernel_of<W, 4, RI>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kern<<<grid, THREADS, smem, st>>>(p);
+  kern<<<dim3((rows + R - 1) / R, d.n_h, d.B), THREADS, smem, st>>>(p);
   return cudaGetLastError();
+}
+
+template <Which W>
+cudaError_t launch(const Dims& d, int rows, const SimtParams& p, cudaStream_t st) {
+  switch (rows_per_thread(d, rows)) {
+    case 4: return launch_rows<W, 4>(d, rows, p, st);
+    case 2: return launch_rows<W, 2>(d, rows, p, st);
+    default: return launch_rows<W, 1>(d, rows, p, st);
+  }
+}
+
+// ---- the rebuild's products: C[m][n] = sum over one or two pairs of A(m, k) B(k, n), any
+// strides, several such products in one launch. A CTA makes one 32 x 32 tile; its four groups
+// of 64 threads each take every fourth block of 16 k, and their sums are added in a fixed
+// order through shared memory. These products are small (a weight gradient is d_c x n_h d
+// with k = all keys): a few dozen tiles, so the k loop's latency is the time, and both the
+// small tile and the split shorten it (72 x 120 with k = 1018: GEMM_NUMBERS).
+struct GemmPair {
+  const void *a, *b;
+  bool a_bf16, b_bf16;
+  int K;
+  ll am, ak, bk, bn;
+};
+struct GemmJob {
+  int M, N, pairs, tiles_n, first_tile;
+  GemmPair p[2];
+  void* c;
+  bool c_bf16;
+  ll cm, cn;
+};
+struct GemmJobs {
+  int n;
+  GemmJob job[3];
+};
+
+__global__ void __launch_bounds__(THREADS) small_gemm_kernel(const GemmJobs jobs) {
+  constexpr int T = 32, KB = 16, GROUPS = 4;
+  __shared__ float As[GROUPS][KB][T + 4], Bs[GROUPS][KB][T + 4];
+  int which = 0;
+  while (which + 1 < jobs.n && static_cast<int>(blockIdx.x) >= jobs.job[which + 1].first_tile) ++which;
+  const GemmJob& j = jobs.job[which];
+  const int tile = static_cast<int>(blockIdx.x) - j.first_tile;
+  const int m0 = tile / j.tiles_n * T, n0 = tile % j.tiles_n * T;
+  const int g = threadIdx.x >> 6, l = threadIdx.x & 63, tx = l & 7, ty = l >> 3;
+  float acc[4][4] = {};
+  for (int q = 0; q < j.pairs; ++q) {
+    const GemmPair& p = j.p[q];
+    const int steps = (p.K + GROUPS * KB - 1) / (GROUPS * KB);
+    // lanes along whichever index is contiguous
+    const bool a_k = p.ak == 1, b_n = p.bn == 1;
+    float ra[8], rb[8];
+    auto fetch = [&](int step) {
+      const int k0 = (step * GROUPS + g) * KB;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = l + 64 * e;  // 512 = 16 k x 32
+        const int am = a_k ? i >> 4 : i & 31, ak = a_k ? i & 15 : i >> 5;
+        const int bk = b_n ? i >> 5 : i & 15, bn = b_n ? i & 31 : i >> 4;
+        ra[e] = m0 + am < j.M && k0 + ak < p.K ? load(p.a, p.a_bf16, (m0 + am) * p.am + (k0 + ak) * p.ak) : 0.f;
+        rb[e] = n0 + bn < j.N && k0 + bk < p.K ? load(p.b, p.b_bf16, (k0 + bk) * p.bk + (n0 + bn) * p.bn) : 0.f;
+      }
+    };
+    fetch(0);
+    for (int step = 0; step < steps; ++step) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = l + 64 * e;
+        As[g][a_k ? i & 15 : i >> 5][a_k ? i >> 4 : i & 31] = ra[e];
+        Bs[g][b_n ? i >> 5 : i & 15][b_n ? i & 31 : i >> 4] = rb[e];
+      }
+      __syncthreads();
+      if (step + 1 < steps) fetch(step + 1);
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        const float4 a = *reinterpret_cast<const float4*>(&As[g][k][4 * ty]);
+        const float4 b = *reinterpret_cast<const float4*>(&Bs[g][k][4 * tx]);
+        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) acc[x][y] = fmaf(av[x], bv[y], acc[x][y]);
+      }
+    }
+  }
+  // the groups' sums, over the operand tiles: [group][32][36]
+  __syncthreads();
+  float* sums = &As[0][0][0] + g * (T * (T + 4) / 2);  // 16 rows' space per group in As, 16 in Bs
+  float* more = &Bs[0][0][0] + g * (T * (T + 4) / 2);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int r = 4 * ty + x;
+    float* d = r < 16 ? sums + r * (T + 4) : more + (r - 16) * (T + 4);
+    *reinterpret_cast<float4*>(d + 4 * tx) = make_float4(acc[x][0], acc[x][1], acc[x][2], acc[x][3]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int i = threadIdx.x + THREADS * e;  // 1024 elements
+    const int r = j.cn == 1 ? i >> 5 : i & 31, c = j.cn == 1 ? i & 31 : i >> 5;
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k)
+      v += (r < 16 ? &As[0][0][0] : &Bs[0][0][0])[k * (T * (T + 4) / 2) + (r & 15) * (T + 4) + c];
+    if (m0 + r < j.M && n0 + c < j.N) store(j.c, j.c_bf16, (m0 + r) * j.cm + (n0 + c) * j.cn, v);
+  }
+}
+
+struct Gemms {
+  GemmJobs jobs{};
+  ll tiles = 0;
+  void add(int M, int N, const GemmPair& p, void* c, bool c_bf16, ll cm, ll cn, const GemmPair* p2 = nullptr) {
+    if (M == 0 || N == 0) return;
+    GemmJob& j = jobs.job[jobs.n++];
+    j = GemmJob{M, N, p2 ? 2 : 1, (N + 31) / 32, static_cast<int>(tiles), {p, p2 ? *p2 : GemmPair{}}, c, c_bf16, cm, cn};
+    tiles += static_cast<ll>((M + 31) / 32) * j.tiles_n;
+  }
+  cudaError_t run(cudaStream_t st) const {
+    if (tiles == 0) return cudaSuccess;
+    if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+    small_gemm_kernel<<<static_cast<unsigned>(tiles), THREADS, 0, st>>>(jobs);
+    return cudaGetLastError();
+  }
+};
+
+// K_nope = c W_UK, V = c W_UV
+cudaError_t rebuild(const Dims& d, bool bf, const void* c, const void* W_UK, const void* W_UV, float* kn, float* v,
+                    cudaStream_t st) {
+  const int M = d.B * d.S;
+  const ll nk = static_cast<ll>(d.n_h) * d.d_nope, nv = static_cast<ll>(d.n_h) * d.d_v;
+  Gemms g;
+  g.add(M, static_cast<int>(nk), GemmPair{c, W_UK, bf, bf, d.d_c, d.d_c, 1, nk, 1}, kn, false, nk, 1);
+  g.add(M, static_cast<int>(nv), GemmPair{c, W_UV, bf, bf, d.d_c, d.d_c, 1, nv, 1}, v, false, nv, 1);
+  return g.run(st);
+}
+
+// dc = dK W_UK^T + dV W_UV^T, dW_UK = c^T dK, dW_UV = c^T dV (k runs over the batch's rows too)
+cudaError_t rebuild_bwd(const Dims& d, bool bf, const void* c, const void* W_UK, const void* W_UV, const float* dk,
+                        const float* dv, const BwdGrads& o, cudaStream_t st) {
+  const int M = d.B * d.S;
+  const ll nk = static_cast<ll>(d.n_h) * d.d_nope, nv = static_cast<ll>(d.n_h) * d.d_v;
+  Gemms g;
+  g.add(d.d_c, static_cast<int>(nk), GemmPair{c, dk, bf, false, M, 1, d.d_c, nk, 1}, o.dW_UK, bf, nk, 1);
+  g.add(d.d_c, static_cast<int>(nv), GemmPair{c, dv, bf, false, M, 1, d.d_c, nv, 1}, o.dW_UV, bf, nv, 1);
+  const GemmPair second{dv, W_UV, false, bf, static_cast<int>(nv), nv, 1, 1, nv};
+  g.add(M, d.d_c, GemmPair{dk, W_UK, false, bf, static_cast<int>(nk), nk, 1, 1, nk}, o.dc_kv, bf, d.d_c, 1, &second);
+  return g.run(st);
 }
 
 }  // namespace
@@ -501,17 +726,18 @@ LaunchResult simt_masked_fwd(const Dims& d, bool is_bf16, const ScoreMods& mods,
   char* at = static_cast<char*>(ws);
   const Ws w = carve(d, is_bf16 ? 2 : 4, false, at);
   LaunchResult r = mask_prepare(d, is_bf16, key_lo, key_hi, c_kv, k_rope, w.mask, false, st);
-  if (r.ok()) r = simt_reconstruct(d, is_bf16, w.mask.c_kv, W_UK, W_UV, w.kn, w.v, true, st);
   if (!r.ok()) return r;
+  r.err = rebuild(d, is_bf16, w.mask.c_kv, W_UK, W_UV, w.kn, w.v, st);
+  if (r.err != cudaSuccess) {
+    r.what = "K/V rebuild (CUDA cores)";
+    return r;
+  }
   SimtParams p = params(d, is_bf16, mods, w);
   p.q = q;
   p.q_bf16 = is_bf16;
   p.out = out;
   p.lse = lse;
-  const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v);
-  const size_t smem = sizeof(float4) * ((ROWS + KFWD) * pk + KFWD * pv + KFWD * 17);
-  r.err = launch(d, masked_simt_fwd<1>, masked_simt_fwd<2>, masked_simt_fwd<4>,
-                 dim3((d.Sq + ROWS - 1) / ROWS, d.n_h, d.B), smem, p, st);
+  r.err = launch<FWD>(d, d.Sq, p, st);
   if (r.err != cudaSuccess) r.what = "masked attention forward (CUDA cores)";
   return r;
 }
@@ -522,8 +748,12 @@ LaunchResult simt_masked_bwd(const Dims& d, bool is_bf16, const ScoreMods& mods,
                              const void* dout, const BwdGrads& g, void* ws, bool reuse_kv, cudaStream_t st) {
   char* at = static_cast<char*>(ws);
   const Ws w = carve(d, is_bf16 ? 2 : 4, true, at);
-  LaunchResult r = mask_prepare(d, is_bf16, key_lo, key_hi, c_kv, k_rope, w.mask, false, st);
-  if (r.ok() && !reuse_kv) r = simt_reconstruct(d, is_bf16, w.mask.c_kv, W_UK, W_UV, w.kn, w.v, true, st);
+  LaunchResult r;
+  if (!reuse_kv) r = mask_prepare(d, is_bf16, key_lo, key_hi, c_kv, k_rope, w.mask, false, st);
+  if (r.ok() && !reuse_kv) {
+    r.err = rebuild(d, is_bf16, w.mask.c_kv, W_UK, W_UV, w.kn, w.v, st);
+    if (r.err != cudaSuccess) r.what = "K/V rebuild (CUDA cores)";
+  }
   if (r.ok()) r = simt_mask_bwd_pre(d, is_bf16, q, out, q8, out8, dout, lse, w.lse_row, w.delta, w.q, w.dout, st);
   if (!r.ok()) return r;
   SimtParams p = params(d, is_bf16, mods, w);
@@ -536,13 +766,8 @@ LaunchResult simt_masked_bwd(const Dims& d, bool is_bf16, const ScoreMods& mods,
   p.dkn = w.dkn;
   p.dv = w.dv;
   p.dkr = w.dkr;
-  const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v);
-  const size_t both = sizeof(float4) * (ROWS + KBWD) * (pk + pv);
-  r.err = launch(d, masked_simt_dq<1>, masked_simt_dq<2>, masked_simt_dq<4>, dim3((d.Sq + ROWS - 1) / ROWS, d.n_h, d.B),
-                 both + sizeof(float4) * KBWD * 17, p, st);
-  if (r.err == cudaSuccess)
-    r.err = launch(d, masked_simt_dkv<1>, masked_simt_dkv<2>, masked_simt_dkv<4>,
-                   dim3((d.S + ROWS - 1) / ROWS, d.n_h, d.B), both + sizeof(float4) * 2 * KBWD * 17, p, st);
+  r.err = launch<DQ>(d, d.Sq, p, st);
+  if (r.err == cudaSuccess) r.err = launch<DKV>(d, d.S, p, st);
   const ll nr = static_cast<ll>(d.B) * d.S * d.d_rope;
   if (r.err == cudaSuccess && nr > 0) {
     const unsigned grid = static_cast<unsigned>((nr + 255) / 256);
@@ -556,7 +781,9 @@ LaunchResult simt_masked_bwd(const Dims& d, bool is_bf16, const ScoreMods& mods,
     r.what = "masked attention backward (CUDA cores)";
     return r;
   }
-  return simt_rebuild_bwd(d, is_bf16, w.mask.c_kv, W_UK, W_UV, w.dkn, w.dv, g.dc_kv, g.dW_UK, g.dW_UV, st);
+  r.err = rebuild_bwd(d, is_bf16, w.mask.c_kv, W_UK, W_UV, w.dkn, w.dv, g, st);
+  if (r.err != cudaSuccess) r.what = "rebuild backward (CUDA cores)";
+  return r;
 }
 
 }  // namespace laga

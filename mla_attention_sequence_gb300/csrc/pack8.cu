@@ -76,30 +76,43 @@ struct Chunk<float> {
   }
 };
 
+// Chunks a thread of the aligned kernels takes, 256 apart, all loads issued before the first
+// use: one 16-byte load per thread in flight (32 KB an SM) leaves the memory partly idle.
+constexpr int UNROLL = 4;
+
 template <typename T>
 __global__ void __launch_bounds__(256) pack8_kernel(ll chunks, const T* __restrict__ x, uint8_t* __restrict__ codes,
                                                     uint8_t* __restrict__ scales) {
   using C = Chunk<T>;
   constexpr int PER = kPackBlock / C::N;  // threads per block
-  const ll i = static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const bool in = i < chunks;
-  float v[C::N];
-  C::get(in ? reinterpret_cast<const uint4*>(x)[i] : make_uint4(0u, 0u, 0u, 0u), v);
-  uint32_t top = 0u;
+  const ll first = static_cast<ll>(blockIdx.x) * (256 * UNROLL) + threadIdx.x;
+  uint4 raw[UNROLL];
 #pragma unroll
-  for (int k = 0; k < C::N; ++k) top = max(top, size_bits(v[k]));
-#pragma unroll
-  for (int o = PER / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const uint32_t e = scale_exponent(top);
-  const float inv = inverse_scale(e);
-  if (!in) return;
-  if constexpr (C::N == 8) {
-    reinterpret_cast<uint2*>(codes)[i] = make_uint2(codes2(v[0], v[1], inv) | codes2(v[2], v[3], inv) << 16,
-                                                    codes2(v[4], v[5], inv) | codes2(v[6], v[7], inv) << 16);
-  } else {
-    reinterpret_cast<uint32_t*>(codes)[i] = codes2(v[0], v[1], inv) | codes2(v[2], v[3], inv) << 16;
+  for (int u = 0; u < UNROLL; ++u) {
+    const ll i = first + 256 * u;
+    raw[u] = i < chunks ? __ldcs(reinterpret_cast<const uint4*>(x) + i) : make_uint4(0u, 0u, 0u, 0u);
   }
-  if (i % PER == 0) scales[i / PER] = static_cast<uint8_t>(e);
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const ll i = first + 256 * u;
+    float v[C::N];
+    C::get(raw[u], v);
+    uint32_t top = 0u;
+#pragma unroll
+    for (int k = 0; k < C::N; ++k) top = max(top, size_bits(v[k]));
+#pragma unroll
+    for (int o = PER / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t e = scale_exponent(top);
+    const float inv = inverse_scale(e);
+    if (i >= chunks) continue;
+    if constexpr (C::N == 8) {
+      reinterpret_cast<uint2*>(codes)[i] = make_uint2(codes2(v[0], v[1], inv) | codes2(v[2], v[3], inv) << 16,
+                                                      codes2(v[4], v[5], inv) | codes2(v[6], v[7], inv) << 16);
+    } else {
+      reinterpret_cast<uint32_t*>(codes)[i] = codes2(v[0], v[1], inv) | codes2(v[2], v[3], inv) << 16;
+    }
+    if (i % PER == 0) scales[i / PER] = static_cast<uint8_t>(e);
+  }
 }
 
 __device__ __forceinline__ float as_float(float v) { return v; }
@@ -125,25 +138,37 @@ __global__ void __launch_bounds__(256) unpack8_kernel(ll chunks, const uint8_t* 
                                                       const uint8_t* __restrict__ scales, T* __restrict__ x) {
   using C = Chunk<T>;
   constexpr int PER = kPackBlock / C::N;
-  const ll i = static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= chunks) return;
-  const float s = scale_value(scales[i / PER]);
-  uint32_t w[C::N / 4];
-  if constexpr (C::N == 8) {
-    const uint2 c = reinterpret_cast<const uint2*>(codes)[i];
-    w[0] = c.x;
-    w[1] = c.y;
-  } else {
-    w[0] = reinterpret_cast<const uint32_t*>(codes)[i];
-  }
-  float v[C::N];
+  constexpr int W = C::N / 4;
+  const ll first = static_cast<ll>(blockIdx.x) * (256 * UNROLL) + threadIdx.x;
+  uint32_t w[UNROLL][W];
+  uint8_t e[UNROLL];
 #pragma unroll
-  for (int k = 0; k < C::N / 2; ++k) {
-    const float2 f = e4m3x2_to_float2(static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1))));
-    v[2 * k] = f.x * s;
-    v[2 * k + 1] = f.y * s;
+  for (int u = 0; u < UNROLL; ++u) {
+    const ll i = first + 256 * u;
+    if (i >= chunks) continue;
+    e[u] = scales[i / PER];
+    if constexpr (W == 2) {
+      const uint2 c = __ldcs(reinterpret_cast<const uint2*>(codes) + i);
+      w[u][0] = c.x;
+      w[u][W - 1] = c.y;
+    } else {
+      w[u][0] = __ldcs(reinterpret_cast<const uint32_t*>(codes) + i);
+    }
   }
-  reinterpret_cast<uint4*>(x)[i] = C::put(v);
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const ll i = first + 256 * u;
+    if (i >= chunks) continue;
+    const float s = scale_value(e[u]);
+    float v[C::N];
+#pragma unroll
+    for (int k = 0; k < C::N / 2; ++k) {
+      const float2 f = e4m3x2_to_float2(static_cast<uint16_t>(w[u][k / 2] >> (16 * (k & 1))));
+      v[2 * k] = f.x * s;
+      v[2 * k + 1] = f.y * s;
+    }
+    reinterpret_cast<uint4*>(x)[i] = C::put(v);
+  }
 }
 
 template <typename T>
@@ -161,7 +186,7 @@ cudaError_t pack(ll rows, int cols, const T* x, uint8_t* codes, uint8_t* scales,
   const int blocks = (cols + kPackBlock - 1) / kPackBlock;
   if (cols % kPackBlock == 0 && aligned(x, 16) && aligned(codes, 8)) {
     const ll chunks = rows * cols / Chunk<T>::N;
-    pack8_kernel<T><<<static_cast<unsigned>((chunks + 255) / 256), 256, 0, st>>>(chunks, x, codes, scales);
+    pack8_kernel<T><<<static_cast<unsigned>((chunks + 256 * UNROLL - 1) / (256 * UNROLL)), 256, 0, st>>>(chunks, x, codes, scales);
   } else {
     pack8_any_kernel<T><<<static_cast<unsigned>((rows * blocks + 7) / 8), 256, 0, st>>>(rows, cols, blocks, x, codes,
                                                                                        scales);
@@ -173,7 +198,7 @@ template <typename T>
 cudaError_t unpack(ll rows, int cols, const Packed& p, T* x, cudaStream_t st) {
   if (cols % kPackBlock == 0 && aligned(x, 16) && aligned(p.codes, 8)) {
     const ll chunks = rows * cols / Chunk<T>::N;
-    unpack8_kernel<T><<<static_cast<unsigned>((chunks + 255) / 256), 256, 0, st>>>(chunks, p.codes, p.scales, x);
+    unpack8_kernel<T><<<static_cast<unsigned>((chunks + 256 * UNROLL - 1) / (256 * UNROLL)), 256, 0, st>>>(chunks, p.codes, p.scales, x);
   } else {
     unpack8_any_kernel<T><<<static_cast<unsigned>((rows * cols + 255) / 256), 256, 0, st>>>(rows, cols, p, x);
   }

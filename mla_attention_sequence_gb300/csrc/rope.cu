@@ -12,6 +12,7 @@
 // memory, and all heads of the token use them.
 #include "rope.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace laga {
@@ -108,14 +109,33 @@ struct Vec<float> {
   }
 };
 
+// Exact division of 0 <= e < 2^26 by a fixed 1 <= d < 2^17.
+struct Div {
+  uint64_t mul;
+  int shift;
+  uint32_t d;
+};
+Div make_div(uint32_t d) {
+  int bits = 0;
+  while ((1u << bits) < d) ++bits;
+  const int shift = 26 + bits;
+  return Div{((uint64_t{1} << shift) + d - 1) / d, shift, d};
+}
+__device__ __forceinline__ int div_by(const Div& v, int e) {
+  return static_cast<int>((static_cast<uint64_t>(e) * v.mul) >> v.shift);
+}
+
 // 16-byte units: rows and their RoPE part aligned to 16 bytes. A unit is a chunk of the
 // no-RoPE part, an interleaved chunk, or a chunk of the first half with its partner in the
-// second (the halves a multiple of the chunk).
+// second (the halves a multiple of the chunk). A thread loads UNROLL units before it works on
+// the first: with one at a time 128 heads of 2048 tokens took 60 us, half the copy's rate.
 template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(THREADS) rope_vec_kernel(const RopeArgs a, const RopeTable t, int per_cta) {
+__global__ void __launch_bounds__(THREADS) rope_vec_kernel(const RopeArgs a, const RopeTable t, int per_cta,
+                                                           const Div per_head) {
   extern __shared__ float2 cs[];
   using V = Vec<T>;
   constexpr int N = V::N;
+  constexpr int UNROLL = INTERLEAVED ? 4 : 2;
   const ll first = static_cast<ll>(blockIdx.x) * per_cta;
   const int tokens = static_cast<int>(min(static_cast<ll>(per_cta), a.tokens - first));
   const int n = a.d_rope / 2, heads = a.q ? a.n_h : 0;
@@ -123,58 +143,72 @@ __global__ void __launch_bounds__(THREADS) rope_vec_kernel(const RopeArgs a, con
   __syncthreads();
   const int rope_units = INTERLEAVED ? a.d_rope / N : n / N;
   const int copy = a.q_out != a.q ? a.d_nope / N : 0;
-  const int per_head = copy + rope_units;
-  const int q_units = heads * per_head, units = q_units + (a.k ? rope_units : 0);
-  const int q_row = (a.d_nope + a.d_rope) / N;  // chunks
+  const int q_units = heads * static_cast<int>(per_head.d), units = q_units + (a.k ? rope_units : 0);
+  const int q_row = (a.d_nope + a.d_rope) / N, half = n / N;  // chunks
   for (int k = 0; k < tokens; ++k) {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q)) + (first + k) * a.n_h * q_row;
     uint4* q_out = reinterpret_cast<uint4*>(static_cast<T*>(a.q_out)) + (first + k) * a.n_h * q_row;
+    const uint4* kr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.k)) + (first + k) * (a.d_rope / N);
+    uint4* k_out = reinterpret_cast<uint4*>(static_cast<T*>(a.k_out)) + (first + k) * (a.d_rope / N);
     const float2* c = cs + k * n;
-    for (int e = threadIdx.x; e < units; e += THREADS) {
-      const uint4* src;
-      uint4* dst;
-      int u;
-      if (e < q_units) {
-        const int h = e / per_head;
-        u = e - h * per_head;
-        src = q + h * q_row;
-        dst = q_out + h * q_row;
-        if (u < copy) {
-          dst[u] = src[u];
+    for (int e0 = threadIdx.x; e0 < units; e0 += THREADS * UNROLL) {
+      uint4 x[UNROLL], y[UNROLL];
+      uint4* dst[UNROLL];
+      int unit[UNROLL];  // < 0: a copy
+#pragma unroll
+      for (int j = 0; j < UNROLL; ++j) {
+        const int e = e0 + THREADS * j;
+        dst[j] = nullptr;
+        if (e >= units) continue;
+        const uint4* src;
+        if (e < q_units) {
+          const int h = div_by(per_head, e);
+          int u = e - h * static_cast<int>(per_head.d);
+          const bool rotated = u >= copy;
+          if (rotated) u += a.d_nope / N - copy;
+          src = q + h * q_row + u;
+          dst[j] = q_out + h * q_row + u;
+          unit[j] = rotated ? u - a.d_nope / N : -1;
+        } else {
+          unit[j] = e - q_units;
+          src = kr + unit[j];
+          dst[j] = k_out + unit[j];
+        }
+        x[j] = __ldcs(src);
+        if (!INTERLEAVED && unit[j] >= 0) y[j] = __ldcs(src + half);
+      }
+#pragma unroll
+      for (int j = 0; j < UNROLL; ++j) {
+        if (!dst[j]) continue;
+        if (unit[j] < 0) {
+          *dst[j] = x[j];
           continue;
         }
-        u -= copy;
-        src += a.d_nope / N;
-        dst += a.d_nope / N;
-      } else {
-        u = e - q_units;
-        src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.k)) + (first + k) * (a.d_rope / N);
-        dst = reinterpret_cast<uint4*>(static_cast<T*>(a.k_out)) + (first + k) * (a.d_rope / N);
-      }
-      if constexpr (INTERLEAVED) {
-        float x[N];
-        V::get(src[u], x);
+        if constexpr (INTERLEAVED) {
+          const float2* w = c + unit[j] * (N / 2);
+          float v[N];
+          V::get(x[j], v);
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          const float2 w = c[u * (N / 2) + i];
-          const float p = x[2 * i], q2 = x[2 * i + 1];
-          x[2 * i] = p * w.x - q2 * w.y;
-          x[2 * i + 1] = p * w.y + q2 * w.x;
-        }
-        dst[u] = V::put(x);
-      } else {
-        float x[N], y[N];
-        V::get(src[u], x);
-        V::get(src[u + n / N], y);
+          for (int i = 0; i < N / 2; ++i) {
+            const float p = v[2 * i], r = v[2 * i + 1];
+            v[2 * i] = p * w[i].x - r * w[i].y;
+            v[2 * i + 1] = p * w[i].y + r * w[i].x;
+          }
+          *dst[j] = V::put(v);
+        } else {
+          const float2* w = c + unit[j] * N;
+          float v[N], z[N];
+          V::get(x[j], v);
+          V::get(y[j], z);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float2 w = c[u * N + i];
-          const float p = x[i], q2 = y[i];
-          x[i] = p * w.x - q2 * w.y;
-          y[i] = p * w.y + q2 * w.x;
+          for (int i = 0; i < N; ++i) {
+            const float p = v[i], r = z[i];
+            v[i] = p * w[i].x - r * w[i].y;
+            z[i] = p * w[i].y + r * w[i].x;
+          }
+          *dst[j] = V::put(v);
+          dst[j][half] = V::put(z);
         }
-        dst[u] = V::put(x);
-        dst[u + n / N] = V::put(y);
       }
     }
   }
@@ -197,12 +231,14 @@ cudaError_t launch(const RopeArgs& a, const RopeTable& t, cudaStream_t st) {
   if (per < 1) per = 1;
   const unsigned grid = static_cast<unsigned>((a.tokens + per - 1) / per);
   const size_t smem = static_cast<size_t>(per) * n * sizeof(float2);
+  const int copy = a.q_out != a.q ? a.d_nope / N : 0;
+  const Div head = make_div(static_cast<uint32_t>(std::max(1, copy + (a.interleaved ? a.d_rope : n) / N)));
   if (!vec)
     rope_any_kernel<T><<<grid, THREADS, smem, st>>>(a, t, static_cast<int>(per));
   else if (a.interleaved)
-    rope_vec_kernel<T, true><<<grid, THREADS, smem, st>>>(a, t, static_cast<int>(per));
+    rope_vec_kernel<T, true><<<grid, THREADS, smem, st>>>(a, t, static_cast<int>(per), head);
   else
-    rope_vec_kernel<T, false><<<grid, THREADS, smem, st>>>(a, t, static_cast<int>(per));
+    rope_vec_kernel<T, false><<<grid, THREADS, smem, st>>>(a, t, static_cast<int>(per), head);
   return cudaGetLastError();
 }
 

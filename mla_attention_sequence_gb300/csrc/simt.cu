@@ -4,10 +4,8 @@
 // reconstruction contractions and one CTA per query row (forward, dq) or per
 // latent row (dK, dV) for attention.
 #include "internal.h"
-#include "mask.h"
 
 #include <cmath>
-#include <type_traits>
 
 namespace laga {
 namespace {
@@ -324,20 +322,6 @@ LaunchResult fwd_t(const Dims& d, const T* q, const T* c_kv, const T* k_rope, co
 }
 
 template <typename T>
-cudaError_t rebuild_bwd(const Dims& d, const T* c_kv, const T* W_UK, const T* W_UV, const float* dkn, const float* dv,
-                        T* dc_kv, T* dW_UK, T* dW_UV, cudaStream_t st) {
-  const int M = d.B * d.S;
-  const ll nk = static_cast<ll>(d.n_h) * d.d_nope, nv = static_cast<ll>(d.n_h) * d.d_v;
-  // dc_kv = dK_nope W_UK^T + dV W_UV^T
-  cudaError_t e = gemm<float, T, T>(st, M, d.d_c, static_cast<int>(nk), dkn, nk, 1, W_UK, 1, nk, dc_kv, d.d_c, 1,
-                                    static_cast<int>(nv), dv, nv, 1, W_UV, 1, nv);
-  // dW = c_kv^T dK (sum over the batch folds into the reduction over B*S rows)
-  if (e == cudaSuccess) e = gemm<T, float, T>(st, d.d_c, static_cast<int>(nk), M, c_kv, 1, d.d_c, dkn, nk, 1, dW_UK, nk, 1);
-  if (e == cudaSuccess) e = gemm<T, float, T>(st, d.d_c, static_cast<int>(nv), M, c_kv, 1, d.d_c, dv, nv, 1, dW_UV, nv, 1);
-  return e;
-}
-
-template <typename T>
 LaunchResult bwd_t(const Dims& d, const T* q, const T* c_kv, const T* k_rope, const T* W_UK, const T* W_UV,
                    const T* out, const float* lse, const T* dout, T* dq, T* dc_kv, T* dk_rope, T* dW_UK, T* dW_UV,
                    void* ws, bool reuse_kv, cudaStream_t st) {
@@ -371,7 +355,16 @@ LaunchResult bwd_t(const Dims& d, const T* q, const T* c_kv, const T* k_rope, co
     r.what = "simt attention backward";
     return r;
   }
-  r.err = rebuild_bwd<T>(d, c_kv, W_UK, W_UV, w.dkn, w.dv, dc_kv, dW_UK, dW_UV, st);
+  const int M = d.B * d.S;
+  const ll nk = static_cast<ll>(d.n_h) * d.d_nope, nv = static_cast<ll>(d.n_h) * d.d_v;
+  // dc_kv = dK_nope W_UK^T + dV W_UV^T
+  r.err = gemm<float, T, T>(st, M, d.d_c, static_cast<int>(nk), w.dkn, nk, 1, W_UK, 1, nk, dc_kv, d.d_c, 1,
+                            static_cast<int>(nv), w.dv, nv, 1, W_UV, 1, nv);
+  // dW = c_kv^T dK (sum over the batch folds into the reduction over B*S rows)
+  if (r.err == cudaSuccess)
+    r.err = gemm<T, float, T>(st, d.d_c, static_cast<int>(nk), M, c_kv, 1, d.d_c, w.dkn, nk, 1, dW_UK, nk, 1);
+  if (r.err == cudaSuccess)
+    r.err = gemm<T, float, T>(st, d.d_c, static_cast<int>(nv), M, c_kv, 1, d.d_c, w.dv, nv, 1, dW_UV, nv, 1);
   if (r.err != cudaSuccess) r.what = "simt reconstruction backward";
   return r;
 }
@@ -380,23 +373,6 @@ LaunchResult bwd_t(const Dims& d, const T* q, const T* c_kv, const T* k_rope, co
 
 size_t simt_fwd_workspace(const Dims& d) { return ws_bytes(d, false); }
 size_t simt_bwd_workspace(const Dims& d) { return ws_bytes(d, true); }
-
-LaunchResult simt_rebuild_bwd(const Dims& d, bool is_bf16, const void* c_kv, const void* W_UK, const void* W_UV,
-                              const float* dkn, const float* dv, void* dc_kv, void* dW_UK, void* dW_UV,
-                              cudaStream_t st) {
-  LaunchResult r;
-  auto call = [&](auto* type) {
-    using T = std::remove_pointer_t<decltype(type)>;
-    r.err = rebuild_bwd<T>(d, static_cast<const T*>(c_kv), static_cast<const T*>(W_UK), static_cast<const T*>(W_UV), dkn,
-                           dv, static_cast<T*>(dc_kv), static_cast<T*>(dW_UK), static_cast<T*>(dW_UV), st);
-  };
-  if (is_bf16)
-    call(static_cast<bf16*>(nullptr));
-  else
-    call(static_cast<float*>(nullptr));
-  if (r.err != cudaSuccess) r.what = "reconstruction backward";
-  return r;
-}
 
 LaunchResult simt_reconstruct(const Dims& d, bool is_bf16, const void* c_kv, const void* W_UK, const void* W_UV,
                               void* k_nope, void* v, bool out_f32, cudaStream_t st) {

@@ -8,6 +8,7 @@ path: calling with CPU tensors, or without the built library, raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -148,10 +149,9 @@ def _stream(device) -> int:
 
 
 def problem_of(q, c_kv, k_rope, W_UK, W_UV, q_offset: int, causal: bool, q_split: int = 0,
-               q_offset2: int = 0, q_stand_in: bool = False) -> Problem:
+               q_offset2: int = 0) -> Problem:
     """Infer and check the problem sizes from the input tensors. q_split > 0 makes
-    rows [q_split, Sq) a second query segment starting at position q_offset2. q_stand_in:
-    q only has q's shape, type and device, and no memory that is read."""
+    rows [q_split, Sq) a second query segment starting at position q_offset2."""
     if q.dim() != 4 or c_kv.dim() != 3 or k_rope.dim() != 3 or W_UK.dim() != 2 or W_UV.dim() != 2:
         raise ValueError("expected q [B,Sq,n_h,d_qk], c_kv [B,S,d_c], k_rope [B,S,d_rope], W [d_c, n_h*d]")
     B, Sq, n_h, d_qk = q.shape
@@ -172,7 +172,7 @@ def problem_of(q, c_kv, k_rope, W_UK, W_UV, q_offset: int, causal: bool, q_split
             raise TypeError("all inputs must share one dtype")
         if not t.is_cuda:
             raise RuntimeError("LAGA MLA runs on CUDA tensors only")
-        if not t.is_contiguous() and not (q_stand_in and t is q):
+        if not t.is_contiguous():
             raise ValueError("inputs must be contiguous")
     return Problem(B=B, Sq=Sq, S=S, n_h=n_h, d_c=d_c, d_nope=d_nope, d_rope=d_rope, d_v=d_v,
                    q_offset=int(q_offset), causal=bool(causal), dtype=dt, q_split=int(q_split),
@@ -313,30 +313,51 @@ def reconstruct(c_kv, W_UK, W_UV, n_h: int, variant: str = "auto"):
 # ---------------------------------------------------------------- packed documents
 #
 # Every call below runs on the current stream of its tensors' device and makes that device
-# current for its launches; all tensors of a call are on one device.
+# current for its launches; all tensors of a call are on one device. The host's share of a
+# small call is most of its time, so what depends on sizes alone is worked out once per sizes.
 
 _TORCH_DTYPES = {torch.float32: "f32", torch.bfloat16: "bf16"}
+_DTYPE_CODES = {torch.float32: 0, torch.bfloat16: 1}
+_INT32, _FP32, _UINT8 = (torch.int32,), (torch.float32,), (torch.uint8,)
 
 
-def _dtype_of(t: torch.Tensor) -> str:
-    if t.dtype not in _TORCH_DTYPES:
+def _code_of(dtype: torch.dtype) -> int:
+    if dtype not in _DTYPE_CODES:
         raise TypeError("tensors must be float32 or bfloat16")
-    return _TORCH_DTYPES[t.dtype]
+    return _DTYPE_CODES[dtype]
 
 
-def _expect(name: str, t: torch.Tensor, shape, dtypes, device) -> torch.Tensor:
-    """A contiguous CUDA tensor of that shape, type and device, or an error that names it."""
+def _expect(name: str, t: torch.Tensor, shape, dtypes, device) -> int:
+    """The address of a contiguous CUDA tensor of that shape, type and device; an error that names it
+    otherwise."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise RuntimeError(f"{name}: LAGA MLA runs on CUDA tensors only")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    return t.data_ptr()
+
+
+# The current stream's handle without the Stream object around it (2 us of a small call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(device, fn, *args):
+    """fn(*args, stream) with `device` current, on its current stream."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(index))
+    if status != LAGA_OK:
+        _raise_if(status)
 
 
 def key_bounds(doc_starts, n_rows: int, q_offset: int = 0, prefix=None, window: int = 0, skv: int | None = None,
@@ -348,19 +369,17 @@ def key_bounds(doc_starts, n_rows: int, q_offset: int = 0, prefix=None, window: 
     the last `window` of them (0: all), and, with prefix (int32 [B, n_docs]), all of the
     document's first prefix[k] keys (call the attention with causal=False then). Rows in no
     document see nothing. skv clamps the bounds (None: only the documents do)."""
-    if doc_starts.dim() != 2 or doc_starts.shape[1] < 2:
+    shape = doc_starts.shape
+    if len(shape) != 2 or shape[1] < 2:
         raise ValueError("doc_starts must be [B, n_docs + 1]")
-    B, n_docs = doc_starts.shape[0], doc_starts.shape[1] - 1
+    B, n_docs = shape[0], shape[1] - 1
     dev = doc_starts.device
-    _expect("doc_starts", doc_starts, (B, n_docs + 1), (torch.int32,), dev)
-    if prefix is not None:
-        _expect("prefix", prefix, (B, n_docs), (torch.int32,), dev)
+    starts = _expect("doc_starts", doc_starts, shape, _INT32, dev)
+    pre = None if prefix is None else _expect("prefix", prefix, (B, n_docs), _INT32, dev)
     lo = torch.empty((B, n_rows), dtype=torch.int32, device=dev)
-    hi = torch.empty_like(lo)
-    with torch.cuda.device(dev):
-        _raise_if(lib().laga_mla_key_bounds(B, n_rows, (1 << 30) - 1 if skv is None else int(skv), int(q_offset),
-                                            int(q_split), int(q_offset2), _ptr(doc_starts), n_docs, _ptr(prefix),
-                                            int(window), _ptr(lo), _ptr(hi), _stream(dev)))
+    hi = torch.empty((B, n_rows), dtype=torch.int32, device=dev)
+    _launch(dev, lib().laga_mla_key_bounds, B, n_rows, (1 << 30) - 1 if skv is None else int(skv), int(q_offset),
+            int(q_split), int(q_offset2), starts, n_docs, pre, int(window), lo.data_ptr(), hi.data_ptr())
     return lo, hi
 
 
@@ -381,43 +400,57 @@ class Packed8:
         return self.codes.device
 
 
+def _scales_shape(shape):
+    return (*shape[:-1], (shape[-1] + 31) // 32)
+
+
 def _check_packed(name: str, p: Packed8):
-    if p.dtype not in _TORCH_DTYPES:
+    """(address of the codes, address of the scales)."""
+    if p.dtype not in _DTYPE_CODES:
         raise TypeError(f"{name}: a checkpoint restores to float32 or bfloat16")
-    _expect(name + ".codes", p.codes, p.codes.shape, (torch.uint8,), p.codes.device)
-    if p.codes.dim() < 1:
+    shape, dev = p.codes.shape, p.codes.device
+    if not shape:
         raise ValueError(f"{name}: a checkpoint has at least one dimension")
-    _expect(name + ".scales", p.scales, (*p.codes.shape[:-1], -(-p.codes.shape[-1] // 32)), (torch.uint8,),
-            p.codes.device)
+    return (_expect(name + ".codes", p.codes, shape, _UINT8, dev),
+            _expect(name + ".scales", p.scales, _scales_shape(shape), _UINT8, dev))
 
 
 def pack8(x: torch.Tensor) -> Packed8:
     """laga_mla_pack8: saves a float32 or bfloat16 tensor in 8 bits along its last dimension."""
-    dt = _dtype_of(x)
-    if x.dim() < 1:
+    dt, shape, dev = x.dtype, x.shape, x.device
+    code = _code_of(dt)
+    if not shape:
         raise ValueError("pack8 needs at least one dimension")
-    _expect("x", x, x.shape, (x.dtype,), x.device)
-    codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-    scales = torch.empty((*x.shape[:-1], -(-x.shape[-1] // 32)), dtype=torch.uint8, device=x.device)
-    if x.numel():
-        with torch.cuda.device(x.device):
-            _raise_if(lib().laga_mla_pack8(DTYPES[dt], x.numel() // x.shape[-1], x.shape[-1], _ptr(x), _ptr(codes),
-                                           _ptr(scales), _stream(x.device)))
-    return Packed8(codes, scales, x.dtype)
+    src = _expect("x", x, shape, (dt,), dev)
+    codes = torch.empty(shape, dtype=torch.uint8, device=dev)
+    scales = torch.empty(_scales_shape(shape), dtype=torch.uint8, device=dev)
+    n, cols = x.numel(), shape[-1]
+    if n:
+        _launch(dev, lib().laga_mla_pack8, code, n // cols, cols, src, codes.data_ptr(), scales.data_ptr())
+    return Packed8(codes, scales, dt)
 
 
 def unpack8(p: Packed8, out: torch.Tensor | None = None) -> torch.Tensor:
     """laga_mla_unpack8: the tensor a checkpoint stands for, in its own type."""
-    _check_packed("p", p)
+    codes, scales = _check_packed("p", p)
+    shape, dev = p.codes.shape, p.codes.device
     if out is None:
-        out = torch.empty(p.shape, dtype=p.dtype, device=p.device)
+        out = torch.empty(shape, dtype=p.dtype, device=dev)
     else:
-        _expect("out", out, p.shape, (p.dtype,), p.device)
-    if out.numel():
-        with torch.cuda.device(p.device):
-            _raise_if(lib().laga_mla_unpack8(DTYPES[_TORCH_DTYPES[p.dtype]], out.numel() // p.shape[-1], p.shape[-1],
-                                             _ptr(p.codes), _ptr(p.scales), _ptr(out), _stream(p.device)))
+        _expect("out", out, shape, (p.dtype,), dev)
+    n, cols = out.numel(), shape[-1]
+    if n:
+        _launch(dev, lib().laga_mla_unpack8, _DTYPE_CODES[p.dtype], n // cols, cols, codes, scales, out.data_ptr())
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_desc(q_shape, d_rope, sections, theta, interleaved, inverse, pos64, code):
+    B, S, n_h, d_qk = q_shape
+    if d_rope > d_qk:
+        raise ValueError("q's last dim must be d_nope + d_rope")
+    return LagaRopeDesc(B * S, n_h, d_qk - d_rope, d_rope, len(sections),
+                        (ctypes.c_int64 * ROPE_MAX_AXES)(*sections), theta, interleaved, inverse, pos64, code)
 
 
 def rope(q, k_rope, pos, sections=None, theta: float = 10000.0, interleaved: bool = True, inverse: bool = False,
@@ -427,43 +460,102 @@ def rope(q, k_rope, pos, sections=None, theta: float = 10000.0, interleaved: boo
     rotated. sections: pairs per axis (None: one axis with all). The outputs are new tensors,
     or q_out / k_out, which may be q / k_rope themselves (in place). inverse=True rotates back:
     pass the gradients of the rotated tensors to get those of q and k_rope."""
-    if k_rope.dim() != 3 or pos.dim() != 3 or q.dim() != 4:
+    shape, dt, dev = q.shape, q.dtype, q.device
+    if len(shape) != 4 or k_rope.dim() != 3 or pos.dim() != 3:
         raise ValueError("expected q [B,S,n_h,d_nope+d_rope], k_rope [B,S,d_rope], pos [n_axes,B,S]")
-    B, S, n_h, d_qk = q.shape
-    d_rope, dev = k_rope.shape[2], k_rope.device
-    dt = _dtype_of(q)
-    _expect("q", q, q.shape, (q.dtype,), dev)
-    _expect("k_rope", k_rope, (B, S, d_rope), (q.dtype,), dev)
-    _expect("pos", pos, (pos.shape[0], B, S), (torch.int32, torch.int64), dev)
-    if d_rope > d_qk:
-        raise ValueError("q's last dim must be d_nope + d_rope")
-    sections = [d_rope // 2] if sections is None else [int(s) for s in sections]
-    if len(sections) != pos.shape[0] or len(sections) > ROPE_MAX_AXES:
+    d_rope, axes = k_rope.shape[2], pos.shape[0]
+    code = _code_of(dt)
+    k_shape = (shape[0], shape[1], d_rope)
+    src = _expect("q", q, shape, (dt,), dev)
+    k_src = _expect("k_rope", k_rope, k_shape, (dt,), dev)
+    at = _expect("pos", pos, (axes, shape[0], shape[1]), (torch.int32, torch.int64), dev)
+    sections = (d_rope // 2,) if sections is None else tuple(map(int, sections))
+    if len(sections) != axes or axes > ROPE_MAX_AXES:
         raise ValueError(f"one section per axis of pos, at most {ROPE_MAX_AXES}")
-    q_out = torch.empty_like(q) if q_out is None else _expect("q_out", q_out, q.shape, (q.dtype,), dev)
-    k_out = torch.empty_like(k_rope) if k_out is None else _expect("k_out", k_out, k_rope.shape, (q.dtype,), dev)
-    d = LagaRopeDesc(B * S, n_h, d_qk - d_rope, d_rope, len(sections),
-                     (ctypes.c_int64 * ROPE_MAX_AXES)(*sections), float(theta), int(bool(interleaved)),
-                     int(bool(inverse)), int(pos.dtype == torch.int64), DTYPES[dt])
-    with torch.cuda.device(dev):
-        _raise_if(lib().laga_mla_rope(ctypes.byref(d), _ptr(pos), _ptr(q), _ptr(k_rope), _ptr(q_out), _ptr(k_out),
-                                      _stream(dev)))
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=dt, device=dev)
+    if k_out is None:
+        k_out = torch.empty(k_shape, dtype=dt, device=dev)
+    d = _rope_desc(shape, d_rope, sections, float(theta), bool(interleaved), bool(inverse), pos.dtype == torch.int64,
+                   code)
+    _launch(dev, lib().laga_mla_rope, d, at, src, k_src, _expect("q_out", q_out, shape, (dt,), dev),
+            _expect("k_out", k_out, k_shape, (dt,), dev))
     return q_out, k_out
 
 
-def _mods(p: Problem, dev, key_lo, key_hi, softcap, slopes) -> LagaMods:
-    for name, t in (("key_lo", key_lo), ("key_hi", key_hi)):
-        if t is not None:
-            _expect(name, t, (p.B, p.Sq), (torch.int32,), dev)
-    if slopes is not None:
-        _expect("slopes", slopes, (p.n_h,), (torch.float32,), dev)
-    return LagaMods(_ptr(key_lo), _ptr(key_hi), _ptr(slopes), float(softcap or 0.0))
+@functools.lru_cache(maxsize=256)
+def _masked_plan(q_shape, c_shape, r_shape, wk_shape, wv_shape, dtype, q_offset, causal, softmax_scale, variant,
+                 q_split, q_offset2):
+    """What a masked call's sizes decide: the Problem, the descriptors without and with the reuse of K and
+    V, the bytes of the forward's and the backward's workspace (0: refused)."""
+    like = [_Sizes(s, dtype) for s in (q_shape, c_shape, r_shape, wk_shape, wv_shape)]
+    p = problem_of(*like, q_offset, causal, q_split, q_offset2)
+    d = make_desc(p, softmax_scale, variant)
+    L = lib()
+    return (p, d, make_desc(p, softmax_scale, variant, FLAG_REUSE_KV), int(L.laga_mla_masked_fwd_workspace_size(d)),
+            int(L.laga_mla_masked_bwd_workspace_size(d)))
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+class _Sizes:
+    """A tensor's shape and type for problem_of, which asks no more of it."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype = shape, dtype
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+
+class _MaskedCall:
+    """The checked arguments that masked_fwd, masked_bwd and masked_workspace share."""
+    __slots__ = ("p", "desc", "reuse", "fwd_bytes", "bwd_bytes", "q", "x", "dev", "dt")
+
+    def __init__(self, q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, softmax_scale, variant, q_split, q_offset2):
+        self.dt, self.dev = c_kv.dtype, c_kv.device
+        if self.dt not in _DTYPE_CODES:
+            raise TypeError("tensors must be float32 or bfloat16")
+        packed = isinstance(q, Packed8)
+        if packed:
+            self.q = LagaPacked(*_check_packed("q", q))
+            if q.dtype != self.dt:
+                raise TypeError("all inputs must share one dtype")
+            if q.device != self.dev:
+                raise ValueError(f"q is on {q.device}, the other tensors on {self.dev}")
+        else:
+            self.q = _expect("q", q, q.shape, (self.dt,), self.dev)
+        self.x = [_expect(n, t, t.shape, (self.dt,), self.dev)
+                  for n, t in (("c_kv", c_kv), ("k_rope", k_rope), ("W_UK", W_UK), ("W_UV", W_UV))]
+        self.p, self.desc, self.reuse, self.fwd_bytes, self.bwd_bytes = _masked_plan(
+            q.shape, c_kv.shape, k_rope.shape, W_UK.shape, W_UV.shape, self.dt, int(q_offset), bool(causal),
+            softmax_scale, variant, int(q_split), int(q_offset2))
+
+    def mods(self, key_lo, key_hi, softcap, slopes) -> LagaMods:
+        p, dev = self.p, self.dev
+        rows = (p.B, p.Sq)
+        return LagaMods(None if key_lo is None else _expect("key_lo", key_lo, rows, _INT32, dev),
+                        None if key_hi is None else _expect("key_hi", key_hi, rows, _INT32, dev),
+                        None if slopes is None else _expect("slopes", slopes, (p.n_h,), _FP32, dev),
+                        softcap or 0.0)
+
+    def workspace(self, nbytes, given):
+        """(the tensor that keeps it alive, its address)."""
+        if given is None:
+            given = torch.empty(nbytes, dtype=torch.uint8, device=self.dev)
+        else:
+            _expect("workspace", given, given.shape, (given.dtype,), self.dev)
+            if given.numel() * given.element_size() < nbytes:
+                raise ValueError("workspace too small")
+        return given, given.data_ptr()
+
+    def output(self, name, t, shape, dtype):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+        _expect(name, t, shape, (dtype,), self.dev)
+        return t
 
 
 def masked_workspace(q, c_kv, k_rope, W_UK, W_UV, key_lo=None, key_hi=None, softcap: float = 0.0, slopes=None,
@@ -471,12 +563,11 @@ def masked_workspace(q, c_kv, k_rope, W_UK, W_UV, key_lo=None, key_hi=None, soft
                      q_split: int = 0, q_offset2: int = 0) -> torch.Tensor:
     """A workspace for masked_fwd and masked_bwd of these arguments; the forward's K and V stay in
     it for a backward with reuse_kv=True."""
-    p = problem_of(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, q_split, q_offset2)
-    d = make_desc(p, softmax_scale, variant)
-    n = int(lib().laga_mla_masked_bwd_workspace_size(ctypes.byref(d)))
-    if n == 0:
-        raise LagaError(2, lib().laga_mla_last_error().decode(errors="replace"))
-    return torch.empty(n, dtype=torch.uint8, device=q.device)
+    c = _MaskedCall(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, softmax_scale, variant, q_split, q_offset2)
+    if c.bwd_bytes == 0:
+        lib().laga_mla_masked_bwd_workspace_size(c.desc)  # the reason, for this thread
+        _raise_if(2)
+    return torch.empty(c.bwd_bytes, dtype=torch.uint8, device=c.dev)
 
 
 def masked_fwd(q, c_kv, k_rope, W_UK, W_UV, key_lo=None, key_hi=None, softcap: float = 0.0, slopes=None,
@@ -487,21 +578,15 @@ def masked_fwd(q, c_kv, k_rope, W_UK, W_UV, key_lo=None, key_hi=None, softcap: f
     causal, j <= its position. softcap > 0: scores become softcap tanh(s / softcap). slopes
     (float32 [n_h]): minus slopes[h] times the distance to the key. A row that sees nothing gets
     out 0 and lse -inf."""
-    p = problem_of(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, q_split, q_offset2)
-    dev = q.device
-    _same_device(dev, c_kv=c_kv, k_rope=k_rope, W_UK=W_UK, W_UV=W_UV, workspace=workspace)
-    m = _mods(p, dev, key_lo, key_hi, softcap, slopes)
-    d = make_desc(p, softmax_scale, variant)
-    L = lib()
-    out = torch.empty((p.B, p.Sq, p.n_h, p.d_v), dtype=q.dtype, device=dev) if out is None else \
-        _expect("out", out, (p.B, p.Sq, p.n_h, p.d_v), (q.dtype,), dev)
-    lse = torch.empty((p.B, p.n_h, p.Sq), dtype=torch.float32, device=dev) if lse is None else \
-        _expect("lse", lse, (p.B, p.n_h, p.Sq), (torch.float32,), dev)
-    nbytes = int(L.laga_mla_masked_fwd_workspace_size(ctypes.byref(d)))
-    ws = _workspace(nbytes, dev, workspace)
-    with torch.cuda.device(dev):
-        _raise_if(L.laga_mla_masked_fwd(ctypes.byref(d), ctypes.byref(m), _ptr(q), _ptr(c_kv), _ptr(k_rope), _ptr(W_UK),
-                                        _ptr(W_UV), _ptr(out), _ptr(lse), _ptr(ws), nbytes, _stream(dev)))
+    if isinstance(q, Packed8):
+        raise ValueError("the forward takes q as a tensor")
+    c = _MaskedCall(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, softmax_scale, variant, q_split, q_offset2)
+    p = c.p
+    m = c.mods(key_lo, key_hi, softcap, slopes)
+    out = c.output("out", out, (p.B, p.Sq, p.n_h, p.d_v), c.dt)
+    lse = c.output("lse", lse, (p.B, p.n_h, p.Sq), torch.float32)
+    ws, at = c.workspace(c.fwd_bytes, workspace)
+    _launch(c.dev, lib().laga_mla_masked_fwd, c.desc, m, c.q, *c.x, out.data_ptr(), lse.data_ptr(), at, c.fwd_bytes)
     return out, lse
 
 
@@ -516,46 +601,32 @@ def masked_bwd(q, c_kv, k_rope, W_UK, W_UV, out, lse, dout, key_lo=None, key_hi=
     packed = isinstance(q, Packed8)
     if packed != isinstance(out, Packed8):
         raise ValueError("q and out come either both as tensors or both as 8-bit checkpoints")
-    if packed:
-        _check_packed("q", q)
-        _check_packed("out", out)
-        if q.dtype != c_kv.dtype or out.dtype != c_kv.dtype:
-            raise TypeError("all inputs must share one dtype")
-        p = problem_of(c_kv.new_empty(1).expand(q.shape), c_kv, k_rope, W_UK, W_UV, q_offset, causal, q_split,
-                       q_offset2, q_stand_in=True)
-    else:
-        p = problem_of(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, q_split, q_offset2)
-    dev, dt = c_kv.device, c_kv.dtype
-    _same_device(dev, q=q, k_rope=k_rope, W_UK=W_UK, W_UV=W_UV, workspace=workspace)
+    c = _MaskedCall(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, softmax_scale, variant, q_split, q_offset2)
+    p, dev, dt = c.p, c.dev, c.dt
     o_shape = (p.B, p.Sq, p.n_h, p.d_v)
     if packed:
-        _expect("out.codes", out.codes, o_shape, (torch.uint8,), dev)
+        out8 = LagaPacked(*_check_packed("out", out))
+        if out.dtype != dt:
+            raise TypeError("all inputs must share one dtype")
+        _expect("out.codes", out.codes, o_shape, _UINT8, dev)
+        tensors = (None, None, c.q, out8)
     else:
-        _expect("out", out, o_shape, (dt,), dev)
-    _expect("lse", lse, (p.B, p.n_h, p.Sq), (torch.float32,), dev)
-    _expect("dout", dout, o_shape, (dt,), dev)
+        tensors = (c.q, _expect("out", out, o_shape, (dt,), dev), None, None)
+    lse_at = _expect("lse", lse, (p.B, p.n_h, p.Sq), _FP32, dev)
+    dout_at = _expect("dout", dout, o_shape, (dt,), dev)
     if reuse_kv and workspace is None:
         raise ValueError("reuse_kv needs the workspace the forward ran with")
-    m = _mods(p, dev, key_lo, key_hi, softcap, slopes)
-    d = make_desc(p, softmax_scale, variant, FLAG_REUSE_KV if reuse_kv else 0)
-    L = lib()
-    shapes = {"dq": (p.B, p.Sq, p.n_h, p.d_qk), "dc_kv": c_kv.shape, "dk_rope": k_rope.shape, "dW_UK": W_UK.shape,
-              "dW_UV": W_UV.shape}
-    if grads is None:
-        grads = {k: torch.empty(s, dtype=dt, device=dev) for k, s in shapes.items()}
-    else:
-        for k, s in shapes.items():
-            _expect(k, grads[k], s, (dt,), dev)
-    q8, out8 = (ctypes.byref(LagaPacked(_ptr(t.codes), _ptr(t.scales))) if packed else None for t in (q, out))
-    nbytes = int(L.laga_mla_masked_bwd_workspace_size(ctypes.byref(d)))
-    ws = _workspace(nbytes, dev, workspace)
-    with torch.cuda.device(dev):
-        _raise_if(L.laga_mla_masked_bwd(ctypes.byref(d), ctypes.byref(m), None if packed else _ptr(q), _ptr(c_kv),
-                                        _ptr(k_rope), _ptr(W_UK), _ptr(W_UV), None if packed else _ptr(out), _ptr(lse),
-                                        _ptr(dout), q8, out8, _ptr(grads["dq"]), _ptr(grads["dc_kv"]),
-                                        _ptr(grads["dk_rope"]), _ptr(grads["dW_UK"]), _ptr(grads["dW_UV"]), _ptr(ws),
-                                        nbytes, _stream(dev)))
-    return grads
+    m = c.mods(key_lo, key_hi, softcap, slopes)
+    given = grads or {}
+    g = {"dq": c.output("dq", given.get("dq"), (p.B, p.Sq, p.n_h, p.d_qk), dt),
+         "dc_kv": c.output("dc_kv", given.get("dc_kv"), c_kv.shape, dt),
+         "dk_rope": c.output("dk_rope", given.get("dk_rope"), k_rope.shape, dt),
+         "dW_UK": c.output("dW_UK", given.get("dW_UK"), W_UK.shape, dt),
+         "dW_UV": c.output("dW_UV", given.get("dW_UV"), W_UV.shape, dt)}
+    ws, at = c.workspace(c.bwd_bytes, workspace)
+    _launch(dev, lib().laga_mla_masked_bwd, c.reuse if reuse_kv else c.desc, m, tensors[0], *c.x, tensors[1], lse_at,
+            dout_at, tensors[2], tensors[3], *(t.data_ptr() for t in g.values()), at, c.bwd_bytes)
+    return g
 
 
 def check(device=None) -> None:
