@@ -375,21 +375,52 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if constexpr (MASKED) {
         partial = !__all_sync(0xffffffffu, lo <= kv_first && hi >= kv_first + 64);
         const unsigned first = static_cast<unsigned>(lo - kv_first), width = static_cast<unsigned>(max(hi - lo, 0));
-        const float dist = pos - static_cast<float>(j * BKV + 64 * half);
+        if (CAP && partial) {
 #pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          const float raw = __uint_as_float(x[k]);
-          float th = 0.f, t2;
-          if constexpr (CAP) {
-            th = tanh_abs(raw * p.mod.u_scale);
-            t2 = fmaf(p.mod.cap_log2, th, -lse2);
+          for (int k = 0; k < 64; ++k)
+            if (static_cast<unsigned>(k) - first >= width) x[k] = 0u;
+        }
+        auto raw = [&](int k) { return f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])); };
+        auto put = [&](int k, F2 v) {
+          const float2 t = parts(v);
+          pr[k] = t.x;
+          pr[k + 1] = t.y;
+        };
+        auto get = [&](int k) { return f2(pr[k], pr[k + 1]); };
+        const F2 neg = f2(-lse2);
+        if constexpr (CAP) {  // x becomes the tanh, kept for dS's factor
+          const F2 us = f2(p.mod.u_scale), c2 = f2(p.mod.cap_log2);
+          if (all_small<64>(x, p.mod.u_scale)) {
+#pragma unroll
+            for (int k = 0; k < 64; k += 2) {
+              const F2 u = mul(raw(k), us);
+              const F2 th = mul(u, tanh_over_u(mul(u, u)));
+              const float2 t = parts(th);
+              x[k] = __float_as_uint(t.x);
+              x[k + 1] = __float_as_uint(t.y);
+              put(k, fma(c2, th, neg));
+            }
           } else {
-            t2 = fmaf(raw, sl2, -lse2);
+#pragma unroll
+            for (int k = 0; k < 64; ++k) {
+              const float th = tanh_abs(__uint_as_float(x[k]) * p.mod.u_scale);
+              x[k] = __float_as_uint(th);
+              pr[k] = fmaf(p.mod.cap_log2, th, -lse2);
+            }
           }
-          if constexpr (BIAS) t2 = fmaf(-slope2, fabsf(dist - static_cast<float>(k)), t2);
-          float e = ex2_approx(t2);
-          if constexpr (CAP) e *= fmaf(-th, th, 1.f);  // d capped / d score
-          pr[k] = e;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) put(k, fma(raw(k), f2(sl2), neg));
+        }
+        if constexpr (BIAS) add_bias<64, -1>(slope2, pos - static_cast<float>(j * BKV + 64 * half), get, put);
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+          pr[k] = ex2_approx(pr[k]);
+          pr[k + 1] = ex2_approx(pr[k + 1]);
+          if constexpr (CAP) {  // d capped / d score = 1 - tanh^2
+            const F2 th = raw(k);
+            put(k, mul(get(k), fma(mul(th, f2(-1.f)), th, f2(1.f))));
+          }
         }
         if (partial) {
 #pragma unroll

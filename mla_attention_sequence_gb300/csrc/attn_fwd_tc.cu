@@ -367,19 +367,42 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
       tmem_wait_ld();
       const int kv0 = (j0 + j) * BKV;
-      if constexpr (CAP || BIAS) {  // raw scores -> exponents
-        const float dist = pos - static_cast<float>(j * BKV);  // to the tile's first key
+      const unsigned first = static_cast<unsigned>(lo - kv0), width = static_cast<unsigned>(max(hi - lo, 0));
+      const bool partial = MASKED && !__all_sync(0xffffffffu, lo <= kv0 && hi >= kv0 + BKV);
+      if (CAP && partial) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) {
-          float t2 = __uint_as_float(x[i]);
-          t2 = CAP ? p.mod.cap_log2 * tanh_abs(t2 * p.mod.u_scale) : t2 * sl2;
-          if constexpr (BIAS) t2 = fmaf(-slope2, fabsf(dist - static_cast<float>(i)), t2);
-          x[i] = __float_as_uint(t2);
+        for (int i = 0; i < 128; ++i)
+          if (static_cast<unsigned>(i) - first >= width) x[i] = 0u;
+      }
+      if constexpr (CAP || BIAS) {  // raw scores -> exponents
+        auto get = [&](int k) { return f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])); };
+        auto put = [&](int k, F2 v) {
+          const float2 t = parts(v);
+          x[k] = __float_as_uint(t.x);
+          x[k + 1] = __float_as_uint(t.y);
+        };
+        if constexpr (CAP) {
+          if (all_small<128>(x, p.mod.u_scale)) {
+            const F2 us = f2(p.mod.u_scale), c2 = f2(p.mod.cap_log2);
+#pragma unroll
+            for (int k = 0; k < 128; k += 2) {
+              const F2 u = mul(get(k), us);
+              put(k, mul(mul(u, c2), tanh_over_u(mul(u, u))));
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              x[k] = __float_as_uint(p.mod.cap_log2 * tanh_abs(__uint_as_float(x[k]) * p.mod.u_scale));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 128; k += 2) put(k, mul(get(k), f2(sl2)));
         }
+        if constexpr (BIAS)  // distance to the tile's first key, falling by one a key
+          add_bias<128, -1>(slope2, pos - static_cast<float>(j * BKV), get, put);
       }
       if constexpr (MASKED) {
-        if (!__all_sync(0xffffffffu, lo <= kv0 && hi >= kv0 + BKV)) {
-          const unsigned first = static_cast<unsigned>(lo - kv0), width = static_cast<unsigned>(max(hi - lo, 0));
+        if (partial) {
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (static_cast<unsigned>(i) - first >= width) x[i] = 0xff800000u;  // -inf

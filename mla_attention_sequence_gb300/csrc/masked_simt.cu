@@ -80,6 +80,30 @@ __device__ __forceinline__ void fill(float4* dst, int pitch, int width, F&& get)
     }
 }
 
+// The same through registers: fetch() issues all of a tile's loads, put() stores them later, so
+// that the next step's tile is on its way while this one is worked on. C: columns per lane.
+template <int ROWS, int C>
+struct Staged {
+  float v[ROWS / 8][C];
+  template <class F>
+  __device__ __forceinline__ void fetch(int width, F&& get) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < ROWS / 8; ++i)
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[i][c] = lane + 32 * c < width ? get(8 * i + warp, lane + 32 * c) : 0.f;
+  }
+  __device__ __forceinline__ void put(float4* dst, int pitch, int width) const {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = (width + 3) & ~3;
+    float* f = reinterpret_cast<float*>(dst);
+#pragma unroll
+    for (int i = 0; i < ROWS / 8; ++i)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (lane + 32 * c < w) f[(8 * i + warp) * pitch * 4 + lane + 32 * c] = v[i][c];
+  }
+};
+
 __device__ __forceinline__ float dot4(float4 a, float4 b, float acc) {
   acc = fmaf(a.x, b.x, acc);
   acc = fmaf(a.y, b.y, acc);
@@ -166,41 +190,69 @@ __device__ __forceinline__ float score_of(const SimtParams& p, float raw, float 
   return s - slope * fabsf(static_cast<float>(pos - key));
 }
 
-template <int ROWS>
-__device__ __forceinline__ void load_k(const SimtParams& p, float4* dst, int pitch, int b, int h, int first) {
-  const Dims& d = p.d;
-  fill<ROWS>(dst, pitch, d.d_qk(), [&](int r, int k) {
+// Element k of row r of a tile that starts at row `first` (0 past the end).
+struct KRows {
+  const SimtParams& p;
+  int b, h, first;
+  __device__ __forceinline__ float operator()(int r, int k) const {
+    const Dims& d = p.d;
     const int j = first + r;
     if (j >= d.S) return 0.f;
     const ll row = static_cast<ll>(b) * d.S + j;
     return k < d.d_nope ? p.kn[(row * d.n_h + h) * d.d_nope + k]
                         : load(p.k_rope, p.rope_bf16, row * d.d_rope + (k - d.d_nope));
-  });
-}
-template <int ROWS>
-__device__ __forceinline__ void load_v(const SimtParams& p, float4* dst, int pitch, int b, int h, int first) {
-  const Dims& d = p.d;
-  fill<ROWS>(dst, pitch, d.d_v, [&](int r, int k) {
+  }
+};
+struct VRows {
+  const SimtParams& p;
+  int b, h, first;
+  __device__ __forceinline__ float operator()(int r, int k) const {
     const int j = first + r;
-    return j < d.S ? p.v[((static_cast<ll>(b) * d.S + j) * d.n_h + h) * d.d_v + k] : 0.f;
-  });
-}
-template <int ROWS>
-__device__ __forceinline__ void load_q(const SimtParams& p, float4* dst, int pitch, int b, int h, int first) {
-  const Dims& d = p.d;
-  fill<ROWS>(dst, pitch, d.d_qk(), [&](int r, int k) {
+    return j < p.d.S ? p.v[((static_cast<ll>(b) * p.d.S + j) * p.d.n_h + h) * p.d.d_v + k] : 0.f;
+  }
+};
+struct QRows {
+  const SimtParams& p;
+  int b, h, first;
+  __device__ __forceinline__ float operator()(int r, int k) const {
     const int i = first + r;
-    return i < d.Sq ? load(p.q, p.q_bf16, ((static_cast<ll>(b) * d.Sq + i) * d.n_h + h) * d.d_qk() + k) : 0.f;
-  });
-}
-template <int ROWS>
-__device__ __forceinline__ void load_do(const SimtParams& p, float4* dst, int pitch, int b, int h, int first) {
-  const Dims& d = p.d;
-  fill<ROWS>(dst, pitch, d.d_v, [&](int r, int k) {
+    return i < p.d.Sq ? load(p.q, p.q_bf16, ((static_cast<ll>(b) * p.d.Sq + i) * p.d.n_h + h) * p.d.d_qk() + k) : 0.f;
+  }
+};
+struct DoRows {
+  const SimtParams& p;
+  int b, h, first;
+  __device__ __forceinline__ float operator()(int r, int k) const {
     const int i = first + r;
-    return i < d.Sq ? p.dout[((static_cast<ll>(b) * d.Sq + i) * d.n_h + h) * d.d_v + k] : 0.f;
-  });
-}
+    return i < p.d.Sq ? p.dout[((static_cast<ll>(b) * p.d.Sq + i) * p.d.n_h + h) * p.d.d_v + k] : 0.f;
+  }
+};
+
+// Two streamed tiles (K and V, or q and dO) of ROWS rows: staged a step ahead where the
+// registers allow (widths up to 128), else loaded in place.
+template <int ROWS, int N>
+struct StreamedPair {
+  static constexpr bool AHEAD = N <= 2;
+  static constexpr int C = AHEAD ? 2 * N : 1;
+  Staged<ROWS, C> x, y;
+  template <class A, class B>
+  __device__ __forceinline__ void ahead(int wx, int wy, A&& a, B&& b) {
+    if constexpr (AHEAD) {
+      x.fetch(wx, a);
+      y.fetch(wy, b);
+    }
+  }
+  template <class A, class B>
+  __device__ __forceinline__ void store(float4* sx, int px, int wx, float4* sy, int py, int wy, A&& a, B&& b) {
+    if constexpr (AHEAD) {
+      x.put(sx, px, wx);
+      y.put(sy, py, wy);
+    } else {
+      fill<ROWS>(sx, px, wx, a);
+      fill<ROWS>(sy, py, wy, b);
+    }
+  }
+};
 
 __device__ __forceinline__ float half_warp_max(float v) {
 #pragma unroll
@@ -225,7 +277,7 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
   const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int i0 = t * ROWS + RI * ty;  // this thread's first row
-  load_q<ROWS>(p, sq, pk, b, h, t * ROWS);
+  fill<ROWS>(sq, pk, d.d_qk(), QRows{p, b, h, t * ROWS});
   int lo[RI], hi[RI];
   bool poisoned[RI];
 #pragma unroll
@@ -246,11 +298,14 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
     for (int c = 0; c < N; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const int2 hull = p.q_hull[static_cast<ll>(b) * (d.sq_pad / 64) + t * ROWS / 64];  // of the 64 rows around
-  for (int j0 = hull.x < hull.y ? hull.x / KFWD * KFWD : 0; j0 < hull.y; j0 += KFWD) {
+  const int j_first = hull.x < hull.y ? hull.x / KFWD * KFWD : 0;
+  StreamedPair<KFWD, N> kv;
+  if (j_first < hull.y) kv.ahead(d.d_qk(), d.d_v, KRows{p, b, h, j_first}, VRows{p, b, h, j_first});
+  for (int j0 = j_first; j0 < hull.y; j0 += KFWD) {
     __syncthreads();
-    load_k<KFWD>(p, sk, pk, b, h, j0);
-    load_v<KFWD>(p, sv, pv, b, h, j0);
+    kv.store(sk, pk, d.d_qk(), sv, pv, d.d_v, KRows{p, b, h, j0}, VRows{p, b, h, j0});
     __syncthreads();
+    if (j0 + KFWD < hull.y) kv.ahead(d.d_qk(), d.d_v, KRows{p, b, h, j0 + KFWD}, VRows{p, b, h, j0 + KFWD});
     float s[RI][4];
     score_tile<RI>(sq, sk, pk, (d.d_qk() + 3) / 4, tx, ty, s);
 #pragma unroll
@@ -324,8 +379,8 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dq(const SimtParams p) {
   const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int i0 = t * ROWS + RI * ty;
-  load_q<ROWS>(p, sq, pk, b, h, t * ROWS);
-  load_do<ROWS>(p, sdo, pv, b, h, t * ROWS);
+  fill<ROWS>(sq, pk, d.d_qk(), QRows{p, b, h, t * ROWS});
+  fill<ROWS>(sdo, pv, d.d_v, DoRows{p, b, h, t * ROWS});
   int lo[RI], hi[RI];
   float L[RI], D[RI];
 #pragma unroll
@@ -345,11 +400,14 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dq(const SimtParams p) {
 #pragma unroll
     for (int c = 0; c < N; ++c) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int2 hull = p.q_hull[static_cast<ll>(b) * (d.sq_pad / 64) + t * ROWS / 64];  // of the 64 rows around
-  for (int j0 = hull.x < hull.y ? hull.x / KBWD * KBWD : 0; j0 < hull.y; j0 += KBWD) {
+  const int j_first = hull.x < hull.y ? hull.x / KBWD * KBWD : 0;
+  StreamedPair<KBWD, N> kv;
+  if (j_first < hull.y) kv.ahead(d.d_qk(), d.d_v, KRows{p, b, h, j_first}, VRows{p, b, h, j_first});
+  for (int j0 = j_first; j0 < hull.y; j0 += KBWD) {
     __syncthreads();
-    load_k<KBWD>(p, sk, pk, b, h, j0);
-    load_v<KBWD>(p, sv, pv, b, h, j0);
+    kv.store(sk, pk, d.d_qk(), sv, pv, d.d_v, KRows{p, b, h, j0}, VRows{p, b, h, j0});
     __syncthreads();
+    if (j0 + KBWD < hull.y) kv.ahead(d.d_qk(), d.d_v, KRows{p, b, h, j0 + KBWD}, VRows{p, b, h, j0 + KBWD});
     float s[RI][2], dp[RI][2];
     score_tile<RI>(sq, sk, pk, (d.d_qk() + 3) / 4, tx, ty, s);
     score_tile<RI>(sdo, sv, pv, (d.d_v + 3) / 4, tx, ty, dp);
@@ -402,8 +460,8 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dkv(const SimtParams p) {
   const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int k0 = t * ROWS + RI * ty;  // this thread's first key
-  load_k<ROWS>(p, sk, pk, b, h, t * ROWS);
-  load_v<ROWS>(p, sv, pv, b, h, t * ROWS);
+  fill<ROWS>(sk, pk, d.d_qk(), KRows{p, b, h, t * ROWS});
+  fill<ROWS>(sv, pv, d.d_v, VRows{p, b, h, t * ROWS});
   const float slope = p.slopes ? p.slopes[h] : 0.f;
   float4 dk[RI][N], dv[RI][N];
 #pragma unroll
@@ -411,13 +469,23 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dkv(const SimtParams p) {
 #pragma unroll
     for (int c = 0; c < N; ++c) dk[i][c] = dv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int nq64 = d.sq_pad / 64;
-  for (int q0 = 0; q0 < d.Sq; q0 += KBWD) {
-    const int2 hull = p.q_hull[static_cast<ll>(b) * nq64 + q0 / 64];
-    if (hull.x >= hull.y || hull.x >= (t + 1) * ROWS || hull.y <= t * ROWS) continue;  // the same for every thread
+  // the next query tile from q0 on that may see these keys (the same for every thread)
+  auto next_tile = [&](int q0) {
+    for (; q0 < d.Sq; q0 += KBWD) {
+      const int2 hull = p.q_hull[static_cast<ll>(b) * nq64 + q0 / 64];
+      if (hull.x < hull.y && hull.x < (t + 1) * ROWS && hull.y > t * ROWS) break;
+    }
+    return q0;
+  };
+  StreamedPair<KBWD, N> qd;
+  int q0 = next_tile(0);
+  if (q0 < d.Sq) qd.ahead(d.d_qk(), d.d_v, QRows{p, b, h, q0}, DoRows{p, b, h, q0});
+  for (int q1; q0 < d.Sq; q0 = q1) {
     __syncthreads();
-    load_q<KBWD>(p, sq, pk, b, h, q0);
-    load_do<KBWD>(p, sdo, pv, b, h, q0);
+    qd.store(sq, pk, d.d_qk(), sdo, pv, d.d_v, QRows{p, b, h, q0}, DoRows{p, b, h, q0});
     __syncthreads();
+    q1 = next_tile(q0 + KBWD);
+    if (q1 < d.Sq) qd.ahead(d.d_qk(), d.d_v, QRows{p, b, h, q1}, DoRows{p, b, h, q1});
     float s[RI][2], dp[RI][2];
     score_tile<RI>(sk, sq, pk, (d.d_qk() + 3) / 4, tx, ty, s);
     score_tile<RI>(sv, sdo, pv, (d.d_v + 3) / 4, tx, ty, dp);
