@@ -118,6 +118,7 @@ struct Params {
   const int2* rows;      // [B][sq_pad] visible interval of each query row
   const int* kt_count;   // [B][skv_pad / 128] query tiles that may see a key tile
   const int* kt_list;    // [B][skv_pad / 128][sq_pad / 64] which
+  const int* seen;       // [B][skv_pad / 128] whether a query tile's walk touches the key tile
   const int* q_bad;      // nonzero: read q and dO from the clean copies
   ModParams mod;
 };
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   // No query tile sees these keys: their gradients are zeros, and only the key-row warps work
   // (with nothing to wait for, the roles could run more than one barrier phase apart).
   const bool unseen = MASKED && n_qt == 0;
+  if (MASKED && p.seen[kt_index] == 0) return;  // nothing reads this tile's gradients either
   auto qtile = [&](int i) {
     if constexpr (MASKED) return kt_list[i];
     return i < n0 ? first0 + i : first1 + (i - n0);
@@ -832,6 +834,7 @@ LaunchResult tc_attn_bwd_dkdv(const Dims& d, const bf16* q, const bf16* k_rope, 
     p.rows = mask->meta.rows;
     p.kt_count = mask->meta.kt_count;
     p.kt_list = mask->meta.kt_list;
+    p.seen = mask->meta.seen;
     p.q_bad = mask->meta.q_bad;
     p.mod = mod_params(d, mask->mods);
     smem = SMEM_BYTES_MASKED;

@@ -25,13 +25,11 @@
 // the step costs the larger of the MMA time and the softmax time rather than a
 // chain of both.
 //
-// Masked instances (MOD >= 0): each query row sees an interval of keys. The CTA walks
-// the 128-key tiles from the lowest key any of its rows sees to the highest; a key tile
-// that every row of a warp sees whole takes no compares. The cap and the distance bias
-// turn the raw scores into exponents before the row maximum is taken.
+// The masked instance: each query row sees an interval of keys. The CTA walks the 128-key
+// tiles from the lowest key any of its rows sees to the highest; a key tile that every row of
+// a warp sees whole takes no compares.
 #include "internal.h"
 #include "ptx.cuh"
-#include "score_mod.cuh"
 
 LAGA_TRACE_DEFINE(fwd)
 
@@ -70,10 +68,9 @@ struct FwdParams {
   int q_split, q_offset2;  // second query segment (q_split = 0: none)
   float scale_log2;  // softmax scale * log2(e), > 0
   float* lse;
-  // masked instances
+  // the masked instance
   const int2* rows;     // [B][sq_pad] visible interval of each query row
-  const int2* q_tiles;  // [B][n_q_tiles] {first key tile, key tiles}
-  ModParams mod;
+  const int4* work;     // [B][n_q_tiles] {query tile, first key tile, key tiles}, longest first
 };
 
 // Absolute position of local query row i (a query tile never straddles the
@@ -87,7 +84,7 @@ __device__ __forceinline__ int n_kv_tiles(const FwdParams& p, int t) {
   return last / BKV + 1;
 }
 
-template <int MOD>
+template <bool MASKED>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                     const __grid_constant__ CUtensorMap mR, const __grid_constant__ CUtensorMap mV,
@@ -117,16 +114,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   // Heaviest query tiles (most key tiles) first.
-  const int t = p.n_q_tiles - 1 - static_cast<int>(blockIdx.x);
+  int t = p.n_q_tiles - 1 - static_cast<int>(blockIdx.x);
   const int h = blockIdx.y;
   const int b = blockIdx.z;
-  constexpr bool MASKED = MOD >= 0;
-  constexpr bool CAP = MASKED && (MOD & kModCap) != 0, BIAS = MASKED && (MOD & kModBias) != 0;
   int n_kv, j0 = 0;  // key tiles walked: [j0, j0 + n_kv)
   if constexpr (MASKED) {
-    const int2 span = p.q_tiles[b * p.n_q_tiles + t];
-    j0 = span.x;
-    n_kv = span.y;
+    const int4 w = p.work[b * p.n_q_tiles + blockIdx.x];
+    t = w.x;
+    j0 = w.y;
+    n_kv = w.z;
   } else {
     n_kv = n_kv_tiles(p, t);
   }
@@ -330,16 +326,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const float sl2 = p.scale_log2;
     int lo = 0, hi = 0;     // masked: this row sees keys [lo, hi)
     bool poisoned = false;  // masked: one of them is not finite
-    float slope2 = 0.f, pos = 0.f;
     if constexpr (MASKED) {
       const int2 v = p.rows[static_cast<long long>(b) * (p.n_q_tiles * BQ) + q_row];
       poisoned = v.x < 0;
       lo = v.x & 0x7fffffff;
       hi = v.y;
-      if constexpr (BIAS) {
-        slope2 = p.mod.slopes[h] * LOG2E;
-        pos = static_cast<float>(q_pos(p, q_row) - j0 * BKV);
-      }
     }
     float m_run = -INFINITY;  // running max of the scaled (log2-domain) scores
     float l_run = 0.f;
@@ -367,42 +358,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
       tmem_wait_ld();
       const int kv0 = (j0 + j) * BKV;
-      const unsigned first = static_cast<unsigned>(lo - kv0), width = static_cast<unsigned>(max(hi - lo, 0));
-      const bool partial = MASKED && !__all_sync(0xffffffffu, lo <= kv0 && hi >= kv0 + BKV);
-      if (CAP && partial) {
-#pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (static_cast<unsigned>(i) - first >= width) x[i] = 0u;
-      }
-      if constexpr (CAP || BIAS) {  // raw scores -> exponents
-        auto get = [&](int k) { return f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])); };
-        auto put = [&](int k, F2 v) {
-          const float2 t = parts(v);
-          x[k] = __float_as_uint(t.x);
-          x[k + 1] = __float_as_uint(t.y);
-        };
-        if constexpr (CAP) {
-          if (all_small<128>(x, p.mod.u_scale)) {
-            const F2 us = f2(p.mod.u_scale), c2 = f2(p.mod.cap_log2);
-#pragma unroll
-            for (int k = 0; k < 128; k += 2) {
-              const F2 u = mul(get(k), us);
-              put(k, mul(mul(u, c2), tanh_over_u(mul(u, u))));
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 128; ++k)
-              x[k] = __float_as_uint(p.mod.cap_log2 * tanh_abs(__uint_as_float(x[k]) * p.mod.u_scale));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 128; k += 2) put(k, mul(get(k), f2(sl2)));
-        }
-        if constexpr (BIAS)  // distance to the tile's first key, falling by one a key
-          add_bias<128, -1>(slope2, pos - static_cast<float>(j * BKV), get, put);
-      }
       if constexpr (MASKED) {
-        if (partial) {
+        if (!__all_sync(0xffffffffu, lo <= kv0 && hi >= kv0 + BKV)) {
+          const unsigned first = static_cast<unsigned>(lo - kv0), width = static_cast<unsigned>(max(hi - lo, 0));
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (static_cast<unsigned>(i) - first >= width) x[i] = 0xff800000u;  // -inf
@@ -427,8 +385,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           m4[a] = max3f(m4[a], __uint_as_float(x[i + 2 * a]), __uint_as_float(x[i + 2 * a + 1]));
         }
       }
-      constexpr bool EXPONENTS = CAP || BIAS;  // x holds exponents, not raw scores
-      const float mt = max3f(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * (EXPONENTS ? 1.f : sl2);
+      const float mt = max3f(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * sl2;
       float m_use = m_run;
       float alpha = 1.f;
       bool rescale = false;
@@ -445,9 +402,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       uint32_t pk[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) {
-        const float s0 = __uint_as_float(x[2 * i]), s1 = __uint_as_float(x[2 * i + 1]);
-        const float p0 = ex2_approx(EXPONENTS ? s0 + neg_m : fmaf(s0, sl2, neg_m));
-        const float p1 = ex2_approx(EXPONENTS ? s1 + neg_m : fmaf(s1, sl2, neg_m));
+        const float p0 = ex2_approx(fmaf(__uint_as_float(x[2 * i]), sl2, neg_m));
+        const float p1 = ex2_approx(fmaf(__uint_as_float(x[2 * i + 1]), sl2, neg_m));
         sum2[i & 1] = add_f32x2(sum2[i & 1], make_float2(p0, p1));
         pk[i] = pack_bf16x2(p0, p1);
       }
@@ -603,17 +559,11 @@ LaunchResult tc_attn_fwd(const Dims& d, const bf16* q, const bf16* k_ws, const b
   p.scale_log2 = d.scale * LOG2E;
   p.lse = lse;
   p.status = device_status_ptr();
-  void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, FwdParams) = attn_fwd_kernel<-1>;
+  void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, FwdParams) = attn_fwd_kernel<false>;
   if (mask) {
     p.rows = mask->meta.rows;
-    p.q_tiles = mask->meta.q_tiles;
-    p.mod = mod_params(d, mask->mods);
-    switch (mod_of(mask->mods)) {
-      case 0: kern = attn_fwd_kernel<0>; break;
-      case kModCap: kern = attn_fwd_kernel<kModCap>; break;
-      case kModBias: kern = attn_fwd_kernel<kModBias>; break;
-      default: kern = attn_fwd_kernel<kModCap | kModBias>; break;
-    }
+    p.work = mask->meta.work;
+    kern = attn_fwd_kernel<true>;
   }
   r.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (r.err != cudaSuccess) {

@@ -102,7 +102,10 @@ __global__ void bwd_pre_kernel(Dims d, const bf16* __restrict__ out, const bf16*
 
 // dk_rope[b, j, :] = sum_g dkr[b, j, g, :] over the dK/dV kernel's head-group
 // partials; 16 threads x 4 columns per row.
-__global__ void rope_sum_kernel(Dims d, int parts, const float* __restrict__ dkr, bf16* __restrict__ dk_rope) {
+// seen (masked attention): whether key tile b * (skv_pad / 128) + tile was walked; the partials of
+// the others were not written.
+__global__ void rope_sum_kernel(Dims d, int parts, const float* __restrict__ dkr, bf16* __restrict__ dk_rope,
+                                const int* __restrict__ seen) {
   const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const long long total = static_cast<long long>(d.B) * d.S * 16;
   if (t >= total) return;
@@ -111,7 +114,7 @@ __global__ void rope_sum_kernel(Dims d, int parts, const float* __restrict__ dkr
   const int j = static_cast<int>(bj % d.S);
   const int b = static_cast<int>(bj / d.S);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (j < d.skv_pad) {
+  if (j < d.skv_pad && (!seen || seen[b * (d.skv_pad / 128) + j / 128])) {
     const float4* src =
         reinterpret_cast<const float4*>(dkr + ((static_cast<long long>(b) * d.skv_pad + j) * parts) * 64) + c4;
     for (int g = 0; g < parts; ++g) {
@@ -140,11 +143,11 @@ LaunchResult tc_bwd_pre(const Dims& d, const bf16* out, const bf16* dout, const 
   return r;
 }
 
-LaunchResult tc_bwd_post(const Dims& d, const BwdWorkspace& w, bf16* dk_rope, cudaStream_t st) {
+LaunchResult tc_bwd_post(const Dims& d, const BwdWorkspace& w, bf16* dk_rope, cudaStream_t st, const int* seen) {
   LaunchResult r;
   const long long t = static_cast<long long>(d.B) * d.S * 16;
   rope_sum_kernel<<<static_cast<unsigned>((t + 255) / 256), 256, 0, st>>>(d, d.n_h / dkdv_heads_per_cta(d.n_h),
-                                                                          w.dkr_ws, dk_rope);
+                                                                          w.dkr_ws, dk_rope, seen);
   r.err = cudaGetLastError();
   if (r.err != cudaSuccess) r.what = "bwd post kernels";
   return r;

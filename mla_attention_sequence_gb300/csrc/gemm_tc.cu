@@ -50,6 +50,11 @@ struct GemmParams {
   int a_head_stride;           // QLAT / OUTPROJ: A columns between heads
   int b_head_stride;           // QLAT: B columns between heads
   int m_first;                 // K/V rebuild: first 128-row tile (a row range of the latent)
+  // LIST instances (masked attention): only the 128-row key tiles that some query walks, as
+  // b * kt + tile, ascending; the others' rows are neither read nor written.
+  const int* key_list;
+  const int* key_count;
+  int kt;  // key tiles per batch element
 };
 
 // Tile order: within a batch element, bands of GROUP_M m-tiles are walked n by n
@@ -145,7 +150,7 @@ __device__ __forceinline__ void epilogue_tile(uint32_t t_acc, int quarter, int l
   }
 }
 
-template <int MODE, int BN, int STAGES, int MH>
+template <int MODE, int BN, int STAGES, int MH, bool LIST>
 __global__ void __launch_bounds__(224, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap mapA0, const __grid_constant__ CUtensorMap mapA1,
                    const __grid_constant__ CUtensorMap mapB0, const __grid_constant__ CUtensorMap mapB1,
@@ -192,8 +197,23 @@ __global__ void __launch_bounds__(224, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
+  static_assert(!LIST || ((MODE == DCKV || MODE == DW) && (MODE == DW || MH == 1)), "listed key tiles");
+  const int keys = LIST ? *p.key_count : 0;
   const int tiles_per_batch = p.m_tiles * p.n_tiles;
-  const int num_tiles = tiles_per_batch * p.batches;
+  // DCKV over a list: one 128-row tile per listed key tile, all n of it in a row. DW: k runs over the
+  // listed tiles, two k-blocks each.
+  const int num_tiles = LIST && MODE == DCKV ? keys * p.n_tiles : tiles_per_batch * p.batches;
+  const int k_blocks = LIST && MODE == DW ? 2 * keys : p.k_blocks;
+  auto coords = [&](int tile, int& b, int& m, int& n) {
+    if constexpr (LIST && MODE == DCKV) {
+      const int key = p.key_list[tile / p.n_tiles];
+      n = tile % p.n_tiles;
+      b = key / p.kt;
+      m = key - b * p.kt;
+    } else {
+      tile_coords(p, tile, b, m, n);
+    }
+  };
 
   if (warp == 0 || warp == 6) {
     if (lane == 0) {
@@ -213,8 +233,9 @@ __global__ void __launch_bounds__(224, 1)
       bool ok = true;
       for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
         int b, m, n;
-        tile_coords(p, tile, b, m, n);
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+        coords(tile, b, m, n);
+        int next_key = LIST && MODE == DW && k_blocks > 0 ? p.key_list[0] : 0, this_key = 0;
+        for (int kb = 0; kb < k_blocks; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1;
           if (!mbar_wait_or_abort(&empty[s], ph ^ 1, abort_flag, 1)) {
@@ -251,8 +272,18 @@ __global__ void __launch_bounds__(224, 1)
           } else {
             const bool second = n >= p.n_tiles_first;
             const int n0 = (second ? n - p.n_tiles_first : n) * BN;
-            const int bb = kb / p.kb_per_batch;
-            const int kk = kb - bb * p.kb_per_batch;
+            int bb, kk;
+            if constexpr (LIST) {
+              if ((kb & 1) == 0) {  // the list is read a tile ahead
+                this_key = next_key;
+                if (kb + 2 < k_blocks) next_key = p.key_list[kb / 2 + 1];
+              }
+              bb = this_key / p.kt;
+              kk = 2 * (this_key - bb * p.kt) + (kb & 1);
+            } else {
+              bb = kb / p.kb_per_batch;
+              kk = kb - bb * p.kb_per_batch;
+            }
             if (load_a) {
 #pragma unroll
               for (int i = 0; i < 2 * MH; ++i)
@@ -294,7 +325,7 @@ __global__ void __launch_bounds__(224, 1)
       }
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + buf * MH * BN;
-      for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+      for (int kb = 0; kb < k_blocks; ++kb, ++it) {
         const int s = it % STAGES;
         if (!warp_wait_token(&full[s], (it / STAGES) & 1, tf, abort_flag, 3)) {
           ok = false;
@@ -313,7 +344,7 @@ __global__ void __launch_bounds__(224, 1)
           mma2_ss_warp(d_tmem + h * BN, a_stage + h * DH, a_stage + h * DH + DA, b_stage, b_stage + DB, C::IDESC,
                        kb != 0 ? 1u : 0u);
         tf = mbar_test(&full[(it + 1) % STAGES], ((it + 1) / STAGES) & 1);
-        if (kb == p.k_blocks - 1) {
+        if (kb == k_blocks - 1) {
           const int nl = local + 1;
           ta = mbar_test(&acc_empty[nl % C::NACC], ((static_cast<uint32_t>(nl / C::NACC)) & 1) ^ 1);
         }
@@ -358,7 +389,7 @@ __global__ void __launch_bounds__(224, 1)
       if (!ok) break;
       tc_fence_after();
       int b, m, n;
-      tile_coords(p, tile, b, m, n);
+      coords(tile, b, m, n);
       const CUtensorMap* omap;
       int n0;
       if constexpr (MODE == DCKV || MODE == QLAT || MODE == OUTPROJ) {
@@ -409,6 +440,7 @@ constexpr int TL_SMEM = TL_STAGES * TL_B_BYTES + 2 * TL_A_BOX + 4 * TL_EPI_BUFS 
 static_assert(TL_ACC_COL + 2 * TL_BN == 512, "TMEM budget");
 static_assert(TL_SMEM <= 232448, "shared memory per CTA");
 
+template <bool LIST>
 __global__ void __launch_bounds__(224, 1)
     recon_tmem_a_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB0,
                         const __grid_constant__ CUtensorMap mapB1, const __grid_constant__ CUtensorMap mapO0,
@@ -465,7 +497,17 @@ __global__ void __launch_bounds__(224, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   // this CTA's contiguous tile range; the latent tile of tile t is key = t / n_tiles
-  const int num_tiles = p.m_tiles * p.n_tiles * p.batches;
+  const int num_tiles = LIST ? *p.key_count * p.n_tiles : p.m_tiles * p.n_tiles * p.batches;
+  auto key_rows = [&](int key, int& b, int& m) {  // batch element and 128-row tile of a latent tile
+    if constexpr (LIST) {
+      const int k = p.key_list[key];
+      b = k / p.kt;
+      m = k - b * p.kt;
+    } else {
+      b = key / p.m_tiles;
+      m = key - b * p.m_tiles + p.m_first;
+    }
+  };
   const int per = num_tiles / gridDim.x, rem = num_tiles % gridDim.x;
   const int t_begin = blockIdx.x * per + min(static_cast<int>(blockIdx.x), rem);
   const int t_end = t_begin + per + (static_cast<int>(blockIdx.x) < rem ? 1 : 0);
@@ -479,7 +521,8 @@ __global__ void __launch_bounds__(224, 1)
         const int key = t / p.n_tiles;
         if (key == cur) continue;
         cur = key;
-        const int b = key / p.m_tiles, m = key - b * p.m_tiles + p.m_first;
+        int b, m;
+        key_rows(key, b, m);
         for (int i = 0; i < A_BOXES; ++i, ++boxes) {
           const int buf = boxes & 1;
           if (!mbar_wait_or_abort(&ast_empty[buf], ((boxes >> 1) & 1) ^ 1, abort_flag, 6)) {
@@ -634,7 +677,8 @@ __global__ void __launch_bounds__(224, 1)
       // every MMA through tile t is done, so the latent columns may be replaced now
       if (t + 1 < t_end && (t + 1) / p.n_tiles != key && !load_latent()) break;
       const int n = t - key * p.n_tiles;
-      const int b = key / p.m_tiles, m = key - b * p.m_tiles + p.m_first;
+      int b, m;
+      key_rows(key, b, m);
       const bool second = n >= p.n_tiles_first;
       const int n0 = (second ? n - p.n_tiles_first : n) * TL_BN;
       epilogue_tile<TL_BN, 1, TL_EPI_BUFS>(tmem_base + TL_ACC_COL + buf * TL_BN, quarter, lane, second ? &mapO1 : &mapO0, n0,
@@ -652,13 +696,13 @@ __global__ void __launch_bounds__(224, 1)
   }
 }
 
-template <int MODE, int BN, int STAGES, int MH = 1>
+template <int MODE, int BN, int STAGES, int MH = 1, bool LIST = false>
 LaunchResult launch_gemm(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
                          const CUtensorMap& b1, const CUtensorMap& o0, const CUtensorMap& o1, const GemmParams& p,
                          cudaStream_t st) {
   using C = Cfg<MODE, BN, STAGES, MH>;
   LaunchResult r;
-  auto kern = gemm_tc_kernel<MODE, BN, STAGES, MH>;
+  auto kern = gemm_tc_kernel<MODE, BN, STAGES, MH, LIST>;
   r.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (r.err != cudaSuccess) {
     r.what = "cudaFuncSetAttribute(gemm)";
@@ -711,7 +755,7 @@ LongKShape long_k_shape(long long tiles_256x256, bool mh2_ok) {
 }
 
 LaunchResult tc_recon_fwd(const Dims& d, const bf16* c_kv, const bf16* W_UK, const bf16* W_UV, bf16* k_ws,
-                          bf16* v_ws, int rows_pad, cudaStream_t st, int m_first, int m_count) {
+                          bf16* v_ws, int rows_pad, cudaStream_t st, int m_first, int m_count, const KeyList* list) {
   LaunchResult r;
   if (d.d_c != TL_DC) {  // the tensor-core path is planned only for d_c = 512
     r.err = cudaErrorInvalidValue;
@@ -747,7 +791,8 @@ LaunchResult tc_recon_fwd(const Dims& d, const bf16* c_kv, const bf16* W_UK, con
     r.what = "tensor map K/V out";
     return r;
   }
-  r.err = cudaFuncSetAttribute(recon_tmem_a_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TL_SMEM);
+  auto kern = list ? recon_tmem_a_kernel<true> : recon_tmem_a_kernel<false>;
+  r.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TL_SMEM);
   if (r.err != cudaSuccess) {
     r.what = "cudaFuncSetAttribute(recon_tmem_a)";
     return r;
@@ -761,14 +806,19 @@ LaunchResult tc_recon_fwd(const Dims& d, const bf16* c_kv, const bf16* W_UK, con
   const int tiles = p.m_tiles * p.n_tiles * p.batches;
   if (tiles == 0) return r;
   p.status = device_status_ptr();
-  recon_tmem_a_kernel<<<std::min(tiles, sm_count()), 224, TL_SMEM, st>>>(a0, b0, b1, o0, o1, p);
+  if (list) {
+    p.key_list = list->tiles;
+    p.key_count = list->count;
+    p.kt = p.m_tiles;
+  }
+  kern<<<std::min(tiles, sm_count()), 224, TL_SMEM, st>>>(a0, b0, b1, o0, o1, p);
   r.err = cudaGetLastError();
   if (r.err != cudaSuccess) r.what = "recon_tmem_a_kernel launch";
   return r;
 }
 
 LaunchResult tc_recon_bwd_dc(const Dims& d, const bf16* dk_ws, const bf16* dv_ws, const bf16* W_UK,
-                             const bf16* W_UV, bf16* dc_kv, cudaStream_t st) {
+                             const bf16* W_UV, bf16* dc_kv, cudaStream_t st, const KeyList* list) {
   // 256 x 256 tiles (two 128-row halves) stream 64 KB per 1024 tensor cycles;
   // 128 x 256 ones 48 KB per 512 and 128 x 128 ones 32 KB per 256. The k loop is
   // n_h * 256 long, so the unoverlapped epilogue of a 256-row tile is cheap.
@@ -776,7 +826,8 @@ LaunchResult tc_recon_bwd_dc(const Dims& d, const bf16* dk_ws, const bf16* dv_ws
   // next element's (or zero-filled) rows; the output map clips those rows.
   LongKShape shape{1, 128};
   if (d.d_c % 256 == 0)
-    shape = long_k_shape(static_cast<long long>(d.B) * ((d.skv_pad + 255) / 256) * (d.d_c / 256), true);
+    // listed key tiles need not be neighbours: 128-row tiles then
+    shape = long_k_shape(static_cast<long long>(d.B) * ((d.skv_pad + 255) / 256) * (d.d_c / 256), list == nullptr);
   const int BN = shape.BN, MH = shape.MH;
   LaunchResult r;
   CUtensorMap a0, a1, b0, b1;
@@ -813,13 +864,20 @@ LaunchResult tc_recon_bwd_dc(const Dims& d, const bf16* dk_ws, const bf16* dv_ws
     r.what = "tensor map dc_kv out";
     return r;
   }
+  if (list) {
+    p.key_list = list->tiles;
+    p.key_count = list->count;
+    p.kt = d.skv_pad / BM;
+    if (BN == 256) return launch_gemm<DCKV, 256, 4, 1, true>(a0, a1, b0, b1, o0, o0, p, st);
+    return launch_gemm<DCKV, 128, 6, 1, true>(a0, a1, b0, b1, o0, o0, p, st);
+  }
   if (MH == 2) return launch_gemm<DCKV, 256, 3, 2>(a0, a1, b0, b1, o0, o0, p, st);
   if (BN == 256) return launch_gemm<DCKV, 256, 4>(a0, a1, b0, b1, o0, o0, p, st);
   return launch_gemm<DCKV, 128, 6>(a0, a1, b0, b1, o0, o0, p, st);
 }
 
 LaunchResult tc_recon_bwd_dw(const Dims& d, const bf16* c_kv, const bf16* dk_ws, const bf16* dv_ws, bf16* dW_UK,
-                             bf16* dW_UV, cudaStream_t st) {
+                             bf16* dW_UV, cudaStream_t st, const KeyList* list) {
   // 256-row tiles (two halves sharing each B k-block) when d_c allows them: the
   // k loop is B * S long, so the unoverlapped epilogue of such a tile is cheap.
   LongKShape shape{1, 128};
@@ -858,6 +916,14 @@ LaunchResult tc_recon_bwd_dw(const Dims& d, const bf16* c_kv, const bf16* dk_ws,
   if (r.cu != CUDA_SUCCESS) {
     r.what = "tensor map dW out";
     return r;
+  }
+  if (list) {
+    p.key_list = list->tiles;
+    p.key_count = list->count;
+    p.kt = d.skv_pad / BM;
+    if (MH == 2) return launch_gemm<DW, 256, 3, 2, true>(a0, a0, b0, b1, o0, o1, p, st);
+    if (BN == 256) return launch_gemm<DW, 256, 4, 1, true>(a0, a0, b0, b1, o0, o1, p, st);
+    return launch_gemm<DW, 128, 6, 1, true>(a0, a0, b0, b1, o0, o1, p, st);
   }
   if (MH == 2) return launch_gemm<DW, 256, 3, 2>(a0, a0, b0, b1, o0, o1, p, st);
   if (BN == 256) return launch_gemm<DW, 256, 4>(a0, a0, b0, b1, o0, o1, p, st);

@@ -65,18 +65,27 @@ bool tc_supported(const Dims& d);
 size_t tc_fwd_workspace(const Dims& d);
 size_t tc_bwd_workspace(const Dims& d);
 
+// The 128-row key tiles that a masked attention walks (device memory): b * (rows_pad / 128) + tile,
+// ascending. With a list the three products below run over its tiles alone: the rebuild leaves
+// the others' K and V unwritten, dc_kv their rows; dW leaves them out of its sum (their gradients
+// are zero).
+struct KeyList {
+  const int* tiles;
+  const int* count;
+};
 // K_nope/V for rows [0, rows) of every batch element into [B][rows_pad][n_h*128] bf16
 // (rows_pad a multiple of 128; rows beyond S come out zero).
 // K_nope / V of latent row tiles [m_first, m_first + m_count) (128 rows each; all of
 // [0, rows_pad / 128) when m_count < 0) into the [B][rows_pad][n_h * 128] buffers.
 LaunchResult tc_recon_fwd(const Dims& d, const bf16* c_kv, const bf16* W_UK, const bf16* W_UV, bf16* k_ws,
-                          bf16* v_ws, int rows_pad, cudaStream_t st, int m_first = 0, int m_count = -1);
+                          bf16* v_ws, int rows_pad, cudaStream_t st, int m_first = 0, int m_count = -1,
+                          const KeyList* list = nullptr);
 // dc_kv = dK_nope W_UK^T + dV W_UV^T (rows < S; rows >= skv_pad zeroed)
 LaunchResult tc_recon_bwd_dc(const Dims& d, const bf16* dk_ws, const bf16* dv_ws, const bf16* W_UK,
-                             const bf16* W_UV, bf16* dc_kv, cudaStream_t st);
+                             const bf16* W_UV, bf16* dc_kv, cudaStream_t st, const KeyList* list = nullptr);
 // dW_UK = sum_b c_kv[b]^T dK_nope[b], dW_UV likewise.
 LaunchResult tc_recon_bwd_dw(const Dims& d, const bf16* c_kv, const bf16* dk_ws, const bf16* dv_ws, bf16* dW_UK,
-                             bf16* dW_UV, cudaStream_t st);
+                             bf16* dW_UV, cudaStream_t st, const KeyList* list = nullptr);
 
 // ---- masked attention (key intervals per query row, capped scores, a bias by distance)
 //
@@ -94,6 +103,8 @@ struct MaskMeta {
   const int* seen;        // [B][skv_pad / 128] whether some query tile's walk touches a key tile
   const int* seen_list;   // the touched ones, b * (skv_pad / 128) + tile, ascending
   const int* seen_count;  // how many
+  const int4* work;       // [B][sq_pad / 128] {query tile, first key tile, key tiles}, longest first
+  int *fwd_ticket, *dq_ticket;  // counters that the kernels' CTAs take items from; 0 at their launch
 };
 
 struct ScoreMods {
@@ -109,9 +120,12 @@ struct MaskArgs {
   ScoreMods mods;
 };
 
-// mask == nullptr: the plain causal (or full) attention.
+// One CTA per query tile. mask: the plain attention (null), or key intervals without a cap or bias.
 LaunchResult tc_attn_fwd(const Dims& d, const bf16* q, const bf16* k_ws, const bf16* v_ws, const bf16* k_rope,
                          bf16* out, float* lse, cudaStream_t st, const MaskArgs* mask = nullptr);
+// Any mods; CTAs that stay and take query tiles.
+LaunchResult tc_masked_attn_fwd(const Dims& d, const MaskArgs& mask, const bf16* q, const bf16* k_ws, const bf16* v_ws,
+                                const bf16* k_rope, bf16* out, float* lse, cudaStream_t st);
 LaunchResult tc_attn_fwd_fused(const Dims& d, const bf16* q, const bf16* c_kv, const bf16* W_UK,
                                const bf16* W_UV, const bf16* k_rope, bf16* out, float* lse, cudaStream_t st);
 
@@ -140,7 +154,8 @@ LaunchResult tc_attn_bwd_dkdv(const Dims& d, const bf16* q, const bf16* k_rope, 
 LaunchResult tc_attn_bwd_dq(const Dims& d, const bf16* q, const bf16* k_rope, const bf16* dout,
                             const BwdWorkspace& w, bf16* dq, cudaStream_t st, const MaskArgs* mask = nullptr);
 // dk_rope = sum over heads of the per-head RoPE-key gradients.
-LaunchResult tc_bwd_post(const Dims& d, const BwdWorkspace& w, bf16* dk_rope, cudaStream_t st);
+LaunchResult tc_bwd_post(const Dims& d, const BwdWorkspace& w, bf16* dk_rope, cudaStream_t st,
+                         const int* seen = nullptr);
 
 // ---- the absorbed MLA form (for comparison; bf16, the tensor-core dims).
 // q_lat [B*Sq][n_h*d_c] = per head q_nope_h W_UK_h^T

@@ -51,11 +51,13 @@ struct MaskBuffers {
   int2 *rows, *q_tiles, *q_hull;
   int *kt_count, *kt_list, *q_bad;
   int *seen, *seen_list;  // [B * kt]: whether a key tile is walked; the walked ones, in order
-  int* counters;          // {tiles in seen_list, CTAs done}
+  int* counters;          // {tiles in seen_list, CTAs done, forward ticket, dq ticket}
+  int4* work;
   uint32_t* bad;  // [B][ceil(S / 32)] bit per key: its latent row is not finite
   char* c_kv;     // [B][S][d_c] with such rows zero, in the inputs' type
   char* k_rope;   // [B][S][d_rope]
-  MaskMeta meta() const { return MaskMeta{rows, q_tiles, q_hull, kt_count, kt_list, q_bad, seen, seen_list, counters}; }
+  MaskMeta meta() const { return MaskMeta{rows, q_tiles, q_hull, kt_count, kt_list, q_bad, seen, seen_list, counters,
+                                             work, counters + 2, counters + 3}; }
 };
 size_t mask_bytes(const Dims& d, int elem);
 MaskBuffers mask_carve(const Dims& d, int elem, char*& p);  // advances p

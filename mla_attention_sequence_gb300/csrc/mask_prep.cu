@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(128) mask_rows_kernel(Dims d, const int* __res
   __shared__ int s_lo[4], s_hi[4];
   const int t = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = t * 128 + threadIdx.x;
-  if (t == 0 && b == 0 && threadIdx.x == 0) *q_bad = counters[0] = counters[1] = 0;
+  if (t == 0 && b == 0 && threadIdx.x == 0) *q_bad = counters[0] = counters[1] = counters[2] = counters[3] = 0;
   int lo = 0, hi = 0;
   if (i < d.Sq) {
     const ll at = static_cast<ll>(b) * d.Sq + i;
@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(128) mask_rows_kernel(Dims d, const int* __res
 __global__ void __launch_bounds__(1024) mask_tiles_kernel(int kt, int nq64, const int2* __restrict__ q_tiles,
                                                           const int2* __restrict__ q_hull, int* __restrict__ kt_count,
                                                           int* __restrict__ kt_list, int* __restrict__ seen,
-                                                          int* __restrict__ seen_list, int* __restrict__ counters) {
+                                                          int* __restrict__ seen_list, int* __restrict__ counters,
+                                                          int4* __restrict__ work) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
   const int2* hull = q_hull + static_cast<ll>(b) * nq64;
   const int2* walk = q_tiles + static_cast<ll>(b) * (nq64 / 2);
@@ -210,6 +211,17 @@ __global__ void __launch_bounds__(1024) mask_tiles_kernel(int kt, int nq64, cons
       kt_count[at] = n;
       seen[at] = touched ? 1 : 0;
     }
+  }
+  // the query tiles by the length of their walk, longest first (ties by number)
+  const int nq = nq64 / 2;
+  for (int q = threadIdx.x; q < nq; q += 1024) {
+    const int2 w = walk[q];
+    int rank = 0;
+    for (int o = 0; o < nq; ++o) {
+      const int n = walk[o].y;
+      rank += n > w.y || (n == w.y && o < q);
+    }
+    work[static_cast<ll>(b) * nq + rank] = make_int4(q, w.x, w.y, 0);
   }
   __shared__ bool last;
   __shared__ int warp_n[32];
@@ -452,7 +464,8 @@ MaskBuffers mask_carve(const Dims& d, int elem, char*& p) {
   m.kt_count = reinterpret_cast<int*>(take(B * kt * 4));
   m.kt_list = reinterpret_cast<int*>(take(B * kt * nq64 * 4));
   m.q_bad = reinterpret_cast<int*>(take(4));
-  m.counters = reinterpret_cast<int*>(take(8));
+  m.counters = reinterpret_cast<int*>(take(16));
+  m.work = reinterpret_cast<int4*>(take(B * (nq64 / 2) * 16));
   m.seen = reinterpret_cast<int*>(take(B * kt * 4));
   m.seen_list = reinterpret_cast<int*>(take(B * kt * 4));
   m.bad = reinterpret_cast<uint32_t*>(take(B * ((d.S + 31) / 32) * 4));
@@ -489,7 +502,7 @@ LaunchResult mask_prepare(const Dims& d, bool is_bf16, const int* key_lo, const 
   }
   if (r.err == cudaSuccess && key_tiles) {
     mask_tiles_kernel<<<d.B, 1024, 0, st>>>(d.skv_pad / 128, d.sq_pad / 64, m.q_tiles, m.q_hull, m.kt_count, m.kt_list,
-                                            m.seen, m.seen_list, m.counters);
+                                            m.seen, m.seen_list, m.counters, m.work);
     r.err = cudaGetLastError();
   }
   if (r.err != cudaSuccess) r.what = "mask preparation";

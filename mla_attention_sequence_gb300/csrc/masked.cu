@@ -33,7 +33,8 @@ Path masked_plan(const laga_mla_desc* desc, Dims* d, laga_status* st, bool for_b
     *st = fail(LAGA_ERR_UNSUPPORTED, "masked attention supports d_nope + d_rope <= 256 and d_v <= 256%s");
     return Path::Invalid;
   }
-  if (d->B > 65535 || d->n_h > 65535) {
+  if (d->B > 65535 || d->n_h > 65535 ||
+      static_cast<int64_t>(d->B) * d->n_h * (d->sq_pad / 128) >= (int64_t(1) << 31) - 65536) {
     *st = fail(LAGA_ERR_UNSUPPORTED, "problem too large%s");
     return Path::Invalid;
   }
@@ -120,14 +121,22 @@ laga_status laga_mla_masked_fwd(const laga_mla_desc* desc, const laga_mla_mods* 
   char* at = static_cast<char*>(workspace) + tc_fwd_workspace(d);
   const MaskBuffers m = mask_carve(d, elem, at);
   const MaskArgs mask{m.meta(), sm};
+  const KeyList list{m.seen_list, m.counters};
   LaunchResult r =
       timed("mask_prepare", s, [&] { return mask_prepare(d, true, lo, hi, c_kv, k_rope, m, true, s); });
   if (r.ok())
     r = timed("recon_fwd_gemm", s,
-              [&] { return tc_recon_fwd(d, cb(m.c_kv), cb(W_UK), cb(W_UV), k_ws, v_ws, d.skv_pad, s); });
+              [&] { return tc_recon_fwd(d, cb(m.c_kv), cb(W_UK), cb(W_UV), k_ws, v_ws, d.skv_pad, s, 0, -1, &list); });
+  // Without a cap or bias a long walk is better off with one CTA per query tile (2048 rows of 128
+  // heads over up to 16384 keys: 1.04 ms against 1.23), short ones with CTAs that stay (2 x 4096
+  // rows of 16 heads, documents of ~100 keys: 52 us against 67; of ~800: 90 against 92). How long
+  // the walks are only the device knows; how long they can be, the sizes say.
+  const bool long_walks = mod_of(sm) == 0 && d.skv_pad >= 64 * 128;
   if (r.ok())
     r = timed("masked_attn_fwd", s, [&] {
-      return tc_attn_fwd(d, cb(q), k_ws, v_ws, cb(m.k_rope), static_cast<bf16*>(out), lse, s, &mask);
+      if (long_walks)
+        return tc_attn_fwd(d, cb(q), k_ws, v_ws, cb(m.k_rope), static_cast<bf16*>(out), lse, s, &mask);
+      return tc_masked_attn_fwd(d, mask, cb(q), k_ws, v_ws, cb(m.k_rope), static_cast<bf16*>(out), lse, s);
     });
   return from_launch(r);
 }
@@ -185,13 +194,14 @@ laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* 
   bf16* q_clean = reinterpret_cast<bf16*>(at);
   bf16* dout_clean = reinterpret_cast<bf16*>(at + tc_clean_q_bytes(d));
   const MaskArgs mask{m.meta(), sm};
+  const KeyList list{m.seen_list, m.counters};
   const bf16* qr = packed ? q_clean : cb(q);  // what the kernels read as q
   const bf16 *c = cb(m.c_kv), *kr = cb(m.k_rope);
   LaunchResult r;
   if (!reuse) {
     r = timed("mask_prepare", s, [&] { return mask_prepare(d, true, lo, hi, c_kv, k_rope, m, true, s); });
     if (r.ok())
-      r = timed("recon_fwd_gemm", s, [&] { return tc_recon_fwd(d, c, cb(W_UK), cb(W_UV), w.k_ws, w.v_ws, d.skv_pad, s); });
+      r = timed("recon_fwd_gemm", s, [&] { return tc_recon_fwd(d, c, cb(W_UK), cb(W_UV), w.k_ws, w.v_ws, d.skv_pad, s, 0, -1, &list); });
   }
   if (r.ok())
     r = timed("masked_bwd_pre", s, [&] {
@@ -204,22 +214,19 @@ laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* 
   if (r.ok())
     r = timed("masked_attn_bwd_dq", s,
               [&] { return tc_attn_bwd_dq(d, qr, kr, cb(dout), w, static_cast<bf16*>(dq), s, &mask); });
+  if (r.ok()) {  // rows of key tiles that nothing walks get zero gradient
+    r.err = cudaMemsetAsync(dc_kv, 0, static_cast<size_t>(d.B) * d.S * d.d_c * 2, s);
+    if (r.err != cudaSuccess) r.what = "zero dc_kv";
+  }
   if (r.ok())
     r = timed("recon_bwd_dc_gemm", s, [&] {
-      return tc_recon_bwd_dc(d, w.dk_ws, w.dv_ws, cb(W_UK), cb(W_UV), static_cast<bf16*>(dc_kv), s);
+      return tc_recon_bwd_dc(d, w.dk_ws, w.dv_ws, cb(W_UK), cb(W_UV), static_cast<bf16*>(dc_kv), s, &list);
     });
   if (r.ok())
     r = timed("recon_bwd_dw_gemm", s, [&] {
-      return tc_recon_bwd_dw(d, c, w.dk_ws, w.dv_ws, static_cast<bf16*>(dW_UK), static_cast<bf16*>(dW_UV), s);
+      return tc_recon_bwd_dw(d, c, w.dk_ws, w.dv_ws, static_cast<bf16*>(dW_UK), static_cast<bf16*>(dW_UV), s, &list);
     });
-  if (r.ok()) r = timed("bwd_post", s, [&] { return tc_bwd_post(d, w, static_cast<bf16*>(dk_rope), s); });
-  if (r.ok() && d.skv_pad < d.S) {
-    // Latent rows beyond the padded visible prefix get zero gradient.
-    r.err = cudaMemset2DAsync(static_cast<bf16*>(dc_kv) + static_cast<size_t>(d.skv_pad) * d.d_c,
-                              static_cast<size_t>(d.S) * d.d_c * 2, 0, static_cast<size_t>(d.S - d.skv_pad) * d.d_c * 2,
-                              d.B, s);
-    if (r.err != cudaSuccess) r.what = "zero dc_kv tail";
-  }
+  if (r.ok()) r = timed("bwd_post", s, [&] { return tc_bwd_post(d, w, static_cast<bf16*>(dk_rope), s, m.seen); });
   return from_launch(r);
 }
 

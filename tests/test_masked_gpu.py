@@ -44,7 +44,7 @@ def inputs(B, Sq, S, n_h, dims, dtype, seed=0):
 
 
 def step(x, dout, variant="auto", **kw):
-    ws = laga.masked_workspace(*x.values(), variant=variant, **kw)
+    ws = laga.masked_workspace(*x.values(), variant=variant, **kw).fill_(255)  # NaN wherever it is not written
     out, lse = laga.masked_fwd(*x.values(), variant=variant, workspace=ws, **kw)
     g = laga.masked_bwd(*x.values(), out, lse, dout, variant=variant, workspace=ws, reuse_kv=True, **kw)
     return {"out": out, "lse": lse, **g}
@@ -152,6 +152,23 @@ def test_key_bounds_two_segments_and_outside():
     # past skv the upper bound is clamped; the interval may be empty then
     assert torch.equal(lo.cpu().long(), torch.from_numpy(want[0])) and torch.equal(hi.cpu().long(),
                                                                                    torch.from_numpy(want[1]))
+
+
+@pytest.mark.parametrize("mod", ["mask", "both"])
+def test_most_key_tiles_unseen(mod):
+    """A few short intervals far apart: the other key tiles are neither rebuilt nor given gradients."""
+    B, Sq, S, n_h = 3, 190, 9000, 2
+    x, dout = inputs(B, Sq, S, n_h, DSV3, torch.bfloat16, 14)
+    g = torch.Generator().manual_seed(3)
+    at = torch.tensor([[0, 5000], [8990, 3], [200, 330]])[:, :, None].expand(B, 2, 95).reshape(B, Sq)
+    lo = (at + torch.randint(0, 20, (B, Sq), generator=g)).int()
+    hi = (lo + torch.randint(1, 90, (B, Sq), generator=g)).int()
+    kw = dict(MODS[mod], key_lo=lo.to(dev()), key_hi=hi.to(dev()), causal=False, q_offset=4000)
+    if mod == "both":
+        kw["slopes"] = slopes(n_h) / 64
+    got = check(x, dout, **kw)
+    seen = ref.visible(Sq, S, lo, hi, causal=False, B=B).any(1).to(dev())
+    assert not got["dc_kv"][~seen].any() and not got["dk_rope"][~seen].any()
 
 
 def test_two_segments():
