@@ -369,14 +369,14 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
 
 // dq of 64 query rows of one head.
 template <int N, int RI>
-__global__ void __launch_bounds__(THREADS) masked_simt_dq(const SimtParams p) {
+__device__ __forceinline__ void masked_simt_dq(const SimtParams& p, int t) {
   constexpr int ROWS = 16 * RI;
   extern __shared__ float4 sm[];
   const Dims& d = p.d;
   const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v);
   float4 *sq = sm, *sdo = sq + ROWS * pk, *sk = sdo + ROWS * pv, *sv = sk + KBWD * pk, *weights = sv + KBWD * pv;
   float* sds = reinterpret_cast<float*>(weights);
-  const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int h = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int i0 = t * ROWS + RI * ty;
   fill<ROWS>(sq, pk, d.d_qk(), QRows{p, b, h, t * ROWS});
@@ -450,14 +450,14 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dq(const SimtParams p) {
 
 // dK (both parts) and dV of 64 keys of one head.
 template <int N, int RI>
-__global__ void __launch_bounds__(THREADS) masked_simt_dkv(const SimtParams p) {
+__device__ __forceinline__ void masked_simt_dkv(const SimtParams& p, int t) {
   constexpr int ROWS = 16 * RI;
   extern __shared__ float4 sm[];
   const Dims& d = p.d;
   const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v);
   float4 *sk = sm, *sv = sk + ROWS * pk, *sq = sv + ROWS * pv, *sdo = sq + KBWD * pk, *weights = sdo + KBWD * pv;
   float *sp = reinterpret_cast<float*>(weights), *sds = sp + KBWD * 17 * RI;
-  const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int h = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int k0 = t * ROWS + RI * ty;  // this thread's first key
   fill<ROWS>(sk, pk, d.d_qk(), KRows{p, b, h, t * ROWS});
@@ -541,6 +541,17 @@ __global__ void __launch_bounds__(THREADS) masked_simt_dkv(const SimtParams p) {
   }
 }
 
+// Both sides of the backward in one launch: neither needs the other's result, and a small
+// problem's CTAs of either alone leave most SMs idle (256 rows, 4 heads: 64 CTAs each).
+template <int N, int RI>
+__global__ void __launch_bounds__(THREADS) masked_simt_bwd(const SimtParams p) {
+  const int q_blocks = (p.d.Sq + 16 * RI - 1) / (16 * RI);
+  if (static_cast<int>(blockIdx.x) < q_blocks)
+    masked_simt_dq<N, RI>(p, blockIdx.x);
+  else
+    masked_simt_dkv<N, RI>(p, static_cast<int>(blockIdx.x) - q_blocks);
+}
+
 // dk_rope[b, j, :] = the heads' RoPE-key gradients summed, in order.
 template <typename T>
 __global__ void masked_simt_rope_sum(ll total, int n_h, int d_rope, const float* __restrict__ dkr, T* __restrict__ dk_rope) {
@@ -611,37 +622,35 @@ int rows_per_thread(const Dims& d, int rows) {
   return ctas >= 2 * sm_count() ? 4 : 2 * ctas >= 2 * sm_count() ? 2 : 1;
 }
 
-enum Which { FWD, DQ, DKV };
-template <Which W, int N, int RI>
+template <bool BWD, int N, int RI>
 constexpr auto kernel_of() {
-  if constexpr (W == FWD)
-    return masked_simt_fwd<N, RI>;
-  else if constexpr (W == DQ)
-    return masked_simt_dq<N, RI>;
+  if constexpr (BWD)
+    return masked_simt_bwd<N, RI>;
   else
-    return masked_simt_dkv<N, RI>;
+    return masked_simt_fwd<N, RI>;
 }
 
-template <Which W, int RI>
-cudaError_t launch_rows(const Dims& d, int rows, const SimtParams& p, cudaStream_t st) {
+template <bool BWD, int RI>
+cudaError_t launch_rows(const Dims& d, const SimtParams& p, cudaStream_t st) {
   const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v), w = std::max(d.d_qk(), d.d_v);
   constexpr int R = 16 * RI;
-  const size_t smem = W == FWD ? sizeof(float4) * ((R + KFWD) * pk + KFWD * pv) + sizeof(float) * KFWD * 17 * RI
-                               : sizeof(float4) * (R + KBWD) * (pk + pv) +
-                                     sizeof(float) * (W == DKV ? 2 : 1) * KBWD * 17 * RI;
-  void (*kern)(SimtParams) = w <= 64 ? kernel_of<W, 1, RI>() : w <= 128 ? kernel_of<W, 2, RI>() : kernel_of<W, 4, RI>();
+  const size_t smem = BWD ? sizeof(float4) * (R + KBWD) * (pk + pv) + sizeof(float) * 2 * KBWD * 17 * RI
+                          : sizeof(float4) * ((R + KFWD) * pk + KFWD * pv) + sizeof(float) * KFWD * 17 * RI;
+  const int blocks = (d.Sq + R - 1) / R + (BWD ? (d.S + R - 1) / R : 0);
+  void (*kern)(SimtParams) =
+      w <= 64 ? kernel_of<BWD, 1, RI>() : w <= 128 ? kernel_of<BWD, 2, RI>() : kernel_of<BWD, 4, RI>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kern<<<dim3((rows + R - 1) / R, d.n_h, d.B), THREADS, smem, st>>>(p);
+  kern<<<dim3(blocks, d.n_h, d.B), THREADS, smem, st>>>(p);
   return cudaGetLastError();
 }
 
-template <Which W>
-cudaError_t launch(const Dims& d, int rows, const SimtParams& p, cudaStream_t st) {
-  switch (rows_per_thread(d, rows)) {
-    case 4: return launch_rows<W, 4>(d, rows, p, st);
-    case 2: return launch_rows<W, 2>(d, rows, p, st);
-    default: return launch_rows<W, 1>(d, rows, p, st);
+template <bool BWD>
+cudaError_t launch(const Dims& d, const SimtParams& p, cudaStream_t st) {
+  switch (rows_per_thread(d, BWD ? d.Sq + d.S : d.Sq)) {
+    case 4: return launch_rows<BWD, 4>(d, p, st);
+    case 2: return launch_rows<BWD, 2>(d, p, st);
+    default: return launch_rows<BWD, 1>(d, p, st);
   }
 }
 
@@ -805,7 +814,7 @@ LaunchResult simt_masked_fwd(const Dims& d, bool is_bf16, const ScoreMods& mods,
   p.q_bf16 = is_bf16;
   p.out = out;
   p.lse = lse;
-  r.err = launch<FWD>(d, d.Sq, p, st);
+  r.err = launch<false>(d, p, st);
   if (r.err != cudaSuccess) r.what = "masked attention forward (CUDA cores)";
   return r;
 }
@@ -834,8 +843,7 @@ LaunchResult simt_masked_bwd(const Dims& d, bool is_bf16, const ScoreMods& mods,
   p.dkn = w.dkn;
   p.dv = w.dv;
   p.dkr = w.dkr;
-  r.err = launch<DQ>(d, d.Sq, p, st);
-  if (r.err == cudaSuccess) r.err = launch<DKV>(d, d.S, p, st);
+  r.err = launch<true>(d, p, st);
   const ll nr = static_cast<ll>(d.B) * d.S * d.d_rope;
   if (r.err == cudaSuccess && nr > 0) {
     const unsigned grid = static_cast<unsigned>((nr + 255) / 256);
