@@ -320,7 +320,7 @@ size_t laga_mla_bwd_workspace_size(const laga_mla_desc* desc) {
   laga_status st;
   switch (plan(desc, &d, &st, true)) {
     case Path::Simt: return simt_bwd_workspace(d);
-    case Path::TensorCore: return tc_bwd_workspace(d);
+    case Path::TensorCore: return tc_bwd_workspace(d, dkdv_heads_per_cta(d.n_h));
     default: return 0;
   }
 }
@@ -414,7 +414,7 @@ laga_status laga_mla_bwd(const laga_mla_desc* desc, const void* q, const void* c
     return fail(LAGA_ERR_INVALID_ARG, "k_rope/dk_rope must be non-null and 16-byte aligned%s");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = desc->dtype == LAGA_DTYPE_BF16;
-  const size_t need = path == Path::Simt ? simt_bwd_workspace(d) : tc_bwd_workspace(d);
+  const size_t need = path == Path::Simt ? simt_bwd_workspace(d) : tc_bwd_workspace(d, dkdv_heads_per_cta(d.n_h));
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(LAGA_ERR_WORKSPACE, "workspace missing, misaligned (256 B) or too small%s");
   if (path == Path::Simt)
@@ -422,7 +422,7 @@ laga_status laga_mla_bwd(const laga_mla_desc* desc, const void* q, const void* c
       return simt_bwd(d, bf, q, c_kv, k_rope, W_UK, W_UV, out, lse, dout, dq, dc_kv, dk_rope, dW_UK, dW_UV,
                       workspace, (desc->flags & LAGA_FLAG_REUSE_KV) != 0, s);
     }));
-  BwdWorkspace w = tc_bwd_carve(d, workspace);
+  BwdWorkspace w = tc_bwd_carve(d, workspace, dkdv_heads_per_cta(d.n_h));
   auto cb = [](const void* p) { return static_cast<const bf16*>(p); };
   LaunchResult r;
   if (!(desc->flags & LAGA_FLAG_REUSE_KV))

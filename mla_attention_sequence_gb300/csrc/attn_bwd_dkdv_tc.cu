@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // Warm L2 with the first tiles of the CTA that will run next on this SM
       // (about one CTA lifetime from now): its start then waits on L2, not HBM.
       auto prefetch_successor = [&]() {
+        if constexpr (MASKED) return;
         const long long nx = gridDim.x, ny = gridDim.y;
         const long long nb = blockIdx.x + nx * (blockIdx.y + ny * blockIdx.z) + p.successor;
         if (nb < nx * ny * gridDim.z) {
@@ -242,7 +243,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tma_prefetch_3d(&mR, 0, nkv0, nbb);
           tma_prefetch_2d(&mV, nh * 128, nrow);
           tma_prefetch_2d(&mV, nh * 128 + 64, nrow);
-          if constexpr (MASKED) return;
           const int nfirst = p.causal ? max(0, nkv0 - p.q_offset) / BQ : 0;
           for (int k = nfirst; k < nfirst + 2 && k < nq; ++k) {
             tma_prefetch_3d(&mQ, nh * 192, k * BQ, nbb);
@@ -786,7 +786,7 @@ LaunchResult tc_attn_bwd_dkdv(const Dims& d, const bf16* q, const bf16* k_rope, 
   // ([B * skv_pad rows][n_h * 128] bf16) and of the RoPE-key partials
   // ([B * skv_pad rows][n_h / G * 64] fp32)
   CUtensorMap mdK, mdV, mdKR;
-  const int G = dkdv_heads_per_cta(d.n_h);
+  const int G = w.G;
   if (r.cu == CUDA_SUCCESS) {
     const uint64_t dims[2] = {kv_inner, kv_rows};
     const uint64_t strides[1] = {kv_inner * 2};

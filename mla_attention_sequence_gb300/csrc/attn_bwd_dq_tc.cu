@@ -75,7 +75,7 @@ struct Params {
   const bf16* dout;  // [B][Sq][n_h][128]
   // masked instances
   const int2* rows;     // [B][sq_pad] visible interval of each query row
-  const int2* q_tiles;  // [B][n_q_tiles] {first key tile, key tiles}
+  const int4* work;     // [B][n_q_tiles] {query tile, first key tile, key tiles}, longest first
   ModParams mod;
 };
 
@@ -123,16 +123,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int t = p.n_q_tiles - 1 - static_cast<int>(blockIdx.x);  // heaviest tiles first
+  int t = p.n_q_tiles - 1 - static_cast<int>(blockIdx.x);  // heaviest tiles first
   const int h = blockIdx.y;
   const int b = blockIdx.z;
   constexpr bool MASKED = MOD >= 0;
   constexpr bool CAP = MASKED && (MOD & kModCap) != 0, BIAS = MASKED && (MOD & kModBias) != 0;
   int n_kv, j0 = 0;  // key tiles walked: [j0, j0 + n_kv)
   if constexpr (MASKED) {
-    const int2 span = p.q_tiles[b * p.n_q_tiles + t];
-    j0 = span.x;
-    n_kv = span.y;
+    const int4 w = p.work[b * p.n_q_tiles + blockIdx.x];
+    t = w.x;
+    j0 = w.y;
+    n_kv = w.z;
   } else {
     n_kv = n_kv_tiles(p, t);
   }
@@ -576,7 +577,7 @@ LaunchResult tc_attn_bwd_dq(const Dims& d, const bf16* q, const bf16* k_rope, co
   void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Params) = attn_bwd_dq_kernel<-1>;
   if (mask) {
     p.rows = mask->meta.rows;
-    p.q_tiles = mask->meta.q_tiles;
+    p.work = mask->meta.work;
     p.mod = mod_params(d, mask->mods);
     switch (mod_of(mask->mods)) {
       case 0: kern = attn_bwd_dq_kernel<0>; break;

@@ -25,17 +25,18 @@ size_t kv_ws_bytes(const Dims& d) { return align_up(static_cast<size_t>(d.B) * d
 
 size_t tc_fwd_workspace(const Dims& d) { return 2 * kv_ws_bytes(d); }
 
-size_t tc_bwd_workspace(const Dims& d) {
+size_t tc_bwd_workspace(const Dims& d, int G) {
   const size_t kv = kv_ws_bytes(d);
-  const size_t dkr = align_up(static_cast<size_t>(d.B) * d.skv_pad * (d.n_h / dkdv_heads_per_cta(d.n_h)) * 64 * 4, 256);
+  const size_t dkr = align_up(static_cast<size_t>(d.B) * d.skv_pad * (d.n_h / G) * 64 * 4, 256);
   const size_t rows = align_up(static_cast<size_t>(d.B) * d.n_h * d.sq_pad * 4, 256);
   return 4 * kv + dkr + 2 * rows;
 }
 
-BwdWorkspace tc_bwd_carve(const Dims& d, void* ws) {
+BwdWorkspace tc_bwd_carve(const Dims& d, void* ws, int G) {
   char* p = static_cast<char*>(ws);
   const size_t kv = kv_ws_bytes(d);
   BwdWorkspace w{};
+  w.G = G;
   w.k_ws = reinterpret_cast<bf16*>(p);
   p += kv;
   w.v_ws = reinterpret_cast<bf16*>(p);
@@ -45,7 +46,7 @@ BwdWorkspace tc_bwd_carve(const Dims& d, void* ws) {
   w.dv_ws = reinterpret_cast<bf16*>(p);
   p += kv;
   w.dkr_ws = reinterpret_cast<float*>(p);
-  p += align_up(static_cast<size_t>(d.B) * d.skv_pad * (d.n_h / dkdv_heads_per_cta(d.n_h)) * 64 * 4, 256);
+  p += align_up(static_cast<size_t>(d.B) * d.skv_pad * (d.n_h / G) * 64 * 4, 256);
   w.lse2 = reinterpret_cast<float*>(p);
   p += align_up(static_cast<size_t>(d.B) * d.n_h * d.sq_pad * 4, 256);
   w.delta = reinterpret_cast<float*>(p);
@@ -146,7 +147,7 @@ LaunchResult tc_bwd_pre(const Dims& d, const bf16* out, const bf16* dout, const 
 LaunchResult tc_bwd_post(const Dims& d, const BwdWorkspace& w, bf16* dk_rope, cudaStream_t st, const int* seen) {
   LaunchResult r;
   const long long t = static_cast<long long>(d.B) * d.S * 16;
-  rope_sum_kernel<<<static_cast<unsigned>((t + 255) / 256), 256, 0, st>>>(d, d.n_h / dkdv_heads_per_cta(d.n_h),
+  rope_sum_kernel<<<static_cast<unsigned>((t + 255) / 256), 256, 0, st>>>(d, d.n_h / w.G,
                                                                           w.dkr_ws, dk_rope, seen);
   r.err = cudaGetLastError();
   if (r.err != cudaSuccess) r.what = "bwd post kernels";

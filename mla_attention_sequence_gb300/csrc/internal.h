@@ -63,7 +63,7 @@ LaunchResult simt_bwd(const Dims& d, bool is_bf16, const void* q, const void* c_
 // ---- tensor-core path (bf16, d_c=512, d_nope=d_v=128, d_rope=64).
 bool tc_supported(const Dims& d);
 size_t tc_fwd_workspace(const Dims& d);
-size_t tc_bwd_workspace(const Dims& d);
+size_t tc_bwd_workspace(const Dims& d, int G);  // G: heads per dK/dV CTA
 
 // The 128-row key tiles that a masked attention walks (device memory): b * (rows_pad / 128) + tile,
 // ascending. With a list the three products below run over its tiles alone: the rebuild leaves
@@ -95,7 +95,6 @@ struct MaskMeta {
   // causal, the past) keys; {0, 0}: the row sees nothing. Bit 31 of the first: some key that
   // the row sees holds a non-finite latent value (the row's result is NaN).
   const int2* rows;
-  const int2* q_tiles;  // [B][sq_pad / 128] {first 128-key tile, tiles >= 1} of a 128-row query tile
   const int2* q_hull;   // [B][sq_pad / 64] {lowest first key, highest one-past-last} of a 64-row tile
   const int* kt_count;  // [B][skv_pad / 128] 64-row query tiles that may see a key tile
   const int* kt_list;   // [B][skv_pad / 128][sq_pad / 64] which, ascending
@@ -104,7 +103,7 @@ struct MaskMeta {
   const int* seen_list;   // the touched ones, b * (skv_pad / 128) + tile, ascending
   const int* seen_count;  // how many
   const int4* work;       // [B][sq_pad / 128] {query tile, first key tile, key tiles}, longest first
-  int *fwd_ticket, *dq_ticket;  // counters that the kernels' CTAs take items from; 0 at their launch
+  int* fwd_ticket;        // the counter that the forward's CTAs take items from; 0 at its launch
 };
 
 struct ScoreMods {
@@ -134,14 +133,15 @@ struct BwdWorkspace {
   bf16* v_ws;       // [B][skv_pad][n_h*128]
   bf16* dk_ws;      // [B][skv_pad][n_h*128]
   bf16* dv_ws;      // [B][skv_pad][n_h*128]
+  int G;            // heads per dK/dV CTA
   float* dkr_ws;    // [B][skv_pad][n_h / G][64]  RoPE-key gradient per head group (fp32)
   float* lse2;      // [B][n_h][sq_pad]  lse * log2(e), +inf on padded rows
   float* delta;     // [B][n_h][sq_pad]  rowsum(dout * out), 0 on padded rows
 };
-BwdWorkspace tc_bwd_carve(const Dims& d, void* ws);
 // Heads per dK/dV CTA (G): the CTA walks G consecutive heads of one key tile and
 // sums their RoPE-key gradients in TMEM, so the workspace holds n_h / G partials.
 int dkdv_heads_per_cta(int n_h);
+BwdWorkspace tc_bwd_carve(const Dims& d, void* ws, int G);
 
 LaunchResult tc_bwd_pre(const Dims& d, const bf16* out, const bf16* dout, const float* lse, const BwdWorkspace& w,
                         cudaStream_t st);

@@ -51,13 +51,13 @@ struct MaskBuffers {
   int2 *rows, *q_tiles, *q_hull;
   int *kt_count, *kt_list, *q_bad;
   int *seen, *seen_list;  // [B * kt]: whether a key tile is walked; the walked ones, in order
-  int* counters;          // {tiles in seen_list, CTAs done, forward ticket, dq ticket}
+  int* counters;          // {tiles in seen_list, CTAs done, forward ticket}
   int4* work;
   uint32_t* bad;  // [B][ceil(S / 32)] bit per key: its latent row is not finite
   char* c_kv;     // [B][S][d_c] with such rows zero, in the inputs' type
   char* k_rope;   // [B][S][d_rope]
-  MaskMeta meta() const { return MaskMeta{rows, q_tiles, q_hull, kt_count, kt_list, q_bad, seen, seen_list, counters,
-                                             work, counters + 2, counters + 3}; }
+  MaskMeta meta() const { return MaskMeta{rows, q_hull, kt_count, kt_list, q_bad, seen, seen_list, counters,
+                                             work, counters + 2}; }
 };
 size_t mask_bytes(const Dims& d, int elem);
 MaskBuffers mask_carve(const Dims& d, int elem, char*& p);  // advances p
@@ -69,9 +69,10 @@ LaunchResult mask_key_bounds(const Dims& d, const int* starts, int n_docs, const
 
 // Row statistics of the masked backward (w.lse2, w.delta) and, if some q or dout row is not
 // finite, clean copies; with q8 / out8, q and out come from checkpoints and q_clean is written.
+// check_q: a non-finite q may have a finite lse (capped scores).
 LaunchResult tc_mask_bwd_pre(const Dims& d, const bf16* q, const bf16* out, const Packed* q8, const Packed* out8,
                              const bf16* dout, const float* lse, const BwdWorkspace& w, bf16* q_clean,
-                             bf16* dout_clean, int* q_bad, cudaStream_t st);
+                             bf16* dout_clean, int* q_bad, bool check_q, cudaStream_t st);
 
 // ---- CUDA cores, any widths up to 256: fp32 K/V, fp32 arithmetic.
 LaunchResult simt_mask_bwd_pre(const Dims& d, bool is_bf16, const void* q, const void* out, const Packed* q8,

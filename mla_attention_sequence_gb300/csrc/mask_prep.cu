@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(128) mask_rows_kernel(Dims d, const int* __res
   __shared__ int s_lo[4], s_hi[4];
   const int t = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = t * 128 + threadIdx.x;
-  if (t == 0 && b == 0 && threadIdx.x == 0) *q_bad = counters[0] = counters[1] = counters[2] = counters[3] = 0;
+  if (t == 0 && b == 0 && threadIdx.x == 0) *q_bad = counters[0] = counters[1] = counters[2] = 0;
   int lo = 0, hi = 0;
   if (i < d.Sq) {
     const ll at = static_cast<ll>(b) * d.Sq + i;
@@ -288,8 +288,11 @@ __global__ void key_bounds_kernel(Dims d, const int* __restrict__ starts, int n_
 // lse2 = lse log2(e) (+inf: the row sees nothing or does not exist; NaN: its q, dout or
 // forward result is not finite), delta = rowsum(dout out), *q_bad if q or dout is not finite.
 // PACKED: q and out come from their 8-bit checkpoints; q is written in bf16 to q_clean (zero
-// if the row is bad), out is only summed.
-template <bool PACKED>
+// if the row is bad), out is only summed. Otherwise q is read for its finiteness alone: with a
+// cap (CHECK_Q) always, else only where lse is not finite, because every score of a row whose q
+// is not finite is not finite, and so is its lse (a cap makes finite scores of infinite ones).
+// That leaves 2 of 7 bytes a value unread.
+template <bool PACKED, bool CHECK_Q>
 __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* __restrict__ q, const bf16* __restrict__ out,
                                                            const Packed q8, const Packed out8,
                                                            const bf16* __restrict__ dout,
@@ -309,6 +312,7 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
   float acc = 0.f;
   bool bad = false;
   uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
+  const float row_lse = in ? lse[(static_cast<ll>(b) * d.n_h + h) * d.Sq + i] : -INFINITY;
   if (in) {
     const uint4 g = reinterpret_cast<const uint4*>(dout + src * 128)[l16];
     uint4 a;
@@ -318,8 +322,10 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
       if (l16 < 8) q1 = unpack8_bf16x8(q8, src, 192, 16 + l16);
     } else {
       a = reinterpret_cast<const uint4*>(out + src * 128)[l16];
-      q0 = reinterpret_cast<const uint4*>(q + src * 192)[l16];
-      if (l16 < 8) q1 = reinterpret_cast<const uint4*>(q + src * 192)[16 + l16];
+      if (CHECK_Q || !finite(row_lse)) {
+        q0 = reinterpret_cast<const uint4*>(q + src * 192)[l16];
+        if (l16 < 8) q1 = reinterpret_cast<const uint4*>(q + src * 192)[16 + l16];
+      }
     }
     bad = bad_bf16x8(g) || bad_bf16x8(q0) || bad_bf16x8(q1);
     const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
   if (row < rows && l16 == 0) {
     float L = INFINITY, D = 0.f;
     if (in) {
-      const float v = lse[(static_cast<ll>(b) * d.n_h + h) * d.Sq + i];
+      const float v = row_lse;
       if (v == -INFINITY) {
         L = INFINITY;  // the row sees nothing: its weights are 0
       } else if (bad || !finite(v) || !finite(acc)) {
@@ -464,7 +470,7 @@ MaskBuffers mask_carve(const Dims& d, int elem, char*& p) {
   m.kt_count = reinterpret_cast<int*>(take(B * kt * 4));
   m.kt_list = reinterpret_cast<int*>(take(B * kt * nq64 * 4));
   m.q_bad = reinterpret_cast<int*>(take(4));
-  m.counters = reinterpret_cast<int*>(take(16));
+  m.counters = reinterpret_cast<int*>(take(12));
   m.work = reinterpret_cast<int4*>(take(B * (nq64 / 2) * 16));
   m.seen = reinterpret_cast<int*>(take(B * kt * 4));
   m.seen_list = reinterpret_cast<int*>(take(B * kt * 4));
@@ -520,16 +526,19 @@ LaunchResult mask_key_bounds(const Dims& d, const int* starts, int n_docs, const
 
 LaunchResult tc_mask_bwd_pre(const Dims& d, const bf16* q, const bf16* out, const Packed* q8, const Packed* out8,
                              const bf16* dout, const float* lse, const BwdWorkspace& w, bf16* q_clean,
-                             bf16* dout_clean, int* q_bad, cudaStream_t st) {
+                             bf16* dout_clean, int* q_bad, bool check_q, cudaStream_t st) {
   LaunchResult r;
   const ll rows = static_cast<ll>(d.B) * d.sq_pad * d.n_h;
   const unsigned grid = static_cast<unsigned>((rows + 15) / 16);
   if (q8)
-    mask_bwd_pre_kernel<true><<<grid, 256, 0, st>>>(d, nullptr, nullptr, *q8, *out8, dout, lse, w.lse2, w.delta, q_clean,
+    mask_bwd_pre_kernel<true, true><<<grid, 256, 0, st>>>(d, nullptr, nullptr, *q8, *out8, dout, lse, w.lse2, w.delta, q_clean,
                                                     q_bad);
+  else if (check_q)
+    mask_bwd_pre_kernel<false, true><<<grid, 256, 0, st>>>(d, q, out, Packed{}, Packed{}, dout, lse, w.lse2, w.delta,
+                                                           q_clean, q_bad);
   else
-    mask_bwd_pre_kernel<false><<<grid, 256, 0, st>>>(d, q, out, Packed{}, Packed{}, dout, lse, w.lse2, w.delta, q_clean,
-                                                     q_bad);
+    mask_bwd_pre_kernel<false, false><<<grid, 256, 0, st>>>(d, q, out, Packed{}, Packed{}, dout, lse, w.lse2, w.delta,
+                                                            q_clean, q_bad);
   r.err = cudaGetLastError();
   if (r.err == cudaSuccess) {
     mask_clean_kernel<<<2 * sm_count(), 256, 0, st>>>(static_cast<ll>(d.B) * d.Sq * d.n_h, q8 ? nullptr : q, dout,

@@ -56,6 +56,16 @@ laga_status check_mods(const laga_mla_mods* mods, ScoreMods* out) {
 
 int elem_size(const laga_mla_desc* desc) { return desc->dtype == LAGA_DTYPE_BF16 ? 2 : 4; }
 
+// Heads per dK/dV CTA: as in the plain backward, fewer where that would leave the 152 SMs fewer
+// than six CTAs each. Documents make CTAs of very different length, and a walk over four heads
+// of the longest sets the time (2 x 4096 rows of 16 heads, 5 documents: 184 us with four heads,
+// 158 with two, 150 with one; 2999 rows of 32 heads, 6 documents, capped: 182 and 119).
+int masked_heads_per_cta(const Dims& d) {
+  int G = dkdv_heads_per_cta(d.n_h);
+  while (G > 1 && static_cast<int64_t>(d.skv_pad / 128) * d.B * (d.n_h / G) < 6 * 152) G /= 2;
+  return G;
+}
+
 size_t tc_clean_q_bytes(const Dims& d) { return align_up(static_cast<size_t>(d.B) * d.Sq * d.n_h * 192 * 2, 256); }
 size_t tc_clean_dout_bytes(const Dims& d) { return align_up(static_cast<size_t>(d.B) * d.Sq * d.n_h * 128 * 2, 256); }
 
@@ -64,7 +74,7 @@ size_t fwd_bytes(const Dims& d, Path path, int elem) {
 }
 size_t bwd_bytes(const Dims& d, Path path, int elem) {
   return path == Path::Simt ? simt_masked_bwd_workspace(d, elem)
-                            : tc_bwd_workspace(d) + mask_bytes(d, elem) + tc_clean_q_bytes(d) + tc_clean_dout_bytes(d);
+                            : tc_bwd_workspace(d, masked_heads_per_cta(d)) + mask_bytes(d, elem) + tc_clean_q_bytes(d) + tc_clean_dout_bytes(d);
 }
 
 bool workspace_ok(const void* ws, size_t have, size_t need) {
@@ -187,10 +197,11 @@ laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* 
   // K, V and the mask's buffers where the forward has them, then the rest of the plain layout
   char* at = static_cast<char*>(workspace) + tc_fwd_workspace(d);
   const MaskBuffers m = mask_carve(d, elem, at);
-  BwdWorkspace w = tc_bwd_carve(d, at - tc_fwd_workspace(d));
+  const int G = masked_heads_per_cta(d);
+  BwdWorkspace w = tc_bwd_carve(d, at - tc_fwd_workspace(d), G);
   w.k_ws = static_cast<bf16*>(workspace);
   w.v_ws = w.k_ws + static_cast<size_t>(d.B) * d.skv_pad * d.n_h * 128;
-  at += tc_bwd_workspace(d) - tc_fwd_workspace(d);
+  at += tc_bwd_workspace(d, G) - tc_fwd_workspace(d);
   bf16* q_clean = reinterpret_cast<bf16*>(at);
   bf16* dout_clean = reinterpret_cast<bf16*>(at + tc_clean_q_bytes(d));
   const MaskArgs mask{m.meta(), sm};
@@ -206,7 +217,7 @@ laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* 
   if (r.ok())
     r = timed("masked_bwd_pre", s, [&] {
       return tc_mask_bwd_pre(d, cb(q), cb(out), packed ? &pq : nullptr, packed ? &po : nullptr, cb(dout), lse, w, q_clean,
-                             dout_clean, m.q_bad, s);
+                             dout_clean, m.q_bad, sm.cap > 0.f, s);
     });
   if (r.ok())
     r = timed("masked_attn_bwd_dkdv", s,

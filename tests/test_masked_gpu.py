@@ -186,8 +186,12 @@ def test_without_mods_is_the_plain_attention():
     x, dout = inputs(2, 300, 700, 4, DSV3, torch.bfloat16, 6)
     got = check(x, dout, q_offset=400)
     g = laga.bwd(*x.values(), got["out"], got["lse"], dout, q_offset=400)
-    for k in GRADS:
+    for k in set(GRADS) - {"dk_rope"}:
         assert torch.equal(got[k], g[k]), k
+    # the heads of dk_rope are summed in fp32 in other groups: 2^-22 of the summands, then one rounding to
+    # bf16 that may fall on the other side (a step, 2^-7)
+    a, b = got["dk_rope"].float(), g["dk_rope"].float()
+    assert bool(((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -20 * b.abs().max()).all())
     again = step(x, dout, q_offset=400)
     for k in got:
         assert torch.equal(got[k], again[k]), k
