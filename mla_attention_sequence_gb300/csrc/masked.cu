@@ -33,6 +33,10 @@ Path masked_plan(const laga_mla_desc* desc, Dims* d, laga_status* st, bool for_b
     *st = fail(LAGA_ERR_UNSUPPORTED, "masked attention supports d_nope + d_rope <= 256 and d_v <= 256%s");
     return Path::Invalid;
   }
+  if (path == Path::Simt && static_cast<int64_t>(d->B) * d->S >= (int64_t(1) << 31)) {
+    *st = fail(LAGA_ERR_UNSUPPORTED, "problem too large%s");
+    return Path::Invalid;
+  }
   if (d->B > 65535 || d->n_h > 65535 ||
       static_cast<int64_t>(d->B) * d->n_h * (d->sq_pad / 128) >= (int64_t(1) << 31) - 65536) {
     *st = fail(LAGA_ERR_UNSUPPORTED, "problem too large%s");

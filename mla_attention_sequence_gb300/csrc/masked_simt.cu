@@ -7,12 +7,14 @@
 // units, so the 16 threads that read 16 consecutive rows as float4 touch different banks.
 // Thread (tx, ty) of 16 x 16 owns tile rows RI ty .. RI ty + RI - 1 and, of the score tile,
 // columns tx, tx + 16, ...; of a head-wide accumulator, columns 64 c + 4 tx .. + 3.
-// N = ceil(widest head / 64) picks the accumulator's width, RI the rows: 4 gives the most
-// multiply-adds per shared-memory load (64 per 8 16-byte loads in the 64 x 64 product), but a
-// problem of a few hundred rows then fills a tenth of the SMs, each walking its keys alone;
-// RI = 1 gives four times the CTAs (measured at 256 rows, 4 heads: RI_NUMBERS).
-// A tile's global loads are issued eight rows deep per warp, lanes along the width; one
-// value at a time cost 14 us per key step.
+// N = ceil(widest head / 64) picks the accumulator's width, RI the rows. More rows a thread
+// mean more multiply-adds per shared-memory load, fewer mean more CTAs, and a problem of a few
+// hundred rows fills few SMs, each walking its keys alone. Measured forward / backward, us:
+//   256 rows x 4 heads, d 48 / 32       RI 1: 39 / 54    2: 42 / 59     4: 50 / 76
+//   2 x 1024 x 6, d 64 / 56             RI 1: 156 / 340  2: 136 / 285   4: 144 / 316
+//   4096 x 8, d 96 / 96                                  2: 3127 / 5542 4: 1964 / 6754
+// A tile's global loads are issued eight rows deep per warp, lanes along the width, and where
+// the registers allow it a step ahead; one value at a time cost 14 us per key step.
 #include "mask.h"
 
 #include <algorithm>
@@ -265,7 +267,7 @@ __device__ __forceinline__ float half_warp_sum(float v) {
   return v;
 }
 
-// out and lse of 64 query rows of one head.
+// out and lse of 16 RI query rows of one head.
 template <int N, int RI>
 __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
   constexpr int ROWS = 16 * RI;
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
   }
 }
 
-// dq of 64 query rows of one head.
+// dq of 16 RI query rows of one head.
 template <int N, int RI>
 __device__ __forceinline__ void masked_simt_dq(const SimtParams& p, int t) {
   constexpr int ROWS = 16 * RI;
@@ -448,7 +450,7 @@ __device__ __forceinline__ void masked_simt_dq(const SimtParams& p, int t) {
   }
 }
 
-// dK (both parts) and dV of 64 keys of one head.
+// dK (both parts) and dV of 16 RI keys of one head.
 template <int N, int RI>
 __device__ __forceinline__ void masked_simt_dkv(const SimtParams& p, int t) {
   constexpr int ROWS = 16 * RI;
@@ -616,10 +618,12 @@ SimtParams params(const Dims& d, bool is_bf16, const ScoreMods& mods, const Ws& 
   return p;
 }
 
-// Rows per thread: 4 unless that leaves CTAs for fewer than two per SM (1: four times as many).
-int rows_per_thread(const Dims& d, int rows) {
-  const ll ctas = static_cast<ll>((rows + 63) / 64) * d.n_h * d.B;
-  return ctas >= 2 * sm_count() ? 4 : 2 * ctas >= 2 * sm_count() ? 2 : 1;
+// Rows per thread, by the CTAs that gives: two once 32-row tiles fill the SMs, four (forward only)
+// once 64-row tiles fill them twice.
+int rows_per_thread(const Dims& d, int rows, bool bwd) {
+  const ll ctas = static_cast<ll>((rows + 63) / 64) * d.n_h * d.B;  // of 64 rows
+  if (!bwd && ctas >= 2 * sm_count()) return 4;
+  return 2 * ctas >= sm_count() ? 2 : 1;
 }
 
 template <bool BWD, int N, int RI>
@@ -647,11 +651,10 @@ cudaError_t launch_rows(const Dims& d, const SimtParams& p, cudaStream_t st) {
 
 template <bool BWD>
 cudaError_t launch(const Dims& d, const SimtParams& p, cudaStream_t st) {
-  switch (rows_per_thread(d, BWD ? d.Sq + d.S : d.Sq)) {
-    case 4: return launch_rows<BWD, 4>(d, p, st);
-    case 2: return launch_rows<BWD, 2>(d, p, st);
-    default: return launch_rows<BWD, 1>(d, p, st);
-  }
+  const int ri = rows_per_thread(d, BWD ? d.Sq + d.S : d.Sq, BWD);
+  if constexpr (!BWD)
+    if (ri == 4) return launch_rows<BWD, 4>(d, p, st);
+  return ri == 2 ? launch_rows<BWD, 2>(d, p, st) : launch_rows<BWD, 1>(d, p, st);
 }
 
 // ---- the rebuild's products: C[m][n] = sum over one or two pairs of A(m, k) B(k, n), any
@@ -659,7 +662,8 @@ cudaError_t launch(const Dims& d, const SimtParams& p, cudaStream_t st) {
 // of 64 threads each take every fourth block of 16 k, and their sums are added in a fixed
 // order through shared memory. These products are small (a weight gradient is d_c x n_h d
 // with k = all keys): a few dozen tiles, so the k loop's latency is the time, and both the
-// small tile and the split shorten it (72 x 120 with k = 1018: GEMM_NUMBERS).
+// small tile and the split shorten it (2 x 509 keys of width 72, 3 heads: the three gradients in
+// 31 us, where 64 x 64 tiles without the split took 182 for each dW).
 struct GemmPair {
   const void *a, *b;
   bool a_bf16, b_bf16;

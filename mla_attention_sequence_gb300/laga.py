@@ -476,6 +476,8 @@ def rope(q, k_rope, pos, sections=None, theta: float = 10000.0, interleaved: boo
         q_out = torch.empty(shape, dtype=dt, device=dev)
     if k_out is None:
         k_out = torch.empty(k_shape, dtype=dt, device=dev)
+    if shape[0] * shape[1] * shape[2] == 0:  # no tokens (or heads): nothing turns
+        return q_out, k_out
     d = _rope_desc(shape, d_rope, sections, float(theta), bool(interleaved), bool(inverse), pos.dtype == torch.int64,
                    code)
     _launch(dev, lib().laga_mla_rope, d, at, src, k_src, _expect("q_out", q_out, shape, (dt,), dev),

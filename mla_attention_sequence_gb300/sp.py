@@ -125,6 +125,31 @@ def _local_bwd_default(q, c_kv, k_rope, W_UK, W_UV, out, lse, dout, q_offset, ca
                     q_offset2=q_offset2)
 
 
+def packed_document_ops(doc_starts, prefix=None, window: int = 0, softcap: float = 0.0, slopes=None):
+    """(local_fwd, local_bwd) for SPAttention on packed documents: the library's masked attention with
+    each rank's rows seeing the keys of their own document (laga.key_bounds of doc_starts [B, n_docs + 1],
+    prefix, window, at the rank's positions in the gathered sequence), capped scores and a bias by
+    distance as in laga.masked_fwd. doc_starts counts positions of the whole sequence and is the same on
+    every rank."""
+    def mods(q, c_kv, q_offset, causal, q_split, q_offset2):
+        from . import laga
+        lo, hi = laga.key_bounds(doc_starts, q.shape[1], q_offset=q_offset, prefix=prefix, window=window,
+                                 skv=c_kv.shape[1], q_split=q_split, q_offset2=q_offset2)
+        return dict(key_lo=lo, key_hi=hi, softcap=softcap, slopes=slopes, q_offset=q_offset,
+                    causal=causal and prefix is None, q_split=q_split, q_offset2=q_offset2)
+
+    def local_fwd(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, q_split, q_offset2):
+        from . import laga
+        return laga.masked_fwd(q, c_kv, k_rope, W_UK, W_UV, **mods(q, c_kv, q_offset, causal, q_split, q_offset2))
+
+    def local_bwd(q, c_kv, k_rope, W_UK, W_UV, out, lse, dout, q_offset, causal, q_split, q_offset2):
+        from . import laga
+        return laga.masked_bwd(q, c_kv, k_rope, W_UK, W_UV, out, lse, dout,
+                               **mods(q, c_kv, q_offset, causal, q_split, q_offset2))
+
+    return local_fwd, local_bwd
+
+
 class SPAttention:
     """One LAGA attention block's forward and backward over an SP process group.
 

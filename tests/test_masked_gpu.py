@@ -497,6 +497,42 @@ def test_two_calls_at_once():
             assert torch.equal(got[i][k], want[i][k]), k
 
 
+@pytest.mark.parametrize("kind", ["contiguous", "zigzag"])
+def test_sequence_parallel_ranks_of_packed_documents(kind):
+    """Each rank's local step, one after the other: their rows make up the whole sequence's out and dq,
+    their latent and weight gradients add up to its (each rounded to bf16 once more: 2^-8)."""
+    from mla_attention_sequence_gb300 import sp
+    B, S, n_h = 2, 1024, 4
+    x, dout = inputs(B, S, S, n_h, DSV3, torch.bfloat16, 22)
+    st = torch.tensor([[0, 100, 700, 1000], [10, 333, 512, 1024]], dtype=torch.int32, device=dev())
+    fwd, bwd = sp.packed_document_ops(st, window=300, softcap=20.0, slopes=slopes(n_h))
+    lo, hi = laga.key_bounds(st, S, window=300)
+    want = check(x, dout, key_lo=lo, key_hi=hi, softcap=20.0, slopes=slopes(n_h))
+    layout = sp.Layout(S, 4, kind)
+    sums = {k: torch.zeros(want[k].shape, device=dev()) for k in GRADS[1:]}
+    for r in range(4):
+        rows = layout.rows(r).to(dev())
+        a = layout.query_args(r)
+        args = (x["q"][:, rows].contiguous(), *list(x.values())[1:])
+        at = (a["q_offset"], True, a["q_split"], a["q_offset2"])
+        out, lse = fwd(*args, *at)
+        g = bwd(*args, out, lse, dout[:, rows].contiguous(), *at)
+        for got, full in ((out, want["out"][:, rows]), (g["dq"], want["dq"][:, rows])):
+            assert float((got.double() - full.double()).norm()) <= 2.0 ** -8 * float(full.double().norm())
+        for k in sums:
+            sums[k] += g[k].float()
+    for k, v in sums.items():
+        assert float((v.double() - want[k].double()).norm()) <= 3 * 2.0 ** -8 * float(want[k].double().norm()), k
+
+
+@pytest.mark.parametrize("which", ["rows", "heads"])
+def test_rope_of_nothing(which):
+    q = torch.empty(1, 0, 2, 8, device=dev()) if which == "rows" else torch.empty(0, 3, 2, 8, device=dev())
+    k = torch.empty(q.shape[0], q.shape[1], 4, device=dev())
+    a, b = laga.rope(q, k, torch.zeros(1, *q.shape[:2], dtype=torch.int32, device=dev()))
+    assert a.shape == q.shape and b.shape == k.shape
+
+
 def test_argument_checks():
     x, dout = inputs(1, 8, 8, 2, (16, 8, 4, 8), torch.float32)
     lo = torch.zeros(1, 8, dtype=torch.int32, device=dev())
