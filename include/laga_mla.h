@@ -251,7 +251,8 @@ laga_status laga_mla_absorbed_fwd(const laga_mla_desc* desc, const void* q, cons
  * Non-finite values in masked places do no harm: a key that no row sees may hold
  * infinities or NaN, and so may the q and dout of a row that sees nothing. A row that
  * sees a key whose latent or RoPE key is not finite gets NaN (out and lse); a key that
- * is seen by such a row, or by one whose q or dout is not finite, gets NaN gradients. */
+ * is seen by such a row, or by one whose q or dout is not finite, gets NaN gradients. A row
+ * whose scores are all -inf (an infinite q) gets NaN as well. */
 typedef struct {
   const int32_t* key_lo; /* [B, Sq], device; NULL: 0 */
   const int32_t* key_hi; /* [B, Sq], device, one past the last visible key; NULL: skv */
@@ -293,8 +294,9 @@ laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* 
 /* key_lo, key_hi [B, Sq] of packed documents. Document k of batch element b holds the keys
  * [doc_starts[b][k], doc_starts[b][k + 1]) (doc_starts [B, n_docs + 1], ascending; repeated
  * entries are empty documents). A row at position p of document k sees the keys of k up to p,
- * at most the last `window` of them (0: all), and, with prefix [B, n_docs], every key of the
- * document's first prefix[b][k] (pass causal = 0 to the attention then). A row in no document
+ * at most the last `window` of them (0: all), or, with prefix [B, n_docs], every key of the
+ * document's first prefix[b][k] too (pass causal = 0 to the attention then; prefix and a window
+ * together are refused: what a row sees would not be one interval). A row in no document
  * (before the first, at or past the last end) sees nothing. Positions as in laga_mla_desc
  * (q_offset, q_split, q_offset2); skv clamps. Device pointers, 4-byte aligned. */
 laga_status laga_mla_key_bounds(int64_t batch, int64_t sq, int64_t skv, int64_t q_offset, int64_t q_split,

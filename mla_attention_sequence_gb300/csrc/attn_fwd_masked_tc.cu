@@ -661,8 +661,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!wait_warp(&pv_done[last_g % NBUF], (last_g / NBUF) & 1, abort_flag, 319)) { ok = false; break; }
         tc_fence_after();
         const uint32_t o_addr = tmem + COL_O + lane_off;
-        // a row that sees nothing: out = 0, lse = -inf; one that sees a non-finite key: NaN
-        const float inv = poisoned ? NAN : l_run == 0.f ? 0.f : 1.f / l_run;
+        // a row that sees nothing: out = 0, lse = -inf; one that sees a non-finite key, or whose
+        // scores are all -inf (an infinite q): NaN
+        const bool bad = poisoned || (lo < hi && l_run == 0.f);
+        const float inv = bad ? NAN : l_run == 0.f ? 0.f : 1.f / l_run;
         uint32_t o[64];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free);  // the next item's PV may overwrite O
         if (q_row < p.Sq) {
-          const float lse = poisoned ? NAN : l_run == 0.f ? -INFINITY : (m + __log2f(l_run)) * 0.6931471805599453f;
+          const float lse = bad ? NAN : l_run == 0.f ? -INFINITY : (m + __log2f(l_run)) * 0.6931471805599453f;
           p.lse[(static_cast<long long>(b) * p.n_h + h) * p.Sq + q_row] = lse;
         }
         // the warp's 32 rows as four [32 rows][64 B] boxes (64-byte swizzle) through its buffer and

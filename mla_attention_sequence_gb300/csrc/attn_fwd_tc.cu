@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const uint32_t o_addr = tmem + COL_O + lane_off;
       float inv = 1.f / l_run;
       if constexpr (MASKED) {
+        if (lo < hi && l_run == 0.f) poisoned = true;  // all its scores are -inf (an infinite q)
         if (l_run == 0.f) inv = 0.f;  // the row sees nothing: out = 0, lse = -inf
         if (poisoned) inv = NAN;
       }

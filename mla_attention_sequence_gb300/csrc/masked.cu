@@ -252,6 +252,8 @@ laga_status laga_mla_key_bounds(int64_t batch, int64_t sq, int64_t skv, int64_t 
   if (batch < 1 || sq < 1 || skv < 1 || n_docs < 1 || q_offset < 0 || q_split < 0 || q_split >= sq || window < 0 ||
       (q_split > 0 && q_offset2 < 0))
     return fail(LAGA_ERR_INVALID_ARG, "key bounds: batch, sq, skv, n_docs >= 1, 0 <= q_split < sq, offsets and window >= 0%s");
+  if (prefix && window > 0)
+    return fail(LAGA_ERR_INVALID_ARG, "key bounds: a prefix outside the window is no interval; give one of the two%s");
   if (batch > 65535 || sq >= lim || skv >= lim || n_docs >= lim || q_offset >= lim || (q_split > 0 && q_offset2 >= lim))
     return fail(LAGA_ERR_UNSUPPORTED, "problem too large%s");
   for (const void* p : {static_cast<const void*>(doc_starts), static_cast<const void*>(key_lo),

@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
     if (i0 + i >= d.Sq) continue;
     float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
     float L = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
-    if (poisoned[i]) inv = L = NAN;
+    if (poisoned[i] || (lo[i] < hi[i] && l[i] == 0.f)) inv = L = NAN;  // l = 0: an infinite q, all scores -inf
     const ll row = (static_cast<ll>(b) * d.Sq + i0 + i) * d.n_h + h;
 #pragma unroll
     for (int c = 0; c < N; ++c) {

@@ -366,8 +366,9 @@ def key_bounds(doc_starts, n_rows: int, q_offset: int = 0, prefix=None, window: 
 
     doc_starts: int32 [B, n_docs + 1], ascending; document k holds the keys [doc_starts[k],
     doc_starts[k + 1]). A row sees the keys of its own document up to its position, at most
-    the last `window` of them (0: all), and, with prefix (int32 [B, n_docs]), all of the
-    document's first prefix[k] keys (call the attention with causal=False then). Rows in no
+    the last `window` of them (0: all), or, with prefix (int32 [B, n_docs]), also all of the
+    document's first prefix[k] keys (call the attention with causal=False then; not together
+    with a window). Rows in no
     document see nothing. skv clamps the bounds (None: only the documents do)."""
     shape = doc_starts.shape
     if len(shape) != 2 or shape[1] < 2:
@@ -476,12 +477,12 @@ def rope(q, k_rope, pos, sections=None, theta: float = 10000.0, interleaved: boo
         q_out = torch.empty(shape, dtype=dt, device=dev)
     if k_out is None:
         k_out = torch.empty(k_shape, dtype=dt, device=dev)
-    if shape[0] * shape[1] * shape[2] == 0:  # no tokens (or heads): nothing turns
+    q_at, k_at = _expect("q_out", q_out, shape, (dt,), dev), _expect("k_out", k_out, k_shape, (dt,), dev)
+    if shape[0] * shape[1] == 0:  # no tokens: nothing turns
         return q_out, k_out
     d = _rope_desc(shape, d_rope, sections, float(theta), bool(interleaved), bool(inverse), pos.dtype == torch.int64,
                    code)
-    _launch(dev, lib().laga_mla_rope, d, at, src, k_src, _expect("q_out", q_out, shape, (dt,), dev),
-            _expect("k_out", k_out, k_shape, (dt,), dev))
+    _launch(dev, lib().laga_mla_rope, d, at, src, k_src, q_at, k_at)
     return q_out, k_out
 
 

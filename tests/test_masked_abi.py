@@ -95,7 +95,7 @@ def test_key_bounds_refusals(L):
         return L.laga_mla_key_bounds(*{**ok, **kw}.values(), None)
     for kw in (dict(B=0), dict(sq=0), dict(skv=0), dict(docs=0), dict(off=-1), dict(split=8), dict(split=-1),
                dict(split=4, off2=-1), dict(window=-1), dict(starts=None), dict(lo=None), dict(hi=P + 1),
-               dict(prefix=P + 2)):
+               dict(prefix=P + 2), dict(prefix=P, window=4)):
         assert call(**kw) == 1, kw
     assert call(B=1 << 20) == 2
     assert call(sq=1 << 31) == 2

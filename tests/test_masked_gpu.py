@@ -241,6 +241,26 @@ def test_non_finite_values_in_masked_places(dtype, dims, value):
         assert got["dq"][row].isnan().all() and torch.equal(got["dq"][~row], clean["dq"][~row])
 
 
+@pytest.mark.parametrize("dtype,dims,S", [(torch.bfloat16, DSV3, 130), (torch.bfloat16, DSV3, 8192),
+                                          (torch.float32, (32, 16, 8, 24), 130)])
+def test_scores_that_are_all_minus_infinity(dtype, dims, S):
+    """A row that sees one key, with an infinite q whose product with it is -inf: exp(-inf + inf), a NaN,
+    and not the zero of a row that sees nothing."""
+    x, dout = inputs(1, 130, S, 2, dims, dtype, 9)
+    x["k_rope"][0, 0, 0] = -1.0
+    clean = step(x, dout)
+    y = {k: v.clone() for k, v in x.items()}
+    y["q"][0, 0, 1, dims[1]] = math.inf
+    got = step(y, dout)
+    row = torch.zeros(1, 130, 2, dtype=torch.bool, device=dev())
+    row[0, 0, 1] = True
+    for k in ("out", "dq"):
+        assert got[k][row].isnan().all() and torch.equal(got[k][~row], clean[k][~row]), k
+    assert got["lse"][0, 1, 0].isnan() and got["lse"].isnan().sum() == 1
+    for k in ("dc_kv", "dk_rope"):
+        assert got[k][0, 0].isnan().all() and torch.equal(got[k][0, 1:], clean[k][0, 1:]), k
+
+
 def test_large_scores_and_far_bias():
     """Scores of a few hundred, a bias that leaves one key: the weights stay those of the definition."""
     x, dout = inputs(1, 150, 300, 2, (16, 8, 4, 8), torch.float32, 8)
