@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int first1 = p.q_split > 0 ? seg_tiles + (p.causal ? min(nq - seg_tiles, max(0, kv0 - p.q_offset2) / BQ) : 0)
                                    : nq;
   const int n0 = seg_tiles - first0;
+  if constexpr (MASKED) after_previous();
   const int kt_index = b * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
   const int n_qt = MASKED ? p.kt_count[kt_index] : n0 + (nq - first1);
   const int* kt_list = MASKED ? p.kt_list + static_cast<long long>(kt_index) * (p.sq_pad / BQ) : nullptr;
@@ -850,8 +851,13 @@ LaunchResult tc_attn_bwd_dkdv(const Dims& d, const bf16* q, const bf16* k_rope, 
     r.what = "cudaFuncSetAttribute(attn_bwd_dkdv)";
     return r;
   }
-  kern<<<dim3(d.skv_pad / BKV, p.n_hg, d.B), NTHREADS, smem, st>>>(mQ, mK, mR, mV, mdO, mdK, mdV, mdKR, mQc, mdOc, p);
-  r.err = cudaGetLastError();
+  const dim3 grid(d.skv_pad / BKV, p.n_hg, d.B);
+  if (mask) {
+    r.err = launch_next(kern, grid, NTHREADS, smem, st, mQ, mK, mR, mV, mdO, mdK, mdV, mdKR, mQc, mdOc, p);
+  } else {
+    kern<<<grid, NTHREADS, smem, st>>>(mQ, mK, mR, mV, mdO, mdK, mdV, mdKR, mQc, mdOc, p);
+    r.err = cudaGetLastError();
+  }
   if (r.err != cudaSuccess) r.what = "attn_bwd_dkdv_kernel launch";
   return r;
 }

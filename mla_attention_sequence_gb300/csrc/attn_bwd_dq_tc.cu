@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   constexpr bool CAP = MASKED && (MOD & kModCap) != 0, BIAS = MASKED && (MOD & kModBias) != 0;
   int n_kv, j0 = 0;  // key tiles walked: [j0, j0 + n_kv)
   if constexpr (MASKED) {
+    after_previous();
     const int4 w = p.work[b * p.n_q_tiles + blockIdx.x];
     t = w.x;
     j0 = w.y;
@@ -591,8 +592,13 @@ LaunchResult tc_attn_bwd_dq(const Dims& d, const bf16* q, const bf16* k_rope, co
     r.what = "cudaFuncSetAttribute(attn_bwd_dq)";
     return r;
   }
-  kern<<<dim3(p.n_q_tiles, d.n_h, d.B), NTHREADS, SMEM_BYTES, st>>>(mQ, mK, mR, mV, mdQ, p);
-  r.err = cudaGetLastError();
+  const dim3 grid(p.n_q_tiles, d.n_h, d.B);
+  if (mask) {
+    r.err = launch_next(kern, grid, NTHREADS, SMEM_BYTES, st, mQ, mK, mR, mV, mdQ, p);
+  } else {
+    kern<<<grid, NTHREADS, SMEM_BYTES, st>>>(mQ, mK, mR, mV, mdQ, p);
+    r.err = cudaGetLastError();
+  }
   if (r.err != cudaSuccess) r.what = "attn_bwd_dq_kernel launch";
   return r;
 }

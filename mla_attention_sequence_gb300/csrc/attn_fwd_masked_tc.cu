@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  after_previous();
 
   // Item i from the ring, by a whole warp; `last`: this reader is done with the slot.
   auto warp_item = [&](int i, Item& it, bool last, int where) -> bool {
@@ -775,8 +776,7 @@ LaunchResult tc_masked_attn_fwd(const Dims& d, const MaskArgs& mask, const bf16*
     r.what = "cudaFuncSetAttribute(attn_fwd_masked)";
     return r;
   }
-  kern<<<std::min(p.total, sm_count()), NTHREADS, SMEM_BYTES, st>>>(mQ, mK, mR, mV, mO, p);
-  r.err = cudaGetLastError();
+  r.err = launch_next(kern, std::min(p.total, sm_count()), NTHREADS, SMEM_BYTES, st, mQ, mK, mR, mV, mO, p);
   if (r.err != cudaSuccess) r.what = "attn_fwd_masked_kernel launch";
   return r;
 }

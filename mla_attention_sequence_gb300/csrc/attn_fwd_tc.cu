@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int b = blockIdx.z;
   int n_kv, j0 = 0;  // key tiles walked: [j0, j0 + n_kv)
   if constexpr (MASKED) {
+    after_previous();
     const int4 w = p.work[b * p.n_q_tiles + blockIdx.x];
     t = w.x;
     j0 = w.y;
@@ -571,8 +572,13 @@ LaunchResult tc_attn_fwd(const Dims& d, const bf16* q, const bf16* k_ws, const b
     r.what = "cudaFuncSetAttribute(attn_fwd)";
     return r;
   }
-  kern<<<dim3(p.n_q_tiles, d.n_h, d.B), NTHREADS, SMEM_BYTES, st>>>(mQ, mK, mR, mV, mO, p);
-  r.err = cudaGetLastError();
+  const dim3 grid(p.n_q_tiles, d.n_h, d.B);
+  if (mask) {
+    r.err = launch_next(kern, grid, NTHREADS, SMEM_BYTES, st, mQ, mK, mR, mV, mO, p);
+  } else {
+    kern<<<grid, NTHREADS, SMEM_BYTES, st>>>(mQ, mK, mR, mV, mO, p);
+    r.err = cudaGetLastError();
+  }
   if (r.err != cudaSuccess) r.what = "attn_fwd_kernel launch";
   return r;
 }

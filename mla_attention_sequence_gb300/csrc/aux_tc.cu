@@ -103,10 +103,12 @@ __global__ void bwd_pre_kernel(Dims d, const bf16* __restrict__ out, const bf16*
 
 // dk_rope[b, j, :] = sum_g dkr[b, j, g, :] over the dK/dV kernel's head-group
 // partials; 16 threads x 4 columns per row.
-// seen (masked attention): whether key tile b * (skv_pad / 128) + tile was walked; the partials of
-// the others were not written.
+// MASKED: seen says whether key tile b * (skv_pad / 128) + tile was walked; the partials of the
+// others were not written, nor will their rows of dc_kv be: both get zeros here.
+template <bool MASKED>
 __global__ void rope_sum_kernel(Dims d, int parts, const float* __restrict__ dkr, bf16* __restrict__ dk_rope,
-                                const int* __restrict__ seen) {
+                                const int* __restrict__ seen, bf16* __restrict__ dc_kv) {
+  if constexpr (MASKED) after_previous();
   const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const long long total = static_cast<long long>(d.B) * d.S * 16;
   if (t >= total) return;
@@ -115,7 +117,15 @@ __global__ void rope_sum_kernel(Dims d, int parts, const float* __restrict__ dkr
   const int j = static_cast<int>(bj % d.S);
   const int b = static_cast<int>(bj / d.S);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (j < d.skv_pad && (!seen || seen[b * (d.skv_pad / 128) + j / 128])) {
+  bool walked = j < d.skv_pad;
+  if constexpr (MASKED) {
+    walked = walked && seen[b * (d.skv_pad / 128) + j / 128] != 0;
+    if (!walked) {
+      uint4* row = reinterpret_cast<uint4*>(dc_kv + bj * d.d_c);
+      for (int k = c4; k < d.d_c / 8; k += 16) row[k] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  if (walked) {
     const float4* src =
         reinterpret_cast<const float4*>(dkr + ((static_cast<long long>(b) * d.skv_pad + j) * parts) * 64) + c4;
     for (int g = 0; g < parts; ++g) {
@@ -144,12 +154,17 @@ LaunchResult tc_bwd_pre(const Dims& d, const bf16* out, const bf16* dout, const 
   return r;
 }
 
-LaunchResult tc_bwd_post(const Dims& d, const BwdWorkspace& w, bf16* dk_rope, cudaStream_t st, const int* seen) {
+LaunchResult tc_bwd_post(const Dims& d, const BwdWorkspace& w, bf16* dk_rope, cudaStream_t st, const int* seen,
+                         bf16* dc_kv) {
   LaunchResult r;
   const long long t = static_cast<long long>(d.B) * d.S * 16;
-  rope_sum_kernel<<<static_cast<unsigned>((t + 255) / 256), 256, 0, st>>>(d, d.n_h / w.G,
-                                                                          w.dkr_ws, dk_rope, seen);
-  r.err = cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>((t + 255) / 256);
+  if (seen) {
+    r.err = launch_next(rope_sum_kernel<true>, grid, 256, 0, st, d, d.n_h / w.G, w.dkr_ws, dk_rope, seen, dc_kv);
+  } else {
+    rope_sum_kernel<false><<<grid, 256, 0, st>>>(d, d.n_h / w.G, w.dkr_ws, dk_rope, nullptr, nullptr);
+    r.err = cudaGetLastError();
+  }
   if (r.err != cudaSuccess) r.what = "bwd post kernels";
   return r;
 }

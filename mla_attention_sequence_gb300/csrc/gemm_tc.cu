@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(224, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if constexpr (LIST) after_previous();
 
   static_assert(!LIST || ((MODE == DCKV || MODE == DW) && (MODE == DW || MH == 1)), "listed key tiles");
   const int keys = LIST ? *p.key_count : 0;
@@ -495,6 +496,7 @@ __global__ void __launch_bounds__(224, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if constexpr (LIST) after_previous();
 
   // this CTA's contiguous tile range; the latent tile of tile t is key = t / n_tiles
   const int num_tiles = LIST ? *p.key_count * p.n_tiles : p.m_tiles * p.n_tiles * p.batches;
@@ -713,8 +715,12 @@ LaunchResult launch_gemm(const CUtensorMap& a0, const CUtensorMap& a1, const CUt
   const int grid = std::min(tiles, sm_count());
   GemmParams pp = p;
   pp.status = device_status_ptr();
-  kern<<<grid, 224, C::SMEM, st>>>(a0, a1, b0, b1, o0, o1, pp);
-  r.err = cudaGetLastError();
+  if constexpr (LIST) {
+    r.err = launch_next(kern, grid, 224, C::SMEM, st, a0, a1, b0, b1, o0, o1, pp);
+  } else {
+    kern<<<grid, 224, C::SMEM, st>>>(a0, a1, b0, b1, o0, o1, pp);
+    r.err = cudaGetLastError();
+  }
   if (r.err != cudaSuccess) r.what = "gemm_tc_kernel launch";
   return r;
 }
@@ -811,8 +817,13 @@ LaunchResult tc_recon_fwd(const Dims& d, const bf16* c_kv, const bf16* W_UK, con
     p.key_count = list->count;
     p.kt = p.m_tiles;
   }
-  kern<<<std::min(tiles, sm_count()), 224, TL_SMEM, st>>>(a0, b0, b1, o0, o1, p);
-  r.err = cudaGetLastError();
+  const int grid = std::min(tiles, sm_count());
+  if (list) {
+    r.err = launch_next(kern, grid, 224, TL_SMEM, st, a0, b0, b1, o0, o1, p);
+  } else {
+    kern<<<grid, 224, TL_SMEM, st>>>(a0, b0, b1, o0, o1, p);
+    r.err = cudaGetLastError();
+  }
   if (r.err != cudaSuccess) r.what = "recon_tmem_a_kernel launch";
   return r;
 }

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
+#include <utility>
 
 namespace laga {
 
@@ -30,6 +31,31 @@ struct LaunchResult {
   const char* what = nullptr;
   bool ok() const { return err == cudaSuccess && cu == CUDA_SUCCESS; }
 };
+
+// The masked calls are chains of short kernels. Each is launched while the one before it still
+// runs (a programmatic dependent launch), sets itself up, and calls after_previous() before it
+// touches global memory; the call returns when every earlier kernel of the chain has ended and
+// its writes are visible, and lets the next one start.
+template <class... P, class... A>
+cudaError_t launch_next(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, std::forward<A>(args)...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void after_previous() {
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+}
+#endif
 
 // Device address of this device's status word (timeouts of bounded waits);
 // nullptr if it cannot be resolved.
@@ -155,7 +181,7 @@ LaunchResult tc_attn_bwd_dq(const Dims& d, const bf16* q, const bf16* k_rope, co
                             const BwdWorkspace& w, bf16* dq, cudaStream_t st, const MaskArgs* mask = nullptr);
 // dk_rope = sum over heads of the per-head RoPE-key gradients.
 LaunchResult tc_bwd_post(const Dims& d, const BwdWorkspace& w, bf16* dk_rope, cudaStream_t st,
-                         const int* seen = nullptr);
+                         const int* seen = nullptr, bf16* dc_kv = nullptr);
 
 // ---- the absorbed MLA form (for comparison; bf16, the tensor-core dims).
 // q_lat [B*Sq][n_h*d_c] = per head q_nope_h W_UK_h^T

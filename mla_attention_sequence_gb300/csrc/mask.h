@@ -44,6 +44,19 @@ __device__ __forceinline__ float unpack8_value(const Packed& p, long long row, i
   const int blocks = (cols + kPackBlock - 1) / kPackBlock;
   return e4m3x2_to_float2(p.codes[row * cols + k]).x * scale_value(p.scales[row * blocks + k / kPackBlock]);
 }
+
+// Whether one of the keys [lo, hi) has its bit set: words step by step from `from`, every `step`th.
+__device__ __forceinline__ bool sees_bad_key(const uint32_t* words, int lo, int hi, int from, int step) {
+  if (lo >= hi) return false;
+  const int w0 = lo >> 5, w1 = (hi - 1) >> 5;
+  for (int w = w0 + from; w <= w1; w += step) {
+    uint32_t m = words[w];
+    if (w == w0) m &= ~0u << (lo & 31);
+    if (w == w1) m &= ~0u >> (31 - ((hi - 1) & 31));
+    if (m) return true;
+  }
+  return false;
+}
 #endif
 
 // The preparation's part of a masked call's workspace.

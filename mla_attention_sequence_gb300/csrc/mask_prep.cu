@@ -32,19 +32,19 @@ __device__ __forceinline__ bool bad_bf16x8(uint4 v) {
   return bad_bf16x2(v.x) || bad_bf16x2(v.y) || bad_bf16x2(v.z) || bad_bf16x2(v.w);
 }
 
-// Latent rows -> clean copies; one CTA per 32 keys of a batch element, a warp for four of
+// Latent rows -> clean copies; one CTA (unit) per 32 keys of a batch element, a warp for four of
 // them. bad[b][word] bit r: key 32 * word + r holds a non-finite value.
 // The tensor-core dims: the four rows' 72 16-byte chunks each are loaded before the first is
 // looked at (row by row the kernel took 11 us however few keys there were).
 constexpr int KEY_ROWS = 4;
 
-__global__ void __launch_bounds__(256) mask_keys_tc_kernel(int S, const bf16* __restrict__ c, const bf16* __restrict__ r,
-                                                           bf16* __restrict__ c_out, bf16* __restrict__ r_out,
-                                                           uint32_t* __restrict__ bad) {
+__device__ __forceinline__ void clean_keys_tc(int S, int unit, int units, const bf16* __restrict__ c,
+                                              const bf16* __restrict__ r, bf16* __restrict__ c_out,
+                                              bf16* __restrict__ r_out, uint32_t* __restrict__ bad) {
   constexpr int NC = 64, NR = 8;  // chunks of a latent row (512 values), of a RoPE key (64)
   __shared__ uint32_t warp_bad[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
-  const int j0 = blockIdx.x * 32 + warp * KEY_ROWS;
+  const int j0 = unit * 32 + warp * KEY_ROWS;
   const uint4* cs = reinterpret_cast<const uint4*>(c) + (static_cast<ll>(b) * S + j0) * NC;
   const uint4* rs = reinterpret_cast<const uint4*>(r) + (static_cast<ll>(b) * S + j0) * NR;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -73,18 +73,18 @@ __global__ void __launch_bounds__(256) mask_keys_tc_kernel(int S, const bf16* __
     uint32_t m = 0u;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m |= warp_bad[k];
-    bad[static_cast<ll>(b) * gridDim.x + blockIdx.x] = m;
+    bad[static_cast<ll>(b) * units + unit] = m;
   }
 }
 
 // Any widths: one value a lane.
 template <typename T>
-__global__ void __launch_bounds__(256) mask_keys_kernel(int S, int d_c, int d_rope, const T* __restrict__ c,
-                                                        const T* __restrict__ r, T* __restrict__ c_out,
-                                                        T* __restrict__ r_out, uint32_t* __restrict__ bad) {
+__device__ __forceinline__ void clean_keys(int S, int unit, int units, int d_c, int d_rope, const T* __restrict__ c,
+                                           const T* __restrict__ r, T* __restrict__ c_out, T* __restrict__ r_out,
+                                           uint32_t* __restrict__ bad) {
   __shared__ uint32_t warp_bad[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
-  const int j0 = blockIdx.x * 32 + warp * KEY_ROWS;
+  const int j0 = unit * 32 + warp * KEY_ROWS;
   uint32_t mask = 0u;
   auto sweep = [&](int width, const T* src, T* dst, bool write) {
     const T* from = src + (static_cast<ll>(b) * S + j0) * width;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(256) mask_keys_kernel(int S, int d_c, int d_ro
     uint32_t m = 0u;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m |= warp_bad[k];
-    bad[static_cast<ll>(b) * gridDim.x + blockIdx.x] = m;
+    bad[static_cast<ll>(b) * units + unit] = m;
   }
 }
 
@@ -122,17 +122,13 @@ __device__ __forceinline__ int position(const Dims& d, int i) {
   return (d.q_split > 0 && i >= d.q_split) ? d.q_offset2 + (i - d.q_split) : d.q_offset + i;
 }
 
-// One CTA of 128 threads per 128-row query tile: thread = row.
-__global__ void __launch_bounds__(128) mask_rows_kernel(Dims d, const int* __restrict__ key_lo,
-                                                        const int* __restrict__ key_hi,
-                                                        const uint32_t* __restrict__ bad, int bad_words,
-                                                        int2* __restrict__ rows, int2* __restrict__ q_tiles,
-                                                        int2* __restrict__ q_hull, int* __restrict__ q_bad,
-                                                        int* __restrict__ counters) {
-  __shared__ int s_lo[4], s_hi[4];
-  const int t = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i = t * 128 + threadIdx.x;
-  if (t == 0 && b == 0 && threadIdx.x == 0) *q_bad = counters[0] = counters[1] = counters[2] = 0;
+// The visible intervals of 256 query rows (two 128-row tiles) of a batch element: thread = row.
+__device__ __forceinline__ void row_intervals(const Dims& d, int unit, const int* __restrict__ key_lo,
+                                              const int* __restrict__ key_hi, int2* __restrict__ rows,
+                                              int2* __restrict__ q_tiles, int2* __restrict__ q_hull) {
+  __shared__ int s_lo[8], s_hi[8];
+  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = unit * 256 + threadIdx.x;
   int lo = 0, hi = 0;
   if (i < d.Sq) {
     const ll at = static_cast<ll>(b) * d.Sq + i;
@@ -141,21 +137,7 @@ __global__ void __launch_bounds__(128) mask_rows_kernel(Dims d, const int* __res
     if (d.causal) hi = min(hi, position(d, i) + 1);
     if (lo >= hi) lo = hi = 0;
   }
-  // rows that see a bad key: only when there is one in this batch element at all
-  const uint32_t* words = bad + static_cast<ll>(b) * bad_words;
-  bool any = false;
-  for (int w = threadIdx.x; w < bad_words; w += 128) any |= words[w] != 0u;
-  bool poisoned = false;
-  if (__syncthreads_or(any) && lo < hi) {
-    const int w0 = lo >> 5, w1 = (hi - 1) >> 5;
-    for (int w = w0; w <= w1 && !poisoned; ++w) {
-      uint32_t m = words[w];
-      if (w == w0) m &= ~0u << (lo & 31);
-      if (w == w1) m &= ~0u >> (31 - ((hi - 1) & 31));
-      poisoned = m != 0u;
-    }
-  }
-  rows[static_cast<ll>(b) * d.sq_pad + i] = make_int2(poisoned ? lo | static_cast<int>(0x80000000u) : lo, hi);
+  if (i < d.sq_pad) rows[static_cast<ll>(b) * d.sq_pad + i] = make_int2(lo, hi);
   const bool some = lo < hi;
   const int wlo = __reduce_min_sync(0xffffffffu, some ? lo : 0x7fffffff);
   const int whi = __reduce_max_sync(0xffffffffu, some ? hi : 0);
@@ -164,29 +146,60 @@ __global__ void __launch_bounds__(128) mask_rows_kernel(Dims d, const int* __res
     s_hi[warp] = whi;
   }
   __syncthreads();
-  if (threadIdx.x < 2)
-    q_hull[static_cast<ll>(b) * (d.sq_pad / 64) + t * 2 + threadIdx.x] =
-        make_int2(min(s_lo[2 * threadIdx.x], s_lo[2 * threadIdx.x + 1]),
-                  max(s_hi[2 * threadIdx.x], s_hi[2 * threadIdx.x + 1]));
-  if (threadIdx.x == 0) {
-    const int l = min(min(s_lo[0], s_lo[1]), min(s_lo[2], s_lo[3]));
-    const int h = max(max(s_hi[0], s_hi[1]), max(s_hi[2], s_hi[3]));
-    // a tile whose rows see nothing still walks one (wholly masked) key tile
-    const int first = l < h ? l / 128 : 0, end = l < h ? (h + 127) / 128 : 1;
-    q_tiles[static_cast<ll>(b) * (d.sq_pad / 128) + t] = make_int2(first, end - first);
+  const int k = threadIdx.x, tile = unit * 2 + (k >> 1);
+  if (k >= 4 || tile * 128 >= d.sq_pad) return;
+  q_hull[static_cast<ll>(b) * (d.sq_pad / 64) + unit * 4 + k] =
+      make_int2(min(s_lo[2 * k], s_lo[2 * k + 1]), max(s_hi[2 * k], s_hi[2 * k + 1]));
+  if (k & 1) return;
+  const int l = min(min(s_lo[2 * k], s_lo[2 * k + 1]), min(s_lo[2 * k + 2], s_lo[2 * k + 3]));
+  const int h = max(max(s_hi[2 * k], s_hi[2 * k + 1]), max(s_hi[2 * k + 2], s_hi[2 * k + 3]));
+  // a tile whose rows see nothing still walks one (wholly masked) key tile
+  const int first = l < h ? l / 128 : 0, end = l < h ? (h + 127) / 128 : 1;
+  q_tiles[static_cast<ll>(b) * (d.sq_pad / 128) + tile] = make_int2(first, end - first);
+}
+
+// Rows and keys of all batch elements in one launch: the first CTAs take the rows, 256 each, the
+// others the keys, 32 each. TC: the tensor-core dims. One launch, because in small calls a launch
+// is most of what any of this costs.
+template <typename T, bool TC>
+__global__ void __launch_bounds__(256)
+    mask_inputs_kernel(const __grid_constant__ Dims d, const int* __restrict__ key_lo, const int* __restrict__ key_hi,
+                       const T* __restrict__ c, const T* __restrict__ r, const __grid_constant__ MaskBuffers m) {
+  after_previous();
+  const int row_units = (d.sq_pad + 255) / 256, units = static_cast<int>(gridDim.x) - row_units;
+  const int unit = static_cast<int>(blockIdx.x) - row_units;
+  if (unit < 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *m.q_bad = m.counters[0] = m.counters[1] = m.counters[2] = 0;
+    row_intervals(d, blockIdx.x, key_lo, key_hi, m.rows, m.q_tiles, m.q_hull);
+  } else if constexpr (TC) {
+    clean_keys_tc(d.S, unit, units, c, r, reinterpret_cast<bf16*>(m.c_kv), reinterpret_cast<bf16*>(m.k_rope), m.bad);
+  } else {
+    clean_keys(d.S, unit, units, d.d_c, d.d_rope, c, r, reinterpret_cast<T*>(m.c_kv), reinterpret_cast<T*>(m.k_rope), m.bad);
   }
 }
 
-// One CTA per batch element, a warp per 128-key tile in turn: the 64-row query tiles whose
-// hull meets it, in order. The CTA that finishes last lists the key tiles (of all batch
+// One CTA per batch element. First, only if one of its keys is bad: bit 31 of the rows that see
+// such a key. Then, a warp per 128-key tile in turn: the 64-row query tiles whose hull meets it, in
+// order. The CTA that finishes last lists the key tiles (of all batch
 // elements, in order) that some query tile's walk touches: only those are rebuilt, and only
 // their gradients summed.
-__global__ void __launch_bounds__(1024) mask_tiles_kernel(int kt, int nq64, const int2* __restrict__ q_tiles,
+__global__ void __launch_bounds__(1024) mask_tiles_kernel(int kt, int nq64, const uint32_t* __restrict__ bad,
+                                                          int bad_words, int2* __restrict__ rows,
+                                                          const int2* __restrict__ q_tiles,
                                                           const int2* __restrict__ q_hull, int* __restrict__ kt_count,
                                                           int* __restrict__ kt_list, int* __restrict__ seen,
                                                           int* __restrict__ seen_list, int* __restrict__ counters,
                                                           int4* __restrict__ work) {
+  after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
+  const uint32_t* words = bad + static_cast<ll>(b) * bad_words;
+  bool any = false;
+  for (int w = threadIdx.x; w < bad_words; w += 1024) any |= words[w] != 0u;
+  if (__syncthreads_or(any))
+    for (int i = threadIdx.x; i < nq64 * 64; i += 1024) {
+      int2& row = rows[static_cast<ll>(b) * nq64 * 64 + i];
+      if (sees_bad_key(words, row.x, row.y, 0, 1)) row.x |= static_cast<int>(0x80000000u);
+    }
   const int2* hull = q_hull + static_cast<ll>(b) * nq64;
   const int2* walk = q_tiles + static_cast<ll>(b) * (nq64 / 2);
   for (int t = warp; t < kt; t += 32) {
@@ -254,6 +267,7 @@ __global__ void __launch_bounds__(1024) mask_tiles_kernel(int kt, int nq64, cons
 // key_lo, key_hi of packed documents: one thread per query row.
 __global__ void key_bounds_kernel(Dims d, const int* __restrict__ starts, int n_docs, const int* __restrict__ prefix,
                                   int window, int* __restrict__ key_lo, int* __restrict__ key_hi) {
+  after_previous();
   const int i = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
   if (i >= d.Sq) return;
   const int pos = position(d, i);
@@ -299,6 +313,7 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
                                                            const float* __restrict__ lse, float* __restrict__ lse2,
                                                            float* __restrict__ delta, bf16* __restrict__ q_clean,
                                                            int* __restrict__ q_bad) {
+  after_previous();
   const ll row = (static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
   const ll rows = static_cast<ll>(d.B) * d.sq_pad * d.n_h;
   const int l16 = threadIdx.x & 15;
@@ -372,6 +387,7 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
 __global__ void __launch_bounds__(256) mask_clean_kernel(ll rows, const bf16* __restrict__ q,
                                                          const bf16* __restrict__ dout, bf16* __restrict__ q_clean,
                                                          bf16* __restrict__ dout_clean, const int* __restrict__ q_bad) {
+  after_previous();
   if (*q_bad == 0) return;
   const int l16 = threadIdx.x & 15;
   const ll step = (static_cast<ll>(gridDim.x) * blockDim.x) >> 4;
@@ -409,6 +425,7 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_any_kernel(Dims d, const T* 
                                                                const T* __restrict__ dout, const float* __restrict__ lse,
                                                                float* __restrict__ lse_row, float* __restrict__ delta,
                                                                float* __restrict__ q_clean, float* __restrict__ dout_clean) {
+  after_previous();
   const ll row = (static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const ll rows = static_cast<ll>(d.B) * d.Sq * d.n_h;
   if (row >= rows) return;
@@ -484,33 +501,22 @@ LaunchResult mask_prepare(const Dims& d, bool is_bf16, const int* key_lo, const 
                           const void* k_rope, const MaskBuffers& m, bool key_tiles, cudaStream_t st) {
   LaunchResult r;
   const int words = (d.S + 31) / 32;
-  const dim3 grid(words, d.B);
-  auto keys = [&](auto* type) {
-    using T = std::remove_pointer_t<decltype(type)>;
-    mask_keys_kernel<T><<<grid, 256, 0, st>>>(d.S, d.d_c, d.d_rope, static_cast<const T*>(c_kv),
-                                              static_cast<const T*>(k_rope), static_cast<T*>(static_cast<void*>(m.c_kv)),
-                                              static_cast<T*>(static_cast<void*>(m.k_rope)), m.bad);
-  };
+  const dim3 grid(words + (d.sq_pad + 255) / 256, d.B);
   auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  auto run = [&](auto* kern, auto* type) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    return launch_next(kern, grid, 256, 0, st, d, key_lo, key_hi, static_cast<const T*>(c_kv),
+                       static_cast<const T*>(k_rope), m);
+  };
   if (is_bf16 && d.d_c == 512 && d.d_rope == 64 && aligned(c_kv) && aligned(k_rope))
-    mask_keys_tc_kernel<<<grid, 256, 0, st>>>(d.S, static_cast<const bf16*>(c_kv), static_cast<const bf16*>(k_rope),
-                                              static_cast<bf16*>(static_cast<void*>(m.c_kv)),
-                                              static_cast<bf16*>(static_cast<void*>(m.k_rope)), m.bad);
+    r.err = run(mask_inputs_kernel<bf16, true>, static_cast<bf16*>(nullptr));
   else if (is_bf16)
-    keys(static_cast<bf16*>(nullptr));
+    r.err = run(mask_inputs_kernel<bf16, false>, static_cast<bf16*>(nullptr));
   else
-    keys(static_cast<float*>(nullptr));
-  r.err = cudaGetLastError();
-  if (r.err == cudaSuccess) {
-    mask_rows_kernel<<<dim3(d.sq_pad / 128, d.B), 128, 0, st>>>(d, key_lo, key_hi, m.bad, words, m.rows, m.q_tiles,
-                                                                m.q_hull, m.q_bad, m.counters);
-    r.err = cudaGetLastError();
-  }
-  if (r.err == cudaSuccess && key_tiles) {
-    mask_tiles_kernel<<<d.B, 1024, 0, st>>>(d.skv_pad / 128, d.sq_pad / 64, m.q_tiles, m.q_hull, m.kt_count, m.kt_list,
-                                            m.seen, m.seen_list, m.counters, m.work);
-    r.err = cudaGetLastError();
-  }
+    r.err = run(mask_inputs_kernel<float, false>, static_cast<float*>(nullptr));
+  if (r.err == cudaSuccess && key_tiles)
+    r.err = launch_next(mask_tiles_kernel, d.B, 1024, 0, st, d.skv_pad / 128, d.sq_pad / 64, m.bad, words, m.rows,
+                        m.q_tiles, m.q_hull, m.kt_count, m.kt_list, m.seen, m.seen_list, m.counters, m.work);
   if (r.err != cudaSuccess) r.what = "mask preparation";
   return r;
 }
@@ -518,8 +524,8 @@ LaunchResult mask_prepare(const Dims& d, bool is_bf16, const int* key_lo, const 
 LaunchResult mask_key_bounds(const Dims& d, const int* starts, int n_docs, const int* prefix, int window, int* key_lo,
                              int* key_hi, cudaStream_t st) {
   LaunchResult r;
-  key_bounds_kernel<<<dim3((d.Sq + 127) / 128, d.B), 128, 0, st>>>(d, starts, n_docs, prefix, window, key_lo, key_hi);
-  r.err = cudaGetLastError();
+  r.err = launch_next(key_bounds_kernel, dim3((d.Sq + 127) / 128, d.B), 128, 0, st, d, starts, n_docs, prefix, window,
+                      key_lo, key_hi);
   if (r.err != cudaSuccess) r.what = "key bounds";
   return r;
 }
@@ -530,21 +536,13 @@ LaunchResult tc_mask_bwd_pre(const Dims& d, const bf16* q, const bf16* out, cons
   LaunchResult r;
   const ll rows = static_cast<ll>(d.B) * d.sq_pad * d.n_h;
   const unsigned grid = static_cast<unsigned>((rows + 15) / 16);
-  if (q8)
-    mask_bwd_pre_kernel<true, true><<<grid, 256, 0, st>>>(d, nullptr, nullptr, *q8, *out8, dout, lse, w.lse2, w.delta, q_clean,
-                                                    q_bad);
-  else if (check_q)
-    mask_bwd_pre_kernel<false, true><<<grid, 256, 0, st>>>(d, q, out, Packed{}, Packed{}, dout, lse, w.lse2, w.delta,
-                                                           q_clean, q_bad);
-  else
-    mask_bwd_pre_kernel<false, false><<<grid, 256, 0, st>>>(d, q, out, Packed{}, Packed{}, dout, lse, w.lse2, w.delta,
-                                                            q_clean, q_bad);
-  r.err = cudaGetLastError();
-  if (r.err == cudaSuccess) {
-    mask_clean_kernel<<<2 * sm_count(), 256, 0, st>>>(static_cast<ll>(d.B) * d.Sq * d.n_h, q8 ? nullptr : q, dout,
-                                                      q_clean, dout_clean, q_bad);
-    r.err = cudaGetLastError();
-  }
+  const auto kern = q8 ? mask_bwd_pre_kernel<true, true>
+                       : check_q ? mask_bwd_pre_kernel<false, true> : mask_bwd_pre_kernel<false, false>;
+  r.err = launch_next(kern, grid, 256, 0, st, d, q, out, q8 ? *q8 : Packed{}, out8 ? *out8 : Packed{}, dout, lse, w.lse2,
+                      w.delta, q_clean, q_bad);
+  if (r.err == cudaSuccess)
+    r.err = launch_next(mask_clean_kernel, 2 * sm_count(), 256, 0, st, static_cast<ll>(d.B) * d.Sq * d.n_h,
+                        q8 ? nullptr : q, dout, q_clean, dout_clean, q_bad);
   if (r.err != cudaSuccess) r.what = "masked backward row pass";
   return r;
 }
@@ -556,15 +554,13 @@ LaunchResult simt_mask_bwd_pre(const Dims& d, bool is_bf16, const void* q, const
   const ll rows = static_cast<ll>(d.B) * d.Sq * d.n_h;
   const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
   const Packed a = q8 ? *q8 : Packed{}, o = out8 ? *out8 : Packed{};
-  if (is_bf16)
-    mask_bwd_pre_any_kernel<bf16><<<grid, 256, 0, st>>>(d, static_cast<const bf16*>(q), static_cast<const bf16*>(out), a, o,
-                                                        q8 != nullptr, static_cast<const bf16*>(dout), lse, lse_row,
-                                                        delta, q_clean, dout_clean);
-  else
-    mask_bwd_pre_any_kernel<float><<<grid, 256, 0, st>>>(d, static_cast<const float*>(q), static_cast<const float*>(out), a,
-                                                         o, q8 != nullptr, static_cast<const float*>(dout), lse, lse_row,
-                                                         delta, q_clean, dout_clean);
-  r.err = cudaGetLastError();
+  auto run = [&](auto* kern, auto* type) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    return launch_next(kern, grid, 256, 0, st, d, static_cast<const T*>(q), static_cast<const T*>(out), a, o,
+                       q8 != nullptr, static_cast<const T*>(dout), lse, lse_row, delta, q_clean, dout_clean);
+  };
+  r.err = is_bf16 ? run(mask_bwd_pre_any_kernel<bf16>, static_cast<bf16*>(nullptr))
+                  : run(mask_bwd_pre_any_kernel<float>, static_cast<float*>(nullptr));
   if (r.err != cudaSuccess) r.what = "masked backward row pass";
   return r;
 }

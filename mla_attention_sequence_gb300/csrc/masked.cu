@@ -229,10 +229,6 @@ laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* 
   if (r.ok())
     r = timed("masked_attn_bwd_dq", s,
               [&] { return tc_attn_bwd_dq(d, qr, kr, cb(dout), w, static_cast<bf16*>(dq), s, &mask); });
-  if (r.ok()) {  // rows of key tiles that nothing walks get zero gradient
-    r.err = cudaMemsetAsync(dc_kv, 0, static_cast<size_t>(d.B) * d.S * d.d_c * 2, s);
-    if (r.err != cudaSuccess) r.what = "zero dc_kv";
-  }
   if (r.ok())
     r = timed("recon_bwd_dc_gemm", s, [&] {
       return tc_recon_bwd_dc(d, w.dk_ws, w.dv_ws, cb(W_UK), cb(W_UV), static_cast<bf16*>(dc_kv), s, &list);
@@ -241,7 +237,7 @@ laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* 
     r = timed("recon_bwd_dw_gemm", s, [&] {
       return tc_recon_bwd_dw(d, c, w.dk_ws, w.dv_ws, static_cast<bf16*>(dW_UK), static_cast<bf16*>(dW_UV), s, &list);
     });
-  if (r.ok()) r = timed("bwd_post", s, [&] { return tc_bwd_post(d, w, static_cast<bf16*>(dk_rope), s, m.seen); });
+  if (r.ok()) r = timed("bwd_post", s, [&] { return tc_bwd_post(d, w, static_cast<bf16*>(dk_rope), s, m.seen, static_cast<bf16*>(dc_kv)); });
   return from_launch(r);
 }
 

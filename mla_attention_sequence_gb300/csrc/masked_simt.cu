@@ -40,6 +40,7 @@ struct SimtParams {
   bool rope_bf16;
   const int2* rows;      // [B][sq_pad]
   const int2* q_hull;    // [B][sq_pad / 64]
+  const uint32_t* bad;   // [B][ceil(S / 32)] bit per key: not finite
   float cap, inv_cap;    // 0: none
   const float* slopes;
   const float* dout;     // [B][Sq][n_h][d_v], clean
@@ -279,14 +280,13 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
   const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int i0 = t * ROWS + RI * ty;  // this thread's first row
+  after_previous();
   fill<ROWS>(sq, pk, d.d_qk(), QRows{p, b, h, t * ROWS});
   int lo[RI], hi[RI];
-  bool poisoned[RI];
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     const int2 v = p.rows[static_cast<ll>(b) * d.sq_pad + i0 + i];
-    poisoned[i] = v.x < 0;
-    lo[i] = v.x & 0x7fffffff;
+    lo[i] = v.x;
     hi[i] = v.y;
   }
   const float slope = p.slopes ? p.slopes[h] : 0.f;
@@ -351,10 +351,14 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
   }
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
+    // the row's 16 threads share the words of the keys it sees
+    const uint32_t* words = p.bad + static_cast<ll>(b) * ((d.S + 31) / 32);
+    const unsigned votes = __ballot_sync(0xffffffffu, sees_bad_key(words, lo[i], hi[i], tx, 16));
+    const bool poisoned = (votes & (threadIdx.x & 16 ? 0xffff0000u : 0xffffu)) != 0u;
     if (i0 + i >= d.Sq) continue;
     float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
     float L = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
-    if (poisoned[i] || (lo[i] < hi[i] && l[i] == 0.f)) inv = L = NAN;  // l = 0: an infinite q, all scores -inf
+    if (poisoned || (lo[i] < hi[i] && l[i] == 0.f)) inv = L = NAN;  // l = 0: an infinite q, all scores -inf
     const ll row = (static_cast<ll>(b) * d.Sq + i0 + i) * d.n_h + h;
 #pragma unroll
     for (int c = 0; c < N; ++c) {
@@ -388,7 +392,7 @@ __device__ __forceinline__ void masked_simt_dq(const SimtParams& p, int t) {
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     const int2 v = p.rows[static_cast<ll>(b) * d.sq_pad + i0 + i];
-    lo[i] = v.x & 0x7fffffff;
+    lo[i] = v.x;
     hi[i] = v.y;
     const bool in = i0 + i < d.Sq;
     const ll at = (static_cast<ll>(b) * d.n_h + h) * d.Sq + i0 + i;
@@ -504,7 +508,7 @@ __device__ __forceinline__ void masked_simt_dkv(const SimtParams& p, int t) {
         const int key = k0 + k;
         float dcap = 1.f;
         const float v = score_of(p, s[k][j], slope, pos, key, &dcap);
-        const float e = key >= (r.x & 0x7fffffff) && key < r.y ? expf(v - L) : 0.f;
+        const float e = key >= r.x && key < r.y ? expf(v - L) : 0.f;
         s[k][j] = e;
         dp[k][j] = e * (dp[k][j] - D) * dcap;
       }
@@ -547,23 +551,12 @@ __device__ __forceinline__ void masked_simt_dkv(const SimtParams& p, int t) {
 // problem's CTAs of either alone leave most SMs idle (256 rows, 4 heads: 64 CTAs each).
 template <int N, int RI>
 __global__ void __launch_bounds__(THREADS) masked_simt_bwd(const SimtParams p) {
+  after_previous();
   const int q_blocks = (p.d.Sq + 16 * RI - 1) / (16 * RI);
   if (static_cast<int>(blockIdx.x) < q_blocks)
     masked_simt_dq<N, RI>(p, blockIdx.x);
   else
     masked_simt_dkv<N, RI>(p, static_cast<int>(blockIdx.x) - q_blocks);
-}
-
-// dk_rope[b, j, :] = the heads' RoPE-key gradients summed, in order.
-template <typename T>
-__global__ void masked_simt_rope_sum(ll total, int n_h, int d_rope, const float* __restrict__ dkr, T* __restrict__ dk_rope) {
-  const ll idx = static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (idx >= total) return;
-  const ll bj = idx / d_rope;
-  const int k = static_cast<int>(idx - bj * d_rope);
-  float acc = 0.f;
-  for (int h = 0; h < n_h; ++h) acc += dkr[(bj * n_h + h) * d_rope + k];
-  dk_rope[idx] = static_cast<T>(acc);
 }
 
 struct Ws {
@@ -611,6 +604,7 @@ SimtParams params(const Dims& d, bool is_bf16, const ScoreMods& mods, const Ws& 
   p.rope_bf16 = is_bf16;
   p.rows = w.mask.rows;
   p.q_hull = w.mask.q_hull;
+  p.bad = w.mask.bad;
   p.cap = mods.cap;
   p.inv_cap = mods.cap > 0.f ? 1.f / mods.cap : 0.f;
   p.slopes = mods.slopes;
@@ -645,8 +639,7 @@ cudaError_t launch_rows(const Dims& d, const SimtParams& p, cudaStream_t st) {
       w <= 64 ? kernel_of<BWD, 1, RI>() : w <= 128 ? kernel_of<BWD, 2, RI>() : kernel_of<BWD, 4, RI>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kern<<<dim3(blocks, d.n_h, d.B), THREADS, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_next(kern, dim3(blocks, d.n_h, d.B), THREADS, smem, st, p);
 }
 
 template <bool BWD>
@@ -677,14 +670,37 @@ struct GemmJob {
   bool c_bf16;
   ll cm, cn;
 };
+// dk_rope[b, j, :] = the heads' RoPE-key gradients summed, in order: the CTAs from first_block on, a
+// thread per value.
+struct RopeSum {
+  int first_block;
+  ll total;
+  int n_h, d_rope;
+  const float* dkr;  // [B][S][n_h][d_rope]
+  void* dk_rope;
+  bool bf16_out;
+};
 struct GemmJobs {
   int n;
   GemmJob job[3];
+  RopeSum rope;
 };
 
-__global__ void __launch_bounds__(THREADS) small_gemm_kernel(const GemmJobs jobs) {
+__global__ void __launch_bounds__(THREADS) small_gemm_kernel(const __grid_constant__ GemmJobs jobs) {
   constexpr int T = 32, KB = 16, GROUPS = 4;
   __shared__ float As[GROUPS][KB][T + 4], Bs[GROUPS][KB][T + 4];
+  after_previous();
+  if (static_cast<int>(blockIdx.x) >= jobs.rope.first_block) {
+    const RopeSum& s = jobs.rope;
+    const ll idx = static_cast<ll>(blockIdx.x - s.first_block) * THREADS + threadIdx.x;
+    if (idx >= s.total) return;
+    const ll bj = idx / s.d_rope;
+    const int k = static_cast<int>(idx - bj * s.d_rope);
+    float acc = 0.f;
+    for (int h = 0; h < s.n_h; ++h) acc += s.dkr[(bj * s.n_h + h) * s.d_rope + k];
+    store(s.dk_rope, s.bf16_out, idx, acc);
+    return;
+  }
   int which = 0;
   while (which + 1 < jobs.n && static_cast<int>(blockIdx.x) >= jobs.job[which + 1].first_tile) ++which;
   const GemmJob& j = jobs.job[which];
@@ -764,11 +780,13 @@ struct Gemms {
     j = GemmJob{M, N, p2 ? 2 : 1, (N + 31) / 32, static_cast<int>(tiles), {p, p2 ? *p2 : GemmPair{}}, c, c_bf16, cm, cn};
     tiles += static_cast<ll>((M + 31) / 32) * j.tiles_n;
   }
-  cudaError_t run(cudaStream_t st) const {
-    if (tiles == 0) return cudaSuccess;
-    if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-    small_gemm_kernel<<<static_cast<unsigned>(tiles), THREADS, 0, st>>>(jobs);
-    return cudaGetLastError();
+  cudaError_t run(cudaStream_t st, const RopeSum& rope = RopeSum{}) {
+    const ll blocks = tiles + (rope.total + THREADS - 1) / THREADS;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    jobs.rope = rope;
+    jobs.rope.first_block = static_cast<int>(tiles);
+    return launch_next(small_gemm_kernel, static_cast<unsigned>(blocks), THREADS, 0, st, jobs);
   }
 };
 
@@ -783,9 +801,9 @@ cudaError_t rebuild(const Dims& d, bool bf, const void* c, const void* W_UK, con
   return g.run(st);
 }
 
-// dc = dK W_UK^T + dV W_UV^T, dW_UK = c^T dK, dW_UV = c^T dV (k runs over the batch's rows too)
+// dc = dK W_UK^T + dV W_UV^T, dW_UK = c^T dK, dW_UV = c^T dV (k runs over the batch's rows too), dk_rope
 cudaError_t rebuild_bwd(const Dims& d, bool bf, const void* c, const void* W_UK, const void* W_UV, const float* dk,
-                        const float* dv, const BwdGrads& o, cudaStream_t st) {
+                        const float* dv, const float* dkr, const BwdGrads& o, cudaStream_t st) {
   const int M = d.B * d.S;
   const ll nk = static_cast<ll>(d.n_h) * d.d_nope, nv = static_cast<ll>(d.n_h) * d.d_v;
   Gemms g;
@@ -793,7 +811,7 @@ cudaError_t rebuild_bwd(const Dims& d, bool bf, const void* c, const void* W_UK,
   g.add(d.d_c, static_cast<int>(nv), GemmPair{c, dv, bf, false, M, 1, d.d_c, nv, 1}, o.dW_UV, bf, nv, 1);
   const GemmPair second{dv, W_UV, false, bf, static_cast<int>(nv), nv, 1, 1, nv};
   g.add(M, d.d_c, GemmPair{dk, W_UK, false, bf, static_cast<int>(nk), nk, 1, 1, nk}, o.dc_kv, bf, d.d_c, 1, &second);
-  return g.run(st);
+  return g.run(st, RopeSum{0, static_cast<ll>(M) * d.d_rope, d.n_h, d.d_rope, dkr, o.dk_rope, bf});
 }
 
 }  // namespace
@@ -848,20 +866,11 @@ LaunchResult simt_masked_bwd(const Dims& d, bool is_bf16, const ScoreMods& mods,
   p.dv = w.dv;
   p.dkr = w.dkr;
   r.err = launch<true>(d, p, st);
-  const ll nr = static_cast<ll>(d.B) * d.S * d.d_rope;
-  if (r.err == cudaSuccess && nr > 0) {
-    const unsigned grid = static_cast<unsigned>((nr + 255) / 256);
-    if (is_bf16)
-      masked_simt_rope_sum<bf16><<<grid, 256, 0, st>>>(nr, d.n_h, d.d_rope, w.dkr, static_cast<bf16*>(g.dk_rope));
-    else
-      masked_simt_rope_sum<float><<<grid, 256, 0, st>>>(nr, d.n_h, d.d_rope, w.dkr, static_cast<float*>(g.dk_rope));
-    r.err = cudaGetLastError();
-  }
   if (r.err != cudaSuccess) {
     r.what = "masked attention backward (CUDA cores)";
     return r;
   }
-  r.err = rebuild_bwd(d, is_bf16, w.mask.c_kv, W_UK, W_UV, w.dkn, w.dv, g, st);
+  r.err = rebuild_bwd(d, is_bf16, w.mask.c_kv, W_UK, W_UV, w.dkn, w.dv, w.dkr, g, st);
   if (r.err != cudaSuccess) r.what = "rebuild backward (CUDA cores)";
   return r;
 }

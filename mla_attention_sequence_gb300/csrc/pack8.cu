@@ -83,6 +83,7 @@ constexpr int UNROLL = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) pack8_kernel(ll chunks, const T* __restrict__ x, uint8_t* __restrict__ codes,
                                                     uint8_t* __restrict__ scales) {
+  after_previous();
   using C = Chunk<T>;
   constexpr int PER = kPackBlock / C::N;  // threads per block
   const ll first = static_cast<ll>(blockIdx.x) * (256 * UNROLL) + threadIdx.x;
@@ -122,6 +123,7 @@ __device__ __forceinline__ float as_float(bf16 v) { return __bfloat162float(v); 
 template <typename T>
 __global__ void __launch_bounds__(256) pack8_any_kernel(ll rows, int cols, int blocks, const T* __restrict__ x,
                                                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  after_previous();
   const ll w = (static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   if (w >= rows * blocks) return;
   const ll row = w / blocks;
@@ -136,6 +138,7 @@ __global__ void __launch_bounds__(256) pack8_any_kernel(ll rows, int cols, int b
 template <typename T>
 __global__ void __launch_bounds__(256) unpack8_kernel(ll chunks, const uint8_t* __restrict__ codes,
                                                       const uint8_t* __restrict__ scales, T* __restrict__ x) {
+  after_previous();
   using C = Chunk<T>;
   constexpr int PER = kPackBlock / C::N;
   constexpr int W = C::N / 4;
@@ -173,6 +176,7 @@ __global__ void __launch_bounds__(256) unpack8_kernel(ll chunks, const uint8_t* 
 
 template <typename T>
 __global__ void __launch_bounds__(256) unpack8_any_kernel(ll rows, int cols, const Packed p, T* __restrict__ x) {
+  after_previous();
   const ll i = static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= rows * cols) return;
   const ll row = i / cols;
@@ -186,23 +190,22 @@ cudaError_t pack(ll rows, int cols, const T* x, uint8_t* codes, uint8_t* scales,
   const int blocks = (cols + kPackBlock - 1) / kPackBlock;
   if (cols % kPackBlock == 0 && aligned(x, 16) && aligned(codes, 8)) {
     const ll chunks = rows * cols / Chunk<T>::N;
-    pack8_kernel<T><<<static_cast<unsigned>((chunks + 256 * UNROLL - 1) / (256 * UNROLL)), 256, 0, st>>>(chunks, x, codes, scales);
-  } else {
-    pack8_any_kernel<T><<<static_cast<unsigned>((rows * blocks + 7) / 8), 256, 0, st>>>(rows, cols, blocks, x, codes,
-                                                                                       scales);
+    const unsigned grid = static_cast<unsigned>((chunks + 256 * UNROLL - 1) / (256 * UNROLL));
+    return launch_next(pack8_kernel<T>, grid, 256, 0, st, chunks, x, codes, scales);
   }
-  return cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>((rows * blocks + 7) / 8);
+  return launch_next(pack8_any_kernel<T>, grid, 256, 0, st, rows, cols, blocks, x, codes, scales);
 }
 
 template <typename T>
 cudaError_t unpack(ll rows, int cols, const Packed& p, T* x, cudaStream_t st) {
   if (cols % kPackBlock == 0 && aligned(x, 16) && aligned(p.codes, 8)) {
     const ll chunks = rows * cols / Chunk<T>::N;
-    unpack8_kernel<T><<<static_cast<unsigned>((chunks + 256 * UNROLL - 1) / (256 * UNROLL)), 256, 0, st>>>(chunks, p.codes, p.scales, x);
-  } else {
-    unpack8_any_kernel<T><<<static_cast<unsigned>((rows * cols + 255) / 256), 256, 0, st>>>(rows, cols, p, x);
+    const unsigned grid = static_cast<unsigned>((chunks + 256 * UNROLL - 1) / (256 * UNROLL));
+    return launch_next(unpack8_kernel<T>, grid, 256, 0, st, chunks, p.codes, p.scales, x);
   }
-  return cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>((rows * cols + 255) / 256);
+  return launch_next(unpack8_any_kernel<T>, grid, 256, 0, st, rows, cols, p, x);
 }
 
 }  // namespace

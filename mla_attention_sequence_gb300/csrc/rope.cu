@@ -43,6 +43,7 @@ __device__ __forceinline__ void fill_angles(const RopeArgs& a, const RopeTable& 
 template <typename T>
 __global__ void __launch_bounds__(THREADS) rope_any_kernel(const RopeArgs a, const RopeTable t, int per_cta) {
   extern __shared__ float2 cs[];
+  after_previous();
   const ll first = static_cast<ll>(blockIdx.x) * per_cta;
   const int tokens = static_cast<int>(min(static_cast<ll>(per_cta), a.tokens - first));
   const int n = a.d_rope / 2, heads = a.q ? a.n_h : 0, rows = heads + (a.k ? 1 : 0);
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(THREADS) rope_vec_kernel(const RopeArgs a, con
   using V = Vec<T>;
   constexpr int N = V::N;
   constexpr int UNROLL = INTERLEAVED ? 4 : 2;
+  after_previous();
   const ll first = static_cast<ll>(blockIdx.x) * per_cta;
   const int tokens = static_cast<int>(min(static_cast<ll>(per_cta), a.tokens - first));
   const int n = a.d_rope / 2, heads = a.q ? a.n_h : 0;
@@ -234,12 +236,9 @@ cudaError_t launch(const RopeArgs& a, const RopeTable& t, cudaStream_t st) {
   const int copy = a.q_out != a.q ? a.d_nope / N : 0;
   const Div head = make_div(static_cast<uint32_t>(std::max(1, copy + (a.interleaved ? a.d_rope : n) / N)));
   if (!vec)
-    rope_any_kernel<T><<<grid, THREADS, smem, st>>>(a, t, static_cast<int>(per));
-  else if (a.interleaved)
-    rope_vec_kernel<T, true><<<grid, THREADS, smem, st>>>(a, t, static_cast<int>(per), head);
-  else
-    rope_vec_kernel<T, false><<<grid, THREADS, smem, st>>>(a, t, static_cast<int>(per), head);
-  return cudaGetLastError();
+    return launch_next(rope_any_kernel<T>, grid, THREADS, smem, st, a, t, static_cast<int>(per));
+  return launch_next(a.interleaved ? rope_vec_kernel<T, true> : rope_vec_kernel<T, false>, grid, THREADS, smem, st, a, t,
+                     static_cast<int>(per), head);
 }
 
 }  // namespace
