@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   constexpr bool CAP = MASKED && (MOD & kModCap) != 0, BIAS = MASKED && (MOD & kModBias) != 0;
   int n_kv, j0 = 0;  // key tiles walked: [j0, j0 + n_kv)
   if constexpr (MASKED) {
-    after_previous();
-    const int4 w = p.work[b * p.n_q_tiles + blockIdx.x];
+    beside_previous();  // dK/dV, whose last CTAs leave SMs to these
+    const int4 w = __ldcg(&p.work[b * p.n_q_tiles + blockIdx.x]);
     t = w.x;
     j0 = w.y;
     n_kv = w.z;
@@ -315,13 +315,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const int limit = p.causal ? q_pos(p, q_row) : p.S - 1;  // last visible key
     const long long roff = (static_cast<long long>(b) * p.n_h + h) * p.sq_pad + q_row;
-    const float lse2 = p.lse2[roff];  // +inf on padded rows: P = 0 there
-    const float Drow = p.delta[roff];
+    const float lse2 = MASKED ? __ldcg(&p.lse2[roff]) : p.lse2[roff];  // +inf on padded rows: P = 0 there
+    const float Drow = MASKED ? __ldcg(&p.delta[roff]) : p.delta[roff];
     const float sl2 = p.scale_log2;
     int lo = 0, hi = 0;  // masked: this row sees keys [lo, hi)
     float slope2 = 0.f, pos = 0.f;
     if constexpr (MASKED) {
-      const int2 v = p.rows[static_cast<long long>(b) * p.sq_pad + q_row];
+      const int2 v = __ldcg(&p.rows[static_cast<long long>(b) * p.sq_pad + q_row]);
       lo = v.x & 0x7fffffff;
       hi = v.y;
       if constexpr (BIAS) {
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       uint32_t w[32];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint4 v = valid ? __ldg(drow + k) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = valid ? (MASKED ? __ldcg(drow + k) : __ldg(drow + k)) : make_uint4(0u, 0u, 0u, 0u);
         w[4 * k + 0] = v.x;
         w[4 * k + 1] = v.y;
         w[4 * k + 2] = v.z;
@@ -512,6 +512,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
+  if constexpr (MASKED)
+    end_after_previous(blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1);
 }
 
 }  // namespace

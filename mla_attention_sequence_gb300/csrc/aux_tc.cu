@@ -108,7 +108,7 @@ __global__ void bwd_pre_kernel(Dims d, const bf16* __restrict__ out, const bf16*
 template <bool MASKED>
 __global__ void rope_sum_kernel(Dims d, int parts, const float* __restrict__ dkr, bf16* __restrict__ dk_rope,
                                 const int* __restrict__ seen, bf16* __restrict__ dc_kv) {
-  if constexpr (MASKED) after_previous();
+  if constexpr (MASKED) beside_previous();  // the weight gradients, which read other things
   const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const long long total = static_cast<long long>(d.B) * d.S * 16;
   if (t >= total) return;
@@ -119,7 +119,7 @@ __global__ void rope_sum_kernel(Dims d, int parts, const float* __restrict__ dkr
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   bool walked = j < d.skv_pad;
   if constexpr (MASKED) {
-    walked = walked && seen[b * (d.skv_pad / 128) + j / 128] != 0;
+    walked = walked && __ldcg(seen + b * (d.skv_pad / 128) + j / 128) != 0;
     if (!walked) {
       uint4* row = reinterpret_cast<uint4*>(dc_kv + bj * d.d_c);
       for (int k = c4; k < d.d_c / 8; k += 16) row[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -129,7 +129,7 @@ __global__ void rope_sum_kernel(Dims d, int parts, const float* __restrict__ dkr
     const float4* src =
         reinterpret_cast<const float4*>(dkr + ((static_cast<long long>(b) * d.skv_pad + j) * parts) * 64) + c4;
     for (int g = 0; g < parts; ++g) {
-      const float4 v = src[g * 16];
+      const float4 v = MASKED ? __ldcg(src + g * 16) : src[g * 16];
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;
@@ -140,6 +140,7 @@ __global__ void rope_sum_kernel(Dims d, int parts, const float* __restrict__ dkr
   o.x = pack_bf16x2_dev(acc.x, acc.y);
   o.y = pack_bf16x2_dev(acc.z, acc.w);
   reinterpret_cast<uint2*>(dk_rope + (static_cast<long long>(b) * d.S + j) * 64)[c4] = o;
+  if constexpr (MASKED) end_after_previous(blockIdx.x == gridDim.x - 1);
 }
 
 }  // namespace

@@ -196,10 +196,14 @@ __global__ void __launch_bounds__(224, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  if constexpr (LIST) after_previous();
+  constexpr bool BESIDE = LIST && MODE == DW;  // needs dK, dV and the latent, not the dc_kv product before it
+  if constexpr (BESIDE)
+    beside_previous();
+  else if constexpr (LIST)
+    after_previous();
 
   static_assert(!LIST || ((MODE == DCKV || MODE == DW) && (MODE == DW || MH == 1)), "listed key tiles");
-  const int keys = LIST ? *p.key_count : 0;
+  const int keys = LIST ? __ldcg(p.key_count) : 0;
   const int tiles_per_batch = p.m_tiles * p.n_tiles;
   // DCKV over a list: one 128-row tile per listed key tile, all n of it in a row. DW: k runs over the
   // listed tiles, two k-blocks each.
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(224, 1)
       for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
         int b, m, n;
         coords(tile, b, m, n);
-        int next_key = LIST && MODE == DW && k_blocks > 0 ? p.key_list[0] : 0, this_key = 0;
+        int next_key = LIST && MODE == DW && k_blocks > 0 ? __ldcg(p.key_list) : 0, this_key = 0;
         for (int kb = 0; kb < k_blocks; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1;
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(224, 1)
             if constexpr (LIST) {
               if ((kb & 1) == 0) {  // the list is read a tile ahead
                 this_key = next_key;
-                if (kb + 2 < k_blocks) next_key = p.key_list[kb / 2 + 1];
+                if (kb + 2 < k_blocks) next_key = __ldcg(p.key_list + kb / 2 + 1);
               }
               bb = this_key / p.kt;
               kk = 2 * (this_key - bb * p.kt) + (kb & 1);
@@ -414,6 +418,7 @@ __global__ void __launch_bounds__(224, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
+  if constexpr (BESIDE) end_after_previous(blockIdx.x == gridDim.x - 1);
 }
 
 // ---- K/V rebuild with the latent tile as a TMEM operand

@@ -55,6 +55,15 @@ __device__ __forceinline__ void after_previous() {
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
 }
+// A kernel that needs nothing of the one just before it in the chain may run beside it: it begins
+// with beside_previous() and its last CTA ends with end_after_previous(), so that whoever waits for
+// this kernel has waited for both. What it does read comes from kernels that had ended before the
+// one beside it passed its own after_previous(), which this one's launch comes after; it reads that
+// through the L2 (TMA, __ldcg), where ended kernels' writes are.
+__device__ __forceinline__ void beside_previous() { cudaTriggerProgrammaticLaunchCompletion(); }
+__device__ __forceinline__ void end_after_previous(bool last_cta) {
+  if (last_cta) cudaGridDependencySynchronize();
+}
 #endif
 
 // Device address of this device's status word (timeouts of bounded waits);

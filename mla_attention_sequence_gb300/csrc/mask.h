@@ -28,8 +28,8 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t v) {  // exact
 // Eight values (chunk `c` of the row) as packed bf16, for cols a multiple of 32: exact but for
 // values below bf16's normal range.
 __device__ __forceinline__ uint4 unpack8_bf16x8(const Packed& p, long long row, int cols, int c) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p.codes + row * cols + c * 8);
-  const float s = scale_value(p.scales[row * (cols / kPackBlock) + (c >> 2)]);
+  const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p.codes + row * cols + c * 8));
+  const float s = scale_value(__ldcg(p.scales + row * (cols / kPackBlock) + (c >> 2)));
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -42,7 +42,7 @@ __device__ __forceinline__ uint4 unpack8_bf16x8(const Packed& p, long long row, 
 
 __device__ __forceinline__ float unpack8_value(const Packed& p, long long row, int cols, int k) {
   const int blocks = (cols + kPackBlock - 1) / kPackBlock;
-  return e4m3x2_to_float2(p.codes[row * cols + k]).x * scale_value(p.scales[row * blocks + k / kPackBlock]);
+  return e4m3x2_to_float2(__ldcg(p.codes + row * cols + k)).x * scale_value(__ldcg(p.scales + row * blocks + k / kPackBlock));
 }
 
 // Whether one of the keys [lo, hi) has its bit set: words step by step from `from`, every `step`th.
@@ -82,15 +82,16 @@ LaunchResult mask_key_bounds(const Dims& d, const int* starts, int n_docs, const
 
 // Row statistics of the masked backward (w.lse2, w.delta) and, if some q or dout row is not
 // finite, clean copies; with q8 / out8, q and out come from checkpoints and q_clean is written.
-// check_q: a non-finite q may have a finite lse (capped scores).
+// check_q: a non-finite q may have a finite lse (capped scores). beside: the kernel launched just
+// before is the rebuild, which writes nothing that this reads.
 LaunchResult tc_mask_bwd_pre(const Dims& d, const bf16* q, const bf16* out, const Packed* q8, const Packed* out8,
                              const bf16* dout, const float* lse, const BwdWorkspace& w, bf16* q_clean,
-                             bf16* dout_clean, int* q_bad, bool check_q, cudaStream_t st);
+                             bf16* dout_clean, int* q_bad, bool check_q, bool beside, cudaStream_t st);
 
 // ---- CUDA cores, any widths up to 256: fp32 K/V, fp32 arithmetic.
 LaunchResult simt_mask_bwd_pre(const Dims& d, bool is_bf16, const void* q, const void* out, const Packed* q8,
                                const Packed* out8, const void* dout, const float* lse, float* lse_row, float* delta,
-                               float* q_clean, float* dout_clean, cudaStream_t st);
+                               float* q_clean, float* dout_clean, bool beside, cudaStream_t st);
 size_t simt_masked_fwd_workspace(const Dims& d, int elem);
 size_t simt_masked_bwd_workspace(const Dims& d, int elem);
 LaunchResult simt_masked_fwd(const Dims& d, bool is_bf16, const ScoreMods& mods, const int* key_lo, const int* key_hi,

@@ -312,8 +312,11 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
                                                            const bf16* __restrict__ dout,
                                                            const float* __restrict__ lse, float* __restrict__ lse2,
                                                            float* __restrict__ delta, bf16* __restrict__ q_clean,
-                                                           int* __restrict__ q_bad) {
-  after_previous();
+                                                           int* __restrict__ q_bad, bool beside) {
+  if (beside)
+    beside_previous();
+  else
+    after_previous();
   const ll row = (static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
   const ll rows = static_cast<ll>(d.B) * d.sq_pad * d.n_h;
   const int l16 = threadIdx.x & 15;
@@ -327,19 +330,19 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
   float acc = 0.f;
   bool bad = false;
   uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
-  const float row_lse = in ? lse[(static_cast<ll>(b) * d.n_h + h) * d.Sq + i] : -INFINITY;
+  const float row_lse = in ? __ldcg(&lse[(static_cast<ll>(b) * d.n_h + h) * d.Sq + i]) : -INFINITY;
   if (in) {
-    const uint4 g = reinterpret_cast<const uint4*>(dout + src * 128)[l16];
+    const uint4 g = __ldcg(reinterpret_cast<const uint4*>(dout + src * 128) + l16);
     uint4 a;
     if constexpr (PACKED) {
       a = unpack8_bf16x8(out8, src, 128, l16);
       q0 = unpack8_bf16x8(q8, src, 192, l16);
       if (l16 < 8) q1 = unpack8_bf16x8(q8, src, 192, 16 + l16);
     } else {
-      a = reinterpret_cast<const uint4*>(out + src * 128)[l16];
+      a = __ldcg(reinterpret_cast<const uint4*>(out + src * 128) + l16);
       if (CHECK_Q || !finite(row_lse)) {
-        q0 = reinterpret_cast<const uint4*>(q + src * 192)[l16];
-        if (l16 < 8) q1 = reinterpret_cast<const uint4*>(q + src * 192)[16 + l16];
+        q0 = __ldcg(reinterpret_cast<const uint4*>(q + src * 192) + l16);
+        if (l16 < 8) q1 = __ldcg(reinterpret_cast<const uint4*>(q + src * 192) + 16 + l16);
       }
     }
     bad = bad_bf16x8(g) || bad_bf16x8(q0) || bad_bf16x8(q1);
@@ -381,6 +384,7 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
     lse2[at] = L;
     delta[at] = D;
   }
+  if (beside) end_after_previous(blockIdx.x == gridDim.x - 1);
 }
 
 // Runs only when *q_bad is set: clean copies of q (unless it was unpacked already) and dout.
@@ -424,8 +428,12 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_any_kernel(Dims d, const T* 
                                                                const Packed q8, const Packed out8, bool packed,
                                                                const T* __restrict__ dout, const float* __restrict__ lse,
                                                                float* __restrict__ lse_row, float* __restrict__ delta,
-                                                               float* __restrict__ q_clean, float* __restrict__ dout_clean) {
-  after_previous();
+                                                               float* __restrict__ q_clean, float* __restrict__ dout_clean,
+                                                               bool beside) {
+  if (beside)
+    beside_previous();
+  else
+    after_previous();
   const ll row = (static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const ll rows = static_cast<ll>(d.B) * d.Sq * d.n_h;
   if (row >= rows) return;
@@ -434,23 +442,23 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_any_kernel(Dims d, const T* 
   const ll bi = row / d.n_h;
   const int i = static_cast<int>(bi % d.Sq);
   const int b = static_cast<int>(bi / d.Sq);
-  auto q_at = [&](int k) { return packed ? unpack8_value(q8, row, dqk, k) : to_f(q[row * dqk + k]); };
+  auto q_at = [&](int k) { return packed ? unpack8_value(q8, row, dqk, k) : to_f(__ldcg(q + row * dqk + k)); };
   float acc = 0.f;
   bool bad = false;
   for (int k = lane; k < dqk; k += 32) bad |= !finite(q_at(k));
   for (int k = lane; k < d.d_v; k += 32) {
-    const float g = to_f(dout[row * d.d_v + k]);
+    const float g = to_f(__ldcg(dout + row * d.d_v + k));
     bad |= !finite(g);
-    acc = fmaf(packed ? unpack8_value(out8, row, d.d_v, k) : to_f(out[row * d.d_v + k]), g, acc);
+    acc = fmaf(packed ? unpack8_value(out8, row, d.d_v, k) : to_f(__ldcg(out + row * d.d_v + k)), g, acc);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
   bad = __any_sync(0xffffffffu, bad);
   for (int k = lane; k < dqk; k += 32) q_clean[row * dqk + k] = bad ? 0.f : q_at(k);
-  for (int k = lane; k < d.d_v; k += 32) dout_clean[row * d.d_v + k] = bad ? 0.f : to_f(dout[row * d.d_v + k]);
+  for (int k = lane; k < d.d_v; k += 32) dout_clean[row * d.d_v + k] = bad ? 0.f : to_f(__ldcg(dout + row * d.d_v + k));
   if (lane == 0) {
     const ll at = (static_cast<ll>(b) * d.n_h + h) * d.Sq + i;
-    const float v = lse[at];
+    const float v = __ldcg(lse + at);
     float L = v, D = acc;
     if (v == -INFINITY) {
       L = INFINITY;
@@ -462,6 +470,7 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_any_kernel(Dims d, const T* 
     lse_row[at] = L;
     delta[at] = D;
   }
+  if (beside) end_after_previous(blockIdx.x == gridDim.x - 1);
 }
 
 }  // namespace
@@ -532,14 +541,14 @@ LaunchResult mask_key_bounds(const Dims& d, const int* starts, int n_docs, const
 
 LaunchResult tc_mask_bwd_pre(const Dims& d, const bf16* q, const bf16* out, const Packed* q8, const Packed* out8,
                              const bf16* dout, const float* lse, const BwdWorkspace& w, bf16* q_clean,
-                             bf16* dout_clean, int* q_bad, bool check_q, cudaStream_t st) {
+                             bf16* dout_clean, int* q_bad, bool check_q, bool beside, cudaStream_t st) {
   LaunchResult r;
   const ll rows = static_cast<ll>(d.B) * d.sq_pad * d.n_h;
   const unsigned grid = static_cast<unsigned>((rows + 15) / 16);
   const auto kern = q8 ? mask_bwd_pre_kernel<true, true>
                        : check_q ? mask_bwd_pre_kernel<false, true> : mask_bwd_pre_kernel<false, false>;
   r.err = launch_next(kern, grid, 256, 0, st, d, q, out, q8 ? *q8 : Packed{}, out8 ? *out8 : Packed{}, dout, lse, w.lse2,
-                      w.delta, q_clean, q_bad);
+                      w.delta, q_clean, q_bad, beside);
   if (r.err == cudaSuccess)
     r.err = launch_next(mask_clean_kernel, 2 * sm_count(), 256, 0, st, static_cast<ll>(d.B) * d.Sq * d.n_h,
                         q8 ? nullptr : q, dout, q_clean, dout_clean, q_bad);
@@ -549,7 +558,7 @@ LaunchResult tc_mask_bwd_pre(const Dims& d, const bf16* q, const bf16* out, cons
 
 LaunchResult simt_mask_bwd_pre(const Dims& d, bool is_bf16, const void* q, const void* out, const Packed* q8,
                                const Packed* out8, const void* dout, const float* lse, float* lse_row, float* delta,
-                               float* q_clean, float* dout_clean, cudaStream_t st) {
+                               float* q_clean, float* dout_clean, bool beside, cudaStream_t st) {
   LaunchResult r;
   const ll rows = static_cast<ll>(d.B) * d.Sq * d.n_h;
   const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
@@ -557,7 +566,7 @@ LaunchResult simt_mask_bwd_pre(const Dims& d, bool is_bf16, const void* q, const
   auto run = [&](auto* kern, auto* type) {
     using T = std::remove_pointer_t<decltype(type)>;
     return launch_next(kern, grid, 256, 0, st, d, static_cast<const T*>(q), static_cast<const T*>(out), a, o,
-                       q8 != nullptr, static_cast<const T*>(dout), lse, lse_row, delta, q_clean, dout_clean);
+                       q8 != nullptr, static_cast<const T*>(dout), lse, lse_row, delta, q_clean, dout_clean, beside);
   };
   r.err = is_bf16 ? run(mask_bwd_pre_any_kernel<bf16>, static_cast<bf16*>(nullptr))
                   : run(mask_bwd_pre_any_kernel<float>, static_cast<float*>(nullptr));

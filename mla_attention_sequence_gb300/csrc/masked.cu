@@ -221,7 +221,7 @@ laga_status laga_mla_masked_bwd(const laga_mla_desc* desc, const laga_mla_mods* 
   if (r.ok())
     r = timed("masked_bwd_pre", s, [&] {
       return tc_mask_bwd_pre(d, cb(q), cb(out), packed ? &pq : nullptr, packed ? &po : nullptr, cb(dout), lse, w, q_clean,
-                             dout_clean, m.q_bad, sm.cap > 0.f, s);
+                             dout_clean, m.q_bad, sm.cap > 0.f, !reuse, s);
     });
   if (r.ok())
     r = timed("masked_attn_bwd_dkdv", s,

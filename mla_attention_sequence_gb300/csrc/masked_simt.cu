@@ -853,7 +853,7 @@ LaunchResult simt_masked_bwd(const Dims& d, bool is_bf16, const ScoreMods& mods,
     r.err = rebuild(d, is_bf16, w.mask.c_kv, W_UK, W_UV, w.kn, w.v, st);
     if (r.err != cudaSuccess) r.what = "K/V rebuild (CUDA cores)";
   }
-  if (r.ok()) r = simt_mask_bwd_pre(d, is_bf16, q, out, q8, out8, dout, lse, w.lse_row, w.delta, w.q, w.dout, st);
+  if (r.ok()) r = simt_mask_bwd_pre(d, is_bf16, q, out, q8, out8, dout, lse, w.lse_row, w.delta, w.q, w.dout, !reuse_kv, st);
   if (!r.ok()) return r;
   SimtParams p = params(d, is_bf16, mods, w);
   p.q = w.q;
