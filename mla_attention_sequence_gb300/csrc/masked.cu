@@ -300,15 +300,22 @@ laga_status laga_mla_rope(const laga_mla_rope_desc* desc, const void* pos, const
   for (const void* p : {q, k_rope, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
     if (reinterpret_cast<uintptr_t>(p) & (e - 1))
       return fail(LAGA_ERR_INVALID_ARG, "rope: tensors must be aligned to their type%s");
-  RopeTable t{};
-  int i = 0;
-  for (int a = 0; a < x.n_axes; ++a)
-    for (int k = 0; k < x.sections[a]; ++k, ++i) {
-      // f(i) / (2 pi) <= 0.16 turns per step, so the fraction fits 64 bits
-      const double turns = std::pow(x.theta, -2.0 * i / static_cast<double>(x.d_rope)) * 0.15915494309189533577;
-      t.turns[i] = static_cast<uint64_t>(std::ldexp(turns, 64));
-      t.axis[i] = static_cast<uint8_t>(a);
-    }
+  // The table of the last call's frequencies, per thread: a program's calls share theta and the
+  // sections, and its powers are half of a small call's host time.
+  static thread_local RopeTable t;
+  static thread_local laga_mla_rope_desc made;  // n_axes 0: none
+  if (made.n_axes != x.n_axes || made.d_rope != x.d_rope || made.theta != x.theta ||
+      !std::equal(x.sections, x.sections + x.n_axes, made.sections)) {
+    int i = 0;
+    for (int a = 0; a < x.n_axes; ++a)
+      for (int k = 0; k < x.sections[a]; ++k, ++i) {
+        // f(i) / (2 pi) <= 0.16 turns per step, so the fraction fits 64 bits
+        const double turns = std::pow(x.theta, -2.0 * i / static_cast<double>(x.d_rope)) * 0.15915494309189533577;
+        t.turns[i] = static_cast<uint64_t>(std::ldexp(turns, 64));
+        t.axis[i] = static_cast<uint8_t>(a);
+      }
+    made = x;
+  }
   RopeArgs g{};
   g.tokens = x.tokens;
   g.n_h = static_cast<int>(x.n_h);

@@ -330,6 +330,9 @@ def _code_of(dtype: torch.dtype) -> int:
 def _expect(name: str, t: torch.Tensor, shape, dtypes, device) -> int:
     """The address of a contiguous CUDA tensor of that shape, type and device; an error that names it
     otherwise."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype in dtypes and t.shape == shape \
+            and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise RuntimeError(f"{name}: LAGA MLA runs on CUDA tensors only")
     if t.device != device:
@@ -338,9 +341,7 @@ def _expect(name: str, t: torch.Tensor, shape, dtypes, device) -> int:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 # The current stream's handle without the Stream object around it (2 us of a small call).
@@ -475,9 +476,14 @@ def rope(q, k_rope, pos, sections=None, theta: float = 10000.0, interleaved: boo
         raise ValueError(f"one section per axis of pos, at most {ROPE_MAX_AXES}")
     if q_out is None:
         q_out = torch.empty(shape, dtype=dt, device=dev)
+        q_at = q_out.data_ptr()
+    else:
+        q_at = _expect("q_out", q_out, shape, (dt,), dev)
     if k_out is None:
         k_out = torch.empty(k_shape, dtype=dt, device=dev)
-    q_at, k_at = _expect("q_out", q_out, shape, (dt,), dev), _expect("k_out", k_out, k_shape, (dt,), dev)
+        k_at = k_out.data_ptr()
+    else:
+        k_at = _expect("k_out", k_out, k_shape, (dt,), dev)
     if shape[0] * shape[1] == 0:  # no tokens: nothing turns
         return q_out, k_out
     d = _rope_desc(shape, d_rope, sections, float(theta), bool(interleaved), bool(inverse), pos.dtype == torch.int64,
@@ -530,11 +536,12 @@ class _MaskedCall:
                 raise ValueError(f"q is on {q.device}, the other tensors on {self.dev}")
         else:
             self.q = _expect("q", q, q.shape, (self.dt,), self.dev)
-        self.x = [_expect(n, t, t.shape, (self.dt,), self.dev)
-                  for n, t in (("c_kv", c_kv), ("k_rope", k_rope), ("W_UK", W_UK), ("W_UV", W_UV))]
+        dts, dev = (self.dt,), self.dev
+        sizes = c_kv.shape, k_rope.shape, W_UK.shape, W_UV.shape
+        self.x = (_expect("c_kv", c_kv, sizes[0], dts, dev), _expect("k_rope", k_rope, sizes[1], dts, dev),
+                  _expect("W_UK", W_UK, sizes[2], dts, dev), _expect("W_UV", W_UV, sizes[3], dts, dev))
         self.p, self.desc, self.reuse, self.fwd_bytes, self.bwd_bytes = _masked_plan(
-            q.shape, c_kv.shape, k_rope.shape, W_UK.shape, W_UV.shape, self.dt, int(q_offset), bool(causal),
-            softmax_scale, variant, int(q_split), int(q_offset2))
+            q.shape, *sizes, self.dt, int(q_offset), bool(causal), softmax_scale, variant, int(q_split), int(q_offset2))
 
     def mods(self, key_lo, key_hi, softcap, slopes) -> LagaMods:
         p, dev = self.p, self.dev
