@@ -30,7 +30,8 @@
 //
 // Masked instances (MOD >= 0): the CTA walks the key tiles between the lowest and the
 // highest key its rows see, as in the forward; with a cap, dS takes the factor
-// 1 - tanh^2 of its score.
+// 1 - tanh^2 of its score. With short documents a CTA's start and end (~9 us around key tiles of
+// ~1.2 us) are most of its time: 2 x 4096 rows of 16 heads, 5 documents and a bias: 123 us.
 #include "internal.h"
 #include "ptx.cuh"
 #include "score_mod.cuh"

@@ -6,12 +6,17 @@
 //   P = 2^(t2 - m), l = sum P, O = sum P V, out = O / l, lse = (m + log2 l) / log2(e)
 //
 // A packed batch is many short key ranges: one CTA per query tile spent ~9 us a tile on its
-// own start and end, around 1 to 5 key tiles of 0.7 us (a 2 x 4096 batch of 40 documents: 67
-// us, 4 us of it products). So one CTA per SM stays and takes (head, query tile) items from a
-// ticket, longest of a head first, and a new item's tiles enter the pipeline while the last
-// one's are still in it. And the masked softmax is longer than the plain one (a bias: +70% of
-// the instructions, a cap: twice), at one warp per scheduler issuing every third cycle: two
-// warpgroups share the score tiles, one the even ones, one the odd ones.
+// own start and end, around 1 to 5 key tiles of 0.7 us. So one CTA per SM stays and takes (head,
+// query tile) items from a ticket, longest of a head first, and a new item's tiles enter the
+// pipeline while the last one's are still in it. And the masked softmax is longer than the plain
+// one (a bias: +70% of the instructions, a cap: twice), at one warp per scheduler issuing every
+// third cycle: two warpgroups share the score tiles, one the even ones, one the odd ones.
+// 2 x 4096 rows of 16 heads in 1 / 5 / 40 documents, us, against one CTA per query tile:
+//   mask alone 178 / 90 / 52 (143 / 92 / 67)   bias 198 / 103 / 58 (234 / 124 / 78)
+//   cap 268 / 143 / 75 (269 / 168 / 96)
+// What bounds it: a 128 x 128 tile's products move 208 KB through shared memory, 1625 cycles at
+// 128 B a cycle, and take ~2100 with their hand-offs; a warpgroup has twice that for its softmax
+// and needs ~2600. S(g) -> P(g) -> S(g + 3) is the chain that sets the pace.
 //
 // Warp roles (384 threads):
 //   warp 0      lane 0: tickets and the item ring; TMA for Q (per item) and K tiles
@@ -28,7 +33,7 @@
 //
 // The softmax makes one pass over a score tile, a loop of four chunks of 32 columns (unrolled, it
 // outgrows the instruction cache and its warps wait for instructions; a second pass for the
-// maximum costs four more TMEM round trips of some 500 cycles each beside the MMAs). Its weights
+// maximum reads the tile from TMEM and caps it twice). Its weights
 // count in 2^m for a reference m that is 0 until scores turn out to be further than 2^100 off;
 // then m moves, and what was written of the tile so far is scaled. At a tile's end the warpgroup
 // settles m with the one that tile g - 1 left for the row in shared memory (the larger stays;

@@ -11,6 +11,9 @@
 // backward). The latent is small (d_c + d_rope values per key, shared by all heads),
 // so its copy is always made: 2 x 19 MB at 16384 keys. q and dout are copied only when
 // a row of theirs is non-finite, which the pass that computes D sees.
+//
+// All of it is launches and latency, not work: the two launches take 11 us for 519 keys and 15
+// for 2 x 4096 (rows, keys and tiles in a launch each took 18 and 23).
 #include "internal.h"
 #include "mask.h"
 
@@ -305,7 +308,8 @@ __global__ void key_bounds_kernel(Dims d, const int* __restrict__ starts, int n_
 // if the row is bad), out is only summed. Otherwise q is read for its finiteness alone: with a
 // cap (CHECK_Q) always, else only where lse is not finite, because every score of a row whose q
 // is not finite is not finite, and so is its lse (a cap makes finite scores of infinite ones).
-// That leaves 2 of 7 bytes a value unread.
+// That leaves 3 of 7 bytes unread (q has 192 values a row, dout and out 128 each). Bound by
+// memory: 2 x 4096 rows of 16 heads, 67 MB, in 24 us with everything from DRAM.
 template <bool PACKED, bool CHECK_Q>
 __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* __restrict__ q, const bf16* __restrict__ out,
                                                            const Packed q8, const Packed out8,
