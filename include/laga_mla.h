@@ -257,7 +257,7 @@ typedef struct {
   const int32_t* key_lo; /* [B, Sq], device; NULL: 0 */
   const int32_t* key_hi; /* [B, Sq], device, one past the last visible key; NULL: skv */
   const float* slopes;   /* [n_h], device; NULL: none */
-  float softcap;         /* 0: none; else finite and > 0 */
+  float softcap;         /* 0: none; else between 1e-20 and 1e30 */
 } laga_mla_mods;
 
 /* A tensor saved in 8 bits by laga_mla_pack8 (rows of the tensor's last dimension). */

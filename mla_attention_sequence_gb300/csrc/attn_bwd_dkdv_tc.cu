@@ -605,7 +605,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               const float raw = __uint_as_float(u[k]);
               float t2;
               if constexpr (CAP) {
-                u[k] = __float_as_uint(tanh_abs(raw * p.mod.u_scale));  // kept for dS's factor
+                const float v = raw * p.mod.u_scale;
+                u[k] = __float_as_uint((MOD & kModFar) != 0 ? tanh_rel(v) : tanh_abs(v));  // kept for dS's factor
                 t2 = fmaf(p.mod.cap_log2, __uint_as_float(u[k]), -lse[k]);
               } else {
                 t2 = fmaf(raw, p.scale_log2, -lse[k]);
@@ -841,11 +842,13 @@ LaunchResult tc_attn_bwd_dkdv(const Dims& d, const bf16* q, const bf16* k_rope, 
     p.q_bad = mask->meta.q_bad;
     p.mod = mod_params(d, mask->mods);
     smem = SMEM_BYTES_MASKED;
-    switch (mod_of(mask->mods)) {
+    switch (mod_of(mask->mods) | (mask->mods.cap > kFarCap ? kModFar : 0)) {
       case 0: kern = attn_bwd_dkdv_kernel<0>; break;
       case kModCap: kern = attn_bwd_dkdv_kernel<kModCap>; break;
       case kModBias: kern = attn_bwd_dkdv_kernel<kModBias>; break;
-      default: kern = attn_bwd_dkdv_kernel<kModCap | kModBias>; break;
+      case kModCap | kModBias: kern = attn_bwd_dkdv_kernel<kModCap | kModBias>; break;
+      case kModCap | kModFar: kern = attn_bwd_dkdv_kernel<kModCap | kModFar>; break;
+      default: kern = attn_bwd_dkdv_kernel<kModCap | kModBias | kModFar>; break;
     }
   }
   r.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -48,8 +48,9 @@ Path masked_plan(const laga_mla_desc* desc, Dims* d, laga_status* st, bool for_b
 laga_status check_mods(const laga_mla_mods* mods, ScoreMods* out) {
   *out = ScoreMods{0.f, nullptr};
   if (!mods) return LAGA_OK;
-  if (!(mods->softcap >= 0.f) || !std::isfinite(mods->softcap))
-    return fail(LAGA_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: none)%s");
+  // outside this range cap or 1 / cap, times the other factors of a score, leaves fp32
+  if (mods->softcap != 0.f && !(mods->softcap >= 1e-20f && mods->softcap <= 1e30f))
+    return fail(LAGA_ERR_INVALID_ARG, "softcap must be 0 (none) or between 1e-20 and 1e30%s");
   auto aligned4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
   if (!aligned4(mods->key_lo) || !aligned4(mods->key_hi) || !aligned4(mods->slopes))
     return fail(LAGA_ERR_INVALID_ARG, "key_lo, key_hi and slopes must be 4-byte aligned%s");

@@ -31,6 +31,13 @@ __device__ __forceinline__ float tanh_abs(float u) {
   return 1.f - __fdividef(2.f, 1.f + ex2_approx(u * 2.8853900817779268f));
 }
 
+// The same for caps so large that 1e-7 of them shows (kModFar): the first terms of tanh's series
+// for small u, exact there to 1e-7 of tanh(u) itself.
+__device__ __forceinline__ float tanh_rel(float u) {
+  const float w = u * u;
+  return fabsf(u) < 0.1f ? u * fmaf(w, fmaf(w, 2.f / 15.f, -1.f / 3.f), 1.f) : tanh_abs(u);
+}
+
 // Two fp32 values in one 64-bit register: products and sums of pairs are one instruction.
 struct F2 {
   uint64_t v;

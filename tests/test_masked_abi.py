@@ -54,7 +54,7 @@ def test_forward_refusals(L):
     assert fwd(L, desc(), o=P + 1) == 1
     assert fwd(L, desc(), r=None) == 1
     assert fwd(L, desc(q_offset=15000)) == 1  # a causal shard past the latent
-    for cap in (-1.0, float("nan"), float("inf")):
+    for cap in (-1.0, float("nan"), float("inf"), 1e-30, 3e38):
         assert fwd(L, desc(), mods(cap=cap)) == 1
         assert b"softcap" in L.laga_mla_last_error()
     assert fwd(L, desc(), mods(lo=P + 2)) == 1

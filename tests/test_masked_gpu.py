@@ -241,6 +241,16 @@ def test_non_finite_values_in_masked_places(dtype, dims, value):
         assert got["dq"][row].isnan().all() and torch.equal(got["dq"][~row], clean["dq"][~row])
 
 
+@pytest.mark.parametrize("dtype,dims", [(torch.bfloat16, DSV3), (torch.float32, (32, 16, 8, 24))])
+@pytest.mark.parametrize("softcap,bias", [(1e-20, False), (600.0, False), (2e4, True), (1e30, False)])
+def test_caps_from_one_end_of_their_range_to_the_other(dtype, dims, softcap, bias):
+    """The smallest makes every visible key weigh the same (and no score a gradient), the largest does
+    nothing; tanh of a score far below its cap has to be right relative to the score."""
+    x, dout = inputs(1, 140, 140, 2, dims, dtype, 8)
+    lo, hi = random_bounds(1, 140, 140, 3)
+    check(x, dout, key_lo=lo, key_hi=hi, softcap=softcap, slopes=slopes(2) if bias else None)
+
+
 @pytest.mark.parametrize("dtype,dims,S", [(torch.bfloat16, DSV3, 130), (torch.bfloat16, DSV3, 8192),
                                           (torch.float32, (32, 16, 8, 24), 130)])
 def test_scores_that_are_all_minus_infinity(dtype, dims, S):
@@ -497,6 +507,51 @@ def test_chain_captured_in_a_graph_and_on_another_stream():
     new = chain(x, pos, case[2], sections, dout)
     for k in new:
         assert torch.equal(got[k], new[k]), k
+    laga.check(dev())
+
+
+@pytest.mark.parametrize("dtype,dims", [(torch.bfloat16, DSV3), (torch.float32, (32, 16, 8, 24))])
+def test_captured_behind_copies_and_a_join_of_streams(dtype, dims):
+    """The chain's first kernel behind a copy, behind another stream's work and behind a chain that shares
+    its workspace; two such graphs replayed one after the other without a wait between them."""
+    kw = dict(softcap=9.0, slopes=slopes(3))
+    problems, graphs, results = [], [], []
+    x0, dout0 = inputs(1, 300, 300, 3, dims, dtype, 41)
+    ws = laga.masked_workspace(*x0.values(), **kw)
+    for seed, starts in ((41, [0, 100, 290]), (42, [0, 33, 34, 300])):
+        x, dout = inputs(1, 300, 300, 3, dims, dtype, seed)
+        st = torch.tensor([starts], dtype=torch.int32, device=dev())
+        problems.append((x, dout, st))
+
+    def work(x, dout, st):
+        y = {k: v.clone() for k, v in x.items()}
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            lo, hi = laga.key_bounds(st, 300)
+            q8 = laga.pack8(y["q"])
+        torch.cuda.current_stream().wait_stream(side)
+        m = dict(kw, key_lo=lo, key_hi=hi, workspace=ws)
+        out, lse = laga.masked_fwd(*y.values(), **m)
+        g = laga.masked_bwd(*y.values(), out, lse, dout, reuse_kv=True, **m)
+        h = laga.masked_bwd(q8, *list(y.values())[1:], laga.pack8(out), lse, dout, **m)
+        return {"out": out, "lse": lse, **g, **{k + " packed": v for k, v in h.items()}}
+
+    want = [work(*p) for p in problems]
+    torch.cuda.synchronize()
+    for p in problems:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            results.append(work(*p))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    for got, w in zip(results, want):
+        for k in w:
+            assert torch.equal(got[k], w[k]), k
     laga.check(dev())
 
 
