@@ -37,18 +37,26 @@ struct LaunchResult {
 // touches global memory; the call returns when every earlier kernel of the chain has ended and
 // its writes are visible, and lets the next one start.
 template <class... P, class... A>
-cudaError_t launch_next(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A&&... args) {
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_next_in_clusters(int ctas, void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                                    A&&... args) {
+  cudaLaunchAttribute attrs[2] = {};
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;  // along x
+  attrs[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t c{};
   c.gridDim = grid;
   c.blockDim = block;
   c.dynamicSmemBytes = smem;
   c.stream = st;
-  c.attrs = &early;
-  c.numAttrs = 1;
+  c.attrs = attrs;
+  c.numAttrs = ctas > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&c, kern, std::forward<A>(args)...);
+}
+template <class... P, class... A>
+cudaError_t launch_next(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A&&... args) {
+  return launch_next_in_clusters(1, kern, grid, block, smem, st, std::forward<A>(args)...);
 }
 #ifdef __CUDACC__
 __device__ __forceinline__ void after_previous() {

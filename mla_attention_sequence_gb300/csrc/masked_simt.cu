@@ -8,17 +8,25 @@
 // Thread (tx, ty) of 16 x 16 owns tile rows RI ty .. RI ty + RI - 1 and, of the score tile,
 // columns tx, tx + 16, ...; of a head-wide accumulator, columns 64 c + 4 tx .. + 3.
 // N = ceil(widest head / 64) picks the accumulator's width, RI the rows. More rows a thread
-// mean more multiply-adds per shared-memory load, fewer mean more CTAs, and a problem of a few
-// hundred rows fills few SMs, each walking its keys alone. Measured forward / backward, us:
-//   256 rows x 4 heads, d 48 / 32       RI 1: 39 / 54    2: 42 / 59     4: 50 / 76
-//   2 x 1024 x 6, d 64 / 56             RI 1: 156 / 340  2: 136 / 285   4: 144 / 316
-//   4096 x 8, d 96 / 96                                  2: 3127 / 5542 4: 1964 / 6754
+// mean more multiply-adds per shared-memory load, fewer mean more CTAs. And a cluster of CTAs
+// shares a tile's walk, each taking every second or fourth step, the results merged through
+// distributed shared memory: walks differ in length (causal rows, documents), the longest sets
+// the time, and a CTA alone on its SM waits for its own latencies. Measured forward / backward,
+// us, rows a thread x CTAs a tile:
+//   256 rows x 4 heads, d 48 / 32      1x1: 25 / 43      2x1: 29 / 44      2x4: 18 / 29
+//   2 x 509 x 3, d 64 / 56             1x1: 46 / 88      2x1: 50 / 84      2x2: 38 / 70
+//   1024 x 2, d 96 / 64                2x1: 162 / 310    2x4: 87 / 145     4x4: 59 / -
+//   4096 x 8, d 64 / 56, 6 documents   2x1: 420 / 983    2x2: 399 / 967    4x2: 415 / -
+//   4096 x 8, d 96 / 96                2x1: 3200 / 5576  2x2: 3025 / 5173  4x2: 1745 / -
+//   600 x 4, d 192 / 128               2x1: 133 / 256    2x2: 83 / 169     4x2: 100 / -
+//   2048 x 4, d 192 / 128              2x1: 635 / 1237   2x2: 531 / 1018   4x2: 453 / -
 // A tile's global loads are issued eight rows deep per warp, lanes along the width, and where
 // the registers allow it a step ahead; one value at a time cost 14 us per key step.
-// What bounds the small problems is each CTA's walk: with one or two CTAs on an SM the schedulers
-// issue in 36% (forward) and 42% (backward) of the cycles, waiting for shared memory and for each
-// other's arithmetic (2 x 509 rows of 3 heads: 35 and 60 us).
+// What bounds it is still each CTA's walk: the schedulers wait for shared memory and for each
+// other's arithmetic more than they issue.
 #include "mask.h"
+
+#include <cooperative_groups.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -35,6 +43,7 @@ __host__ __device__ __forceinline__ int pitch4(int width) { return ((width + 3) 
 
 struct SimtParams {
   Dims d;
+  int splits;            // CTAs (a cluster) that share a tile's walk, every splits-th step each
   const void* q;         // [B][Sq][n_h][d_qk]; the forward's in the inputs' type, else fp32
   bool q_bf16;
   const float* kn;       // [B][S][n_h][d_nope]
@@ -146,10 +155,8 @@ __device__ __forceinline__ void put_weights(float* w, int n, int ty, const float
   float* d = w + (n * 17 + ty) * RI;
   if constexpr (RI == 4)
     *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
-  else if constexpr (RI == 2)
-    *reinterpret_cast<float2*>(d) = make_float2(v[0], v[1]);
   else
-    d[0] = v[0];
+    *reinterpret_cast<float2*>(d) = make_float2(v[0], v[1]);
 }
 
 // acc[i][c] += sum_n Wt[n][RI ty + i] B[n][64 c + 4 tx ..]
@@ -271,6 +278,32 @@ __device__ __forceinline__ float half_warp_sum(float v) {
   return v;
 }
 
+// A cluster's CTAs put their threads' partial results into their shared memory (one that is free
+// by then), the first one takes the others' in order, and nobody leaves before that.
+template <int COUNT, class Take>
+__device__ __forceinline__ bool merge_in_cluster(const SimtParams& p, float4* buf, const float4 (&mine)[COUNT], Take&& take) {
+  if (p.splits == 1) return true;
+  namespace cg = cooperative_groups;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const unsigned rank = cluster.block_rank();
+  __syncthreads();
+  if (rank != 0)
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) buf[i * THREADS + threadIdx.x] = mine[i];
+  cluster.sync();
+  if (rank == 0)
+    for (int r = 1; r < p.splits; ++r) {
+      const float4* from = cluster.map_shared_rank(buf, r);
+      float4 v[COUNT];
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) v[i] = from[i * THREADS + threadIdx.x];
+      take(v);
+    }
+  cluster.sync();
+  return rank == 0;
+}
+__device__ __forceinline__ float4 plus(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
 // out and lse of 16 RI query rows of one head.
 template <int N, int RI>
 __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
@@ -280,7 +313,7 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
   const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v);
   float4 *sq = sm, *sk = sq + ROWS * pk, *sv = sk + KFWD * pk, *weights = sv + KFWD * pv;
   float* sp = reinterpret_cast<float*>(weights);
-  const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int t = blockIdx.x / p.splits, rank = blockIdx.x - t * p.splits, step = p.splits * KFWD, h = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int i0 = t * ROWS + RI * ty;  // this thread's first row
   after_previous();
@@ -303,14 +336,14 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
     for (int c = 0; c < N; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const int2 hull = p.q_hull[static_cast<ll>(b) * (d.sq_pad / 64) + t * ROWS / 64];  // of the 64 rows around
-  const int j_first = hull.x < hull.y ? hull.x / KFWD * KFWD : 0;
+  const int j_first = (hull.x < hull.y ? hull.x / KFWD * KFWD : 0) + rank * KFWD;
   StreamedPair<KFWD, N> kv;
   if (j_first < hull.y) kv.ahead(d.d_qk(), d.d_v, KRows{p, b, h, j_first}, VRows{p, b, h, j_first});
-  for (int j0 = j_first; j0 < hull.y; j0 += KFWD) {
+  for (int j0 = j_first; j0 < hull.y; j0 += step) {
     __syncthreads();
     kv.store(sk, pk, d.d_qk(), sv, pv, d.d_v, KRows{p, b, h, j0}, VRows{p, b, h, j0});
     __syncthreads();
-    if (j0 + KFWD < hull.y) kv.ahead(d.d_qk(), d.d_v, KRows{p, b, h, j0 + KFWD}, VRows{p, b, h, j0 + KFWD});
+    if (j0 + step < hull.y) kv.ahead(d.d_qk(), d.d_v, KRows{p, b, h, j0 + step}, VRows{p, b, h, j0 + step});
     float s[RI][4];
     score_tile<RI>(sq, sk, pk, (d.d_qk() + 3) / 4, tx, ty, s);
 #pragma unroll
@@ -352,6 +385,30 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
     __syncthreads();
     weighted_rows<RI, N>(sp, sv, pv, KFWD, (d.d_v + 3) / 4, tx, ty, o);
   }
+  float4 part[RI * (N + 1)];
+#pragma unroll
+  for (int i = 0; i < RI; ++i) {
+    part[i * (N + 1)] = make_float4(m[i], l[i], 0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < N; ++c) part[i * (N + 1) + 1 + c] = o[i][c];
+  }
+  const bool writes = merge_in_cluster(p, sm, part, [&](const float4 (&v)[RI * (N + 1)]) {
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      const float4 w = v[i * (N + 1)];
+      const float mn = fmaxf(m[i], w.x), base = mn == -INFINITY ? 0.f : mn;
+      const float a = expf(m[i] - base), g = expf(w.x - base);
+      l[i] = l[i] * a + w.y * g;
+      m[i] = mn;
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        const float4 x = v[i * (N + 1) + 1 + c];
+        o[i][c] = make_float4(o[i][c].x * a + x.x * g, o[i][c].y * a + x.y * g, o[i][c].z * a + x.z * g,
+                              o[i][c].w * a + x.w * g);
+      }
+    }
+  });
+  if (!writes) return;
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     // the row's 16 threads share the words of the keys it sees
@@ -378,7 +435,7 @@ __global__ void __launch_bounds__(THREADS) masked_simt_fwd(const SimtParams p) {
 
 // dq of 16 RI query rows of one head.
 template <int N, int RI>
-__device__ __forceinline__ void masked_simt_dq(const SimtParams& p, int t) {
+__device__ __forceinline__ void masked_simt_dq(const SimtParams& p, int t, int rank) {
   constexpr int ROWS = 16 * RI;
   extern __shared__ float4 sm[];
   const Dims& d = p.d;
@@ -409,14 +466,14 @@ __device__ __forceinline__ void masked_simt_dq(const SimtParams& p, int t) {
 #pragma unroll
     for (int c = 0; c < N; ++c) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int2 hull = p.q_hull[static_cast<ll>(b) * (d.sq_pad / 64) + t * ROWS / 64];  // of the 64 rows around
-  const int j_first = hull.x < hull.y ? hull.x / KBWD * KBWD : 0;
+  const int step = p.splits * KBWD, j_first = (hull.x < hull.y ? hull.x / KBWD * KBWD : 0) + rank * KBWD;
   StreamedPair<KBWD, N> kv;
   if (j_first < hull.y) kv.ahead(d.d_qk(), d.d_v, KRows{p, b, h, j_first}, VRows{p, b, h, j_first});
-  for (int j0 = j_first; j0 < hull.y; j0 += KBWD) {
+  for (int j0 = j_first; j0 < hull.y; j0 += step) {
     __syncthreads();
     kv.store(sk, pk, d.d_qk(), sv, pv, d.d_v, KRows{p, b, h, j0}, VRows{p, b, h, j0});
     __syncthreads();
-    if (j0 + KBWD < hull.y) kv.ahead(d.d_qk(), d.d_v, KRows{p, b, h, j0 + KBWD}, VRows{p, b, h, j0 + KBWD});
+    if (j0 + step < hull.y) kv.ahead(d.d_qk(), d.d_v, KRows{p, b, h, j0 + step}, VRows{p, b, h, j0 + step});
     float s[RI][2], dp[RI][2];
     score_tile<RI>(sq, sk, pk, (d.d_qk() + 3) / 4, tx, ty, s);
     score_tile<RI>(sdo, sv, pv, (d.d_v + 3) / 4, tx, ty, dp);
@@ -441,6 +498,14 @@ __device__ __forceinline__ void masked_simt_dq(const SimtParams& p, int t) {
     __syncthreads();
     weighted_rows<RI, N>(sds, sk, pk, KBWD, (d.d_qk() + 3) / 4, tx, ty, acc);
   }
+  float4 part[RI * N];
+#pragma unroll
+  for (int i = 0; i < RI * N; ++i) part[i] = acc[i / N][i % N];
+  const bool writes = merge_in_cluster(p, sm, part, [&](const float4 (&v)[RI * N]) {
+#pragma unroll
+    for (int i = 0; i < RI * N; ++i) acc[i / N][i % N] = plus(acc[i / N][i % N], v[i]);
+  });
+  if (!writes) return;
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     if (i0 + i >= d.Sq) continue;
@@ -459,7 +524,7 @@ __device__ __forceinline__ void masked_simt_dq(const SimtParams& p, int t) {
 
 // dK (both parts) and dV of 16 RI keys of one head.
 template <int N, int RI>
-__device__ __forceinline__ void masked_simt_dkv(const SimtParams& p, int t) {
+__device__ __forceinline__ void masked_simt_dkv(const SimtParams& p, int t, int rank) {
   constexpr int ROWS = 16 * RI;
   extern __shared__ float4 sm[];
   const Dims& d = p.d;
@@ -487,13 +552,18 @@ __device__ __forceinline__ void masked_simt_dkv(const SimtParams& p, int t) {
     return q0;
   };
   StreamedPair<KBWD, N> qd;
+  auto after = [&](int q0) {  // this CTA's next one
+    for (int k = 0; k < p.splits && q0 < d.Sq; ++k) q0 = next_tile(q0 + KBWD);
+    return q0;
+  };
   int q0 = next_tile(0);
+  for (int k = 0; k < rank && q0 < d.Sq; ++k) q0 = next_tile(q0 + KBWD);
   if (q0 < d.Sq) qd.ahead(d.d_qk(), d.d_v, QRows{p, b, h, q0}, DoRows{p, b, h, q0});
   for (int q1; q0 < d.Sq; q0 = q1) {
     __syncthreads();
     qd.store(sq, pk, d.d_qk(), sdo, pv, d.d_v, QRows{p, b, h, q0}, DoRows{p, b, h, q0});
     __syncthreads();
-    q1 = next_tile(q0 + KBWD);
+    q1 = after(q0);
     if (q1 < d.Sq) qd.ahead(d.d_qk(), d.d_v, QRows{p, b, h, q1}, DoRows{p, b, h, q1});
     float s[RI][2], dp[RI][2];
     score_tile<RI>(sk, sq, pk, (d.d_qk() + 3) / 4, tx, ty, s);
@@ -528,6 +598,20 @@ __device__ __forceinline__ void masked_simt_dkv(const SimtParams& p, int t) {
     weighted_rows<RI, N>(sp, sdo, pv, KBWD, (d.d_v + 3) / 4, tx, ty, dv);
     weighted_rows<RI, N>(sds, sq, pk, KBWD, (d.d_qk() + 3) / 4, tx, ty, dk);
   }
+  float4 part[2 * RI * N];
+#pragma unroll
+  for (int i = 0; i < RI * N; ++i) {
+    part[2 * i] = dk[i / N][i % N];
+    part[2 * i + 1] = dv[i / N][i % N];
+  }
+  const bool writes = merge_in_cluster(p, sm, part, [&](const float4 (&v)[2 * RI * N]) {
+#pragma unroll
+    for (int i = 0; i < RI * N; ++i) {
+      dk[i / N][i % N] = plus(dk[i / N][i % N], v[2 * i]);
+      dv[i / N][i % N] = plus(dv[i / N][i % N], v[2 * i + 1]);
+    }
+  });
+  if (!writes) return;
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     const int j = k0 + i;
@@ -556,10 +640,11 @@ template <int N, int RI>
 __global__ void __launch_bounds__(THREADS) masked_simt_bwd(const SimtParams p) {
   after_previous();
   const int q_blocks = (p.d.Sq + 16 * RI - 1) / (16 * RI);
-  if (static_cast<int>(blockIdx.x) < q_blocks)
-    masked_simt_dq<N, RI>(p, blockIdx.x);
+  const int t = blockIdx.x / p.splits, rank = blockIdx.x - t * p.splits;
+  if (t < q_blocks)
+    masked_simt_dq<N, RI>(p, t, rank);
   else
-    masked_simt_dkv<N, RI>(p, static_cast<int>(blockIdx.x) - q_blocks);
+    masked_simt_dkv<N, RI>(p, t - q_blocks, rank);
 }
 
 struct Ws {
@@ -615,12 +700,19 @@ SimtParams params(const Dims& d, bool is_bf16, const ScoreMods& mods, const Ws& 
   return p;
 }
 
-// Rows per thread, by the CTAs that gives: two once 32-row tiles fill the SMs, four (forward only)
-// once 64-row tiles fill them twice.
-int rows_per_thread(const Dims& d, int rows, bool bwd) {
-  const ll ctas = static_cast<ll>((rows + 63) / 64) * d.n_h * d.B;  // of 64 rows
-  if (!bwd && ctas >= 2 * sm_count()) return 4;
-  return 2 * ctas >= sm_count() ? 2 : 1;
+// Rows per thread and CTAs per tile, by the table at the top: four rows a thread (forward only;
+// the backward's accumulators leave no registers for them) where the accumulators are wide enough
+// to gain from it and, for the widest, the tiles many; four CTAs a tile as long as that does not
+// overfill the SMs, else two; never more than a walk can have steps.
+struct Tiling {
+  int rows, splits;
+};
+Tiling tiling(const Dims& d, int n, bool bwd) {
+  const ll of64 = (static_cast<ll>(bwd ? d.Sq + d.S : d.Sq) + 63) / 64 * d.n_h * d.B;  // tiles of 64 rows
+  const int rows = !bwd && (n == 2 || (n == 4 && of64 >= 64)) ? 4 : 2;
+  const int steps = bwd ? (std::max(d.Sq, d.S) + KBWD - 1) / KBWD : (d.S + KFWD - 1) / KFWD;
+  const int most = 4 * (of64 * 4 / rows) <= (bwd ? 512 : 256) ? 4 : 2;
+  return Tiling{rows, steps >= most ? most : steps >= 2 ? 2 : 1};
 }
 
 template <bool BWD, int N, int RI>
@@ -631,26 +723,35 @@ constexpr auto kernel_of() {
     return masked_simt_fwd<N, RI>;
 }
 
-template <bool BWD, int RI>
-cudaError_t launch_rows(const Dims& d, const SimtParams& p, cudaStream_t st) {
-  const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v), w = std::max(d.d_qk(), d.d_v);
+template <bool BWD, int N, int RI>
+cudaError_t launch_rows(const Dims& d, SimtParams p, int splits, cudaStream_t st) {
+  const int pk = pitch4(d.d_qk()), pv = pitch4(d.d_v);
   constexpr int R = 16 * RI;
-  const size_t smem = BWD ? sizeof(float4) * (R + KBWD) * (pk + pv) + sizeof(float) * 2 * KBWD * 17 * RI
-                          : sizeof(float4) * ((R + KFWD) * pk + KFWD * pv) + sizeof(float) * KFWD * 17 * RI;
+  size_t smem = BWD ? sizeof(float4) * (R + KBWD) * (pk + pv) + sizeof(float) * 2 * KBWD * 17 * RI
+                    : sizeof(float4) * ((R + KFWD) * pk + KFWD * pv) + sizeof(float) * KFWD * 17 * RI;
+  if (splits > 1) smem = std::max(smem, sizeof(float4) * THREADS * RI * (BWD ? 2 * N : N + 1));  // partial results
+  p.splits = splits;
   const int blocks = (d.Sq + R - 1) / R + (BWD ? (d.S + R - 1) / R : 0);
-  void (*kern)(SimtParams) =
-      w <= 64 ? kernel_of<BWD, 1, RI>() : w <= 128 ? kernel_of<BWD, 2, RI>() : kernel_of<BWD, 4, RI>();
+  void (*kern)(SimtParams) = kernel_of<BWD, N, RI>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_next(kern, dim3(blocks, d.n_h, d.B), THREADS, smem, st, p);
+  return launch_next_in_clusters(splits, kern, dim3(blocks * splits, d.n_h, d.B), THREADS, smem, st, p);
 }
 
 template <bool BWD>
 cudaError_t launch(const Dims& d, const SimtParams& p, cudaStream_t st) {
-  const int ri = rows_per_thread(d, BWD ? d.Sq + d.S : d.Sq, BWD);
-  if constexpr (!BWD)
-    if (ri == 4) return launch_rows<BWD, 4>(d, p, st);
-  return ri == 2 ? launch_rows<BWD, 2>(d, p, st) : launch_rows<BWD, 1>(d, p, st);
+  const int w = std::max(d.d_qk(), d.d_v), n = w <= 64 ? 1 : w <= 128 ? 2 : 4;
+  const Tiling t = tiling(d, n, BWD);
+  if constexpr (BWD) {
+    return n == 1   ? launch_rows<true, 1, 2>(d, p, t.splits, st)
+           : n == 2 ? launch_rows<true, 2, 2>(d, p, t.splits, st)
+                    : launch_rows<true, 4, 2>(d, p, t.splits, st);
+  } else {
+    return n == 1        ? launch_rows<false, 1, 2>(d, p, t.splits, st)
+           : n == 2      ? launch_rows<false, 2, 4>(d, p, t.splits, st)
+           : t.rows == 2 ? launch_rows<false, 4, 2>(d, p, t.splits, st)
+                         : launch_rows<false, 4, 4>(d, p, t.splits, st);
+  }
 }
 
 // ---- the rebuild's products: C[m][n] = sum over one or two pairs of A(m, k) B(k, n), any
@@ -659,7 +760,10 @@ cudaError_t launch(const Dims& d, const SimtParams& p, cudaStream_t st) {
 // order through shared memory. These products are small (a weight gradient is d_c x n_h d
 // with k = all keys): a few dozen tiles, so the k loop's latency is the time, and both the
 // small tile and the split shorten it (2 x 509 keys of width 72, 3 heads: the three gradients in
-// 31 us, where 64 x 64 tiles without the split took 182 for each dW).
+// 31 us, where 64 x 64 tiles without the split took 182 for each dW). Where k is long and the tiles
+// few, a cluster of two or four CTAs shares a tile's k too: the whole backward of that problem takes
+// 92 us with one CTA a tile, 73 with two, 70 with four (of 256 keys, 4 heads: 33 / 29 / 30); the
+// rebuild's short k loses by it (18 / 20 / 23).
 struct GemmPair {
   const void *a, *b;
   bool a_bf16, b_bf16;
@@ -685,6 +789,7 @@ struct RopeSum {
 };
 struct GemmJobs {
   int n;
+  int slices;  // CTAs (a cluster) that share a tile's k, every slices-th step each
   GemmJob job[3];
   RopeSum rope;
 };
@@ -704,10 +809,11 @@ __global__ void __launch_bounds__(THREADS) small_gemm_kernel(const __grid_consta
     store(s.dk_rope, s.bf16_out, idx, acc);
     return;
   }
+  const int tile_id = static_cast<int>(blockIdx.x) / jobs.slices, rank = static_cast<int>(blockIdx.x) - tile_id * jobs.slices;
   int which = 0;
-  while (which + 1 < jobs.n && static_cast<int>(blockIdx.x) >= jobs.job[which + 1].first_tile) ++which;
+  while (which + 1 < jobs.n && tile_id >= jobs.job[which + 1].first_tile) ++which;
   const GemmJob& j = jobs.job[which];
-  const int tile = static_cast<int>(blockIdx.x) - j.first_tile;
+  const int tile = tile_id - j.first_tile;
   const int m0 = tile / j.tiles_n * T, n0 = tile % j.tiles_n * T;
   const int g = threadIdx.x >> 6, l = threadIdx.x & 63, tx = l & 7, ty = l >> 3;
   float acc[4][4] = {};
@@ -728,8 +834,8 @@ __global__ void __launch_bounds__(THREADS) small_gemm_kernel(const __grid_consta
         rb[e] = n0 + bn < j.N && k0 + bk < p.K ? load(p.b, p.b_bf16, (k0 + bk) * p.bk + (n0 + bn) * p.bn) : 0.f;
       }
     };
-    fetch(0);
-    for (int step = 0; step < steps; ++step) {
+    if (rank < steps) fetch(rank);
+    for (int step = rank; step < steps; step += jobs.slices) {
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -738,7 +844,7 @@ __global__ void __launch_bounds__(THREADS) small_gemm_kernel(const __grid_consta
         Bs[g][b_n ? i >> 5 : i & 15][b_n ? i & 31 : i >> 4] = rb[e];
       }
       __syncthreads();
-      if (step + 1 < steps) fetch(step + 1);
+      if (step + jobs.slices < steps) fetch(step + jobs.slices);
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
         const float4 a = *reinterpret_cast<const float4*>(&As[g][k][4 * ty]);
@@ -762,15 +868,39 @@ __global__ void __launch_bounds__(THREADS) small_gemm_kernel(const __grid_consta
     *reinterpret_cast<float4*>(d + 4 * tx) = make_float4(acc[x][0], acc[x][1], acc[x][2], acc[x][3]);
   }
   __syncthreads();
+  float v[4];  // of the tile's 1024 elements
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int i = threadIdx.x + THREADS * e;  // 1024 elements
+    const int i = threadIdx.x + THREADS * e;
     const int r = j.cn == 1 ? i >> 5 : i & 31, c = j.cn == 1 ? i & 31 : i >> 5;
-    float v = 0.f;
+    v[e] = 0.f;
 #pragma unroll
     for (int k = 0; k < GROUPS; ++k)
-      v += (r < 16 ? &As[0][0][0] : &Bs[0][0][0])[k * (T * (T + 4) / 2) + (r & 15) * (T + 4) + c];
-    if (m0 + r < j.M && n0 + c < j.N) store(j.c, j.c_bf16, (m0 + r) * j.cm + (n0 + c) * j.cn, v);
+      v[e] += (r < 16 ? &As[0][0][0] : &Bs[0][0][0])[k * (T * (T + 4) / 2) + (r & 15) * (T + 4) + c];
+  }
+  if (jobs.slices > 1) {  // the slices' sums, in order, by the first CTA
+    namespace cg = cooperative_groups;
+    const cg::cluster_group cluster = cg::this_cluster();
+    float* part = &As[0][0][0];
+    __syncthreads();
+    if (rank != 0)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[threadIdx.x + THREADS * e] = v[e];
+    cluster.sync();
+    if (rank == 0)
+      for (int r = 1; r < jobs.slices; ++r) {
+        const float* from = cluster.map_shared_rank(part, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += from[threadIdx.x + THREADS * e];
+      }
+    cluster.sync();
+    if (rank != 0) return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int i = threadIdx.x + THREADS * e;
+    const int r = j.cn == 1 ? i >> 5 : i & 31, c = j.cn == 1 ? i & 31 : i >> 5;
+    if (m0 + r < j.M && n0 + c < j.N) store(j.c, j.c_bf16, (m0 + r) * j.cm + (n0 + c) * j.cn, v[e]);
   }
 }
 
@@ -784,12 +914,19 @@ struct Gemms {
     tiles += static_cast<ll>((M + 31) / 32) * j.tiles_n;
   }
   cudaError_t run(cudaStream_t st, const RopeSum& rope = RopeSum{}) {
-    const ll blocks = tiles + (rope.total + THREADS - 1) / THREADS;
+    int steps = 0;
+    for (int i = 0; i < jobs.n; ++i)
+      for (int q = 0; q < jobs.job[i].pairs; ++q) steps = std::max(steps, (jobs.job[i].p[q].K + 63) / 64);
+    int slices = 1;
+    while (steps >= 4 && slices < 4 && 2 * slices <= steps && 4 * slices * tiles <= 9 * sm_count()) slices *= 2;
+    const ll ropes = (rope.total + THREADS - 1) / THREADS;
+    const ll blocks = (tiles + (ropes + slices - 1) / slices) * slices;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    jobs.slices = slices;
     jobs.rope = rope;
-    jobs.rope.first_block = static_cast<int>(tiles);
-    return launch_next(small_gemm_kernel, static_cast<unsigned>(blocks), THREADS, 0, st, jobs);
+    jobs.rope.first_block = static_cast<int>(tiles * slices);
+    return launch_next_in_clusters(slices, small_gemm_kernel, static_cast<unsigned>(blocks), THREADS, 0, st, jobs);
   }
 };
 
