@@ -11,6 +11,7 @@ import ctypes
 import functools
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -328,10 +329,10 @@ def _code_of(dtype: torch.dtype) -> int:
 
 
 def _expect(name: str, t: torch.Tensor, shape, dtypes, device) -> int:
-    """The address of a contiguous CUDA tensor of that shape, type and device; an error that names it
-    otherwise."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype in dtypes and t.shape == shape \
-            and t.is_contiguous():
+    """The address of a contiguous CUDA tensor of that shape (None: any), type and device; an error that
+    names it otherwise."""
+    if isinstance(t, torch.Tensor) and t.get_device() == device.index and t.dtype in dtypes and t.is_contiguous() \
+            and (shape is None or t.shape == shape):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise RuntimeError(f"{name}: LAGA MLA runs on CUDA tensors only")
@@ -339,7 +340,7 @@ def _expect(name: str, t: torch.Tensor, shape, dtypes, device) -> int:
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}")
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
 
@@ -349,10 +350,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _launch(device, fn, *args):
     """fn(*args, stream) with `device` current, on its current stream."""
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
@@ -376,7 +380,7 @@ def key_bounds(doc_starts, n_rows: int, q_offset: int = 0, prefix=None, window: 
         raise ValueError("doc_starts must be [B, n_docs + 1]")
     B, n_docs = shape[0], shape[1] - 1
     dev = doc_starts.device
-    starts = _expect("doc_starts", doc_starts, shape, _INT32, dev)
+    starts = _expect("doc_starts", doc_starts, None, _INT32, dev)
     pre = None if prefix is None else _expect("prefix", prefix, (B, n_docs), _INT32, dev)
     lo = torch.empty((B, n_rows), dtype=torch.int32, device=dev)
     hi = torch.empty((B, n_rows), dtype=torch.int32, device=dev)
@@ -413,7 +417,7 @@ def _check_packed(name: str, p: Packed8):
     shape, dev = p.codes.shape, p.codes.device
     if not shape:
         raise ValueError(f"{name}: a checkpoint has at least one dimension")
-    return (_expect(name + ".codes", p.codes, shape, _UINT8, dev),
+    return (_expect(name + ".codes", p.codes, None, _UINT8, dev),
             _expect(name + ".scales", p.scales, _scales_shape(shape), _UINT8, dev))
 
 
@@ -423,7 +427,7 @@ def pack8(x: torch.Tensor) -> Packed8:
     code = _code_of(dt)
     if not shape:
         raise ValueError("pack8 needs at least one dimension")
-    src = _expect("x", x, shape, (dt,), dev)
+    src = _expect("x", x, None, (dt,), dev)
     codes = torch.empty(shape, dtype=torch.uint8, device=dev)
     scales = torch.empty(_scales_shape(shape), dtype=torch.uint8, device=dev)
     n, cols = x.numel(), shape[-1]
@@ -468,7 +472,7 @@ def rope(q, k_rope, pos, sections=None, theta: float = 10000.0, interleaved: boo
     d_rope, axes = k_rope.shape[2], pos.shape[0]
     code = _code_of(dt)
     k_shape = (shape[0], shape[1], d_rope)
-    src = _expect("q", q, shape, (dt,), dev)
+    src = _expect("q", q, None, (dt,), dev)
     k_src = _expect("k_rope", k_rope, k_shape, (dt,), dev)
     at = _expect("pos", pos, (axes, shape[0], shape[1]), (torch.int32, torch.int64), dev)
     sections = (d_rope // 2,) if sections is None else tuple(map(int, sections))
@@ -495,14 +499,23 @@ def rope(q, k_rope, pos, sections=None, theta: float = 10000.0, interleaved: boo
 @functools.lru_cache(maxsize=256)
 def _masked_plan(q_shape, c_shape, r_shape, wk_shape, wv_shape, dtype, q_offset, causal, softmax_scale, variant,
                  q_split, q_offset2):
-    """What a masked call's sizes decide: the Problem, the descriptors without and with the reuse of K and
+    """What a masked call's sizes decide: the other tensors' shapes, the descriptors without and with the reuse of K and
     V, the bytes of the forward's and the backward's workspace (0: refused)."""
     like = [_Sizes(s, dtype) for s in (q_shape, c_shape, r_shape, wk_shape, wv_shape)]
     p = problem_of(*like, q_offset, causal, q_split, q_offset2)
     d = make_desc(p, softmax_scale, variant)
     L = lib()
-    return (p, d, make_desc(p, softmax_scale, variant, FLAG_REUSE_KV), int(L.laga_mla_masked_fwd_workspace_size(d)),
+    shapes = _Shapes((p.B, p.Sq), (p.n_h,), (p.B, p.Sq, p.n_h, p.d_qk), (p.B, p.Sq, p.n_h, p.d_v), (p.B, p.n_h, p.Sq))
+    return (shapes, d, make_desc(p, softmax_scale, variant, FLAG_REUSE_KV), int(L.laga_mla_masked_fwd_workspace_size(d)),
             int(L.laga_mla_masked_bwd_workspace_size(d)))
+
+
+class _Shapes(NamedTuple):
+    rows: tuple
+    heads: tuple
+    q: tuple
+    out: tuple
+    lse: tuple
 
 
 class _Sizes:
@@ -521,51 +534,50 @@ class _Sizes:
 
 class _MaskedCall:
     """The checked arguments that masked_fwd, masked_bwd and masked_workspace share."""
-    __slots__ = ("p", "desc", "reuse", "fwd_bytes", "bwd_bytes", "q", "x", "dev", "dt")
+    __slots__ = ("shapes", "desc", "reuse", "fwd_bytes", "bwd_bytes", "q", "x", "dev", "dt", "dts")
 
     def __init__(self, q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, softmax_scale, variant, q_split, q_offset2):
-        self.dt, self.dev = c_kv.dtype, c_kv.device
-        if self.dt not in _DTYPE_CODES:
+        self.dt, self.dev = dt, dev = c_kv.dtype, c_kv.device
+        if dt not in _DTYPE_CODES:
             raise TypeError("tensors must be float32 or bfloat16")
-        packed = isinstance(q, Packed8)
-        if packed:
+        self.dts = dts = (dt,)
+        if isinstance(q, Packed8):
             self.q = LagaPacked(*_check_packed("q", q))
-            if q.dtype != self.dt:
+            if q.dtype != dt:
                 raise TypeError("all inputs must share one dtype")
-            if q.device != self.dev:
-                raise ValueError(f"q is on {q.device}, the other tensors on {self.dev}")
+            if q.device != dev:
+                raise ValueError(f"q is on {q.device}, the other tensors on {dev}")
         else:
-            self.q = _expect("q", q, q.shape, (self.dt,), self.dev)
-        dts, dev = (self.dt,), self.dev
-        sizes = c_kv.shape, k_rope.shape, W_UK.shape, W_UV.shape
-        self.x = (_expect("c_kv", c_kv, sizes[0], dts, dev), _expect("k_rope", k_rope, sizes[1], dts, dev),
-                  _expect("W_UK", W_UK, sizes[2], dts, dev), _expect("W_UV", W_UV, sizes[3], dts, dev))
-        self.p, self.desc, self.reuse, self.fwd_bytes, self.bwd_bytes = _masked_plan(
-            q.shape, *sizes, self.dt, int(q_offset), bool(causal), softmax_scale, variant, int(q_split), int(q_offset2))
+            self.q = _expect("q", q, None, dts, dev)
+        self.x = (_expect("c_kv", c_kv, None, dts, dev), _expect("k_rope", k_rope, None, dts, dev),
+                  _expect("W_UK", W_UK, None, dts, dev), _expect("W_UV", W_UV, None, dts, dev))
+        self.shapes, self.desc, self.reuse, self.fwd_bytes, self.bwd_bytes = _masked_plan(
+            q.shape, c_kv.shape, k_rope.shape, W_UK.shape, W_UV.shape, dt, int(q_offset), bool(causal), softmax_scale,
+            variant, int(q_split), int(q_offset2))
 
     def mods(self, key_lo, key_hi, softcap, slopes) -> LagaMods:
-        p, dev = self.p, self.dev
-        rows = (p.B, p.Sq)
-        return LagaMods(None if key_lo is None else _expect("key_lo", key_lo, rows, _INT32, dev),
-                        None if key_hi is None else _expect("key_hi", key_hi, rows, _INT32, dev),
-                        None if slopes is None else _expect("slopes", slopes, (p.n_h,), _FP32, dev),
+        shapes, dev = self.shapes, self.dev
+        return LagaMods(None if key_lo is None else _expect("key_lo", key_lo, shapes.rows, _INT32, dev),
+                        None if key_hi is None else _expect("key_hi", key_hi, shapes.rows, _INT32, dev),
+                        None if slopes is None else _expect("slopes", slopes, shapes.heads, _FP32, dev),
                         softcap or 0.0)
 
     def workspace(self, nbytes, given):
         """(the tensor that keeps it alive, its address)."""
         if given is None:
             given = torch.empty(nbytes, dtype=torch.uint8, device=self.dev)
-        else:
-            _expect("workspace", given, given.shape, (given.dtype,), self.dev)
-            if given.numel() * given.element_size() < nbytes:
-                raise ValueError("workspace too small")
-        return given, given.data_ptr()
+            return given, given.data_ptr()
+        at = _expect("workspace", given, None, (given.dtype,), self.dev)
+        if given.numel() * given.element_size() < nbytes:
+            raise ValueError("workspace too small")
+        return given, at
 
-    def output(self, name, t, shape, dtype):
+    def output(self, name, t, shape, dtypes):
+        """(the output, its address): `t`, or a new tensor."""
         if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-        _expect(name, t, shape, (dtype,), self.dev)
-        return t
+            t = torch.empty(shape, dtype=dtypes[0], device=self.dev)
+            return t, t.data_ptr()
+        return t, _expect(name, t, shape, dtypes, self.dev)
 
 
 def masked_workspace(q, c_kv, k_rope, W_UK, W_UV, key_lo=None, key_hi=None, softcap: float = 0.0, slopes=None,
@@ -591,12 +603,11 @@ def masked_fwd(q, c_kv, k_rope, W_UK, W_UV, key_lo=None, key_hi=None, softcap: f
     if isinstance(q, Packed8):
         raise ValueError("the forward takes q as a tensor")
     c = _MaskedCall(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, softmax_scale, variant, q_split, q_offset2)
-    p = c.p
     m = c.mods(key_lo, key_hi, softcap, slopes)
-    out = c.output("out", out, (p.B, p.Sq, p.n_h, p.d_v), c.dt)
-    lse = c.output("lse", lse, (p.B, p.n_h, p.Sq), torch.float32)
+    out, out_at = c.output("out", out, c.shapes.out, c.dts)
+    lse, lse_at = c.output("lse", lse, c.shapes.lse, _FP32)
     ws, at = c.workspace(c.fwd_bytes, workspace)
-    _launch(c.dev, lib().laga_mla_masked_fwd, c.desc, m, c.q, *c.x, out.data_ptr(), lse.data_ptr(), at, c.fwd_bytes)
+    _launch(c.dev, lib().laga_mla_masked_fwd, c.desc, m, c.q, *c.x, out_at, lse_at, at, c.fwd_bytes)
     return out, lse
 
 
@@ -612,31 +623,30 @@ def masked_bwd(q, c_kv, k_rope, W_UK, W_UV, out, lse, dout, key_lo=None, key_hi=
     if packed != isinstance(out, Packed8):
         raise ValueError("q and out come either both as tensors or both as 8-bit checkpoints")
     c = _MaskedCall(q, c_kv, k_rope, W_UK, W_UV, q_offset, causal, softmax_scale, variant, q_split, q_offset2)
-    p, dev, dt = c.p, c.dev, c.dt
-    o_shape = (p.B, p.Sq, p.n_h, p.d_v)
+    dev, dts, shapes = c.dev, c.dts, c.shapes
     if packed:
         out8 = LagaPacked(*_check_packed("out", out))
-        if out.dtype != dt:
+        if out.dtype != c.dt:
             raise TypeError("all inputs must share one dtype")
-        _expect("out.codes", out.codes, o_shape, _UINT8, dev)
-        tensors = (None, None, c.q, out8)
+        _expect("out.codes", out.codes, shapes.out, _UINT8, dev)
+        q_at, out_at, q8 = None, None, c.q
     else:
-        tensors = (c.q, _expect("out", out, o_shape, (dt,), dev), None, None)
-    lse_at = _expect("lse", lse, (p.B, p.n_h, p.Sq), _FP32, dev)
-    dout_at = _expect("dout", dout, o_shape, (dt,), dev)
+        q_at, out_at, q8, out8 = c.q, _expect("out", out, shapes.out, dts, dev), None, None
+    lse_at = _expect("lse", lse, shapes.lse, _FP32, dev)
+    dout_at = _expect("dout", dout, shapes.out, dts, dev)
     if reuse_kv and workspace is None:
         raise ValueError("reuse_kv needs the workspace the forward ran with")
     m = c.mods(key_lo, key_hi, softcap, slopes)
-    given = grads or {}
-    g = {"dq": c.output("dq", given.get("dq"), (p.B, p.Sq, p.n_h, p.d_qk), dt),
-         "dc_kv": c.output("dc_kv", given.get("dc_kv"), c_kv.shape, dt),
-         "dk_rope": c.output("dk_rope", given.get("dk_rope"), k_rope.shape, dt),
-         "dW_UK": c.output("dW_UK", given.get("dW_UK"), W_UK.shape, dt),
-         "dW_UV": c.output("dW_UV", given.get("dW_UV"), W_UV.shape, dt)}
+    given = (grads or {}).get
+    dq, a0 = c.output("dq", given("dq"), shapes.q, dts)
+    dc_kv, a1 = c.output("dc_kv", given("dc_kv"), c_kv.shape, dts)
+    dk_rope, a2 = c.output("dk_rope", given("dk_rope"), k_rope.shape, dts)
+    dW_UK, a3 = c.output("dW_UK", given("dW_UK"), W_UK.shape, dts)
+    dW_UV, a4 = c.output("dW_UV", given("dW_UV"), W_UV.shape, dts)
     ws, at = c.workspace(c.bwd_bytes, workspace)
-    _launch(dev, lib().laga_mla_masked_bwd, c.reuse if reuse_kv else c.desc, m, tensors[0], *c.x, tensors[1], lse_at,
-            dout_at, tensors[2], tensors[3], *(t.data_ptr() for t in g.values()), at, c.bwd_bytes)
-    return g
+    _launch(dev, lib().laga_mla_masked_bwd, c.reuse if reuse_kv else c.desc, m, q_at, *c.x, out_at, lse_at, dout_at, q8,
+            out8, a0, a1, a2, a3, a4, at, c.bwd_bytes)
+    return {"dq": dq, "dc_kv": dc_kv, "dk_rope": dk_rope, "dW_UK": dW_UK, "dW_UV": dW_UV}
 
 
 def check(device=None) -> None:
