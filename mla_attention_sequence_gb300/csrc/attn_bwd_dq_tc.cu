@@ -77,6 +77,8 @@ struct Params {
   // masked instances
   const int2* rows;     // [B][sq_pad] visible interval of each query row
   const int4* work;     // [B][n_q_tiles] {query tile, first key tile, key tiles}, longest first
+  const bf16* q;        // [B][Sq][n_h][192], what mQ maps
+  int successor;        // linear block distance to the CTA that will next run on this SM (the SM count)
   ModParams mod;
 };
 
@@ -94,6 +96,21 @@ __device__ __forceinline__ int q_pos(const Params& p, int i) {
 __device__ __forceinline__ int n_kv_tiles(const Params& p, int t) {
   const int last = p.causal ? q_pos(p, min(p.Sq, (t + 1) * BQ) - 1) : p.S - 1;
   return last / BKV + 1;
+}
+
+// Row r of q (half 0) or dO (half 1) of the CTA that will next run on this SM, into L2: the inputs
+// come from DRAM, and the first product waits for them. Ordinary prefetches, so that the TMA queue,
+// in which this CTA's own loads wait their turn, stays free of them.
+__device__ __forceinline__ void prefetch_next(const Params& p, int r, int half) {
+  const long long nx = gridDim.x, ny = gridDim.y;
+  const long long next = blockIdx.x + nx * (blockIdx.y + ny * blockIdx.z) + p.successor;
+  if (next >= nx * ny * gridDim.z) return;
+  const int h = static_cast<int>((next / nx) % ny), b = static_cast<int>(next / (nx * ny));
+  const int i = __ldcg(&p.work[b * p.n_q_tiles + static_cast<int>(next % nx)].x) * BQ + r;
+  if (i >= p.Sq) return;
+  const long long row = (static_cast<long long>(b) * p.Sq + i) * p.n_h + h;
+  const char* at = reinterpret_cast<const char*>(half == 0 ? p.q + row * 192 : p.dout + row * 128);
+  for (int k = 0; k < (half == 0 ? 3 : 2); ++k) prefetch_l2(at + 128 * k);
 }
 
 template <int MOD>
@@ -140,6 +157,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     n_kv = n_kv_tiles(p, t);
   }
 
+  if (lane == 0) LAGA_TRACE_POINT(dq, 1, t >= 0 ? 0 : 1);
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     for (int i = 0; i < K_STAGES; ++i) {
@@ -168,6 +186,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (lane == 0) LAGA_TRACE_POINT(dq, 2, 0);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -179,9 +198,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tma_load_3d(smem + OFF_Q, &mQ, q_full, h * 192, q0, b);
       tma_load_3d(smem + OFF_Q + BOX, &mQ, q_full, h * 192 + 64, q0, b);
       tma_load_3d(smem + OFF_Q + 2 * BOX, &mQ, q_full, h * 192 + 128, q0, b);
+      LAGA_TRACE_POINT(dq, 3, 0);
       int j = 0;
       for (; j < n_kv; ++j) {
         const int s = j % K_STAGES;
+        // the start's loads compete: first what the first product needs
+        if (MASKED && j == 1 && !mbar_wait_or_abort(q_full, 0, abort_flag, 70)) break;
         if (!mbar_wait_or_abort(&k_empty[s], ((j / K_STAGES) & 1) ^ 1, abort_flag, 71)) break;
         uint8_t* dst = smem + OFF_K + s * K_BYTES;
         mbar_arrive_expect_tx(&k_full[s], K_BYTES);
@@ -189,6 +211,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tma_load_2d(dst, &mK, &k_full[s], h * 128, row);
         tma_load_2d(dst + BOX, &mK, &k_full[s], h * 128 + 64, row);
         tma_load_3d(dst + 2 * BOX, &mR, &k_full[s], 0, (j0 + j) * BKV, b);
+        LAGA_TRACE_POINT(dq, 4, j);
       }
       if (j < n_kv) {
         mbar_drain(q_full, 0);
@@ -221,7 +244,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // read. Each barrier is tested (without blocking) inside the MMA group that
     // precedes its use, before that group's last block of four, and consumed as a
     // token after the group.
-    bool ok = warp_wait_or_abort(q_full, 0, abort_flag, 73) && warp_wait_or_abort(do_tmem, 0, abort_flag, 77);
+    bool ok = warp_wait_or_abort(q_full, 0, abort_flag, 73);
+    if (lane == 0) LAGA_TRACE_POINT(dq, 5, 0);
+    if constexpr (!MASKED) ok = ok && warp_wait_or_abort(do_tmem, 0, abort_flag, 77);
+    if (lane == 0) LAGA_TRACE_POINT(dq, 6, 0);
     bool issued = false;
     tc_fence_after();
     const uint64_t q_desc = sdesc_sw128(smem_u32(smem + OFF_Q), 16, 1024);
@@ -274,6 +300,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         mma_commit_warp(&k_empty[s]);
       }
+      if (MASKED && j1 == 0 && !warp_wait_or_abort(do_tmem, 0, abort_flag, 77)) { ok = false; break; }
       if (j1 >= 0 && j1 < n_kv) {  // dP(j+1): S(j+1) released, V(j+1) in
         if (!warp_wait_token(s_free, j1 & 1, tf, abort_flag, 78)) { ok = false; break; }
         if (!warp_wait_token(&v_full[j1 % V_STAGES], (j1 / V_STAGES) & 1, tv, abort_flag, 75)) {
@@ -292,6 +319,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           break;
         }
         tc_fence_after();
+        if (lane == 0) LAGA_TRACE_POINT(dq, 7, j2);
         issue_s(j2, [&]() {
           if (j1 >= 0 && j1 < n_kv) td = mbar_test(ds_full, j1 & 1);
         });
@@ -347,7 +375,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       uint32_t w[32];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint4 v = valid ? (MASKED ? __ldcg(drow + k) : __ldg(drow + k)) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = valid ? __ldg(drow + k) : make_uint4(0u, 0u, 0u, 0u);
         w[4 * k + 0] = v.x;
         w[4 * k + 1] = v.y;
         w[4 * k + 2] = v.z;
@@ -358,7 +386,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(do_tmem);
+      if (lane == 0) LAGA_TRACE_POINT(dq, 8, 0);
     }
+    if constexpr (MASKED) prefetch_next(p, r, half);
     for (int j = 0; j < n_kv && ok; ++j) {
       const uint32_t ph = j & 1;
       if (!warp_wait(s_full, ph, 81)) { ok = false; break; }
@@ -582,6 +612,8 @@ LaunchResult tc_attn_bwd_dq(const Dims& d, const bf16* q, const bf16* k_rope, co
   if (mask) {
     p.rows = mask->meta.rows;
     p.work = mask->meta.work;
+    p.q = q;
+    p.successor = sm_count();
     p.mod = mod_params(d, mask->mods);
     switch (mod_of(mask->mods)) {
       case 0: kern = attn_bwd_dq_kernel<0>; break;
