@@ -42,7 +42,6 @@ def _flags(ptxas_verbose: bool):
          "--expt-relaxed-constexpr", "-Xcompiler", "-Wno-unused-function"]
     if ptxas_verbose:
         f += ["-Xptxas", "-v"]
-    f += os.environ.get("LAGA_X","").split()
     if TRACE:
         f += ["-DLAGA_TRACE", f"-DLAGA_TRACE_BY={int(os.environ.get('LAGA_TRACE_BY', '0'))}"]
     return f
