@@ -113,7 +113,7 @@ __device__ __forceinline__ void prefetch_next(const Params& p, int r, int half) 
   if (i >= p.Sq) return;
   const long long row = (static_cast<long long>(b) * p.Sq + i) * p.n_h + h;
   const char* at = reinterpret_cast<const char*>(half == 0 ? p.q + row * 192 : p.dout + row * 128);
-  for (int k = 0; k < (half == 0 ? 3 : 2); ++k) prefetch_l2(at + 128 * k);
+  for (int k = 0; k < (half == 0 ? 3 : 2); ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * k));
 }
 
 template <int MOD>

@@ -309,7 +309,8 @@ __global__ void key_bounds_kernel(Dims d, const int* __restrict__ starts, int n_
 // cap (CHECK_Q) always, else only where lse is not finite, because every score of a row whose q
 // is not finite is not finite, and so is its lse (a cap makes finite scores of infinite ones).
 // That leaves 3 of 7 bytes unread (q has 192 values a row, dout and out 128 each). Bound by
-// memory: 2 x 4096 rows of 16 heads, 67 MB, in 24 us with everything from DRAM.
+// memory: 2 x 4096 rows of 16 heads, 67 MB, in 21 us with everything from DRAM (more rows a thread,
+// their loads issued together: 33).
 template <bool PACKED, bool CHECK_Q>
 __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* __restrict__ q, const bf16* __restrict__ out,
                                                            const Packed q8, const Packed out8,
@@ -325,10 +326,18 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
   const ll rows = static_cast<ll>(d.B) * d.sq_pad * d.n_h;
   const int l16 = threadIdx.x & 15;
   // heads fastest: neighbouring rows are neighbours in q, out and dout
-  const int h = static_cast<int>(row % d.n_h);
-  const ll bi = row / d.n_h;
-  const int i = static_cast<int>(bi % d.sq_pad);
-  const int b = static_cast<int>(bi / d.sq_pad);
+  int h, i, b;
+  if (rows < (ll(1) << 31)) {  // cheaper divisions
+    const uint32_t r = static_cast<uint32_t>(row), bi = r / static_cast<uint32_t>(d.n_h);
+    h = static_cast<int>(r - bi * d.n_h);
+    b = static_cast<int>(bi / static_cast<uint32_t>(d.sq_pad));
+    i = static_cast<int>(bi - b * static_cast<uint32_t>(d.sq_pad));
+  } else {
+    const ll bi = row / d.n_h;
+    h = static_cast<int>(row - bi * d.n_h);
+    b = static_cast<int>(bi / d.sq_pad);
+    i = static_cast<int>(bi - static_cast<ll>(b) * d.sq_pad);
+  }
   const bool in = row < rows && i < d.Sq;
   const ll src = (static_cast<ll>(b) * d.Sq + i) * d.n_h + h;
   float acc = 0.f;
@@ -349,7 +358,8 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
         if (l16 < 8) q1 = __ldcg(reinterpret_cast<const uint4*>(q + src * 192) + 16 + l16);
       }
     }
-    bad = bad_bf16x8(g) || bad_bf16x8(q0) || bad_bf16x8(q1);
+    if (PACKED || CHECK_Q || !finite(row_lse)) bad = bad_bf16x8(q0) || bad_bf16x8(q1);
+    float zero = 0.f;  // NaN once a value of dout is not finite: one multiply-add a value, where bit tests take two
     const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
     const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&g);
 #pragma unroll
@@ -358,7 +368,9 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
       const float2 gf = __bfloat1622float2(g2[k]);
       acc = fmaf(af.x, gf.x, acc);
       acc = fmaf(af.y, gf.y, acc);
+      zero = fmaf(gf.x, 0.f, fmaf(gf.y, 0.f, zero));
     }
+    bad = bad || zero != 0.f;
   }
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);

@@ -572,6 +572,42 @@ def test_two_calls_at_once():
             assert torch.equal(got[i][k], want[i][k]), k
 
 
+@pytest.mark.parametrize("dtype,dims", [(torch.bfloat16, DSV3), (torch.float32, (32, 16, 8, 24))])
+def test_new_values_at_the_same_addresses(dtype, dims):
+    """Steps enqueued one after the other without a wait, their inputs replaced in place between them: each
+    sees its own (kernels of a call start before the one before them has ended)."""
+    n, S, n_h = 6, 700, 4
+    problems = [inputs(2, S, S, n_h, dims, dtype, 50 + i) for i in range(n)]
+    starts = [torch.tensor([[0, 100 * i + 1, 640], [5, 300, 690 - i]], dtype=torch.int32, device=dev()) for i in range(n)]
+    x, dout, st = {k: v.clone() for k, v in problems[0][0].items()}, problems[0][1].clone(), starts[0].clone()
+    ws = laga.masked_workspace(*x.values())
+    results = {False: [], True: []}
+    for wait in (True, False):
+        for (y, dy), s in zip(problems, starts):
+            for k, v in y.items():
+                x[k].copy_(v)
+            dout.copy_(dy)
+            st.copy_(s)
+            lo, hi = laga.key_bounds(st, S)
+            if wait:
+                torch.cuda.synchronize()
+            kw = dict(key_lo=lo, key_hi=hi, softcap=20.0, workspace=ws)
+            out, lse = laga.masked_fwd(*x.values(), **kw)
+            if wait:
+                torch.cuda.synchronize()
+            g = laga.masked_bwd(*x.values(), out, lse, dout, reuse_kv=True, **kw)
+            if wait:
+                torch.cuda.synchronize()
+            h = laga.masked_bwd(laga.pack8(x["q"]), *list(x.values())[1:], laga.pack8(out), lse, dout, **kw)
+            if wait:
+                torch.cuda.synchronize()
+            results[wait].append([out, lse, *g.values(), *h.values()])
+    torch.cuda.synchronize()
+    for a, b in zip(results[False], results[True]):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    laga.check(dev())
+
+
 @pytest.mark.parametrize("kind", ["contiguous", "zigzag"])
 def test_sequence_parallel_ranks_of_packed_documents(kind):
     """Each rank's local step, one after the other: their rows make up the whole sequence's out and dq,
