@@ -301,7 +301,7 @@ __global__ void key_bounds_kernel(Dims d, const int* __restrict__ starts, int n_
   key_hi[at] = hi;
 }
 
-// ---- the backward's row pass, tensor-core dims: 16 lanes per (b, h, i) of the padded rows.
+// ---- the backward's row pass, tensor-core dims: 8 lanes per (b, h, i) of the padded rows.
 // lse2 = lse log2(e) (+inf: the row sees nothing or does not exist; NaN: its q, dout or
 // forward result is not finite), delta = rowsum(dout out), *q_bad if q or dout is not finite.
 // PACKED: q and out come from their 8-bit checkpoints; q is written in bf16 to q_clean (zero
@@ -309,8 +309,8 @@ __global__ void key_bounds_kernel(Dims d, const int* __restrict__ starts, int n_
 // cap (CHECK_Q) always, else only where lse is not finite, because every score of a row whose q
 // is not finite is not finite, and so is its lse (a cap makes finite scores of infinite ones).
 // That leaves 3 of 7 bytes unread (q has 192 values a row, dout and out 128 each). Bound by
-// memory: 2 x 4096 rows of 16 heads, 67 MB, in 21 us with everything from DRAM (more rows a thread,
-// their loads issued together: 33).
+// memory: 2 x 4096 rows of 16 heads, 67 MB, in 15 us with everything from DRAM (16 lanes a row: 18,
+// bound by instructions).
 template <bool PACKED, bool CHECK_Q>
 __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* __restrict__ q, const bf16* __restrict__ out,
                                                            const Packed q8, const Packed out8,
@@ -322,9 +322,9 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
     beside_previous();
   else
     after_previous();
-  const ll row = (static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
+  const ll row = (static_cast<ll>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
   const ll rows = static_cast<ll>(d.B) * d.sq_pad * d.n_h;
-  const int l16 = threadIdx.x & 15;
+  const int l8 = threadIdx.x & 7;
   // heads fastest: neighbouring rows are neighbours in q, out and dout
   int h, i, b;
   if (rows < (ll(1) << 31)) {  // cheaper divisions
@@ -342,47 +342,53 @@ __global__ void __launch_bounds__(256) mask_bwd_pre_kernel(Dims d, const bf16* _
   const ll src = (static_cast<ll>(b) * d.Sq + i) * d.n_h + h;
   float acc = 0.f;
   bool bad = false;
-  uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
+  uint4 qv[3] = {};  // 16-byte chunks l8, l8 + 8, ... of the row's q
   const float row_lse = in ? __ldcg(&lse[(static_cast<ll>(b) * d.n_h + h) * d.Sq + i]) : -INFINITY;
   if (in) {
-    const uint4 g = __ldcg(reinterpret_cast<const uint4*>(dout + src * 128) + l16);
-    uint4 a;
+    uint4 g[2], a[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) g[c] = __ldcg(reinterpret_cast<const uint4*>(dout + src * 128) + l8 + 8 * c);
     if constexpr (PACKED) {
-      a = unpack8_bf16x8(out8, src, 128, l16);
-      q0 = unpack8_bf16x8(q8, src, 192, l16);
-      if (l16 < 8) q1 = unpack8_bf16x8(q8, src, 192, 16 + l16);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) a[c] = unpack8_bf16x8(out8, src, 128, l8 + 8 * c);
+#pragma unroll
+      for (int c = 0; c < 3; ++c) qv[c] = unpack8_bf16x8(q8, src, 192, l8 + 8 * c);
     } else {
-      a = __ldcg(reinterpret_cast<const uint4*>(out + src * 128) + l16);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) a[c] = __ldcg(reinterpret_cast<const uint4*>(out + src * 128) + l8 + 8 * c);
       if (CHECK_Q || !finite(row_lse)) {
-        q0 = __ldcg(reinterpret_cast<const uint4*>(q + src * 192) + l16);
-        if (l16 < 8) q1 = __ldcg(reinterpret_cast<const uint4*>(q + src * 192) + 16 + l16);
+#pragma unroll
+        for (int c = 0; c < 3; ++c) qv[c] = __ldcg(reinterpret_cast<const uint4*>(q + src * 192) + l8 + 8 * c);
       }
     }
-    if (PACKED || CHECK_Q || !finite(row_lse)) bad = bad_bf16x8(q0) || bad_bf16x8(q1);
+    if (PACKED || CHECK_Q || !finite(row_lse)) bad = bad_bf16x8(qv[0]) || bad_bf16x8(qv[1]) || bad_bf16x8(qv[2]);
     float zero = 0.f;  // NaN once a value of dout is not finite: one multiply-add a value, where bit tests take two
-    const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
-    const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&g);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 af = __bfloat1622float2(a2[k]);
-      const float2 gf = __bfloat1622float2(g2[k]);
-      acc = fmaf(af.x, gf.x, acc);
-      acc = fmaf(af.y, gf.y, acc);
-      zero = fmaf(gf.x, 0.f, fmaf(gf.y, 0.f, zero));
+    for (int c = 0; c < 2; ++c) {
+      const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a[c]);
+      const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&g[c]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 af = __bfloat1622float2(a2[k]);
+        const float2 gf = __bfloat1622float2(g2[k]);
+        acc = fmaf(af.x, gf.x, acc);
+        acc = fmaf(af.y, gf.y, acc);
+        zero = fmaf(gf.x, 0.f, fmaf(gf.y, 0.f, zero));
+      }
     }
     bad = bad || zero != 0.f;
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  for (int o = 4; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
   const unsigned votes = __ballot_sync(0xffffffffu, bad);
-  bad = (votes & (threadIdx.x & 16 ? 0xffff0000u : 0xffffu)) != 0u;
+  bad = ((votes >> (threadIdx.x & 24)) & 0xffu) != 0u;
   if (PACKED && in) {
     uint4* dst = reinterpret_cast<uint4*>(q_clean + src * 192);
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    dst[l16] = bad ? zero : q0;
-    if (l16 < 8) dst[16 + l16] = bad ? zero : q1;
+#pragma unroll
+    for (int c = 0; c < 3; ++c) dst[l8 + 8 * c] = bad ? zero : qv[c];
   }
-  if (row < rows && l16 == 0) {
+  if (row < rows && l8 == 0) {
     float L = INFINITY, D = 0.f;
     if (in) {
       const float v = row_lse;
@@ -560,7 +566,7 @@ LaunchResult tc_mask_bwd_pre(const Dims& d, const bf16* q, const bf16* out, cons
                              bf16* dout_clean, int* q_bad, bool check_q, bool beside, cudaStream_t st) {
   LaunchResult r;
   const ll rows = static_cast<ll>(d.B) * d.sq_pad * d.n_h;
-  const unsigned grid = static_cast<unsigned>((rows + 15) / 16);
+  const unsigned grid = static_cast<unsigned>((rows + 31) / 32);
   const auto kern = q8 ? mask_bwd_pre_kernel<true, true>
                        : check_q ? mask_bwd_pre_kernel<false, true> : mask_bwd_pre_kernel<false, false>;
   r.err = launch_next(kern, grid, 256, 0, st, d, q, out, q8 ? *q8 : Packed{}, out8 ? *out8 : Packed{}, dout, lse, w.lse2,
