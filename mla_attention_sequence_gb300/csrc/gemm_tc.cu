@@ -518,8 +518,20 @@ __global__ void __launch_bounds__(224, 1)
     }
   };
   const int per = num_tiles / gridDim.x, rem = num_tiles % gridDim.x;
-  const int t_begin = blockIdx.x * per + min(static_cast<int>(blockIdx.x), rem);
-  const int t_end = t_begin + per + (static_cast<int>(blockIdx.x) < rem ? 1 : 0);
+  int t_begin = blockIdx.x * per + min(static_cast<int>(blockIdx.x), rem);
+  int t_end = t_begin + per + (static_cast<int>(blockIdx.x) < rem ? 1 : 0);
+  if constexpr (LIST) {
+    // Few latent tiles: a range that ends at a latent tile's end saves the load of a second one,
+    // which takes as long as some three output tiles (2999 keys of 32 heads: 32.6 -> 30.7 us, 4001
+    // of 16: 28.2 -> 26.1, 2 x 4096 of 16: 39.4 -> 38.8).
+    const int keys = num_tiles / p.n_tiles, grid = static_cast<int>(gridDim.x);
+    const int splits = keys > 0 ? min(grid / keys, p.n_tiles) : 0;
+    if (splits > 0 && (p.n_tiles + splits - 1) / splits <= per + (rem > 0 ? 1 : 0) + 3) {
+      const int key = static_cast<int>(blockIdx.x) / splits, part = static_cast<int>(blockIdx.x) - key * splits;
+      t_begin = key < keys ? key * p.n_tiles + part * p.n_tiles / splits : 0;
+      t_end = key < keys ? key * p.n_tiles + (part + 1) * p.n_tiles / splits : 0;
+    }
+  }
 
   if (warp == 0) {
     if (lane == 0) {
