@@ -171,6 +171,29 @@ def test_most_key_tiles_unseen(mod):
     assert not got["dc_kv"][~seen].any() and not got["dk_rope"][~seen].any()
 
 
+@pytest.mark.parametrize("mod", MODS)
+@pytest.mark.parametrize("docs", ["one", "many", "uneven"])
+def test_many_tiles_per_sm(docs, mod):
+    """Several (head, query tile) items and CTAs of each kernel on every SM, walks of one to eleven key tiles."""
+    B, S, n_h = 2, 1300, 24
+    starts = {"one": [[0, 1300], [7, 1290]], "uneven": [[0, 3, 900, 910, 1300], [0, 600, 601, 1000, 1000]],
+              "many": [list(range(0, 1300, 43))[:31], list(range(5, 1300, 42))[:31]]}[docs]
+    x, dout = inputs(B, S, S, n_h, DSV3, torch.bfloat16, 24)
+    kw = dict(MODS[mod])
+    if "slopes" in kw:
+        kw["slopes"] = slopes(n_h)
+    lo, hi = laga.key_bounds(torch.tensor(starts, dtype=torch.int32, device=dev()), S)
+    check(x, dout, key_lo=lo, key_hi=hi, **kw)
+
+
+def test_long_rows_without_mods():
+    """The form for walks that can be long, with several query tiles and heads, and rows that see little."""
+    B, Sq, S, n_h = 1, 400, 8300, 6
+    x, dout = inputs(B, Sq, S, n_h, DSV3, torch.bfloat16, 25)
+    lo, hi = random_bounds(B, Sq, S, 8)
+    check(x, dout, key_lo=lo, key_hi=hi, causal=False, q_offset=7000)
+
+
 def test_two_segments():
     B, Sq, S, n_h = 1, 256 + 70, 1024, 4
     x, dout = inputs(B, Sq, S, n_h, DSV3, torch.bfloat16, 5)
