@@ -552,8 +552,8 @@ class _MaskedCall:
         self.x = (_expect("c_kv", c_kv, None, dts, dev), _expect("k_rope", k_rope, None, dts, dev),
                   _expect("W_UK", W_UK, None, dts, dev), _expect("W_UV", W_UV, None, dts, dev))
         self.shapes, self.desc, self.reuse, self.fwd_bytes, self.bwd_bytes = _masked_plan(
-            q.shape, c_kv.shape, k_rope.shape, W_UK.shape, W_UV.shape, dt, int(q_offset), bool(causal), softmax_scale,
-            variant, int(q_split), int(q_offset2))
+            q.shape, c_kv.shape, k_rope.shape, W_UK.shape, W_UV.shape, dt, int(q_offset), bool(causal),
+            None if softmax_scale is None else float(softmax_scale), variant, int(q_split), int(q_offset2))
 
     def mods(self, key_lo, key_hi, softcap, slopes) -> LagaMods:
         shapes, dev = self.shapes, self.dev

@@ -659,6 +659,17 @@ def test_sequence_parallel_ranks_of_packed_documents(kind):
         assert float((v.double() - want[k].double()).norm()) <= 3 * 2.0 ** -8 * float(want[k].double().norm()), k
 
 
+def test_a_scale_held_in_a_tensor():
+    """Its value counts at each call, not the object."""
+    x, _ = inputs(1, 40, 40, 2, (16, 8, 4, 8), torch.float32)
+    scale = torch.tensor(0.25)
+    for value in (0.25, 1.5):
+        scale.fill_(value)
+        out, lse = laga.masked_fwd(*x.values(), softmax_scale=scale)
+        want, want_lse = laga.masked_fwd(*x.values(), softmax_scale=value)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 @pytest.mark.parametrize("which", ["rows", "heads"])
 def test_rope_of_nothing(which):
     q = torch.empty(1, 0, 2, 8, device=dev()) if which == "rows" else torch.empty(0, 3, 2, 8, device=dev())
