@@ -402,12 +402,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       bool partial = false;  // masked: some row of the warp does not see every key of the half-tile
       if constexpr (MASKED) {
         partial = !__all_sync(0xffffffffu, lo <= kv_first && hi >= kv_first + 64);
-        const unsigned first = static_cast<unsigned>(lo - kv_first), width = static_cast<unsigned>(max(hi - lo, 0));
-        if (CAP && partial) {
+        // where the tile is partial, what of it is masked
+        auto mask_out = [&](auto&& drop) {
+          const uint32_t bits[2] = {visible_bits(lo - kv_first, hi - kv_first),
+                                    visible_bits(lo - kv_first - 32, hi - kv_first - 32)};
 #pragma unroll
           for (int k = 0; k < 64; ++k)
-            if (static_cast<unsigned>(k) - first >= width) x[k] = 0u;
-        }
+            if (!((bits[k >> 5] >> (k & 31)) & 1u)) drop(k);
+        };
+        if (CAP && partial) mask_out([&](int k) { x[k] = 0u; });
         auto raw = [&](int k) { return f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])); };
         auto put = [&](int k, F2 v) {
           const float2 t = parts(v);
@@ -450,11 +453,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             put(k, mul(get(k), fma(mul(th, f2(-1.f)), th, f2(1.f))));
           }
         }
-        if (partial) {
-#pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (static_cast<unsigned>(k) - first >= width) pr[k] = 0.f;
-        }
+        if (partial) mask_out([&](int k) { pr[k] = 0.f; });
       } else if (kv_first + 63 <= limit) {  // every key of the half-tile visible
 #pragma unroll
         for (int k = 0; k < 64; ++k) pr[k] = ex2_approx(fmaf(__uint_as_float(x[k]), sl2, -lse2));

@@ -12,8 +12,8 @@
 // one (a bias: +70% of the instructions, a cap: twice), at one warp per scheduler issuing every
 // third cycle: two warpgroups share the score tiles, one the even ones, one the odd ones.
 // 2 x 4096 rows of 16 heads in 1 / 5 / 40 documents, us, against one CTA per query tile:
-//   mask alone 178 / 90 / 52 (143 / 92 / 67)   bias 198 / 103 / 58 (234 / 124 / 78)
-//   cap 268 / 143 / 75 (269 / 168 / 96)
+//   mask alone 179 / 90 / 51 (143 / 92 / 67)   bias 200 / 103 / 57 (234 / 124 / 78)
+//   cap 262 / 134 / 69 (269 / 168 / 96)
 // What bounds it: a 128 x 128 tile's products move 208 KB through shared memory, 1625 cycles at
 // 128 B a cycle, and take ~2100 with their hand-offs; a warpgroup has twice that for its softmax
 // and needs ~2600. S(g) -> P(g) -> S(g + 3) is the chain that sets the pace.
@@ -127,15 +127,16 @@ struct Params {
   ModParams mod;
 };
 
-// 32 raw scores -> exponents t2, -inf where masked. first, width: the visible keys among them;
-// dist: to the first of them.
+// 32 raw scores -> exponents t2, -inf where masked. [first, end): the visible keys among
+// them, where not all are (partial); dist: to the first of them.
 template <bool CAP, bool BIAS>
-__device__ __forceinline__ void exponents(uint32_t (&x)[32], bool partial, unsigned first, unsigned width,
+__device__ __forceinline__ void exponents(uint32_t (&x)[32], bool partial, int first, int end,
                                           const Params& p, float slope2, float dist) {
   if (CAP && partial) {  // a masked score must not decide how the row's others are capped
+    const uint32_t bits = visible_bits(first, end);
 #pragma unroll
     for (int k = 0; k < 32; ++k)
-      if (static_cast<unsigned>(k) - first >= width) x[k] = 0u;
+      if (!((bits >> k) & 1u)) x[k] = 0u;
   }
   if constexpr (CAP) {
     if (all_small<32>(x, p.mod.u_scale)) {
@@ -169,9 +170,10 @@ __device__ __forceinline__ void exponents(uint32_t (&x)[32], bool partial, unsig
     }
   }
   if (partial) {
+    const uint32_t bits = visible_bits(first, end);
 #pragma unroll
     for (int k = 0; k < 32; ++k)
-      if (static_cast<unsigned>(k) - first >= width) x[k] = 0xff800000u;  // -inf
+      if (!((bits >> k) & 1u)) x[k] = 0xff800000u;  // -inf
   }
 }
 
@@ -544,7 +546,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint32_t s_addr = tmem + buf * 128 + lane_off;
         const int kt = BIAS ? it.n - 1 - (g - g0) : g - g0;  // key tile of the walk
         const int kv0 = (it.j0 + kt) * BKV;
-        const unsigned width = static_cast<unsigned>(max(hi - lo, 0));
         bool tile_seen = false;
         // weights already written (chunks of 16 columns before `end`) times 2^by
         auto scale_weights = [&](int end, const Pow2& factor) {
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tmem_wait_ld();
           const int k0 = kv0 + 32 * c;
           const bool partial = !__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + 32);
-          exponents<CAP, BIAS>(x, partial, static_cast<unsigned>(lo - k0), width, p, slope2,
+          exponents<CAP, BIAS>(x, partial, lo - k0, hi - k0, p, slope2,
                                pos - static_cast<float>(kt * BKV + 32 * c));
           float a0 = max3f(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2])), a1 = __uint_as_float(x[3]);
 #pragma unroll

@@ -30,6 +30,7 @@
 // a warp sees whole takes no compares.
 #include "internal.h"
 #include "ptx.cuh"
+#include "score_mod.cuh"
 
 LAGA_TRACE_DEFINE(fwd)
 
@@ -361,10 +362,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int kv0 = (j0 + j) * BKV;
       if constexpr (MASKED) {
         if (!__all_sync(0xffffffffu, lo <= kv0 && hi >= kv0 + BKV)) {
-          const unsigned first = static_cast<unsigned>(lo - kv0), width = static_cast<unsigned>(max(hi - lo, 0));
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (static_cast<unsigned>(i) - first >= width) x[i] = 0xff800000u;  // -inf
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = visible_bits(lo - kv0 - 32 * c, hi - kv0 - 32 * c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((bits >> i) & 1u)) x[32 * c + i] = 0xff800000u;  // -inf
+          }
         }
       } else if (kv0 + BKV - 1 > limit) {
 #pragma unroll

@@ -38,6 +38,18 @@ __device__ __forceinline__ float tanh_rel(float u) {
   return fabsf(u) < 0.1f ? u * fmaf(w, fmaf(w, 2.f / 15.f, -1.f / 3.f), 1.f) : tanh_abs(u);
 }
 
+// Bit k of 32: key k of a run is visible, for the visible interval [first, end) relative to the run.
+// Testing a bit a key costs less than comparing each key's index (2 x 4096 rows in 5 documents,
+// capped: forward 141 -> 134 us, dq 151 -> 147). Only where a tile is partly masked: made for every
+// tile, the bits cost dq 3% of a long walk.
+__device__ __forceinline__ uint32_t visible_bits(int first, int end) {
+  const int a = min(max(first, 0), 32), e = min(max(end, 0), 32);
+  uint32_t below_a, below_e;  // shl gives 0 for 32, and 0 - 1 all bits
+  asm("shl.b32 %0, 1, %1;" : "=r"(below_a) : "r"(a));
+  asm("shl.b32 %0, 1, %1;" : "=r"(below_e) : "r"(e));
+  return (below_e - 1u) & ~(below_a - 1u);
+}
+
 // Two fp32 values in one 64-bit register: products and sums of pairs are one instruction.
 struct F2 {
   uint64_t v;
