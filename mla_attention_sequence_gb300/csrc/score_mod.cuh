@@ -50,6 +50,18 @@ __device__ __forceinline__ uint32_t visible_bits(int first, int end) {
   return (below_e - 1u) & ~(below_a - 1u);
 }
 
+// Bit j of lane i becomes bit i of lane j.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+  constexpr uint32_t low[5] = {0x0000ffffu, 0x00ff00ffu, 0x0f0f0f0fu, 0x33333333u, 0x55555555u};
+#pragma unroll
+  for (int s = 0; s < 5; ++s) {
+    const int j = 16 >> s;
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+    x = lane & j ? ((y >> j) & low[s]) | (x & ~low[s]) : (x & low[s]) | ((y & low[s]) << j);
+  }
+  return x;
+}
+
 // Two fp32 values in one 64-bit register: products and sums of pairs are one instruction.
 struct F2 {
   uint64_t v;
