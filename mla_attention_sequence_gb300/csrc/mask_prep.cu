@@ -241,12 +241,14 @@ __global__ void __launch_bounds__(1024) mask_tiles_kernel(int kt, int nq64, cons
   }
   __shared__ bool last;
   __shared__ int warp_n[32];
-  __threadfence();
+  if (gridDim.x > 1) __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(&counters[1], 1) == static_cast<int>(gridDim.x) - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
+  if (gridDim.x > 1) {  // a batch of one needs no count of its CTAs
+    if (threadIdx.x == 0) last = atomicAdd(&counters[1], 1) == static_cast<int>(gridDim.x) - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+  }
   const int total = kt * static_cast<int>(gridDim.x);
   int base = 0;
   for (int i0 = 0; i0 < total; i0 += 1024) {
@@ -255,11 +257,9 @@ __global__ void __launch_bounds__(1024) mask_tiles_kernel(int kt, int nq64, cons
     const unsigned m = __ballot_sync(0xffffffffu, in);
     if (lane == 0) warp_n[warp] = __popc(m);
     __syncthreads();
-    int before = base, all = 0;
-    for (int k = 0; k < 32; ++k) {
-      if (k < warp) before += warp_n[k];
-      all += warp_n[k];
-    }
+    const int n = warp_n[lane];
+    const int before = base + __reduce_add_sync(0xffffffffu, lane < warp ? n : 0);
+    const int all = __reduce_add_sync(0xffffffffu, n);
     if (in) seen_list[before + __popc(m & ((1u << lane) - 1u))] = i;
     base += all;
     __syncthreads();
