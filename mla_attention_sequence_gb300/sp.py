@@ -155,11 +155,18 @@ class SPAttention:
 
     Every rank calls forward / backward with its own shard (layout.rows(rank) of
     the sequence): q, dout [B, S/SP, n_h, .]; c_kv_shard [B, S/SP, d_c];
-    k_rope_shard [B, S/SP, d_rope]; and the full W_UK, W_UV (replicated)."""
+    k_rope_shard [B, S/SP, d_rope]; and the full W_UK, W_UV (replicated).
+
+    local_fwd / local_bwd replace the plain local steps. overlap=True rebuilds K/V as the
+    chunks of the latent arrive and runs the steps of `ops` (the plain causal attention)
+    instead, so it refuses a local_fwd or local_bwd, which it would never call."""
 
     def __init__(self, layout: Layout, group=None, causal: bool = True,
                  local_fwd: Callable | None = None, local_bwd: Callable | None = None,
                  overlap: bool = False, ops=None):
+        if overlap and (local_fwd is not None or local_bwd is not None):
+            raise ValueError("overlap=True runs the steps of `ops`, not local_fwd / local_bwd (a mask in them would be "
+                             "lost): give one or the other")
         self.layout = layout
         self.group = group
         self.causal = causal

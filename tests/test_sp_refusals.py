@@ -1,0 +1,35 @@
+"""What SPAttention and the packed documents' local steps refuse, before any collective or launch."""
+import os
+import socket
+
+import pytest
+import torch
+import torch.distributed as dist
+
+from mla_attention_sequence_gb300.sp import LibraryOps, Layout, SPAttention, packed_document_ops
+
+
+@pytest.fixture(scope="module")
+def group():
+    with socket.socket(socket.AF_INET, socket.SOCK_STREAM) as s:
+        s.bind(("127.0.0.1", 0))
+        port = s.getsockname()[1]
+    os.environ["MASTER_ADDR"] = "127.0.0.1"
+    os.environ["MASTER_PORT"] = str(port)
+    dist.init_process_group("gloo", rank=0, world_size=1)
+    yield
+    dist.destroy_process_group()
+
+
+STARTS = torch.tensor([[0, 3, 8]], dtype=torch.int32)
+
+
+def test_overlap_refuses_local_steps_that_it_would_not_call(group):
+    fwd, bwd = packed_document_ops(STARTS)
+    for kw in (dict(local_fwd=fwd, local_bwd=bwd), dict(local_fwd=fwd), dict(local_bwd=bwd),
+               dict(local_fwd=fwd, local_bwd=bwd, ops=LibraryOps())):
+        with pytest.raises(ValueError, match="overlap"):
+            SPAttention(Layout(8, 1), overlap=True, **kw)
+    SPAttention(Layout(8, 1), overlap=True)
+    SPAttention(Layout(8, 1), overlap=True, ops=LibraryOps())
+    SPAttention(Layout(8, 1), local_fwd=fwd, local_bwd=bwd)
