@@ -130,9 +130,13 @@ def packed_document_ops(doc_starts, prefix=None, window: int = 0, softcap: float
     each rank's rows seeing the keys of their own document (laga.key_bounds of doc_starts [B, n_docs + 1],
     prefix, window, at the rank's positions in the gathered sequence), capped scores and a bias by
     distance as in laga.masked_fwd. doc_starts counts positions of the whole sequence and is the same on
-    every rank."""
+    every rank. Without a prefix the rows see no further than themselves, so the steps refuse
+    causal=False (prefixes as long as the documents let a row see all of its own)."""
     def mods(q, c_kv, q_offset, causal, q_split, q_offset2):
         from . import laga
+        if not causal and prefix is None:
+            raise ValueError("packed documents without a prefix are causal: use SPAttention(causal=True), or give "
+                             "prefixes as long as the documents")
         lo, hi = laga.key_bounds(doc_starts, q.shape[1], q_offset=q_offset, prefix=prefix, window=window,
                                  skv=c_kv.shape[1], q_split=q_split, q_offset2=q_offset2)
         return dict(key_lo=lo, key_hi=hi, softcap=softcap, slopes=slopes, q_offset=q_offset,

@@ -33,3 +33,17 @@ def test_overlap_refuses_local_steps_that_it_would_not_call(group):
     SPAttention(Layout(8, 1), overlap=True)
     SPAttention(Layout(8, 1), overlap=True, ops=LibraryOps())
     SPAttention(Layout(8, 1), local_fwd=fwd, local_bwd=bwd)
+
+
+def test_documents_refuse_attention_that_is_not_causal():
+    fwd, bwd = packed_document_ops(STARTS, window=2)
+    x = [torch.zeros(1, 8, 1, 4), torch.zeros(1, 8, 4), torch.zeros(1, 8, 2), torch.zeros(4, 2), torch.zeros(4, 2)]
+    out, lse = torch.zeros(1, 8, 1, 2), torch.zeros(1, 1, 8)
+    with pytest.raises(ValueError, match="causal"):
+        fwd(*x, 0, False, 0, 0)
+    with pytest.raises(ValueError, match="causal"):
+        bwd(*x, out, lse, out, 0, False, 0, 0)
+    # with prefixes the rows see ahead as far as those reach, whatever `causal` says; CPU tensors are refused later
+    fwd, _ = packed_document_ops(STARTS, prefix=torch.tensor([[3, 5]], dtype=torch.int32))
+    with pytest.raises(RuntimeError, match="CUDA"):
+        fwd(*x, 0, False, 0, 0)
