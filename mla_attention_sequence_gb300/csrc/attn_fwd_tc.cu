@@ -384,9 +384,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int i = 4; i < 128; i += 8) {
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-          if constexpr (MASKED) {  // exactly the tile's 128 scores: a far biased row's maximum may be any number
-            if (i + 2 * a >= 128) continue;
-          }
+          if (i + 2 * a >= 128) continue;  // exactly the tile's 128 scores: their maximum may be any number
           m4[a] = max3f(m4[a], __uint_as_float(x[i + 2 * a]), __uint_as_float(x[i + 2 * a + 1]));
         }
       }
