@@ -586,13 +586,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint32_t s_addr = tmem + COL_S + 64u * (gs & 1) + lane_off;
         float pr[32];
         uint32_t u[32];
+        bool partial = false;       // masked: some query of the half-tile does not see some key of the warp,
+        uint32_t queries = 0u;      // and which see this thread's, a bit each
         {
           tmem_ld32(s_addr + 32 * half, u);
           tmem_wait_ld();
           if constexpr (MASKED) {
             const int2 mine = reinterpret_cast<const int2*>(smem + OFF_BND + s * BND_BYTES)[32 * half + lane];  // a query's
             const int k_first = kv0 + quarter * 32;  // the warp's first key row
-            const bool whole = __all_sync(0xffffffffu, (mine.x & 0x7fffffff) <= k_first && mine.y >= k_first + 32);
+            partial = !__all_sync(0xffffffffu, (mine.x & 0x7fffffff) <= k_first && mine.y >= k_first + 32);
             float slope2 = 0.f, dist = 0.f;
             if constexpr (BIAS) {
               const int qi = reinterpret_cast<const volatile int*>(smem + OFF_QT)[s] * BQ + 32 * half;
@@ -614,9 +616,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               if constexpr (BIAS) t2 = fmaf(-slope2, fabsf(dist + static_cast<float>(k)), t2);
               pr[k] = ex2_approx(t2);
             }
-            if (!whole) {  // a query a lane, its keys a bit each; turned over: a key a lane, its queries a bit each
-              const uint32_t queries =
-                  transpose_bits(visible_bits((mine.x & 0x7fffffff) - k_first, mine.y - k_first), lane);
+            if (partial) {  // a query a lane, its keys a bit each; turned over: a key a lane, its queries a bit each
+              queries = transpose_bits(visible_bits((mine.x & 0x7fffffff) - k_first, mine.y - k_first), lane);
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (!((queries >> k) & 1u)) pr[k] = 0.f;
@@ -661,10 +662,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(dp_free);  // dP(i+1) may overwrite the dP^T columns
           uint32_t w[16];
+          auto ds = [&](int k) { return pr[k] * (__uint_as_float(u[k]) - dlt[k]); };
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            w[k] = pack_bf16x2(pr[2 * k] * (__uint_as_float(u[2 * k]) - dlt[2 * k]),
-                               pr[2 * k + 1] * (__uint_as_float(u[2 * k + 1]) - dlt[2 * k + 1]));
+          for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(ds(2 * k), ds(2 * k + 1));
+          if (MASKED && partial) {
+            // A masked pair's dP (or, capped, its score) may have overflowed, from padding's dO or q: its dS is 0
+            // all the same. Setting every masked dS to 0 costs 1 to 2% of a call on short documents, looking for
+            // a value that is not finite half a percent.
+            uint32_t odd = 0u;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) odd = times_zero_plus_bf16x2(w[k], odd);
+            if (odd & 0x7fff7fffu) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                w[k] = pack_bf16x2((queries >> (2 * k)) & 1u ? ds(2 * k) : 0.f,
+                                   (queries >> (2 * k)) & 2u ? ds(2 * k + 1) : 0.f);
+            }
+          }
           // dS^T packed over this half's second 16 score columns of S^T(i) (already read)
           tmem_st16(s_addr + 32 * half + 16, w);
         }

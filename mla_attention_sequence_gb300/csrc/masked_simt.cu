@@ -581,9 +581,10 @@ __device__ __forceinline__ void masked_simt_dkv(const SimtParams& p, int t, int 
         const int key = k0 + k;
         float dcap = 1.f;
         const float v = score_of(p, s[k][j], slope, pos, key, &dcap);
-        const float e = key >= r.x && key < r.y ? expf(v - L) : 0.f;
+        const bool sees = key >= r.x && key < r.y;
+        const float e = sees ? expf(v - L) : 0.f;
         s[k][j] = e;
-        dp[k][j] = e * (dp[k][j] - D) * dcap;
+        dp[k][j] = sees ? e * (dp[k][j] - D) * dcap : 0.f;  // a masked dP may have overflowed (padding's dO)
       }
       float w[RI], g[RI];
 #pragma unroll

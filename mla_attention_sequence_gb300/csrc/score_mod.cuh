@@ -62,6 +62,13 @@ __device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
   return x;
 }
 
+// a * 0 + c on both halves: c, or a NaN where a is not finite.
+__device__ __forceinline__ uint32_t times_zero_plus_bf16x2(uint32_t a, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0u), "r"(c));
+  return r;
+}
+
 // Two fp32 values in one 64-bit register: products and sums of pairs are one instruction.
 struct F2 {
   uint64_t v;
