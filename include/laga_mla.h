@@ -248,8 +248,10 @@ laga_status laga_mla_absorbed_fwd(const laga_mla_desc* desc, const void* q, cons
  * desc->causal). Bounds outside [0, skv] are clamped; a row with none left sees
  * nothing: its out is 0, its lse -inf, its dq 0, and it adds to no gradient.
  * softcap and slopes are constants here (no gradient).
- * Non-finite values in masked places do no harm: a key that no row sees may hold
- * infinities or NaN, and so may the q and dout of a row that sees nothing. A row that
+ * What masked places hold does no harm: a key that no row sees may hold infinities, NaN or
+ * values of any size, and so may the q and dout of a row that sees nothing. A latent or RoPE
+ * value above 2^112 in size counts as not finite (the K and V rebuilt from it may not be; up
+ * to it they are while no column of W_UK or W_UV adds up to 2^16 in size). A row that
  * sees a key whose latent or RoPE key is not finite gets NaN (out and lse); a key that
  * is seen by such a row, or by one whose q or dout is not finite, gets NaN gradients. A row
  * whose scores are all -inf (an infinite q) gets NaN as well. */

@@ -136,7 +136,7 @@ LaunchResult tc_recon_bwd_dw(const Dims& d, const bf16* c_kv, const bf16* dk_ws,
 struct MaskMeta {
   // [B][sq_pad] {first visible key, one past the last}, clamped to the existing (and, when
   // causal, the past) keys; {0, 0}: the row sees nothing. Bit 31 of the first: some key that
-  // the row sees holds a non-finite latent value (the row's result is NaN).
+  // the row sees holds a latent value that does not count as finite (the row's result is NaN).
   const int2* rows;
   const int2* q_hull;   // [B][sq_pad / 64] {lowest first key, highest one-past-last} of a 64-row tile
   const int* kt_count;  // [B][skv_pad / 128] 64-row query tiles that may see a key tile

@@ -66,7 +66,7 @@ struct MaskBuffers {
   int *seen, *seen_list;  // [B * kt]: whether a key tile is walked; the walked ones, in order
   int* counters;          // {tiles in seen_list, CTAs done, forward ticket}
   int4* work;
-  uint32_t* bad;  // [B][ceil(S / 32)] bit per key: its latent row is not finite
+  uint32_t* bad;  // [B][ceil(S / 32)] bit per key: its latent row does not count as finite
   char* c_kv;     // [B][S][d_c] with such rows zero, in the inputs' type
   char* k_rope;   // [B][S][d_rope]
   MaskMeta meta() const { return MaskMeta{rows, q_hull, kt_count, kt_list, q_bad, seen, seen_list, counters,

@@ -1,6 +1,6 @@
 // What the masked attention runs before its kernels: the visible interval of every
 // query row, the tiles that follow from it, and copies of the inputs in which rows
-// holding a non-finite value are zero.
+// holding a non-finite value (in the latent: one that its rebuild may make non-finite) are zero.
 //
 // Why the copies: the attention kernels give a masked score the weight 0 and then
 // multiply it by the key's V row (forward), or by the query's q and dO rows (dK, dV).
@@ -27,6 +27,19 @@ using ll = long long;
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(bf16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
+// The largest size of a latent or RoPE value that counts as finite: beyond it the rebuilt K and V may
+// not be (below it they are while no column of the weights adds up to 2^16), and 0 times an infinite V
+// is a NaN. Uninitialised padding holds 3e38 as readily as a NaN, and some masks fill with the type's lowest value.
+constexpr float kLatentMax = 0x1p112f;
+__device__ __forceinline__ bool latent_ok(float v) { return fabsf(v) <= kLatentMax; }  // false for a NaN
+// whether any of eight packed bf16 of a latent row is not
+__device__ __forceinline__ bool bad_latent_x2(uint32_t w) {
+  constexpr uint32_t top = (112u + 127u) << 7;  // kLatentMax as bf16
+  return (w & 0x7fffu) > top || (w & 0x7fff0000u) > top << 16;
+}
+__device__ __forceinline__ bool bad_latent_x8(uint4 v) {
+  return bad_latent_x2(v.x) || bad_latent_x2(v.y) || bad_latent_x2(v.z) || bad_latent_x2(v.w);
+}
 // whether any of eight packed bf16 is infinite or NaN
 __device__ __forceinline__ bool bad_bf16x2(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
@@ -36,7 +49,7 @@ __device__ __forceinline__ bool bad_bf16x8(uint4 v) {
 }
 
 // Latent rows -> clean copies; one CTA (unit) per 32 keys of a batch element, a warp for four of
-// them. bad[b][word] bit r: key 32 * word + r holds a non-finite value.
+// them. bad[b][word] bit r: key 32 * word + r holds a value that does not count as finite.
 // The tensor-core dims: the four rows' 72 16-byte chunks each are loaded before the first is
 // looked at (row by row the kernel took 11 us however few keys there were).
 constexpr int KEY_ROWS = 4;
@@ -57,11 +70,11 @@ __device__ __forceinline__ void clean_keys_tc(int S, int unit, int units, const 
 #pragma unroll
     for (int i = 0; i < 2; ++i) v[k][i] = j0 + k < S ? cs[k * NC + 32 * i + lane] : zero;
   w = j0 + (lane >> 3) < S ? rs[lane] : zero;  // the four RoPE keys, eight lanes each
-  const unsigned rope_bad = __ballot_sync(0xffffffffu, bad_bf16x8(w));
+  const unsigned rope_bad = __ballot_sync(0xffffffffu, bad_latent_x8(w));
   uint32_t mask = 0u;
 #pragma unroll
   for (int k = 0; k < KEY_ROWS; ++k)
-    if (__any_sync(0xffffffffu, bad_bf16x8(v[k][0]) || bad_bf16x8(v[k][1])) || (rope_bad & (0xffu << (8 * k)))) mask |= 1u << k;
+    if (__any_sync(0xffffffffu, bad_latent_x8(v[k][0]) || bad_latent_x8(v[k][1])) || (rope_bad & (0xffu << (8 * k)))) mask |= 1u << k;
   uint4* cd = reinterpret_cast<uint4*>(c_out) + (static_cast<ll>(b) * S + j0) * NC;
   uint4* rd = reinterpret_cast<uint4*>(r_out) + (static_cast<ll>(b) * S + j0) * NR;
 #pragma unroll
@@ -100,7 +113,7 @@ __device__ __forceinline__ void clean_keys(int S, int unit, int units, int d_c, 
 #pragma unroll
       for (int k = 0; k < KEY_ROWS; ++k) {
         if (!write) {
-          if (__any_sync(0xffffffffu, !finite(to_f(v[k])))) mask |= 1u << k;
+          if (__any_sync(0xffffffffu, !latent_ok(to_f(v[k])))) mask |= 1u << k;
         } else if (i < width && j0 + k < S) {
           to[static_cast<ll>(k) * width + i] = (mask >> k) & 1u ? static_cast<T>(0.f) : v[k];
         }

@@ -70,3 +70,48 @@ def test_q_of_rows_that_see_nothing(dtype, dims, value, cap):
     for b, end in ENDS:
         assert not got["out"][b, end:].any() and not got["dq"][b, end:].any()
     laga.check(dev())
+
+
+@pytest.mark.parametrize("dtype,dims", KINDS)
+@pytest.mark.parametrize("value", HUGE)
+@pytest.mark.parametrize("cap", [0.0, 9.0])
+@pytest.mark.parametrize("seen_by_padding", [False, True])
+def test_keys_outside_the_documents(dtype, dims, value, cap, seen_by_padding):
+    """The padding's latents, RoPE keys, q and dout are huge; seen_by_padding: and a document of its own, whose
+    results (and with them the weights' gradients) are anything."""
+    x, dout, kw = packed(dtype, dims, seen_by_padding)
+    kw["softcap"] = cap
+    want = step(x, dout, **kw)
+    y, dy = {k: v.clone() for k, v in x.items()}, dout.clone()
+    for b, end in ENDS:
+        y["c_kv"][b, end:] = value
+        y["k_rope"][b, end:, ::3] = -value
+        y["q"][b, end:] = value
+        dy[b, end:] = value
+    got = step(y, dy, **kw)
+    same_rows(got, want, ("dW_UK", "dW_UV") if seen_by_padding else ())
+    if not seen_by_padding:
+        for b, end in ENDS:
+            assert not got["dc_kv"][b, end:].any() and not got["dk_rope"][b, end:].any()
+    laga.check(dev())
+
+
+@pytest.mark.parametrize("dtype,dims", KINDS[:2])
+def test_a_row_that_sees_a_key_out_of_range(dtype, dims):
+    """A latent value above 2^112 counts as not finite: the rows that see its key get NaN, no others; at 2^112
+    it is a value like any other."""
+    x, dout, kw = packed(dtype, dims)
+    want = step(x, dout, **kw)
+    y = {k: v.clone() for k, v in x.items()}
+    y["c_kv"][0, 150, 5] = 1.5 * 2.0 ** 112
+    got = step(y, dout, **kw)
+    hit = torch.zeros(B, S, dtype=torch.bool, device=dev())
+    hit[0, 150:230] = True
+    assert got["out"][hit].isnan().all() and torch.equal(got["out"][~hit], want["out"][~hit])
+    assert got["dq"][hit].isnan().all() and torch.equal(got["dq"][~hit], want["dq"][~hit])
+    y["c_kv"][0, 150, 5] = -2.0 ** 112
+    y["W_UK"][5] = 0.0  # its scores stay small; its V does not
+    y["W_UV"][5] = 2.0 ** -112
+    out, lse = laga.masked_fwd(*y.values(), **kw)
+    assert bool(out[hit].isfinite().all()) and bool(lse[0, :, 150:230].isfinite().all())
+    laga.check(dev())
