@@ -34,7 +34,7 @@
 // The softmax makes one pass over a score tile, a loop of four chunks of 32 columns (unrolled, it
 // outgrows the instruction cache and its warps wait for instructions; a second pass for the
 // maximum reads the tile from TMEM and caps it twice). Its weights
-// count in 2^m for a reference m that is 0 until scores turn out to be further than 2^100 off;
+// count in 2^m for a reference m that is 0 until scores turn out to be further than 2^32 off;
 // then m moves, and what was written of the tile so far is scaled. At a tile's end the warpgroup
 // settles m with the one that tile g - 1 left for the row in shared memory (the larger stays;
 // weights and O follow it), passes it on and hands P over. With a bias the tiles are walked from
@@ -80,10 +80,13 @@ constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
 constexpr uint32_t IDESC_PV = idesc_bf16(128, 128, false, true);
 constexpr float LOG2E = 1.4426950408889634f;
 // The weights are 2^(t2 - m) for a reference m that need not be the maximum, only near enough:
-// bf16 and fp32 have the same exponents, so 2^100 rounds no worse than 1, and sums of 2^27
-// such weights stay finite. A row starts with m = 0; m is always a whole number, so that a move
-// to another m scales weights by a power of two, exactly.
-constexpr float FAR = 100.f;  // scores further off than this move the reference
+// bf16 and fp32 have the same exponents, so 2^32 rounds no worse than 1. But O holds weights times
+// V in fp32: with 2^FAR at most, 2^16 keys of a V up to 2^80 stay finite, and with 2^-FAR at least
+// a V down to 2^-80 keeps its bits (a FAR of 100 lost both ends at V of 2^36 and 2^-40, and
+// bought little: 2 x 4096 rows with a bias, the step 474 us against 478; capped 139 and 140). Below 32,
+// scores of ordinary size would move the reference. A row starts with m = 0; m is always a whole number, so that a
+// move to another m scales weights by a power of two, exactly.
+constexpr float FAR = 32.f;  // scores further off than this move the reference
 // The bounded waits of this kernel, kept short: a wait is inlined a dozen times, and the control
 // warps' code competes for the instruction cache with the softmax (with the clock-reading form
 // the issue loop took some 1750 cycles a tile, most of it waiting for instructions). The limit
