@@ -310,8 +310,9 @@ laga_status laga_mla_key_bounds(int64_t batch, int64_t sq, int64_t skv, int64_t 
  * Pair i of the d_rope / 2 pairs (x, y) turns by a = pos[axis(i)][token] * theta^(-2i/d_rope):
  * (x cos a - y sin a, x sin a + y cos a); the first sections[0] pairs use axis 0, the next
  * sections[1] axis 1, and so on. interleaved: pair i is (2i, 2i + 1), else (i, i + d_rope/2).
- * inverse turns by -a, which is also the gradient's way back. Positions may be negative and
- * as far as their type goes: the angle is exact to 2^-32 turns. */
+ * inverse turns by -a, which is also the gradient's way back. Positions may be negative. The
+ * angle is off by at most 2^-26 + 2^-32 + |pos| 2^-65 turns (2^-26: its rounding to fp32 before the
+ * sine and cosine are taken), so a position of 2^31 is as good as a near one and one of 2^39 half so. */
 #define LAGA_ROPE_MAX_AXES 4
 typedef struct {
   int64_t tokens, n_h, d_nope, d_rope;

@@ -82,10 +82,10 @@ constexpr float LOG2E = 1.4426950408889634f;
 // The weights are 2^(t2 - m) for a reference m that need not be the maximum, only near enough:
 // bf16 and fp32 have the same exponents, so 2^32 rounds no worse than 1. But O holds weights times
 // V in fp32: with 2^FAR at most, 2^16 keys of a V up to 2^80 stay finite, and with 2^-FAR at least
-// a V down to 2^-80 keeps its bits (a FAR of 100 lost both ends at V of 2^36 and 2^-40, and
-// bought little: 2 x 4096 rows with a bias, the step 474 us against 478; capped 139 and 140). Below 32,
-// scores of ordinary size would move the reference. A row starts with m = 0; m is always a whole number, so that a
-// move to another m scales weights by a power of two, exactly.
+// a V down to 2^-80 keeps its bits. (A FAR of 100 lost both ends at V of 2^36 and 2^-40 and was no
+// faster: 2 x 4096 rows with a bias take 478 us the step with either.) Below 32, scores of ordinary size would
+// move the reference. A row starts with m = 0; m is always a whole number, so that a move to another m
+// scales weights by a power of two, exactly.
 constexpr float FAR = 32.f;  // scores further off than this move the reference
 // The bounded waits of this kernel, kept short: a wait is inlined a dozen times, and the control
 // warps' code competes for the instruction cache with the softmax (with the clock-reading form

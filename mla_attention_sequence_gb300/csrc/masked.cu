@@ -82,6 +82,37 @@ size_t bwd_bytes(const Dims& d, Path path, int elem) {
                             : tc_bwd_workspace(d, masked_heads_per_cta(d)) + mask_bytes(d, elem) + tc_clean_q_bytes(d) + tc_clean_dout_bytes(d);
 }
 
+// ---- the rotation's frequencies. Positions multiply a frequency's error, so that a double's 53 bits
+// would be 2^-25 turns off at position 2^31; a pair of doubles (their exact sum, some 106 bits) leaves
+// nothing but the rounding of the 64-bit fraction itself.
+struct Pair {
+  double hi, lo;
+};
+Pair sum_of(double a, double b) {  // exact for |a| >= |b|
+  const double s = a + b;
+  return Pair{s, b - (s - a)};
+}
+Pair operator*(Pair a, Pair b) {
+  const double p = a.hi * b.hi;
+  return sum_of(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+
+// theta^(-1/n): a double's guess x, and one Newton step for x^n theta = 1.
+Pair root_step(double theta, int n) {
+  const double x = std::pow(theta, -1.0 / n);
+  Pair r{theta, 0.0}, square{x, 0.0};
+  for (int k = n; k > 0; k >>= 1, square = square * square)
+    if (k & 1) r = r * square;
+  return sum_of(x, x * ((1.0 - r.hi) - r.lo) / n);
+}
+
+// Turns per position step as a fraction of 2^64, to the nearest: f / (2 pi), at most 0.16.
+uint64_t turns_of(Pair f) {
+  const Pair t = f * Pair{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
+  const double h = std::ldexp(t.hi, 64), whole = std::floor(h);
+  return static_cast<uint64_t>(whole) + static_cast<uint64_t>(std::llrint((h - whole) + std::ldexp(t.lo, 64)));
+}
+
 bool workspace_ok(const void* ws, size_t have, size_t need) {
   return ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0;
 }
@@ -307,12 +338,12 @@ laga_status laga_mla_rope(const laga_mla_rope_desc* desc, const void* pos, const
   static thread_local laga_mla_rope_desc made;  // n_axes 0: none
   if (made.n_axes != x.n_axes || made.d_rope != x.d_rope || made.theta != x.theta ||
       !std::equal(x.sections, x.sections + x.n_axes, made.sections)) {
+    const Pair step = root_step(x.theta, static_cast<int>(x.d_rope / 2));
+    Pair f{1.0, 0.0};
     int i = 0;
     for (int a = 0; a < x.n_axes; ++a)
-      for (int k = 0; k < x.sections[a]; ++k, ++i) {
-        // f(i) / (2 pi) <= 0.16 turns per step, so the fraction fits 64 bits
-        const double turns = std::pow(x.theta, -2.0 * i / static_cast<double>(x.d_rope)) * 0.15915494309189533577;
-        t.turns[i] = static_cast<uint64_t>(std::ldexp(turns, 64));
+      for (int k = 0; k < x.sections[a]; ++k, ++i, f = f * step) {
+        t.turns[i] = turns_of(f);
         t.axis[i] = static_cast<uint8_t>(a);
       }
     made = x;

@@ -1,11 +1,11 @@
 // Rotary positions with several axes: pair i of a head's RoPE part turns by the angle
 // pos[axis(i)] * f(i). Its gradient is the turn back (inverse).
 //
-// The angle is kept in turns as a 64-bit fraction: f(i) / (2 pi) rounded to 2^-64 (its
-// 53-bit value is exact there) times the integer position, modulo one turn by the
-// multiplication's own wrap-around. Far positions so lose nothing: at position 2^20 an
-// fp32 product would be off by up to 0.06 rad. The top 32 bits then go to the fp32 sine
-// and cosine of a multiple of pi.
+// The angle is kept in turns as a 64-bit fraction: f(i) / (2 pi) rounded to 2^-64 times the
+// integer position, modulo one turn by the multiplication's own wrap-around. So it is off by
+// at most |position| 2^-65 turns, where at position 2^20 an fp32 product would be off by up to
+// 0.06 rad. Its top 32 bits (2^-32 turns more) then go, rounded to fp32's 24 (2^-26 turns),
+// to the fp32 sine and cosine of a multiple of pi.
 //
 // Memory bound: q is read and written once (the no-RoPE part is copied, or left alone in
 // place). One CTA takes a few tokens: it computes their cosines and sines once, in shared
