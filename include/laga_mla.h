@@ -283,7 +283,9 @@ laga_status laga_mla_masked_fwd(const laga_mla_desc* desc, const laga_mla_mods* 
 /* Backward: the gradients of <dout, out> as for laga_mla_bwd, with the same mods as the
  * forward. q and out come either as tensors (q8, out8 NULL) or as 8-bit checkpoints
  * (q and out NULL): then P = exp(s - lse) with the scores of the restored q, and
- * D = rowsum(dout o out) of the restored out. LAGA_FLAG_REUSE_KV: the workspace is the
+ * D = rowsum(dout o out) of the restored out. P's rows sum to 1 only if lse comes from a forward
+ * on that restored q (laga_mla_unpack8 of the checkpoint): q's rounding to 8 bits otherwise acts
+ * on P in proportion to the scores. LAGA_FLAG_REUSE_KV: the workspace is the
  * one laga_mla_masked_fwd used for the same inputs, descriptor and mods, its first
  * laga_mla_masked_fwd_workspace_size bytes intact (K, V and what the bounds became: the
  * bounds are not read again). */

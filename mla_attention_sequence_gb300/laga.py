@@ -422,7 +422,8 @@ def _check_packed(name: str, p: Packed8):
 
 
 def pack8(x: torch.Tensor) -> Packed8:
-    """laga_mla_pack8: saves a float32 or bfloat16 tensor in 8 bits along its last dimension."""
+    """laga_mla_pack8: saves a float32 or bfloat16 tensor in 8 bits along its last dimension. A q for
+    masked_bwd is packed before the forward (see there)."""
     dt, shape, dev = x.dtype, x.shape, x.device
     code = _code_of(dt)
     if not shape:
@@ -616,8 +617,10 @@ def masked_bwd(q, c_kv, k_rope, W_UK, W_UV, out, lse, dout, key_lo=None, key_hi=
                variant: str = "auto", workspace: torch.Tensor | None = None, grads: dict | None = None,
                reuse_kv: bool = False, q_split: int = 0, q_offset2: int = 0):
     """laga_mla_masked_bwd: dict dq, dc_kv, dk_rope, dW_UK, dW_UV of <dout, out>, with the forward's
-    arguments. q and out may both be Packed8 checkpoints (pack8 of the forward's q and out): the
-    backward reads them in 8 bits. reuse_kv=True: `workspace` is the one the forward ran with, its
+    arguments. q and out may both be Packed8 checkpoints: the backward reads them in 8 bits. Pack q
+    before the forward and run it on unpack8 of the checkpoint, so that lse belongs to the q that the
+    backward sees; with lse of the q before its rounding the weights exp(s - lse) do not sum to 1, the
+    further off the larger the scores. reuse_kv=True: `workspace` is the one the forward ran with, its
     K and V intact."""
     packed = isinstance(q, Packed8)
     if packed != isinstance(out, Packed8):
