@@ -56,14 +56,14 @@ def load_peaks():
 # DRAM traffic per launch of a kernel, from one ncu capture of the kernel source
 # identified by `src_sha` (sha256 of the kernel file followed by csrc/ptx.cuh,
 # first 16 hex digits). It is reported only while the source is unchanged.
-# attn_bwd_dkdv: dram__bytes_read.sum + dram__bytes_write.sum = 740.7 + 562.7 MB
+# attn_bwd_dkdv: dram__bytes_read.sum + dram__bytes_write.sum = 741.2 + 562.5 MB
 # on the n_h = 64 last-rank shard (the full n_h = 128 shard exceeds the size rule
 # for a multi-pass capture); the kernel's work and both byte streams (K/V and
 # Q/dO tiles in, dK/dV and the head-group RoPE-key partials out) scale with the
 # head count, so x2.
 MEASURED_TRAFFIC = {
-    "attn_bwd_dkdv": {"src": "attn_bwd_dkdv_tc.cu", "src_sha": "019d0ec278a7b01d",
-                      "bytes_per_launch": {"dsv3_sp8_rank7_S16384_h128": 2 * (740.734976e6 + 562.735872e6)}},
+    "attn_bwd_dkdv": {"src": "attn_bwd_dkdv_tc.cu", "src_sha": "30882edc2543b8b6",
+                      "bytes_per_launch": {"dsv3_sp8_rank7_S16384_h128": 2 * (741.229312e6 + 562.467584e6)}},
 }
 
 

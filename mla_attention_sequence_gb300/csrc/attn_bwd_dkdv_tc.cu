@@ -52,8 +52,8 @@
 // list; each stage also brings its 64 rows' visible intervals. q and dO may be read
 // from copies whose non-finite rows are zero (a masked query row's P^T and dS^T are 0,
 // but 0 times a NaN of its q or dO row would reach every key of the tile). 2 x 4096 rows of 16
-// heads, 5 documents and a bias: 147 us; 2048 rows of 128 heads over the 16384 keys of 4 documents:
-// 2.3 to 2.4 ms, the plain kernel's rate. Partly masked tiles by a bit a key and query (see
+// heads, 5 documents and a bias: 150 us; 2048 rows of 128 heads over the 16384 keys of 4 documents:
+// 2.4 ms, the plain kernel's rate. Partly masked tiles by a bit a key and query (see
 // transpose_bits) instead of two compares: 40 documents 94 -> 90 us, the shard in 40 292 -> 270.
 #include "internal.h"
 #include "ptx.cuh"

@@ -1,5 +1,12 @@
 // C ABI of the operators around packed documents: key bounds, masked attention forward and
 // backward, rotary positions, 8-bit checkpoints. Argument checks, workspace layout, dispatch.
+//
+// Where the bf16 calls round to fewer bits than the fp32 they sum in: K and V, the weights P and dS,
+// because they are operands of bf16 products (as fp32 each would be split in two or three, and every
+// product would take as many times as long); dK and dV, because they are the next products' operands and
+// are stored between the kernels (twice the bytes in fp32); out, from which the backward takes D, because
+// the caller keeps it in bf16. As in the plain calls: 0.003 to 0.004 from 64 bits where one rounding of
+// the outputs gives 0.0017. The CUDA-core path rounds inputs and outputs alone.
 #include "api_util.h"
 #include "mask.h"
 #include "rope.h"
@@ -175,8 +182,9 @@ laga_status laga_mla_masked_fwd(const laga_mla_desc* desc, const laga_mla_mods* 
               [&] { return tc_recon_fwd(d, cb(m.c_kv), cb(W_UK), cb(W_UV), k_ws, v_ws, d.skv_pad, s, 0, -1, &list); });
   // Without a cap or bias a long walk is better off with one CTA per query tile (2048 rows of 128
   // heads over up to 16384 keys: 1.04 ms against 1.23), short ones with CTAs that stay (2 x 4096
-  // rows of 16 heads, documents of ~100 keys: 52 us against 67; of ~800: 90 against 92). How long
-  // the walks are only the device knows; how long they can be, the sizes say.
+  // rows of 16 heads, documents of ~100 keys: 52 us against 67; of ~800: 90 against 92; but one
+  // document of 4096: 179 against 143). How long the walks are only the device knows; how long they
+  // can be, the sizes say.
   const bool long_walks = mod_of(sm) == 0 && d.skv_pad >= 64 * 128;
   if (r.ok())
     r = timed("masked_attn_fwd", s, [&] {
