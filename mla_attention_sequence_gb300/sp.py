@@ -131,7 +131,8 @@ def packed_document_ops(doc_starts, prefix=None, window: int = 0, softcap: float
     prefix, window, at the rank's positions in the gathered sequence), capped scores and a bias by
     distance as in laga.masked_fwd. doc_starts counts positions of the whole sequence and is the same on
     every rank. Without a prefix the rows see no further than themselves, so the steps refuse
-    causal=False (prefixes as long as the documents let a row see all of its own)."""
+    causal=False (prefixes as long as the documents let a row see all of its own). The two belong
+    together: SPAttention refuses a backward with one of them and another step."""
     def mods(q, c_kv, q_offset, causal, q_split, q_offset2):
         from . import laga
         if not causal and prefix is None:
@@ -151,6 +152,7 @@ def packed_document_ops(doc_starts, prefix=None, window: int = 0, softcap: float
         return laga.masked_bwd(q, c_kv, k_rope, W_UK, W_UV, out, lse, dout,
                                **mods(q, c_kv, q_offset, causal, q_split, q_offset2))
 
+    local_fwd.partner, local_bwd.partner = local_bwd, local_fwd
     return local_fwd, local_bwd
 
 
@@ -271,6 +273,10 @@ class SPAttention:
         summed over all ranks' queries) and dW_UK, dW_UV (summed over the group)."""
         if self._saved is None:
             raise RuntimeError("backward before forward")
+        fwd, bwd = self.local_fwd, self.local_bwd
+        if getattr(fwd, "partner", bwd) is not bwd or getattr(bwd, "partner", fwd) is not fwd:
+            raise ValueError("local_fwd and local_bwd are not of one packed_document_ops: the backward's mask would not "
+                             "be the forward's")
         q, c_kv, k_rope, W_UK, W_UV, out, lse = self._saved
         pos = self.layout.query_args(self.rank)
         if self._ws is not None:  # overlapped forward: its workspace still holds K_nope / V

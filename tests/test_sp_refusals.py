@@ -47,3 +47,27 @@ def test_documents_refuse_attention_that_is_not_causal():
     fwd, _ = packed_document_ops(STARTS, prefix=torch.tensor([[3, 5]], dtype=torch.int32))
     with pytest.raises(RuntimeError, match="CUDA"):
         fwd(*x, 0, False, 0, 0)
+
+
+def test_backward_refuses_another_mask_than_the_forwards(group):
+    (fwd, bwd), (other, _) = packed_document_ops(STARTS), packed_document_ops(STARTS, window=2)
+    saved = (None,) * 7
+    for kw in (dict(local_fwd=fwd), dict(local_bwd=bwd), dict(local_fwd=other, local_bwd=bwd)):
+        block = SPAttention(Layout(8, 1), **kw)
+        block._saved = saved  # as a forward leaves it
+        with pytest.raises(ValueError, match="mask"):
+            block.backward(None)
+    calls = []
+
+    def plain_fwd(*a):
+        calls.append("fwd")
+
+    def plain_bwd(*a):
+        calls.append("bwd")
+        raise KeyError("reached")
+    for kw in (dict(local_bwd=plain_bwd), dict(local_fwd=plain_fwd, local_bwd=plain_bwd)):
+        block = SPAttention(Layout(8, 1), **kw)
+        block._saved = saved
+        with pytest.raises(KeyError):
+            block.backward(None)
+    assert calls == ["bwd", "bwd"]
