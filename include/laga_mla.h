@@ -344,6 +344,91 @@ laga_status laga_mla_pack8(int32_t dtype, int64_t rows, int64_t cols, const void
 laga_status laga_mla_unpack8(int32_t dtype, int64_t rows, int64_t cols, const uint8_t* codes, const uint8_t* scales,
                              void* x, laga_stream_t stream);
 
+/* ---- RMS norms of the query heads and of the shared RoPE key, with the rotation in the same pass:
+ *   q_out[t,h,:] = R(pos_t) (q[t,h,:] / sqrt(mean(q[t,h,:]^2) + eps) o q_weight),
+ * the mean over the whole head (d_nope + d_rope), the rotation on its RoPE part; k_out likewise from
+ * k_rope and k_weight [d_rope]. desc as for laga_mla_rope (inverse 0), d_nope + d_rope <= 1024, eps
+ * between 1e-30 and 1e10. q with q_weight and q_out, or k_rope with k_weight and k_out, may be NULL.
+ * q_out and k_out may be q and k_rope themselves, and may not overlap them otherwise. Pointers aligned
+ * to their type (16 bytes for the fast path). */
+laga_status laga_mla_norm_rope(const laga_mla_rope_desc* desc, float eps, const void* pos, const void* q,
+                               const void* k_rope, const void* q_weight, const void* k_weight, void* q_out, void* k_out,
+                               laga_stream_t stream);
+
+/* Its backward: from dq_out and dk_out, the gradients of q_out and k_out, those of q, k_rope and both
+ * weights (summed over all rows in a fixed order). q and k_rope are the rows before the norm. dq may be
+ * dq_out or q, dk_rope may be dk_out or k_rope. workspace: laga_mla_norm_rope_bwd_workspace_size bytes
+ * (0: refused), 256-byte aligned, overwritten. What belongs to a NULL q or k_rope is NULL too. */
+size_t laga_mla_norm_rope_bwd_workspace_size(const laga_mla_rope_desc* desc);
+laga_status laga_mla_norm_rope_bwd(const laga_mla_rope_desc* desc, float eps, const void* pos, const void* dq_out,
+                                   const void* dk_out, const void* q, const void* k_rope, const void* q_weight,
+                                   const void* k_weight, void* dq, void* dk_rope, void* dq_weight, void* dk_weight,
+                                   void* workspace, size_t workspace_bytes, laga_stream_t stream);
+
+/* ---- A paged cache for decoding: per token the latent in 4 bits and the rotated RoPE key.
+ * Position p of sequence b lies in row p % page_size of page table[b][p / page_size].
+ * A block of 16 latent values has a scale, the smallest of the grid with 6 scale >= its largest size
+ * (the largest of the grid if there is none), and 4-bit codes: the nearest of 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6 times the scale (indices 0 .. 7, ties to the even index) with a sign (8). Two codes in a byte, the
+ * even column's in the low half; a scale byte is the upper 8 of an fp16's 15 bits below the sign, at
+ * most 226 (1.25 * 2^13). So values are held to 1/4 of their block's largest size or better, down to
+ * steps of 2^-18; sizes above 61440 become 61440. A block with a value that is not finite gets the
+ * scale 255 and reads as NaN throughout. RoPE keys are kept in dtype.
+ * A position that the call needs and that has no page (the table too short, or an entry that is no
+ * page) is never accessed: an append leaves it out, a read gives NaN, a row of the attention that sees
+ * it gets NaN, and the next laga_mla_check returns LAGA_ERR_INVALID_ARG. */
+typedef struct {
+  uint8_t* codes;    /* [pages, page_size, ceil(d_c / 2)] */
+  uint8_t* scales;   /* [pages, page_size, ceil(d_c / 16)] */
+  void* k_rope;      /* [pages, page_size, d_rope], dtype (NULL if d_rope is 0) */
+  int64_t pages;
+  int64_t page_size; /* <= 65536 */
+  int64_t d_c;       /* <= 1024 */
+  int64_t d_rope;    /* <= 256 */
+  int32_t dtype;     /* laga_dtype of k_rope and of the calls' tensors */
+} laga_mla_cache4;
+
+/* Appends rows i < counts[b] (counts NULL: all) of the padded batch c_kv [batch, rows, d_c], k_rope
+ * [batch, rows, d_rope] at positions starts[b] + i of sequence b. On the way the keys are normed (with
+ * k_weight [d_rope] and eps; k_weight NULL: not) and turned as by laga_mla_rope (rope NULL: not): by
+ * pos [n_axes, batch * rows], or with pos NULL by their positions in the sequence (one axis).
+ * rope->tokens is batch * rows; its n_h and d_nope are not used. Two rows of one call that lie in the
+ * same place (sequences that share a page they both write) leave it undefined. table [batch,
+ * max_pages]; starts, counts [batch]. Device pointers; cache arrays 16-byte aligned, tensors aligned
+ * to their type. */
+laga_status laga_mla_cache4_append(const laga_mla_cache4* cache, int64_t batch, int64_t rows, int64_t max_pages,
+                                   const int32_t* table, const int32_t* starts, const int32_t* counts, const void* c_kv,
+                                   const void* k_rope, const void* k_weight, float eps, const laga_mla_rope_desc* rope,
+                                   const void* pos, laga_stream_t stream);
+
+/* Reads positions starts[b] + i, i < counts[b] (NULL: all rows), back as c_kv [batch, rows, d_c] and
+ * k_rope [batch, rows, d_rope] (for a chunk of a prompt over cached tokens by laga_mla_fwd, which
+ * rebuilds K and V). Rows past counts[b] become zero. */
+laga_status laga_mla_cache4_read(const laga_mla_cache4* cache, int64_t batch, int64_t rows, int64_t max_pages,
+                                 const int32_t* table, const int32_t* starts, const int32_t* counts, void* c_kv,
+                                 void* k_rope, laga_stream_t stream);
+
+/* Attention of the last sq tokens of each sequence over the cache, q already normed and turned:
+ * out [batch, sq, n_h, d_v] and lse [batch, n_h, sq] as laga_mla_masked_fwd gives them on the values
+ * that the cache stands for, computed in the latent space (q W_UK^T against the latents; the context
+ * of latents times W_UV). lengths[b] counts the cached tokens, the call's own among them; query i is
+ * at position lengths[b] - sq + i and sees the keys j < lengths[b], j <= its position when causal, and
+ * mods' key_lo <= j < key_hi. Rows that see nothing (an empty sequence, a padded row before the first
+ * position): out 0, lse -inf. A row that sees a key whose latent or RoPE key is not finite gets NaN;
+ * what other places of the pool hold does no harm. */
+typedef struct {
+  int64_t batch, sq, n_h, d_nope, d_v; /* d_nope + d_rope <= 256, d_v <= 256 */
+  int64_t max_pages;                   /* columns of table */
+  int32_t causal;
+  float softmax_scale;                 /* <= 0 selects 1/sqrt(d_nope + d_rope) */
+  int32_t variant;                     /* LAGA_VARIANT_AUTO or LAGA_VARIANT_SIMT */
+} laga_mla_cache4_desc;
+size_t laga_mla_cache4_fwd_workspace_size(const laga_mla_cache4_desc* desc, const laga_mla_cache4* cache);
+laga_status laga_mla_cache4_fwd(const laga_mla_cache4_desc* desc, const laga_mla_cache4* cache, const laga_mla_mods* mods,
+                                const int32_t* table, const int32_t* lengths, const void* q, const void* W_UK,
+                                const void* W_UV, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                laga_stream_t stream);
+
 /* Largest workspace, in bytes, that laga_mla_fwd_noalloc can stand in for. */
 #define LAGA_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)
 
@@ -369,7 +454,7 @@ laga_status laga_mla_fwd_noalloc(const laga_mla_desc* desc, const void* q, const
 
 /* Synchronises the stream, then reads and clears this device's status word.
  * Returns LAGA_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last
- * check, LAGA_ERR_CUDA if the stream reports an error, else LAGA_OK. */
+ * check, LAGA_ERR_INVALID_ARG if one met a cached position without a page, LAGA_ERR_CUDA if the stream reports an error, else LAGA_OK. */
 laga_status laga_mla_check(laga_stream_t stream);
 
 /* Static string naming a status code. */
@@ -404,7 +489,8 @@ laga_status laga_mla_selftest_timeout(laga_stream_t stream);
 /* Library ABI version: major*10000 + minor*100 + patch. 200 (0.2.0): laga_mla_desc
  * gained q_split and q_offset2 (two-segment query shards); zero them for the
  * single-segment behaviour of 100. 300 (0.3.0): masked attention, rotary positions,
- * 8-bit checkpoints; nothing that was there changed. */
+ * 8-bit checkpoints; nothing that was there changed. 400 (0.4.0): norms with rotation, the paged
+ * 4-bit latent cache and attention over it; nothing that was there changed. */
 int laga_mla_version(void);
 
 #ifdef __cplusplus

@@ -574,6 +574,10 @@ laga_status laga_mla_check(laga_stream_t stream) {
     std::snprintf(t_last_error, sizeof(t_last_error), "device wait expired (site %d)", status >> 8);
     return LAGA_ERR_TIMEOUT;
   }
+  if ((status & 0xff) == LAGA_ERR_INVALID_ARG) {
+    std::snprintf(t_last_error, sizeof(t_last_error), "a cached position without a page in the table (site %d)", status >> 8);
+    return LAGA_ERR_INVALID_ARG;
+  }
   return LAGA_OK;
 }
 
@@ -613,6 +617,6 @@ int laga_mla_profile_read(const char** names, float* ms, int max) {
   return n;
 }
 
-int laga_mla_version(void) { return 300; }
+int laga_mla_version(void) { return 400; }
 
 }  // extern "C"

@@ -27,6 +27,15 @@ LaunchResult timed(const char* name, cudaStream_t s, F&& f) {
 
 enum class Path { Invalid, Simt, TensorCore, TensorCoreFused };
 
+// Checks a masked call's mods; fills out.
+laga_status check_mods(const laga_mla_mods* mods, ScoreMods* out);
+
+// Checks a rotation's descriptor and positions; fills args but for the tensors, and the table of
+// its frequencies (of this host thread, until its next call).
+struct RopeArgs;
+struct RopeTable;
+laga_status rope_plan(const laga_mla_rope_desc* desc, const void* pos, RopeArgs* args, const RopeTable** table);
+
 // Validate the descriptor; fill dims; choose a path. On error, sets *st.
 Path plan(const laga_mla_desc* desc, Dims* d, laga_status* st, bool for_bwd);
 

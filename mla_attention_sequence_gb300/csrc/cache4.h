@@ -1,0 +1,149 @@
+// The paged cache of latents in 4 bits: its layout, and the interfaces of the kernels that write it,
+// read it and attend over it.
+#pragma once
+#include "rope.h"
+
+namespace laga {
+
+constexpr int kCacheBlock = 16;      // latent values that share a scale
+constexpr int kCacheTopScale = 226;  // largest scale, 1.25 * 2^13: 6 of them are the largest value, 61440
+constexpr int kCacheNanScale = 255;  // a block that held a value that is not finite
+
+// A scale byte is the upper 8 of an fp16's 15 bits below the sign. A code of at most two significant
+// bits times a scale of at most four is a multiple of 2^-18 of at most 61440: exact in fp16 (and in
+// bf16 and fp32), so that what the cache stands for needs no rounding as an operand of a product.
+struct CacheView {
+  uint8_t* codes;   // [pages][page][ceil(d_c / 2)], the even column in the low half of a byte
+  uint8_t* scales;  // [pages][page][ceil(d_c / 16)]
+  void* keys;       // [pages][page][d_rope]
+  long long pages;
+  int page, d_c, d_rope;
+  bool is_bf16;  // the keys' type
+  __host__ __device__ int code_bytes() const { return (d_c + 1) / 2; }
+  __host__ __device__ int blocks() const { return (d_c + kCacheBlock - 1) / kCacheBlock; }
+};
+
+// Which pages a sequence's positions lie in: page k of sequence b is table[b][k].
+struct PageTable {
+  const int* table;  // [B][most]
+  int B, most;
+};
+
+struct CacheRows {  // rows of a padded batch, at positions starts[b] + i for i < counts[b]
+  PageTable pages;
+  int rows;           // per sequence
+  const int* starts;  // [B]
+  const int* counts;  // [B], or null: all
+};
+
+struct CacheAppend {
+  CacheView cache;
+  CacheRows at;
+  const void *c_kv, *k_rope;  // [B][rows][d_c], [B][rows][d_rope]
+  const void* w_k;            // null: no norm
+  float eps;
+  bool turn;         // rotate the keys
+  bool own_pos;      // by rope.pos, else by the position itself
+  RopeArgs rope;     // tokens, d_rope, layout, positions
+  int* status;
+};
+LaunchResult cache4_append(const CacheAppend& a, const RopeTable& t, cudaStream_t st);
+
+struct CacheRead {
+  CacheView cache;
+  CacheRows at;
+  void *c_kv, *k_rope;
+  int* status;
+};
+LaunchResult cache4_read(const CacheRead& a, cudaStream_t st);
+
+// ---- attention over the cache
+//
+// The rows of a sequence are its Sq queries times n_h heads, row i n_h + h; an item is a tile of `tile`
+// of them. The keys an item's rows see lie in one interval; its key tiles of `keys` and those of all
+// items, one after the other, are shared out evenly among `parts` groups of CTAs. An item that one
+// part holds whole is written at once; of a split one each part leaves its piece in a slot (2 part if
+// it began earlier, 2 part + 1 otherwise), and a second kernel joins the pieces.
+struct CacheAttn {
+  CacheView cache;
+  PageTable pages;
+  const int* lengths;  // [B] cached tokens
+  const int *key_lo, *key_hi;  // [B][Sq] or null
+  int Sq, n_h, rows;   // rows = Sq * n_h
+  int tile, row_tiles, keys, parts, least;  // least: key tiles worth a part of their own
+  bool causal;
+  float scale;
+  ScoreMods mods;
+  int* first;    // [items + 1] first key tile of each item in the order of all
+  int2* hull;    // [items] keys seen by some row; {-1, -1}: a length past the table
+  float* part_o;     // [2 parts][tile][d_c]
+  float2* part_ml;   // [2 parts][tile] {running maximum, sum}
+  float* lse;        // [B][n_h][Sq]
+  int* status;
+  __host__ __device__ int items() const { return pages.B * row_tiles; }
+};
+
+LaunchResult cache4_plan(const CacheAttn& a, cudaStream_t st);
+// Joins split items, fills the rows of empty ones. ctx [B * rows][d_c], bf16 or fp32. log2_units: the
+// maxima are in units of log2, else natural.
+LaunchResult cache4_join(const CacheAttn& a, void* ctx, bool ctx_bf16, bool log2_units, cudaStream_t st);
+
+// CUDA cores, any widths: q_lat and ctx in fp32.
+constexpr int kSimtRows = 8, kSimtKeys = 32;
+LaunchResult cache4_simt_qlat(const CacheAttn& a, bool is_bf16, int d_nope, const void* q, const void* W_UK, float* q_lat,
+                              cudaStream_t st);
+LaunchResult cache4_simt_attn(const CacheAttn& a, bool is_bf16, int d_nope, const void* q, const float* q_lat, float* ctx,
+                              cudaStream_t st);
+LaunchResult cache4_simt_out(const CacheAttn& a, bool is_bf16, int d_v, const float* ctx, const void* W_UV, void* out,
+                             cudaStream_t st);
+
+#ifdef __CUDACC__
+// The pool's row of position p of sequence b, or -1 where the table has none.
+__device__ __forceinline__ long long cache_slot(const CacheView& c, const PageTable& t, int b, long long p) {
+  if (p < 0) return -1;
+  const long long k = p / c.page;
+  if (k >= t.most) return -1;
+  const int id = __ldg(t.table + static_cast<long long>(b) * t.most + k);
+  if (id < 0 || id >= c.pages) return -1;
+  return static_cast<long long>(id) * c.page + (p - k * c.page);
+}
+
+constexpr int kStatusBadPage = 1;  // LAGA_ERR_INVALID_ARG in the device's status word
+__device__ __forceinline__ void report_page(int* status, int where) {
+  if (status) atomicCAS(status, 0, kStatusBadPage | (where << 8));
+}
+
+// The keys [lo, hi) that query i of sequence b sees.
+__device__ __forceinline__ int2 cache_row_bounds(const CacheAttn& a, int b, int i) {
+  const int len = __ldg(a.lengths + b);
+  const long long at = static_cast<long long>(b) * a.Sq + i;
+  int lo = a.key_lo ? max(0, __ldg(a.key_lo + at)) : 0;
+  int hi = a.key_hi ? min(len, __ldg(a.key_hi + at)) : len;
+  if (a.causal) hi = min(hi, len - a.Sq + i + 1);
+  return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+// A part's share of all key tiles.
+struct CacheShare {
+  int quota, begin, end;
+};
+__device__ __forceinline__ CacheShare cache_share(const CacheAttn& a, int part) {
+  const int total = __ldcg(a.first + a.items());
+  const int quota = max(a.least, (total + a.parts - 1) / a.parts);
+  const long long begin = static_cast<long long>(part) * quota;
+  return CacheShare{quota, static_cast<int>(min(begin, static_cast<long long>(total))),
+                    static_cast<int>(min(begin + quota, static_cast<long long>(total)))};
+}
+// The last item that begins at or before key tile t.
+__device__ __forceinline__ int cache_item_of(const CacheAttn& a, int t) {
+  int lo = 0, hi = a.items();  // first[lo] <= t < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldcg(a.first + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+#endif
+
+}  // namespace laga

@@ -52,20 +52,6 @@ Path masked_plan(const laga_mla_desc* desc, Dims* d, laga_status* st, bool for_b
   return path;
 }
 
-laga_status check_mods(const laga_mla_mods* mods, ScoreMods* out) {
-  *out = ScoreMods{0.f, nullptr};
-  if (!mods) return LAGA_OK;
-  // outside this range cap or 1 / cap, times the other factors of a score, leaves fp32
-  if (mods->softcap != 0.f && !(mods->softcap >= 1e-20f && mods->softcap <= 1e30f))
-    return fail(LAGA_ERR_INVALID_ARG, "softcap must be 0 (none) or between 1e-20 and 1e30%s");
-  auto aligned4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
-  if (!aligned4(mods->key_lo) || !aligned4(mods->key_hi) || !aligned4(mods->slopes))
-    return fail(LAGA_ERR_INVALID_ARG, "key_lo, key_hi and slopes must be 4-byte aligned%s");
-  out->cap = mods->softcap;
-  out->slopes = mods->slopes;
-  return LAGA_OK;
-}
-
 int elem_size(const laga_mla_desc* desc) { return desc->dtype == LAGA_DTYPE_BF16 ? 2 : 4; }
 
 // Heads per dK/dV CTA: as in the plain backward, fewer where that would leave the 152 SMs fewer
@@ -125,6 +111,74 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
 }
 
 }  // namespace
+
+laga_status check_mods(const laga_mla_mods* mods, ScoreMods* out) {
+  *out = ScoreMods{0.f, nullptr};
+  if (!mods) return LAGA_OK;
+  // outside this range cap or 1 / cap, times the other factors of a score, leaves fp32
+  if (mods->softcap != 0.f && !(mods->softcap >= 1e-20f && mods->softcap <= 1e30f))
+    return fail(LAGA_ERR_INVALID_ARG, "softcap must be 0 (none) or between 1e-20 and 1e30%s");
+  auto aligned4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+  if (!aligned4(mods->key_lo) || !aligned4(mods->key_hi) || !aligned4(mods->slopes))
+    return fail(LAGA_ERR_INVALID_ARG, "key_lo, key_hi and slopes must be 4-byte aligned%s");
+  out->cap = mods->softcap;
+  out->slopes = mods->slopes;
+  return LAGA_OK;
+}
+
+laga_status rope_plan(const laga_mla_rope_desc* desc, const void* pos, RopeArgs* args, const RopeTable** table) {
+  if (!desc) return fail(LAGA_ERR_INVALID_ARG, "null descriptor%s");
+  const laga_mla_rope_desc& x = *desc;
+  const int64_t lim = int64_t(1) << 40;
+  if (x.tokens < 1 || x.n_h < 1 || x.d_nope < 0 || x.d_rope < 2 || x.d_rope % 2 != 0 || x.n_axes < 1 ||
+      x.n_axes > LAGA_ROPE_MAX_AXES)
+    return fail(LAGA_ERR_INVALID_ARG, "rope: tokens, n_h >= 1, d_nope >= 0, even d_rope >= 2, 1 <= n_axes <= 4%s");
+  if (x.dtype != LAGA_DTYPE_F32 && x.dtype != LAGA_DTYPE_BF16)
+    return fail(LAGA_ERR_UNSUPPORTED, "dtype must be LAGA_DTYPE_F32 or LAGA_DTYPE_BF16%s");
+  if (x.tokens >= (int64_t(1) << 31) || x.n_h >= 65536 || x.d_nope >= 65536 || x.d_rope > 2 * kRopePairs ||
+      x.tokens * x.n_h * (x.d_nope + x.d_rope) >= lim || x.n_h * (x.d_nope + x.d_rope) >= (int64_t(1) << 26))
+    return fail(LAGA_ERR_UNSUPPORTED, "rope: problem too large (d_rope <= 256)%s");
+  if (!(x.theta >= 1.0) || !std::isfinite(x.theta))
+    return fail(LAGA_ERR_INVALID_ARG, "rope: theta must be finite and >= 1%s");
+  int64_t pairs = 0;
+  for (int a = 0; a < x.n_axes; ++a) {
+    if (x.sections[a] < 0) return fail(LAGA_ERR_INVALID_ARG, "rope: sections must be >= 0%s");
+    pairs += x.sections[a];
+  }
+  if (pairs != x.d_rope / 2) return fail(LAGA_ERR_INVALID_ARG, "rope: the sections must add up to d_rope / 2%s");
+  const uintptr_t pe = x.pos64 ? 8 : 4;
+  if (!pos || (reinterpret_cast<uintptr_t>(pos) & (pe - 1)))
+    return fail(LAGA_ERR_INVALID_ARG, "rope: pos must be non-null and aligned to its type%s");
+  // The table of the last call's frequencies, per thread: a program's calls share theta and the
+  // sections, and its powers are half of a small call's host time.
+  static thread_local RopeTable t;
+  static thread_local laga_mla_rope_desc made;  // n_axes 0: none
+  if (made.n_axes != x.n_axes || made.d_rope != x.d_rope || made.theta != x.theta ||
+      !std::equal(x.sections, x.sections + x.n_axes, made.sections)) {
+    const Pair step = root_step(x.theta, static_cast<int>(x.d_rope / 2));
+    Pair f{1.0, 0.0};
+    int i = 0;
+    for (int a = 0; a < x.n_axes; ++a)
+      for (int k = 0; k < x.sections[a]; ++k, ++i, f = f * step) {
+        t.turns[i] = turns_of(f);
+        t.axis[i] = static_cast<uint8_t>(a);
+      }
+    made = x;
+  }
+  RopeArgs& g = *args;
+  g.tokens = x.tokens;
+  g.n_h = static_cast<int>(x.n_h);
+  g.d_nope = static_cast<int>(x.d_nope);
+  g.d_rope = static_cast<int>(x.d_rope);
+  g.interleaved = x.interleaved != 0;
+  g.inverse = x.inverse != 0;
+  g.pos64 = x.pos64 != 0;
+  g.is_bf16 = x.dtype == LAGA_DTYPE_BF16;
+  g.pos = pos;
+  *table = &t;
+  return LAGA_OK;
+}
+
 }  // namespace laga
 
 using namespace laga;
@@ -313,65 +367,22 @@ laga_status laga_mla_key_bounds(int64_t batch, int64_t sq, int64_t skv, int64_t 
 
 laga_status laga_mla_rope(const laga_mla_rope_desc* desc, const void* pos, const void* q, const void* k_rope, void* q_out,
                           void* k_out, laga_stream_t stream) {
-  if (!desc) return fail(LAGA_ERR_INVALID_ARG, "null descriptor%s");
-  const laga_mla_rope_desc& x = *desc;
-  const int64_t lim = int64_t(1) << 40;
-  if (x.tokens < 1 || x.n_h < 1 || x.d_nope < 0 || x.d_rope < 2 || x.d_rope % 2 != 0 || x.n_axes < 1 ||
-      x.n_axes > LAGA_ROPE_MAX_AXES)
-    return fail(LAGA_ERR_INVALID_ARG, "rope: tokens, n_h >= 1, d_nope >= 0, even d_rope >= 2, 1 <= n_axes <= 4%s");
-  if (x.dtype != LAGA_DTYPE_F32 && x.dtype != LAGA_DTYPE_BF16)
-    return fail(LAGA_ERR_UNSUPPORTED, "dtype must be LAGA_DTYPE_F32 or LAGA_DTYPE_BF16%s");
-  if (x.tokens >= (int64_t(1) << 31) || x.n_h >= 65536 || x.d_nope >= 65536 || x.d_rope > 2 * kRopePairs ||
-      x.tokens * x.n_h * (x.d_nope + x.d_rope) >= lim || x.n_h * (x.d_nope + x.d_rope) >= (int64_t(1) << 26))
-    return fail(LAGA_ERR_UNSUPPORTED, "rope: problem too large (d_rope <= 256)%s");
-  if (!(x.theta >= 1.0) || !std::isfinite(x.theta))
-    return fail(LAGA_ERR_INVALID_ARG, "rope: theta must be finite and >= 1%s");
-  int64_t pairs = 0;
-  for (int a = 0; a < x.n_axes; ++a) {
-    if (x.sections[a] < 0) return fail(LAGA_ERR_INVALID_ARG, "rope: sections must be >= 0%s");
-    pairs += x.sections[a];
-  }
-  if (pairs != x.d_rope / 2) return fail(LAGA_ERR_INVALID_ARG, "rope: the sections must add up to d_rope / 2%s");
-  const uintptr_t e = x.dtype == LAGA_DTYPE_BF16 ? 2 : 4, pe = x.pos64 ? 8 : 4;
-  if (!pos || (reinterpret_cast<uintptr_t>(pos) & (pe - 1)))
-    return fail(LAGA_ERR_INVALID_ARG, "rope: pos must be non-null and aligned to its type%s");
+  RopeArgs g{};
+  const RopeTable* t = nullptr;
+  const laga_status st = rope_plan(desc, pos, &g, &t);
+  if (st != LAGA_OK) return st;
   if ((!q && !k_rope) || !q != !q_out || !k_rope != !k_out)
     return fail(LAGA_ERR_INVALID_ARG, "rope: q or k_rope, each with its output%s");
+  const uintptr_t e = g.is_bf16 ? 2 : 4;
   for (const void* p : {q, k_rope, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
     if (reinterpret_cast<uintptr_t>(p) & (e - 1))
       return fail(LAGA_ERR_INVALID_ARG, "rope: tensors must be aligned to their type%s");
-  // The table of the last call's frequencies, per thread: a program's calls share theta and the
-  // sections, and its powers are half of a small call's host time.
-  static thread_local RopeTable t;
-  static thread_local laga_mla_rope_desc made;  // n_axes 0: none
-  if (made.n_axes != x.n_axes || made.d_rope != x.d_rope || made.theta != x.theta ||
-      !std::equal(x.sections, x.sections + x.n_axes, made.sections)) {
-    const Pair step = root_step(x.theta, static_cast<int>(x.d_rope / 2));
-    Pair f{1.0, 0.0};
-    int i = 0;
-    for (int a = 0; a < x.n_axes; ++a)
-      for (int k = 0; k < x.sections[a]; ++k, ++i, f = f * step) {
-        t.turns[i] = turns_of(f);
-        t.axis[i] = static_cast<uint8_t>(a);
-      }
-    made = x;
-  }
-  RopeArgs g{};
-  g.tokens = x.tokens;
-  g.n_h = static_cast<int>(x.n_h);
-  g.d_nope = static_cast<int>(x.d_nope);
-  g.d_rope = static_cast<int>(x.d_rope);
-  g.interleaved = x.interleaved != 0;
-  g.inverse = x.inverse != 0;
-  g.pos64 = x.pos64 != 0;
-  g.is_bf16 = x.dtype == LAGA_DTYPE_BF16;
-  g.pos = pos;
   g.q = q;
   g.k = k_rope;
   g.q_out = q_out;
   g.k_out = k_out;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return from_launch(timed("rope", s, [&] { return rope(g, t, s); }));
+  return from_launch(timed("rope", s, [&] { return rope(g, *t, s); }));
 }
 
 static laga_status check_pack(int32_t dtype, int64_t rows, int64_t cols, const void* x, const void* codes,

@@ -11,7 +11,7 @@
 // place). One CTA takes a few tokens: it computes their cosines and sines once, in shared
 // memory, and all heads of the token use them. 2048 tokens of 128 bf16 heads of 192 (202 MB):
 // 34.5 us, 5.85 TB/s, 86% of a plain copy's rate.
-#include "rope.h"
+#include "rope_device.cuh"
 
 #include <algorithm>
 #include <type_traits>
@@ -19,26 +19,7 @@
 namespace laga {
 namespace {
 
-using ll = long long;
 constexpr int THREADS = 256;
-
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(bf16 v) { return __bfloat162float(v); }
-
-// cos and sin of the CTA's tokens x pairs into shared memory.
-__device__ __forceinline__ void fill_angles(const RopeArgs& a, const RopeTable& t, ll first, int tokens, float2* cs) {
-  const int n = a.d_rope / 2;
-  for (int e = threadIdx.x; e < tokens * n; e += THREADS) {
-    const int k = e / n, i = e - k * n;
-    const ll at = t.axis[i] * a.tokens + first + k;
-    const ll p = a.pos64 ? static_cast<const ll*>(a.pos)[at] : static_cast<ll>(static_cast<const int*>(a.pos)[at]);
-    const uint64_t turn = static_cast<uint64_t>(p) * t.turns[i];
-    const float half_turns = static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f;  // [-1, 1]
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    cs[e] = make_float2(c, a.inverse ? -s : s);
-  }
-}
 
 // One value at a time: any widths and alignment. q is [token][head][d_nope + d_rope].
 template <typename T>
@@ -48,7 +29,7 @@ __global__ void __launch_bounds__(THREADS) rope_any_kernel(const RopeArgs a, con
   const ll first = static_cast<ll>(blockIdx.x) * per_cta;
   const int tokens = static_cast<int>(min(static_cast<ll>(per_cta), a.tokens - first));
   const int n = a.d_rope / 2, heads = a.q ? a.n_h : 0, rows = heads + (a.k ? 1 : 0);
-  fill_angles(a, t, first, tokens, cs);
+  fill_angles<THREADS>(a, t, first, tokens, cs);
   __syncthreads();
   // a unit is one pair, or one value of the no-RoPE part when it has to be copied
   const int copy = a.q_out != a.q ? a.d_nope : 0;
@@ -73,43 +54,6 @@ __global__ void __launch_bounds__(THREADS) rope_any_kernel(const RopeArgs a, con
     dst[i1] = static_cast<T>(x * c.y + y * c.x);
   }
 }
-
-template <typename T>
-struct Vec;
-template <>
-struct Vec<bf16> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void get(uint4 v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[2 * k] = __uint_as_float(w[k] << 16);
-      x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ uint4 put(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Vec<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ void get(uint4 v, float (&x)[4]) {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z);
-    x[3] = __uint_as_float(v.w);
-  }
-  static __device__ __forceinline__ uint4 put(const float (&x)[4]) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-  }
-};
 
 // Exact division of 0 <= e < 2^26 by a fixed 1 <= d < 2^17.
 struct Div {
@@ -142,7 +86,7 @@ __global__ void __launch_bounds__(THREADS) rope_vec_kernel(const RopeArgs a, con
   const ll first = static_cast<ll>(blockIdx.x) * per_cta;
   const int tokens = static_cast<int>(min(static_cast<ll>(per_cta), a.tokens - first));
   const int n = a.d_rope / 2, heads = a.q ? a.n_h : 0;
-  fill_angles(a, t, first, tokens, cs);
+  fill_angles<THREADS>(a, t, first, tokens, cs);
   __syncthreads();
   const int rope_units = INTERLEAVED ? a.d_rope / N : n / N;
   const int copy = a.q_out != a.q ? a.d_nope / N : 0;
@@ -217,13 +161,11 @@ __global__ void __launch_bounds__(THREADS) rope_vec_kernel(const RopeArgs a, con
   }
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 template <typename T>
 cudaError_t launch(const RopeArgs& a, const RopeTable& t, cudaStream_t st) {
   constexpr int N = Vec<T>::N;
   const bool vec = a.d_nope % N == 0 && a.d_rope % N == 0 && (a.interleaved || (a.d_rope / 2) % N == 0) &&
-                   aligned16(a.q) && aligned16(a.q_out) && aligned16(a.k) && aligned16(a.k_out);
+                   aligned_to_16(a.q) && aligned_to_16(a.q_out) && aligned_to_16(a.k) && aligned_to_16(a.k_out);
   const int n = a.d_rope / 2;
   const ll work = static_cast<ll>((a.q ? a.n_h : 0)) * (a.d_nope + a.d_rope) + (a.k ? a.d_rope : 0);  // values a token
   // a few tokens per CTA when a token is little work, but no fewer CTAs than two per SM

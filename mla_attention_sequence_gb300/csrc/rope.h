@@ -1,10 +1,11 @@
-// Interface of the rotary positions' kernel.
+// Interface of the rotary positions' kernels, alone and with the norms before them.
 #pragma once
 #include "internal.h"
 
 namespace laga {
 
 constexpr int kRopePairs = 128;  // most rotated pairs (d_rope <= 256)
+constexpr int kNormWidth = 1024;  // widest normed head
 
 struct RopeTable {
   uint64_t turns[kRopePairs];  // pair i: turns per position step, as a fraction of 2^64
@@ -21,5 +22,19 @@ struct RopeArgs {
 };
 
 LaunchResult rope(const RopeArgs& a, const RopeTable& table, cudaStream_t st);
+
+// Norms and rotation: a.q, a.k the rows before the norm; a.q_out, a.k_out the results.
+struct NormArgs {
+  RopeArgs rope;
+  float eps;
+  const void *w_q, *w_k;  // [d_nope + d_rope], [d_rope]
+  // backward: the gradients of the results; rope.q_out, rope.k_out are then those of the rows
+  const void *z_q, *z_k;
+  void *dw_q, *dw_k;
+  float* partials;  // norm_rope_bwd_partials(..) values of scratch
+};
+LaunchResult norm_rope(const NormArgs& a, const RopeTable& table, cudaStream_t st);
+LaunchResult norm_rope_bwd(const NormArgs& a, const RopeTable& table, cudaStream_t st);
+size_t norm_rope_bwd_partials(const RopeArgs& a);
 
 }  // namespace laga

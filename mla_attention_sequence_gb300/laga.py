@@ -32,7 +32,9 @@ EXPORTS = ("laga_mla_fwd_workspace_size", "laga_mla_bwd_workspace_size", "laga_m
            "laga_mla_version", "laga_mla_selftest_timeout", "laga_mla_absorbed_fwd",
            "laga_mla_absorbed_fwd_workspace_size", "laga_mla_reconstruct_rows", "laga_mla_masked_fwd",
            "laga_mla_masked_bwd", "laga_mla_masked_fwd_workspace_size", "laga_mla_masked_bwd_workspace_size",
-           "laga_mla_key_bounds", "laga_mla_rope", "laga_mla_pack8", "laga_mla_unpack8")
+           "laga_mla_key_bounds", "laga_mla_rope", "laga_mla_pack8", "laga_mla_unpack8", "laga_mla_norm_rope",
+           "laga_mla_norm_rope_bwd", "laga_mla_norm_rope_bwd_workspace_size", "laga_mla_cache4_append",
+           "laga_mla_cache4_read", "laga_mla_cache4_fwd", "laga_mla_cache4_fwd_workspace_size")
 
 
 class LagaDesc(ctypes.Structure):
@@ -65,6 +67,20 @@ class LagaRopeDesc(ctypes.Structure):
                 ("d_rope", ctypes.c_int64), ("n_axes", ctypes.c_int64), ("sections", ctypes.c_int64 * ROPE_MAX_AXES),
                 ("theta", ctypes.c_double), ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32),
                 ("pos64", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class LagaCache4(ctypes.Structure):
+    """Mirror of laga_mla_cache4."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("k_rope", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("d_c", ctypes.c_int64),
+                ("d_rope", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class LagaCache4Desc(ctypes.Structure):
+    """Mirror of laga_mla_cache4_desc."""
+    _fields_ = [("batch", ctypes.c_int64), ("sq", ctypes.c_int64), ("n_h", ctypes.c_int64), ("d_nope", ctypes.c_int64),
+                ("d_v", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("causal", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float), ("variant", ctypes.c_int32)]
 
 
 class LagaError(RuntimeError):
@@ -116,6 +132,20 @@ def lib() -> ctypes.CDLL:
     for f in (L.laga_mla_masked_fwd, L.laga_mla_masked_bwd, L.laga_mla_key_bounds, L.laga_mla_rope, L.laga_mla_pack8,
               L.laga_mla_unpack8):
         f.restype = st
+    f32, pr, pc, pcd = ctypes.c_float, ctypes.POINTER(LagaRopeDesc), ctypes.POINTER(LagaCache4), \
+        ctypes.POINTER(LagaCache4Desc)
+    L.laga_mla_norm_rope.argtypes = [pr, f32] + [vp] * 8
+    L.laga_mla_norm_rope_bwd.argtypes = [pr, f32] + [vp] * 12 + [sz, vp]
+    L.laga_mla_norm_rope_bwd_workspace_size.argtypes = [pr]
+    L.laga_mla_cache4_append.argtypes = [pc, i64, i64, i64] + [vp] * 6 + [f32, pr, vp, vp]
+    L.laga_mla_cache4_read.argtypes = [pc, i64, i64, i64] + [vp] * 6
+    L.laga_mla_cache4_fwd.argtypes = [pcd, pc, pm] + [vp] * 8 + [sz, vp]
+    L.laga_mla_cache4_fwd_workspace_size.argtypes = [pcd, pc]
+    for f in (L.laga_mla_norm_rope, L.laga_mla_norm_rope_bwd, L.laga_mla_cache4_append, L.laga_mla_cache4_read,
+              L.laga_mla_cache4_fwd):
+        f.restype = st
+    for f in (L.laga_mla_norm_rope_bwd_workspace_size, L.laga_mla_cache4_fwd_workspace_size):
+        f.restype = sz
     L.laga_mla_check.argtypes = [vp]
     L.laga_mla_check.restype = st
     L.laga_mla_selftest_timeout.argtypes = [vp]
@@ -652,8 +682,308 @@ def masked_bwd(q, c_kv, k_rope, W_UK, W_UV, out, lse, dout, key_lo=None, key_hi=
     return {"dq": dq, "dc_kv": dc_kv, "dk_rope": dk_rope, "dW_UK": dW_UK, "dW_UV": dW_UV}
 
 
+# ---------------------------------------------------------------- norms with rotation, the 4-bit cache
+
+
+def _norm_call(q, k_rope, pos, q_weight, k_weight, sections, theta, interleaved):
+    """(descriptor, shapes of q and k_rope or None, addresses of pos, q, k_rope, q_weight, k_weight, type, device)."""
+    like = q if q is not None else k_rope
+    if like is None:
+        raise ValueError("give q, k_rope or both")
+    dt, dev = like.dtype, like.device
+    code = _code_of(dt)
+    dts = (dt,)
+    if pos.dim() != 3 or (q is not None and q.dim() != 4) or (k_rope is not None and k_rope.dim() != 3):
+        raise ValueError("expected q [B,S,n_h,d_nope+d_rope], k_rope [B,S,d_rope], pos [n_axes,B,S]")
+    B, S = like.shape[:2]
+    if k_rope is not None:
+        d_rope = k_rope.shape[2]
+    elif sections is None:
+        raise ValueError("without k_rope the sections say how much of a head turns")
+    else:
+        d_rope = 2 * sum(map(int, sections))
+    sections = (d_rope // 2,) if sections is None else tuple(map(int, sections))
+    axes = pos.shape[0]
+    if len(sections) != axes or axes > ROPE_MAX_AXES:
+        raise ValueError(f"one section per axis of pos, at most {ROPE_MAX_AXES}")
+    q_at = k_at = wq_at = wk_at = None
+    if q is not None:
+        q_at = _expect("q", q, None, dts, dev)
+        wq_at = _expect("q_weight", q_weight, (q.shape[3],), dts, dev)
+    elif q_weight is not None:
+        raise ValueError("q_weight without q")
+    if k_rope is not None:
+        k_at = _expect("k_rope", k_rope, (B, S, d_rope), dts, dev)
+        wk_at = _expect("k_weight", k_weight, (d_rope,), dts, dev)
+    elif k_weight is not None:
+        raise ValueError("k_weight without k_rope")
+    at = _expect("pos", pos, (axes, B, S), (torch.int32, torch.int64), dev)
+    d = _rope_desc(tuple(q.shape) if q is not None else (B, S, 1, d_rope), d_rope, sections, float(theta),
+                   bool(interleaved), False, pos.dtype == torch.int64, code) if B * S else None
+    return d, (at, q_at, k_at, wq_at, wk_at), dts, dev
+
+
+def _made(name, t, like, dts, dev):
+    """(the output, its address): `t`, or a new tensor of like's shape; (None, None) where like is None."""
+    if like is None:
+        if t is not None:
+            raise ValueError(f"{name} without its input")
+        return None, None
+    if t is None:
+        t = torch.empty(like.shape, dtype=dts[0], device=dev)
+        return t, t.data_ptr()
+    return t, _expect(name, t, like.shape, dts, dev)
+
+
+def norm_rope(q, k_rope, pos, q_weight, k_weight=None, eps: float = 1e-6, sections=None, theta: float = 10000.0,
+              interleaved: bool = True, q_out=None, k_out=None):
+    """laga_mla_norm_rope: RMS norms of the query heads (over d_nope + d_rope, times q_weight) and of the
+    shared RoPE key (times k_weight), and the rotation of rope in the same pass; returns (q, k_rope).
+    Either may be None, with its weight (without k_rope, sections say how much of a head turns). q_out /
+    k_out may be q / k_rope themselves."""
+    d, (at, q_at, k_at, wq, wk), dts, dev = _norm_call(q, k_rope, pos, q_weight, k_weight, sections, theta, interleaved)
+    q_out, qo = _made("q_out", q_out, q, dts, dev)
+    k_out, ko = _made("k_out", k_out, k_rope, dts, dev)
+    if d is not None:
+        _launch(dev, lib().laga_mla_norm_rope, d, eps, at, q_at, k_at, wq, wk, qo, ko)
+    return q_out, k_out
+
+
+def norm_rope_bwd(dq_out, dk_out, q, k_rope, pos, q_weight, k_weight=None, eps: float = 1e-6, sections=None,
+                  theta: float = 10000.0, interleaved: bool = True, workspace: torch.Tensor | None = None,
+                  grads: dict | None = None):
+    """laga_mla_norm_rope_bwd: dict dq, dk_rope, dw_q, dw_k from the gradients of norm_rope's results and
+    its arguments (q and k_rope before the norm); what belongs to a None is left out. grads: tensors to
+    write to by those names (dq may be dq_out or q, dk_rope may be dk_out or k_rope)."""
+    d, (at, q_at, k_at, wq, wk), dts, dev = _norm_call(q, k_rope, pos, q_weight, k_weight, sections, theta, interleaved)
+    zq = zk = None
+    if q is not None:
+        zq = _expect("dq_out", dq_out, q.shape, dts, dev)
+    elif dq_out is not None:
+        raise ValueError("dq_out without q")
+    if k_rope is not None:
+        zk = _expect("dk_out", dk_out, k_rope.shape, dts, dev)
+    elif dk_out is not None:
+        raise ValueError("dk_out without k_rope")
+    given = (grads or {}).get
+    res, to = {}, []
+    for name, like in (("dq", q), ("dk_rope", k_rope), ("dw_q", q_weight), ("dw_k", k_weight)):
+        t, address = _made(name, given(name), like, dts, dev)
+        to.append(address)
+        if t is not None:
+            res[name] = t
+    if d is None:  # no rows: nothing to sum
+        for name in ("dw_q", "dw_k"):
+            if name in res:
+                res[name].zero_()
+        return res
+    nbytes = _norm_bwd_bytes(bytes(d))
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = workspace.data_ptr()
+    else:
+        ws = _expect("workspace", workspace, None, (workspace.dtype,), dev)
+        if workspace.numel() * workspace.element_size() < nbytes:
+            raise ValueError("workspace too small")
+    _launch(dev, lib().laga_mla_norm_rope_bwd, d, eps, at, zq, zk, q_at, k_at, wq, wk, *to, ws, nbytes)
+    return res
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_bwd_bytes(desc: bytes) -> int:
+    return int(lib().laga_mla_norm_rope_bwd_workspace_size(LagaRopeDesc.from_buffer_copy(desc)))
+
+
+CACHE4_BLOCK = 16
+
+
+@dataclass
+class Cache4:
+    """A paged pool of cached tokens: latents in 4 bits (codes uint8 [pages, page_size, ceil(d_c / 2)], scales
+    uint8 [pages, page_size, ceil(d_c / 16)]; the format stands in laga_mla.h) and rotated RoPE keys
+    [pages, page_size, d_rope], in the type of the calls' tensors."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    k_rope: torch.Tensor
+    d_c: int
+
+    @property
+    def page_size(self):
+        return self.codes.shape[1]
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def cache4(pages: int, page_size: int, d_c: int, d_rope: int, dtype=torch.bfloat16, device="cuda") -> Cache4:
+    """An empty pool of `pages` pages."""
+    _code_of(dtype)
+    return Cache4(torch.zeros(pages, page_size, (d_c + 1) // 2, dtype=torch.uint8, device=device),
+                  torch.zeros(pages, page_size, -(-d_c // CACHE4_BLOCK), dtype=torch.uint8, device=device),
+                  torch.zeros(pages, page_size, d_rope, dtype=dtype, device=device), d_c)
+
+
+def _check_cache(c: Cache4):
+    """(descriptor, the tensors' allowed types, device)."""
+    if c.codes.dim() != 3 or c.k_rope.dim() != 3:
+        raise ValueError("a cache's tensors are [pages, page_size, ...]")
+    pages, page = c.codes.shape[:2]
+    dev, dt = c.codes.device, c.k_rope.dtype
+    code = _code_of(dt)
+    d_rope = c.k_rope.shape[2]
+    codes = _expect("cache.codes", c.codes, (pages, page, (c.d_c + 1) // 2), _UINT8, dev)
+    scales = _expect("cache.scales", c.scales, (pages, page, -(-c.d_c // CACHE4_BLOCK)), _UINT8, dev)
+    keys = _expect("cache.k_rope", c.k_rope, (pages, page, d_rope), (dt,), dev)
+    return LagaCache4(codes, scales, keys if d_rope else None, pages, page, c.d_c, d_rope, code), (dt,), dev
+
+
+def _table(table, dev):
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be [B, max_pages]")
+    return _expect("table", table, None, _INT32, dev)
+
+
+def cache4_append(cache: Cache4, c_kv, k_rope, table, starts, counts=None, k_weight=None, eps: float = 1e-6, pos=None,
+                  sections=None, theta: float | None = 10000.0, interleaved: bool = True) -> None:
+    """laga_mla_cache4_append: writes rows i < counts[b] (None: all) of c_kv [B, S, d_c] and k_rope [B, S, d_rope]
+    to positions starts[b] + i of sequence b, whose pages are table[b] (int32 [B, max_pages]; starts, counts int32
+    [B]). The latents are stored in 4 bits; the keys are normed with k_weight (None: not) and rotated as by rope,
+    by pos [n_axes, B, S] or by their positions in the sequence (theta None: stored as they come)."""
+    d, dts, dev = _check_cache(cache)
+    d_rope = d.d_rope
+    if c_kv.dim() != 3:
+        raise ValueError("expected c_kv [B,S,d_c]")
+    B, S = c_kv.shape[:2]
+    c_at = _expect("c_kv", c_kv, (B, S, cache.d_c), dts, dev)
+    k_at = _expect("k_rope", k_rope, (B, S, d_rope), dts, dev)
+    t_at = _table(table, dev)
+    if table.shape[0] != B:
+        raise ValueError("table has a row for each sequence")
+    s_at = _expect("starts", starts, (B,), _INT32, dev)
+    n_at = None if counts is None else _expect("counts", counts, (B,), _INT32, dev)
+    w_at = None if k_weight is None else _expect("k_weight", k_weight, (d_rope,), dts, dev)
+    rope_desc = p_at = None
+    if theta is not None and d_rope and B * S:
+        axes = 1 if pos is None else pos.shape[0]
+        sections = (d_rope // 2,) if sections is None else tuple(map(int, sections))
+        if len(sections) != axes or axes > ROPE_MAX_AXES:
+            raise ValueError(f"one section per axis of pos (one without pos), at most {ROPE_MAX_AXES}")
+        if pos is not None:
+            p_at = _expect("pos", pos, (axes, B, S), (torch.int32, torch.int64), dev)
+        rope_desc = _rope_desc((B, S, 1, d_rope), d_rope, sections, float(theta), bool(interleaved), False,
+                               pos is not None and pos.dtype == torch.int64, d.dtype)
+    elif pos is not None:
+        raise ValueError("pos without a rotation")
+    if B * S:
+        _launch(dev, lib().laga_mla_cache4_append, d, B, S, table.shape[1], t_at, s_at, n_at, c_at,
+                k_at if d_rope else None, w_at, eps, rope_desc, p_at)
+
+
+def cache4_read(cache: Cache4, table, starts, rows: int, counts=None, c_kv=None, k_rope=None):
+    """laga_mla_cache4_read: (c_kv [B, rows, d_c], k_rope [B, rows, d_rope]), the values that positions
+    starts[b] + i, i < counts[b] (None: rows), of the cache stand for; zeros past counts[b]. c_kv / k_rope: tensors
+    to write to."""
+    d, dts, dev = _check_cache(cache)
+    t_at = _table(table, dev)
+    B, rows = table.shape[0], int(rows)
+    s_at = _expect("starts", starts, (B,), _INT32, dev)
+    n_at = None if counts is None else _expect("counts", counts, (B,), _INT32, dev)
+    if c_kv is None:
+        c_kv = torch.empty((B, rows, cache.d_c), dtype=dts[0], device=dev)
+    if k_rope is None:
+        k_rope = torch.empty((B, rows, d.d_rope), dtype=dts[0], device=dev)
+    c_at = _expect("c_kv", c_kv, (B, rows, cache.d_c), dts, dev)
+    k_at = _expect("k_rope", k_rope, (B, rows, d.d_rope), dts, dev)
+    if B * rows:
+        _launch(dev, lib().laga_mla_cache4_read, d, B, rows, table.shape[1], t_at, s_at, n_at, c_at,
+                k_at if d.d_rope else None)
+    return c_kv, k_rope
+
+
+@functools.lru_cache(maxsize=256)
+def _cache4_plan(q_shape, wk_shape, wv_shape, pages, page_size, d_c, d_rope, code, max_pages, causal, softmax_scale,
+                 variant):
+    """What a cached call's sizes decide: the descriptor, d_nope, d_v and the workspace's bytes."""
+    if len(q_shape) != 4 or len(wk_shape) != 2 or len(wv_shape) != 2:
+        raise ValueError("expected q [B,Sq,n_h,d_nope+d_rope], W_UK [d_c,n_h*d_nope], W_UV [d_c,n_h*d_v]")
+    B, Sq, n_h, d_qk = q_shape
+    if wk_shape[0] != d_c or wv_shape[0] != d_c:
+        raise ValueError("W_UK and W_UV have a row for each latent column of the cache")
+    if n_h < 1 or wk_shape[1] % n_h or wv_shape[1] % n_h:
+        raise ValueError("W_UK / W_UV columns must be n_h * head width")
+    d_nope, d_v = wk_shape[1] // n_h, wv_shape[1] // n_h
+    if d_nope + d_rope != d_qk:
+        raise ValueError("q's last dim must be d_nope + the cache's d_rope")
+    d = LagaCache4Desc(B, Sq, n_h, d_nope, d_v, max_pages, causal, softmax_scale or 0.0, VARIANTS[variant])
+    nbytes = 0
+    if B * Sq:
+        nbytes = int(lib().laga_mla_cache4_fwd_workspace_size(d, LagaCache4(None, None, None, pages, page_size, d_c,
+                                                                              d_rope, code)))
+        if nbytes == 0:
+            _raise_if(2)
+    return d, d_v, nbytes
+
+
+def _cache4_call(q, cache, W_UK, W_UV, table, causal, softmax_scale, variant):
+    c, dts, dev = _check_cache(cache)
+    at = (_expect("q", q, None, dts, dev), _expect("W_UK", W_UK, None, dts, dev), _expect("W_UV", W_UV, None, dts, dev))
+    t_at = _table(table, dev)
+    d, d_v, nbytes = _cache4_plan(tuple(q.shape), tuple(W_UK.shape), tuple(W_UV.shape), c.pages, c.page_size, c.d_c,
+                                  c.d_rope, c.dtype, table.shape[1], bool(causal),
+                                  None if softmax_scale is None else float(softmax_scale), variant)
+    if table.shape[0] != q.shape[0]:
+        raise ValueError("table has a row for each sequence")
+    return c, dts, dev, at, t_at, d, d_v, nbytes
+
+
+def cache4_workspace(q, cache: Cache4, W_UK, W_UV, table, causal: bool = True, softmax_scale: float | None = None,
+                     variant: str = "auto") -> torch.Tensor:
+    """A workspace for cache4_fwd of these sizes. Calls in flight at the same time, replayed graphs among them, need
+    one each."""
+    *_, dev, _, _, _, _, nbytes = _cache4_call(q, cache, W_UK, W_UV, table, causal, softmax_scale, variant)
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def cache4_fwd(q, cache: Cache4, W_UK, W_UV, table, lengths, key_lo=None, key_hi=None, softcap: float = 0.0, slopes=None,
+               causal: bool = True, softmax_scale: float | None = None, variant: str = "auto",
+               workspace: torch.Tensor | None = None, out=None, lse=None):
+    """laga_mla_cache4_fwd: (out [B,Sq,n_h,d_v], lse [B,n_h,Sq] fp32) of the last Sq tokens of each sequence over its
+    lengths[b] cached tokens (int32 [B]; the call's own among them), q normed and rotated. Query i is at position
+    lengths[b] - Sq + i; causal, key_lo / key_hi (int32 [B, Sq]), softcap and slopes as for masked_fwd. The table
+    (int32 [B, max_pages]) names each sequence's pages."""
+    c, dts, dev, at, t_at, d, d_v, nbytes = _cache4_call(q, cache, W_UK, W_UV, table, causal, softmax_scale, variant)
+    B, Sq, n_h, _ = q.shape
+    n_at = _expect("lengths", lengths, (B,), _INT32, dev)
+    m = LagaMods(None if key_lo is None else _expect("key_lo", key_lo, (B, Sq), _INT32, dev),
+                 None if key_hi is None else _expect("key_hi", key_hi, (B, Sq), _INT32, dev),
+                 None if slopes is None else _expect("slopes", slopes, (n_h,), _FP32, dev), softcap or 0.0)
+    if out is None:
+        out = torch.empty((B, Sq, n_h, d_v), dtype=dts[0], device=dev)
+        o_at = out.data_ptr()
+    else:
+        o_at = _expect("out", out, (B, Sq, n_h, d_v), dts, dev)
+    if lse is None:
+        lse = torch.empty((B, n_h, Sq), dtype=torch.float32, device=dev)
+        l_at = lse.data_ptr()
+    else:
+        l_at = _expect("lse", lse, (B, n_h, Sq), _FP32, dev)
+    if B * Sq == 0:
+        return out, lse
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = workspace.data_ptr()
+    else:
+        ws = _expect("workspace", workspace, None, (workspace.dtype,), dev)
+        if workspace.numel() * workspace.element_size() < nbytes:
+            raise ValueError("workspace too small")
+    _launch(dev, lib().laga_mla_cache4_fwd, d, c, m, t_at, n_at, at[0], at[1], at[2], o_at, l_at, ws, nbytes)
+    return out, lse
+
+
 def check(device=None) -> None:
-    """laga_mla_check on the current stream: raise on a device-side timeout or CUDA error."""
+    """laga_mla_check on the current stream: raise on a device-side timeout, a cached position without a page, or a
+    CUDA error."""
     dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
     _raise_if(lib().laga_mla_check(_stream(dev)))
 
