@@ -97,6 +97,10 @@ LaunchResult cache4_simt_attn(const CacheAttn& a, bool is_bf16, int d_nope, cons
 LaunchResult cache4_simt_out(const CacheAttn& a, bool is_bf16, int d_v, const float* ctx, const void* W_UV, void* out,
                              cudaStream_t st);
 
+// Tensor cores, bf16 with d_c = 512, d_rope = 64: q_lat and ctx in bf16.
+constexpr int kTcRows = 128, kTcKeys = 64;
+LaunchResult cache4_tc_attn(const CacheAttn& a, const bf16* q, const bf16* q_lat, bf16* ctx, cudaStream_t st);
+
 #ifdef __CUDACC__
 // The pool's row of position p of sequence b, or -1 where the table has none.
 __device__ __forceinline__ long long cache_slot(const CacheView& c, const PageTable& t, int b, long long p) {

@@ -80,6 +80,7 @@ laga_status check_rows(int64_t batch, int64_t rows, int64_t max_pages, const int
 struct AttnSizes {
   CacheAttn a;
   int d_nope, d_v;
+  bool tc;
   size_t items_bytes, hull_bytes, lat_bytes, ml_bytes, o_bytes;
   size_t total() const { return items_bytes + hull_bytes + 2 * lat_bytes + ml_bytes + o_bytes; }
 };
@@ -112,9 +113,11 @@ laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cach
   s->d_v = static_cast<int>(d->d_v);
   a.scale = d->softmax_scale > 0.f ? d->softmax_scale
                                    : 1.f / std::sqrt(static_cast<float>(d->d_nope + cache->d_rope));
-  a.tile = kSimtRows;
-  a.keys = kSimtKeys;
-  a.parts = 2 * sm_count();
+  s->tc = d->variant == LAGA_VARIANT_AUTO && a.cache.is_bf16 && a.cache.d_c == 512 && a.cache.d_rope == 64 &&
+          s->d_nope == 128 && s->d_v == 128;
+  a.tile = s->tc ? kTcRows : kSimtRows;
+  a.keys = s->tc ? kTcKeys : kSimtKeys;
+  a.parts = s->tc ? sm_count() / 2 : 2 * sm_count();  // tensor cores: two CTAs a part, one a SM
   a.least = 1;
   a.row_tiles = (a.rows + a.tile - 1) / a.tile;
   const int64_t items = static_cast<int64_t>(a.pages.B) * a.row_tiles;
@@ -123,7 +126,7 @@ laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cach
     return fail(LAGA_ERR_UNSUPPORTED, "cache attention: problem too large (rows times the table's room)%s");
   s->items_bytes = align_up((items + 1) * sizeof(int), 256);
   s->hull_bytes = align_up(items * sizeof(int2), 256);
-  s->lat_bytes = align_up(static_cast<size_t>(a.pages.B) * a.rows * a.cache.d_c * 4, 256);
+  s->lat_bytes = align_up(static_cast<size_t>(a.pages.B) * a.rows * a.cache.d_c * (s->tc ? 2 : 4), 256);
   s->ml_bytes = align_up(static_cast<size_t>(2) * a.parts * a.tile * sizeof(float2), 256);
   s->o_bytes = align_up(static_cast<size_t>(2) * a.parts * a.tile * a.cache.d_c * 4, 256);
   return LAGA_OK;
@@ -281,6 +284,22 @@ laga_status laga_mla_cache4_fwd(const laga_mla_cache4_desc* desc, const laga_mla
   const bool b16 = a.cache.is_bf16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   LaunchResult r = timed("cache4_plan", s, [&] { return cache4_plan(a, s); });
+  if (z.tc) {
+    auto cb = [](const void* p) { return static_cast<const bf16*>(p); };
+    bf16 *q_lat = reinterpret_cast<bf16*>(lat), *c = reinterpret_cast<bf16*>(ctx);
+    Dims d{};
+    d.B = 1;
+    d.Sq = a.pages.B * a.Sq;
+    d.n_h = a.n_h;
+    d.d_c = 512;
+    d.d_nope = d.d_v = 128;
+    d.d_rope = 64;
+    if (r.ok()) r = timed("cache4_qlat", s, [&] { return tc_absorbed_qlat(d, cb(q), cb(W_UK), q_lat, s); });
+    if (r.ok()) r = timed("cache4_attn", s, [&] { return cache4_tc_attn(a, cb(q), q_lat, c, s); });
+    if (r.ok()) r = timed("cache4_join", s, [&] { return cache4_join(a, c, true, true, s); });
+    if (r.ok()) r = timed("cache4_out", s, [&] { return tc_absorbed_outproj(d, c, cb(W_UV), static_cast<bf16*>(out), s); });
+    return from_launch(r);
+  }
   float* q_lat = reinterpret_cast<float*>(lat);
   float* c = reinterpret_cast<float*>(ctx);
   if (r.ok()) r = timed("cache4_qlat", s, [&] { return cache4_simt_qlat(a, b16, z.d_nope, q, W_UK, q_lat, s); });
