@@ -275,17 +275,22 @@ __global__ void __launch_bounds__(1024) plan_kernel(const CacheAttn a) {
   if (threadIdx.x == 0) a.first[items] = before;
 }
 
-// Rows blockIdx.y, + gridDim.y, .. of item blockIdx.x; 128 threads, 4 columns each at a time.
+// Rows blockIdx.y, + gridDim.y, .. of item blockIdx.x. The pieces' weights first, in shared memory (128
+// pieces at a time), then the columns, four a thread, all of a batch's loads before its sums.
+constexpr int JOIN_THREADS = 128;
 template <typename T>
-__global__ void __launch_bounds__(128) join_kernel(const CacheAttn a, T* ctx, float to_log) {
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const CacheAttn a, T* ctx, float to_log) {
+  __shared__ float weights[JOIN_THREADS];
+  __shared__ float2 red[JOIN_THREADS / 32];
   after_previous();
   const int item = blockIdx.x, b = item / a.row_tiles, r0 = (item - b * a.row_tiles) * a.tile;
-  const int2 hull = __ldcg(a.hull + item);
   const int begin = __ldcg(a.first + item), end = __ldcg(a.first + item + 1);
   const CacheShare share = cache_share(a, 0);
   const int p0 = begin / share.quota, p1 = end > begin ? (end - 1) / share.quota : p0;
   if (end > begin && p0 == p1) return;  // written by the part that had it all
-  const int rows = min(a.tile, a.rows - r0), d_c = a.cache.d_c;
+  const int2 hull = __ldcg(a.hull + item);
+  const int rows = min(a.tile, a.rows - r0), d_c = a.cache.d_c, pieces = p1 - p0 + 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
     const ll row = static_cast<ll>(b) * a.rows + r0 + r;
     const int i = (r0 + r) / a.n_h, h = (r0 + r) - i * a.n_h;
@@ -293,32 +298,69 @@ __global__ void __launch_bounds__(128) join_kernel(const CacheAttn a, T* ctx, fl
     float* lse = a.lse + (static_cast<ll>(b) * a.n_h + h) * a.Sq + i;
     if (end == begin) {  // no keys: zero, or NaN where the table had no room
       const float v = hull.x < 0 ? __int_as_float(0x7fc00000) : 0.f;
-      for (int c = threadIdx.x; c < d_c; c += 128) out[c] = static_cast<T>(v);
+      for (int c = threadIdx.x; c < d_c; c += JOIN_THREADS) out[c] = static_cast<T>(v);
       if (threadIdx.x == 0) *lse = hull.x < 0 ? v : -INFINITY;
       continue;
     }
-    auto slot = [&](int p) { return static_cast<ll>(2 * p + (p == p0 ? 1 : 0)) * a.tile + r; };
+    // piece k is part p0 + k's; the first began the item
+    auto slot = [&](int k) { return static_cast<ll>(2 * (p0 + k) + (k == 0 ? 1 : 0)) * a.tile + r; };
+    // each thread its pieces' maximum and sum, then the CTA's, in a fixed order
     float m = -INFINITY, l = 0.f;
-    for (int p = p0; p <= p1; ++p) m = fmaxf(m, __ldcg(a.part_ml + slot(p)).x);
-    // the weight of a piece: e^(its maximum - m); a piece that saw nothing has none
-    auto weight = [&](float mp) { return mp == -INFINITY ? 0.f : exp2f((mp - m) * to_log); };
-    for (int p = p0; p <= p1; ++p) {
-      const float2 v = __ldcg(a.part_ml + slot(p));
-      l += v.y * weight(v.x) + (v.y != v.y ? v.y : 0.f);  // NaN stays NaN
-    }
+    auto add = [&](float2 v) {
+      const float to = fmaxf(m, v.x);
+      const float from = to == -INFINITY ? 0.f : to;
+      l = l * exp2f((m - from) * to_log) + v.y * exp2f((v.x - from) * to_log);  // 2^-inf = 0; a NaN sum stays one
+      m = to;
+    };
+    for (int k = threadIdx.x; k < pieces; k += JOIN_THREADS) add(__ldcg(a.part_ml + slot(k)));
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) add(make_float2(__shfl_down_sync(0xffffffffu, m, k), __shfl_down_sync(0xffffffffu, l, k)));
+    __syncthreads();  // red and weights of the row before
+    if (lane == 0) red[warp] = make_float2(m, l);
+    __syncthreads();
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < JOIN_THREADS / 32; ++k) add(red[k]);
     l = row_sum(l, cache_row_bounds(a, b, i));
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int c = threadIdx.x; c < d_c; c += 128) {
-      float sum = 0.f;
-#pragma unroll 8
-      for (int p = p0; p <= p1; ++p) {
-        const float w = weight(__ldcg(a.part_ml + slot(p)).x);
-        const float o = __ldcg(a.part_o + slot(p) * d_c + c);
-        sum = fmaf(w, o, sum);
-      }
-      out[c] = static_cast<T>(l != l ? l : sum * inv);
-    }
+    const float inv = l != l ? l : l == 0.f ? 0.f : 1.f / l, from = m == -INFINITY ? 0.f : m;
     if (threadIdx.x == 0) *lse = l == 0.f ? -INFINITY : m * (to_log * 0.6931471805599453f) + logf(l);
+    for (int c0 = 0; c0 < d_c; c0 += 4 * JOIN_THREADS) {
+      const int c = c0 + 4 * threadIdx.x;
+      const bool vec = d_c % 4 == 0;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k0 = 0; k0 < pieces; k0 += JOIN_THREADS) {
+        const int n = min(JOIN_THREADS, pieces - k0);
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) < n)
+          weights[threadIdx.x] = exp2f((__ldcg(a.part_ml + slot(k0 + threadIdx.x)).x - from) * to_log);
+        __syncthreads();
+        if (c < d_c && vec) {
+#pragma unroll 8
+          for (int k = 0; k < n; ++k) {
+            const float w = weights[k];
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(k0 + k) * d_c + c));
+            sum.x = fmaf(w, o.x, sum.x);
+            sum.y = fmaf(w, o.y, sum.y);
+            sum.z = fmaf(w, o.z, sum.z);
+            sum.w = fmaf(w, o.w, sum.w);
+          }
+        } else if (c < d_c) {
+          for (int k = 0; k < n; ++k) {
+            const float w = weights[k];
+            const float* o = a.part_o + slot(k0 + k) * d_c + c;
+            sum.x = fmaf(w, __ldcg(o), sum.x);
+            if (c + 1 < d_c) sum.y = fmaf(w, __ldcg(o + 1), sum.y);
+            if (c + 2 < d_c) sum.z = fmaf(w, __ldcg(o + 2), sum.z);
+            if (c + 3 < d_c) sum.w = fmaf(w, __ldcg(o + 3), sum.w);
+          }
+        }
+      }
+      if (c < d_c) out[c] = static_cast<T>(sum.x * inv);
+      if (c + 1 < d_c) out[c + 1] = static_cast<T>(sum.y * inv);
+      if (c + 2 < d_c) out[c + 2] = static_cast<T>(sum.z * inv);
+      if (c + 3 < d_c) out[c + 3] = static_cast<T>(sum.w * inv);
+    }
   }
 }
 
@@ -590,8 +632,8 @@ LaunchResult cache4_join(const CacheAttn& a, void* ctx, bool ctx_bf16, bool log2
   const float to_log = log2_units ? 1.f : 1.4426950408889634f;
   const ll rows = static_cast<ll>(a.items()) * std::min(a.tile, a.rows);
   const dim3 grid(static_cast<unsigned>(a.items()), static_cast<unsigned>(rows > 65536 ? 8 : std::min(a.tile, a.rows)));
-  r.err = ctx_bf16 ? launch_next(join_kernel<bf16>, grid, 128, 0, st, a, static_cast<bf16*>(ctx), to_log)
-                   : launch_next(join_kernel<float>, grid, 128, 0, st, a, static_cast<float*>(ctx), to_log);
+  r.err = ctx_bf16 ? launch_next(join_kernel<bf16>, grid, JOIN_THREADS, 0, st, a, static_cast<bf16*>(ctx), to_log)
+                   : launch_next(join_kernel<float>, grid, JOIN_THREADS, 0, st, a, static_cast<float*>(ctx), to_log);
   if (r.err != cudaSuccess) r.what = "cache4_join";
   return r;
 }

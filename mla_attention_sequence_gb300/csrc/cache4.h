@@ -99,7 +99,9 @@ LaunchResult cache4_simt_out(const CacheAttn& a, bool is_bf16, int d_v, const fl
 
 // Tensor cores, bf16 with d_c = 512, d_rope = 64: q_lat and ctx in bf16.
 constexpr int kTcRows = 128, kTcKeys = 64;
-LaunchResult cache4_tc_attn(const CacheAttn& a, const bf16* q, const bf16* q_lat, bf16* ctx, cudaStream_t st);
+// query: cache4_tc_query_bytes of scratch. ctx may be q_lat.
+size_t cache4_tc_query_bytes(long long rows);
+LaunchResult cache4_tc_attn(const CacheAttn& a, const bf16* q, const bf16* q_lat, void* query, bf16* ctx, cudaStream_t st);
 
 #ifdef __CUDACC__
 // The pool's row of position p of sequence b, or -1 where the table has none.
@@ -110,6 +112,15 @@ __device__ __forceinline__ long long cache_slot(const CacheView& c, const PageTa
   const int id = __ldg(t.table + static_cast<long long>(b) * t.most + k);
   if (id < 0 || id >= c.pages) return -1;
   return static_cast<long long>(id) * c.page + (p - k * c.page);
+}
+
+// The same for a position that fits in 31 bits, without branches and with a division of half the length;
+// *there: whether the table has it (else the slot is some slot of the pool).
+__device__ __forceinline__ long long cache_slot_of(const CacheView& c, const PageTable& t, int b, int p, bool* there) {
+  const uint32_t at = static_cast<uint32_t>(max(p, 0)), k = at / static_cast<uint32_t>(c.page);
+  const int id = __ldg(t.table + static_cast<long long>(b) * t.most + min(k, static_cast<uint32_t>(t.most - 1)));
+  *there = p >= 0 && k < static_cast<uint32_t>(t.most) && id >= 0 && id < c.pages;
+  return static_cast<long long>(*there ? id : 0) * c.page + (at - k * c.page);
 }
 
 constexpr int kStatusBadPage = 1;  // LAGA_ERR_INVALID_ARG in the device's status word

@@ -10,22 +10,24 @@
 //
 // One CTA per (part of the key tiles, half of the context's columns): TMEM cannot hold 128 x 512 fp32
 // context columns beside the scores, so both halves of a part compute the scores. Of the query tile
-// (nine [128 x 64] boxes, 144 KB) five boxes stay in TMEM as the A operand and four in shared memory,
+// (nine [128 x 64] boxes, 144 KB) four boxes stay in TMEM as the A operand and five in shared memory,
 // which leaves room there for two key tiles of 64 (nine [64 x 64] boxes, 72 KB each): one is being
 // expanded while the other is read by the products. With the query all in shared memory only one
 // would fit, and reading A from there would bound the products (6 KB for every 32 cycles of an
 // N = 64 step, 128 bytes a cycle).
 //
-// Warp roles (416 threads): warps 0..3 load the queries and do the softmax, one row a thread (their
-// TMEM lanes); warp 4 allocates TMEM and issues the MMAs; warps 5..12 expand the key tiles: a lane has
+// Warp roles (416 threads): warps 0..3 load the queries (TMA; what goes to TMEM by way of the place of
+// what stays) and do the softmax, one row a thread (their TMEM lanes); warp 4 allocates TMEM and issues the MMAs; warps 5..12 expand the key tiles: a lane has
 // a block of 16 values of one key (two keys' four blocks make eight lanes' stores hit eight different
 // 16-byte columns of the swizzled rows), and loads the next tile's bytes before it works on this one's.
 // The boxes that the context's product does not read are refilled as soon as the scores are done.
-// TMEM columns: query [0,160), S [160,224), P [224,256), O [256,512).
+// TMEM columns: query [0,128), S [128,192) and [192,256) in turn, P over its S, O [256,512).
 #include "cache4.h"
 #include "score_mod.cuh"
 
 #include <cuda_fp16.h>
+
+LAGA_TRACE_DEFINE(cache4)
 
 namespace laga {
 namespace {
@@ -33,13 +35,14 @@ namespace {
 using ll = long long;
 constexpr int BQ = 128, BKV = 64;
 constexpr int NBOX = 9, QBOX = 16384, KBOX = 8192;
-constexpr int Q_TMEM = 5;                    // query boxes in TMEM
+constexpr int Q_TMEM = 4;                    // query boxes in TMEM
 constexpr int K_BYTES = NBOX * KBOX;
 constexpr int Q_BYTES = (NBOX - Q_TMEM) * QBOX;
-constexpr int SMEM_BYTES = 2 * K_BYTES + Q_BYTES + 1024 + 512;
+constexpr int SMEM_BYTES = 2 * K_BYTES + Q_BYTES + 1024 + 256;
+static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 constexpr int SOFTMAX_WARPS = 4, PRODUCER_WARPS = 8, MMA_WARP = 4;
 constexpr int NTHREADS = 32 * (SOFTMAX_WARPS + 1 + PRODUCER_WARPS);
-constexpr uint32_t TMEM_COLS = 512, COL_S = 160, COL_P = 224, COL_O = 256;
+constexpr uint32_t TMEM_COLS = 512, COL_S = 128, COL_O = 256;
 constexpr int HALF = 256;
 // kind::f16 with fp16 operands is idesc_bf16 without the two type fields
 constexpr uint32_t F16 = ~((1u << 7) | (1u << 10));
@@ -50,8 +53,7 @@ constexpr float LIFT = 6.f, SLACK = 8.f;  // weights: the maximum's 2^6 when m i
 
 struct Params {
   CacheAttn a;
-  const bf16* q_lat;  // [B * rows][512]
-  const bf16* q;      // [B * rows][192], the RoPE part at 128
+  const float* up;    // [B * rows] what a row's scores are scaled up by; NaN: its result is NaN
   bf16* ctx;          // [B * rows][512]
   float sl2;          // scale * log2(e)
   ModParams mod;      // u_scale, cap_log2
@@ -115,84 +117,157 @@ __device__ __forceinline__ uint4 expand8(uint32_t codes, uint32_t s) {
   v.w = mul_f16x2(v.w, s);
   return v;
 }
-__device__ __forceinline__ bool bf16x2_finite(uint32_t w) {
-  return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
-}
-__device__ __forceinline__ bool finite8(uint4 v) {
-  return bf16x2_finite(v.x) && bf16x2_finite(v.y) && bf16x2_finite(v.z) && bf16x2_finite(v.w);
-}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// Eight bf16 values times `by`, as fp16 or (exactly, by a power of two) as bf16; their largest size.
+__device__ __forceinline__ uint4 f16_8(uint4 v, float by) {
+  return make_uint4(pack_f16x2(bf16_lo(v.x) * by, bf16_hi(v.x) * by), pack_f16x2(bf16_lo(v.y) * by, bf16_hi(v.y) * by),
+                    pack_f16x2(bf16_lo(v.z) * by, bf16_hi(v.z) * by), pack_f16x2(bf16_lo(v.w) * by, bf16_hi(v.w) * by));
+}
+__device__ __forceinline__ uint4 bf16_8(uint4 v, float by) {
+  return make_uint4(pack_bf16x2(bf16_lo(v.x) * by, bf16_hi(v.x) * by), pack_bf16x2(bf16_lo(v.y) * by, bf16_hi(v.y) * by),
+                    pack_bf16x2(bf16_lo(v.z) * by, bf16_hi(v.z) * by), pack_bf16x2(bf16_lo(v.w) * by, bf16_hi(v.w) * by));
+}
+__device__ __forceinline__ float size8(uint4 v) {
+  const float a = max3f(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x)), fabsf(bf16_lo(v.y)));
+  const float b = max3f(fabsf(bf16_hi(v.y)), fabsf(bf16_lo(v.z)), fabsf(bf16_hi(v.z)));
+  return max3f(fmaxf(a, b), fabsf(bf16_lo(v.w)), fabsf(bf16_hi(v.w)));
+}
+// 2^-e brings a row's largest size to between 2^8 and 2^9 (within what a power of two can).
+__device__ __forceinline__ int row_exponent(float top) {
+  return min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 8, -118), 118);
+}
+// Eight bf16 values, all finite (0 times an infinity or a NaN is a NaN).
+__device__ __forceinline__ bool finite8(uint4 v) {
+  uint32_t z = times_zero_plus_bf16x2(v.x, 0u);
+  z = times_zero_plus_bf16x2(v.y, z);
+  z = times_zero_plus_bf16x2(v.z, z);
+  z = times_zero_plus_bf16x2(v.w, z);
+  return (z & 0x7fff7fffu) == 0;
+}
 __device__ __forceinline__ uint4 ldg4(const void* p) { return __ldcg(static_cast<const uint4*>(p)); }
 
-// What a producer lane holds of one key tile: its block of 16 values in each of the eight latent boxes,
-// eight of the key's 32 scales (its neighbours have the others), two of its eight RoPE chunks.
+// What a producer lane holds of one key tile: its block of 16 values in each of the eight latent boxes
+// (first the four outside this CTA's half of the values), eight of the key's 32 scales (its neighbours
+// have the others), two of its eight RoPE chunks.
 struct Held {
-  uint2 codes[8], scales;
+  uint2 codes[8];
+  uint32_t scales[8];
   uint4 rope[2];
-  bool bad;
+  bool live, bad;  // a key to expand (else zeros); a key that should be there and is not
 };
-__device__ __forceinline__ void hold(const CacheAttn& a, const Piece& p, int tile, int key, int lane4, Held& h) {
+__device__ __forceinline__ void hold(const CacheAttn& a, const Piece& p, int tile, int key, int lane4, int vh, Held& h) {
   const int at = p.key0 + tile * BKV + key;
   const bool wanted = at >= p.hull.x && at < p.hull.y;
-  const ll slot = wanted ? cache_slot(a.cache, a.pages, p.b, at) : -1;
-  h.bad = wanted && slot < 0;
-  if (slot >= 0) {
-    const uint2* c = reinterpret_cast<const uint2*>(a.cache.codes + slot * 256) + lane4;
+  bool there;
+  const ll slot = cache_slot_of(a.cache, a.pages, p.b, wanted ? at : p.hull.x, &there);
+  h.live = wanted && there;
+  h.bad = wanted && !there;
+  const uint2* c = reinterpret_cast<const uint2*>(a.cache.codes + slot * 256) + lane4;
+  const uint8_t* s = a.cache.scales + slot * 32 + lane4;
+  const uint4* r = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.cache.keys) + slot * 64) + 2 * lane4;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) h.codes[k] = __ldg(c + 4 * k);
-    h.scales = __ldg(reinterpret_cast<const uint2*>(a.cache.scales + slot * 32) + lane4);
-    const uint4* r = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.cache.keys) + slot * 64) + 2 * lane4;
-    h.rope[0] = __ldg(r);
-    h.rope[1] = __ldg(r + 1);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) h.codes[k] = make_uint2(0, 0);
-    h.scales = make_uint2(0, 0);
-    h.rope[0] = h.rope[1] = make_uint4(0, 0, 0, 0);
+  for (int k = 0; k < 4; ++k) {
+    h.codes[k] = __ldg(c + 16 * (1 - vh) + 4 * k);
+    h.codes[4 + k] = __ldg(c + 16 * vh + 4 * k);
+    h.scales[k] = __ldg(s + 16 * (1 - vh) + 4 * k);
+    h.scales[4 + k] = __ldg(s + 16 * vh + 4 * k);
+  }
+  h.rope[0] = __ldg(r);
+  h.rope[1] = __ldg(r + 1);
+}
+
+// A warp's wait for a phase, all lanes together: the phase that is over costs a test and a vote. (One
+// lane waiting for the others costs two more convergence points and their taken branches; the waits of
+// a warp that comes by once a tile took hundreds of cycles then, even for phases long over.)
+__device__ __forceinline__ bool pass(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int where) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = global_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((it & 63u) == 0) {
+      const bool late = global_ns() - t0 > kWaitLimitNs;
+      if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
+        if (late) *abort_flag = kStatusTimeout | (where << 8);
+        __syncwarp();
+        return false;
+      }
+    }
   }
 }
 
+// The queries as operands: each row's 512 latent values as fp16 and 64 RoPE values as bf16, both times
+// the power of two that brings the row's largest size to 2^8 .. 2^9, and that power's inverse. A row
+// that holds a value that is not finite: zeros, and NaN in the power's place. A warp a row.
+constexpr int QUERY_WARPS = 8;
+__global__ void __launch_bounds__(32 * QUERY_WARPS) cache4_query_kernel(ll rows, const bf16* q_lat, const bf16* q,
+                                                                        uint8_t* out, float* up) {
+  after_previous();
+  const ll row = static_cast<ll>(blockIdx.x) * QUERY_WARPS + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const uint4* src = reinterpret_cast<const uint4*>(q_lat + row * 512);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint4 v0 = ldg4(src + lane), v1 = ldg4(src + 32 + lane);
+  const uint4 v2 = lane < 8 ? ldg4(reinterpret_cast<const uint4*>(q + row * 192 + 128) + lane) : zero;
+  float top = max3f(size8(v0), size8(v1), size8(v2));
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+  const bool fine = __all_sync(0xffffffffu, finite8(v0) && finite8(v1) && finite8(v2));
+  const int e = fine && top > 0.f ? row_exponent(top) : 0;
+  const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  uint4* to = reinterpret_cast<uint4*>(out + row * (2 * 576));
+  to[lane] = fine ? f16_8(v0, down) : zero;
+  to[32 + lane] = fine ? f16_8(v1, down) : zero;
+  if (lane < 8) to[64 + lane] = fine ? bf16_8(v2, down) : zero;
+  if (lane == 0) up[row] = fine ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __int_as_float(0x7fc00000);
+}
+
 template <int MOD>
-__global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p) {
+__global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_constant__ CUtensorMap mQ, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* sK = smem;
   uint8_t* sQ = smem + 2 * K_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sQ + Q_BYTES);
-  uint64_t* k_full = bars;        // [2] a key tile is expanded
-  uint64_t* ka_free = bars + 2;   // [2] its scores are done: the boxes outside this half's values
-  uint64_t* kb_free = bars + 4;   // [2] its context product is done: the others
+  uint64_t* ka_full = bars + 12;  // [2] a key tile's boxes outside this half's values are expanded
+  uint64_t* kb_full = bars;       // [2] the others
+  uint64_t* ka_free = bars + 2;   // [2] the scores are done: the former may be refilled
+  uint64_t* kb_free = bars + 4;   // [2] the context product is done: the latter
   uint64_t* s_full = bars + 6;
-  uint64_t* s_empty = bars + 7;   // S is in registers
   uint64_t* p_full = bars + 8;
   uint64_t* pv_done = bars + 9;   // P read, O up to date
-  uint64_t* q_full = bars + 10;
+  uint64_t* q_full = bars + 10;   // the TMEM boxes are there
+  uint64_t* q_stage = bars + 7;   // they are in shared memory
+  uint64_t* q_rest = bars + 17;   // the other boxes are there
+  uint64_t* q_idle = bars + 18;   // the softmax warps are done with the queries' place
   uint64_t* drain = bars + 11;
-  uint8_t* bad = reinterpret_cast<uint8_t*>(bars + 12);  // [2][8] a bit a key: it does not count as finite
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
+  uint8_t* bad = reinterpret_cast<uint8_t*>(bars + 14);  // [2][8] a bit a key: it does not count as finite
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheAttn& a = p.a;
   const int part = blockIdx.x >> 1, vh = blockIdx.x & 1;  // vh: this CTA's half of the context's columns
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], PRODUCER_WARPS);
+      mbar_init(&ka_full[i], PRODUCER_WARPS);
+      mbar_init(&kb_full[i], PRODUCER_WARPS);
       mbar_init(&ka_free[i], 1);
       mbar_init(&kb_free[i], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_empty, SOFTMAX_WARPS);
     mbar_init(p_full, SOFTMAX_WARPS);
     mbar_init(pv_done, 1);
     mbar_init(q_full, SOFTMAX_WARPS);
+    mbar_init(q_stage, 1);
+    mbar_init(q_rest, 1);
+    mbar_init(q_idle, SOFTMAX_WARPS);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -206,6 +281,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   after_previous();
+  LAGA_TRACE_CTA_BEGIN(cache4);
 
   Walk walk(a, part);
   Piece pc;
@@ -218,56 +294,50 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p
     bool ok = true, more = walk.next(pc);
     int j = 0;
     Held cur;
-    if (more) hold(a, pc, 0, key, b4, cur);
+    if (more) hold(a, pc, 0, key, b4, vh, cur);
     while (more && ok) {
       Held nxt;
       if (++j == pc.tiles) {
         j = 0;
         more = walk.next(pc);
       }
-      if (more) hold(a, pc, j, key, b4, nxt);
+      if (more) hold(a, pc, j, key, b4, vh, nxt);
+      LAGA_TRACE_POINT(cache4, 0, n);
       if (cur.bad && b4 == 0) report_page(a.status, 305);
       const int buf = n & 1;
       const uint32_t ph = static_cast<uint32_t>(((n >> 1) & 1) ^ 1);
       uint8_t* k = sK + buf * K_BYTES;
       bool fine = !cur.bad;
-      auto box = [&](int c) {
-        const uint32_t word = __shfl_sync(0xffffffffu, (c & 1) ? cur.scales.y : cur.scales.x, (lane & ~3) | (c >> 1));
-        const uint32_t e = (word >> (8 * b4)) & 0xffu;
-        uint2 w = cur.codes[c];
-        uint32_t s = (e << 7) | (e << 23);
-        if (e >= 248u) {  // a block that reads as NaN: zeros here, and every row that sees the key gets NaN
-          s = 0;
-          w = make_uint2(0, 0);
-          fine = false;
-        }
-        *reinterpret_cast<uint4*>(k + c * KBOX + off0) = expand8(w.x, s);
-        *reinterpret_cast<uint4*>(k + c * KBOX + off1) = expand8(w.y, s);
+      // The held block i, of box c. A block that reads as NaN: zeros here, and every row that sees the
+      // key gets NaN.
+      auto box = [&](int i, int c) {
+        const uint32_t e = cur.scales[i];
+        const bool number = e < 248u;
+        const uint32_t s = number && cur.live ? e * 0x800080u : 0u;
+        fine = fine && (number || !cur.live);
+        *reinterpret_cast<uint4*>(k + c * KBOX + off0) = expand8(cur.codes[i].x, s);
+        *reinterpret_cast<uint4*>(k + c * KBOX + off1) = expand8(cur.codes[i].y, s);
       };
-      if (!warp_wait_or_abort(&ka_free[buf], ph, abort_flag, 401)) break;
-      if (vh) {
+      if (!pass(&ka_free[buf], ph, abort_flag, 401)) break;
+      LAGA_TRACE_POINT(cache4, 1, n);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) box(c);
-      } else {
+      for (int i = 0; i < 4; ++i) box(i, 4 * (1 - vh) + i);
 #pragma unroll
-        for (int c = 4; c < 8; ++c) box(c);
+      for (int i = 0; i < 2; ++i) {
+        const bool number = finite8(cur.rope[i]);
+        fine = fine && (number || !cur.live);
+        if (!(number && cur.live)) cur.rope[i] = make_uint4(0, 0, 0, 0);
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (!finite8(cur.rope[i])) {
-          cur.rope[i] = make_uint4(0, 0, 0, 0);
-          fine = false;
-        }
       *reinterpret_cast<uint4*>(k + 8 * KBOX + off0) = cur.rope[0];
       *reinterpret_cast<uint4*>(k + 8 * KBOX + off1) = cur.rope[1];
-      if (!warp_wait_or_abort(&kb_free[buf], ph, abort_flag, 402)) break;
-      if (vh) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ka_full[buf]);
+      LAGA_TRACE_POINT(cache4, 2, n);
+      if (!pass(&kb_free[buf], ph, abort_flag, 402)) break;
+      LAGA_TRACE_POINT(cache4, 3, n);
 #pragma unroll
-        for (int c = 4; c < 8; ++c) box(c);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) box(c);
-      }
+      for (int i = 0; i < 4; ++i) box(4 + i, 4 * vh + i);
       const uint32_t odd = ~__ballot_sync(0xffffffffu, fine);  // four lanes a key
       if (lane == 0) {
         uint32_t bits = 0;
@@ -277,7 +347,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[buf]);
+      if (lane == 0) mbar_arrive(&kb_full[buf]);
+      LAGA_TRACE_POINT(cache4, 4, n);
       cur = nxt;
       ++n;
     }
@@ -287,41 +358,58 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p
     const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
     int n = 0, seg = 0;
     auto context = [&](int m, bool first) -> bool {  // O (+)= P(m) V(m)
-      if (!warp_wait_or_abort(p_full, m & 1, abort_flag, 411)) return false;
+      if (!pass(p_full, m & 1, abort_flag, 411)) return false;
+      LAGA_TRACE_POINT(cache4, 7, m);
       tc_fence_after();
       const uint64_t v = sdesc_sw128(smem_u32(sK + (m & 1) * K_BYTES + vh * 4 * KBOX), KBOX, 1024);
-      const uint32_t pp = tmem + COL_P;
+      const uint32_t pp = tmem + COL_S + (m & 1) * BKV;
       mma4_ts_warp(tmem + COL_O, pp, pp + 8, pp + 16, pp + 24, v, v + (2048 >> 4), v + (4096 >> 4), v + (6144 >> 4), IDESC_PV,
                    first ? 0u : 1u);
       mma_commit_warp(&kb_free[m & 1]);
       mma_commit_warp(pv_done);
       return true;
     };
+    // S (+)= Q K^T over boxes [c0, c1). Loops, not straight code: the four roles' instructions together
+    // outgrow the instruction cache otherwise.
+    auto scores = [&](uint32_t s, uint64_t kd, int c0, int c1, bool fresh) {
+#pragma unroll 1
+      for (int c = c0; c < c1; ++c) {
+        const uint64_t k = kd + ((c * KBOX) >> 4);
+        if (c < Q_TMEM) {
+          const uint32_t q = tmem + 32 * c;
+          mma4_ts_warp(s, q, q + 8, q + 16, q + 24, k, k + 2, k + 4, k + 6, IDESC_S, fresh && c == c0 ? 0u : 1u);
+        } else {
+          const uint64_t q = q_desc + (((c - Q_TMEM) * QBOX) >> 4);
+          mma4_ss_warp(s, q, q + 2, q + 4, q + 6, k, k + 2, k + 4, k + 6, c == 8 ? IDESC_ROPE : IDESC_S, fresh && c == c0 ? 0u : 1u);
+        }
+      }
+    };
     while (ok && walk.next(pc)) {
-      ok = warp_wait_or_abort(q_full, seg & 1, abort_flag, 412);
+      ok = pass(q_full, seg & 1, abort_flag, 412) && pass(q_rest, seg & 1, abort_flag, 416);
       ++seg;
       for (int j = 0; j < pc.tiles && ok; ++j, ++n) {
-        ok = warp_wait_or_abort(&k_full[n & 1], (n >> 1) & 1, abort_flag, 413) &&
-             (n == 0 || warp_wait_or_abort(s_empty, (n - 1) & 1, abort_flag, 414));
+        // the boxes that are there first; the context of the tile before between the two groups, since
+        // it frees the buffer that the tile after this one needs; then the boxes of the values
+        // (P of the tile two before, in this S's place, was read by a product issued earlier)
+        ok = pass(&ka_full[n & 1], (n >> 1) & 1, abort_flag, 413);
         if (!ok) break;
         tc_fence_after();
+        LAGA_TRACE_POINT(cache4, 5, n);
         const uint64_t kd = sdesc_sw128(smem_u32(sK + (n & 1) * K_BYTES), 16, 1024);
-        const uint32_t s = tmem + COL_S;
-#pragma unroll
-        for (int c = 0; c < NBOX; ++c) {
-          const uint64_t k = kd + ((c * KBOX) >> 4);
-          if (c < Q_TMEM) {
-            const uint32_t q = tmem + 32 * c;
-            mma4_ts_warp(s, q, q + 8, q + 16, q + 24, k, k + 2, k + 4, k + 6, IDESC_S, c > 0 ? 1u : 0u);
-          } else {
-            const uint64_t q = q_desc + (((c - Q_TMEM) * QBOX) >> 4);
-            mma4_ss_warp(s, q, q + 2, q + 4, q + 6, k, k + 2, k + 4, k + 6, c == 8 ? IDESC_ROPE : IDESC_S, 1u);
-          }
-        }
+        const uint32_t s = tmem + COL_S + (n & 1) * BKV;
+        scores(s, kd, 4 * (1 - vh), 4 * (1 - vh) + 4, true);
+        scores(s, kd, 8, 9, false);
         issued = true;
+        LAGA_TRACE_POINT(cache4, 6, n);
+        if (j > 0 && !(ok = context(n - 1, j == 1))) break;
+        ok = pass(&kb_full[n & 1], (n >> 1) & 1, abort_flag, 415);
+        if (!ok) break;
+        tc_fence_after();
+        LAGA_TRACE_POINT(cache4, 11, n);
+        scores(s, kd, 4 * vh, 4 * vh + 4, false);
         mma_commit_warp(&ka_free[n & 1]);
         mma_commit_warp(s_full);
-        if (j > 0) ok = context(n - 1, j == 1);
+        LAGA_TRACE_POINT(cache4, 12, n);
       }
       if (ok) ok = context(n - 1, pc.tiles == 1);
     }
@@ -335,44 +423,33 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p
     const int r = threadIdx.x;
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const float nan = __int_as_float(0x7fc00000);
-    int n = 0;
-    bool ok = true;
+    int n = 0, seg = 0;
+    bool ok = true, staged = false, rest = false;  // warp 0: copies of this piece are under way or done
     while (ok && walk.next(pc)) {
+      staged = rest = false;
       const bool there = r < pc.rows;
       const ll row = static_cast<ll>(pc.b) * a.rows + pc.r0 + (there ? r : 0);
       const int qi = (pc.r0 + r) / a.n_h, h = pc.r0 + r - qi * a.n_h;
       const int2 seen = there ? cache_row_bounds(a, pc.b, qi) : make_int2(0, 0);
-      const uint4* ql = reinterpret_cast<const uint4*>(p.q_lat + row * 512);
-      const uint4* qr = reinterpret_cast<const uint4*>(p.q + row * 192 + 128);
-      float top = 0.f;
-      bool odd = false;  // the row's result is NaN
-      if (there) {
-        auto look = [&](uint4 v) {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = max3f(top, fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i])));
-          odd = odd || !finite8(v);
-        };
-#pragma unroll 8
-        for (int c = 0; c < 64; ++c) look(ldg4(ql + c));
-#pragma unroll
-        for (int c = 0; c < 8; ++c) look(ldg4(qr + c));
+      const ll row0 = static_cast<ll>(pc.b) * a.rows + pc.r0;
+      // q_idle's phases: twice a piece, after the boxes for TMEM have been read and after O is out
+      if (warp == 0) {
+        if (seg > 0 && !pass(q_idle, 1, abort_flag, 424)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_stage, Q_TMEM * QBOX);
+          for (int c = 0; c < Q_TMEM; ++c) tma_load_2d(sQ + c * QBOX, &mQ, q_stage, 64 * c, static_cast<int>(row0));
+        }
+        staged = true;
       }
-      // the row's largest size becomes 2^8 to 2^9
-      const int e = top > 0.f && !odd ? min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 8, -118), 118) : 0;
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      const bool load = there && !odd;
-      auto f16_8 = [&](uint4 v) {
-        return make_uint4(pack_f16x2(bf16_lo(v.x) * down, bf16_hi(v.x) * down), pack_f16x2(bf16_lo(v.y) * down, bf16_hi(v.y) * down),
-                          pack_f16x2(bf16_lo(v.z) * down, bf16_hi(v.z) * down), pack_f16x2(bf16_lo(v.w) * down, bf16_hi(v.w) * down));
-      };
+      const float up = there ? __ldcg(p.up + row) : 1.f;
+      bool odd = up != up;  // the row's result is NaN
+      if (!pass(q_stage, seg & 1, abort_flag, 425)) { ok = false; break; }
 #pragma unroll 1
       for (int c = 0; c < Q_TMEM; ++c) {
         uint32_t u[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint4 v = f16_8(load ? ldg4(ql + 8 * c + i) : make_uint4(0, 0, 0, 0));
+          const uint4 v = *reinterpret_cast<const uint4*>(sQ + c * QBOX + sw128_offset(static_cast<uint32_t>(r), static_cast<uint32_t>(i)));
           u[4 * i] = v.x;
           u[4 * i + 1] = v.y;
           u[4 * i + 2] = v.z;
@@ -380,25 +457,25 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p
         }
         tmem_st32(tmem + 32 * c + lane_off, u);
       }
-#pragma unroll 1
-      for (int c = Q_TMEM; c < NBOX; ++c) {
-        uint8_t* box = sQ + (c - Q_TMEM) * QBOX;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint4 v = load ? (c < 8 ? ldg4(ql + 8 * c + i) : ldg4(qr + i)) : make_uint4(0, 0, 0, 0);
-          if (c < 8)
-            v = f16_8(v);
-          else
-            v = make_uint4(pack_bf16x2(bf16_lo(v.x) * down, bf16_hi(v.x) * down), pack_bf16x2(bf16_lo(v.y) * down, bf16_hi(v.y) * down),
-                           pack_bf16x2(bf16_lo(v.z) * down, bf16_hi(v.z) * down), pack_bf16x2(bf16_lo(v.w) * down, bf16_hi(v.w) * down));
-          *reinterpret_cast<uint4*>(box + sw128_offset(static_cast<uint32_t>(r), static_cast<uint32_t>(i))) = v;
-        }
-      }
+      fence_proxy_async_smem();  // read before the next copies write there
       tmem_wait_st();
       tc_fence_before();
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) {
+        mbar_arrive(q_idle);
+        mbar_arrive(q_full);
+      }
+      if (warp == 0) {
+        if (!pass(q_idle, 0, abort_flag, 426)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_rest, Q_BYTES);
+          for (int c = Q_TMEM; c < NBOX; ++c)
+            tma_load_2d(sQ + (c - Q_TMEM) * QBOX, &mQ, q_rest, 64 * c, static_cast<int>(row0));
+        }
+        rest = true;
+      }
+      ++seg;
+      LAGA_TRACE_POINT(cache4, 13, n);
 
       const float f = MOD & kModCap ? p.mod.u_scale * up : p.sl2 * up;  // score -> log2 units, or -> tanh's argument
       float slope2 = 0.f, pos = 0.f;
@@ -408,17 +485,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p
       }
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < pc.tiles && ok; ++j, ++n) {
-        if (!warp_wait_or_abort(s_full, n & 1, abort_flag, 421)) { ok = false; break; }
+        if (!pass(s_full, n & 1, abort_flag, 421)) { ok = false; break; }
+        LAGA_TRACE_POINT(cache4, 8, n);
         tc_fence_after();
         uint32_t x[64];
-        tmem_ld32(tmem + COL_S + lane_off, *reinterpret_cast<uint32_t(*)[32]>(x));
-        tmem_ld32(tmem + COL_S + 32 + lane_off, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+        const uint32_t s_at = tmem + COL_S + (n & 1) * BKV + lane_off;
+        tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(x));
+        tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
         uint2 bits;
         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(bits.x), "=r"(bits.y) : "r"(smem_u32(bad + (n & 1) * 8)));
         tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty);
         const int k0 = pc.key0 + j * BKV;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
@@ -461,8 +537,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p
           pk[i] = pack_f16x2(w0, w1);
         }
         l = fmaf(l, alpha, sum);
-        // O and P are the products' until the tile before is done
-        if (j > 0 && !warp_wait_or_abort(pv_done, (n - 1) & 1, abort_flag, 422)) { ok = false; break; }
+        LAGA_TRACE_POINT(cache4, 9, n);
+        // O is the products' until the tile before is done
+        if (j > 0 && !pass(pv_done, (n - 1) & 1, abort_flag, 422)) { ok = false; break; }
         tc_fence_after();
         if (__any_sync(0xffffffffu, rescale)) {
           const uint32_t o = tmem + COL_O + lane_off;
@@ -476,60 +553,92 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p
             tmem_st32(o + c * 32, u);
           }
         }
-        tmem_st32(tmem + COL_P + lane_off, pk);
+        tmem_st32(s_at, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
+        LAGA_TRACE_POINT(cache4, 10, n);
       }
-      if (!ok || !warp_wait_or_abort(pv_done, (n - 1) & 1, abort_flag, 423)) { ok = false; break; }
+      if (!ok || !pass(pv_done, (n - 1) & 1, abort_flag, 423)) { ok = false; break; }
       tc_fence_after();
       if (odd) l = nan;
+      LAGA_TRACE_POINT(cache4, 14, n);
+      // O out, 128 bytes a row at a time, turned in the queries' place (their products are done) so that a
+      // store writes whole lines.
       const uint32_t o = tmem + COL_O + lane_off;
-      if (pc.begins && pc.ends) {
-        if (l == 0.f && seen.x < seen.y) l = nan;  // every score it sees is -inf
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        bf16* out = p.ctx + row * 512 + vh * HALF;
+      uint8_t* stage = sQ + warp * 4096;
+      const bool whole = pc.begins && pc.ends;
+      const ll slot = static_cast<ll>(2 * part + (pc.begins ? 1 : 0)) * BQ;
+      if (whole && l == 0.f && seen.x < seen.y) l = nan;  // every score it sees is -inf
+      const float inv = l != l ? nan : l == 0.f ? 0.f : 1.f / l;
+      if (there && vh == 0) {
+        if (whole)
+          a.lse[(static_cast<ll>(pc.b) * a.n_h + h) * a.Sq + qi] = l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
+        else
+          a.part_ml[slot + r] = make_float2(m, l);
+      }
+      // row by row of the warp's 32, 16 bytes a lane
+      auto put = [&](uint8_t* base, ll row_bytes) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + sw128_offset(static_cast<uint32_t>(rr), lane & 7u));
+          if (warp * 32 + rr < pc.rows) *reinterpret_cast<uint4*>(base + (warp * 32 + rr) * row_bytes + 16 * (lane & 7)) = v;
+        }
+        __syncwarp();
+      };
+      if (whole) {
+        uint8_t* out = reinterpret_cast<uint8_t*>(p.ctx + row0 * 512 + vh * HALF);
 #pragma unroll 1
-        for (int c = 0; c < HALF / 32; ++c) {
-          uint32_t u[32];
-          tmem_ld32(o + c * 32, u);
-          tmem_wait_ld();
-          if (there) {
-            uint4* dst = reinterpret_cast<uint4*>(out + c * 32);
+        for (int c = 0; c < HALF / 64; ++c) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t u[32];
+            tmem_ld32(o + c * 64 + g * 32, u);
+            tmem_wait_ld();
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-              float y[8];
+              uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = l != l ? nan : __uint_as_float(u[8 * v + i]) * inv;
-              dst[v] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack_bf16x2(__uint_as_float(u[8 * v + 2 * i]) * inv, __uint_as_float(u[8 * v + 2 * i + 1]) * inv);
+              *reinterpret_cast<uint4*>(stage + sw128_offset(lane, 4 * g + v)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
+          put(out + 128 * c, 1024);
         }
-        if (there && vh == 0)
-          a.lse[(static_cast<ll>(pc.b) * a.n_h + h) * a.Sq + qi] = l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
       } else {
-        const ll slot = static_cast<ll>(2 * part + (pc.begins ? 1 : 0)) * BQ + r;
-        if (there && vh == 0) a.part_ml[slot] = make_float2(m, l);
-        float* out = a.part_o + slot * 512 + vh * HALF;
+        uint8_t* out = reinterpret_cast<uint8_t*>(a.part_o + slot * 512 + vh * HALF);
 #pragma unroll 1
         for (int c = 0; c < HALF / 32; ++c) {
           uint32_t u[32];
           tmem_ld32(o + c * 32, u);
           tmem_wait_ld();
-          if (there) {
-            uint4* dst = reinterpret_cast<uint4*>(out + c * 32);
 #pragma unroll
-            for (int v = 0; v < 8; ++v) dst[v] = make_uint4(u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
-          }
+          for (int v = 0; v < 8; ++v)
+            *reinterpret_cast<uint4*>(stage + sw128_offset(lane, v)) = make_uint4(u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
+          put(out + 128 * c, 2048);
         }
       }
+      LAGA_TRACE_POINT(cache4, 15, n);
       tc_fence_before();  // O has been read before the next piece's products overwrite it (q_full, p_full)
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_idle);
     }
+    if (!ok && warp == 0 && lane == 0) {  // given up: let the copies under way land
+      const uint32_t ph = static_cast<uint32_t>((rest ? seg - 1 : seg) & 1);
+      if (staged) mbar_drain(q_stage, ph);
+      if (rest) mbar_drain(q_rest, ph);
+    }
+    __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
+  LAGA_TRACE_CTA_END(cache4);
   if (threadIdx.x == 0) publish_abort(abort_flag, a.status);
   if (warp == MMA_WARP) {
     tc_fence_after();
@@ -539,22 +648,39 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const Params p
 
 }  // namespace
 
-LaunchResult cache4_tc_attn(const CacheAttn& a, const bf16* q, const bf16* q_lat, bf16* ctx, cudaStream_t st) {
+size_t cache4_tc_query_bytes(long long rows) { return align_up(static_cast<size_t>(rows) * 576 * 2, 256) + align_up(static_cast<size_t>(rows) * 4, 256); }
+
+LaunchResult cache4_tc_attn(const CacheAttn& a, const bf16* q, const bf16* q_lat, void* query, bf16* ctx, cudaStream_t st) {
+  const ll rows = static_cast<ll>(a.pages.B) * a.rows;
+  float* up = reinterpret_cast<float*>(static_cast<char*>(query) + align_up(static_cast<size_t>(rows) * 576 * 2, 256));
+  LaunchResult r;
+  CUtensorMap mQ;
+  const uint64_t dims[2] = {576, static_cast<uint64_t>(rows)}, strides[1] = {576 * 2};
+  const uint32_t box[2] = {64, BQ};
+  r.cu = make_tmap(&mQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, query, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!r.ok()) {
+    r.what = "tensor map cache4 queries";
+    return r;
+  }
+  r.err = launch_next(cache4_query_kernel, static_cast<unsigned>((rows + QUERY_WARPS - 1) / QUERY_WARPS), 32 * QUERY_WARPS, 0, st,
+                      rows, q_lat, q, static_cast<uint8_t*>(query), up);
+  if (r.err != cudaSuccess) {
+    r.what = "cache4_query";
+    return r;
+  }
   Params p{};
   p.a = a;
-  p.q_lat = q_lat;
-  p.q = q;
+  p.up = up;
   p.ctx = ctx;
   p.sl2 = a.scale * 1.4426950408889634f;
   Dims d{};
   d.scale = a.scale;
   p.mod = mod_params(d, a.mods);
-  LaunchResult r;
   const int mod = mod_of(a.mods);
   auto kern = mod == 0 ? cache4_attn_kernel<0> : mod == kModCap ? cache4_attn_kernel<kModCap>
             : mod == kModBias ? cache4_attn_kernel<kModBias> : cache4_attn_kernel<kModCap | kModBias>;
   r.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (r.err == cudaSuccess) r.err = launch_next(kern, 2 * a.parts, NTHREADS, SMEM_BYTES, st, p);
+  if (r.err == cudaSuccess) r.err = launch_next(kern, 2 * a.parts, NTHREADS, SMEM_BYTES, st, mQ, p);
   if (r.err != cudaSuccess) r.what = "cache4_attn";
   return r;
 }

@@ -81,8 +81,8 @@ struct AttnSizes {
   CacheAttn a;
   int d_nope, d_v;
   bool tc;
-  size_t items_bytes, hull_bytes, lat_bytes, ml_bytes, o_bytes;
-  size_t total() const { return items_bytes + hull_bytes + 2 * lat_bytes + ml_bytes + o_bytes; }
+  size_t items_bytes, hull_bytes, lat_bytes, query_bytes, ml_bytes, o_bytes;  // lat: q_lat, and the context over it
+  size_t total() const { return items_bytes + hull_bytes + lat_bytes + query_bytes + ml_bytes + o_bytes; }
 };
 
 laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cache, bool sizes_only, AttnSizes* s) {
@@ -127,6 +127,8 @@ laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cach
   s->items_bytes = align_up((items + 1) * sizeof(int), 256);
   s->hull_bytes = align_up(items * sizeof(int2), 256);
   s->lat_bytes = align_up(static_cast<size_t>(a.pages.B) * a.rows * a.cache.d_c * (s->tc ? 2 : 4), 256);
+  // CUDA cores: the context in a place of its own, since other CTAs still read the rows' queries
+  s->query_bytes = s->tc ? cache4_tc_query_bytes(static_cast<int64_t>(a.pages.B) * a.rows) : s->lat_bytes;
   s->ml_bytes = align_up(static_cast<size_t>(2) * a.parts * a.tile * sizeof(float2), 256);
   s->o_bytes = align_up(static_cast<size_t>(2) * a.parts * a.tile * a.cache.d_c * 4, 256);
   return LAGA_OK;
@@ -278,7 +280,7 @@ laga_status laga_mla_cache4_fwd(const laga_mla_cache4_desc* desc, const laga_mla
   a.first = reinterpret_cast<int*>(take(z.items_bytes));
   a.hull = reinterpret_cast<int2*>(take(z.hull_bytes));
   char* lat = take(z.lat_bytes);
-  char* ctx = take(z.lat_bytes);
+  char* query = take(z.query_bytes);
   a.part_ml = reinterpret_cast<float2*>(take(z.ml_bytes));
   a.part_o = reinterpret_cast<float*>(take(z.o_bytes));
   const bool b16 = a.cache.is_bf16;
@@ -286,7 +288,8 @@ laga_status laga_mla_cache4_fwd(const laga_mla_cache4_desc* desc, const laga_mla
   LaunchResult r = timed("cache4_plan", s, [&] { return cache4_plan(a, s); });
   if (z.tc) {
     auto cb = [](const void* p) { return static_cast<const bf16*>(p); };
-    bf16 *q_lat = reinterpret_cast<bf16*>(lat), *c = reinterpret_cast<bf16*>(ctx);
+    bf16* q_lat = reinterpret_cast<bf16*>(lat);
+    bf16* c = q_lat;
     Dims d{};
     d.B = 1;
     d.Sq = a.pages.B * a.Sq;
@@ -295,13 +298,13 @@ laga_status laga_mla_cache4_fwd(const laga_mla_cache4_desc* desc, const laga_mla
     d.d_nope = d.d_v = 128;
     d.d_rope = 64;
     if (r.ok()) r = timed("cache4_qlat", s, [&] { return tc_absorbed_qlat(d, cb(q), cb(W_UK), q_lat, s); });
-    if (r.ok()) r = timed("cache4_attn", s, [&] { return cache4_tc_attn(a, cb(q), q_lat, c, s); });
+    if (r.ok()) r = timed("cache4_attn", s, [&] { return cache4_tc_attn(a, cb(q), q_lat, query, c, s); });
     if (r.ok()) r = timed("cache4_join", s, [&] { return cache4_join(a, c, true, true, s); });
     if (r.ok()) r = timed("cache4_out", s, [&] { return tc_absorbed_outproj(d, c, cb(W_UV), static_cast<bf16*>(out), s); });
     return from_launch(r);
   }
   float* q_lat = reinterpret_cast<float*>(lat);
-  float* c = reinterpret_cast<float*>(ctx);
+  float* c = reinterpret_cast<float*>(query);
   if (r.ok()) r = timed("cache4_qlat", s, [&] { return cache4_simt_qlat(a, b16, z.d_nope, q, W_UK, q_lat, s); });
   if (r.ok()) r = timed("cache4_attn", s, [&] { return cache4_simt_attn(a, b16, z.d_nope, q, q_lat, c, s); });
   if (r.ok()) r = timed("cache4_join", s, [&] { return cache4_join(a, c, false, false, s); });
