@@ -97,11 +97,15 @@ LaunchResult cache4_simt_attn(const CacheAttn& a, bool is_bf16, int d_nope, cons
 LaunchResult cache4_simt_out(const CacheAttn& a, bool is_bf16, int d_v, const float* ctx, const void* W_UV, void* out,
                              cudaStream_t st);
 
-// Tensor cores, bf16 with d_c = 512, d_rope = 64: q_lat and ctx in bf16.
-constexpr int kTcRows = 128, kTcKeys = 64;
-// query: cache4_tc_query_bytes of scratch. ctx may be q_lat.
+// Tensor cores, bf16 with d_c = 512, d_rope = 64: q_lat and ctx in bf16. The query step makes operands
+// of q_lat and q in cache4_tc_query_bytes of scratch; ctx may then be where q_lat was.
 size_t cache4_tc_query_bytes(long long rows);
-LaunchResult cache4_tc_attn(const CacheAttn& a, const bf16* q, const bf16* q_lat, void* query, bf16* ctx, cudaStream_t st);
+const float* cache4_tc_query_up(const void* query, long long rows);
+LaunchResult cache4_tc_query(const CacheAttn& a, const bf16* q, const bf16* q_lat, void* query, cudaStream_t st);
+constexpr int kTcRows = 128, kTcKeys = 64;  // tcgen05
+LaunchResult cache4_tc_attn(const CacheAttn& a, const void* query, bf16* ctx, cudaStream_t st);
+constexpr int kMmaRows = 16, kMmaKeys = 32;  // mma.sync, for few rows
+LaunchResult cache4_mma_attn(const CacheAttn& a, const uint8_t* query, const float* up, bf16* ctx, cudaStream_t st);
 
 #ifdef __CUDACC__
 // The pool's row of position p of sequence b, or -1 where the table has none.

@@ -23,16 +23,14 @@
 // The boxes that the context's product does not read are refilled as soon as the scores are done.
 // TMEM columns: query [0,128), S [128,192) and [192,256) in turn, P over its S, O [256,512).
 #include "cache4.h"
+#include "cache4_tc.cuh"
 #include "score_mod.cuh"
-
-#include <cuda_fp16.h>
 
 LAGA_TRACE_DEFINE(cache4)
 
 namespace laga {
 namespace {
 
-using ll = long long;
 constexpr int BQ = 128, BKV = 64;
 constexpr int NBOX = 9, QBOX = 16384, KBOX = 8192;
 constexpr int Q_TMEM = 4;                    // query boxes in TMEM
@@ -49,7 +47,6 @@ constexpr uint32_t F16 = ~((1u << 7) | (1u << 10));
 constexpr uint32_t IDESC_S = idesc_bf16(BQ, BKV, false, false) & F16;
 constexpr uint32_t IDESC_ROPE = idesc_bf16(BQ, BKV, false, false);
 constexpr uint32_t IDESC_PV = idesc_bf16(BQ, HALF, false, true) & F16;
-constexpr float LIFT = 6.f, SLACK = 8.f;  // weights: the maximum's 2^6 when m is set, up to 2^14 before m is moved
 
 struct Params {
   CacheAttn a;
@@ -59,97 +56,6 @@ struct Params {
   ModParams mod;      // u_scale, cap_log2
 };
 
-// One part's piece of an item: its key tiles, in the order of the walk.
-struct Piece {
-  int item, b, r0, rows, tiles, key0;
-  int2 hull;
-  bool begins, ends;
-};
-struct Walk {
-  const CacheAttn& a;
-  CacheShare share;
-  int t, item;
-  __device__ __forceinline__ Walk(const CacheAttn& a_, int part) : a(a_), share(cache_share(a_, part)) {
-    t = share.begin;
-    item = t < share.end ? cache_item_of(a, t) - 1 : 0;
-  }
-  __device__ __forceinline__ bool next(Piece& p) {
-    if (t >= share.end) return false;
-    int begin, end;
-    do {
-      ++item;
-      begin = __ldcg(a.first + item);
-      end = __ldcg(a.first + item + 1);
-    } while (end <= t);  // items without keys
-    p.item = item;
-    p.b = item / a.row_tiles;
-    p.r0 = (item - p.b * a.row_tiles) * BQ;
-    p.rows = min(BQ, a.rows - p.r0);
-    p.hull = __ldcg(a.hull + item);
-    p.key0 = (p.hull.x / BKV + (t - begin)) * BKV;
-    p.begins = t == begin;
-    p.ends = end <= share.end;
-    p.tiles = min(end, share.end) - t;
-    t += p.tiles;
-    return true;
-  }
-};
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// Eight codes times a scale (both halves of s), exactly: eight fp16 values in order.
-__device__ __forceinline__ uint4 expand8(uint32_t codes, uint32_t s) {
-  uint4 v;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-      : "r"(codes));
-  v.x = mul_f16x2(v.x, s);
-  v.y = mul_f16x2(v.y, s);
-  v.z = mul_f16x2(v.z, s);
-  v.w = mul_f16x2(v.w, s);
-  return v;
-}
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// Eight bf16 values times `by`, as fp16 or (exactly, by a power of two) as bf16; their largest size.
-__device__ __forceinline__ uint4 f16_8(uint4 v, float by) {
-  return make_uint4(pack_f16x2(bf16_lo(v.x) * by, bf16_hi(v.x) * by), pack_f16x2(bf16_lo(v.y) * by, bf16_hi(v.y) * by),
-                    pack_f16x2(bf16_lo(v.z) * by, bf16_hi(v.z) * by), pack_f16x2(bf16_lo(v.w) * by, bf16_hi(v.w) * by));
-}
-__device__ __forceinline__ uint4 bf16_8(uint4 v, float by) {
-  return make_uint4(pack_bf16x2(bf16_lo(v.x) * by, bf16_hi(v.x) * by), pack_bf16x2(bf16_lo(v.y) * by, bf16_hi(v.y) * by),
-                    pack_bf16x2(bf16_lo(v.z) * by, bf16_hi(v.z) * by), pack_bf16x2(bf16_lo(v.w) * by, bf16_hi(v.w) * by));
-}
-__device__ __forceinline__ float size8(uint4 v) {
-  const float a = max3f(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x)), fabsf(bf16_lo(v.y)));
-  const float b = max3f(fabsf(bf16_hi(v.y)), fabsf(bf16_lo(v.z)), fabsf(bf16_hi(v.z)));
-  return max3f(fmaxf(a, b), fabsf(bf16_lo(v.w)), fabsf(bf16_hi(v.w)));
-}
-// 2^-e brings a row's largest size to between 2^8 and 2^9 (within what a power of two can).
-__device__ __forceinline__ int row_exponent(float top) {
-  return min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 8, -118), 118);
-}
-// Eight bf16 values, all finite (0 times an infinity or a NaN is a NaN).
-__device__ __forceinline__ bool finite8(uint4 v) {
-  uint32_t z = times_zero_plus_bf16x2(v.x, 0u);
-  z = times_zero_plus_bf16x2(v.y, z);
-  z = times_zero_plus_bf16x2(v.z, z);
-  z = times_zero_plus_bf16x2(v.w, z);
-  return (z & 0x7fff7fffu) == 0;
-}
-__device__ __forceinline__ uint4 ldg4(const void* p) { return __ldcg(static_cast<const uint4*>(p)); }
 
 // What a producer lane holds of one key tile: its block of 16 values in each of the eight latent boxes
 // (first the four outside this CTA's half of the values), eight of the key's 32 scales (its neighbours
@@ -283,7 +189,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
   after_previous();
   LAGA_TRACE_CTA_BEGIN(cache4);
 
-  Walk walk(a, part);
+  Walk<BQ, BKV> walk(a, part);
   Piece pc;
   if (warp > MMA_WARP) {
     // ---------------- expand key tiles
@@ -650,9 +556,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
 
 size_t cache4_tc_query_bytes(long long rows) { return align_up(static_cast<size_t>(rows) * 576 * 2, 256) + align_up(static_cast<size_t>(rows) * 4, 256); }
 
-LaunchResult cache4_tc_attn(const CacheAttn& a, const bf16* q, const bf16* q_lat, void* query, bf16* ctx, cudaStream_t st) {
+const float* cache4_tc_query_up(const void* query, long long rows) {
+  return reinterpret_cast<const float*>(static_cast<const char*>(query) + align_up(static_cast<size_t>(rows) * 576 * 2, 256));
+}
+
+LaunchResult cache4_tc_query(const CacheAttn& a, const bf16* q, const bf16* q_lat, void* query, cudaStream_t st) {
   const ll rows = static_cast<ll>(a.pages.B) * a.rows;
-  float* up = reinterpret_cast<float*>(static_cast<char*>(query) + align_up(static_cast<size_t>(rows) * 576 * 2, 256));
+  LaunchResult r;
+  r.err = launch_next(cache4_query_kernel, static_cast<unsigned>((rows + QUERY_WARPS - 1) / QUERY_WARPS), 32 * QUERY_WARPS, 0, st,
+                      rows, q_lat, q, static_cast<uint8_t*>(query), const_cast<float*>(cache4_tc_query_up(query, rows)));
+  if (r.err != cudaSuccess) r.what = "cache4_query";
+  return r;
+}
+
+LaunchResult cache4_tc_attn(const CacheAttn& a, const void* query, bf16* ctx, cudaStream_t st) {
+  const ll rows = static_cast<ll>(a.pages.B) * a.rows;
   LaunchResult r;
   CUtensorMap mQ;
   const uint64_t dims[2] = {576, static_cast<uint64_t>(rows)}, strides[1] = {576 * 2};
@@ -662,15 +580,9 @@ LaunchResult cache4_tc_attn(const CacheAttn& a, const bf16* q, const bf16* q_lat
     r.what = "tensor map cache4 queries";
     return r;
   }
-  r.err = launch_next(cache4_query_kernel, static_cast<unsigned>((rows + QUERY_WARPS - 1) / QUERY_WARPS), 32 * QUERY_WARPS, 0, st,
-                      rows, q_lat, q, static_cast<uint8_t*>(query), up);
-  if (r.err != cudaSuccess) {
-    r.what = "cache4_query";
-    return r;
-  }
   Params p{};
   p.a = a;
-  p.up = up;
+  p.up = cache4_tc_query_up(query, rows);
   p.ctx = ctx;
   p.sl2 = a.scale * 1.4426950408889634f;
   Dims d{};

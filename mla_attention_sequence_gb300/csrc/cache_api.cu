@@ -77,10 +77,13 @@ laga_status check_rows(int64_t batch, int64_t rows, int64_t max_pages, const int
   return LAGA_OK;
 }
 
+// Rows of a sequence up to which mma.sync's form is used.
+constexpr int kFewRows = 64;
+
 struct AttnSizes {
   CacheAttn a;
   int d_nope, d_v;
-  bool tc;
+  bool tc, few;  // tensor cores; mma.sync's form of them
   size_t items_bytes, hull_bytes, lat_bytes, query_bytes, ml_bytes, o_bytes;  // lat: q_lat, and the context over it
   size_t total() const { return items_bytes + hull_bytes + lat_bytes + query_bytes + ml_bytes + o_bytes; }
 };
@@ -115,9 +118,11 @@ laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cach
                                    : 1.f / std::sqrt(static_cast<float>(d->d_nope + cache->d_rope));
   s->tc = d->variant == LAGA_VARIANT_AUTO && a.cache.is_bf16 && a.cache.d_c == 512 && a.cache.d_rope == 64 &&
           s->d_nope == 128 && s->d_v == 128;
-  a.tile = s->tc ? kTcRows : kSimtRows;
-  a.keys = s->tc ? kTcKeys : kSimtKeys;
-  a.parts = s->tc ? sm_count() / 2 : 2 * sm_count();  // tensor cores: two CTAs a part, one a SM
+  s->few = s->tc && a.rows <= kFewRows;
+  a.tile = s->few ? kMmaRows : s->tc ? kTcRows : kSimtRows;
+  a.keys = s->few ? kMmaKeys : s->tc ? kTcKeys : kSimtKeys;
+  // tcgen05: two CTAs a part, one a SM; else one, two a SM
+  a.parts = s->tc && !s->few ? sm_count() / 2 : 2 * sm_count();
   a.least = 1;
   a.row_tiles = (a.rows + a.tile - 1) / a.tile;
   const int64_t items = static_cast<int64_t>(a.pages.B) * a.row_tiles;
@@ -298,7 +303,13 @@ laga_status laga_mla_cache4_fwd(const laga_mla_cache4_desc* desc, const laga_mla
     d.d_nope = d.d_v = 128;
     d.d_rope = 64;
     if (r.ok()) r = timed("cache4_qlat", s, [&] { return tc_absorbed_qlat(d, cb(q), cb(W_UK), q_lat, s); });
-    if (r.ok()) r = timed("cache4_attn", s, [&] { return cache4_tc_attn(a, cb(q), q_lat, query, c, s); });
+    if (r.ok()) r = timed("cache4_query", s, [&] { return cache4_tc_query(a, cb(q), q_lat, query, s); });
+    if (r.ok())
+      r = timed("cache4_attn", s, [&] {
+        if (!z.few) return cache4_tc_attn(a, query, c, s);
+        return cache4_mma_attn(a, reinterpret_cast<const uint8_t*>(query),
+                               cache4_tc_query_up(query, static_cast<long long>(a.pages.B) * a.rows), c, s);
+      });
     if (r.ok()) r = timed("cache4_join", s, [&] { return cache4_join(a, c, true, true, s); });
     if (r.ok()) r = timed("cache4_out", s, [&] { return tc_absorbed_outproj(d, c, cb(W_UV), static_cast<bf16*>(out), s); });
     return from_launch(r);
