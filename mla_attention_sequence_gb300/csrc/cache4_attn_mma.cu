@@ -186,14 +186,16 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
     for (int j = 0; j < pc.tiles; ++j, ++n) {
       const int stage = n % STAGES;
       const uint32_t base = stages + stage * STAGE_BYTES + g * KEY_BYTES;
-      // ---- expand, and this warp's part of the scores
+      // ---- expand, and this warp's part of the scores. (Straight code: the four key groups' chains of
+      // products run beside each other.)
       uint32_t kv[4][2][8];
-      uint32_t strange = 0;
+      uint2 rope[4];
+      uint32_t strange = 0;  // a bit a key group: this lane's key is not finite
 #pragma unroll
       for (int kt = 0; kt < 4; ++kt) {  // 8 keys, one a lane group
         const uint32_t at = base + kt * 8 * KEY_BYTES;
         const uint2 sc = lds8(at + 256 + 8 * warp);
-        uint2 rope = lds8(at + 288 + 32 * warp + 8 * t4);
+        rope[kt] = lds8(at + 288 + 32 * warp + 8 * t4);
         bool fine = true;
 #pragma unroll
         for (int G = 0; G < 2; ++G) {
@@ -212,56 +214,83 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
           kv[kt][G][6] = y.z;
           kv[kt][G][7] = y.w;
         }
-        const bool number = finite4(rope);
+        const bool number = finite4(rope[kt]);
         fine = fine && number;
-        if (!number) rope = make_uint2(0, 0);
-        const uint32_t votes = __ballot_sync(0xffffffffu, !fine);
-        if (votes) {  // a bit a key from a bit a lane
-#pragma unroll
-          for (int i = 0; i < 8; ++i) strange |= ((votes >> (4 * i)) & 15u) ? 1u << (8 * kt + i) : 0u;
-        }
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_bf16(s, qr, rope.x, rope.y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mma_f16(s, qa[k], kv[kt][k >> 2][2 * (k & 3)], kv[kt][k >> 2][2 * (k & 3) + 1]);
-        float* to = sp + (warp * ROWS + g) * SP_STRIDE + 8 * kt + 2 * t4;
-        *reinterpret_cast<float2*>(to) = make_float2(s[0], s[1]);
-        *reinterpret_cast<float2*>(to + 8 * SP_STRIDE) = make_float2(s[2], s[3]);
+        rope[kt].x = number ? rope[kt].x : 0u;
+        rope[kt].y = number ? rope[kt].y : 0u;
+        strange |= fine ? 0u : 1u << kt;
       }
-      if (lane == 0) bad[warp] = strange;
+      float s[4][4];
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+        s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.f;
+        mma_bf16(s[kt], qr, rope[kt].x, rope[kt].y);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) mma_f16(s[kt], qa[k], kv[kt][k >> 2][2 * (k & 3)], kv[kt][k >> 2][2 * (k & 3) + 1]);
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+        float* to = sp + (warp * ROWS + g) * SP_STRIDE + 8 * kt + 2 * t4;
+        *reinterpret_cast<float2*>(to) = make_float2(s[kt][0], s[kt][1]);
+        *reinterpret_cast<float2*>(to + 8 * SP_STRIDE) = make_float2(s[kt][2], s[kt][3]);
+      }
+      uint32_t strange_keys = 0;
+      if (__any_sync(0xffffffffu, strange)) {
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          const uint32_t votes = __ballot_sync(0xffffffffu, (strange >> kt) & 1u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) strange_keys |= ((votes >> (4 * i)) & 15u) ? 1u << (8 * kt + i) : 0u;
+        }
+      }
+      if (lane == 0) bad[warp] = strange_keys;
       const uint32_t lost = missing[stage];
       __syncthreads();  // the scores' parts are there; the stage has been read, and the weights before
       load();
-      // ---- weights: four rows, a key a lane
+      // ---- weights: four rows, a key a lane. m stays while no weight passes 2^(LIFT + SLACK), so that a
+      // tile needs no maximum but one vote.
       const int key0 = pc.key0 + j * KEYS, key = key0 + lane;
       const uint32_t not_finite = bad[0] | bad[1] | bad[2] | bad[3] | lost;
-      uint32_t changed = 0;
+      float x[4], by[4];
+      bool over = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* from = sp + (4 * warp + i) * SP_STRIDE + lane;
+        float v = (from[0] + from[ROWS * SP_STRIDE]) + (from[2 * ROWS * SP_STRIDE] + from[3 * ROWS * SP_STRIDE]);
+        v *= f[i];
+        if constexpr ((MOD & kModCap) != 0) v = tanh_rel(v) * p.mod.cap_log2;
+        if constexpr ((MOD & kModBias) != 0) v = fmaf(-slope2[i], fabsf(pos[i] - static_cast<float>(j * KEYS)), v);
+        x[i] = key >= seen[i].x && key < seen[i].y ? v : -INFINITY;
+        over = over || x[i] > m[i] + (LIFT + SLACK);
+        by[i] = 1.f;
+      }
+      if (not_finite) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (__any_sync(0xffffffffu, key >= seen[i].x && key < seen[i].y && ((not_finite >> lane) & 1u))) odd |= 1u << i;
+      }
+      const bool changed = __any_sync(0xffffffffu, over);
+      if (changed) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float top = warp_max(x[i]) - LIFT;
+          if (top > m[i] + SLACK) {
+            by[i] = m[i] == -INFINITY ? 1.f : ex2_approx(m[i] - top);
+            m[i] = top;
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * warp + i;
-        const float* from = sp + r * SP_STRIDE + lane;
-        float s = (from[0] + from[ROWS * SP_STRIDE]) + (from[2 * ROWS * SP_STRIDE] + from[3 * ROWS * SP_STRIDE]);
-        s *= f[i];
-        if constexpr ((MOD & kModCap) != 0) s = tanh_rel(s) * p.mod.cap_log2;
-        if constexpr ((MOD & kModBias) != 0) s = fmaf(-slope2[i], fabsf(pos[i] - static_cast<float>(j * KEYS)), s);
-        const bool visible = key >= seen[i].x && key < seen[i].y;
-        if (!visible) s = -INFINITY;
-        if (not_finite && __any_sync(0xffffffffu, visible && ((not_finite >> lane) & 1u))) odd |= 1u << i;
-        const float top = warp_max(s) - LIFT;
-        float by = 1.f;
-        if (m[i] == -INFINITY) {
-          m[i] = top;
-        } else if (top > m[i] + SLACK) {
-          by = ex2_approx(m[i] - top);
-          m[i] = top;
-          changed = 1;
-        }
-        const float w = ex2_approx(s - (m[i] == -INFINITY ? 0.f : m[i]));
-        l[i] = fmaf(l[i], by, w);
+        const float w = ex2_approx(x[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+        l[i] = fmaf(l[i], by[i], w);
         ps[r * PS_STRIDE + lane] = __float2half_rn(w);
-        if (lane == 0) scale_by[r] = by;
+        if (lane == 0) scale_by[r] = by[i];
       }
-      if (lane == 0) reinterpret_cast<uint8_t*>(rescale)[warp] = static_cast<uint8_t>(changed);
+      if (lane == 0) reinterpret_cast<uint8_t*>(rescale)[warp] = changed ? 1 : 0;
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");  // the next tile
       __syncthreads();
       // ---- context
