@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(SIMT_THREADS) simt_attn_kernel(const CacheAttn
           const int e = scales[i / (kCacheBlock / 2)];
           const float2 f = codes_to_float2(codes[i]);
           const float s = scale_of(e);
-          fine = fine && e < 248;
+          fine = fine && e <= kCacheTopScale;
           to[2 * i] = f.x * s;
           if (2 * i + 1 < d_c) to[2 * i + 1] = f.y * s;
         }

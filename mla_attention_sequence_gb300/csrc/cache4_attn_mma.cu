@@ -14,9 +14,12 @@
 // owns. The parts of the scores are added up in shared memory, four rows a warp with a key a lane,
 // where the softmax's weights come from; they return as the context's A operand.
 //
-// Tiles of 32 keys come in by cp.async (26 chunks of 16 bytes a token, zeros for tokens outside the
-// item's interval), STAGES deep; two barriers a tile. The rows' stride of 416 bytes makes four tokens'
-// 32 bytes fall into different banks.
+// Tiles of 32 keys come in by bulk copies, three for each run of tokens that lie together in the pool,
+// STAGES deep, issued by the four warps in turn; two barriers a tile. A key outside the item's
+// interval, or without a page, is not copied: its lanes hold zeros. A key whose latent or RoPE key is not
+// finite shows in every row's score (0 times it is a NaN), so that no tile pays for a look at its values:
+// where a score is not finite the tile's scores are looked at key by key, the bad keys' lanes are zeroed,
+// and the rows that see one are marked.
 #include "cache4.h"
 #include "cache4_tc.cuh"
 #include "score_mod.cuh"
@@ -26,11 +29,10 @@ namespace {
 
 constexpr int ROWS = kMmaRows, KEYS = kMmaKeys, WARPS = 4, THREADS = 32 * WARPS;
 constexpr int STAGES = 6;
-constexpr int KEY_BYTES = 256 + 32 + 128;  // codes, scales, RoPE key
-constexpr int STAGE_BYTES = KEYS * KEY_BYTES;
+constexpr int CODES = KEYS * 256, SCALES = KEYS * 32, ROPE = KEYS * 128, STAGE_BYTES = CODES + SCALES + ROPE;
 constexpr int SP_STRIDE = 40, PS_STRIDE = 40;  // floats, halves: rows of 32 keys
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + WARPS * ROWS * SP_STRIDE * 4 + ROWS * PS_STRIDE * 2 + STAGES * 4 + WARPS * 4 +
-                           ROWS * 4 + 16;
+constexpr int SP_BYTES = WARPS * ROWS * SP_STRIDE * 4, PS_BYTES = ROWS * PS_STRIDE * 2;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SP_BYTES + PS_BYTES + 512;
 
 struct Params {
   CacheAttn a;
@@ -56,78 +58,97 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ uint2 lds8(uint32_t at) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
   return v;
 }
 
+// The CTA's barrier; true if no warp has given up.
+__device__ __forceinline__ bool together(bool ok) { return __syncthreads_and(ok) != 0; }
+
 template <int MOD>
 __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Params p) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  float* sp = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);        // [4][16][40] parts of the scores
-  __half* ps = reinterpret_cast<__half*>(sp + WARPS * ROWS * SP_STRIDE);    // [16][40] weights
-  uint32_t* missing = reinterpret_cast<uint32_t*>(ps + ROWS * PS_STRIDE);   // [STAGES] a bit a key: it has no page
-  uint32_t* bad = missing + STAGES;                                         // [4] .. : a warp saw it not finite
-  float* scale_by = reinterpret_cast<float*>(bad + WARPS);                  // [16] what the context so far is scaled by
-  uint32_t* rescale = reinterpret_cast<uint32_t*>(scale_by + ROWS);         // a bit a warp: some row's is not 1
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* sp = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);            // [4][16][40] parts of the scores
+  __half* ps = reinterpret_cast<__half*>(smem + STAGES * STAGE_BYTES + SP_BYTES);  // [16][40] weights
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + SP_BYTES + PS_BYTES);  // [STAGES]
+  uint32_t* live = reinterpret_cast<uint32_t*>(full + STAGES);    // [STAGES] a bit a key: it was copied
+  uint32_t* missing = live + STAGES;                              // [STAGES] a bit a key: it has no page
+  uint32_t* bad = missing + STAGES;                               // [4] a bit a key: a warp's scores of it are not finite
+  float* scale_by = reinterpret_cast<float*>(bad + WARPS);        // [16] what the context so far is scaled by
+  uint32_t* flags = reinterpret_cast<uint32_t*>(scale_by + ROWS);  // a byte a warp: 1 some row is rescaled, 2 some key is bad
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(flags + 1);
   const CacheAttn& a = p.a;
   const int part = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const uint32_t stages = smem_u32(smem);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
   after_previous();
 
   Walk<ROWS, KEYS> walk(a, part);
   Piece pc;
-  // The loads run STAGES - 1 tiles ahead, across pieces: a walk of their own.
+  // ---- copies: this warp's tiles are warp, warp + 4, .. of the part's, a lane a key. Where a key lies
+  // is looked up when the warp's tile before is issued, so that the table's latency is nobody's.
   Walk<ROWS, KEYS> ahead(a, part);
   Piece next;
-  int next_tile = 0;
   bool more = ahead.next(next);
-  int loaded = 0;
-  // Four lanes a key: chunks q, q + 4, .. of its 26.
-  auto load = [&]() {
-    const int s = loaded % STAGES;
-    if (more) {
-      const int key = threadIdx.x >> 2, q = threadIdx.x & 3, at = next.key0 + next_tile * KEYS + key;
-      const bool wanted = at >= next.hull.x && at < next.hull.y;
-      bool there;
-      const ll slot = cache_slot_of(a.cache, a.pages, next.b, wanted ? at : next.hull.x, &there);
-      const bool live = wanted && there;
-      const uint32_t gone = __ballot_sync(0xffffffffu, wanted && !there);
-      if (lane == 0) {
-        uint32_t bits = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) bits |= ((gone >> (4 * i)) & 1u) << i;
-        reinterpret_cast<uint8_t*>(missing + s)[warp] = static_cast<uint8_t>(bits);
-        if (gone) report_page(a.status, 306);
-      }
-      const uint32_t to = stages + s * STAGE_BYTES + key * KEY_BYTES;
-      const uint8_t* codes = a.cache.codes + slot * 256 + 16 * q;
-      const uint8_t* keys = static_cast<const uint8_t*>(a.cache.keys) + slot * 128 + 16 * q;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) copy16(to + 16 * (q + 4 * i), codes + 64 * i, live);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) copy16(to + 288 + 16 * (q + 4 * i), keys + 64 * i, live);
-      if (q < 2) copy16(to + 256 + 16 * q, a.cache.scales + slot * 32 + 16 * q, live);
-      if (++next_tile == next.tiles) {
-        next_tile = 0;
-        more = ahead.next(next);
-      }
+  int next_tile = warp, issued = warp;
+  ll slot = 0;
+  uint32_t keys = 0, gone = 0;  // a bit a key: to copy; without a page
+  auto look = [&]() {
+    while (more && next_tile >= next.tiles) {
+      next_tile -= next.tiles;
+      more = ahead.next(next);
     }
-    ++loaded;
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (!more) return;
+    const int at = next.key0 + next_tile * KEYS + lane;
+    const bool wanted = at >= next.hull.x && at < next.hull.y;
+    bool there;
+    slot = cache_slot_of(a.cache, a.pages, next.b, wanted ? at : next.hull.x, &there);
+    keys = wanted && there;
+    gone = wanted && !there;
   };
-  if (!more) return;
+  auto issue = [&]() {
+    if (!more) return;
+    const int st = issued % STAGES;
+    const bool mine = keys != 0;
+    const uint32_t all = __ballot_sync(0xffffffffu, mine), lost = __ballot_sync(0xffffffffu, gone != 0);
+    const ll before = __shfl_up_sync(0xffffffffu, slot, 1);
+    const bool starts = mine && (lane == 0 || !((all >> (lane - 1)) & 1u) || before + 1 != slot);
+    const uint32_t runs = __ballot_sync(0xffffffffu, starts);
+    if (lane == 0) {
+      live[st] = all;
+      missing[st] = lost;
+      if (lost) report_page(a.status, 306);
+      mbar_arrive_expect_tx(&full[st], __popc(all) * 416);
+    }
+    __syncwarp();
+    if (starts) {
+      // up to the next run's start or the next key that is not copied
+      const uint32_t after = lane == 31 ? 0u : (runs | ~all) >> (lane + 1);
+      const int len = after ? __ffs(after) : 32 - lane;
+      uint8_t* to = smem + st * STAGE_BYTES;
+      bulk_load(to + lane * 256, a.cache.codes + slot * 256, len * 256, &full[st]);
+      bulk_load(to + CODES + lane * 32, a.cache.scales + slot * 32, len * 32, &full[st]);
+      bulk_load(to + CODES + SCALES + lane * 128, static_cast<const uint8_t*>(a.cache.keys) + slot * 128, len * 128, &full[st]);
+    }
+    __syncwarp();
+    issued += WARPS;
+    next_tile += WARPS;
+    look();
+  };
+  look();
 #pragma unroll 1
-  for (int i = 0; i < STAGES - 1; ++i) load();
-  asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-  __syncthreads();
+  while (issued < STAGES && more) issue();
 
+  const uint32_t stages = smem_u32(smem);
   int n = 0;
-  while (walk.next(pc)) {
+  bool ok = true;
+  while (ok && walk.next(pc)) {
     // this warp's part of the queries: the k steps' A operands, in the order of its lanes' codes
     const ll row0 = static_cast<ll>(pc.b) * a.rows + pc.r0;
     uint32_t qa[8][4], qr[4];
@@ -185,25 +206,25 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
 
     for (int j = 0; j < pc.tiles; ++j, ++n) {
       const int stage = n % STAGES;
-      const uint32_t base = stages + stage * STAGE_BYTES + g * KEY_BYTES;
+      ok = pass(&full[stage], (n / STAGES) & 1, abort_flag, 432);
+      const uint32_t base = stages + stage * STAGE_BYTES;
       // ---- expand, and this warp's part of the scores. (Straight code: the four key groups' chains of
       // products run beside each other.)
       uint32_t kv[4][2][8];
       uint2 rope[4];
-      uint32_t strange = 0;  // a bit a key group: this lane's key is not finite
+      const uint32_t copied = live[stage], lost = missing[stage];
 #pragma unroll
       for (int kt = 0; kt < 4; ++kt) {  // 8 keys, one a lane group
-        const uint32_t at = base + kt * 8 * KEY_BYTES;
-        const uint2 sc = lds8(at + 256 + 8 * warp);
-        rope[kt] = lds8(at + 288 + 32 * warp + 8 * t4);
-        bool fine = true;
+        const int key = 8 * kt + g;
+        const uint2 sc = lds8(base + CODES + key * 32 + 8 * warp);
+        rope[kt] = lds8(base + CODES + SCALES + key * 128 + 32 * warp + 8 * t4);
+        // odd keys' groups the other way round: half as many keys meet in a bank
+        const uint32_t at = base + key * 256 + 64 * warp + 8 * t4, swap = 32 * (g & 1);
+        const uint2 w0 = lds8(at + swap), w1 = lds8(at + (swap ^ 32));
 #pragma unroll
         for (int G = 0; G < 2; ++G) {
-          const uint2 w = lds8(at + 64 * warp + 32 * G + 8 * t4);
-          const uint32_t e = ((G ? sc.y : sc.x) >> (8 * t4)) & 0xffu;
-          const bool number = e < 248u;
-          fine = fine && number;
-          const uint32_t s = number ? e * 0x800080u : 0u;
+          const uint2 w = (g & 1) == G ? w0 : w1;
+          const uint32_t s = (((G ? sc.y : sc.x) >> (8 * t4)) & 0xffu) * 0x800080u;
           const uint4 x = expand8(w.x, s), y = expand8(w.y, s);
           kv[kt][G][0] = x.x;
           kv[kt][G][1] = x.y;
@@ -214,12 +235,20 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
           kv[kt][G][6] = y.z;
           kv[kt][G][7] = y.w;
         }
-        const bool number = finite4(rope[kt]);
-        fine = fine && number;
-        rope[kt].x = number ? rope[kt].x : 0u;
-        rope[kt].y = number ? rope[kt].y : 0u;
-        strange |= fine ? 0u : 1u << kt;
       }
+      auto clear = [&](uint32_t keep) {  // zeros for the keys whose bit is not set
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          const bool here = (keep >> (8 * kt + g)) & 1u;
+#pragma unroll
+          for (int G = 0; G < 2; ++G)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) kv[kt][G][k] = here ? kv[kt][G][k] : 0u;
+          rope[kt].x = here ? rope[kt].x : 0u;
+          rope[kt].y = here ? rope[kt].y : 0u;
+        }
+      };
+      if (copied != 0xffffffffu) clear(copied);
       float s[4][4];
 #pragma unroll
       for (int kt = 0; kt < 4; ++kt) {
@@ -236,29 +265,19 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
         *reinterpret_cast<float2*>(to) = make_float2(s[kt][0], s[kt][1]);
         *reinterpret_cast<float2*>(to + 8 * SP_STRIDE) = make_float2(s[kt][2], s[kt][3]);
       }
-      uint32_t strange_keys = 0;
-      if (__any_sync(0xffffffffu, strange)) {
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-          const uint32_t votes = __ballot_sync(0xffffffffu, (strange >> kt) & 1u);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) strange_keys |= ((votes >> (4 * i)) & 15u) ? 1u << (8 * kt + i) : 0u;
-        }
-      }
-      if (lane == 0) bad[warp] = strange_keys;
-      const uint32_t lost = missing[stage];
-      __syncthreads();  // the scores' parts are there; the stage has been read, and the weights before
-      load();
+      ok = together(ok);  // the scores' parts are there; the tile, and the weights before, have been read
+      if (!ok) break;
+      if (((n + STAGES) & (WARPS - 1)) == warp) issue();
       // ---- weights: four rows, a key a lane. m stays while no weight passes 2^(LIFT + SLACK), so that a
       // tile needs no maximum but one vote.
       const int key0 = pc.key0 + j * KEYS, key = key0 + lane;
-      const uint32_t not_finite = bad[0] | bad[1] | bad[2] | bad[3] | lost;
       float x[4], by[4];
-      bool over = false;
+      bool over = false, strange = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float* from = sp + (4 * warp + i) * SP_STRIDE + lane;
         float v = (from[0] + from[ROWS * SP_STRIDE]) + (from[2 * ROWS * SP_STRIDE] + from[3 * ROWS * SP_STRIDE]);
+        strange = strange || !(fabsf(v) <= 3.402823466e38f);
         v *= f[i];
         if constexpr ((MOD & kModCap) != 0) v = tanh_rel(v) * p.mod.cap_log2;
         if constexpr ((MOD & kModBias) != 0) v = fmaf(-slope2[i], fabsf(pos[i] - static_cast<float>(j * KEYS)), v);
@@ -266,10 +285,18 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
         over = over || x[i] > m[i] + (LIFT + SLACK);
         by[i] = 1.f;
       }
-      if (not_finite) {
+      // a key that is not finite: no weight, and NaN for the rows that see it
+      const uint32_t not_finite = __ballot_sync(0xffffffffu, strange);
+      if (lane == 0) bad[warp] = not_finite;
+      if (not_finite | lost) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (__any_sync(0xffffffffu, key >= seen[i].x && key < seen[i].y && ((not_finite >> lane) & 1u))) odd |= 1u << i;
+        for (int i = 0; i < 4; ++i) {
+          const bool hit = key >= seen[i].x && key < seen[i].y && (((not_finite | lost) >> lane) & 1u);
+          if (__any_sync(0xffffffffu, hit)) odd |= 1u << i;
+        }
+        over = over && !((not_finite >> lane) & 1u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = ((not_finite >> lane) & 1u) ? -INFINITY : x[i];
       }
       const bool changed = __any_sync(0xffffffffu, over);
       if (changed) {
@@ -290,11 +317,12 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
         ps[r * PS_STRIDE + lane] = __float2half_rn(w);
         if (lane == 0) scale_by[r] = by[i];
       }
-      if (lane == 0) reinterpret_cast<uint8_t*>(rescale)[warp] = changed ? 1 : 0;
-      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");  // the next tile
-      __syncthreads();
+      if (lane == 0) reinterpret_cast<uint8_t*>(flags)[warp] = (changed ? 1 : 0) | (not_finite ? 2 : 0);
+      together(true);
       // ---- context
-      if (*rescale) {
+      const uint32_t flag = *flags;
+      if (flag & 0x02020202u) clear(~(bad[0] | bad[1] | bad[2] | bad[3]));
+      if (flag & 0x01010101u) {
         const float x = scale_by[g], y = scale_by[g + 8];
 #pragma unroll
         for (int G = 0; G < 2; ++G)
@@ -322,7 +350,8 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
     }
 
     // ---- the piece's end: sums of the rows to all warps
-    __syncthreads();
+    if (!ok) break;
+    together(true);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * warp + i;
@@ -344,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
         }
       }
     }
-    __syncthreads();
+    together(true);
     // a lane has 16 columns of each of its two groups, of rows g and g + 8
     if (pc.begins && pc.ends) {
 #pragma unroll
@@ -378,9 +407,13 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
           }
       }
     }
-    __syncthreads();  // the sums have been read before the next piece's factors
+    together(true);  // the sums have been read before the next piece's factors
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (!ok) {  // given up: let the copies under way land
+    for (int i = issued - WARPS; i >= max(n, 0); i -= WARPS) mbar_drain(&full[i % STAGES], (i / STAGES) & 1);
+    __syncthreads();
+    if (threadIdx.x == 0) publish_abort(abort_flag, a.status);
+  }
 }
 
 }  // namespace

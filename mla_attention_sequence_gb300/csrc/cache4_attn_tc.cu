@@ -87,25 +87,6 @@ __device__ __forceinline__ void hold(const CacheAttn& a, const Piece& p, int til
   h.rope[1] = __ldg(r + 1);
 }
 
-// A warp's wait for a phase, all lanes together: the phase that is over costs a test and a vote. (One
-// lane waiting for the others costs two more convergence points and their taken branches; the waits of
-// a warp that comes by once a tile took hundreds of cycles then, even for phases long over.)
-__device__ __forceinline__ bool pass(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int where) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const unsigned long long t0 = global_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if ((it & 63u) == 0) {
-      const bool late = global_ns() - t0 > kWaitLimitNs;
-      if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
-        if (late) *abort_flag = kStatusTimeout | (where << 8);
-        __syncwarp();
-        return false;
-      }
-    }
-  }
-}
-
 // The queries as operands: each row's 512 latent values as fp16 and 64 RoPE values as bf16, both times
 // the power of two that brings the row's largest size to 2^8 .. 2^9, and that power's inverse. A row
 // that holds a value that is not finite: zeros, and NaN in the power's place. A warp a row.
@@ -218,7 +199,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
       // key gets NaN.
       auto box = [&](int i, int c) {
         const uint32_t e = cur.scales[i];
-        const bool number = e < 248u;
+        const bool number = e <= kCacheTopScale;
         const uint32_t s = number && cur.live ? e * 0x800080u : 0u;
         fine = fine && (number || !cur.live);
         *reinterpret_cast<uint4*>(k + c * KBOX + off0) = expand8(cur.codes[i].x, s);

@@ -106,6 +106,25 @@ __device__ __forceinline__ bool finite8(uint4 v) {
   return (z & 0x7fff7fffu) == 0;
 }
 __device__ __forceinline__ uint4 ldg4(const void* p) { return __ldcg(static_cast<const uint4*>(p)); }
+// A warp's wait for a phase, all lanes together: the phase that is over costs a test and a vote. (One
+// lane waiting for the others costs two more convergence points and their taken branches; the waits of
+// a warp that comes by once a tile took hundreds of cycles then, even for phases long over.)
+__device__ __forceinline__ bool pass(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int where) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = global_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((it & 63u) == 0) {
+      const bool late = global_ns() - t0 > kWaitLimitNs;
+      if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
+        if (late) *abort_flag = kStatusTimeout | (where << 8);
+        __syncwarp();
+        return false;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
