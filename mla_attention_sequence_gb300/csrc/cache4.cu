@@ -218,68 +218,16 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) read_kernel(const CacheRead a)
 
 // ---------------------------------------------------------------- sharing out and joining
 
-// A row's sum of weights at its end: 0 of a row that sees keys (whose scores were all -inf) is NaN.
-__device__ __forceinline__ float row_sum(float l, int2 seen) {
-  return l == 0.f && seen.x < seen.y ? __int_as_float(0x7fc00000) : l;
-}
-
-// One CTA: the items' intervals of keys, and the running sum of their key tiles.
 __global__ void __launch_bounds__(1024) plan_kernel(const CacheAttn a) {
-  __shared__ int sums[32];
   after_previous();
-  const int items = a.items(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const ll room = static_cast<ll>(a.pages.most) * a.cache.page;
-  int before = 0;
-  for (int j0 = 0; j0 < items; j0 += 1024) {
-    const int j = j0 + threadIdx.x;
-    int tiles = 0;
-    if (j < items) {
-      const int b = j / a.row_tiles, r0 = (j - b * a.row_tiles) * a.tile, r1 = min(r0 + a.tile, a.rows) - 1;
-      int lo = 0x7fffffff, hi = 0;
-      for (int i = r0 / a.n_h; i <= r1 / a.n_h; ++i) {
-        const int2 s = cache_row_bounds(a, b, i);
-        if (s.x >= s.y) continue;
-        lo = min(lo, s.x);
-        hi = max(hi, s.y);
-      }
-      if (hi > room) {  // keys that the table has no room for
-        report_page(a.status, 303);
-        a.hull[j] = make_int2(-1, -1);
-      } else {
-        a.hull[j] = hi > 0 ? make_int2(lo, hi) : make_int2(0, 0);
-        if (hi > 0) tiles = (hi - 1) / a.keys - lo / a.keys + 1;
-      }
-    }
-    int run = tiles;  // inclusive sum over the warp, then over the warps
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, run, m);
-      if (lane >= m) run += o;
-    }
-    if (lane == 31) sums[warp] = run;
-    __syncthreads();
-    if (warp == 0) {
-      int s = sums[lane];
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, s, m);
-        if (lane >= m) s += o;
-      }
-      sums[lane] = s;
-    }
-    __syncthreads();
-    if (j < items) a.first[j] = before + (warp ? sums[warp - 1] : 0) + run - tiles;
-    before += sums[31];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) a.first[items] = before;
+  cache4_plan_items<1024>(a);
 }
 
 // Rows blockIdx.y, + gridDim.y, .. of item blockIdx.x. The pieces' weights first, in shared memory (128
 // pieces at a time), then the columns, four a thread, all of a batch's loads before its sums.
 constexpr int JOIN_THREADS = 128;
-template <typename T>
-__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const CacheAttn a, T* ctx, float to_log) {
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const CacheAttn a, float* ctx) {
+  constexpr float to_log = 1.4426950408889634f;
   __shared__ float weights[JOIN_THREADS];
   __shared__ float2 red[JOIN_THREADS / 32];
   after_previous();
@@ -294,11 +242,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const CacheAttn a, T
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
     const ll row = static_cast<ll>(b) * a.rows + r0 + r;
     const int i = (r0 + r) / a.n_h, h = (r0 + r) - i * a.n_h;
-    T* out = ctx + row * d_c;
+    float* out = ctx + row * d_c;
     float* lse = a.lse + (static_cast<ll>(b) * a.n_h + h) * a.Sq + i;
     if (end == begin) {  // no keys: zero, or NaN where the table had no room
       const float v = hull.x < 0 ? __int_as_float(0x7fc00000) : 0.f;
-      for (int c = threadIdx.x; c < d_c; c += JOIN_THREADS) out[c] = static_cast<T>(v);
+      for (int c = threadIdx.x; c < d_c; c += JOIN_THREADS) out[c] = v;
       if (threadIdx.x == 0) *lse = hull.x < 0 ? v : -INFINITY;
       continue;
     }
@@ -324,7 +272,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const CacheAttn a, T
     for (int k = 0; k < JOIN_THREADS / 32; ++k) add(red[k]);
     l = row_sum(l, cache_row_bounds(a, b, i));
     const float inv = l != l ? l : l == 0.f ? 0.f : 1.f / l, from = m == -INFINITY ? 0.f : m;
-    if (threadIdx.x == 0) *lse = l == 0.f ? -INFINITY : m * (to_log * 0.6931471805599453f) + logf(l);
+    if (threadIdx.x == 0) *lse = l == 0.f ? -INFINITY : m + logf(l);
     for (int c0 = 0; c0 < d_c; c0 += 4 * JOIN_THREADS) {
       const int c = c0 + 4 * threadIdx.x;
       const bool vec = d_c % 4 == 0;
@@ -356,10 +304,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const CacheAttn a, T
           }
         }
       }
-      if (c < d_c) out[c] = static_cast<T>(sum.x * inv);
-      if (c + 1 < d_c) out[c + 1] = static_cast<T>(sum.y * inv);
-      if (c + 2 < d_c) out[c + 2] = static_cast<T>(sum.z * inv);
-      if (c + 3 < d_c) out[c + 3] = static_cast<T>(sum.w * inv);
+      if (c < d_c) out[c] = sum.x * inv;
+      if (c + 1 < d_c) out[c + 1] = sum.y * inv;
+      if (c + 2 < d_c) out[c + 2] = sum.z * inv;
+      if (c + 3 < d_c) out[c + 3] = sum.w * inv;
     }
   }
 }
@@ -627,13 +575,11 @@ LaunchResult cache4_plan(const CacheAttn& a, cudaStream_t st) {
   return r;
 }
 
-LaunchResult cache4_join(const CacheAttn& a, void* ctx, bool ctx_bf16, bool log2_units, cudaStream_t st) {
+LaunchResult cache4_join(const CacheAttn& a, float* ctx, cudaStream_t st) {
   LaunchResult r;
-  const float to_log = log2_units ? 1.f : 1.4426950408889634f;
   const ll rows = static_cast<ll>(a.items()) * std::min(a.tile, a.rows);
   const dim3 grid(static_cast<unsigned>(a.items()), static_cast<unsigned>(rows > 65536 ? 8 : std::min(a.tile, a.rows)));
-  r.err = ctx_bf16 ? launch_next(join_kernel<bf16>, grid, JOIN_THREADS, 0, st, a, static_cast<bf16*>(ctx), to_log)
-                   : launch_next(join_kernel<float>, grid, JOIN_THREADS, 0, st, a, static_cast<float*>(ctx), to_log);
+  r.err = launch_next(join_kernel, grid, JOIN_THREADS, 0, st, a, ctx);
   if (r.err != cudaSuccess) r.what = "cache4_join";
   return r;
 }

@@ -84,28 +84,33 @@ struct CacheAttn {
 };
 
 LaunchResult cache4_plan(const CacheAttn& a, cudaStream_t st);
-// Joins split items, fills the rows of empty ones. ctx [B * rows][d_c], bf16 or fp32. log2_units: the
-// maxima are in units of log2, else natural.
-LaunchResult cache4_join(const CacheAttn& a, void* ctx, bool ctx_bf16, bool log2_units, cudaStream_t st);
-
-// CUDA cores, any widths: q_lat and ctx in fp32.
+// CUDA cores, any widths: q_lat and ctx in fp32. The join joins split items (maxima in natural units) and
+// fills the rows of empty ones.
 constexpr int kSimtRows = 8, kSimtKeys = 32;
 LaunchResult cache4_simt_qlat(const CacheAttn& a, bool is_bf16, int d_nope, const void* q, const void* W_UK, float* q_lat,
                               cudaStream_t st);
 LaunchResult cache4_simt_attn(const CacheAttn& a, bool is_bf16, int d_nope, const void* q, const float* q_lat, float* ctx,
                               cudaStream_t st);
+LaunchResult cache4_join(const CacheAttn& a, float* ctx, cudaStream_t st);
 LaunchResult cache4_simt_out(const CacheAttn& a, bool is_bf16, int d_v, const float* ctx, const void* W_UV, void* out,
                              cudaStream_t st);
 
-// Tensor cores, bf16 with d_c = 512, d_rope = 64: q_lat and ctx in bf16. The query step makes operands
-// of q_lat and q in cache4_tc_query_bytes of scratch; ctx may then be where q_lat was.
-size_t cache4_tc_query_bytes(long long rows);
-const float* cache4_tc_query_up(const void* query, long long rows);
-LaunchResult cache4_tc_query(const CacheAttn& a, const bf16* q, const bf16* q_lat, void* query, cudaStream_t st);
+// Tensor cores, bf16 with d_c = 512, d_nope = d_v = 128, d_rope = 64: a plan and operands of the queries,
+// the attention (maxima in units of log2, whole items' context normalised in fp32), the joining with the
+// output's product. A row of `query` is 512 fp16 and 64 bf16, times the power of two whose inverse is
+// the row's `up` (NaN: the row's result is).
+struct CacheOperands {
+  uint8_t* query;  // [B * rows][1152]
+  float* up;       // [B * rows]
+  float* ctx;      // [B * rows][512]
+};
+constexpr int kQueryBytes = 1152;
+LaunchResult cache4_tc_prepare(const CacheAttn& a, const bf16* q, const bf16* W_UK, const CacheOperands& x, cudaStream_t st);
 constexpr int kTcRows = 128, kTcKeys = 64;  // tcgen05
-LaunchResult cache4_tc_attn(const CacheAttn& a, const void* query, bf16* ctx, cudaStream_t st);
+LaunchResult cache4_tc_attn(const CacheAttn& a, const CacheOperands& x, cudaStream_t st);
 constexpr int kMmaRows = 16, kMmaKeys = 32;  // mma.sync, for few rows
-LaunchResult cache4_mma_attn(const CacheAttn& a, const uint8_t* query, const float* up, bf16* ctx, cudaStream_t st);
+LaunchResult cache4_mma_attn(const CacheAttn& a, const CacheOperands& x, cudaStream_t st);
+LaunchResult cache4_tc_finish(const CacheAttn& a, const CacheOperands& x, const bf16* W_UV, bf16* out, cudaStream_t st);
 
 #ifdef __CUDACC__
 // The pool's row of position p of sequence b, or -1 where the table has none.
@@ -162,6 +167,62 @@ __device__ __forceinline__ int cache_item_of(const CacheAttn& a, int t) {
     else hi = mid;
   }
   return lo;
+}
+// A row's sum of weights at its end: 0 of a row that sees keys (whose scores were all -inf) is NaN.
+__device__ __forceinline__ float row_sum(float l, int2 seen) {
+  return l == 0.f && seen.x < seen.y ? __int_as_float(0x7fc00000) : l;
+}
+
+// One CTA: the items' intervals of keys, and the running sum of their key tiles.
+template <int THREADS>
+__device__ __forceinline__ void cache4_plan_items(const CacheAttn& a) {
+  __shared__ int sums[32];
+  const int items = a.items(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long room = static_cast<long long>(a.pages.most) * a.cache.page;
+  int before = 0;
+  for (int j0 = 0; j0 < items; j0 += THREADS) {
+    const int j = j0 + threadIdx.x;
+    int tiles = 0;
+    if (j < items) {
+      const int b = j / a.row_tiles, r0 = (j - b * a.row_tiles) * a.tile, r1 = min(r0 + a.tile, a.rows) - 1;
+      int lo = 0x7fffffff, hi = 0;
+      for (int i = r0 / a.n_h; i <= r1 / a.n_h; ++i) {
+        const int2 s = cache_row_bounds(a, b, i);
+        if (s.x >= s.y) continue;
+        lo = min(lo, s.x);
+        hi = max(hi, s.y);
+      }
+      if (hi > room) {  // keys that the table has no room for
+        report_page(a.status, 303);
+        a.hull[j] = make_int2(-1, -1);
+      } else {
+        a.hull[j] = hi > 0 ? make_int2(lo, hi) : make_int2(0, 0);
+        if (hi > 0) tiles = (hi - 1) / a.keys - lo / a.keys + 1;
+      }
+    }
+    int run = tiles;  // inclusive sum over the warp, then over the warps
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, run, m);
+      if (lane >= m) run += o;
+    }
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    if (warp == 0) {
+      int s = lane < THREADS / 32 ? sums[lane] : 0;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, s, m);
+        if (lane >= m) s += o;
+      }
+      sums[lane] = s;
+    }
+    __syncthreads();
+    if (j < items) a.first[j] = before + (warp ? sums[warp - 1] : 0) + run - tiles;
+    before += sums[31];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.first[items] = before;
 }
 #endif
 

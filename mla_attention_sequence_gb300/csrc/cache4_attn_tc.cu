@@ -50,8 +50,7 @@ constexpr uint32_t IDESC_PV = idesc_bf16(BQ, HALF, false, true) & F16;
 
 struct Params {
   CacheAttn a;
-  const float* up;    // [B * rows] what a row's scores are scaled up by; NaN: its result is NaN
-  bf16* ctx;          // [B * rows][512]
+  CacheOperands x;
   float sl2;          // scale * log2(e)
   ModParams mod;      // u_scale, cap_log2
 };
@@ -85,33 +84,6 @@ __device__ __forceinline__ void hold(const CacheAttn& a, const Piece& p, int til
   }
   h.rope[0] = __ldg(r);
   h.rope[1] = __ldg(r + 1);
-}
-
-// The queries as operands: each row's 512 latent values as fp16 and 64 RoPE values as bf16, both times
-// the power of two that brings the row's largest size to 2^8 .. 2^9, and that power's inverse. A row
-// that holds a value that is not finite: zeros, and NaN in the power's place. A warp a row.
-constexpr int QUERY_WARPS = 8;
-__global__ void __launch_bounds__(32 * QUERY_WARPS) cache4_query_kernel(ll rows, const bf16* q_lat, const bf16* q,
-                                                                        uint8_t* out, float* up) {
-  after_previous();
-  const ll row = static_cast<ll>(blockIdx.x) * QUERY_WARPS + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const uint4* src = reinterpret_cast<const uint4*>(q_lat + row * 512);
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint4 v0 = ldg4(src + lane), v1 = ldg4(src + 32 + lane);
-  const uint4 v2 = lane < 8 ? ldg4(reinterpret_cast<const uint4*>(q + row * 192 + 128) + lane) : zero;
-  float top = max3f(size8(v0), size8(v1), size8(v2));
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-  const bool fine = __all_sync(0xffffffffu, finite8(v0) && finite8(v1) && finite8(v2));
-  const int e = fine && top > 0.f ? row_exponent(top) : 0;
-  const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  uint4* to = reinterpret_cast<uint4*>(out + row * (2 * 576));
-  to[lane] = fine ? f16_8(v0, down) : zero;
-  to[32 + lane] = fine ? f16_8(v1, down) : zero;
-  if (lane < 8) to[64 + lane] = fine ? bf16_8(v2, down) : zero;
-  if (lane == 0) up[row] = fine ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __int_as_float(0x7fc00000);
 }
 
 template <int MOD>
@@ -328,7 +300,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         }
         staged = true;
       }
-      const float up = there ? __ldcg(p.up + row) : 1.f;
+      const float up = there ? __ldcg(p.x.up + row) : 1.f;
       bool odd = up != up;  // the row's result is NaN
       if (!pass(q_stage, seg & 1, abort_flag, 425)) { ok = false; break; }
 #pragma unroll 1
@@ -465,49 +437,31 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         else
           a.part_ml[slot + r] = make_float2(m, l);
       }
-      // row by row of the warp's 32, 16 bytes a lane
-      auto put = [&](uint8_t* base, ll row_bytes) {
+      float* out = (whole ? p.x.ctx + row0 * 512 : a.part_o + slot * 512) + vh * HALF;
+      const float by = whole ? inv : 1.f;
+#pragma unroll 1
+      for (int c = 0; c < HALF / 32; ++c) {
+        uint32_t u[32];
+        tmem_ld32(o + c * 32, u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          float4 w;
+          w.x = __uint_as_float(u[4 * v]) * by;
+          w.y = __uint_as_float(u[4 * v + 1]) * by;
+          w.z = __uint_as_float(u[4 * v + 2]) * by;
+          w.w = __uint_as_float(u[4 * v + 3]) * by;
+          *reinterpret_cast<float4*>(stage + sw128_offset(lane, v)) = w;
+        }
+        // row by row of the warp's 32, 16 bytes a lane
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int rr = 4 * i + (lane >> 3);
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + sw128_offset(static_cast<uint32_t>(rr), lane & 7u));
-          if (warp * 32 + rr < pc.rows) *reinterpret_cast<uint4*>(base + (warp * 32 + rr) * row_bytes + 16 * (lane & 7)) = v;
+          const float4 v = *reinterpret_cast<const float4*>(stage + sw128_offset(static_cast<uint32_t>(rr), lane & 7u));
+          if (warp * 32 + rr < pc.rows) *reinterpret_cast<float4*>(out + (warp * 32 + rr) * 512 + c * 32 + 4 * (lane & 7)) = v;
         }
         __syncwarp();
-      };
-      if (whole) {
-        uint8_t* out = reinterpret_cast<uint8_t*>(p.ctx + row0 * 512 + vh * HALF);
-#pragma unroll 1
-        for (int c = 0; c < HALF / 64; ++c) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint32_t u[32];
-            tmem_ld32(o + c * 64 + g * 32, u);
-            tmem_wait_ld();
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16x2(__uint_as_float(u[8 * v + 2 * i]) * inv, __uint_as_float(u[8 * v + 2 * i + 1]) * inv);
-              *reinterpret_cast<uint4*>(stage + sw128_offset(lane, 4 * g + v)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          put(out + 128 * c, 1024);
-        }
-      } else {
-        uint8_t* out = reinterpret_cast<uint8_t*>(a.part_o + slot * 512 + vh * HALF);
-#pragma unroll 1
-        for (int c = 0; c < HALF / 32; ++c) {
-          uint32_t u[32];
-          tmem_ld32(o + c * 32, u);
-          tmem_wait_ld();
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            *reinterpret_cast<uint4*>(stage + sw128_offset(lane, v)) = make_uint4(u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
-          put(out + 128 * c, 2048);
-        }
       }
       LAGA_TRACE_POINT(cache4, 15, n);
       tc_fence_before();  // O has been read before the next piece's products overwrite it (q_full, p_full)
@@ -535,36 +489,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
 
 }  // namespace
 
-size_t cache4_tc_query_bytes(long long rows) { return align_up(static_cast<size_t>(rows) * 576 * 2, 256) + align_up(static_cast<size_t>(rows) * 4, 256); }
-
-const float* cache4_tc_query_up(const void* query, long long rows) {
-  return reinterpret_cast<const float*>(static_cast<const char*>(query) + align_up(static_cast<size_t>(rows) * 576 * 2, 256));
-}
-
-LaunchResult cache4_tc_query(const CacheAttn& a, const bf16* q, const bf16* q_lat, void* query, cudaStream_t st) {
-  const ll rows = static_cast<ll>(a.pages.B) * a.rows;
-  LaunchResult r;
-  r.err = launch_next(cache4_query_kernel, static_cast<unsigned>((rows + QUERY_WARPS - 1) / QUERY_WARPS), 32 * QUERY_WARPS, 0, st,
-                      rows, q_lat, q, static_cast<uint8_t*>(query), const_cast<float*>(cache4_tc_query_up(query, rows)));
-  if (r.err != cudaSuccess) r.what = "cache4_query";
-  return r;
-}
-
-LaunchResult cache4_tc_attn(const CacheAttn& a, const void* query, bf16* ctx, cudaStream_t st) {
+LaunchResult cache4_tc_attn(const CacheAttn& a, const CacheOperands& x, cudaStream_t st) {
   const ll rows = static_cast<ll>(a.pages.B) * a.rows;
   LaunchResult r;
   CUtensorMap mQ;
-  const uint64_t dims[2] = {576, static_cast<uint64_t>(rows)}, strides[1] = {576 * 2};
+  const uint64_t dims[2] = {kQueryBytes / 2, static_cast<uint64_t>(rows)}, strides[1] = {kQueryBytes};
   const uint32_t box[2] = {64, BQ};
-  r.cu = make_tmap(&mQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, query, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  r.cu = make_tmap(&mQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x.query, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!r.ok()) {
     r.what = "tensor map cache4 queries";
     return r;
   }
   Params p{};
   p.a = a;
-  p.up = cache4_tc_query_up(query, rows);
-  p.ctx = ctx;
+  p.x = x;
   p.sl2 = a.scale * 1.4426950408889634f;
   Dims d{};
   d.scale = a.scale;

@@ -76,20 +76,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Eight bf16 values times `by`, as fp16 or (exactly, by a power of two) as bf16; their largest size.
-__device__ __forceinline__ uint4 f16_8(uint4 v, float by) {
-  return make_uint4(pack_f16x2(bf16_lo(v.x) * by, bf16_hi(v.x) * by), pack_f16x2(bf16_lo(v.y) * by, bf16_hi(v.y) * by),
-                    pack_f16x2(bf16_lo(v.z) * by, bf16_hi(v.z) * by), pack_f16x2(bf16_lo(v.w) * by, bf16_hi(v.w) * by));
-}
-__device__ __forceinline__ uint4 bf16_8(uint4 v, float by) {
-  return make_uint4(pack_bf16x2(bf16_lo(v.x) * by, bf16_hi(v.x) * by), pack_bf16x2(bf16_lo(v.y) * by, bf16_hi(v.y) * by),
-                    pack_bf16x2(bf16_lo(v.z) * by, bf16_hi(v.z) * by), pack_bf16x2(bf16_lo(v.w) * by, bf16_hi(v.w) * by));
-}
-__device__ __forceinline__ float size8(uint4 v) {
-  const float a = max3f(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x)), fabsf(bf16_lo(v.y)));
-  const float b = max3f(fabsf(bf16_hi(v.y)), fabsf(bf16_lo(v.z)), fabsf(bf16_hi(v.z)));
-  return max3f(fmaxf(a, b), fabsf(bf16_lo(v.w)), fabsf(bf16_hi(v.w)));
-}
 // 2^-e brings a row's largest size to between 2^8 and 2^9 (within what a power of two can).
 __device__ __forceinline__ int row_exponent(float top) {
   return min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 8, -118), 118);
@@ -125,6 +111,21 @@ __device__ __forceinline__ bool pass(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));

@@ -84,8 +84,8 @@ struct AttnSizes {
   CacheAttn a;
   int d_nope, d_v;
   bool tc, few;  // tensor cores; mma.sync's form of them
-  size_t items_bytes, hull_bytes, lat_bytes, query_bytes, ml_bytes, o_bytes;  // lat: q_lat, and the context over it
-  size_t total() const { return items_bytes + hull_bytes + lat_bytes + query_bytes + ml_bytes + o_bytes; }
+  size_t items_bytes, hull_bytes, query_bytes, up_bytes, ctx_bytes, ml_bytes, o_bytes;
+  size_t total() const { return items_bytes + hull_bytes + query_bytes + up_bytes + ctx_bytes + ml_bytes + o_bytes; }
 };
 
 laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cache, bool sizes_only, AttnSizes* s) {
@@ -131,9 +131,10 @@ laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cach
     return fail(LAGA_ERR_UNSUPPORTED, "cache attention: problem too large (rows times the table's room)%s");
   s->items_bytes = align_up((items + 1) * sizeof(int), 256);
   s->hull_bytes = align_up(items * sizeof(int2), 256);
-  s->lat_bytes = align_up(static_cast<size_t>(a.pages.B) * a.rows * a.cache.d_c * (s->tc ? 2 : 4), 256);
-  // CUDA cores: the context in a place of its own, since other CTAs still read the rows' queries
-  s->query_bytes = s->tc ? cache4_tc_query_bytes(static_cast<int64_t>(a.pages.B) * a.rows) : s->lat_bytes;
+  const size_t rows = static_cast<size_t>(a.pages.B) * a.rows;
+  s->ctx_bytes = align_up(rows * a.cache.d_c * 4, 256);
+  s->query_bytes = s->tc ? align_up(rows * kQueryBytes, 256) : s->ctx_bytes;  // CUDA cores: q_lat in fp32
+  s->up_bytes = s->tc ? align_up(rows * 4, 256) : 0;
   s->ml_bytes = align_up(static_cast<size_t>(2) * a.parts * a.tile * sizeof(float2), 256);
   s->o_bytes = align_up(static_cast<size_t>(2) * a.parts * a.tile * a.cache.d_c * 4, 256);
   return LAGA_OK;
@@ -284,42 +285,28 @@ laga_status laga_mla_cache4_fwd(const laga_mla_cache4_desc* desc, const laga_mla
   };
   a.first = reinterpret_cast<int*>(take(z.items_bytes));
   a.hull = reinterpret_cast<int2*>(take(z.hull_bytes));
-  char* lat = take(z.lat_bytes);
-  char* query = take(z.query_bytes);
+  CacheOperands x;
+  x.query = reinterpret_cast<uint8_t*>(take(z.query_bytes));
+  x.up = reinterpret_cast<float*>(take(z.up_bytes));
+  x.ctx = reinterpret_cast<float*>(take(z.ctx_bytes));
   a.part_ml = reinterpret_cast<float2*>(take(z.ml_bytes));
   a.part_o = reinterpret_cast<float*>(take(z.o_bytes));
   const bool b16 = a.cache.is_bf16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  LaunchResult r = timed("cache4_plan", s, [&] { return cache4_plan(a, s); });
+  LaunchResult r;
   if (z.tc) {
     auto cb = [](const void* p) { return static_cast<const bf16*>(p); };
-    bf16* q_lat = reinterpret_cast<bf16*>(lat);
-    bf16* c = q_lat;
-    Dims d{};
-    d.B = 1;
-    d.Sq = a.pages.B * a.Sq;
-    d.n_h = a.n_h;
-    d.d_c = 512;
-    d.d_nope = d.d_v = 128;
-    d.d_rope = 64;
-    if (r.ok()) r = timed("cache4_qlat", s, [&] { return tc_absorbed_qlat(d, cb(q), cb(W_UK), q_lat, s); });
-    if (r.ok()) r = timed("cache4_query", s, [&] { return cache4_tc_query(a, cb(q), q_lat, query, s); });
-    if (r.ok())
-      r = timed("cache4_attn", s, [&] {
-        if (!z.few) return cache4_tc_attn(a, query, c, s);
-        return cache4_mma_attn(a, reinterpret_cast<const uint8_t*>(query),
-                               cache4_tc_query_up(query, static_cast<long long>(a.pages.B) * a.rows), c, s);
-      });
-    if (r.ok()) r = timed("cache4_join", s, [&] { return cache4_join(a, c, true, true, s); });
-    if (r.ok()) r = timed("cache4_out", s, [&] { return tc_absorbed_outproj(d, c, cb(W_UV), static_cast<bf16*>(out), s); });
+    r = timed("cache4_prepare", s, [&] { return cache4_tc_prepare(a, cb(q), cb(W_UK), x, s); });
+    if (r.ok()) r = timed("cache4_attn", s, [&] { return z.few ? cache4_mma_attn(a, x, s) : cache4_tc_attn(a, x, s); });
+    if (r.ok()) r = timed("cache4_finish", s, [&] { return cache4_tc_finish(a, x, cb(W_UV), static_cast<bf16*>(out), s); });
     return from_launch(r);
   }
-  float* q_lat = reinterpret_cast<float*>(lat);
-  float* c = reinterpret_cast<float*>(query);
+  float* q_lat = reinterpret_cast<float*>(x.query);
+  r = timed("cache4_plan", s, [&] { return cache4_plan(a, s); });
   if (r.ok()) r = timed("cache4_qlat", s, [&] { return cache4_simt_qlat(a, b16, z.d_nope, q, W_UK, q_lat, s); });
-  if (r.ok()) r = timed("cache4_attn", s, [&] { return cache4_simt_attn(a, b16, z.d_nope, q, q_lat, c, s); });
-  if (r.ok()) r = timed("cache4_join", s, [&] { return cache4_join(a, c, false, false, s); });
-  if (r.ok()) r = timed("cache4_out", s, [&] { return cache4_simt_out(a, b16, z.d_v, c, W_UV, out, s); });
+  if (r.ok()) r = timed("cache4_attn", s, [&] { return cache4_simt_attn(a, b16, z.d_nope, q, q_lat, x.ctx, s); });
+  if (r.ok()) r = timed("cache4_join", s, [&] { return cache4_join(a, x.ctx, s); });
+  if (r.ok()) r = timed("cache4_out", s, [&] { return cache4_simt_out(a, b16, z.d_v, x.ctx, W_UV, out, s); });
   return from_launch(r);
 }
 
