@@ -17,9 +17,8 @@
 // N = 64 step, 128 bytes a cycle).
 //
 // Warp roles (416 threads): warps 0..3 load the queries (TMA; what goes to TMEM by way of the place of
-// what stays) and do the softmax, one row a thread (their TMEM lanes); warp 4 allocates TMEM and issues the MMAs; warps 5..12 expand the key tiles: a lane has
-// a block of 16 values of one key (two keys' four blocks make eight lanes' stores hit eight different
-// 16-byte columns of the swizzled rows), and loads the next tile's bytes before it works on this one's.
+// what stays) and do the softmax, one row a thread (their TMEM lanes); warp 4 allocates TMEM and issues the MMAs; warps 5..12 expand the key tiles, four lanes a key,
+// and load the next tile's bytes before they work on this one's.
 // The boxes that the context's product does not read are refilled as soon as the scores are done.
 // TMEM columns: query [0,128), S [128,192) and [192,256) in turn, P over its S, O [256,512).
 #include "cache4.h"
@@ -56,13 +55,14 @@ struct Params {
 };
 
 
-// What a producer lane holds of one key tile: its block of 16 values in each of the eight latent boxes
-// (first the four outside this CTA's half of the values), eight of the key's 32 scales (its neighbours
-// have the others), two of its eight RoPE chunks.
+// What a producer lane holds of one key tile: of each two latent boxes (first the two pairs outside this
+// CTA's half of the values) 16 bytes of codes, two blocks; eight of the key's 32 scales (its neighbours
+// have the others); two of the key's eight RoPE chunks. Few wide loads: every load of a warp touches eight
+// keys' lines, and with a load a block and a scale (18 instead of 7) they and the stores behind them took
+// longer than the products.
 struct Held {
-  uint2 codes[8];
-  uint32_t scales[8];
-  uint4 rope[2];
+  uint4 codes[4], rope[2];
+  uint2 scales;
   bool live, bad;  // a key to expand (else zeros); a key that should be there and is not
 };
 __device__ __forceinline__ void hold(const CacheAttn& a, const Piece& p, int tile, int key, int lane4, int vh, Held& h) {
@@ -72,18 +72,59 @@ __device__ __forceinline__ void hold(const CacheAttn& a, const Piece& p, int til
   const ll slot = cache_slot_of(a.cache, a.pages, p.b, wanted ? at : p.hull.x, &there);
   h.live = wanted && there;
   h.bad = wanted && !there;
-  const uint2* c = reinterpret_cast<const uint2*>(a.cache.codes + slot * 256) + lane4;
-  const uint8_t* s = a.cache.scales + slot * 32 + lane4;
+  const uint4* c = reinterpret_cast<const uint4*>(a.cache.codes + slot * 256) + lane4;
   const uint4* r = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.cache.keys) + slot * 64) + 2 * lane4;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    h.codes[k] = __ldg(c + 16 * (1 - vh) + 4 * k);
-    h.codes[4 + k] = __ldg(c + 16 * vh + 4 * k);
-    h.scales[k] = __ldg(s + 16 * (1 - vh) + 4 * k);
-    h.scales[4 + k] = __ldg(s + 16 * vh + 4 * k);
+  for (int k = 0; k < 2; ++k) {
+    h.codes[k] = __ldg(c + 4 * (2 * (1 - vh) + k));
+    h.codes[2 + k] = __ldg(c + 4 * (2 * vh + k));
   }
+  h.scales = __ldg(reinterpret_cast<const uint2*>(a.cache.scales + slot * 32) + lane4);
   h.rope[0] = __ldg(r);
   h.rope[1] = __ldg(r + 1);
+}
+
+// Shared-memory descriptors differ in their low words alone (the address, and for MN-major tiles the
+// distance of their atoms): blocks of four K16 steps take those, so that an MMA costs its warp the fewest
+// instructions. With whole descriptors added up outside, a box of four took ~300 cycles to issue beside
+// the other roles, twice what it takes to run.
+constexpr uint32_t DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(const void* at, uint32_t lbo) { return (smem_u32(at) >> 4) | ((lbo >> 4) << 16); }
+// D (+)= A B over four steps; a, b: low words, `b_step` between the steps of b (A's are 2, or 8 TMEM columns).
+template <bool A_TMEM, uint32_t B_STEP>
+__device__ __forceinline__ void mma4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (A_TMEM)
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 v;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 t, %3, %3;\n\t"
+        "mov.b64 v, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], v, %3, p;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, %6;\n\tmov.b64 v, {y, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], v, %3, t;\n\t"
+        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, %7;\n\tmov.b64 v, {y, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], v, %3, t;\n\t"
+        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, %8;\n\tmov.b64 v, {y, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], v, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(DESC_HIGH), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 u, v;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 t, %3, %3;\n\t"
+        "mov.b64 u, {%1, %5};\n\tmov.b64 v, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, p;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, %6;\n\tmov.b64 u, {x, %5};\n\tmov.b64 v, {y, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, t;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, %7;\n\tmov.b64 u, {x, %5};\n\tmov.b64 v, {y, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, t;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, %8;\n\tmov.b64 u, {x, %5};\n\tmov.b64 v, {y, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(DESC_HIGH), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)
+        : "memory");
 }
 
 template <int MOD>
@@ -148,7 +189,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
     // ---------------- expand key tiles
     const int pw = warp - MMA_WARP - 1, key = 8 * pw + (lane >> 2), b4 = lane & 3;
     const uint32_t row = static_cast<uint32_t>(key);
-    const uint32_t off0 = sw128_offset(row, 2 * b4), off1 = sw128_offset(row, 2 * b4 + 1);
+    const uint32_t off0 = sw128_offset(row, 2 * b4), off1 = sw128_offset(row, 2 * b4 + 1);  // RoPE chunks
+    const uint32_t chunk = 4 * (b4 & 1) + (b4 & 2);
+    const uint32_t offs[4] = {sw128_offset(row, chunk), sw128_offset(row, chunk + 1), sw128_offset(row, chunk ^ 2),
+                              sw128_offset(row, (chunk ^ 2) + 1)};
     int n = 0;
     bool ok = true, more = walk.next(pc);
     int j = 0;
@@ -167,20 +211,29 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
       const uint32_t ph = static_cast<uint32_t>(((n >> 1) & 1) ^ 1);
       uint8_t* k = sK + buf * K_BYTES;
       bool fine = !cur.bad;
-      // The held block i, of box c. A block that reads as NaN: zeros here, and every row that sees the
-      // key gets NaN.
-      auto box = [&](int i, int c) {
-        const uint32_t e = cur.scales[i];
-        const bool number = e <= kCacheTopScale;
-        const uint32_t s = number && cur.live ? e * 0x800080u : 0u;
-        fine = fine && (number || !cur.live);
-        *reinterpret_cast<uint4*>(k + c * KBOX + off0) = expand8(cur.codes[i].x, s);
-        *reinterpret_cast<uint4*>(k + c * KBOX + off1) = expand8(cur.codes[i].y, s);
+      // The held pair j, boxes 2 i and 2 i + 1: a lane's two blocks are a half of a box's row, its upper
+      // lanes' in the other order, so that eight lanes (two keys) store to eight different 16-byte columns.
+      // A block that reads as NaN: zeros here, and every row that sees the key gets NaN.
+      auto boxes = [&](int j, int i) {
+        const uint32_t x = __shfl_sync(0xffffffffu, cur.scales.x, (lane & ~3) | i);
+        const uint32_t y = __shfl_sync(0xffffffffu, cur.scales.y, (lane & ~3) | i);
+        const uint32_t two = ((b4 & 2) ? y : x) >> (16 * (b4 & 1));
+        const bool turned = (b4 & 2) != 0;
+        const uint32_t e0 = (turned ? two >> 8 : two) & 0xffu, e1 = (turned ? two : two >> 8) & 0xffu;
+        const uint4 w = cur.codes[j];
+        const bool n0 = e0 <= kCacheTopScale, n1 = e1 <= kCacheTopScale;
+        fine = fine && ((n0 && n1) || !cur.live);
+        const uint32_t s0 = n0 && cur.live ? e0 * 0x800080u : 0u, s1 = n1 && cur.live ? e1 * 0x800080u : 0u;
+        uint8_t* to = k + (2 * i + (b4 >> 1)) * KBOX;
+        *reinterpret_cast<uint4*>(to + offs[0]) = expand8(turned ? w.z : w.x, s0);
+        *reinterpret_cast<uint4*>(to + offs[1]) = expand8(turned ? w.w : w.y, s0);
+        *reinterpret_cast<uint4*>(to + offs[2]) = expand8(turned ? w.x : w.z, s1);
+        *reinterpret_cast<uint4*>(to + offs[3]) = expand8(turned ? w.y : w.w, s1);
       };
       if (!pass(&ka_free[buf], ph, abort_flag, 401)) break;
       LAGA_TRACE_POINT(cache4, 1, n);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) box(i, 4 * (1 - vh) + i);
+      boxes(0, 2 * (1 - vh));
+      boxes(1, 2 * (1 - vh) + 1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const bool number = finite8(cur.rope[i]);
@@ -195,8 +248,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
       LAGA_TRACE_POINT(cache4, 2, n);
       if (!pass(&kb_free[buf], ph, abort_flag, 402)) break;
       LAGA_TRACE_POINT(cache4, 3, n);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) box(4 + i, 4 * vh + i);
+      boxes(2, 2 * vh);
+      boxes(3, 2 * vh + 1);
       const uint32_t odd = ~__ballot_sync(0xffffffffu, fine);  // four lanes a key
       if (lane == 0) {
         uint32_t bits = 0;
@@ -214,34 +267,29 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
   } else if (warp == MMA_WARP) {
     // ---------------- products
     bool ok = true, issued = false;
-    const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint32_t q_low = desc_low(sQ, 16), k_low = desc_low(sK, 16), v_low = desc_low(sK + vh * 4 * KBOX, KBOX);
     int n = 0, seg = 0;
     auto context = [&](int m, bool first) -> bool {  // O (+)= P(m) V(m)
       if (!pass(p_full, m & 1, abort_flag, 411)) return false;
       LAGA_TRACE_POINT(cache4, 7, m);
       tc_fence_after();
-      const uint64_t v = sdesc_sw128(smem_u32(sK + (m & 1) * K_BYTES + vh * 4 * KBOX), KBOX, 1024);
-      const uint32_t pp = tmem + COL_S + (m & 1) * BKV;
-      mma4_ts_warp(tmem + COL_O, pp, pp + 8, pp + 16, pp + 24, v, v + (2048 >> 4), v + (4096 >> 4), v + (6144 >> 4), IDESC_PV,
-                   first ? 0u : 1u);
+      mma4<true, 2048 / 16>(tmem + COL_O, tmem + COL_S + (m & 1) * BKV, v_low + (m & 1) * (K_BYTES / 16), IDESC_PV, first ? 0u : 1u);
       mma_commit_warp(&kb_free[m & 1]);
       mma_commit_warp(pv_done);
       return true;
     };
-    // S (+)= Q K^T over boxes [c0, c1). Loops, not straight code: the four roles' instructions together
-    // outgrow the instruction cache otherwise.
-    auto scores = [&](uint32_t s, uint64_t kd, int c0, int c1, bool fresh) {
-#pragma unroll 1
-      for (int c = c0; c < c1; ++c) {
-        const uint64_t k = kd + ((c * KBOX) >> 4);
-        if (c < Q_TMEM) {
-          const uint32_t q = tmem + 32 * c;
-          mma4_ts_warp(s, q, q + 8, q + 16, q + 24, k, k + 2, k + 4, k + 6, IDESC_S, fresh && c == c0 ? 0u : 1u);
-        } else {
-          const uint64_t q = q_desc + (((c - Q_TMEM) * QBOX) >> 4);
-          mma4_ss_warp(s, q, q + 2, q + 4, q + 6, k, k + 2, k + 4, k + 6, c == 8 ? IDESC_ROPE : IDESC_S, fresh && c == c0 ? 0u : 1u);
-        }
-      }
+    // S (+)= Q K^T over four latent boxes: those in TMEM (0 .. 3), those in shared memory, the RoPE box.
+    auto low_boxes = [&](uint32_t s, uint32_t k, uint32_t accumulate) {
+#pragma unroll
+      for (int c = 0; c < Q_TMEM; ++c) mma4<true, 2>(s, tmem + 32 * c, k + c * (KBOX / 16), IDESC_S, c ? 1u : accumulate);
+    };
+    auto high_boxes = [&](uint32_t s, uint32_t k, uint32_t accumulate) {
+#pragma unroll
+      for (int c = Q_TMEM; c < 8; ++c)
+        mma4<false, 2>(s, q_low + (c - Q_TMEM) * (QBOX / 16), k + c * (KBOX / 16), IDESC_S, c > Q_TMEM ? 1u : accumulate);
+    };
+    auto rope_box = [&](uint32_t s, uint32_t k) {
+      mma4<false, 2>(s, q_low + (8 - Q_TMEM) * (QBOX / 16), k + 8 * (KBOX / 16), IDESC_ROPE, 1u);
     };
     while (ok && walk.next(pc)) {
       ok = pass(q_full, seg & 1, abort_flag, 412) && pass(q_rest, seg & 1, abort_flag, 416);
@@ -254,10 +302,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         if (!ok) break;
         tc_fence_after();
         LAGA_TRACE_POINT(cache4, 5, n);
-        const uint64_t kd = sdesc_sw128(smem_u32(sK + (n & 1) * K_BYTES), 16, 1024);
-        const uint32_t s = tmem + COL_S + (n & 1) * BKV;
-        scores(s, kd, 4 * (1 - vh), 4 * (1 - vh) + 4, true);
-        scores(s, kd, 8, 9, false);
+        const uint32_t s = tmem + COL_S + (n & 1) * BKV, k = k_low + (n & 1) * (K_BYTES / 16);
+        if (vh)
+          low_boxes(s, k, 0u);
+        else
+          high_boxes(s, k, 0u);
+        rope_box(s, k);
         issued = true;
         LAGA_TRACE_POINT(cache4, 6, n);
         if (j > 0 && !(ok = context(n - 1, j == 1))) break;
@@ -265,7 +315,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         if (!ok) break;
         tc_fence_after();
         LAGA_TRACE_POINT(cache4, 11, n);
-        scores(s, kd, 4 * vh, 4 * vh + 4, false);
+        if (vh)
+          high_boxes(s, k, 1u);
+        else
+          low_boxes(s, k, 1u);
         mma_commit_warp(&ka_free[n & 1]);
         mma_commit_warp(s_full);
         LAGA_TRACE_POINT(cache4, 12, n);

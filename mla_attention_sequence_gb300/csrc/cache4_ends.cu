@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(THREADS, 1) prepare_kernel(const CacheAttn a, 
 // the output's columns [16 (w % 8), ..) over half w / 8 of the latent columns.
 constexpr int A_STRIDE = 520;  // bf16 values: rows fall into different banks
 constexpr int FINISH_SMEM = 2 * TOKENS * A_STRIDE * 2;
+static_assert(FINISH_SMEM >= WARPS * 512 * 4, "the warps' sums fit");
 __global__ void __launch_bounds__(THREADS, 1) finish_kernel(const CacheAttn a, int tokens, const CacheOperands x, const bf16* W,
                                                             bf16* out) {
   __shared__ __align__(16) uint8_t smem[FINISH_SMEM];
@@ -138,8 +139,10 @@ __global__ void __launch_bounds__(THREADS, 1) finish_kernel(const CacheAttn a, i
     for (int i = 0; i < 2; ++i)
       w[k][i] = __ldg(reinterpret_cast<const uint2*>(W + static_cast<ll>(c0 + 16 * k + 8 * i + g) * a.n_h * 128 + h * 128 + v0 + 4 * t4));
   after_previous();
-  // ---- the context of this warp's token: 4 columns at 4 lane + 128 j
-  const int token = t0 + warp;
+  // ---- the context of this warp's token: 4 columns at 4 lane + 128 j. Where the tokens are few, several
+  // warps share a token's pieces (warp `sub` of `shared` takes every `shared`th).
+  const int here = min(TOKENS, tokens - t0), shared = here > 8 ? 1 : here > 4 ? 2 : here > 2 ? 4 : here > 1 ? 8 : 16;
+  const int token = t0 + warp / shared, sub = warp % shared;
   float4 c[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) c[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -155,10 +158,13 @@ __global__ void __launch_bounds__(THREADS, 1) finish_kernel(const CacheAttn a, i
 #pragma unroll
       for (int j = 0; j < 4; ++j) c[j] = make_float4(v, v, v, v);
       if (lane == 0) *lse = v != v ? v : -INFINITY;
+      if (sub > 0) c[0] = c[1] = c[2] = c[3] = make_float4(0.f, 0.f, 0.f, 0.f);
     } else if (p0 == p1) {  // one part had it all
-      const float4* from = reinterpret_cast<const float4*>(x.ctx + (static_cast<ll>(token) * a.n_h + h) * 512) + lane;
+      if (sub == 0) {
+        const float4* from = reinterpret_cast<const float4*>(x.ctx + (static_cast<ll>(token) * a.n_h + h) * 512) + lane;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = __ldcg(from + 32 * j);
+        for (int j = 0; j < 4; ++j) c[j] = __ldcg(from + 32 * j);
+      }
     } else {
       // piece k is part p0 + k's; the first began the item
       const int pieces = p1 - p0 + 1;
@@ -175,13 +181,14 @@ __global__ void __launch_bounds__(THREADS, 1) finish_kernel(const CacheAttn a, i
       l = row_sum(l, cache_row_bounds(a, y.b, y.i));
       const float from = m == -INFINITY ? 0.f : m, inv = l != l ? l : l == 0.f ? 0.f : 1.f / l;
       if (lane == 0) *lse = l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
-      for (int k0 = 0; k0 < pieces; k0 += 32) {
-        const float mine = k0 + lane < pieces ? exp2f(__ldcg(a.part_ml + slot(k0 + lane)).x - from) * inv : 0.f;
-        const int n = min(32, pieces - k0);
+      for (int k0 = sub; k0 < pieces; k0 += 32 * shared) {
+        const int at = k0 + lane * shared;
+        const float mine = at < pieces ? exp2f(__ldcg(a.part_ml + slot(at)).x - from) * inv : 0.f;
+        const int n = min(32, (pieces - k0 + shared - 1) / shared);
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
           const float by = __shfl_sync(0xffffffffu, mine, k);
-          const float4* o = reinterpret_cast<const float4*>(a.part_o + slot(k0 + k) * 512) + lane;
+          const float4* o = reinterpret_cast<const float4*>(a.part_o + slot(k0 + k * shared) * 512) + lane;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float4 v = __ldcg(o + 32 * j);
@@ -194,13 +201,32 @@ __global__ void __launch_bounds__(THREADS, 1) finish_kernel(const CacheAttn a, i
       }
     }
   }
+  if (shared > 1) {  // the warps' sums, in their order
+    float4* sums = reinterpret_cast<float4*>(smem);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[warp * 128 + 32 * j + lane] = c[j];
+    __syncthreads();
+    if (sub == 0)
+      for (int k = 1; k < shared; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 v = sums[(warp + k) * 128 + 32 * j + lane];
+          c[j].x += v.x;
+          c[j].y += v.y;
+          c[j].z += v.z;
+          c[j].w += v.w;
+        }
+    __syncthreads();
+  }
+  if (sub == 0) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint2 first = make_uint2(pack_bf16x2(c[j].x, c[j].y), pack_bf16x2(c[j].z, c[j].w));
     const uint2 second = make_uint2(pack_bf16x2(c[j].x - bf16_lo(first.x), c[j].y - bf16_hi(first.x)),
                                     pack_bf16x2(c[j].z - bf16_lo(first.y), c[j].w - bf16_hi(first.y)));
-    *reinterpret_cast<uint2*>(hi + warp * A_STRIDE + 128 * j + 4 * lane) = first;
-    *reinterpret_cast<uint2*>(lo + warp * A_STRIDE + 128 * j + 4 * lane) = second;
+    *reinterpret_cast<uint2*>(hi + (warp / shared) * A_STRIDE + 128 * j + 4 * lane) = first;
+    *reinterpret_cast<uint2*>(lo + (warp / shared) * A_STRIDE + 128 * j + 4 * lane) = second;
+  }
   }
   __syncthreads();
   // ---- times the weights
