@@ -10,15 +10,17 @@
 //
 // One CTA per (part of the key tiles, half of the context's columns): TMEM cannot hold 128 x 512 fp32
 // context columns beside the scores, so both halves of a part compute the scores. Of the query tile
-// (nine [128 x 64] boxes, 144 KB) four boxes stay in TMEM as the A operand and five in shared memory,
+// (nine [128 x 64] boxes, 144 KB) the four of this half's values stay in TMEM as the A operand and five in
+// shared memory,
 // which leaves room there for two key tiles of 64 (nine [64 x 64] boxes, 72 KB each): one is being
 // expanded while the other is read by the products. With the query all in shared memory only one
 // would fit, and reading A from there would bound the products (6 KB for every 32 cycles of an
 // N = 64 step, 128 bytes a cycle).
 //
-// Warp roles (416 threads): warps 0..3 load the queries (TMA; what goes to TMEM by way of the place of
-// what stays) and do the softmax, one row a thread (their TMEM lanes); warp 4 allocates TMEM and issues the MMAs; warps 5..12 expand the key tiles, four lanes a key,
-// and load the next tile's bytes before they work on this one's.
+// Warp roles: warps 0..3 load the queries (TMA; what goes to TMEM by way of the place of
+// what stays) and do the softmax, one row a thread (their TMEM lanes); warp 4 allocates TMEM and issues the MMAs; eight of the others expand the key tiles, four lanes a
+// key, and load the next tile's bytes before they work on this one's. None of those is on the MMA warp's
+// scheduler (warps 4 k): two of them there were late by half a tile, and every product with them.
 // The boxes that the context's product does not read are refilled as soon as the scores are done.
 // TMEM columns: query [0,128), S [128,192) and [192,256) in turn, P over its S, O [256,512).
 #include "cache4.h"
@@ -38,7 +40,7 @@ constexpr int Q_BYTES = (NBOX - Q_TMEM) * QBOX;
 constexpr int SMEM_BYTES = 2 * K_BYTES + Q_BYTES + 1024 + 256;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 constexpr int SOFTMAX_WARPS = 4, PRODUCER_WARPS = 8, MMA_WARP = 4;
-constexpr int NTHREADS = 32 * (SOFTMAX_WARPS + 1 + PRODUCER_WARPS);
+constexpr int NTHREADS = 512;  // warps 8, 12 and 15 have no work
 constexpr uint32_t TMEM_COLS = 512, COL_S = 128, COL_O = 256;
 constexpr int HALF = 256;
 // kind::f16 with fp16 operands is idesc_bf16 without the two type fields
@@ -56,13 +58,13 @@ struct Params {
 
 
 // What a producer lane holds of one key tile: of each two latent boxes (first the two pairs outside this
-// CTA's half of the values) 16 bytes of codes, two blocks; eight of the key's 32 scales (its neighbours
-// have the others); two of the key's eight RoPE chunks. Few wide loads: every load of a warp touches eight
-// keys' lines, and with a load a block and a scale (18 instead of 7) they and the stores behind them took
+// CTA's half of the values) 16 bytes of codes, two blocks, and their scales; two of the key's eight RoPE
+// chunks. Few wide loads: every load of a warp touches eight
+// keys' lines, and with a load a block and a scale (18 instead of 10) they and the stores behind them took
 // longer than the products.
 struct Held {
   uint4 codes[4], rope[2];
-  uint2 scales;
+  uint32_t scales[4];
   bool live, bad;  // a key to expand (else zeros); a key that should be there and is not
 };
 __device__ __forceinline__ void hold(const CacheAttn& a, const Piece& p, int tile, int key, int lane4, int vh, Held& h) {
@@ -73,13 +75,15 @@ __device__ __forceinline__ void hold(const CacheAttn& a, const Piece& p, int til
   h.live = wanted && there;
   h.bad = wanted && !there;
   const uint4* c = reinterpret_cast<const uint4*>(a.cache.codes + slot * 256) + lane4;
+  const uint16_t* s = reinterpret_cast<const uint16_t*>(a.cache.scales + slot * 32) + lane4;
   const uint4* r = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.cache.keys) + slot * 64) + 2 * lane4;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     h.codes[k] = __ldg(c + 4 * (2 * (1 - vh) + k));
     h.codes[2 + k] = __ldg(c + 4 * (2 * vh + k));
+    h.scales[k] = __ldg(s + 4 * (2 * (1 - vh) + k));
+    h.scales[2 + k] = __ldg(s + 4 * (2 * vh + k));
   }
-  h.scales = __ldg(reinterpret_cast<const uint2*>(a.cache.scales + slot * 32) + lane4);
   h.rope[0] = __ldg(r);
   h.rope[1] = __ldg(r + 1);
 }
@@ -127,6 +131,14 @@ __device__ __forceinline__ void mma4(uint32_t d, uint32_t a, uint32_t b, uint32_
         : "memory");
 }
 
+// A bit for each four lanes of which some bit is set.
+__device__ __forceinline__ uint32_t keys_of(uint32_t lanes) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bits |= ((lanes >> (4 * i)) & 15u) ? 1u << i : 0u;
+  return bits;
+}
+
 template <int MOD>
 __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_constant__ CUtensorMap mQ, const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -144,10 +156,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
   uint64_t* pv_done = bars + 9;   // P read, O up to date
   uint64_t* q_full = bars + 10;   // the TMEM boxes are there
   uint64_t* q_stage = bars + 7;   // they are in shared memory
-  uint64_t* q_rest = bars + 17;   // the other boxes are there
-  uint64_t* q_idle = bars + 18;   // the softmax warps are done with the queries' place
+  uint64_t* q_rest = bars + 14;   // the other boxes are there
+  uint64_t* q_idle = bars + 15;   // the softmax warps are done with the queries' place
   uint64_t* drain = bars + 11;
-  uint8_t* bad = reinterpret_cast<uint8_t*>(bars + 14);  // [2][8] a bit a key: it does not count as finite
+  uint32_t* bad = reinterpret_cast<uint32_t*>(bars + 20);  // [2][8] of each expanding warp: lanes whose key does not count as finite
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -187,24 +199,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
   Piece pc;
   if (warp > MMA_WARP) {
     // ---------------- expand key tiles
-    const int pw = warp - MMA_WARP - 1, key = 8 * pw + (lane >> 2), b4 = lane & 3;
+    const int pw = warp - 5 - (warp > 8) - (warp > 12), key = 8 * pw + (lane >> 2), b4 = lane & 3;
     const uint32_t row = static_cast<uint32_t>(key);
     const uint32_t off0 = sw128_offset(row, 2 * b4), off1 = sw128_offset(row, 2 * b4 + 1);  // RoPE chunks
+    const bool turned = (b4 & 2) != 0;
+    const uint32_t pick = turned ? 0x4441u : 0x4440u;  // the first stored block's scale; the other's with bit 0 turned
     const uint32_t chunk = 4 * (b4 & 1) + (b4 & 2);
     const uint32_t offs[4] = {sw128_offset(row, chunk), sw128_offset(row, chunk + 1), sw128_offset(row, chunk ^ 2),
                               sw128_offset(row, (chunk ^ 2) + 1)};
     int n = 0;
-    bool ok = true, more = walk.next(pc);
+    bool ok = true, more = warp % 4 != 0 && warp < 15 && walk.next(pc);
     int j = 0;
     Held cur;
     if (more) hold(a, pc, 0, key, b4, vh, cur);
     while (more && ok) {
-      Held nxt;
-      if (++j == pc.tiles) {
-        j = 0;
-        more = walk.next(pc);
-      }
-      if (more) hold(a, pc, j, key, b4, vh, nxt);
       LAGA_TRACE_POINT(cache4, 0, n);
       if (cur.bad && b4 == 0) report_page(a.status, 305);
       const int buf = n & 1;
@@ -214,54 +222,69 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
       // The held pair j, boxes 2 i and 2 i + 1: a lane's two blocks are a half of a box's row, its upper
       // lanes' in the other order, so that eight lanes (two keys) store to eight different 16-byte columns.
       // A block that reads as NaN: zeros here, and every row that sees the key gets NaN.
-      auto boxes = [&](int j, int i) {
-        const uint32_t x = __shfl_sync(0xffffffffu, cur.scales.x, (lane & ~3) | i);
-        const uint32_t y = __shfl_sync(0xffffffffu, cur.scales.y, (lane & ~3) | i);
-        const uint32_t two = ((b4 & 2) ? y : x) >> (16 * (b4 & 1));
-        const bool turned = (b4 & 2) != 0;
-        const uint32_t e0 = (turned ? two >> 8 : two) & 0xffu, e1 = (turned ? two : two >> 8) & 0xffu;
-        const uint4 w = cur.codes[j];
-        const bool n0 = e0 <= kCacheTopScale, n1 = e1 <= kCacheTopScale;
-        fine = fine && ((n0 && n1) || !cur.live);
-        const uint32_t s0 = n0 && cur.live ? e0 * 0x800080u : 0u, s1 = n1 && cur.live ? e1 * 0x800080u : 0u;
-        uint8_t* to = k + (2 * i + (b4 >> 1)) * KBOX;
-        *reinterpret_cast<uint4*>(to + offs[0]) = expand8(turned ? w.z : w.x, s0);
-        *reinterpret_cast<uint4*>(to + offs[1]) = expand8(turned ? w.w : w.y, s0);
-        *reinterpret_cast<uint4*>(to + offs[2]) = expand8(turned ? w.x : w.z, s1);
-        *reinterpret_cast<uint4*>(to + offs[3]) = expand8(turned ? w.y : w.w, s1);
+      struct Pair {
+        uint4 v[4];
       };
-      if (!pass(&ka_free[buf], ph, abort_flag, 401)) break;
-      LAGA_TRACE_POINT(cache4, 1, n);
-      boxes(0, 2 * (1 - vh));
-      boxes(1, 2 * (1 - vh) + 1);
+      // all eight scales at once: a byte above the largest scale has its upper bit and the sum's set
+      static_assert(kCacheTopScale == 0xe2, "the sum below");
+      const uint32_t s01 = cur.scales[0] | cur.scales[1] << 16, s23 = cur.scales[2] | cur.scales[3] << 16;
+      const uint32_t over = ((((s01 & 0x7f7f7f7fu) + 0x1d1d1d1du) & s01) | (((s23 & 0x7f7f7f7fu) + 0x1d1d1d1du) & s23)) & 0x80808080u;
+      fine = fine && (over == 0 || !cur.live);
+      if (__any_sync(0xffffffffu, over != 0)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if ((cur.scales[j] & 0xffu) > kCacheTopScale) cur.scales[j] &= 0xff00u;
+          if ((cur.scales[j] >> 8) > kCacheTopScale) cur.scales[j] &= 0xffu;
+        }
+      }
+      auto expand = [&](int j) {
+        const uint32_t two = cur.live ? cur.scales[j] : 0u;
+        const uint32_t s0 = __byte_perm(two, 0, pick) * 0x800080u, s1 = __byte_perm(two, 0, pick ^ 1u) * 0x800080u;
+        const uint4 w = cur.codes[j];
+        return Pair{{expand8(turned ? w.z : w.x, s0), expand8(turned ? w.w : w.y, s0), expand8(turned ? w.x : w.z, s1),
+                     expand8(turned ? w.y : w.w, s1)}};
+      };
+      auto store = [&](const Pair& p, int i) {
+        uint8_t* to = k + (2 * i + (b4 >> 1)) * KBOX;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) *reinterpret_cast<uint4*>(to + offs[x]) = p.v[x];
+      };
+      const Pair a0 = expand(0), a1 = expand(1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const bool number = finite8(cur.rope[i]);
         fine = fine && (number || !cur.live);
         if (!(number && cur.live)) cur.rope[i] = make_uint4(0, 0, 0, 0);
       }
-      *reinterpret_cast<uint4*>(k + 8 * KBOX + off0) = cur.rope[0];
-      *reinterpret_cast<uint4*>(k + 8 * KBOX + off1) = cur.rope[1];
+      const Pair v0 = expand(2), v1 = expand(3);
+      const uint4 r0 = cur.rope[0], r1 = cur.rope[1];
+      // The next tile's bytes into the same registers, now: a wait for one of a warp's loads can be a wait
+      // for all that are under way, so that loads issued before the expansion were waited for there.
+      if (++j == pc.tiles) {
+        j = 0;
+        more = walk.next(pc);
+      }
+      if (more) hold(a, pc, j, key, b4, vh, cur);
+      if (!pass(&ka_free[buf], ph, abort_flag, 401)) break;
+      LAGA_TRACE_POINT(cache4, 1, n);
+      store(a0, 2 * (1 - vh));
+      store(a1, 2 * (1 - vh) + 1);
+      *reinterpret_cast<uint4*>(k + 8 * KBOX + off0) = r0;
+      *reinterpret_cast<uint4*>(k + 8 * KBOX + off1) = r1;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ka_full[buf]);
       LAGA_TRACE_POINT(cache4, 2, n);
       if (!pass(&kb_free[buf], ph, abort_flag, 402)) break;
       LAGA_TRACE_POINT(cache4, 3, n);
-      boxes(2, 2 * vh);
-      boxes(3, 2 * vh + 1);
+      store(v0, 2 * vh);
+      store(v1, 2 * vh + 1);
       const uint32_t odd = ~__ballot_sync(0xffffffffu, fine);  // four lanes a key
-      if (lane == 0) {
-        uint32_t bits = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) bits |= ((odd >> (4 * i)) & 15u) ? 1u << i : 0u;
-        bad[buf * 8 + pw] = static_cast<uint8_t>(bits);
-      }
+      if (lane == 0) bad[buf * 8 + pw] = odd;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&kb_full[buf]);
       LAGA_TRACE_POINT(cache4, 4, n);
-      cur = nxt;
       ++n;
     }
   } else if (warp == MMA_WARP) {
@@ -278,50 +301,41 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
       mma_commit_warp(pv_done);
       return true;
     };
-    // S (+)= Q K^T over four latent boxes: those in TMEM (0 .. 3), those in shared memory, the RoPE box.
-    auto low_boxes = [&](uint32_t s, uint32_t k, uint32_t accumulate) {
+    // S = Q K^T over the boxes outside this half's values and the RoPE box; S += over the values' boxes
+    const uint32_t ka_at = 4 * (1 - vh) * (KBOX / 16), kb_at = 4 * vh * (KBOX / 16);
+    auto first_boxes = [&](uint32_t s, uint32_t k) {
 #pragma unroll
-      for (int c = 0; c < Q_TMEM; ++c) mma4<true, 2>(s, tmem + 32 * c, k + c * (KBOX / 16), IDESC_S, c ? 1u : accumulate);
+      for (int c = 0; c < 4; ++c) mma4<false, 2>(s, q_low + c * (QBOX / 16), k + ka_at + c * (KBOX / 16), IDESC_S, c ? 1u : 0u);
+      mma4<false, 2>(s, q_low + 4 * (QBOX / 16), k + 8 * (KBOX / 16), IDESC_ROPE, 1u);
     };
-    auto high_boxes = [&](uint32_t s, uint32_t k, uint32_t accumulate) {
+    auto other_boxes = [&](uint32_t s, uint32_t k) {
 #pragma unroll
-      for (int c = Q_TMEM; c < 8; ++c)
-        mma4<false, 2>(s, q_low + (c - Q_TMEM) * (QBOX / 16), k + c * (KBOX / 16), IDESC_S, c > Q_TMEM ? 1u : accumulate);
-    };
-    auto rope_box = [&](uint32_t s, uint32_t k) {
-      mma4<false, 2>(s, q_low + (8 - Q_TMEM) * (QBOX / 16), k + 8 * (KBOX / 16), IDESC_ROPE, 1u);
+      for (int c = 0; c < Q_TMEM; ++c) mma4<true, 2>(s, tmem + 32 * c, k + kb_at + c * (KBOX / 16), IDESC_S, 1u);
     };
     while (ok && walk.next(pc)) {
       ok = pass(q_full, seg & 1, abort_flag, 412) && pass(q_rest, seg & 1, abort_flag, 416);
       ++seg;
       for (int j = 0; j < pc.tiles && ok; ++j, ++n) {
-        // the boxes that are there first; the context of the tile before between the two groups, since
-        // it frees the buffer that the tile after this one needs; then the boxes of the values
-        // (P of the tile two before, in this S's place, was read by a product issued earlier)
+        // All of a tile's scores before the context of the tile before, so that its weights are worked out
+        // beside them; first the boxes outside this half's values, whose place has been free for longer.
+        // (P of the tile two before, in this S's place, was read by a product issued earlier.)
         ok = pass(&ka_full[n & 1], (n >> 1) & 1, abort_flag, 413);
         if (!ok) break;
         tc_fence_after();
         LAGA_TRACE_POINT(cache4, 5, n);
         const uint32_t s = tmem + COL_S + (n & 1) * BKV, k = k_low + (n & 1) * (K_BYTES / 16);
-        if (vh)
-          low_boxes(s, k, 0u);
-        else
-          high_boxes(s, k, 0u);
-        rope_box(s, k);
+        first_boxes(s, k);
         issued = true;
         LAGA_TRACE_POINT(cache4, 6, n);
-        if (j > 0 && !(ok = context(n - 1, j == 1))) break;
         ok = pass(&kb_full[n & 1], (n >> 1) & 1, abort_flag, 415);
         if (!ok) break;
         tc_fence_after();
         LAGA_TRACE_POINT(cache4, 11, n);
-        if (vh)
-          high_boxes(s, k, 1u);
-        else
-          low_boxes(s, k, 1u);
+        other_boxes(s, k);
         mma_commit_warp(&ka_free[n & 1]);
         mma_commit_warp(s_full);
         LAGA_TRACE_POINT(cache4, 12, n);
+        if (j > 0) ok = context(n - 1, j == 1);
       }
       if (ok) ok = context(n - 1, pc.tiles == 1);
     }
@@ -349,7 +363,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         if (seg > 0 && !pass(q_idle, 1, abort_flag, 424)) { ok = false; break; }
         if (lane == 0) {
           mbar_arrive_expect_tx(q_stage, Q_TMEM * QBOX);
-          for (int c = 0; c < Q_TMEM; ++c) tma_load_2d(sQ + c * QBOX, &mQ, q_stage, 64 * c, static_cast<int>(row0));
+          for (int c = 0; c < Q_TMEM; ++c) tma_load_2d(sQ + c * QBOX, &mQ, q_stage, 64 * (4 * vh + c), static_cast<int>(row0));
         }
         staged = true;
       }
@@ -381,8 +395,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         if (!pass(q_idle, 0, abort_flag, 426)) { ok = false; break; }
         if (lane == 0) {
           mbar_arrive_expect_tx(q_rest, Q_BYTES);
-          for (int c = Q_TMEM; c < NBOX; ++c)
-            tma_load_2d(sQ + (c - Q_TMEM) * QBOX, &mQ, q_rest, 64 * c, static_cast<int>(row0));
+          for (int c = 0; c < 5; ++c)
+            tma_load_2d(sQ + c * QBOX, &mQ, q_rest, c < 4 ? 64 * (4 * (1 - vh) + c) : 512, static_cast<int>(row0));
         }
         rest = true;
       }
@@ -404,8 +418,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         const uint32_t s_at = tmem + COL_S + (n & 1) * BKV + lane_off;
         tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(x));
         tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
-        uint2 bits;
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(bits.x), "=r"(bits.y) : "r"(smem_u32(bad + (n & 1) * 8)));
+        uint4 w0, w1;
+        const uint32_t bad_at = smem_u32(bad + (n & 1) * 8);
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w0.x), "=r"(w0.y), "=r"(w0.z), "=r"(w0.w) : "r"(bad_at));
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w1.x), "=r"(w1.y), "=r"(w1.z), "=r"(w1.w) : "r"(bad_at + 16));
+        uint2 bits = make_uint2(0, 0);
+        if ((w0.x | w0.y | w0.z | w0.w) | (w1.x | w1.y | w1.z | w1.w))  // a bit a key
+          bits = make_uint2(keys_of(w0.x) | keys_of(w0.y) << 8 | keys_of(w0.z) << 16 | keys_of(w0.w) << 24,
+                            keys_of(w1.x) | keys_of(w1.y) << 8 | keys_of(w1.z) << 16 | keys_of(w1.w) << 24);
         tmem_wait_ld();
         const int k0 = pc.key0 + j * BKV;
 #pragma unroll
