@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(SIMT_THREADS) simt_attn_kernel(const CacheAttn
   const int part = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const CacheShare share = cache_share(a, part);
   if (share.begin >= share.end) return;
-  int item = cache_item_of(a, share.begin);
+  int item = __ldcg(a.part_item + part);
   for (int t = share.begin; t < share.end; ++item) {
     const int item_begin = __ldcg(a.first + item), item_end = __ldcg(a.first + item + 1);
     if (item_end <= t) continue;  // no keys

@@ -75,6 +75,7 @@ struct CacheAttn {
   float scale;
   ScoreMods mods;
   int* first;    // [items + 1] first key tile of each item in the order of all
+  int* part_item;  // [parts] the item in which a part's share begins
   int2* hull;    // [items] keys seen by some row; {-1, -1}: a length past the table
   float* part_o;     // [2 parts][tile][d_c]
   float2* part_ml;   // [2 parts][tile] {running maximum, sum}
@@ -158,16 +159,6 @@ __device__ __forceinline__ CacheShare cache_share(const CacheAttn& a, int part) 
   return CacheShare{quota, static_cast<int>(min(begin, static_cast<long long>(total))),
                     static_cast<int>(min(begin + quota, static_cast<long long>(total)))};
 }
-// The last item that begins at or before key tile t.
-__device__ __forceinline__ int cache_item_of(const CacheAttn& a, int t) {
-  int lo = 0, hi = a.items();  // first[lo] <= t < first[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldcg(a.first + mid) <= t) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
 // A row's sum of weights at its end: 0 of a row that sees keys (whose scores were all -inf) is NaN.
 __device__ __forceinline__ float row_sum(float l, int2 seen) {
   return l == 0.f && seen.x < seen.y ? __int_as_float(0x7fc00000) : l;
@@ -223,6 +214,19 @@ __device__ __forceinline__ void cache4_plan_items(const CacheAttn& a) {
     __syncthreads();
   }
   if (threadIdx.x == 0) a.first[items] = before;
+  // the item in which each part's share begins: the last one that begins at or before it
+  __syncthreads();
+  const int quota = max(a.least, (before + a.parts - 1) / a.parts);
+  for (int p = threadIdx.x; p < a.parts; p += THREADS) {
+    const long long t = static_cast<long long>(p) * quota;
+    int lo = 0, hi = items;  // first[lo] <= t < first[hi], if t is within them
+    while (t < before && hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.first[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    a.part_item[p] = lo;
+  }
 }
 #endif
 

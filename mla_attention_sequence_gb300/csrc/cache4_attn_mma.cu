@@ -64,46 +64,72 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
 
   Walk<ROWS, KEYS> walk(a, part);
   Piece pc;
-  // The loads run STAGES - 1 tiles ahead, across pieces: a walk of their own.
+  // The loads run STAGES - 1 tiles ahead, across pieces: a walk of their own. Four lanes a key: chunks q,
+  // q + 4, .. of its 26. The key's place among the pages is kept from tile to tile, and its entry of the
+  // table is fetched a tile before it is used.
   Walk<ROWS, KEYS> ahead(a, part);
   Piece next;
-  int next_tile = 0;
   bool more = ahead.next(next);
-  int loaded = 0;
-  // Four lanes a key: chunks q, q + 4, .. of its 26.
+  if (!more) return;
+  const int my_key = threadIdx.x >> 2, q = threadIdx.x & 3, page = a.cache.page;
+  int loaded = 0, left = next.tiles, at = 0, page_row = 0, id = -1;
+  uint32_t page_of = 0;
+  bool wanted = false;
+  auto fetch = [&]() {
+    wanted = at >= next.hull.x && at < next.hull.y;
+    const uint32_t k = min(page_of, static_cast<uint32_t>(a.pages.most - 1));
+    id = wanted ? __ldg(a.pages.table + static_cast<ll>(next.b) * a.pages.most + k) : -1;
+    if (page_of != k) id = -1;
+  };
+  auto begin_piece = [&]() {
+    left = next.tiles;
+    at = next.key0 + my_key;
+    page_of = static_cast<uint32_t>(at) / static_cast<uint32_t>(page);
+    page_row = at - static_cast<int>(page_of) * page;
+    fetch();
+  };
+  begin_piece();
   auto load = [&]() {
     const int s = loaded % STAGES;
     if (more) {
-      const int key = threadIdx.x >> 2, q = threadIdx.x & 3, at = next.key0 + next_tile * KEYS + key;
-      const bool wanted = at >= next.hull.x && at < next.hull.y;
-      bool there;
-      const ll slot = cache_slot_of(a.cache, a.pages, next.b, wanted ? at : next.hull.x, &there);
-      const bool live = wanted && there;
+      const bool there = id >= 0 && id < a.cache.pages, live = wanted && there;
+      const ll slot = live ? static_cast<ll>(id) * page + page_row : 0;
       const uint32_t gone = __ballot_sync(0xffffffffu, wanted && !there);
-      if (lane == 0) {
-        uint32_t bits = 0;
+      if (lane == 0) reinterpret_cast<uint8_t*>(missing + s)[warp] = 0;
+      if (gone) {
+        if (lane == 0) {
+          uint32_t bits = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) bits |= ((gone >> (4 * i)) & 1u) << i;
-        reinterpret_cast<uint8_t*>(missing + s)[warp] = static_cast<uint8_t>(bits);
-        if (gone) report_page(a.status, 306);
+          for (int i = 0; i < 8; ++i) bits |= ((gone >> (4 * i)) & 1u) << i;
+          reinterpret_cast<uint8_t*>(missing + s)[warp] = static_cast<uint8_t>(bits);
+          report_page(a.status, 306);
+        }
+        __syncwarp();
       }
-      const uint32_t to = stages + s * STAGE_BYTES + key * KEY_BYTES;
+      const uint32_t to = stages + s * STAGE_BYTES + my_key * KEY_BYTES + 16 * q;
       const uint8_t* codes = a.cache.codes + slot * 256 + 16 * q;
       const uint8_t* keys = static_cast<const uint8_t*>(a.cache.keys) + slot * 128 + 16 * q;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) copy16(to + 16 * (q + 4 * i), codes + 64 * i, live);
+      for (int i = 0; i < 4; ++i) copy16(to + 64 * i, codes + 64 * i, live);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) copy16(to + 288 + 16 * (q + 4 * i), keys + 64 * i, live);
-      if (q < 2) copy16(to + 256 + 16 * q, a.cache.scales + slot * 32 + 16 * q, live);
-      if (++next_tile == next.tiles) {
-        next_tile = 0;
+      for (int i = 0; i < 2; ++i) copy16(to + 288 + 64 * i, keys + 64 * i, live);
+      if (q < 2) copy16(to + 256, a.cache.scales + slot * 32 + 16 * q, live);
+      if (--left == 0) {
         more = ahead.next(next);
+        if (more) begin_piece();
+      } else {
+        at += KEYS;
+        page_row += KEYS;
+        while (page_row >= page) {
+          page_row -= page;
+          ++page_of;
+        }
+        fetch();
       }
     }
     ++loaded;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (!more) return;
 #pragma unroll 1
   for (int i = 0; i < STAGES - 1; ++i) load();
   asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");

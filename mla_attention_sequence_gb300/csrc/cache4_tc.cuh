@@ -24,7 +24,7 @@ struct Walk {
   int t, item;
   __device__ __forceinline__ Walk(const CacheAttn& a_, int part) : a(a_), share(cache_share(a_, part)) {
     t = share.begin;
-    item = t < share.end ? cache_item_of(a, t) - 1 : 0;
+    item = __ldcg(a.part_item + part) - 1;
   }
   __device__ __forceinline__ bool next(Piece& p) {
     if (t >= share.end) return false;

@@ -84,8 +84,10 @@ struct AttnSizes {
   CacheAttn a;
   int d_nope, d_v;
   bool tc, few;  // tensor cores; mma.sync's form of them
-  size_t items_bytes, hull_bytes, query_bytes, up_bytes, ctx_bytes, ml_bytes, o_bytes;
-  size_t total() const { return items_bytes + hull_bytes + query_bytes + up_bytes + ctx_bytes + ml_bytes + o_bytes; }
+  size_t items_bytes, parts_bytes, hull_bytes, query_bytes, up_bytes, ctx_bytes, ml_bytes, o_bytes;
+  size_t total() const {
+    return items_bytes + parts_bytes + hull_bytes + query_bytes + up_bytes + ctx_bytes + ml_bytes + o_bytes;
+  }
 };
 
 laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cache, bool sizes_only, AttnSizes* s) {
@@ -130,6 +132,7 @@ laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cach
   if (items * (room / a.keys + 2) >= lim || room > lim - 2 * a.keys)
     return fail(LAGA_ERR_UNSUPPORTED, "cache attention: problem too large (rows times the table's room)%s");
   s->items_bytes = align_up((items + 1) * sizeof(int), 256);
+  s->parts_bytes = align_up(a.parts * sizeof(int), 256);
   s->hull_bytes = align_up(items * sizeof(int2), 256);
   const size_t rows = static_cast<size_t>(a.pages.B) * a.rows;
   s->ctx_bytes = align_up(rows * a.cache.d_c * 4, 256);
@@ -284,6 +287,7 @@ laga_status laga_mla_cache4_fwd(const laga_mla_cache4_desc* desc, const laga_mla
     return p;
   };
   a.first = reinterpret_cast<int*>(take(z.items_bytes));
+  a.part_item = reinterpret_cast<int*>(take(z.parts_bytes));
   a.hull = reinterpret_cast<int2*>(take(z.hull_bytes));
   CacheOperands x;
   x.query = reinterpret_cast<uint8_t*>(take(z.query_bytes));
