@@ -12,7 +12,14 @@
 // Memory bound: a row is held in registers between its sum and its result, so each value is read once
 // and written once. Eight lanes share a row (24 chunks of 16 bytes for a bf16 head of 192: three a
 // lane), so that a sum takes three shuffles and a warp has four rows in flight; rows wider than 24
-// chunks take a whole warp.
+// chunks take a whole warp. As many CTAs as the SMs hold deal the rows out evenly, each warp takes
+// consecutive rows, loads the next ones before it works on those at hand, and makes a token's angles
+// once for all heads that it has of it.
+//
+// 2048 tokens of 128 heads of 192 in bf16 (events around the launches, 201 MB moved forward, 302 MB
+// backward): 41 us forward, 64 us backward with the sum of the partials. A CTA a token, without loads
+// ahead: 47 and 92. Forward with 4 CTAs an SM 43, with 4 and no loads ahead 45, with warps of 32 rows 49
+// (angles again for each); backward with 3 CTAs an SM and no loads ahead 101.
 #include "rope_device.cuh"
 
 #include <algorithm>
@@ -22,7 +29,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int BWD_CTAS_PER_SM = 4;
+constexpr int BWD_CTAS_PER_SM = 4;  // at most: rows of partials
 
 // x^2 of a value above 2^60 leaves fp32 in a sum of 1024: such rows are scaled down first.
 constexpr float kBigSum = 0x1p120f;
@@ -71,7 +78,7 @@ struct RowOps {
   static __device__ __forceinline__ int partner(const RowShape& s, int c) {
     return c - s.nope < s.half ? c + s.half : c - s.half;
   }
-  static __device__ __forceinline__ void load(const T* row, const RowShape& s, int l, bool active, bool partners,
+  static __device__ __forceinline__ void load(const T* row, const RowShape& s, int l, bool active, [[maybe_unused]] bool partners,
                                               Held& h) {
     const uint4* p = reinterpret_cast<const uint4*>(row);
 #pragma unroll
@@ -119,10 +126,18 @@ struct RowOps {
     return sum;
   }
 
-  static __device__ __forceinline__ void forward(const T* src, T* dst, const RowShape& s, const float* w,
+  // The weights of chunk c, laid out for the row's lanes: N / 4 quarters, chunks of 16 bytes beside each other.
+  static __device__ __forceinline__ int weight_at(int pitch, int c, int quarter) { return quarter * pitch + 4 * c; }
+  static __device__ __forceinline__ void weights(const float* w, int pitch, int c, float (&v)[N]) {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+      const float4 f = *reinterpret_cast<const float4*>(w + weight_at(pitch, c, q));
+      v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
+    }
+  }
+
+  static __device__ __forceinline__ void forward(const Held& h, T* dst, const RowShape& s, const float* w, int pitch,
                                                  const float2* cs, float eps, int l, bool active) {
-    Held h;
-    load(src, s, l, active, true, h);
     const float sum = sum_lanes<LANES>(squares(h, 1.f));
     const Scale sc = row_scale<LANES>(sum, s.inv_d, eps, [&](float by) { return squares(h, by); });
     __syncwarp();  // in place: every lane of the row has loaded
@@ -130,46 +145,46 @@ struct RowOps {
     for (int k = 0; k < K; ++k) {
       const int c = l + LANES * k;
       if (!active || c >= s.chunks) continue;
-      float v[N], o[N];
+      float v[N], o[N], wv[N];
       V::get(h.own[k], v);
+      weights(w, pitch, c, wv);
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = v[i] * sc.down * sc.r * w[c * N + i];
+      for (int i = 0; i < N; ++i) v[i] = v[i] * sc.down * sc.r * wv[i];
       if constexpr (!INTERLEAVED) {
         if (c >= s.nope) {
-          const float* wo = w + partner(s, c) * N;
+          weights(w, pitch, partner(s, c), wv);
           V::get(h.other[k], o);
 #pragma unroll
-          for (int i = 0; i < N; ++i) o[i] = o[i] * sc.down * sc.r * wo[i];
+          for (int i = 0; i < N; ++i) o[i] = o[i] * sc.down * sc.r * wv[i];
         }
       }
       turn(s, c, cs, 1.f, v, o);
-      reinterpret_cast<uint4*>(dst)[c] = V::put(v);
+      __stcs(reinterpret_cast<uint4*>(dst) + c, V::put(v));
     }
   }
 
-  static __device__ __forceinline__ void backward(const T* src, const T* grad, T* dst, const RowShape& s,
-                                                  const float* w, const float2* cs, float eps, int l, bool active,
-                                                  float (&acc)[K][N]) {
-    Held x, z;
-    load(src, s, l, active, false, x);
-    load(grad, s, l, active, true, z);
+  static __device__ __forceinline__ void backward(const Held& x, const Held& z, T* dst, const RowShape& s,
+                                                  const float* w, int pitch, const float2* cs, float eps, int l,
+                                                  bool active, float (&acc)[K][N]) {
     const float sum = sum_lanes<LANES>(squares(x, 1.f));
     const Scale sc = row_scale<LANES>(sum, s.inv_d, eps, [&](float by) { return squares(x, by); });
     float dot = 0.f, dy[K][N];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = l + LANES * k;
-      float v[N], o[N];
+      float v[N], o[N], wv[N];
       V::get(z.own[k], dy[k]);
       if (!active || c >= s.chunks) continue;
       if constexpr (!INTERLEAVED) V::get(z.other[k], o);
       turn(s, c, cs, -1.f, dy[k], o);
       V::get(x.own[k], v);
+      weights(w, pitch, c, wv);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float xh = v[i] * sc.down * sc.r, p = dy[k][i] * xh;
         acc[k][i] += p;
-        dot = fmaf(p, w[c * N + i], dot);
+        dot = fmaf(p, wv[i], dot);
+        dy[k][i] *= wv[i];
       }
     }
     const float mean = sum_lanes<LANES>(dot) * s.inv_d;
@@ -181,9 +196,8 @@ struct RowOps {
       float v[N];
       V::get(x.own[k], v);
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        v[i] = sc.down * sc.r * (dy[k][i] * w[c * N + i] - v[i] * sc.down * sc.r * mean);
-      reinterpret_cast<uint4*>(dst)[c] = V::put(v);
+      for (int i = 0; i < N; ++i) v[i] = sc.down * sc.r * (dy[k][i] - v[i] * sc.down * sc.r * mean);
+      __stcs(reinterpret_cast<uint4*>(dst) + c, V::put(v));
     }
   }
 };
@@ -214,67 +228,112 @@ __device__ __forceinline__ void reduce_columns(float (&acc)[K][Vec<T>::N], const
   __syncthreads();
 }
 
-// Rows of 16-byte chunks. A CTA takes `per` tokens at a time (their cosines and sines once, for all
-// heads), the forward's one such group, the backward's every gridDim-th.
+// How the rows are dealt out: the first `ctas_q` CTAs take the queries' rows and the others the keys',
+// `share` consecutive rows a warp.
+struct NormDeal {
+  int ctas_q, ctas_k;
+  ll share_q, share_k;
+  int held;   // tokens whose cosines and sines a warp holds at a time
+  int pitch;  // of the weights' quarters in shared memory, in floats
+};
+
+// CTAs of a variant that an SM holds: rows in flight against registers (the figures above).
+template <int LANES, int K, bool BWD>
+constexpr int kNormCtas = LANES * K > 64 ? (BWD ? 1 : 2) : (BWD ? 2 : 3);
+
+// Rows of 16-byte chunks. A warp keeps the cosines and sines of the tokens that it is at, and the next
+// rows' loads are under way while it works on its rows.
 template <typename T, bool INTERLEAVED, int LANES, int K, bool BWD>
-__global__ void __launch_bounds__(THREADS) norm_vec_kernel(const NormArgs a, const RopeTable t, int per) {
+__global__ void __launch_bounds__(THREADS, (kNormCtas<LANES, K, BWD>))
+    norm_vec_kernel(const NormArgs a, const RopeTable t, const NormDeal deal) {
   using R = RowOps<T, INTERLEAVED, LANES, K>;
+  using Held = typename R::Held;
   constexpr int N = R::N, ROWS = 32 / LANES;  // rows of a warp
-  extern __shared__ float smem[];
+  extern __shared__ __align__(16) float smem[];
   const RopeArgs& p = a.rope;
-  const int d = p.d_nope + p.d_rope, n = p.d_rope / 2;
-  float* w = smem;                                         // [d], then the keys' [d_rope]
-  float2* cs = reinterpret_cast<float2*>(smem + ((d + p.d_rope + 3) & ~3));  // [per][n]
-  float* red = reinterpret_cast<float*>(cs + per * n);     // backward: [WARPS][d]
+  const int n = p.d_rope / 2, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES;
+  const bool keys = static_cast<int>(blockIdx.x) >= deal.ctas_q;
+  const int heads = keys ? 1 : p.n_h, nope = keys ? 0 : p.d_nope, width = nope + p.d_rope, pitch = deal.pitch;
+  const RowShape s{width / N, nope / N, n / N, 1.f / width};
+  float* w = smem;  // [N / 4][pitch]
+  float2* cs = reinterpret_cast<float2*>(smem + N / 4 * pitch) + warp * deal.held * n;  // [held][n] a warp
+  const T* in = static_cast<const T*>(keys ? p.k : p.q);
+  const T* grad = static_cast<const T*>(keys ? a.z_k : a.z_q);
+  T* out = static_cast<T*>(keys ? p.k_out : p.q_out);
+  const ll share = keys ? deal.share_k : deal.share_q;
+  const ll begin = (static_cast<ll>(blockIdx.x - (keys ? deal.ctas_q : 0)) * WARPS + warp) * share;
+  const int rows = static_cast<int>(max(min(share, p.tokens * heads - begin), 0ll));  // of this warp
+  const ll first_token = begin / heads;
+  const int first_head = static_cast<int>(begin - first_token * heads);
+  const int tokens = rows ? (first_head + rows - 1) / heads + 1 : 0;
   after_previous();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES;
-  if (p.q)
-    for (int i = threadIdx.x; i < d; i += THREADS) w[i] = to_f(static_cast<const T*>(a.w_q)[i]);
-  if (p.k)
-    for (int i = threadIdx.x; i < p.d_rope; i += THREADS) w[d + i] = to_f(static_cast<const T*>(a.w_k)[i]);
-  const ll groups = (p.tokens + per - 1) / per;
-  for (int kind = 0; kind < 2; ++kind) {
-    const void* src = kind ? p.k : p.q;
-    if (!src) continue;
-    const int heads = kind ? 1 : p.n_h, nope = kind ? 0 : p.d_nope, width = nope + p.d_rope;
-    const RowShape s{width / N, nope / N, n / N, 1.f / width};
-    const T* in = static_cast<const T*>(src);
-    const T* grad = static_cast<const T*>(kind ? a.z_k : a.z_q);
-    T* out = static_cast<T*>(kind ? p.k_out : p.q_out);
-    const float* wk = w + (kind ? d : 0);
-    float acc[K][N];
+
+  int row = lane / LANES, head = first_head + row, token = head / heads;  // this lane's, from the warp's first
+  head -= token * heads;
+  const ll at0 = begin * width;
+  Held x, z;
+  auto load = [&](int r, Held& hx, Held& hz) {
+    const bool active = r < rows;
+    const ll at = at0 + static_cast<ll>(active ? r : 0) * width;
+    R::load(in + at, s, l, active, !BWD, hx);
+    if constexpr (BWD) R::load(grad + at, s, l, active, true, hz);
+  };
+  load(row, x, z);
+  const T* weight = static_cast<const T*>(keys ? a.w_k : a.w_q);
+  for (int i = threadIdx.x; i < width; i += THREADS)
+    w[R::weight_at(pitch, i / N, i % N / 4) + i % 4] = to_f(weight[i]);
+  __syncthreads();
+
+  float acc[K][N];
+  if constexpr (BWD)
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[k][i] = 0.f;
+  int held0 = 0, held1 = 0;  // the tokens whose angles are there
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += ROWS) {
+    Held nx, nz;
+    load(row + ROWS, nx, nz);
+    const bool active = row < rows;
+    const int last = min(__shfl_sync(0xffffffffu, token, 31), tokens - 1);
+    if (last >= held1) {
+      held0 = __shfl_sync(0xffffffffu, token, 0);
+      held1 = min(held0 + deal.held, tokens);
+      __syncwarp();
+      const ll from = first_token + held0;
+#pragma unroll 4
+      for (int e = lane; e < (held1 - held0) * n; e += 32) {
+        const int k = e / n, i = e - k * n;
+        const ll at = t.axis[i] * p.tokens + from + k;
+        const ll pos = p.pos64 ? static_cast<const ll*>(p.pos)[at] : static_cast<ll>(static_cast<const int*>(p.pos)[at]);
+        cs[e] = cos_sin(pos, t.turns[i]);
+      }
+      __syncwarp();
+    }
+    const float2* angles = cs + (active ? token - held0 : 0) * n;
+    T* to = out + at0 + static_cast<ll>(active ? row : 0) * width;
     if constexpr (BWD)
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[k][i] = 0.f;
-    for (ll g = blockIdx.x; g < groups; g += gridDim.x) {
-      const ll first = g * per;
-      const int tokens = static_cast<int>(min(static_cast<ll>(per), p.tokens - first));
-      if (BWD || kind == 0 || !p.q) {  // else the first pass' angles stand
-        __syncthreads();
-        fill_angles<THREADS>(p, t, first, tokens, cs);
-        __syncthreads();
-      }
-      const int rows = tokens * heads;
-      const ll base = first * heads * width;
-      for (int r0 = warp * ROWS; r0 < rows; r0 += WARPS * ROWS) {
-        const int row = r0 + lane / LANES;
-        const bool active = row < rows;
-        const ll at = base + static_cast<ll>(active ? row : 0) * width;
-        const float2* angles = cs + (active ? row / heads : 0) * n;
-        if constexpr (BWD)
-          R::backward(in + at, grad + at, out + at, s, wk, angles, a.eps, l, active, acc);
-        else
-          R::forward(in + at, out + at, s, wk, angles, a.eps, l, active);
-      }
+      R::backward(x, z, to, s, w, pitch, angles, a.eps, l, active, acc);
+    else
+      R::forward(x, to, s, w, pitch, angles, a.eps, l, active);
+    row += ROWS;
+    head += ROWS;
+    if (head >= heads) {
+      const int k = head / heads;
+      token += k;
+      head -= k * heads;
     }
-    if constexpr (BWD) {
-      __syncthreads();
-      // rows of partials: all CTAs' queries, then all CTAs' keys
-      float* to = a.partials + (kind ? static_cast<ll>(gridDim.x) * d : 0) + static_cast<ll>(blockIdx.x) * width;
-      reduce_columns<T, LANES, K>(acc, s, red, to);
-    }
+    x = nx;
+    if constexpr (BWD) z = nz;
+  }
+  if constexpr (BWD) {
+    // rows of partials: the CTAs' of the queries, then those of the keys
+    const int d = p.d_nope + p.d_rope;
+    float* to = a.partials + (keys ? static_cast<ll>(deal.ctas_q) * d + static_cast<ll>(blockIdx.x - deal.ctas_q) * width
+                                   : static_cast<ll>(blockIdx.x) * width);
+    __syncthreads();  // the angles' place is taken again
+    reduce_columns<T, LANES, K>(acc, s, smem + N / 4 * pitch, to);
   }
 }
 
@@ -379,34 +438,64 @@ __global__ void __launch_bounds__(THREADS) norm_any_kernel(const NormArgs a, con
   }
 }
 
-// dw of the queries' (blockIdx.y 0) or the keys' weight: the CTAs' partials, 32 columns a CTA.
+// dw of the queries' (blockIdx.y 0) or the keys' weight: the CTAs' partials, 32 columns a CTA, every
+// 32nd row a warp.
+constexpr int DW_WARPS = 32;
 template <typename T>
-__global__ void __launch_bounds__(THREADS) norm_dw_kernel(const float* partials, int ctas, int d, int d_rope, T* dw_q,
-                                                          T* dw_k) {
-  __shared__ float red[WARPS][32];
+__global__ void __launch_bounds__(32 * DW_WARPS) norm_dw_kernel(const float* partials, int ctas_q, int ctas_k, int d,
+                                                                int d_rope, T* dw_q, T* dw_k) {
+  __shared__ float red[DW_WARPS][33];
   after_previous();
   T* out = blockIdx.y ? dw_k : dw_q;
-  const int width = blockIdx.y ? d_rope : d, col = blockIdx.x * 32 + (threadIdx.x & 31), j = threadIdx.x >> 5;
+  const int width = blockIdx.y ? d_rope : d, ctas = blockIdx.y ? ctas_k : ctas_q;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   if (!out || static_cast<int>(blockIdx.x * 32) >= width) return;
-  const float* p = partials + (blockIdx.y ? static_cast<ll>(ctas) * d : 0) + col;
+  const float* p = partials + (blockIdx.y ? static_cast<ll>(ctas_q) * d : 0) + col;
   float sum = 0.f;
-  if (col < width)
-    for (int k = j; k < ctas; k += WARPS) sum += __ldcg(p + static_cast<ll>(k) * width);
-  red[j][threadIdx.x & 31] = sum;
-  __syncthreads();
-  if (j == 0 && col < width) {
-    for (int k = 1; k < WARPS; ++k) sum += red[k][threadIdx.x];
-    out[col] = static_cast<T>(sum);
+  if (col < width) {
+#pragma unroll 8
+    for (int k = warp; k < ctas; k += DW_WARPS) sum += __ldcg(p + static_cast<ll>(k) * width);
   }
-}
-
-template <typename T, int LANES, int K, bool BWD>
-cudaError_t launch_vec(const NormArgs& a, const RopeTable& t, int per, unsigned grid, size_t smem, cudaStream_t st) {
-  return launch_next(a.rope.interleaved ? norm_vec_kernel<T, true, LANES, K, BWD> : norm_vec_kernel<T, false, LANES, K, BWD>,
-                     grid, THREADS, smem, st, a, t, per);
+  red[warp][lane] = sum;
+  __syncthreads();
+  // a warp joins the 32 sums of one column
+  const float v = sum_lanes<32>(red[lane][warp]);
+  const int mine = blockIdx.x * 32 + warp;
+  if (lane == 0 && mine < width) out[mine] = static_cast<T>(v);
 }
 
 int bwd_ctas() { return BWD_CTAS_PER_SM * sm_count(); }
+
+template <typename T, int LANES, int K, bool BWD>
+cudaError_t launch_vec(const NormArgs& a, const RopeTable& t, NormDeal& deal, cudaStream_t st) {
+  constexpr int N = Vec<T>::N, ROWS = 32 / LANES, CTAS = kNormCtas<LANES, K, BWD>;
+  const RopeArgs& p = a.rope;
+  const int d = p.d_nope + p.d_rope, n = p.d_rope / 2, widest = p.q ? d : p.d_rope;
+  // Whole steps of ROWS rows a warp, as many for all; the keys' warps take a share of the same length in bytes.
+  const ll q_rows = p.q ? p.tokens * p.n_h : 0, k_rows = p.k ? p.tokens : 0, warps = static_cast<ll>(CTAS) * sm_count() * WARPS;
+  const auto up = [](ll x, ll y) { return (x + y - 1) / y; };
+  // a token's angles cost about as much as the bytes of 16 RoPE rows
+  const double angle_cost = 16. * p.d_rope * p.tokens;
+  const double q_cost = q_rows ? static_cast<double>(q_rows) * d + angle_cost : 0.;
+  const double k_cost = k_rows ? static_cast<double>(k_rows) * p.d_rope + angle_cost : 0.;
+  const auto deal_out = [&](ll rows, double cost, ll& share) {
+    const ll of_these = std::max<ll>(WARPS, static_cast<ll>(warps * (cost / (q_cost + k_cost))) / WARPS * WARPS);
+    share = std::max<ll>(up(up(rows, of_these), ROWS), 1) * ROWS;
+    return static_cast<int>(up(rows, share * WARPS));
+  };
+  deal.ctas_q = q_rows ? deal_out(q_rows, q_cost, deal.share_q) : 0;
+  deal.ctas_k = k_rows ? deal_out(k_rows, k_cost, deal.share_k) : 0;
+  // tokens that a step can touch; more where a token is few rows, as far as 4 KB a warp go
+  const int step = ROWS == 1 ? 1 : (ROWS - 2) / (k_rows ? 1 : p.n_h) + 2;
+  deal.held = std::max(step, std::min(32 / (k_rows ? 1 : std::min(p.n_h, 32)), 4096 / static_cast<int>(n * sizeof(float2))));
+  deal.pitch = 4 * (widest / N);
+  const size_t angles = static_cast<size_t>(WARPS) * deal.held * n * sizeof(float2);
+  const size_t red = BWD ? static_cast<size_t>(WARPS) * widest * sizeof(float) : 0;
+  const size_t smem = static_cast<size_t>(N / 4) * deal.pitch * sizeof(float) + std::max(angles, red);
+  return launch_next(p.interleaved ? norm_vec_kernel<T, true, LANES, K, BWD> : norm_vec_kernel<T, false, LANES, K, BWD>,
+                     static_cast<unsigned>(deal.ctas_q + deal.ctas_k), THREADS, smem, st, a, t,
+                     static_cast<const NormDeal&>(deal));
+}
 
 template <typename T, bool BWD>
 cudaError_t launch(const NormArgs& a, const RopeTable& t, cudaStream_t st) {
@@ -416,29 +505,30 @@ cudaError_t launch(const NormArgs& a, const RopeTable& t, cudaStream_t st) {
   const bool vec = p.d_nope % N == 0 && p.d_rope % N == 0 && (p.interleaved || n % N == 0) && aligned_to_16(p.q) &&
                    aligned_to_16(p.q_out) && aligned_to_16(p.k) && aligned_to_16(p.k_out) && aligned_to_16(a.z_q) &&
                    aligned_to_16(a.z_k) && widest / N <= 128;
-  // a few tokens per CTA when a token is little work, but no fewer CTAs than two per SM
-  const ll work = static_cast<ll>(p.q ? p.n_h : 0) * d + (p.k ? p.d_rope : 0);
-  ll per = std::min<ll>({work > 0 ? 4096 / work : 1, p.tokens / (2 * static_cast<ll>(sm_count())), 16});
-  if (per < 1) per = 1;
-  const ll groups = (p.tokens + per - 1) / per;
-  const unsigned grid = static_cast<unsigned>(BWD ? std::min<ll>(groups, bwd_ctas()) : groups);
-  const size_t angles = static_cast<size_t>(per) * n * sizeof(float2);
-  const size_t red = BWD ? static_cast<size_t>(WARPS) * widest * sizeof(float) : 0;
+  NormDeal deal{};
   cudaError_t e;
   if (!vec) {
+    // a few tokens per CTA when a token is little work, but no fewer CTAs than two per SM
+    const ll work = static_cast<ll>(p.q ? p.n_h : 0) * d + (p.k ? p.d_rope : 0);
+    ll per = std::min<ll>({work > 0 ? 4096 / work : 1, p.tokens / (2 * static_cast<ll>(sm_count())), 16});
+    if (per < 1) per = 1;
+    const ll groups = (p.tokens + per - 1) / per;
+    const unsigned grid = static_cast<unsigned>(BWD ? std::min<ll>(groups, bwd_ctas()) : groups);
+    const size_t angles = static_cast<size_t>(per) * n * sizeof(float2);
+    const size_t red = BWD ? static_cast<size_t>(WARPS) * widest * sizeof(float) : 0;
+    deal.ctas_q = deal.ctas_k = static_cast<int>(grid);
     e = launch_next(norm_any_kernel<T, BWD>, grid, THREADS, angles + red, st, a, t, static_cast<int>(per));
   } else {
-    const size_t smem = ((d + p.d_rope + 3) & ~3) * sizeof(float) + angles + red;
-    const int chunks = widest / N, k = static_cast<int>(per);
-    e = chunks <= 24   ? launch_vec<T, 8, 3, BWD>(a, t, k, grid, smem, st)
-        : chunks <= 32 ? launch_vec<T, 32, 1, BWD>(a, t, k, grid, smem, st)
-        : chunks <= 64 ? launch_vec<T, 32, 2, BWD>(a, t, k, grid, smem, st)
-                       : launch_vec<T, 32, 4, BWD>(a, t, k, grid, smem, st);
+    const int chunks = widest / N;
+    e = chunks <= 24   ? launch_vec<T, 8, 3, BWD>(a, t, deal, st)
+        : chunks <= 32 ? launch_vec<T, 32, 1, BWD>(a, t, deal, st)
+        : chunks <= 64 ? launch_vec<T, 32, 2, BWD>(a, t, deal, st)
+                       : launch_vec<T, 32, 4, BWD>(a, t, deal, st);
   }
   if constexpr (BWD) {
     if (e == cudaSuccess)
-      e = launch_next(norm_dw_kernel<T>, dim3((widest + 31) / 32, p.k ? 2 : 1), THREADS, 0, st,
-                      static_cast<const float*>(a.partials), static_cast<int>(grid), d, p.d_rope,
+      e = launch_next(norm_dw_kernel<T>, dim3((widest + 31) / 32, p.k ? 2 : 1), 32 * DW_WARPS, 0, st,
+                      static_cast<const float*>(a.partials), deal.ctas_q, deal.ctas_k, d, p.d_rope,
                       p.q ? static_cast<T*>(a.dw_q) : nullptr, p.k ? static_cast<T*>(a.dw_k) : nullptr);
   }
   return e;
