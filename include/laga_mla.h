@@ -373,7 +373,7 @@ laga_status laga_mla_norm_rope_bwd(const laga_mla_rope_desc* desc, float eps, co
  * even column's in the low half; a scale byte is the upper 8 of an fp16's 15 bits below the sign, at
  * most 226 (1.25 * 2^13). So values are held to 1/4 of their block's largest size or better, down to
  * steps of 2^-18; sizes above 61440 become 61440. A block with a value that is not finite gets the
- * scale 255 and reads as NaN throughout. RoPE keys are kept in dtype.
+ * scale 255 and reads as NaN throughout, as with any byte past 226. RoPE keys are kept in dtype.
  * A position that the call needs and that has no page (the table too short, or an entry that is no
  * page) is never accessed: an append leaves it out, a read gives NaN, a row of the attention that sees
  * it gets NaN, and the next laga_mla_check returns LAGA_ERR_INVALID_ARG. */

@@ -1,9 +1,12 @@
 // The paged 4-bit latent cache: rows written and read, the sharing out of an attention call's key
 // tiles and the joining of its pieces, and the attention on the CUDA cores for any widths.
 //
-// Writing and reading are bound by memory (a prompt) or by a launch (a token): a warp takes a row, a
-// lane a block of 16 latents (at d_c = 512 each lane exactly one) and a pair of the RoPE key, so that
-// the only thing that lanes exchange is the key's sum of squares.
+// Writing and reading are bound by latency (a launch; a row's place behind its start and its table's
+// entry) and, writing, by instructions. A warp takes a row, a lane a block of 16 latents (at d_c = 512
+// each lane exactly one) and a pair of the RoPE key, so that the only thing that lanes exchange is the
+// key's sum of squares. 12288 rows of 512 + 64 in bf16 (events around the launch, 6 us of it the launch's
+// own): 18 us written, 10 read, 3 of DRAM either way. Codes by comparisons with the borders for bf16 too
+// instead of the conversion: 25 written; with 4, 6 and 12 CTAs' shares an SM 18 .. 19 and 11 .. 12.
 #include "cache4.h"
 #include "rope_device.cuh"
 
@@ -15,10 +18,15 @@
 namespace laga {
 namespace {
 
-constexpr int ROW_WARPS = 8;
+constexpr int ROW_WARPS = 8, ROW_CTAS = 3;  // CTAs an SM holds at once
 
 __device__ __forceinline__ float scale_of(int byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
+}
+
+// What a stored scale byte stands for: those past the grid are blocks that are not finite.
+__device__ __forceinline__ float value_scale(int byte) {
+  return byte > kCacheTopScale ? __int_as_float(0x7fc00000) : scale_of(byte);
 }
 
 // The smallest scale s of the grid with 6 s >= top (the largest scale if there is none), exactly: a
@@ -38,13 +46,14 @@ __device__ __forceinline__ int scale_for(float top) {
   return e;
 }
 
-// The code of v: its nearest multiple of s, ties to the even code. The halves between neighbours are
-// few-bit multiples of s, exact in fp32.
+// The code of v: its nearest multiple of s, ties to the even code; s > 0. Bit by bit: the borders of one
+// level are two or four of the halves between neighbours, which are few-bit multiples of s, exact in fp32.
 __device__ __forceinline__ uint32_t code_for(float v, float s) {
   const float a = fabsf(v);
-  uint32_t c = (a > 0.25f * s) + (a >= 0.75f * s) + (a > 1.25f * s) + (a >= 1.75f * s) + (a > 2.5f * s) +
-               (a >= 3.5f * s) + (a > 5.f * s);
-  return s > 0.f ? c | (v < 0.f ? 8u : 0u) : (v < 0.f ? 8u : 0u);
+  const bool b2 = a >= 1.75f * s;
+  const bool b1 = a >= (b2 ? 3.5f * s : 0.75f * s);
+  const bool b0 = a > (b1 ? (b2 ? 5.f * s : 1.25f * s) : (b2 ? 2.5f * s : 0.25f * s));
+  return (v < 0.f ? 8u : 0u) | (b2 ? 4u : 0u) | (b1 ? 2u : 0u) | (b0 ? 1u : 0u);
 }
 
 __device__ __forceinline__ float2 codes_to_float2(uint32_t byte) {
@@ -68,7 +77,7 @@ __device__ __forceinline__ uint2 encode_block(const float (&v)[16], int* scale) 
     top = fmaxf(top, fabsf(v[i]));
   }
   const int e = finite ? scale_for(top) : kCacheNanScale;
-  const float s = finite ? scale_of(e) : 1.f;
+  const float s = finite && e > 0 ? scale_of(e) : 1.f;  // e = 0: zeros only
   uint2 w = make_uint2(0, 0);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -79,139 +88,276 @@ __device__ __forceinline__ uint2 encode_block(const float (&v)[16], int* scale) 
   return finite ? w : make_uint2(0, 0);
 }
 
-// The row of the padded batch that this warp takes: its sequence, its position, its slot in the pool
-// (-1: none). False past the batch.
-struct CacheRow {
-  int b, i;
-  ll row, p, slot;
+// The same for 16 bf16 values in two chunks, by the conversion instruction on v / s. That is exact although
+// 1 / s is not: a border between two codes is a number of 3 bits times s, s one of 4, so v of 8 bits is
+// either on it or more than 2^-9 of it away. v (1 / s) is within 2^-22 of v / s, and rounded to 12 bits it
+// is the border in the first case (the conversion sends ties to the even code) and on v's side of it in the
+// other. A sum with +0 turns -0 into +0, whose code has no sign.
+__device__ __forceinline__ uint2 encode_block(const uint4 (&held)[2], int* scale) {
+  const uint32_t x[8] = {held[0].x, held[0].y, held[0].z, held[0].w, held[1].x, held[1].y, held[1].z, held[1].w};
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // sizes compare as integers; what is not finite comes out on top
+    const uint32_t a = x[i] & 0x7fff7fffu;
+    most = __vmaxu2(most, a);
+  }
+  const uint32_t top = max(most & 0xffffu, most >> 16);
+  const bool finite = top < 0x7f80u;
+  const int e = finite ? scale_for(__uint_as_float(top << 16)) : kCacheNanScale;
+  const float inv = finite && e > 0 ? 1.f / scale_of(e) : 0.f;
+  auto near = [&](float v) {
+    return __uint_as_float((__float_as_uint(fmaf(v, inv, 0.f)) + 0x800u) & 0xfffff000u);
+  };
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    b[i] = __nv_cvt_float2_to_fp4x2(make_float2(near(__uint_as_float(x[i] << 16)), near(__uint_as_float(x[i] & 0xffff0000u))),
+                                    __NV_E2M1, cudaRoundNearest);
+  *scale = e;
+  const uint2 w = make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                             __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+  return finite ? w : make_uint2(0, 0);
+}
+
+// The rows of the padded batch that a warp takes: `per` (at most 32) consecutive ones. Lane j finds the
+// place of the j-th, so that the loads behind each other that this takes are waited for once.
+struct WarpRows {
+  ll first;
+  int n;     // rows; 0 past the batch
+  ll p;      // lane's row: its position, and its slot in the pool (-1: none)
+  ll slot;
   bool stored;  // i < counts[b]
 };
-__device__ __forceinline__ bool cache_row(const CacheView& c, const CacheRows& at, int* status, int where, CacheRow& r) {
-  r.row = static_cast<ll>(blockIdx.x) * ROW_WARPS + (threadIdx.x >> 5);
-  if (r.row >= static_cast<ll>(at.pages.B) * at.rows) return false;
-  r.b = static_cast<int>(r.row / at.rows);
-  r.i = static_cast<int>(r.row - static_cast<ll>(r.b) * at.rows);
-  r.stored = !at.counts || r.i < __ldg(at.counts + r.b);
-  r.p = static_cast<ll>(__ldg(at.starts + r.b)) + r.i;
-  r.slot = r.stored ? cache_slot(c, at.pages, r.b, r.p) : -1;
-  if (r.stored && r.slot < 0 && (threadIdx.x & 31) == 0) report_page(status, where);
-  return true;
+__device__ __forceinline__ WarpRows warp_rows(const CacheRows& at, int per) {
+  WarpRows r;
+  r.first = (static_cast<ll>(blockIdx.x) * ROW_WARPS + (threadIdx.x >> 5)) * per;
+  r.n = static_cast<int>(max(0ll, min(static_cast<ll>(per), static_cast<ll>(at.pages.B) * at.rows - r.first)));
+  return r;
+}
+__device__ __forceinline__ void find_slots(const CacheView& c, const CacheRows& at, int* status, int where, WarpRows& r) {
+  const int j = threadIdx.x & 31;
+  r.p = 0;
+  r.slot = -1;
+  r.stored = false;
+  if (j >= r.n) return;
+  const ll row = r.first + j;
+  const int b = static_cast<int>(row / at.rows), i = static_cast<int>(row - static_cast<ll>(b) * at.rows);
+  r.stored = !at.counts || i < __ldg(at.counts + b);
+  r.p = static_cast<ll>(__ldg(at.starts + b)) + i;
+  if (!r.stored) return;
+  r.slot = cache_slot(c, at.pages, b, r.p);
+  if (r.slot < 0) report_page(status, where);
 }
 
-// VEC: d_c a multiple of 16 and the latents 16-byte aligned.
+// VEC: d_c a multiple of 16 and the latents 16-byte aligned. The next row's first block and key are
+// loaded before the row at hand is worked on; a lane's frequency, weights and first block of columns are
+// the same in every row (read once: lanes that index the kernel's arguments differently are served one
+// after the other).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(ROW_WARPS * 32) append_kernel(const CacheAppend a, const RopeTable t) {
+__global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) append_kernel(const CacheAppend a, const RopeTable t, int per) {
+  constexpr int N = Vec<T>::N, V = VEC ? 16 / N : 1;
   after_previous();
-  CacheRow r;
-  if (!cache_row(a.cache, a.at, a.status, 301, r) || r.slot < 0) return;
-  const int lane = threadIdx.x & 31, d_c = a.cache.d_c, bytes = a.cache.code_bytes();
-  const T* c = static_cast<const T*>(a.c_kv) + r.row * d_c;
-  uint8_t* codes = a.cache.codes + r.slot * bytes;
-  uint8_t* scales = a.cache.scales + r.slot * a.cache.blocks();
-  for (int k = lane; k < a.cache.blocks(); k += 32) {
-    float v[16];
-    if constexpr (VEC) {
-      constexpr int N = Vec<T>::N;
-#pragma unroll
-      for (int j = 0; j < 16 / N; ++j) {
-        float x[N];
-        Vec<T>::get(__ldcs(reinterpret_cast<const uint4*>(c + k * 16) + j), x);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[j * N + i] = x[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = k * 16 + i < d_c ? to_f(c[k * 16 + i]) : 0.f;
-    }
-    int e;
-    const uint2 w = encode_block(v, &e);
-    scales[k] = static_cast<uint8_t>(e);
-    if constexpr (VEC) {
-      *reinterpret_cast<uint2*>(codes + k * 8) = w;
-    } else {
-      for (int j = 0; j < 8 && k * 8 + j < bytes; ++j)
-        codes[k * 8 + j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-    }
-  }
-  const int dr = a.cache.d_rope, n = dr / 2;
-  if (dr == 0) return;
-  const T* x = static_cast<const T*>(a.k_rope) + r.row * dr;
-  T* out = static_cast<T*>(a.cache.keys) + r.slot * dr;
+  WarpRows rows = warp_rows(a.at, per);
+  if (rows.n == 0) return;
+  const int lane = threadIdx.x & 31, d_c = a.cache.d_c, bytes = a.cache.code_bytes(), blocks = a.cache.blocks();
+  const int dr = a.cache.d_rope, n = (dr + 1) / 2;  // odd only without a rotation
   const T* w = static_cast<const T*>(a.w_k);
-  float down = 1.f, f = 1.f;
-  if (w) {
-    float sum = 0.f;
-    for (int i = lane; i < dr; i += 32) sum = fmaf(to_f(x[i]), to_f(x[i]), sum);
-    sum = warp_sum(sum);
-    if (!(sum < 0x1p120f)) {  // squares that may have left fp32
-      down = 0x1p-70f;
-      sum = 0.f;
-      for (int i = lane; i < dr; i += 32) sum = fmaf(to_f(x[i]) * down, to_f(x[i]) * down, sum);
-      sum = warp_sum(sum);
-    }
-    f = rsqrtf(fmaf(sum, 1.f / dr, a.eps * down * down));
+  // a lane's pair of the key: of the rotation, and without one any two
+  const bool between = a.turn && a.rope.interleaved;
+  auto first = [&](int u) { return between ? 2 * u : u; };
+  auto second = [&](int u) { return between ? 2 * u + 1 : n + u; };
+  struct Pair {
+    float x0, x1;
+  };
+  auto pair_of = [&](const T* x, int u) {
+    return Pair{to_f(x[first(u)]), second(u) < dr ? to_f(x[second(u)]) : 0.f};
+  };
+  auto latents = [&](ll row) { return static_cast<const T*>(a.c_kv) + row * d_c; };
+  auto key = [&](ll row) { return static_cast<const T*>(a.k_rope) + row * dr; };
+  auto load = [&](ll row, int k, uint4 (&to)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) to[j] = __ldcs(reinterpret_cast<const uint4*>(latents(row) + k * 16) + j);
+  };
+  uint4 held[V], ahead[V];
+  Pair x{0.f, 0.f}, nx{0.f, 0.f}, wk{1.f, 1.f};
+  auto fetch = [&](ll row) {
+    if constexpr (VEC)
+      if (lane < blocks) load(row, lane, ahead);
+    if (lane < n) nx = pair_of(key(row), lane);
+  };
+  fetch(rows.first);
+  find_slots(a.cache, a.at, a.status, 301, rows);
+  if (w && lane < n) wk = pair_of(w, lane);
+  uint64_t turns = 0;
+  int axis = 0;
+  if (a.turn && lane < n) {
+    turns = t.turns[lane];
+    axis = t.axis[lane];
   }
-  auto value = [&](int i) { return w ? to_f(x[i]) * down * f * to_f(w[i]) : to_f(x[i]); };
-  if (!a.turn) {
-    for (int i = lane; i < dr; i += 32) out[i] = static_cast<T>(value(i));
-    return;
-  }
-  for (int u = lane; u < n; u += 32) {
-    ll p = r.p;
-    if (a.own_pos) {
-      const ll at = t.axis[u] * a.rope.tokens + r.row;
-      p = a.rope.pos64 ? static_cast<const ll*>(a.rope.pos)[at] : static_cast<ll>(static_cast<const int*>(a.rope.pos)[at]);
+
+#pragma unroll 1
+  for (int j = 0; j < rows.n; ++j) {
+    const ll row = rows.first + j, p = __shfl_sync(0xffffffffu, rows.p, j), slot = __shfl_sync(0xffffffffu, rows.slot, j);
+#pragma unroll
+    for (int i = 0; i < V; ++i) held[i] = ahead[i];
+    x = nx;
+    if (j + 1 < rows.n) fetch(row + 1);
+    if (slot < 0) continue;
+    uint8_t* codes = a.cache.codes + slot * bytes;
+    uint8_t* scales = a.cache.scales + slot * blocks;
+    for (int k = lane; k < blocks; k += 32) {
+      int e;
+      uint2 q;
+      if constexpr (VEC)
+        if (k != lane) load(row, k, held);
+      if constexpr (VEC && N == 8) {
+        q = encode_block(held, &e);
+      } else {
+        float v[16];
+        if constexpr (VEC) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float y[N];
+            Vec<T>::get(held[i], y);
+#pragma unroll
+            for (int m = 0; m < N; ++m) v[i * N + m] = y[m];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = k * 16 + i < d_c ? to_f(latents(row)[k * 16 + i]) : 0.f;
+        }
+        q = encode_block(v, &e);
+      }
+      scales[k] = static_cast<uint8_t>(e);
+      if constexpr (VEC) {
+        *reinterpret_cast<uint2*>(codes + k * 8) = q;
+      } else {
+        for (int i = 0; i < 8 && k * 8 + i < bytes; ++i)
+          codes[k * 8 + i] = static_cast<uint8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+      }
     }
-    const float2 cs = cos_sin(p, t.turns[u]);
-    const int i0 = a.rope.interleaved ? 2 * u : u, i1 = a.rope.interleaved ? 2 * u + 1 : n + u;
-    const float y0 = value(i0), y1 = value(i1);
-    out[i0] = static_cast<T>(y0 * cs.x - y1 * cs.y);
-    out[i1] = static_cast<T>(y0 * cs.y + y1 * cs.x);
+    if (dr == 0) continue;
+    T* out = static_cast<T*>(a.cache.keys) + slot * dr;
+    float down = 1.f, f = 1.f;
+    if (w) {
+      auto squares = [&](float by) {
+        float sum = 0.f;
+        for (int u = lane; u < n; u += 32) {
+          const Pair y = u == lane ? x : pair_of(key(row), u);
+          sum = fmaf(y.x0 * by, y.x0 * by, fmaf(y.x1 * by, y.x1 * by, sum));
+        }
+        return warp_sum(sum);
+      };
+      float sum = squares(1.f);
+      if (!(sum < 0x1p120f)) {  // squares that may have left fp32
+        down = 0x1p-70f;
+        sum = squares(down);
+      }
+      f = rsqrtf(fmaf(sum, 1.f / dr, a.eps * down * down));
+    }
+    for (int u = lane; u < n; u += 32) {
+      const int i0 = first(u), i1 = second(u);
+      Pair y = u == lane ? x : pair_of(key(row), u);
+      if (w) {
+        const Pair by = u == lane ? wk : pair_of(w, u);
+        y.x0 = y.x0 * down * f * by.x0;
+        y.x1 = y.x1 * down * f * by.x1;
+      }
+      if (a.turn) {
+        ll pos = p;
+        if (a.own_pos) {
+          const ll at = (u == lane ? axis : t.axis[u]) * a.rope.tokens + row;
+          pos = a.rope.pos64 ? static_cast<const ll*>(a.rope.pos)[at] : static_cast<ll>(static_cast<const int*>(a.rope.pos)[at]);
+        }
+        const float2 cs = cos_sin(pos, u == lane ? turns : t.turns[u]);
+        y = {y.x0 * cs.x - y.x1 * cs.y, y.x0 * cs.y + y.x1 * cs.x};
+      }
+      out[i0] = static_cast<T>(y.x0);
+      if (i1 < dr) out[i1] = static_cast<T>(y.x1);
+    }
   }
 }
 
+// The next row's first block and key values are loaded before the row at hand is written.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(ROW_WARPS * 32) read_kernel(const CacheRead a) {
+__global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) read_kernel(const CacheRead a, int per) {
+  constexpr int N = Vec<T>::N, KEYS = 2;  // key values of a lane that are loaded ahead
   after_previous();
-  CacheRow r;
-  if (!cache_row(a.cache, a.at, a.status, 302, r)) return;
-  const int lane = threadIdx.x & 31, d_c = a.cache.d_c, dr = a.cache.d_rope;
-  T* c = static_cast<T*>(a.c_kv) + r.row * d_c;
-  T* key = static_cast<T*>(a.k_rope) + r.row * dr;
-  const float fill = r.stored ? __int_as_float(0x7fc00000) : 0.f;  // a row that the table has no page for: NaN
-  if (r.slot < 0) {
-    for (int i = lane; i < d_c; i += 32) c[i] = static_cast<T>(fill);
-    for (int i = lane; i < dr; i += 32) key[i] = static_cast<T>(fill);
-    return;
-  }
-  const uint8_t* codes = a.cache.codes + r.slot * a.cache.code_bytes();
-  const uint8_t* scales = a.cache.scales + r.slot * a.cache.blocks();
-  const T* from = static_cast<const T*>(a.cache.keys) + r.slot * dr;
-  for (int i = lane; i < dr; i += 32) key[i] = from[i];
-  if constexpr (VEC) {
-    constexpr int N = Vec<T>::N;
-    for (int k = lane; k < a.cache.blocks(); k += 32) {
-      const uint2 w = *reinterpret_cast<const uint2*>(codes + k * 8);
-      const float s = scale_of(scales[k]);
-      float v[16];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 f = codes_to_float2(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 0xffu);
-        v[2 * j] = f.x * s;
-        v[2 * j + 1] = f.y * s;
-      }
-#pragma unroll
-      for (int j = 0; j < 16 / N; ++j) {
-        float x[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = v[j * N + i];
-        reinterpret_cast<uint4*>(c + k * 16)[j] = Vec<T>::put(x);
+  WarpRows rows = warp_rows(a.at, per);
+  if (rows.n == 0) return;
+  find_slots(a.cache, a.at, a.status, 302, rows);
+  const int lane = threadIdx.x & 31, d_c = a.cache.d_c, dr = a.cache.d_rope, blocks = a.cache.blocks();
+  uint2 w = make_uint2(0, 0), nw = w;
+  int e = 0, ne = 0;
+  T x[KEYS], nx[KEYS];
+  auto codes_of = [&](ll slot) { return a.cache.codes + slot * a.cache.code_bytes(); };
+  auto scales_of = [&](ll slot) { return a.cache.scales + slot * blocks; };
+  auto key_of = [&](ll slot) { return static_cast<const T*>(a.cache.keys) + slot * dr; };
+  auto fetch = [&](ll slot) {
+    if (slot < 0) return;
+    if constexpr (VEC) {
+      if (lane < blocks) {
+        nw = __ldcg(reinterpret_cast<const uint2*>(codes_of(slot)) + lane);
+        ne = __ldcg(scales_of(slot) + lane);
       }
     }
-  } else {
-    for (int i = lane; i < d_c; i += 32) {
-      const float2 f = codes_to_float2(codes[i >> 1]);
-      c[i] = static_cast<T>((i & 1 ? f.y : f.x) * scale_of(scales[i / kCacheBlock]));
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i)
+      if (lane + 32 * i < dr) nx[i] = __ldcg(key_of(slot) + lane + 32 * i);
+  };
+  ll next = __shfl_sync(0xffffffffu, rows.slot, 0);
+  fetch(next);
+#pragma unroll 1
+  for (int j = 0; j < rows.n; ++j) {
+    const ll row = rows.first + j, slot = next;
+    const bool stored = __shfl_sync(0xffffffffu, rows.stored, j);
+    w = nw;
+    e = ne;
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) x[i] = nx[i];
+    if (j + 1 < rows.n) {
+      next = __shfl_sync(0xffffffffu, rows.slot, j + 1);
+      fetch(next);
+    }
+    T* c = static_cast<T*>(a.c_kv) + row * d_c;
+    T* key = static_cast<T*>(a.k_rope) + row * dr;
+    if (slot < 0) {
+      const float fill = stored ? __int_as_float(0x7fc00000) : 0.f;  // a row that the table has no page for: NaN
+      for (int i = lane; i < d_c; i += 32) c[i] = static_cast<T>(fill);
+      for (int i = lane; i < dr; i += 32) key[i] = static_cast<T>(fill);
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i)
+      if (lane + 32 * i < dr) key[lane + 32 * i] = x[i];
+    for (int i = lane + 32 * KEYS; i < dr; i += 32) key[i] = __ldcg(key_of(slot) + i);
+    if constexpr (VEC) {
+      for (int k = lane; k < blocks; k += 32) {
+        if (k != lane) {
+          w = __ldcg(reinterpret_cast<const uint2*>(codes_of(slot)) + k);
+          e = __ldcg(scales_of(slot) + k);
+        }
+        const float s = value_scale(e);
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = codes_to_float2(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xffu);
+          v[2 * i] = f.x * s;
+          v[2 * i + 1] = f.y * s;
+        }
+#pragma unroll
+        for (int m = 0; m < 16 / N; ++m) {
+          float y[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) y[i] = v[m * N + i];
+          reinterpret_cast<uint4*>(c + k * 16)[m] = Vec<T>::put(y);
+        }
+      }
+    } else {
+      for (int i = lane; i < d_c; i += 32) {
+        const float2 f = codes_to_float2(__ldcg(codes_of(slot) + (i >> 1)));
+        c[i] = static_cast<T>((i & 1 ? f.y : f.x) * value_scale(__ldcg(scales_of(slot) + i / kCacheBlock)));
+      }
     }
   }
 }
@@ -534,23 +680,31 @@ __global__ void __launch_bounds__(SIMT_THREADS) simt_attn_kernel(const CacheAttn
   }
 }
 
+// Rows of a warp, so that the SMs hold all CTAs at once (as far as 32 rows go), and the CTAs.
+struct RowDeal {
+  int per;
+  unsigned grid;
+};
+RowDeal deal_rows(const CacheRows& at) {
+  const ll rows = static_cast<ll>(at.pages.B) * at.rows, warps = static_cast<ll>(ROW_CTAS) * sm_count() * ROW_WARPS;
+  const ll per = std::min<ll>(std::max<ll>((rows + warps - 1) / warps, 1), 32);
+  return {static_cast<int>(per), static_cast<unsigned>((rows + per * ROW_WARPS - 1) / (per * ROW_WARPS))};
+}
 template <typename T>
 LaunchResult append(const CacheAppend& a, const RopeTable& t, cudaStream_t st) {
-  const ll rows = static_cast<ll>(a.at.pages.B) * a.at.rows;
-  const unsigned grid = static_cast<unsigned>((rows + ROW_WARPS - 1) / ROW_WARPS);
+  const RowDeal d = deal_rows(a.at);
   const bool vec = a.cache.d_c % 16 == 0 && aligned_to_16(a.c_kv);
   LaunchResult r;
-  r.err = launch_next(vec ? append_kernel<T, true> : append_kernel<T, false>, grid, ROW_WARPS * 32, 0, st, a, t);
+  r.err = launch_next(vec ? append_kernel<T, true> : append_kernel<T, false>, d.grid, ROW_WARPS * 32, 0, st, a, t, d.per);
   if (r.err != cudaSuccess) r.what = "cache4_append";
   return r;
 }
 template <typename T>
 LaunchResult read(const CacheRead& a, cudaStream_t st) {
-  const ll rows = static_cast<ll>(a.at.pages.B) * a.at.rows;
-  const unsigned grid = static_cast<unsigned>((rows + ROW_WARPS - 1) / ROW_WARPS);
+  const RowDeal d = deal_rows(a.at);
   const bool vec = a.cache.d_c % 16 == 0 && aligned_to_16(a.c_kv);
   LaunchResult r;
-  r.err = launch_next(vec ? read_kernel<T, true> : read_kernel<T, false>, grid, ROW_WARPS * 32, 0, st, a);
+  r.err = launch_next(vec ? read_kernel<T, true> : read_kernel<T, false>, d.grid, ROW_WARPS * 32, 0, st, a, d.per);
   if (r.err != cudaSuccess) r.what = "cache4_read";
   return r;
 }

@@ -152,6 +152,35 @@ def test_every_scale_and_special_values(dtype):
     assert abs(c[2 * 226 + 1]).max() == 61440 and np.isnan(c[-3:]).all()
 
 
+def test_every_bf16_value_next_to_the_borders():
+    """All bf16 values from an eighth of a scale to its largest multiple, both signs, for each form of a scale."""
+    blocks = []
+    for e in (1, 2, 3, 5, 7, 8, 9, 11, 15, *range(120, 128), 219, 225, 226):
+        s = float(cref.scale_values()[e])
+        lo, hi = (int(torch.tensor(v, dtype=torch.bfloat16).view(torch.int16)) for v in (s / 8, 6 * s))
+        v = torch.arange(lo, hi + 1, dtype=torch.int16).view(torch.bfloat16)
+        v = v[v.double() <= 6 * s]
+        v = torch.cat([v, -v])
+        v = torch.cat([v, v.new_zeros(-v.numel() % 15)]).view(-1, 15)
+        blocks.append(torch.cat([v.new_full((v.shape[0], 1), 6 * s), v], 1))
+    x = torch.cat(blocks)
+    n = x.shape[0]
+    cache = pool(n, 1, 16, 0, torch.bfloat16)
+    table = torch.arange(n, dtype=torch.int32, device=dev())[None].contiguous()
+    laga.cache4_append(cache, x[None].to(dev()), torch.empty(1, n, 0, dtype=torch.bfloat16, device=dev()), table, i32(0))
+    codes, scales, _ = cref.encode(x.double().numpy())
+    assert np.array_equal(cache.scales.cpu().numpy()[:, 0], scales) and np.array_equal(cache.codes.cpu().numpy()[:, 0], codes)
+
+
+@pytest.mark.parametrize("d_c", [32, 20])
+def test_bytes_past_the_largest_scale_are_not_finite(d_c):
+    cache = laga.cache4(1, 256, d_c, 0, torch.float32, dev())
+    cache.codes.fill_(0x21)
+    cache.scales.copy_(torch.arange(256, device=dev(), dtype=torch.uint8)[None, :, None].expand_as(cache.scales))
+    c, _ = laga.cache4_read(cache, torch.zeros(1, 1, dtype=torch.int32, device=dev()), i32(0), 256)
+    assert torch.equal(c[0].isnan().all(1), torch.arange(256, device=dev()) > cref.TOP) and c[0, :cref.TOP + 1].isfinite().all()
+
+
 def test_keys_turned_by_positions_of_several_axes():
     B, S, dr = 2, 13, 24
     cache = pool(8, 8, 32, dr, torch.float32)
