@@ -565,52 +565,68 @@ __global__ void __launch_bounds__(SIMT_THREADS) simt_attn_kernel(const CacheAttn
     for (; t < stop; ++t) {
       const int key0 = (hull.x / kSimtKeys + (t - item_begin)) * kSimtKeys;
       __syncthreads();
-      if (threadIdx.x < kSimtKeys) bad[threadIdx.x] = 0;
-      __syncthreads();
-      for (int k = warp; k < kSimtKeys; k += SIMT_THREADS / 32) {
-        float* to = sk + k * stride;
-        const int p = key0 + k;
-        const ll slot = p >= hull.x && p < hull.y ? cache_slot(a.cache, a.pages, b, p) : -1;
-        if (slot < 0) {
-          for (int i = lane; i < D; i += 32) to[i] = 0.f;
-          if (lane == 0 && p >= hull.x && p < hull.y) {
-            bad[k] = 1;
-            report_page(a.status, 304);
+      // Eight keys a warp, a lane finds the place of one; all eight's loads are under way at once.
+      const int p = key0 + 8 * warp + (lane & 7);
+      const bool wanted = p >= hull.x && p < hull.y;
+      const ll mine = wanted ? cache_slot(a.cache, a.pages, b, p) : -1;
+      uint32_t strange = wanted && mine < 0 ? 1u << (lane & 7) : 0u;  // a bit a key: it is not finite
+      if (strange && lane < 8) report_page(a.status, 304);
+      float* to = sk + 8 * warp * stride;
+      const int bytes = a.cache.code_bytes(), blocks = a.cache.blocks();
+      for (int i0 = 0; i0 < bytes; i0 += 32) {
+        const int i = i0 + lane;
+        uint32_t code[8], e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const ll slot = __shfl_sync(0xffffffffu, mine, k);
+          code[k] = e[k] = 0;
+          if (slot >= 0 && i < bytes) {
+            code[k] = __ldcg(a.cache.codes + slot * bytes + i);
+            e[k] = __ldcg(a.cache.scales + slot * blocks + i / (kCacheBlock / 2));
           }
-          continue;
         }
-        const uint8_t* codes = a.cache.codes + slot * a.cache.code_bytes();
-        const uint8_t* scales = a.cache.scales + slot * a.cache.blocks();
-        const T* key = static_cast<const T*>(a.cache.keys) + slot * dr;
-        bool fine = true;
-        for (int i = lane; i < (d_c + 1) / 2; i += 32) {
-          const int e = scales[i / (kCacheBlock / 2)];
-          const float2 f = codes_to_float2(codes[i]);
-          const float s = scale_of(e);
-          fine = fine && e <= kCacheTopScale;
-          to[2 * i] = f.x * s;
-          if (2 * i + 1 < d_c) to[2 * i + 1] = f.y * s;
-        }
-        for (int i = lane; i < dr; i += 32) {
-          const float v = to_f(key[i]);
-          fine = fine && fabsf(v) <= 3.402823466e38f;
-          to[d_c + i] = v;
-        }
-        if (!__all_sync(0xffffffffu, fine)) {
-          for (int i = lane; i < D; i += 32) to[i] = 0.f;
-          if (lane == 0) bad[k] = 1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const bool number = e[k] <= kCacheTopScale;
+          if (!number) strange |= 1u << k;
+          const float2 f = codes_to_float2(code[k]);
+          const float by = number ? scale_of(e[k]) : 0.f;
+          if (2 * i < d_c) to[k * stride + 2 * i] = f.x * by;
+          if (2 * i + 1 < d_c) to[k * stride + 2 * i + 1] = f.y * by;
         }
       }
+      for (int i0 = 0; i0 < dr; i0 += 32) {
+        const int i = i0 + lane;
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const ll slot = __shfl_sync(0xffffffffu, mine, k);
+          x[k] = slot >= 0 && i < dr ? to_f(__ldcg(static_cast<const T*>(a.cache.keys) + slot * dr + i)) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const bool number = fabsf(x[k]) <= 3.402823466e38f;
+          if (!number) strange |= 1u << k;
+          if (i < dr) to[k * stride + d_c + i] = number ? x[k] : 0.f;
+        }
+      }
+      strange = __reduce_or_sync(0xffffffffu, strange);
+      if (lane < 8) bad[8 * warp + lane] = (strange >> lane) & 1u;
       __syncthreads();
+      float both[2] = {0.f, 0.f};
+      {
+        const float *x = sq + 2 * warp * D, *y = sk + lane * stride;
+#pragma unroll 8
+        for (int k = 0; k < D; ++k) {
+          both[0] = fmaf(x[k], y[k], both[0]);
+          both[1] = fmaf(x[D + k], y[k], both[1]);
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int r = warp * 2 + j, p = key0 + lane;
         const int2 seen = bounds[r];
-        float s = 0.f;
-        const float* x = sq + r * D;
-        const float* y = sk + lane * stride;
-        for (int k = 0; k < D; ++k) s = fmaf(x[k], y[k], s);
-        s *= a.scale;
+        float s = both[j] * a.scale;
         if (a.mods.cap > 0.f) s = a.mods.cap * tanhf(s / a.mods.cap);
         if (a.mods.slopes) {
           const int i = (r0 + r) / a.n_h, h = (r0 + r) - i * a.n_h;
@@ -639,10 +655,15 @@ __global__ void __launch_bounds__(SIMT_THREADS) simt_attn_kernel(const CacheAttn
         if (col >= d_c) break;
 #pragma unroll
         for (int r = 0; r < kSimtRows; ++r) acc[r][c] *= sa[r];
-        for (int k = 0; k < kSimtKeys; ++k) {
-          const float v = sk[k * stride + col];
+#pragma unroll 2
+        for (int k = 0; k < kSimtKeys; k += 4) {
+          const float* v = sk + k * stride + col;
+          const float v0 = v[0], v1 = v[stride], v2 = v[2 * stride], v3 = v[3 * stride];
 #pragma unroll
-          for (int r = 0; r < kSimtRows; ++r) acc[r][c] = fmaf(sp[r * kSimtKeys + k], v, acc[r][c]);
+          for (int r = 0; r < kSimtRows; ++r) {
+            const float4 w = *reinterpret_cast<const float4*>(sp + r * kSimtKeys + k);
+            acc[r][c] = fmaf(w.w, v3, fmaf(w.z, v2, fmaf(w.y, v1, fmaf(w.x, v0, acc[r][c]))));
+          }
         }
       }
     }
