@@ -364,11 +364,6 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) read_kernel(const Ca
 
 // ---------------------------------------------------------------- sharing out and joining
 
-__global__ void __launch_bounds__(1024) plan_kernel(const CacheAttn a) {
-  after_previous();
-  cache4_plan_items<1024>(a);
-}
-
 // Rows blockIdx.y, + gridDim.y, .. of item blockIdx.x. The pieces' weights first, in shared memory (128
 // pieces at a time), then the columns, four a thread, all of a batch's loads before its sums.
 constexpr int JOIN_THREADS = 128;
@@ -461,11 +456,16 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const CacheAttn a, f
 // ---------------------------------------------------------------- CUDA cores, any widths
 
 // q_lat[token][h][c] = sum over k of q[token][h][k] W_UK[c][h d_nope + k]: 32 tokens x 32 columns a CTA.
+// One more CTA makes the plan.
 template <typename T>
-__global__ void __launch_bounds__(256) simt_qlat_kernel(int tokens, int n_h, int d_c, int d_nope, int d_qk, const T* q,
-                                                        const T* W, float* q_lat) {
+__global__ void __launch_bounds__(256) simt_prepare_kernel(const CacheAttn a, int d_nope, const T* q, const T* W, float* q_lat) {
   __shared__ float sq[32][33], sw[32][33];
   after_previous();
+  if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) cache4_plan_items<256>(a);
+    return;
+  }
+  const int tokens = a.pages.B * a.Sq, n_h = a.n_h, d_c = a.cache.d_c, d_qk = d_nope + a.cache.d_rope;
   const int c0 = blockIdx.x * 32, h = blockIdx.y, x = threadIdx.x & 31, y = threadIdx.x >> 5;
   for (int t0 = blockIdx.z * 32; t0 < tokens; t0 += gridDim.z * 32) {
     float acc[4] = {};
@@ -743,13 +743,6 @@ LaunchResult cache4_read(const CacheRead& a, cudaStream_t st) {
   return a.cache.is_bf16 ? read<bf16>(a, st) : read<float>(a, st);
 }
 
-LaunchResult cache4_plan(const CacheAttn& a, cudaStream_t st) {
-  LaunchResult r;
-  r.err = launch_next(plan_kernel, 1, 1024, 0, st, a);
-  if (r.err != cudaSuccess) r.what = "cache4_plan";
-  return r;
-}
-
 LaunchResult cache4_join(const CacheAttn& a, float* ctx, cudaStream_t st) {
   LaunchResult r;
   const ll rows = static_cast<ll>(a.items()) * std::min(a.tile, a.rows);
@@ -759,16 +752,15 @@ LaunchResult cache4_join(const CacheAttn& a, float* ctx, cudaStream_t st) {
   return r;
 }
 
-LaunchResult cache4_simt_qlat(const CacheAttn& a, bool is_bf16, int d_nope, const void* q, const void* W_UK, float* q_lat,
-                              cudaStream_t st) {
+LaunchResult cache4_simt_prepare(const CacheAttn& a, bool is_bf16, int d_nope, const void* q, const void* W_UK, float* q_lat,
+                                 cudaStream_t st) {
   LaunchResult r;
-  const int tokens = a.pages.B * a.Sq, d_c = a.cache.d_c, d_qk = d_nope + a.cache.d_rope;
-  const dim3 grid((d_c + 31) / 32, a.n_h, token_tiles(a));
-  r.err = is_bf16 ? launch_next(simt_qlat_kernel<bf16>, grid, 256, 0, st, tokens, a.n_h, d_c, d_nope, d_qk,
-                                static_cast<const bf16*>(q), static_cast<const bf16*>(W_UK), q_lat)
-                  : launch_next(simt_qlat_kernel<float>, grid, 256, 0, st, tokens, a.n_h, d_c, d_nope, d_qk,
-                                static_cast<const float*>(q), static_cast<const float*>(W_UK), q_lat);
-  if (r.err != cudaSuccess) r.what = "cache4_simt_qlat";
+  const dim3 grid((a.cache.d_c + 31) / 32 + 1, a.n_h, token_tiles(a));
+  r.err = is_bf16 ? launch_next(simt_prepare_kernel<bf16>, grid, 256, 0, st, a, d_nope, static_cast<const bf16*>(q),
+                                static_cast<const bf16*>(W_UK), q_lat)
+                  : launch_next(simt_prepare_kernel<float>, grid, 256, 0, st, a, d_nope, static_cast<const float*>(q),
+                                static_cast<const float*>(W_UK), q_lat);
+  if (r.err != cudaSuccess) r.what = "cache4_simt_prepare";
   return r;
 }
 

@@ -84,12 +84,11 @@ struct CacheAttn {
   __host__ __device__ int items() const { return pages.B * row_tiles; }
 };
 
-LaunchResult cache4_plan(const CacheAttn& a, cudaStream_t st);
 // CUDA cores, any widths: q_lat and ctx in fp32. The join joins split items (maxima in natural units) and
 // fills the rows of empty ones.
 constexpr int kSimtRows = 8, kSimtKeys = 32;
-LaunchResult cache4_simt_qlat(const CacheAttn& a, bool is_bf16, int d_nope, const void* q, const void* W_UK, float* q_lat,
-                              cudaStream_t st);
+LaunchResult cache4_simt_prepare(const CacheAttn& a, bool is_bf16, int d_nope, const void* q, const void* W_UK,
+                                 float* q_lat, cudaStream_t st);
 LaunchResult cache4_simt_attn(const CacheAttn& a, bool is_bf16, int d_nope, const void* q, const float* q_lat, float* ctx,
                               cudaStream_t st);
 LaunchResult cache4_join(const CacheAttn& a, float* ctx, cudaStream_t st);

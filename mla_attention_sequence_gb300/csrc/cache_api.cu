@@ -77,8 +77,16 @@ laga_status check_rows(int64_t batch, int64_t rows, int64_t max_pages, const int
   return LAGA_OK;
 }
 
-// Rows of a sequence up to which mma.sync's form is used.
-constexpr int kFewRows = 64;
+// Which form of the tensor cores: mma.sync's time goes with the tiles of 16 rows, the tcgen05 form's with
+// tiles of 128, and it begins later. Kernel's time in us at 16, 32, 48 and 64 rows a sequence, mma.sync :
+// tcgen05 (events):
+//   48 sequences of 2000 .. 8192 tokens   55 : 102   95 : 105   133 : 105   175 : 105
+//   8 of them                             20 : 31    27 : 32    35 : 31     41 : 31
+//   one of 8000                           14 : 20    16 : 20    17 : 18     18 : 18
+//   one of 600                            12 : 14    12 : 14    12 : 14     12 : 14
+// So mma.sync up to 32 rows, and up to 64 while what the table has room for is at most about three of its
+// key tiles for each of its CTAs.
+constexpr int kFewRows = 32, kFewRowsShort = 64, kShortTiles = 3;
 
 struct AttnSizes {
   CacheAttn a;
@@ -120,7 +128,8 @@ laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cach
                                    : 1.f / std::sqrt(static_cast<float>(d->d_nope + cache->d_rope));
   s->tc = d->variant == LAGA_VARIANT_AUTO && a.cache.is_bf16 && a.cache.d_c == 512 && a.cache.d_rope == 64 &&
           s->d_nope == 128 && s->d_v == 128;
-  s->few = s->tc && a.rows <= kFewRows;
+  const double short_tiles = static_cast<double>(d->batch) * ((a.rows + kMmaRows - 1) / kMmaRows) * d->max_pages * cache->page_size / kMmaKeys;
+  s->few = s->tc && (a.rows <= kFewRows || (a.rows <= kFewRowsShort && short_tiles <= kShortTiles * 2. * sm_count()));
   a.tile = s->few ? kMmaRows : s->tc ? kTcRows : kSimtRows;
   a.keys = s->few ? kMmaKeys : s->tc ? kTcKeys : kSimtKeys;
   // tcgen05: two CTAs a part, one a SM; else one, two a SM
@@ -306,8 +315,7 @@ laga_status laga_mla_cache4_fwd(const laga_mla_cache4_desc* desc, const laga_mla
     return from_launch(r);
   }
   float* q_lat = reinterpret_cast<float*>(x.query);
-  r = timed("cache4_plan", s, [&] { return cache4_plan(a, s); });
-  if (r.ok()) r = timed("cache4_qlat", s, [&] { return cache4_simt_qlat(a, b16, z.d_nope, q, W_UK, q_lat, s); });
+  r = timed("cache4_prepare", s, [&] { return cache4_simt_prepare(a, b16, z.d_nope, q, W_UK, q_lat, s); });
   if (r.ok()) r = timed("cache4_attn", s, [&] { return cache4_simt_attn(a, b16, z.d_nope, q, q_lat, x.ctx, s); });
   if (r.ok()) r = timed("cache4_join", s, [&] { return cache4_join(a, x.ctx, s); });
   if (r.ok()) r = timed("cache4_out", s, [&] { return cache4_simt_out(a, b16, z.d_v, x.ctx, W_UV, out, s); });
