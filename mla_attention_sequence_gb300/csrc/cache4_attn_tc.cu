@@ -37,10 +37,11 @@ constexpr int NBOX = 9, QBOX = 16384, KBOX = 8192;
 constexpr int Q_TMEM = 4;                    // query boxes in TMEM
 constexpr int K_BYTES = NBOX * KBOX;
 constexpr int Q_BYTES = (NBOX - Q_TMEM) * QBOX;
-constexpr int SMEM_BYTES = 2 * K_BYTES + Q_BYTES + 1024 + 256;
+constexpr int SMEM_BYTES = 2 * K_BYTES + Q_BYTES + 1024 + 512;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 constexpr int SOFTMAX_WARPS = 4, PRODUCER_WARPS = 8, MMA_WARP = 4;
-constexpr int NTHREADS = 512;  // warps 8, 12 and 15 have no work
+constexpr int NTHREADS = 768;  // warps 8, 12 and 16 have no work
+constexpr int SOFTMAX_REGS = 120, OTHER_REGS = 72;  // of 80 a thread at launch: 120 + 5 * 72 = 6 * 80
 constexpr uint32_t TMEM_COLS = 512, COL_S = 128, COL_O = 256;
 constexpr int HALF = 256;
 // kind::f16 with fp16 operands is idesc_bf16 without the two type fields
@@ -57,35 +58,191 @@ struct Params {
 };
 
 
-// What a producer lane holds of one key tile: of each two latent boxes (first the two pairs outside this
-// CTA's half of the values) 16 bytes of codes, two blocks, and their scales; two of the key's eight RoPE
-// chunks. Few wide loads: every load of a warp touches eight
-// keys' lines, and with a load a block and a scale (18 instead of 10) they and the stores behind them took
-// longer than the products.
+// A producer lane's key in the tile to be loaded next: its place among the sequence's pages, kept from tile
+// to tile, and its page, fetched a tile before it is used (the fetch behind the loads that need it took a
+// third of a producer's time).
+struct KeyPlace {
+  int at, page_row, id;
+  uint32_t page_of;
+  bool wanted;
+  __device__ __forceinline__ void fetch(const CacheAttn& a, const Piece& p) {
+    wanted = at >= p.hull.x && at < p.hull.y;
+    const uint32_t k = min(page_of, static_cast<uint32_t>(a.pages.most - 1));
+    id = wanted ? __ldg(a.pages.table + static_cast<ll>(p.b) * a.pages.most + k) : -1;
+    if (page_of != k) id = -1;
+  }
+  __device__ __forceinline__ void begin(const CacheAttn& a, const Piece& p, int key) {
+    at = p.key0 + key;
+    page_of = static_cast<uint32_t>(at) / static_cast<uint32_t>(a.cache.page);
+    page_row = at - static_cast<int>(page_of) * a.cache.page;
+    fetch(a, p);
+  }
+  __device__ __forceinline__ void step(const CacheAttn& a, const Piece& p) {
+    at += BKV;
+    page_row += BKV;
+    if (page_row >= a.cache.page) {
+      page_row -= a.cache.page;
+      ++page_of;
+      if (page_row >= a.cache.page) {  // pages of less than a tile
+        const int k = page_row / a.cache.page;
+        page_row -= k * a.cache.page;
+        page_of += k;
+      }
+    }
+    fetch(a, p);
+  }
+};
+
+// What a producer lane holds of one key tile: of each of two latent pairs of boxes (FIRST: those outside
+// this CTA's half of the values, else those of it) 16 bytes of codes, two blocks, and their scales; FIRST
+// also two of the key's eight RoPE chunks. Few wide loads: every load of a warp touches eight keys' lines.
+template <bool FIRST>
 struct Held {
-  uint4 codes[4], rope[2];
-  uint32_t scales[4];
+  uint4 codes[2], rope[FIRST ? 2 : 1];
+  uint32_t scales[2];
   bool live, bad;  // a key to expand (else zeros); a key that should be there and is not
 };
-__device__ __forceinline__ void hold(const CacheAttn& a, const Piece& p, int tile, int key, int lane4, int vh, Held& h) {
-  const int at = p.key0 + tile * BKV + key;
-  const bool wanted = at >= p.hull.x && at < p.hull.y;
-  bool there;
-  const ll slot = cache_slot_of(a.cache, a.pages, p.b, wanted ? at : p.hull.x, &there);
-  h.live = wanted && there;
-  h.bad = wanted && !there;
-  const uint4* c = reinterpret_cast<const uint4*>(a.cache.codes + slot * 256) + lane4;
-  const uint16_t* s = reinterpret_cast<const uint16_t*>(a.cache.scales + slot * 32) + lane4;
-  const uint4* r = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.cache.keys) + slot * 64) + 2 * lane4;
+template <bool FIRST>
+__device__ __forceinline__ void hold(const CacheAttn& a, const KeyPlace& k, int lane4, int half, Held<FIRST>& h) {
+  const bool there = k.id >= 0 && k.id < a.cache.pages;
+  h.live = k.wanted && there;
+  h.bad = k.wanted && !there;
+  const ll slot = h.live ? static_cast<ll>(k.id) * a.cache.page + k.page_row : 0;
+  const uint4* c = reinterpret_cast<const uint4*>(a.cache.codes + slot * 256 + 128 * half) + lane4;
+  const uint16_t* s = reinterpret_cast<const uint16_t*>(a.cache.scales + slot * 32 + 16 * half) + lane4;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    h.codes[k] = __ldg(c + 4 * (2 * (1 - vh) + k));
-    h.codes[2 + k] = __ldg(c + 4 * (2 * vh + k));
-    h.scales[k] = __ldg(s + 4 * (2 * (1 - vh) + k));
-    h.scales[2 + k] = __ldg(s + 4 * (2 * vh + k));
+  for (int i = 0; i < 2; ++i) {
+    h.codes[i] = __ldg(c + 4 * i);
+    h.scales[i] = __ldg(s + 4 * i);
   }
-  h.rope[0] = __ldg(r);
-  h.rope[1] = __ldg(r + 1);
+  if constexpr (FIRST) {
+    const uint4* r = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.cache.keys) + slot * 64) + 2 * lane4;
+    h.rope[0] = __ldg(r);
+    h.rope[1] = __ldg(r + 1);
+  }
+}
+
+template <int REGS, bool MORE>
+__device__ __forceinline__ void take_registers() {
+  if constexpr (MORE)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+// A producer warp: keys [8 pw, 8 pw + 8) of every key tile, FIRST the boxes outside this CTA's half of the
+// values and the RoPE box, else the others. Four lanes a key.
+template <bool FIRST>
+__device__ __forceinline__ void expand_tiles(const CacheAttn& a, Walk<BQ, BKV>& walk, int pw, int vh, uint8_t* sK, uint64_t* full,
+                                             uint64_t* free_, uint32_t* bad, volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31, key = 8 * pw + (lane >> 2), b4 = lane & 3, half = FIRST ? 1 - vh : vh;
+  const uint32_t row = static_cast<uint32_t>(key);
+  const bool turned = (b4 & 2) != 0;
+  const uint32_t pick = turned ? 0x4441u : 0x4440u;  // the first stored block's scale; the other's with bit 0 turned
+  // A lane's two blocks are a half of a box's row, its upper lanes' in the other order, so that eight lanes
+  // (two keys) store to eight different 16-byte columns.
+  const uint32_t chunk = 4 * (b4 & 1) + (b4 & 2);
+  const uint32_t offs[4] = {sw128_offset(row, chunk), sw128_offset(row, chunk + 1), sw128_offset(row, chunk ^ 2),
+                            sw128_offset(row, (chunk ^ 2) + 1)};
+  uint8_t* const boxes = sK + (4 * half + (b4 >> 1)) * KBOX;
+  Piece pc;
+  Held<FIRST> cur;
+  KeyPlace place;
+  int left = 0;
+  bool more = walk.next(pc);  // a tile whose place is known
+  auto begin_piece = [&]() {
+    left = pc.tiles;
+    place.begin(a, pc, key);
+  };
+  auto take = [&]() {  // that tile's bytes, and the place of the one behind it
+    hold<FIRST>(a, place, b4, half, cur);
+    if (--left > 0) {
+      place.step(a, pc);
+    } else {
+      more = walk.next(pc);
+      if (more) begin_piece();
+    }
+  };
+  if (!more) return;
+  begin_piece();
+  take();
+  bool held = true;
+  struct Pair {
+    uint4 v[4];
+  };
+  auto expand = [&](int i) {
+    const uint32_t two = cur.live ? cur.scales[i] : 0u;
+    const uint32_t s0 = __byte_perm(two, 0, pick) * 0x800080u, s1 = __byte_perm(two, 0, pick ^ 1u) * 0x800080u;
+    const uint4 w = cur.codes[i];
+    return Pair{{expand8(turned ? w.z : w.x, s0), expand8(turned ? w.w : w.y, s0), expand8(turned ? w.x : w.z, s1),
+                 expand8(turned ? w.y : w.w, s1)}};
+  };
+#pragma unroll 1
+  for (int n = 0; held; ++n) {
+    LAGA_TRACE_POINT(cache4, FIRST ? 0 : 3, n);
+    const int buf = n & 1;
+    const uint32_t ph = static_cast<uint32_t>(((n >> 1) & 1) ^ 1);
+    uint8_t* const to = boxes + buf * K_BYTES;
+    auto store = [&](const Pair& p, int i) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) *reinterpret_cast<uint4*>(to + 2 * i * KBOX + offs[x]) = p.v[x];
+    };
+    // A block that reads as NaN: zeros here, and every row that sees the key gets NaN. All scales at once: a
+    // byte above the largest scale has its upper bit and the sum's set.
+    static_assert(kCacheTopScale == 0xe2, "the sum below");
+    const uint32_t s01 = cur.scales[0] | cur.scales[1] << 16;
+    const uint32_t over = ((s01 & 0x7f7f7f7fu) + 0x1d1d1d1du) & s01 & 0x80808080u;
+    bool fine = over == 0 || !cur.live;
+    if (FIRST) {
+      fine = fine && !cur.bad;
+      if (cur.bad && b4 == 0) report_page(a.status, 305);
+    }
+    if (__any_sync(0xffffffffu, over != 0)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if ((cur.scales[i] & 0xffu) > kCacheTopScale) cur.scales[i] &= 0xff00u;
+        if ((cur.scales[i] >> 8) > kCacheTopScale) cur.scales[i] &= 0xffu;
+      }
+    }
+    // The next tile's bytes go into the same registers, as soon as these have been expanded: a wait for one
+    // of a warp's loads can be a wait for all that are under way.
+    auto advance = [&]() {
+      held = more;
+      if (more) take();
+    };
+    if constexpr (FIRST) {
+      // free since the scores of two tiles before: expanded and stored pair by pair
+      if (!pass(&free_[buf], ph, abort_flag, 401)) return;
+      LAGA_TRACE_POINT(cache4, 1, n);
+      store(expand(0), 0);
+      const Pair v1 = expand(1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool number = finite8(cur.rope[i]);
+        fine = fine && (number || !cur.live);
+        if (!(number && cur.live)) cur.rope[i] = make_uint4(0, 0, 0, 0);
+      }
+      uint8_t* rope = sK + buf * K_BYTES + 8 * KBOX;
+      *reinterpret_cast<uint4*>(rope + sw128_offset(row, 2 * b4)) = cur.rope[0];
+      *reinterpret_cast<uint4*>(rope + sw128_offset(row, 2 * b4 + 1)) = cur.rope[1];
+      advance();
+      store(v1, 1);
+    } else {
+      // free since the context of two tiles before, just before they are needed: expanded ahead
+      const Pair v0 = expand(0), v1 = expand(1);
+      advance();
+      if (!pass(&free_[buf], ph, abort_flag, 402)) return;
+      LAGA_TRACE_POINT(cache4, 4, n);
+      store(v0, 0);
+      store(v1, 1);
+    }
+    const uint32_t odd = ~__ballot_sync(0xffffffffu, fine);  // four lanes a key
+    if (lane == 0) bad[(n & 3) * 16 + (FIRST ? 0 : 8) + pw] = odd;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[buf]);
+    LAGA_TRACE_POINT(cache4, FIRST ? 2 : 16, n);
+  }
 }
 
 // Shared-memory descriptors differ in their low words alone (the address, and for MN-major tiles the
@@ -159,7 +316,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
   uint64_t* q_rest = bars + 14;   // the other boxes are there
   uint64_t* q_idle = bars + 15;   // the softmax warps are done with the queries' place
   uint64_t* drain = bars + 11;
-  uint32_t* bad = reinterpret_cast<uint32_t*>(bars + 20);  // [2][8] of each expanding warp: lanes whose key does not count as finite
+  uint32_t* bad = reinterpret_cast<uint32_t*>(bars + 20);  // [4][16] of each producer, tiles in turn: lanes whose key is not finite
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -198,96 +355,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
   Walk<BQ, BKV> walk(a, part);
   Piece pc;
   if (warp > MMA_WARP) {
-    // ---------------- expand key tiles
-    const int pw = warp - 5 - (warp > 8) - (warp > 12), key = 8 * pw + (lane >> 2), b4 = lane & 3;
-    const uint32_t row = static_cast<uint32_t>(key);
-    const uint32_t off0 = sw128_offset(row, 2 * b4), off1 = sw128_offset(row, 2 * b4 + 1);  // RoPE chunks
-    const bool turned = (b4 & 2) != 0;
-    const uint32_t pick = turned ? 0x4441u : 0x4440u;  // the first stored block's scale; the other's with bit 0 turned
-    const uint32_t chunk = 4 * (b4 & 1) + (b4 & 2);
-    const uint32_t offs[4] = {sw128_offset(row, chunk), sw128_offset(row, chunk + 1), sw128_offset(row, chunk ^ 2),
-                              sw128_offset(row, (chunk ^ 2) + 1)};
-    int n = 0;
-    bool ok = true, more = warp % 4 != 0 && warp < 15 && walk.next(pc);
-    int j = 0;
-    Held cur;
-    if (more) hold(a, pc, 0, key, b4, vh, cur);
-    while (more && ok) {
-      LAGA_TRACE_POINT(cache4, 0, n);
-      if (cur.bad && b4 == 0) report_page(a.status, 305);
-      const int buf = n & 1;
-      const uint32_t ph = static_cast<uint32_t>(((n >> 1) & 1) ^ 1);
-      uint8_t* k = sK + buf * K_BYTES;
-      bool fine = !cur.bad;
-      // The held pair j, boxes 2 i and 2 i + 1: a lane's two blocks are a half of a box's row, its upper
-      // lanes' in the other order, so that eight lanes (two keys) store to eight different 16-byte columns.
-      // A block that reads as NaN: zeros here, and every row that sees the key gets NaN.
-      struct Pair {
-        uint4 v[4];
-      };
-      // all eight scales at once: a byte above the largest scale has its upper bit and the sum's set
-      static_assert(kCacheTopScale == 0xe2, "the sum below");
-      const uint32_t s01 = cur.scales[0] | cur.scales[1] << 16, s23 = cur.scales[2] | cur.scales[3] << 16;
-      const uint32_t over = ((((s01 & 0x7f7f7f7fu) + 0x1d1d1d1du) & s01) | (((s23 & 0x7f7f7f7fu) + 0x1d1d1d1du) & s23)) & 0x80808080u;
-      fine = fine && (over == 0 || !cur.live);
-      if (__any_sync(0xffffffffu, over != 0)) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if ((cur.scales[j] & 0xffu) > kCacheTopScale) cur.scales[j] &= 0xff00u;
-          if ((cur.scales[j] >> 8) > kCacheTopScale) cur.scales[j] &= 0xffu;
-        }
-      }
-      auto expand = [&](int j) {
-        const uint32_t two = cur.live ? cur.scales[j] : 0u;
-        const uint32_t s0 = __byte_perm(two, 0, pick) * 0x800080u, s1 = __byte_perm(two, 0, pick ^ 1u) * 0x800080u;
-        const uint4 w = cur.codes[j];
-        return Pair{{expand8(turned ? w.z : w.x, s0), expand8(turned ? w.w : w.y, s0), expand8(turned ? w.x : w.z, s1),
-                     expand8(turned ? w.y : w.w, s1)}};
-      };
-      auto store = [&](const Pair& p, int i) {
-        uint8_t* to = k + (2 * i + (b4 >> 1)) * KBOX;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) *reinterpret_cast<uint4*>(to + offs[x]) = p.v[x];
-      };
-      const Pair a0 = expand(0), a1 = expand(1);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool number = finite8(cur.rope[i]);
-        fine = fine && (number || !cur.live);
-        if (!(number && cur.live)) cur.rope[i] = make_uint4(0, 0, 0, 0);
-      }
-      const Pair v0 = expand(2), v1 = expand(3);
-      const uint4 r0 = cur.rope[0], r1 = cur.rope[1];
-      // The next tile's bytes into the same registers, now: a wait for one of a warp's loads can be a wait
-      // for all that are under way, so that loads issued before the expansion were waited for there.
-      if (++j == pc.tiles) {
-        j = 0;
-        more = walk.next(pc);
-      }
-      if (more) hold(a, pc, j, key, b4, vh, cur);
-      if (!pass(&ka_free[buf], ph, abort_flag, 401)) break;
-      LAGA_TRACE_POINT(cache4, 1, n);
-      store(a0, 2 * (1 - vh));
-      store(a1, 2 * (1 - vh) + 1);
-      *reinterpret_cast<uint4*>(k + 8 * KBOX + off0) = r0;
-      *reinterpret_cast<uint4*>(k + 8 * KBOX + off1) = r1;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ka_full[buf]);
-      LAGA_TRACE_POINT(cache4, 2, n);
-      if (!pass(&kb_free[buf], ph, abort_flag, 402)) break;
-      LAGA_TRACE_POINT(cache4, 3, n);
-      store(v0, 2 * vh);
-      store(v1, 2 * vh + 1);
-      const uint32_t odd = ~__ballot_sync(0xffffffffu, fine);  // four lanes a key
-      if (lane == 0) bad[buf * 8 + pw] = odd;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&kb_full[buf]);
-      LAGA_TRACE_POINT(cache4, 4, n);
-      ++n;
-    }
+    take_registers<OTHER_REGS, false>();
+    // ---------------- expand key tiles: warps 4 k excepted, but for the last
+    const int pw = warp == 20 ? 15 : warp % 4 == 0 ? 16 : warp - 5 - (warp > 8) - (warp > 12) - (warp > 16) - (warp > 20);
+    if (pw < PRODUCER_WARPS)
+      expand_tiles<true>(a, walk, pw, vh, sK, ka_full, ka_free, bad, abort_flag);
+    else if (pw < 2 * PRODUCER_WARPS)
+      expand_tiles<false>(a, walk, pw - PRODUCER_WARPS, vh, sK, kb_full, kb_free, bad, abort_flag);
   } else if (warp == MMA_WARP) {
+    take_registers<OTHER_REGS, false>();
     // ---------------- products
     bool ok = true, issued = false;
     const uint32_t q_low = desc_low(sQ, 16), k_low = desc_low(sK, 16), v_low = desc_low(sK + vh * 4 * KBOX, KBOX);
@@ -345,6 +421,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
       __syncwarp();
     }
   } else {
+    take_registers<SOFTMAX_REGS, true>();
     // ---------------- queries and softmax: thread = row of the tile = TMEM lane
     const int r = threadIdx.x;
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
@@ -418,14 +495,27 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         const uint32_t s_at = tmem + COL_S + (n & 1) * BKV + lane_off;
         tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(x));
         tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
-        uint4 w0, w1;
-        const uint32_t bad_at = smem_u32(bad + (n & 1) * 8);
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w0.x), "=r"(w0.y), "=r"(w0.z), "=r"(w0.w) : "r"(bad_at));
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w1.x), "=r"(w1.y), "=r"(w1.z), "=r"(w1.w) : "r"(bad_at + 16));
+        // lanes of the producers whose key is not finite, by eights of them; a bit a key
         uint2 bits = make_uint2(0, 0);
-        if ((w0.x | w0.y | w0.z | w0.w) | (w1.x | w1.y | w1.z | w1.w))  // a bit a key
-          bits = make_uint2(keys_of(w0.x) | keys_of(w0.y) << 8 | keys_of(w0.z) << 16 | keys_of(w0.w) << 24,
-                            keys_of(w1.x) | keys_of(w1.y) << 8 | keys_of(w1.z) << 16 | keys_of(w1.w) << 24);
+        {
+          uint32_t w[8], any = 0;
+          const uint32_t at = smem_u32(bad + (n & 3) * 16);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint4 x, y;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at + 16 * i));
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(at + 16 * i + 32));
+            w[4 * i] = x.x | y.x;
+            w[4 * i + 1] = x.y | y.y;
+            w[4 * i + 2] = x.z | y.z;
+            w[4 * i + 3] = x.w | y.w;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) any |= w[i];
+          if (any)
+            bits = make_uint2(keys_of(w[0]) | keys_of(w[1]) << 8 | keys_of(w[2]) << 16 | keys_of(w[3]) << 24,
+                              keys_of(w[4]) | keys_of(w[5]) << 8 | keys_of(w[6]) << 16 | keys_of(w[7]) << 24);
+        }
         tmem_wait_ld();
         const int k0 = pc.key0 + j * BKV;
 #pragma unroll
