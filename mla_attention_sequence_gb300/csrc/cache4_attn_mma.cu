@@ -74,12 +74,11 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
   const int my_key = threadIdx.x >> 2, q = threadIdx.x & 3, page = a.cache.page;
   int loaded = 0, left = next.tiles, at = 0, page_row = 0, id = -1;
   uint32_t page_of = 0;
-  bool wanted = false;
-  auto fetch = [&]() {
+  bool wanted = false, in = false;
+  auto fetch = [&]() {  // id is not looked at before it is used: that would wait for it
     wanted = at >= next.hull.x && at < next.hull.y;
-    const uint32_t k = min(page_of, static_cast<uint32_t>(a.pages.most - 1));
-    id = wanted ? __ldg(a.pages.table + static_cast<ll>(next.b) * a.pages.most + k) : -1;
-    if (page_of != k) id = -1;
+    in = page_of < static_cast<uint32_t>(a.pages.most);
+    if (wanted && in) id = __ldg(a.pages.table + static_cast<ll>(next.b) * a.pages.most + page_of);
   };
   auto begin_piece = [&]() {
     left = next.tiles;
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
   auto load = [&]() {
     const int s = loaded % STAGES;
     if (more) {
-      const bool there = id >= 0 && id < a.cache.pages, live = wanted && there;
+      const bool there = in && id >= 0 && id < a.cache.pages, live = wanted && there;
       const ll slot = live ? static_cast<ll>(id) * page + page_row : 0;
       const uint32_t gone = __ballot_sync(0xffffffffu, wanted && !there);
       if (lane == 0) reinterpret_cast<uint8_t*>(missing + s)[warp] = 0;

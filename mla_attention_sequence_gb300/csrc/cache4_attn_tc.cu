@@ -35,13 +35,16 @@ namespace {
 constexpr int BQ = 128, BKV = 64;
 constexpr int NBOX = 9, QBOX = 16384, KBOX = 8192;
 constexpr int Q_TMEM = 4;                    // query boxes in TMEM
-constexpr int K_BYTES = NBOX * KBOX;
+constexpr int V_BUFS = 3, V_BYTES = 4 * KBOX, PAIR_BYTES = 2 * KBOX;
+constexpr int K_BYTES = V_BUFS * V_BYTES + 2 * PAIR_BYTES + 2 * KBOX;  // values, the other boxes in pairs, RoPE
 constexpr int Q_BYTES = (NBOX - Q_TMEM) * QBOX;
-constexpr int SMEM_BYTES = 2 * K_BYTES + Q_BYTES + 1024 + 512;
+constexpr int SMEM_BYTES = K_BYTES + Q_BYTES + 1024 + 512;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 constexpr int SOFTMAX_WARPS = 4, PRODUCER_WARPS = 8, MMA_WARP = 4;
-constexpr int NTHREADS = 768;  // warps 8, 12 and 16 have no work
-constexpr int SOFTMAX_REGS = 120, OTHER_REGS = 72;  // of 80 a thread at launch: 120 + 5 * 72 = 6 * 80
+constexpr int NTHREADS = 768;  // warps 5 .. 7 have no work
+// Of 80 registers a thread at launch: 136 + 24 + 4 * 80 = 6 * 80. The producers keep theirs, which is as few
+// as they need: a spilled value is fetched behind the loads of the next tile, for hundreds of cycles.
+constexpr int SOFTMAX_REGS = 136, MMA_REGS = 24;
 constexpr uint32_t TMEM_COLS = 512, COL_S = 128, COL_O = 256;
 constexpr int HALF = 256;
 // kind::f16 with fp16 operands is idesc_bf16 without the two type fields
@@ -62,14 +65,17 @@ struct Params {
 // to tile, and its page, fetched a tile before it is used (the fetch behind the loads that need it took a
 // third of a producer's time).
 struct KeyPlace {
-  int at, page_row, id;
+  int at, page_row, loaded;  // loaded: the table's entry, not looked at before it is used (that would wait for it)
   uint32_t page_of;
-  bool wanted;
+  bool wanted, in;  // within the item's interval; within the table
   __device__ __forceinline__ void fetch(const CacheAttn& a, const Piece& p) {
     wanted = at >= p.hull.x && at < p.hull.y;
-    const uint32_t k = min(page_of, static_cast<uint32_t>(a.pages.most - 1));
-    id = wanted ? __ldg(a.pages.table + static_cast<ll>(p.b) * a.pages.most + k) : -1;
-    if (page_of != k) id = -1;
+    in = page_of < static_cast<uint32_t>(a.pages.most);
+    if (wanted && in) loaded = __ldg(a.pages.table + static_cast<ll>(p.b) * a.pages.most + page_of);
+  }
+  // the page; -1 for a key outside the interval, -2 for one without a page
+  __device__ __forceinline__ int id(const CacheAttn& a) const {
+    return !wanted ? -1 : in && loaded >= 0 && loaded < a.cache.pages ? loaded : -2;
   }
   __device__ __forceinline__ void begin(const CacheAttn& a, const Piece& p, int key) {
     at = p.key0 + key;
@@ -93,21 +99,21 @@ struct KeyPlace {
   }
 };
 
-// What a producer lane holds of one key tile: of each of two latent pairs of boxes (FIRST: those outside
-// this CTA's half of the values, else those of it) 16 bytes of codes, two blocks, and their scales; FIRST
-// also two of the key's eight RoPE chunks. Few wide loads: every load of a warp touches eight keys' lines.
-template <bool FIRST>
+// What a producer lane holds of one key tile: of each of two pairs of boxes 16 bytes of codes, two blocks,
+// and their scales; for the VALUES' boxes also two of the key's eight RoPE chunks. Few wide loads: every
+// load of a warp touches eight keys' lines.
+template <bool VALUES>
 struct Held {
-  uint4 codes[2], rope[FIRST ? 2 : 1];
+  uint4 codes[2], rope[VALUES ? 2 : 1];
   uint32_t scales[2];
   bool live, bad;  // a key to expand (else zeros); a key that should be there and is not
 };
-template <bool FIRST>
-__device__ __forceinline__ void hold(const CacheAttn& a, const KeyPlace& k, int lane4, int half, Held<FIRST>& h) {
-  const bool there = k.id >= 0 && k.id < a.cache.pages;
-  h.live = k.wanted && there;
-  h.bad = k.wanted && !there;
-  const ll slot = h.live ? static_cast<ll>(k.id) * a.cache.page + k.page_row : 0;
+template <bool VALUES>
+__device__ __forceinline__ void hold(const CacheAttn& a, const KeyPlace& k, int lane4, int half, Held<VALUES>& h) {
+  const int id = k.id(a);
+  h.live = id >= 0;
+  h.bad = id == -2;
+  const ll slot = h.live ? static_cast<ll>(id) * a.cache.page + k.page_row : 0;
   const uint4* c = reinterpret_cast<const uint4*>(a.cache.codes + slot * 256 + 128 * half) + lane4;
   const uint16_t* s = reinterpret_cast<const uint16_t*>(a.cache.scales + slot * 32 + 16 * half) + lane4;
 #pragma unroll
@@ -115,13 +121,16 @@ __device__ __forceinline__ void hold(const CacheAttn& a, const KeyPlace& k, int 
     h.codes[i] = __ldg(c + 4 * i);
     h.scales[i] = __ldg(s + 4 * i);
   }
-  if constexpr (FIRST) {
+  if constexpr (VALUES) {
     const uint4* r = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.cache.keys) + slot * 64) + 2 * lane4;
     h.rope[0] = __ldg(r);
     h.rope[1] = __ldg(r + 1);
   }
 }
 
+__device__ __forceinline__ void sts16(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 template <int REGS, bool MORE>
 __device__ __forceinline__ void take_registers() {
   if constexpr (MORE)
@@ -130,23 +139,29 @@ __device__ __forceinline__ void take_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
-// A producer warp: keys [8 pw, 8 pw + 8) of every key tile, FIRST the boxes outside this CTA's half of the
-// values and the RoPE box, else the others. Four lanes a key.
-template <bool FIRST>
-__device__ __forceinline__ void expand_tiles(const CacheAttn& a, Walk<BQ, BKV>& walk, int pw, int vh, uint8_t* sK, uint64_t* full,
-                                             uint64_t* free_, uint32_t* bad, volatile int* abort_flag) {
-  const int lane = threadIdx.x & 31, key = 8 * pw + (lane >> 2), b4 = lane & 3, half = FIRST ? 1 - vh : vh;
+// The key tiles' places in shared memory and their barriers.
+struct Tiles {
+  uint8_t *values, *pairs, *rope;  // [3] of four boxes; [2], of each tile in turn the first and second pair; [2]
+  uint64_t *v_full, *v_free;       // [3] values and RoPE of a tile are there; its context is done
+  uint64_t *p_full, *p_free;       // [2] a pair is there; its scores are done
+  uint64_t* r_free;                // [2] the tile's scores are done
+  uint32_t* bad;                   // [4][16] of each producer, tiles in turn: lanes whose key is not finite
+  volatile int* abort_flag;
+};
+
+// A producer warp: keys [8 pw, 8 pw + 8) of every key tile, of it the boxes of this CTA's half of the VALUES
+// and the RoPE box, or the others. Four lanes a key.
+template <bool VALUES>
+__device__ __forceinline__ void expand_tiles(const CacheAttn& a, Walk<BQ, BKV>& walk, int pw, int vh, const Tiles& t) {
+  const int lane = threadIdx.x & 31, key = 8 * pw + (lane >> 2), b4 = lane & 3, half = VALUES ? vh : 1 - vh;
   const uint32_t row = static_cast<uint32_t>(key);
   const bool turned = (b4 & 2) != 0;
   const uint32_t pick = turned ? 0x4441u : 0x4440u;  // the first stored block's scale; the other's with bit 0 turned
   // A lane's two blocks are a half of a box's row, its upper lanes' in the other order, so that eight lanes
   // (two keys) store to eight different 16-byte columns.
-  const uint32_t chunk = 4 * (b4 & 1) + (b4 & 2);
-  const uint32_t offs[4] = {sw128_offset(row, chunk), sw128_offset(row, chunk + 1), sw128_offset(row, chunk ^ 2),
-                            sw128_offset(row, (chunk ^ 2) + 1)};
-  uint8_t* const boxes = sK + (4 * half + (b4 >> 1)) * KBOX;
+  const uint32_t boxes = smem_u32(VALUES ? t.values : t.pairs) + (b4 >> 1) * KBOX + sw128_offset(row, 4 * (b4 & 1) + (b4 & 2));
   Piece pc;
-  Held<FIRST> cur;
+  Held<VALUES> cur;
   KeyPlace place;
   int left = 0;
   bool more = walk.next(pc);  // a tile whose place is known
@@ -155,7 +170,7 @@ __device__ __forceinline__ void expand_tiles(const CacheAttn& a, Walk<BQ, BKV>& 
     place.begin(a, pc, key);
   };
   auto take = [&]() {  // that tile's bytes, and the place of the one behind it
-    hold<FIRST>(a, place, b4, half, cur);
+    hold<VALUES>(a, place, b4, half, cur);
     if (--left > 0) {
       place.step(a, pc);
     } else {
@@ -177,23 +192,27 @@ __device__ __forceinline__ void expand_tiles(const CacheAttn& a, Walk<BQ, BKV>& 
     return Pair{{expand8(turned ? w.z : w.x, s0), expand8(turned ? w.w : w.y, s0), expand8(turned ? w.x : w.z, s1),
                  expand8(turned ? w.y : w.w, s1)}};
   };
+  auto store = [&](const Pair& p, uint32_t to) {  // columns c, c + 1, c ^ 2, (c ^ 2) + 1 of the box's row
+#pragma unroll
+    for (int x = 0; x < 4; ++x) sts16(to ^ (16 * x), p.v[x]);
+  };
+  auto arrive = [&](uint64_t* bar) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  int buf = 0;  // n % V_BUFS
+  uint32_t v_ph = 1;
 #pragma unroll 1
   for (int n = 0; held; ++n) {
-    LAGA_TRACE_POINT(cache4, FIRST ? 0 : 3, n);
-    const int buf = n & 1;
-    const uint32_t ph = static_cast<uint32_t>(((n >> 1) & 1) ^ 1);
-    uint8_t* const to = boxes + buf * K_BYTES;
-    auto store = [&](const Pair& p, int i) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) *reinterpret_cast<uint4*>(to + 2 * i * KBOX + offs[x]) = p.v[x];
-    };
+    LAGA_TRACE_POINT(cache4, VALUES ? 3 : 0, n);
     // A block that reads as NaN: zeros here, and every row that sees the key gets NaN. All scales at once: a
     // byte above the largest scale has its upper bit and the sum's set.
     static_assert(kCacheTopScale == 0xe2, "the sum below");
     const uint32_t s01 = cur.scales[0] | cur.scales[1] << 16;
     const uint32_t over = ((s01 & 0x7f7f7f7fu) + 0x1d1d1d1du) & s01 & 0x80808080u;
     bool fine = over == 0 || !cur.live;
-    if (FIRST) {
+    if (!VALUES) {
       fine = fine && !cur.bad;
       if (cur.bad && b4 == 0) report_page(a.status, 305);
     }
@@ -210,11 +229,15 @@ __device__ __forceinline__ void expand_tiles(const CacheAttn& a, Walk<BQ, BKV>& 
       held = more;
       if (more) take();
     };
-    if constexpr (FIRST) {
-      // free since the scores of two tiles before: expanded and stored pair by pair
-      if (!pass(&free_[buf], ph, abort_flag, 401)) return;
-      LAGA_TRACE_POINT(cache4, 1, n);
-      store(expand(0), 0);
+    auto report = [&]() {
+      const uint32_t odd = ~__ballot_sync(0xffffffffu, fine);  // four lanes a key
+      if (lane == 0) t.bad[(n & 3) * 16 + (VALUES ? 8 : 0) + pw] = odd;
+    };
+    if constexpr (VALUES) {
+      if (!pass(&t.v_free[buf], v_ph, t.abort_flag, 402)) return;
+      if (!pass(&t.r_free[n & 1], static_cast<uint32_t>(((n >> 1) & 1) ^ 1), t.abort_flag, 403)) return;
+      LAGA_TRACE_POINT(cache4, 4, n);
+      store(expand(0), boxes + buf * V_BYTES);
       const Pair v1 = expand(1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -222,26 +245,33 @@ __device__ __forceinline__ void expand_tiles(const CacheAttn& a, Walk<BQ, BKV>& 
         fine = fine && (number || !cur.live);
         if (!(number && cur.live)) cur.rope[i] = make_uint4(0, 0, 0, 0);
       }
-      uint8_t* rope = sK + buf * K_BYTES + 8 * KBOX;
-      *reinterpret_cast<uint4*>(rope + sw128_offset(row, 2 * b4)) = cur.rope[0];
-      *reinterpret_cast<uint4*>(rope + sw128_offset(row, 2 * b4 + 1)) = cur.rope[1];
+      const uint32_t rope = smem_u32(t.rope) + (n & 1) * KBOX + sw128_offset(row, 2 * b4);
+      sts16(rope, cur.rope[0]);
+      sts16(rope ^ 16, cur.rope[1]);
       advance();
-      store(v1, 1);
+      store(v1, boxes + buf * V_BYTES + PAIR_BYTES);
+      report();
+      arrive(&t.v_full[buf]);
+      LAGA_TRACE_POINT(cache4, 16, n);
+      if (++buf == V_BUFS) {
+        buf = 0;
+        v_ph ^= 1;
+      }
     } else {
-      // free since the context of two tiles before, just before they are needed: expanded ahead
-      const Pair v0 = expand(0), v1 = expand(1);
+      if (!pass(&t.p_free[0], static_cast<uint32_t>((n & 1) ^ 1), t.abort_flag, 401)) return;
+      LAGA_TRACE_POINT(cache4, 1, n);
+      store(expand(0), boxes);
+      arrive(&t.p_full[0]);
+      const Pair v1 = expand(1);
       advance();
-      if (!pass(&free_[buf], ph, abort_flag, 402)) return;
-      LAGA_TRACE_POINT(cache4, 4, n);
-      store(v0, 0);
-      store(v1, 1);
+      LAGA_TRACE_POINT(cache4, 17, n);
+      if (!pass(&t.p_free[1], static_cast<uint32_t>((n & 1) ^ 1), t.abort_flag, 404)) return;
+      LAGA_TRACE_POINT(cache4, 18, n);
+      store(v1, boxes + PAIR_BYTES);
+      report();
+      arrive(&t.p_full[1]);
+      LAGA_TRACE_POINT(cache4, 2, n);
     }
-    const uint32_t odd = ~__ballot_sync(0xffffffffu, fine);  // four lanes a key
-    if (lane == 0) bad[(n & 3) * 16 + (FIRST ? 0 : 8) + pw] = odd;
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&full[buf]);
-    LAGA_TRACE_POINT(cache4, FIRST ? 2 : 16, n);
   }
 }
 
@@ -296,39 +326,61 @@ __device__ __forceinline__ uint32_t keys_of(uint32_t lanes) {
   return bits;
 }
 
+// Two fp32 values to an instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pair(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+
 template <int MOD>
 __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_constant__ CUtensorMap mQ, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  uint8_t* sK = smem;
-  uint8_t* sQ = smem + 2 * K_BYTES;
+  uint8_t* sQ = smem + K_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sQ + Q_BYTES);
-  uint64_t* ka_full = bars + 12;  // [2] a key tile's boxes outside this half's values are expanded
-  uint64_t* kb_full = bars;       // [2] the others
-  uint64_t* ka_free = bars + 2;   // [2] the scores are done: the former may be refilled
-  uint64_t* kb_free = bars + 4;   // [2] the context product is done: the latter
-  uint64_t* s_full = bars + 6;
-  uint64_t* p_full = bars + 8;
-  uint64_t* pv_done = bars + 9;   // P read, O up to date
-  uint64_t* q_full = bars + 10;   // the TMEM boxes are there
-  uint64_t* q_stage = bars + 7;   // they are in shared memory
-  uint64_t* q_rest = bars + 14;   // the other boxes are there
-  uint64_t* q_idle = bars + 15;   // the softmax warps are done with the queries' place
-  uint64_t* drain = bars + 11;
-  uint32_t* bad = reinterpret_cast<uint32_t*>(bars + 20);  // [4][16] of each producer, tiles in turn: lanes whose key is not finite
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
+  uint64_t* s_full = bars + 12;
+  uint64_t* p_full = bars + 13;
+  uint64_t* pv_done = bars + 14;  // P read, O up to date
+  uint64_t* q_full = bars + 15;   // the TMEM boxes are there
+  uint64_t* q_stage = bars + 16;  // they are in shared memory
+  uint64_t* q_rest = bars + 17;   // the other boxes are there
+  uint64_t* q_idle = bars + 18;   // the softmax warps are done with the queries' place
+  uint64_t* drain = bars + 19;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const Tiles t{smem, smem + V_BUFS * V_BYTES, smem + V_BUFS * V_BYTES + 2 * PAIR_BYTES, bars, bars + 3, bars + 6, bars + 8,
+                bars + 10, reinterpret_cast<uint32_t*>(bars + 22), abort_flag};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheAttn& a = p.a;
   const int part = blockIdx.x >> 1, vh = blockIdx.x & 1;  // vh: this CTA's half of the context's columns
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < V_BUFS; ++i) {
+      mbar_init(&t.v_full[i], PRODUCER_WARPS);
+      mbar_init(&t.v_free[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ka_full[i], PRODUCER_WARPS);
-      mbar_init(&kb_full[i], PRODUCER_WARPS);
-      mbar_init(&ka_free[i], 1);
-      mbar_init(&kb_free[i], 1);
+      mbar_init(&t.p_full[i], PRODUCER_WARPS);
+      mbar_init(&t.p_free[i], 1);
+      mbar_init(&t.r_free[i], 1);
     }
     mbar_init(s_full, 1);
     mbar_init(p_full, SOFTMAX_WARPS);
@@ -354,66 +406,70 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
 
   Walk<BQ, BKV> walk(a, part);
   Piece pc;
-  if (warp > MMA_WARP) {
-    take_registers<OTHER_REGS, false>();
-    // ---------------- expand key tiles: warps 4 k excepted, but for the last
-    const int pw = warp == 20 ? 15 : warp % 4 == 0 ? 16 : warp - 5 - (warp > 8) - (warp > 12) - (warp > 16) - (warp > 20);
-    if (pw < PRODUCER_WARPS)
-      expand_tiles<true>(a, walk, pw, vh, sK, ka_full, ka_free, bad, abort_flag);
-    else if (pw < 2 * PRODUCER_WARPS)
-      expand_tiles<false>(a, walk, pw - PRODUCER_WARPS, vh, sK, kb_full, kb_free, bad, abort_flag);
+  if (warp >= 8) {
+    // ---------------- expand key tiles: four of each kind in turn, so that each scheduler has some of both
+    const int i = warp - 8, pw = 4 * (i >> 3) + (i & 3);
+    if ((i & 4) == 0)
+      expand_tiles<false>(a, walk, pw, vh, t);
+    else
+      expand_tiles<true>(a, walk, pw, vh, t);
+  } else if (warp > MMA_WARP) {
+    take_registers<MMA_REGS, false>();
   } else if (warp == MMA_WARP) {
-    take_registers<OTHER_REGS, false>();
+    take_registers<MMA_REGS, false>();
     // ---------------- products
     bool ok = true, issued = false;
-    const uint32_t q_low = desc_low(sQ, 16), k_low = desc_low(sK, 16), v_low = desc_low(sK + vh * 4 * KBOX, KBOX);
-    int n = 0, seg = 0;
-    auto context = [&](int m, bool first) -> bool {  // O (+)= P(m) V(m)
+    const uint32_t q_low = desc_low(sQ, 16), pair_low = desc_low(t.pairs, 16), rope_low = desc_low(t.rope, 16);
+    const uint32_t key_low = desc_low(t.values, 16), value_low = desc_low(t.values, KBOX);
+    int n = 0, seg = 0, buf = 0, before = V_BUFS - 1;  // n % V_BUFS, (n - 1) % V_BUFS
+    uint32_t v_ph = 0;
+    auto context = [&](int m, int at, bool first) -> bool {  // O (+)= P(m) V(m)
       if (!pass(p_full, m & 1, abort_flag, 411)) return false;
       LAGA_TRACE_POINT(cache4, 7, m);
       tc_fence_after();
-      mma4<true, 2048 / 16>(tmem + COL_O, tmem + COL_S + (m & 1) * BKV, v_low + (m & 1) * (K_BYTES / 16), IDESC_PV, first ? 0u : 1u);
-      mma_commit_warp(&kb_free[m & 1]);
+      mma4<true, 2048 / 16>(tmem + COL_O, tmem + COL_S + (m & 1) * BKV, value_low + at * (V_BYTES / 16), IDESC_PV, first ? 0u : 1u);
+      mma_commit_warp(&t.v_free[at]);
       mma_commit_warp(pv_done);
       return true;
-    };
-    // S = Q K^T over the boxes outside this half's values and the RoPE box; S += over the values' boxes
-    const uint32_t ka_at = 4 * (1 - vh) * (KBOX / 16), kb_at = 4 * vh * (KBOX / 16);
-    auto first_boxes = [&](uint32_t s, uint32_t k) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) mma4<false, 2>(s, q_low + c * (QBOX / 16), k + ka_at + c * (KBOX / 16), IDESC_S, c ? 1u : 0u);
-      mma4<false, 2>(s, q_low + 4 * (QBOX / 16), k + 8 * (KBOX / 16), IDESC_ROPE, 1u);
-    };
-    auto other_boxes = [&](uint32_t s, uint32_t k) {
-#pragma unroll
-      for (int c = 0; c < Q_TMEM; ++c) mma4<true, 2>(s, tmem + 32 * c, k + kb_at + c * (KBOX / 16), IDESC_S, 1u);
     };
     while (ok && walk.next(pc)) {
       ok = pass(q_full, seg & 1, abort_flag, 412) && pass(q_rest, seg & 1, abort_flag, 416);
       ++seg;
       for (int j = 0; j < pc.tiles && ok; ++j, ++n) {
         // All of a tile's scores before the context of the tile before, so that its weights are worked out
-        // beside them; first the boxes outside this half's values, whose place has been free for longer.
-        // (P of the tile two before, in this S's place, was read by a product issued earlier.)
-        ok = pass(&ka_full[n & 1], (n >> 1) & 1, abort_flag, 413);
-        if (!ok) break;
-        tc_fence_after();
-        LAGA_TRACE_POINT(cache4, 5, n);
-        const uint32_t s = tmem + COL_S + (n & 1) * BKV, k = k_low + (n & 1) * (K_BYTES / 16);
-        first_boxes(s, k);
-        issued = true;
-        LAGA_TRACE_POINT(cache4, 6, n);
-        ok = pass(&kb_full[n & 1], (n >> 1) & 1, abort_flag, 415);
+        // beside them; first the pairs, whose places are refilled as soon as their scores are done. (P of the
+        // tile two before, in this S's place, was read by a product issued earlier.)
+        const uint32_t s = tmem + COL_S + (n & 1) * BKV;
+#pragma unroll
+        for (int i = 0; i < 2 && ok; ++i) {
+          ok = pass(&t.p_full[i], n & 1, abort_flag, 413 + i);
+          if (!ok) break;
+          tc_fence_after();
+          LAGA_TRACE_POINT(cache4, 5 + i, n);
+          mma4<false, 2>(s, q_low + 2 * i * (QBOX / 16), pair_low + i * (PAIR_BYTES / 16), IDESC_S, i ? 1u : 0u);
+          mma4<false, 2>(s, q_low + (2 * i + 1) * (QBOX / 16), pair_low + i * (PAIR_BYTES / 16) + KBOX / 16, IDESC_S, 1u);
+          mma_commit_warp(&t.p_free[i]);
+          issued = true;
+        }
+        ok = ok && pass(&t.v_full[buf], v_ph, abort_flag, 415);
         if (!ok) break;
         tc_fence_after();
         LAGA_TRACE_POINT(cache4, 11, n);
-        other_boxes(s, k);
-        mma_commit_warp(&ka_free[n & 1]);
+        mma4<false, 2>(s, q_low + 4 * (QBOX / 16), rope_low + (n & 1) * (KBOX / 16), IDESC_ROPE, 1u);
+#pragma unroll
+        for (int c = 0; c < Q_TMEM; ++c)
+          mma4<true, 2>(s, tmem + 32 * c, key_low + buf * (V_BYTES / 16) + c * (KBOX / 16), IDESC_S, 1u);
+        mma_commit_warp(&t.r_free[n & 1]);
         mma_commit_warp(s_full);
         LAGA_TRACE_POINT(cache4, 12, n);
-        if (j > 0) ok = context(n - 1, j == 1);
+        if (j > 0) ok = context(n - 1, before, j == 1);
+        before = buf;
+        if (++buf == V_BUFS) {
+          buf = 0;
+          v_ph ^= 1;
+        }
       }
-      if (ok) ok = context(n - 1, pc.tiles == 1);
+      if (ok) ok = context(n - 1, before, pc.tiles == 1);
     }
     if (!ok && issued) {
       mma_commit_warp(drain);
@@ -499,7 +555,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         uint2 bits = make_uint2(0, 0);
         {
           uint32_t w[8], any = 0;
-          const uint32_t at = smem_u32(bad + (n & 3) * 16);
+          const uint32_t at = smem_u32(t.bad + (n & 3) * 16);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint4 x, y;
@@ -518,12 +574,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         }
         tmem_wait_ld();
         const int k0 = pc.key0 + j * BKV;
+        const uint64_t f2 = both(f);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          float s = __uint_as_float(x[i]) * f;
-          if constexpr ((MOD & kModCap) != 0) s = tanh_rel(s) * p.mod.cap_log2;
-          if constexpr ((MOD & kModBias) != 0) s = fmaf(-slope2, fabsf(pos - static_cast<float>(j * BKV + i)), s);
-          x[i] = __float_as_uint(s);
+        for (int i = 0; i < 32; ++i) {
+          const float2 s = halves(mul2(pair(x[2 * i], x[2 * i + 1]), f2));
+          x[2 * i] = __float_as_uint(s.x);
+          x[2 * i + 1] = __float_as_uint(s.y);
+        }
+        if constexpr (MOD != 0) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            float s = __uint_as_float(x[i]);
+            if constexpr ((MOD & kModCap) != 0) s = tanh_rel(s) * p.mod.cap_log2;
+            if constexpr ((MOD & kModBias) != 0) s = fmaf(-slope2, fabsf(pos - static_cast<float>(j * BKV + i)), s);
+            x[i] = __float_as_uint(s);
+          }
         }
         if (k0 < seen.x || k0 + BKV > seen.y) {
           const uint32_t v0 = visible_bits(seen.x - k0, seen.y - k0), v1 = visible_bits(seen.x - k0 - 32, seen.y - k0 - 32);
@@ -550,14 +615,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
           rescale = true;
         }
         const float neg = m == -INFINITY ? 0.f : -m;
-        float sum = 0.f;
+        const uint64_t neg2 = both(neg);
+        uint64_t sums = 0;
         uint32_t pk[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float w0 = ex2_approx(__uint_as_float(x[2 * i]) + neg), w1 = ex2_approx(__uint_as_float(x[2 * i + 1]) + neg);
-          sum += w0 + w1;
+          const float2 s = halves(add2(pair(x[2 * i], x[2 * i + 1]), neg2));
+          const float w0 = ex2_approx(s.x), w1 = ex2_approx(s.y);
+          sums = add2(sums, pair(__float_as_uint(w0), __float_as_uint(w1)));
           pk[i] = pack_f16x2(w0, w1);
         }
+        const float sum = halves(sums).x + halves(sums).y;
         l = fmaf(l, alpha, sum);
         LAGA_TRACE_POINT(cache4, 9, n);
         // O is the products' until the tile before is done
