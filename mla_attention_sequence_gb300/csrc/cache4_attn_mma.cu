@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
         const float* from = sp + (4 * warp + i) * SP_STRIDE + lane;
         float v = (from[0] + from[ROWS * SP_STRIDE]) + (from[2 * ROWS * SP_STRIDE] + from[3 * ROWS * SP_STRIDE]);
         v *= f[i];
-        if constexpr ((MOD & kModCap) != 0) v = tanh_rel(v) * p.mod.cap_log2;
+        if constexpr ((MOD & kModCap) != 0) v = ((MOD & kModFar) != 0 ? tanh_rel(v) : tanh_abs(v)) * p.mod.cap_log2;
         if constexpr ((MOD & kModBias) != 0) v = fmaf(-slope2[i], fabsf(pos[i] - static_cast<float>(j * KEYS)), v);
         x[i] = key >= seen[i].x && key < seen[i].y ? v : -INFINITY;
         over = over || x[i] > m[i] + (LIFT + SLACK);
@@ -386,9 +386,15 @@ LaunchResult cache4_mma_attn(const CacheAttn& a, const CacheOperands& x, cudaStr
   d.scale = a.scale;
   p.mod = mod_params(d, a.mods);
   LaunchResult r;
-  const int mod = mod_of(a.mods);
-  auto kern = mod == 0 ? cache4_attn_mma_kernel<0> : mod == kModCap ? cache4_attn_mma_kernel<kModCap>
-            : mod == kModBias ? cache4_attn_mma_kernel<kModBias> : cache4_attn_mma_kernel<kModCap | kModBias>;
+  auto kern = cache4_attn_mma_kernel<0>;
+  switch (mod_of(a.mods) | (a.mods.cap > kFarCap ? kModFar : 0)) {
+    case 0: break;
+    case kModCap: kern = cache4_attn_mma_kernel<kModCap>; break;
+    case kModBias: kern = cache4_attn_mma_kernel<kModBias>; break;
+    case kModCap | kModBias: kern = cache4_attn_mma_kernel<kModCap | kModBias>; break;
+    case kModCap | kModFar: kern = cache4_attn_mma_kernel<kModCap | kModFar>; break;
+    default: kern = cache4_attn_mma_kernel<kModCap | kModBias | kModFar>; break;
+  }
   r.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (r.err == cudaSuccess) r.err = launch_next(kern, a.parts, THREADS, SMEM_BYTES, st, p);
   if (r.err != cudaSuccess) r.what = "cache4_attn_mma";

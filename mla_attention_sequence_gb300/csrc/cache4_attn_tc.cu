@@ -327,16 +327,31 @@ __device__ __forceinline__ uint32_t keys_of(uint32_t lanes) {
 }
 
 // Two fp32 values to an instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(__float_as_uint(lo)), "r"(__float_as_uint(hi)));
+  return v;
+}
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
   uint64_t v;
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
   return v;
 }
-__device__ __forceinline__ uint64_t both(float v) { return pair(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ uint64_t both(float v) { return pair(v, v); }
 __device__ __forceinline__ float2 halves(uint64_t v) {
   uint32_t lo, hi;
   asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
   return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t v;
@@ -536,7 +551,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
       ++seg;
       LAGA_TRACE_POINT(cache4, 13, n);
 
-      const float f = MOD & kModCap ? p.mod.u_scale * up : p.sl2 * up;  // score -> log2 units, or -> tanh's argument
+      const float f = up * (MOD & kModFar ? p.mod.u_scale : MOD & kModCap ? p.mod.u_scale * 2.8853900817779268f : p.sl2);
       float slope2 = 0.f, pos = 0.f;
       if constexpr ((MOD & kModBias) != 0) {
         if (there) slope2 = __ldg(p.mod.slopes + h) * 1.4426950408889634f;
@@ -574,18 +589,26 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         }
         tmem_wait_ld();
         const int k0 = pc.key0 + j * BKV;
+        // f turns a product into log2 units, or with a cap c into the exponent of e^2u = 2^(f s):
+        // c tanh(u) = c - 2 c / (1 + e^2u), to 1e-7 of c; far: by tanh_rel, which is small where u is
         const uint64_t f2 = both(f);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float2 s = halves(mul2(pair(x[2 * i], x[2 * i + 1]), f2));
+          uint64_t v = mul2(pair(x[2 * i], x[2 * i + 1]), f2);
+          if constexpr ((MOD & (kModCap | kModFar)) == kModCap) {
+            const float2 e = halves(v);
+            const float2 y = halves(add2(pair(ex2_approx(e.x), ex2_approx(e.y)), both(1.f)));
+            v = fma2(pair(rcp_approx(y.x), rcp_approx(y.y)), both(-2.f * p.mod.cap_log2), both(p.mod.cap_log2));
+          }
+          const float2 s = halves(v);
           x[2 * i] = __float_as_uint(s.x);
           x[2 * i + 1] = __float_as_uint(s.y);
         }
-        if constexpr (MOD != 0) {
+        if constexpr ((MOD & (kModFar | kModBias)) != 0) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) {
             float s = __uint_as_float(x[i]);
-            if constexpr ((MOD & kModCap) != 0) s = tanh_rel(s) * p.mod.cap_log2;
+            if constexpr ((MOD & kModFar) != 0) s = tanh_rel(s) * p.mod.cap_log2;
             if constexpr ((MOD & kModBias) != 0) s = fmaf(-slope2, fabsf(pos - static_cast<float>(j * BKV + i)), s);
             x[i] = __float_as_uint(s);
           }
@@ -622,7 +645,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         for (int i = 0; i < 32; ++i) {
           const float2 s = halves(add2(pair(x[2 * i], x[2 * i + 1]), neg2));
           const float w0 = ex2_approx(s.x), w1 = ex2_approx(s.y);
-          sums = add2(sums, pair(__float_as_uint(w0), __float_as_uint(w1)));
+          sums = add2(sums, pair(w0, w1));
           pk[i] = pack_f16x2(w0, w1);
         }
         const float sum = halves(sums).x + halves(sums).y;
@@ -738,9 +761,15 @@ LaunchResult cache4_tc_attn(const CacheAttn& a, const CacheOperands& x, cudaStre
   Dims d{};
   d.scale = a.scale;
   p.mod = mod_params(d, a.mods);
-  const int mod = mod_of(a.mods);
-  auto kern = mod == 0 ? cache4_attn_kernel<0> : mod == kModCap ? cache4_attn_kernel<kModCap>
-            : mod == kModBias ? cache4_attn_kernel<kModBias> : cache4_attn_kernel<kModCap | kModBias>;
+  auto kern = cache4_attn_kernel<0>;
+  switch (mod_of(a.mods) | (a.mods.cap > kFarCap ? kModFar : 0)) {
+    case 0: break;
+    case kModCap: kern = cache4_attn_kernel<kModCap>; break;
+    case kModBias: kern = cache4_attn_kernel<kModBias>; break;
+    case kModCap | kModBias: kern = cache4_attn_kernel<kModCap | kModBias>; break;
+    case kModCap | kModFar: kern = cache4_attn_kernel<kModCap | kModFar>; break;
+    default: kern = cache4_attn_kernel<kModCap | kModBias | kModFar>; break;
+  }
   r.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (r.err == cudaSuccess) r.err = launch_next(kern, 2 * a.parts, NTHREADS, SMEM_BYTES, st, mQ, p);
   if (r.err != cudaSuccess) r.what = "cache4_attn";

@@ -155,8 +155,8 @@ struct ScoreMods {
 };
 // The attention kernels' instances: -1 the plain causal ones; >= 0 masked, bits as below.
 constexpr int kModCap = 1, kModBias = 2;
-// dK/dV only, with kModCap: a cap of which tanh_abs's error, 1e-7, is no longer small beside a
-// weight's rounding to bf16. (The forward and dq take a relative form for small scores anyhow.)
+// dK/dV and the cache attention, with kModCap: a cap of which tanh_abs's error, 1e-7, is no longer small
+// beside a weight's rounding. (The forward and dq take a relative form for small scores anyhow.)
 constexpr int kModFar = 4;
 constexpr float kFarCap = 512.f;
 inline int mod_of(const ScoreMods& m) { return (m.cap > 0.f ? kModCap : 0) | (m.slopes ? kModBias : 0); }

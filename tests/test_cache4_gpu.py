@@ -265,7 +265,8 @@ def compare(cache, table, lengths, q, W_UK, W_UV, tol=None, lse_tol=None, varian
     return out, lse
 
 
-MODS = {"plain": {}, "cap": dict(softcap=3.0), "bias": dict(slopes=True), "both": dict(softcap=8.0, slopes=True)}
+MODS = {"plain": {}, "cap": dict(softcap=3.0), "bias": dict(slopes=True), "both": dict(softcap=8.0, slopes=True), "far": dict(softcap=3000.0),
+        "far both": dict(softcap=900.0, slopes=True)}
 CASES = {  # lengths, page, Sq, n_h
     "one": ([1], 1, 1, 1), "empty": ([0, 0], 4, 1, 2), "some": ([5, 0, 64, 65, 128], 16, 1, 3), "short": ([2, 7, 1], 16, 4, 2),
     "pages": ([300, 17, 129], 48, 3, 5), "rows": ([200, 131], 64, 9, 16), "wide": ([90, 411], 7, 2, 33), "long": ([3001], 128, 1, 16)}
