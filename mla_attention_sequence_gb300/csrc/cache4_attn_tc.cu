@@ -9,20 +9,30 @@
 // 2^-30 of the largest). The RoPE key's product is bf16 times bf16 into the same accumulator.
 //
 // One CTA per (part of the key tiles, half of the context's columns): TMEM cannot hold 128 x 512 fp32
-// context columns beside the scores, so both halves of a part compute the scores. Of the query tile
-// (nine [128 x 64] boxes, 144 KB) the four of this half's values stay in TMEM as the A operand and five in
-// shared memory,
-// which leaves room there for two key tiles of 64 (nine [64 x 64] boxes, 72 KB each): one is being
-// expanded while the other is read by the products. With the query all in shared memory only one
-// would fit, and reading A from there would bound the products (6 KB for every 32 cycles of an
-// N = 64 step, 128 bytes a cycle).
+// context columns beside the scores, so both halves of a part compute the scores. Of the query tile (nine
+// [128 x 64] boxes, 144 KB) the four of this half's values stay in TMEM as the A operand and five in shared
+// memory: with all of it there too few key tiles would fit beside it, and reading A from there bounds the
+// products (6 KB for every 52 cycles of an N = 64 step, near 128 bytes a cycle; from TMEM 38 cycles).
 //
-// Warp roles: warps 0..3 load the queries (TMA; what goes to TMEM by way of the place of
-// what stays) and do the softmax, one row a thread (their TMEM lanes); warp 4 allocates TMEM and issues the MMAs; eight of the others expand the key tiles, four lanes a
-// key, and load the next tile's bytes before they work on this one's. None of those is on the MMA warp's
-// scheduler (warps 4 k): two of them there were late by half a tile, and every product with them.
-// The boxes that the context's product does not read are refilled as soon as the scores are done.
+// A tile of 64 keys is nine [64 x 64] boxes: the four of this half's values, which the context's product
+// reads long after the scores, in three places in turn; the four others, whose place is free again as soon
+// as their scores are done, a pair at a time; the RoPE box, two places. The products' order is, tile by
+// tile, the scores of tile n (20 steps with A in shared memory, then 16 with A in TMEM) and the context of
+// tile n - 1 (4 steps), so that the softmax of a tile has the scores of the next one beside it: 2200 cycles
+// of the tensor cores a tile, of which the loop takes 2500. It is bound by shared memory: the products read
+// 184 KB a tile (1440 cycles at 128 bytes a cycle), the producers write 72 and load 26 through the same path.
+//
+// Warp roles: warps 0 .. 3 load the queries (TMA; what goes to TMEM by way of the place of what stays) and do
+// the softmax, one row a thread (their TMEM lanes); warp 4 allocates TMEM and issues the MMAs; warps 8 .. 23
+// expand the key tiles, eight the values and the RoPE box, eight the others, four lanes a key, each with its
+// next tile's bytes under way.
 // TMEM columns: query [0,128), S [128,192) and [192,256) in turn, P over its S, O [256,512).
+//
+// 24 sequences of 4000 .. 16384 tokens, 128 heads (events): 83 us for 67 GFLOP; 131072 tokens alone: 41 us. On
+// the way: eight producers with two whole tiles' places 104; sixteen 88; three places for the values 86; two
+// values an instruction in the softmax 83. With eight lanes a key (whole lines a load, half the load's
+// wavefronts, but one barrier for both pairs) 95 .. 108, with a warp that asks for tiles ahead of time in the
+// L2 no gain, with the keys on the MMA's M 176.
 #include "cache4.h"
 #include "cache4_tc.cuh"
 #include "score_mod.cuh"
@@ -59,7 +69,6 @@ struct Params {
   float sl2;          // scale * log2(e)
   ModParams mod;      // u_scale, cap_log2
 };
-
 
 // A producer lane's key in the tile to be loaded next: its place among the sequence's pages, kept from tile
 // to tile, and its page, fetched a tile before it is used (the fetch behind the loads that need it took a

@@ -5,7 +5,9 @@
 // Per head a product of a few tokens with 128 KB of weights, so what counts is that the weights are read
 // once, all of a CTA's loads at once, and how many launches wait for each other: as a plan, a product, a
 // scaling, a join and a product they took 53 us around an attention of 12 (three tokens of 16 heads, event
-// times). A CTA takes a head and 16 tokens (the rows of an mma.sync tile). The sums of q_lat stay fp32
+// times), as two launches 21. A CTA takes a head and 16 tokens at a time (the rows of an mma.sync tile). 24
+// tokens of 128 heads (events): 13 and 20 us, 17 MB of weights each (2.5 at memory's rate) and 20 MB of pieces;
+// a CTA for each 16 tokens of a head, which reads the weights twice, 15 and 23. The sums of q_lat stay fp32
 // until they are scaled to fp16; the context is split in two bf16 parts (its first 16 bits of fraction),
 // both multiplied: neither costs the result a rounding that shows.
 #include "cache4.h"

@@ -80,10 +80,11 @@ laga_status check_rows(int64_t batch, int64_t rows, int64_t max_pages, const int
 // Which form of the tensor cores: mma.sync's time goes with the tiles of 16 rows, the tcgen05 form's with
 // tiles of 128, and it begins later. Kernel's time in us at 16, 32, 48 and 64 rows a sequence, mma.sync :
 // tcgen05 (events):
-//   48 sequences of 2000 .. 8192 tokens   55 : 102   95 : 105   133 : 105   175 : 105
-//   8 of them                             20 : 31    27 : 32    35 : 31     41 : 31
-//   one of 8000                           14 : 20    16 : 20    17 : 18     18 : 18
-//   one of 600                            12 : 14    12 : 14    12 : 14     12 : 14
+//   48 sequences of 2000 .. 8192 tokens   55 : 94    94 : 89    133 : 90    174 : 88
+//   8 of them                             20 : 29    27 : 30    35 : 29     41 : 30
+//   4 of 500 .. 2000                      12 : 16    14 : 14    16 : 15     18 : 14
+//   one of 8000                           14 : 19    16 : 18    17 : 18     19 : 17
+//   one of 600                            10 : 14    10 : 14    11 : 14     12 : 14
 // So mma.sync up to 32 rows, and up to 64 while what the table has room for is at most about three of its
 // key tiles for each of its CTAs.
 constexpr int kFewRows = 32, kFewRowsShort = 64, kShortTiles = 3;
