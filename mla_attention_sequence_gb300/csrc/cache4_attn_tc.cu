@@ -35,6 +35,7 @@
 // L2 no gain, with the keys on the MMA's M 176.
 #include "cache4.h"
 #include "cache4_tc.cuh"
+#include "f32x2.cuh"
 #include "score_mod.cuh"
 
 LAGA_TRACE_DEFINE(cache4)
@@ -335,44 +336,11 @@ __device__ __forceinline__ uint32_t keys_of(uint32_t lanes) {
   return bits;
 }
 
-// Two fp32 values to an instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(__float_as_uint(lo)), "r"(__float_as_uint(hi)));
-  return v;
-}
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-  return v;
-}
-__device__ __forceinline__ uint64_t both(float v) { return pair(v, v); }
-__device__ __forceinline__ float2 halves(uint64_t v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t v;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
-  return v;
-}
 __device__ __forceinline__ float rcp_approx(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t v;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-  return v;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t v;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-  return v;
-}
-
 template <int MOD>
 __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_constant__ CUtensorMap mQ, const Params p) {
   extern __shared__ uint8_t smem_raw[];

@@ -365,6 +365,61 @@ def test_values_that_are_not_finite(dtype, dims, what):
     assert torch.equal(lse.cpu().transpose(1, 2)[~bad], clean[1].cpu().transpose(1, 2)[~bad])
 
 
+@pytest.mark.parametrize("page", [5, 64])
+@pytest.mark.parametrize("n_h", [6, 33])  # 24 and 132 rows a sequence: both forms of the tensor cores
+def test_any_block_that_is_not_finite(n_h, page):
+    """Each block of 16 and each key's place in a tile, one at a time: NaN in the rows that see it, bits as before elsewhere."""
+    lengths, Sq = [203, 70], 4
+    cache, table = filled(lengths, page, DSV3, torch.bfloat16)
+    q, W_UK, W_UV = queries(2, Sq, n_h, DSV3, torch.bfloat16)
+    n = i32(*lengths)
+    clean = laga.cache4_fwd(q, cache, W_UK, W_UV, table, n)
+    assert clean[0].isfinite().all()
+    hi = torch.full((2, Sq), 2 ** 30, dtype=torch.int32, device=dev())
+    hi[0, 2] = 40
+    part = laga.cache4_fwd(q, cache, W_UK, W_UV, table, n, key_hi=hi)
+    for k in range(64):
+        p, block, byte = 3 * k + 13, (k * 11) % 32, (227, 254, 255)[k % 3]
+        at = int(table[0, p // page]), p % page
+        if k % 4 == 3:
+            tensor, index, value = cache.k_rope, (*at, (5 * k) % 64), float(("nan", "inf", "-inf")[k % 3])
+        else:
+            tensor, index, value = cache.scales, (*at, block), byte
+        was = tensor[index].clone()
+        tensor[index] = value
+        sees = torch.tensor([p <= lengths[0] - Sq + i for i in range(Sq)])
+        for kw, want, rows in (({}, clean, sees), (dict(key_hi=hi), part, sees & torch.tensor([True, True, p < 40, True]))):
+            out, lse = (t.cpu() for t in laga.cache4_fwd(q, cache, W_UK, W_UV, table, n, **kw))
+            assert out[0, rows].isnan().all() and lse[0][:, rows].isnan().all(), (p, k)
+            assert torch.equal(out[0, ~rows], want[0].cpu()[0, ~rows]) and torch.equal(out[1], want[0].cpu()[1]), (p, k)
+        tensor[index] = was
+    out, lse = laga.cache4_fwd(q, cache, W_UK, W_UV, table, n)
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+    laga.check(dev())
+
+
+@pytest.mark.parametrize("n_h", [6, 33])
+def test_pages_missing_inside(n_h):
+    """Entries that are no page: NaN for the rows that see their keys, whatever else the tile holds."""
+    lengths, Sq, page = [203, 70], 4, 7
+    cache, table = filled(lengths, page, DSV3, torch.bfloat16)
+    q, W_UK, W_UV = queries(2, Sq, n_h, DSV3, torch.bfloat16)
+    n = i32(*lengths)
+    hi = torch.full((2, Sq), 2 ** 30, dtype=torch.int32, device=dev())
+    hi[0, 1] = 60
+    clean = laga.cache4_fwd(q, cache, W_UK, W_UV, table, n, key_hi=hi)
+    laga.check(dev())
+    for entry, value in ((9, -1), (14, 10 ** 6), (28, -2 ** 31), (20, 2 ** 31 - 1)):
+        broken = table.clone()
+        broken[0, entry] = value
+        out, lse = (t.cpu() for t in laga.cache4_fwd(q, cache, W_UK, W_UV, broken, n, key_hi=hi))
+        with pytest.raises(laga.LagaError, match="page"):
+            laga.check(dev())
+        rows = torch.tensor([True, entry * page < 60, True, True])
+        assert out[0, rows].isnan().all() and lse[0][:, rows].isnan().all()
+        assert torch.equal(out[0, ~rows], clean[0].cpu()[0, ~rows]) and torch.equal(out[1], clean[0].cpu()[1])
+
+
 @pytest.mark.parametrize("dtype,dims", [(torch.bfloat16, DSV3), (torch.float32, (64, 32, 16, 32))])
 def test_tables_that_do_not_hold_the_sequence(dtype, dims):
     lengths = [100, 100, 100]
