@@ -11,15 +11,17 @@
 //
 // Memory bound: a row is held in registers between its sum and its result, so each value is read once
 // and written once. Eight lanes share a row (24 chunks of 16 bytes for a bf16 head of 192: three a
-// lane), so that a sum takes three shuffles and a warp has four rows in flight; rows wider than 24
+// lane), so that a sum takes three shuffles and a warp has four rows at a time; rows wider than 24
 // chunks take a whole warp. As many CTAs as the SMs hold deal the rows out evenly, each warp takes
-// consecutive rows, loads the next ones before it works on those at hand, and makes a token's angles
+// consecutive rows, has the next ones loaded while it works on those at hand, and makes a token's angles
 // once for all heads that it has of it.
 //
-// 2048 tokens of 128 heads of 192 in bf16 (events around the launches, 201 MB moved forward, 302 MB
-// backward): 41 us forward, 64 us backward with the sum of the partials. A CTA a token, without loads
-// ahead: 47 and 92. Forward with 4 CTAs an SM 43, with 4 and no loads ahead 45, with warps of 32 rows 49
-// (angles again for each); backward with 3 CTAs an SM and no loads ahead 101.
+// 2048 tokens of 128 heads of 192 in bf16, 201 MB moved forward, 302 MB backward (replayed from a graph):
+// 35.5 us forward (halves 36.5), 53 us backward with the sum of the partials. A CTA a token, without loads
+// ahead: 43 and 87. Forward through shared memory 37.4, in halves through registers 52 (spills; with two CTAs
+// an SM 40); backward through registers 58, with two steps of rows ahead 55. Forward with 4 CTAs an SM 2 us
+// more, with warps of 32 rows 8 (angles again for each); backward with 3 CTAs 22 more.
+#include "ptx.cuh"
 #include "rope_device.cuh"
 
 #include <algorithm>
@@ -35,6 +37,9 @@ constexpr int BWD_CTAS_PER_SM = 4;  // at most: rows of partials
 constexpr float kBigSum = 0x1p120f;
 constexpr float kDown = 0x1p-70f;
 
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 template <int LANES>
 __device__ __forceinline__ float sum_lanes(float v) {
 #pragma unroll
@@ -71,23 +76,34 @@ struct RowOps {
   using V = Vec<T>;
   static constexpr int N = V::N;
 
-  // What a lane keeps of a row: its chunks, and for the layout in halves their partners.
-  struct Held {
-    uint4 own[K], other[INTERLEAVED ? 1 : K];
-  };
+  // A warp's rows of one step, as they come: chunk c of its row j at place j chunks + c.
   static __device__ __forceinline__ int partner(const RowShape& s, int c) {
     return c - s.nope < s.half ? c + s.half : c - s.half;
   }
-  static __device__ __forceinline__ void load(const T* row, const RowShape& s, int l, bool active, [[maybe_unused]] bool partners,
-                                              Held& h) {
+  static __device__ __forceinline__ void fetch(uint32_t to, const T* row, const RowShape& s, int l, bool active) {
     const uint4* p = reinterpret_cast<const uint4*>(row);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = l + LANES * k;
-      const bool there = active && c < s.chunks;
-      h.own[k] = there ? __ldcs(p + c) : make_uint4(0, 0, 0, 0);
-      if constexpr (!INTERLEAVED)
-        h.other[k] = partners && there && c >= s.nope ? __ldcs(p + partner(s, c)) : make_uint4(0, 0, 0, 0);
+      if (active && c < s.chunks) copy16(to + 16 * c, p + c);
+    }
+  }
+  struct Held {
+    uint4 own[K];
+  };
+  static __device__ __forceinline__ void load(const T* row, const RowShape& s, int l, bool active, Held& h) {
+    const uint4* p = reinterpret_cast<const uint4*>(row);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = l + LANES * k;
+      h.own[k] = active && c < s.chunks ? __ldcs(p + c) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  static __device__ __forceinline__ void load(const uint4* row, const RowShape& s, int l, bool active, Held& h) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = l + LANES * k;
+      h.own[k] = active && c < s.chunks ? row[c] : make_uint4(0, 0, 0, 0);
     }
   }
   // The turned values of chunk c: v and, in halves, o (already weighted) are its own and its partner's.
@@ -136,11 +152,10 @@ struct RowOps {
     }
   }
 
-  static __device__ __forceinline__ void forward(const Held& h, T* dst, const RowShape& s, const float* w, int pitch,
+  static __device__ __forceinline__ void forward(const Held& h, const uint4* row, T* dst, const RowShape& s, const float* w, int pitch,
                                                  const float2* cs, float eps, int l, bool active) {
     const float sum = sum_lanes<LANES>(squares(h, 1.f));
     const Scale sc = row_scale<LANES>(sum, s.inv_d, eps, [&](float by) { return squares(h, by); });
-    __syncwarp();  // in place: every lane of the row has loaded
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = l + LANES * k;
@@ -153,7 +168,7 @@ struct RowOps {
       if constexpr (!INTERLEAVED) {
         if (c >= s.nope) {
           weights(w, pitch, partner(s, c), wv);
-          V::get(h.other[k], o);
+          V::get(row[partner(s, c)], o);
 #pragma unroll
           for (int i = 0; i < N; ++i) o[i] = o[i] * sc.down * sc.r * wv[i];
         }
@@ -163,7 +178,7 @@ struct RowOps {
     }
   }
 
-  static __device__ __forceinline__ void backward(const Held& x, const Held& z, T* dst, const RowShape& s,
+  static __device__ __forceinline__ void backward(const Held& x, const Held& z, const uint4* z_row, T* dst, const RowShape& s,
                                                   const float* w, int pitch, const float2* cs, float eps, int l,
                                                   bool active, float (&acc)[K][N]) {
     const float sum = sum_lanes<LANES>(squares(x, 1.f));
@@ -175,7 +190,8 @@ struct RowOps {
       float v[N], o[N], wv[N];
       V::get(z.own[k], dy[k]);
       if (!active || c >= s.chunks) continue;
-      if constexpr (!INTERLEAVED) V::get(z.other[k], o);
+      if constexpr (!INTERLEAVED)
+        if (c >= s.nope) V::get(z_row[partner(s, c)], o);
       turn(s, c, cs, -1.f, dy[k], o);
       V::get(x.own[k], v);
       weights(w, pitch, c, wv);
@@ -188,7 +204,6 @@ struct RowOps {
       }
     }
     const float mean = sum_lanes<LANES>(dot) * s.inv_d;
-    __syncwarp();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = l + LANES * k;
@@ -235,8 +250,13 @@ struct NormDeal {
   ll share_q, share_k;
   int held;   // tokens whose cosines and sines a warp holds at a time
   int pitch;  // of the weights' quarters in shared memory, in floats
+  int rows;   // with a ring: bytes of a warp's rows of one step, of x (backward: as many of z behind them)
 };
 
+// Whether the next rows come to shared memory (two steps a warp) or to registers, of which the backward has
+// none left; a layout in halves reads its rows' partners there.
+template <bool INTERLEAVED, bool BWD>
+constexpr bool kNormRing = BWD || !INTERLEAVED;
 // CTAs of a variant that an SM holds: rows in flight against registers (the figures above).
 template <int LANES, int K, bool BWD>
 constexpr int kNormCtas = LANES * K > 64 ? (BWD ? 1 : 2) : (BWD ? 2 : 3);
@@ -249,6 +269,8 @@ __global__ void __launch_bounds__(THREADS, (kNormCtas<LANES, K, BWD>))
   using R = RowOps<T, INTERLEAVED, LANES, K>;
   using Held = typename R::Held;
   constexpr int N = R::N, ROWS = 32 / LANES;  // rows of a warp
+  constexpr bool RING = kNormRing<INTERLEAVED, BWD>;
+  constexpr int KINDS = BWD ? 2 : 1;
   extern __shared__ __align__(16) float smem[];
   const RopeArgs& p = a.rope;
   const int n = p.d_rope / 2, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES;
@@ -256,7 +278,10 @@ __global__ void __launch_bounds__(THREADS, (kNormCtas<LANES, K, BWD>))
   const int heads = keys ? 1 : p.n_h, nope = keys ? 0 : p.d_nope, width = nope + p.d_rope, pitch = deal.pitch;
   const RowShape s{width / N, nope / N, n / N, 1.f / width};
   float* w = smem;  // [N / 4][pitch]
-  float2* cs = reinterpret_cast<float2*>(smem + N / 4 * pitch) + warp * deal.held * n;  // [held][n] a warp
+  // then a warp's two steps of rows, then its angles [held][n]
+  uint8_t* ring = reinterpret_cast<uint8_t*>(smem + N / 4 * pitch) + warp * (2 * KINDS * deal.rows);
+  float2* cs = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(smem + N / 4 * pitch) + WARPS * (2 * KINDS * deal.rows)) +
+               warp * deal.held * n;
   const T* in = static_cast<const T*>(keys ? p.k : p.q);
   const T* grad = static_cast<const T*>(keys ? a.z_k : a.z_q);
   T* out = static_cast<T*>(keys ? p.k_out : p.q_out);
@@ -271,14 +296,22 @@ __global__ void __launch_bounds__(THREADS, (kNormCtas<LANES, K, BWD>))
   int row = lane / LANES, head = first_head + row, token = head / heads;  // this lane's, from the warp's first
   head -= token * heads;
   const ll at0 = begin * width;
-  Held x, z;
-  auto load = [&](int r, Held& hx, Held& hz) {
-    const bool active = r < rows;
-    const ll at = at0 + static_cast<ll>(active ? r : 0) * width;
-    R::load(in + at, s, l, active, !BWD, hx);
-    if constexpr (BWD) R::load(grad + at, s, l, active, true, hz);
+  const uint32_t ring_at = smem_u32(ring) + (lane / LANES) * width * sizeof(T);
+  Held nx;  // without a ring: the next rows
+  // asks for the rows of the step at r0, of an even or odd one
+  auto ask = [&](int r0, int which) {
+    const int r = r0 + lane / LANES;
+    const bool there = r < rows;
+    const ll at = at0 + static_cast<ll>(there ? r : 0) * width;
+    if constexpr (RING) {
+      R::fetch(ring_at + which * (KINDS * deal.rows), in + at, s, l, there);
+      if constexpr (BWD) R::fetch(ring_at + which * (KINDS * deal.rows) + deal.rows, grad + at, s, l, there);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else {
+      R::load(in + at, s, l, there, nx);
+    }
   };
-  load(row, x, z);
+  ask(0, 0);
   const T* weight = static_cast<const T*>(keys ? a.w_k : a.w_q);
   for (int i = threadIdx.x; i < width; i += THREADS)
     w[R::weight_at(pitch, i / N, i % N / 4) + i % 4] = to_f(weight[i]);
@@ -293,9 +326,22 @@ __global__ void __launch_bounds__(THREADS, (kNormCtas<LANES, K, BWD>))
   int held0 = 0, held1 = 0;  // the tokens whose angles are there
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += ROWS) {
-    Held nx, nz;
-    load(row + ROWS, nx, nz);
     const bool active = row < rows;
+    const int which = (r0 / ROWS) & 1;
+    const uint8_t* from = ring + which * (KINDS * deal.rows) + (lane / LANES) * width * sizeof(T);
+    const uint4 *x_row = reinterpret_cast<const uint4*>(from), *z_row = reinterpret_cast<const uint4*>(from + deal.rows);
+    Held x, z;
+    if constexpr (RING) {
+      __syncwarp();  // all lanes have read the rows of the step before, whose place is taken now
+      ask(r0 + ROWS, which ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      R::load(x_row, s, l, active, x);
+      if constexpr (BWD) R::load(z_row, s, l, active, z);
+    } else {
+      x = nx;
+      ask(r0 + ROWS, 0);
+    }
     const int last = min(__shfl_sync(0xffffffffu, token, 31), tokens - 1);
     if (last >= held1) {
       held0 = __shfl_sync(0xffffffffu, token, 0);
@@ -314,9 +360,9 @@ __global__ void __launch_bounds__(THREADS, (kNormCtas<LANES, K, BWD>))
     const float2* angles = cs + (active ? token - held0 : 0) * n;
     T* to = out + at0 + static_cast<ll>(active ? row : 0) * width;
     if constexpr (BWD)
-      R::backward(x, z, to, s, w, pitch, angles, a.eps, l, active, acc);
+      R::backward(x, z, z_row, to, s, w, pitch, angles, a.eps, l, active, acc);
     else
-      R::forward(x, to, s, w, pitch, angles, a.eps, l, active);
+      R::forward(x, x_row, to, s, w, pitch, angles, a.eps, l, active);
     row += ROWS;
     head += ROWS;
     if (head >= heads) {
@@ -324,15 +370,14 @@ __global__ void __launch_bounds__(THREADS, (kNormCtas<LANES, K, BWD>))
       token += k;
       head -= k * heads;
     }
-    x = nx;
-    if constexpr (BWD) z = nz;
   }
   if constexpr (BWD) {
     // rows of partials: the CTAs' of the queries, then those of the keys
     const int d = p.d_nope + p.d_rope;
     float* to = a.partials + (keys ? static_cast<ll>(deal.ctas_q) * d + static_cast<ll>(blockIdx.x - deal.ctas_q) * width
                                    : static_cast<ll>(blockIdx.x) * width);
-    __syncthreads();  // the angles' place is taken again
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the rows' and the angles' places are taken again
     reduce_columns<T, LANES, K>(acc, s, smem + N / 4 * pitch, to);
   }
 }
@@ -489,11 +534,17 @@ cudaError_t launch_vec(const NormArgs& a, const RopeTable& t, NormDeal& deal, cu
   const int step = ROWS == 1 ? 1 : (ROWS - 2) / (k_rows ? 1 : p.n_h) + 2;
   deal.held = std::max(step, std::min(32 / (k_rows ? 1 : std::min(p.n_h, 32)), 4096 / static_cast<int>(n * sizeof(float2))));
   deal.pitch = 4 * (widest / N);
+  deal.rows = BWD || !p.interleaved ? static_cast<int>(ROWS * widest * sizeof(T)) : 0;
   const size_t angles = static_cast<size_t>(WARPS) * deal.held * n * sizeof(float2);
+  const size_t ring = static_cast<size_t>(WARPS) * 2 * (BWD ? 2 : 1) * deal.rows;
   const size_t red = BWD ? static_cast<size_t>(WARPS) * widest * sizeof(float) : 0;
-  const size_t smem = static_cast<size_t>(N / 4) * deal.pitch * sizeof(float) + std::max(angles, red);
-  return launch_next(p.interleaved ? norm_vec_kernel<T, true, LANES, K, BWD> : norm_vec_kernel<T, false, LANES, K, BWD>,
-                     static_cast<unsigned>(deal.ctas_q + deal.ctas_k), THREADS, smem, st, a, t,
+  const size_t smem = static_cast<size_t>(N / 4) * deal.pitch * sizeof(float) + std::max(ring + angles, red);
+  const auto kern = p.interleaved ? norm_vec_kernel<T, true, LANES, K, BWD> : norm_vec_kernel<T, false, LANES, K, BWD>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_next(kern, static_cast<unsigned>(deal.ctas_q + deal.ctas_k), THREADS, smem, st, a, t,
                      static_cast<const NormDeal&>(deal));
 }
 
