@@ -730,7 +730,7 @@ def _made(name, t, like, dts, dev):
             raise ValueError(f"{name} without its input")
         return None, None
     if t is None:
-        t = torch.empty(like.shape, dtype=dts[0], device=dev)
+        t = torch.empty_like(like)  # contiguous and of the calls' type, as `like` has been found to be
         return t, t.data_ptr()
     return t, _expect(name, t, like.shape, dts, dev)
 
