@@ -348,15 +348,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* sQ = smem + K_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sQ + Q_BYTES);
-  uint64_t* s_full = bars + 12;
-  uint64_t* p_full = bars + 13;
-  uint64_t* pv_done = bars + 14;  // P read, O up to date
-  uint64_t* q_full = bars + 15;   // the TMEM boxes are there
-  uint64_t* q_stage = bars + 16;  // they are in shared memory
-  uint64_t* q_rest = bars + 17;   // the other boxes are there
-  uint64_t* q_idle = bars + 18;   // the softmax warps are done with the queries' place
-  uint64_t* drain = bars + 19;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
+  uint64_t* s_full = bars + 12;   // [2] the scores in that place are there
+  uint64_t* p_full = bars + 14;
+  uint64_t* pv_done = bars + 15;  // P read, O up to date
+  uint64_t* q_full = bars + 16;   // the TMEM boxes are there
+  uint64_t* q_stage = bars + 17;  // they are in shared memory
+  uint64_t* q_rest = bars + 18;   // the other boxes are there
+  uint64_t* q_idle = bars + 19;   // the softmax warps are done with the queries' place
+  uint64_t* drain = bars + 20;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const Tiles t{smem, smem + V_BUFS * V_BYTES, smem + V_BUFS * V_BYTES + 2 * PAIR_BYTES, bars, bars + 3, bars + 6, bars + 8,
                 bars + 10, reinterpret_cast<uint32_t*>(bars + 22), abort_flag};
@@ -373,8 +373,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
       mbar_init(&t.p_full[i], PRODUCER_WARPS);
       mbar_init(&t.p_free[i], 1);
       mbar_init(&t.r_free[i], 1);
+      mbar_init(&s_full[i], 1);
     }
-    mbar_init(s_full, 1);
     mbar_init(p_full, SOFTMAX_WARPS);
     mbar_init(pv_done, 1);
     mbar_init(q_full, SOFTMAX_WARPS);
@@ -430,7 +430,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
       for (int j = 0; j < pc.tiles && ok; ++j, ++n) {
         // All of a tile's scores before the context of the tile before, so that its weights are worked out
         // beside them; first the pairs, whose places are refilled as soon as their scores are done. (P of the
-        // tile two before, in this S's place, was read by a product issued earlier.)
+        // tile two before, in this S's place, was read by a product issued earlier.) The scores of two tiles
+        // can be done before a softmax warp has looked at the first, so each place has its own barrier: it is
+        // over again with the tile after next, which waits for all four warps' weights of this one.
         const uint32_t s = tmem + COL_S + (n & 1) * BKV;
 #pragma unroll
         for (int i = 0; i < 2 && ok; ++i) {
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         for (int c = 0; c < Q_TMEM; ++c)
           mma4<true, 2>(s, tmem + 32 * c, key_low + buf * (V_BYTES / 16) + c * (KBOX / 16), IDESC_S, 1u);
         mma_commit_warp(&t.r_free[n & 1]);
-        mma_commit_warp(s_full);
+        mma_commit_warp(&s_full[n & 1]);
         LAGA_TRACE_POINT(cache4, 12, n);
         if (j > 0) ok = context(n - 1, before, j == 1);
         before = buf;
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
       }
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < pc.tiles && ok; ++j, ++n) {
-        if (!pass(s_full, n & 1, abort_flag, 421)) { ok = false; break; }
+        if (!pass(&s_full[n & 1], (n >> 1) & 1, abort_flag, 421)) { ok = false; break; }
         LAGA_TRACE_POINT(cache4, 8, n);
         tc_fence_after();
         uint32_t x[64];
