@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
       const int qi = (pc.r0 + r) / a.n_h, h = pc.r0 + r - qi * a.n_h;
       seen[i] = there ? cache_row_bounds(a, pc.b, qi) : make_int2(0, 0);
       const float up = there ? __ldcg(p.x.up + row0 + r) : 1.f;
-      if (up != up) odd |= 1u << i;
+      if (up != up && seen[i].x < seen[i].y) odd |= 1u << i;  // a row that sees nothing is 0 whatever it holds
       f[i] = (MOD & kModCap ? p.mod.u_scale : p.sl2) * (up != up ? 1.f : up);
       slope2[i] = pos[i] = 0.f;
       if constexpr ((MOD & kModBias) != 0) {

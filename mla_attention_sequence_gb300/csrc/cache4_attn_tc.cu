@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         staged = true;
       }
       const float up = there ? __ldcg(p.x.up + row) : 1.f;
-      bool odd = up != up;  // the row's result is NaN
+      bool odd = up != up && seen.x < seen.y;  // the row's result is NaN (one that sees nothing is 0 whatever it holds)
       if (!pass(q_stage, seg & 1, abort_flag, 425)) { ok = false; break; }
 #pragma unroll 1
       for (int c = 0; c < Q_TMEM; ++c) {
