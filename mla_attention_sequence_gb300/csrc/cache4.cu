@@ -377,7 +377,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const CacheAttn a, f
   const CacheShare share = cache_share(a, 0);
   const int p0 = begin / share.quota, p1 = end > begin ? (end - 1) / share.quota : p0;
   if (end > begin && p0 == p1) return;  // written by the part that had it all
-  const int2 hull = __ldcg(a.hull + item);
   const int rows = min(a.tile, a.rows - r0), d_c = a.cache.d_c, pieces = p1 - p0 + 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
@@ -385,10 +384,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const CacheAttn a, f
     const int i = (r0 + r) / a.n_h, h = (r0 + r) - i * a.n_h;
     float* out = ctx + row * d_c;
     float* lse = a.lse + (static_cast<ll>(b) * a.n_h + h) * a.Sq + i;
-    if (end == begin) {  // no keys: zero, or NaN where the table had no room
-      const float v = hull.x < 0 ? __int_as_float(0x7fc00000) : 0.f;
+    if (end == begin) {
+      const float v = lost_row(cache_row_bounds(a, b, i));
       for (int c = threadIdx.x; c < d_c; c += JOIN_THREADS) out[c] = v;
-      if (threadIdx.x == 0) *lse = hull.x < 0 ? v : -INFINITY;
+      if (threadIdx.x == 0) *lse = v != v ? v : -INFINITY;
       continue;
     }
     // piece k is part p0 + k's; the first began the item

@@ -76,7 +76,7 @@ struct CacheAttn {
   ScoreMods mods;
   int* first;    // [items + 1] first key tile of each item in the order of all
   int* part_item;  // [parts] the item in which a part's share begins
-  int2* hull;    // [items] keys seen by some row; {-1, -1}: a length past the table
+  int2* hull;    // [items] keys seen by some row, of those past the table's room the first alone
   float* part_o;     // [2 parts][tile][d_c]
   float2* part_ml;   // [2 parts][tile] {running maximum, sum}
   float* lse;        // [B][n_h][Sq]
@@ -162,6 +162,8 @@ __device__ __forceinline__ CacheShare cache_share(const CacheAttn& a, int part) 
 __device__ __forceinline__ float row_sum(float l, int2 seen) {
   return l == 0.f && seen.x < seen.y ? __int_as_float(0x7fc00000) : l;
 }
+// The result of a row of an item without key tiles: 0, or NaN where it sees keys, all past the table's room.
+__device__ __forceinline__ float lost_row(int2 seen) { return seen.x < seen.y ? __int_as_float(0x7fc00000) : 0.f; }
 
 // One CTA: the items' intervals of keys, and the running sum of their key tiles.
 template <int THREADS>
@@ -182,13 +184,16 @@ __device__ __forceinline__ void cache4_plan_items(const CacheAttn& a) {
         lo = min(lo, s.x);
         hi = max(hi, s.y);
       }
-      if (hi > room) {  // keys that the table has no room for
+      // Keys that the table has no room for: the first of them stays in the interval, as a key without a page
+      // to the rows that see it. A row that sees only others ends without a weight (row_sum), or its whole
+      // item without a tile (lost_row).
+      if (hi > room) {
         report_page(a.status, 303);
-        a.hull[j] = make_int2(-1, -1);
-      } else {
-        a.hull[j] = hi > 0 ? make_int2(lo, hi) : make_int2(0, 0);
-        if (hi > 0) tiles = (hi - 1) / a.keys - lo / a.keys + 1;
+        hi = static_cast<int>(room) + 1;
       }
+      if (lo >= hi) lo = hi = 0;
+      a.hull[j] = make_int2(lo, hi);
+      if (lo < hi) tiles = (hi - 1) / a.keys - lo / a.keys + 1;
     }
     int run = tiles;  // inclusive sum over the warp, then over the warps
 #pragma unroll

@@ -157,14 +157,13 @@ __global__ void __launch_bounds__(THREADS, 1) finish_kernel(const CacheAttn a, i
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (token < tokens) {
-      const float nan = __int_as_float(0x7fc00000);
       const Row y = row_of(a, token, h);
       const int begin = __ldcg(a.first + y.item), end = __ldcg(a.first + y.item + 1);
       const CacheShare share = cache_share(a, 0);
       const int p0 = begin / share.quota, p1 = end > begin ? (end - 1) / share.quota : p0;
       float* lse = a.lse + (static_cast<ll>(y.b) * a.n_h + h) * a.Sq + y.i;
-      if (end == begin) {  // no keys: zero, or NaN where the table had no room
-        const float v = __ldcg(a.hull + y.item).x < 0 ? nan : 0.f;
+      if (end == begin) {
+        const float v = lost_row(cache_row_bounds(a, y.b, y.i));
 #pragma unroll
         for (int j = 0; j < 4; ++j) c[j] = make_float4(v, v, v, v);
         if (lane == 0) *lse = v != v ? v : -INFINITY;
