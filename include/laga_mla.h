@@ -454,7 +454,7 @@ laga_status laga_mla_fwd_noalloc(const laga_mla_desc* desc, const void* q, const
 
 /* Synchronises the stream, then reads and clears this device's status word.
  * Returns LAGA_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last
- * check, LAGA_ERR_INVALID_ARG if one met a cached position without a page,
+ * check, else LAGA_ERR_INVALID_ARG if one met a cached position without a page;
  * LAGA_ERR_CUDA if the stream reports an error, else LAGA_OK. */
 laga_status laga_mla_check(laga_stream_t stream);
 

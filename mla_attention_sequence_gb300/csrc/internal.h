@@ -74,7 +74,7 @@ __device__ __forceinline__ void end_after_previous(bool last_cta) {
 }
 #endif
 
-// Device address of this device's status word (timeouts of bounded waits);
+// Device address of this device's status word (timeouts of bounded waits, cached positions without a page);
 // nullptr if it cannot be resolved.
 int* device_status_ptr();
 // Handle of the calling thread's current CUDA context (nullptr if none): the key,

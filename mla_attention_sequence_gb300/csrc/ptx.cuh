@@ -490,10 +490,17 @@ __device__ __forceinline__ bool warp_wait_token(uint64_t* bar, uint32_t parity, 
   return __all_sync(0xffffffffu, ok);
 }
 
-// Called by one thread after the CTA's final barrier: publish an abort.
+// Called by one thread after the CTA's final barrier: publish an abort. The first expired wait stays in the
+// word; a lesser code that was there (a cached position without a page, which spoils rows of one call) makes
+// room for it.
 __device__ __forceinline__ void publish_abort(volatile int* abort_flag, int* status) {
   const int a = *abort_flag;
-  if (a != 0 && status != nullptr) atomicCAS(status, 0, a);
+  if (a == 0 || status == nullptr) return;
+  for (int k = 0, seen = 0; k < 4; ++k) {
+    const int was = atomicCAS(status, seen, a);
+    if (was == seen || (was & 0xff) == kStatusTimeout) return;
+    seen = was;
+  }
 }
 }  // namespace laga
 
