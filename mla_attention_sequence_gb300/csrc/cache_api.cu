@@ -230,7 +230,11 @@ laga_status laga_mla_cache4_append(const laga_mla_cache4* cache, int64_t batch, 
   a.turn = rope != nullptr && a.cache.d_rope > 0;
   if (a.turn) {
     a.own_pos = pos != nullptr;
-    st = rope_plan(rope, pos ? pos : starts, &a.rope, &t);
+    laga_mla_rope_desc x = *rope;  // the rows have no heads, and without pos no type of it
+    x.n_h = 1;
+    x.d_nope = 0;
+    if (!pos) x.pos64 = 0;
+    st = rope_plan(&x, pos ? pos : starts, &a.rope, &t);
     if (st != LAGA_OK) return st;
     if (rope->d_rope != cache->d_rope || rope->tokens != batch * rows || rope->dtype != cache->dtype || rope->inverse)
       return fail(LAGA_ERR_INVALID_ARG, "cache4_append: the rotation's tokens, d_rope and dtype are the rows' and the cache's, not inverse%s");

@@ -148,3 +148,14 @@ def test_reference_encoding_of_known_blocks():
     assert scales.tolist() == [[15 * 8, 226]]
     np.testing.assert_array_equal(vals[0], [6, -6, 0, 1, 1, 2, 2, 4, 4, -4, 0.5, 4, 0, 1, 2, 3, 61440, 0, 0, 61440])
     np.testing.assert_array_equal(cref.decode(torch.from_numpy(codes), torch.from_numpy(scales), 20)[0].numpy(), vals[0])
+
+
+def test_append_ignores_what_its_rotation_does_not_use(L):
+    """The rows of an append have no heads: its rotation's n_h and d_nope are not looked at, nor is a limit that they
+    would pass; without pos neither is pos64. (Another field is wrong in each call: none gets as far as a launch.)"""
+    for kw, starts in ((dict(n_h=0, d_nope=0), P), (dict(n_h=-3, d_nope=-1), P), (dict(n_h=1 << 20), P), (dict(d_nope=1 << 20), P),
+                       (dict(n_h=60000, d_nope=60000), P), (dict(pos64=1), P + 4)):
+        rope = rope_desc(inverse=1, **kw)
+        assert L.laga_mla_cache4_append(ctypes.byref(cache()), 2, 2, 3, P, starts, None, P, P, None, 1e-6, ctypes.byref(rope),
+                                        None, None) == 1
+        assert b"not inverse" in L.laga_mla_last_error(), (kw, L.laga_mla_last_error())
