@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
     // the four rows whose softmax this warp does
     float f[4], m[4], l[4], slope2[4], pos[4];
     int2 seen[4];
-    uint32_t odd = 0;  // a bit a row: its result is NaN
+    uint32_t odd = 0;  // a bit a row: its result is NaN, if it sees anything
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * warp + i;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
       const int qi = (pc.r0 + r) / a.n_h, h = pc.r0 + r - qi * a.n_h;
       seen[i] = there ? cache_row_bounds(a, pc.b, qi) : make_int2(0, 0);
       const float up = there ? __ldcg(p.x.up + row0 + r) : 1.f;
-      if (up != up && seen[i].x < seen[i].y) odd |= 1u << i;  // a row that sees nothing is 0 whatever it holds
+      if (up != up) odd |= 1u << i;
       f[i] = (MOD & kModCap ? p.mod.u_scale : p.sl2) * (up != up ? 1.f : up);
       slope2[i] = pos[i] = 0.f;
       if constexpr ((MOD & kModBias) != 0) {
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 2) cache4_attn_mma_kernel(const Param
       float sum = l[i];
 #pragma unroll
       for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-      if ((odd >> i) & 1u) sum = __int_as_float(0x7fc00000);
+      if (((odd >> i) & 1u) && seen[i].x < seen[i].y) sum = __int_as_float(0x7fc00000);  // a row that sees nothing is 0 whatever it holds
       if (pc.begins && pc.ends && sum == 0.f && seen[i].x < seen[i].y) sum = __int_as_float(0x7fc00000);
       if (lane == 0) {
         scale_by[r] = sum;
