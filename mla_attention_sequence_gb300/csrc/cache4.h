@@ -70,7 +70,7 @@ struct CacheAttn {
   const int* lengths;  // [B] cached tokens
   const int *key_lo, *key_hi;  // [B][Sq] or null
   int Sq, n_h, rows;   // rows = Sq * n_h
-  int tile, row_tiles, keys, parts, least;  // least: key tiles worth a part of their own
+  int tile, row_tiles, keys, parts;
   bool causal;
   float scale;
   ScoreMods mods;
@@ -123,15 +123,6 @@ __device__ __forceinline__ long long cache_slot(const CacheView& c, const PageTa
   return static_cast<long long>(id) * c.page + (p - k * c.page);
 }
 
-// The same for a position that fits in 31 bits, without branches and with a division of half the length;
-// *there: whether the table has it (else the slot is some slot of the pool).
-__device__ __forceinline__ long long cache_slot_of(const CacheView& c, const PageTable& t, int b, int p, bool* there) {
-  const uint32_t at = static_cast<uint32_t>(max(p, 0)), k = at / static_cast<uint32_t>(c.page);
-  const int id = __ldg(t.table + static_cast<long long>(b) * t.most + min(k, static_cast<uint32_t>(t.most - 1)));
-  *there = p >= 0 && k < static_cast<uint32_t>(t.most) && id >= 0 && id < c.pages;
-  return static_cast<long long>(*there ? id : 0) * c.page + (at - k * c.page);
-}
-
 constexpr int kStatusBadPage = 1;  // LAGA_ERR_INVALID_ARG in the device's status word
 __device__ __forceinline__ void report_page(int* status, int where) {
   if (status) atomicCAS(status, 0, kStatusBadPage | (where << 8));
@@ -153,7 +144,7 @@ struct CacheShare {
 };
 __device__ __forceinline__ CacheShare cache_share(const CacheAttn& a, int part) {
   const int total = __ldcg(a.first + a.items());
-  const int quota = max(a.least, (total + a.parts - 1) / a.parts);
+  const int quota = max(1, (total + a.parts - 1) / a.parts);
   const long long begin = static_cast<long long>(part) * quota;
   return CacheShare{quota, static_cast<int>(min(begin, static_cast<long long>(total))),
                     static_cast<int>(min(begin + quota, static_cast<long long>(total)))};
@@ -220,7 +211,7 @@ __device__ __forceinline__ void cache4_plan_items(const CacheAttn& a) {
   if (threadIdx.x == 0) a.first[items] = before;
   // the item in which each part's share begins: the last one that begins at or before it
   __syncthreads();
-  const int quota = max(a.least, (before + a.parts - 1) / a.parts);
+  const int quota = max(1, (before + a.parts - 1) / a.parts);
   for (int p = threadIdx.x; p < a.parts; p += THREADS) {
     const long long t = static_cast<long long>(p) * quota;
     int lo = 0, hi = items;  // first[lo] <= t < first[hi], if t is within them

@@ -35,7 +35,6 @@
 // L2 no gain, with the keys on the MMA's M 176.
 #include "cache4.h"
 #include "cache4_tc.cuh"
-#include "f32x2.cuh"
 #include "score_mod.cuh"
 
 LAGA_TRACE_DEFINE(cache4)
@@ -570,16 +569,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
         const int k0 = pc.key0 + j * BKV;
         // f turns a product into log2 units, or with a cap c into the exponent of e^2u = 2^(f s):
         // c tanh(u) = c - 2 c / (1 + e^2u), to 1e-7 of c; far: by tanh_rel, which is small where u is
-        const uint64_t f2 = both(f);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          uint64_t v = mul2(pair(x[2 * i], x[2 * i + 1]), f2);
+          F2 v = mul(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2(f));
           if constexpr ((MOD & (kModCap | kModFar)) == kModCap) {
-            const float2 e = halves(v);
-            const float2 y = halves(add2(pair(ex2_approx(e.x), ex2_approx(e.y)), both(1.f)));
-            v = fma2(pair(rcp_approx(y.x), rcp_approx(y.y)), both(-2.f * p.mod.cap_log2), both(p.mod.cap_log2));
+            const float2 e = parts(v);
+            const float2 y = parts(add(f2(ex2_approx(e.x), ex2_approx(e.y)), f2(1.f)));
+            v = fma(f2(rcp_approx(y.x), rcp_approx(y.y)), f2(-2.f * p.mod.cap_log2), f2(p.mod.cap_log2));
           }
-          const float2 s = halves(v);
+          const float2 s = parts(v);
           x[2 * i] = __float_as_uint(s.x);
           x[2 * i + 1] = __float_as_uint(s.y);
         }
@@ -617,17 +615,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache4_attn_kernel(const __grid_c
           rescale = true;
         }
         const float neg = m == -INFINITY ? 0.f : -m;
-        const uint64_t neg2 = both(neg);
-        uint64_t sums = 0;
+        F2 sums = f2(0.f);
         uint32_t pk[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float2 s = halves(add2(pair(x[2 * i], x[2 * i + 1]), neg2));
+          const float2 s = parts(add(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2(neg)));
           const float w0 = ex2_approx(s.x), w1 = ex2_approx(s.y);
-          sums = add2(sums, pair(w0, w1));
+          sums = add(sums, f2(w0, w1));
           pk[i] = pack_f16x2(w0, w1);
         }
-        const float sum = halves(sums).x + halves(sums).y;
+        const float sum = parts(sums).x + parts(sums).y;
         l = fmaf(l, alpha, sum);
         LAGA_TRACE_POINT(cache4, 9, n);
         // O is the products' until the tile before is done

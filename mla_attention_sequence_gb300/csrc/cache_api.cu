@@ -135,7 +135,6 @@ laga_status attn_plan(const laga_mla_cache4_desc* d, const laga_mla_cache4* cach
   a.keys = s->few ? kMmaKeys : s->tc ? kTcKeys : kSimtKeys;
   // tcgen05: two CTAs a part, one a SM; else one, two a SM
   a.parts = s->tc && !s->few ? sm_count() / 2 : 2 * sm_count();
-  a.least = 1;
   a.row_tiles = (a.rows + a.tile - 1) / a.tile;
   const int64_t items = static_cast<int64_t>(a.pages.B) * a.row_tiles;
   const int64_t room = std::min(d->max_pages * cache->page_size, lim - 1);
