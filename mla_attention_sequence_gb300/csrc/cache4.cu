@@ -1,10 +1,11 @@
 // The paged 4-bit latent cache: rows written and read, the sharing out of an attention call's key
 // tiles and the joining of its pieces, and the attention on the CUDA cores for any widths.
 //
-// Writing and reading are bound by latency (a launch; a row's place behind its start and its table's
-// entry) and, writing, by instructions. A warp takes a row, a lane a block of 16 latents (at d_c = 512
-// each lane exactly one) and a pair of the RoPE key, so that the only thing that lanes exchange is the
-// key's sum of squares. 12288 rows of 512 + 64 in bf16 (events around the launch, 6 us of it the launch's
+// Writing and reading are bound by latency: a launch; a row's place behind its start and its table's
+// entry; writing, a row's chain of a sum over the warp, a root and a cosine (500 instructions a row, issued
+// in 45% of the cycles). A warp takes a row, a lane a block of 16 latents (at d_c = 512 each lane exactly
+// one) and a pair of the RoPE key, so that the only thing that lanes exchange is the key's sum of squares.
+// 12288 rows of 512 + 64 in bf16 (events around the launch, 6 us of it the launch's
 // own): 18 us written, 10 read, 3 of DRAM either way. Codes by comparisons with the borders for bf16 too
 // instead of the conversion: 25 written; with 4, 6 and 12 CTAs' shares an SM 18 .. 19 and 11 .. 12.
 #include "cache4.h"

@@ -18,9 +18,10 @@
 // item's interval), STAGES deep; two barriers a tile. The rows' stride of 416 bytes makes four tokens'
 // 32 bytes fall into different banks.
 //
-// 64 sequences of 1000 .. 8192 tokens, 16 heads (events): 63 us, 116 MB read, 28% of memory's rate. Not memory
-// bounds it (all sequences on one page: 2 us less), but 700 instructions a warp and tile, 256 of which expand
-// the codes and 68 are products, issued in 42% of the cycles. Measured and dropped: bulk copies issued by the
+// 64 sequences of 1000 .. 8192 tokens, 16 heads (events): 63 us, 116 MB read, 28% of memory's rate. Latency
+// bounds it: neither memory (all sequences on one page: 2 us less) nor issue is full (42% of the cycles; 700
+// instructions a warp and tile, 256 of which expand the codes and 68 are products), but 255 registers leave
+// two warps a scheduler, which wait at two barriers a tile. Measured and dropped: bulk copies issued by the
 // warps in turn 72, eight warps of 64 columns 111, tiles of 16 keys with three CTAs an SM 94, the values by way
 // of shared memory and ldmatrix instead of movmatrix 65, and with three CTAs an SM 68, the loads' place among
 // the pages worked out for every tile anew 68.

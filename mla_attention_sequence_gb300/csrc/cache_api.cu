@@ -86,7 +86,8 @@ laga_status check_rows(int64_t batch, int64_t rows, int64_t max_pages, const int
 //   one of 8000                           14 : 19    16 : 18    17 : 18     19 : 17
 //   one of 600                            10 : 14    10 : 14    11 : 14     12 : 14
 // So mma.sync up to 32 rows, and up to 64 while what the table has room for is at most about three of its
-// key tiles for each of its CTAs.
+// key tiles for each of its CTAs. The lengths are on the GPU, so the table's width stands for them: in a table
+// far wider than its sequences 33 to 64 rows take the tcgen05 form (one of 600: 14 us for 11), whose bits differ.
 constexpr int kFewRows = 32, kFewRowsShort = 64, kShortTiles = 3;
 
 struct AttnSizes {
