@@ -76,7 +76,7 @@ struct CacheAttn {
   ScoreMods mods;
   int* first;    // [items + 1] first key tile of each item in the order of all
   int* part_item;  // [parts] the item in which a part's share begins
-  int2* hull;    // [items] keys seen by some row, of those past the table's room the first alone
+  int2* hull;    // [items] keys seen by some row, of those past the table's room the first few
   float* part_o;     // [2 parts][tile][d_c]
   float2* part_ml;   // [2 parts][tile] {running maximum, sum}
   float* lse;        // [B][n_h][Sq]
@@ -175,12 +175,13 @@ __device__ __forceinline__ void cache4_plan_items(const CacheAttn& a) {
         lo = min(lo, s.x);
         hi = max(hi, s.y);
       }
-      // Keys that the table has no room for: the first of them stays in the interval, as a key without a page
-      // to the rows that see it. A row that sees only others ends without a weight (row_sum), or its whole
-      // item without a tile (lost_row).
+      // Keys that the table has no room for: those up to the end of the first one's tile stay in the interval,
+      // as keys without a page to the rows that see them (a key past the interval, in its last tile, would pass
+      // for one of zeros). A row that sees only others ends without a weight (row_sum), or its whole item
+      // without a tile (lost_row).
       if (hi > room) {
         report_page(a.status, 303);
-        hi = static_cast<int>(room) + 1;
+        hi = min(hi, (static_cast<int>(room) / a.keys + 1) * a.keys);
       }
       if (lo >= hi) lo = hi = 0;
       a.hull[j] = make_int2(lo, hi);

@@ -105,7 +105,11 @@ def test_rows_beside_rows_that_see_past_the_table(form):
                                            (far, [0, 0, 0], [m, 0, far], [2], [1]), (far, [0, m - 1, 5], [m - 1, m, m + 1], [2], []),
                                            (m + 900, [m + 1, m + 500, 0], [m + 2, far, 0], [0, 1], [2]),
                                            (m + 900, [0, m + 500, 5], [50, m + 700, m], [1], []),
-                                           (m + 900, [m] * 3, [m + 900] * 3, [0, 1, 2], [])):
+                                           (m + 900, [m] * 3, [m + 900] * 3, [0, 1, 2], []),
+                                           # keys past the room in the last tile that has others in it
+                                           (m + 900, [0, m + 3, 5], [50, m + 9, m], [1], []),
+                                           (m + 900, [m - 5, m + 1, 0], [m, m + 2, 0], [1], [2]),
+                                           (m + 900, [m + 2, m, m + 1], [m + 40, m + 1, far], [0, 1, 2], [])):
             kw = {} if lo is None else dict(key_lo=i32(*lo)[None], key_hi=i32(*hi)[None])
             out, lse = laga.cache4_fwd(q[b:b + 1], cache, W_UK, W_UV, tables[b], i32(length), variant=variant, **kw)
             with pytest.raises(laga.LagaError, match="page"):
